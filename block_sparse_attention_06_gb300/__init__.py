@@ -28,6 +28,8 @@ MSA_OP_DECODE = 1
 MSA_OP_PREFILL = 2
 MSA_OP_SELECT_PREFILL = 3
 MSA_OP_SELECT_INVERT_PREFILL = 4
+MSA_OP_TREE = 5
+MSA_TREE_MAX_NODES = 64
 
 STATUS = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_CUDA",
           4: "MSA_ERR_DEVICE_BOUNDS", 5: "MSA_ERR_TIMEOUT", 6: "MSA_ERR_WORKSPACE",
@@ -80,6 +82,11 @@ def _load() -> ctypes.CDLL:
         "msa_offload_gather": [P, P, I, P, I, D, P, P, P, P, P],
         "msa_stage_from_host": [P, P, S, P],
         "msa_select_prefill": [P, P, P, P, P, I, I, I, D, P, P, S, P, P],
+        "msa_tree_rows": [P, P, P, I, I, D, P, P, P, P, P],
+        "msa_tree_index_score": [P, P, P, P, P, P, P, I, I, I, D, P, P, P],
+        "msa_sparse_attn_tree": [P, P, P, P, P, P, P, P, P, P, I, I, I, D, P, P, P, S, P, P],
+        "msa_verify_tree": [P, P, I, P, P, P, P, P, I, I, P, P, P, P, P],
+        "msa_commit_tree": [P, P, P, I, P, P, P, P, P, P, P, P, I, I, I, D, P, P, P],
         "msa_check": [P, P],
     }
     for name, argt in sigs.items():
@@ -509,6 +516,191 @@ def msa_decode_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, seq_len
     return out, lse, sel, page_table, row_len, scores
 
 
+# ------------------------------------------------------------------ drafted trees (speculative decode)
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _call_on(dev, name: str, *args):
+    """_call with the tensors' device current (kernels launch on the current device)."""
+    if dev.index == torch.cuda.current_device():
+        _call(name, *args)
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args)
+
+
+def _req_tree(node_off, ctx_lens=None):
+    _req(node_off, torch.int32, "node_off")
+    if node_off.dim() != 1 or node_off.shape[0] < 2:
+        raise ValueError("node_off must be [n_req + 1]")
+    n_req = node_off.shape[0] - 1
+    if ctx_lens is not None:
+        _req(ctx_lens, torch.int32, "ctx_lens", (n_req,))
+    return n_req
+
+
+def msa_tree_rows(node_off, parents, ctx_lens, dims: Dims, q_req=None, q_pos=None, anc=None, err_word=None):
+    """Positions and ancestors of the rows of drafted trees -> (q_req, q_pos, anc); anc is int64,
+    bit m of a row's word set where node m is the row's ancestor or the row itself."""
+    n_req = _req_tree(node_off, ctx_lens)
+    _req(parents, torch.int32, "parents")
+    if parents.dim() != 1:
+        raise ValueError("parents must be [n_rows]")
+    n_rows, dev = parents.shape[0], parents.device
+    f = dict(device=dev)
+    q_req = torch.empty((n_rows,), dtype=torch.int32, **f) if q_req is None else q_req
+    q_pos = torch.empty((n_rows,), dtype=torch.int32, **f) if q_pos is None else q_pos
+    anc = torch.empty((n_rows,), dtype=torch.int64, **f) if anc is None else anc
+    _req(q_req, torch.int32, "q_req", (n_rows,))
+    _req(q_pos, torch.int32, "q_pos", (n_rows,))
+    _req(anc, torch.int64, "anc", (n_rows,))
+    err_word = new_err_word(dev) if err_word is None else err_word
+    _same_device(dev, node_off=node_off, ctx_lens=ctx_lens, q_req=q_req, q_pos=q_pos, anc=anc, err_word=err_word)
+    d = dims.c()
+    _call_on(dev, "msa_tree_rows", _ptr(node_off), _ptr(parents), _ptr(ctx_lens), n_rows, n_req, ctypes.byref(d),
+             _ptr(q_req), _ptr(q_pos), _ptr(anc), _ptr(err_word), _stream(dev))
+    return q_req, q_pos, anc
+
+
+def msa_tree_index_score(q_idx, kidx_cache, kidx_new, block_table, ctx_lens, node_off, anc, dims: Dims, scores=None,
+                         err_word=None):
+    """Block scores of the nodes of drafted trees: msa_index_score over the cached tokens and each
+    node's drafted ancestors (anc from msa_tree_rows)."""
+    n_req = _req_tree(node_off, ctx_lens)
+    n_rows, dev = q_idx.shape[0], q_idx.device
+    _req(q_idx, torch.bfloat16, "q_idx", (n_rows, dims.G, dims.Di))
+    _req(kidx_cache, torch.bfloat16, "kidx_cache")
+    if kidx_cache.dim() != 4 or tuple(kidx_cache.shape[1:]) != (dims.page_size, dims.G, dims.Di):
+        raise ValueError("kidx_cache must be [n_pages][128][G][Di]")
+    _req(kidx_new, torch.bfloat16, "kidx_new", (n_rows, dims.G, dims.Di))
+    _req(block_table, torch.int32, "block_table", (n_req, dims.max_blocks))
+    _req(anc, torch.int64, "anc", (n_rows,))
+    if scores is None:
+        scores = torch.empty((n_rows, dims.G, dims.max_blocks), dtype=torch.float32, device=dev)
+    _req(scores, torch.float32, "scores", (n_rows, dims.G, dims.max_blocks))
+    err_word = new_err_word(dev) if err_word is None else err_word
+    _same_device(dev, kidx_cache=kidx_cache, kidx_new=kidx_new, block_table=block_table, ctx_lens=ctx_lens,
+                 node_off=node_off, anc=anc, scores=scores, err_word=err_word)
+    d = dims.c()
+    _call_on(dev, "msa_tree_index_score", _ptr(q_idx), _ptr(kidx_cache), _ptr(kidx_new), _ptr(block_table),
+             _ptr(ctx_lens), _ptr(node_off), _ptr(anc), n_rows, n_req, kidx_cache.shape[0], ctypes.byref(d),
+             _ptr(scores), _ptr(err_word), _stream(dev))
+    return scores
+
+
+def msa_sparse_attn_tree(q, k_cache, v_cache, k_new, v_new, block_table, ctx_lens, node_off, anc, sel, dims: Dims,
+                         out=None, lse=None, workspace=None, err_word=None):
+    """Sparse attention of the nodes of drafted trees: the cached tokens of each row's selected
+    blocks and the row's drafted ancestors whose block is selected -> (out, lse)."""
+    n_req = _req_tree(node_off, ctx_lens)
+    n_rows, dev = q.shape[0], q.device
+    _req(q, torch.bfloat16, "q", (n_rows, dims.Hq, dims.D))
+    _req(k_cache, torch.bfloat16, "k_cache")
+    _req(v_cache, torch.bfloat16, "v_cache", tuple(k_cache.shape))
+    if k_cache.dim() != 4 or tuple(k_cache.shape[1:]) != (dims.page_size, dims.G, dims.D):
+        raise ValueError("k_cache must be [n_pages][128][G][D]")
+    _req(k_new, torch.bfloat16, "k_new", (n_rows, dims.G, dims.D))
+    _req(v_new, torch.bfloat16, "v_new", (n_rows, dims.G, dims.D))
+    _req(block_table, torch.int32, "block_table", (n_req, dims.max_blocks))
+    _req(anc, torch.int64, "anc", (n_rows,))
+    _req(sel, torch.int32, "sel", (n_rows, dims.G, dims.topk))
+    if out is None:
+        out = torch.empty((n_rows, dims.Hq, dims.D), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((n_rows, dims.Hq), dtype=torch.float32, device=dev)
+    _req(out, torch.bfloat16, "out", (n_rows, dims.Hq, dims.D))
+    _req(lse, torch.float32, "lse", (n_rows, dims.Hq))
+    if workspace is None:
+        need = msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims)
+        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
+    _req(workspace, torch.uint8, "workspace")
+    err_word = new_err_word(dev) if err_word is None else err_word
+    _same_device(dev, k_cache=k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new, block_table=block_table,
+                 ctx_lens=ctx_lens, node_off=node_off, anc=anc, sel=sel, out=out, lse=lse, workspace=workspace,
+                 err_word=err_word)
+    d = dims.c()
+    _call_on(dev, "msa_sparse_attn_tree", _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_new), _ptr(v_new),
+             _ptr(block_table), _ptr(ctx_lens), _ptr(node_off), _ptr(anc), _ptr(sel), n_rows, n_req, k_cache.shape[0],
+             ctypes.byref(d), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err_word), _stream(dev))
+    return out, lse
+
+
+def msa_verify_tree(target_probs, draft_probs, tokens, node_off, parents, u_accept, u_next, path=None,
+                    n_accepted=None, next_token=None, err_word=None):
+    """Accept drafted tokens against the target's probabilities from given random numbers ->
+    (path, n_accepted, next_token); draft_probs None: drafts chosen without chance."""
+    n_req = _req_tree(node_off)
+    _req(target_probs, torch.float32, "target_probs")
+    if target_probs.dim() != 2 or target_probs.shape[1] < 1:
+        raise ValueError("target_probs must be [n_rows][vocab]")
+    (n_rows, vocab), dev = target_probs.shape, target_probs.device
+    if draft_probs is not None:
+        _req(draft_probs, torch.float32, "draft_probs", (n_rows, vocab))
+    _req(tokens, torch.int32, "tokens", (n_rows,))
+    _req(parents, torch.int32, "parents", (n_rows,))
+    _req(u_accept, torch.float32, "u_accept", (n_rows,))
+    _req(u_next, torch.float32, "u_next", (n_req,))
+    f = dict(dtype=torch.int32, device=dev)
+    path = torch.empty((n_rows,), **f) if path is None else path
+    n_accepted = torch.empty((n_req,), **f) if n_accepted is None else n_accepted
+    next_token = torch.empty((n_req,), **f) if next_token is None else next_token
+    _req(path, torch.int32, "path", (n_rows,))
+    _req(n_accepted, torch.int32, "n_accepted", (n_req,))
+    _req(next_token, torch.int32, "next_token", (n_req,))
+    err_word = new_err_word(dev) if err_word is None else err_word
+    _same_device(dev, draft_probs=draft_probs, tokens=tokens, node_off=node_off, parents=parents, u_accept=u_accept,
+                 u_next=u_next, path=path, n_accepted=n_accepted, next_token=next_token, err_word=err_word)
+    _call_on(dev, "msa_verify_tree", _ptr(target_probs), _ptr(draft_probs), vocab, _ptr(tokens), _ptr(node_off),
+             _ptr(parents), _ptr(u_accept), _ptr(u_next), n_rows, n_req, _ptr(path), _ptr(n_accepted),
+             _ptr(next_token), _ptr(err_word), _stream(dev))
+    return path, n_accepted, next_token
+
+
+def _layers(t, lead: int):
+    """A tensor of all layers; one layer's tensor may come without the layer dimension."""
+    return t if not isinstance(t, torch.Tensor) or t.dim() == lead + 1 else t.unsqueeze(0)
+
+
+def msa_commit_tree(k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache, block_table, ctx_lens, node_off, path,
+                    n_accepted, dims: Dims, new_lens=None, err_word=None):
+    """Append the accepted paths to the caches of all layers (in place) -> new_lens.  Rows are
+    [n_layers][n_rows][G][D], caches [n_layers][n_pages][128][G][D] (the k-index with Di); for one
+    layer the leading dimension may be left out."""
+    n_req = _req_tree(node_off, ctx_lens)
+    k_new, v_new, kidx_new = _layers(k_new, 3), _layers(v_new, 3), _layers(kidx_new, 3)
+    k_cache, v_cache, kidx_cache = _layers(k_cache, 4), _layers(v_cache, 4), _layers(kidx_cache, 4)
+    _req(k_new, torch.bfloat16, "k_new")
+    _req(k_cache, torch.bfloat16, "k_cache")
+    if k_new.dim() != 4 or tuple(k_new.shape[2:]) != (dims.G, dims.D):
+        raise ValueError("k_new must be [n_layers][n_rows][G][D]")
+    L, n_rows, dev = k_new.shape[0], k_new.shape[1], k_new.device
+    if k_cache.dim() != 5 or k_cache.shape[0] != L or tuple(k_cache.shape[2:]) != (dims.page_size, dims.G, dims.D):
+        raise ValueError("k_cache must be [n_layers][n_pages][128][G][D]")
+    n_pages = k_cache.shape[1]
+    _req(v_new, torch.bfloat16, "v_new", tuple(k_new.shape))
+    _req(kidx_new, torch.bfloat16, "kidx_new", (L, n_rows, dims.G, dims.Di))
+    _req(v_cache, torch.bfloat16, "v_cache", tuple(k_cache.shape))
+    _req(kidx_cache, torch.bfloat16, "kidx_cache", (L, n_pages, dims.page_size, dims.G, dims.Di))
+    _req(block_table, torch.int32, "block_table", (n_req, dims.max_blocks))
+    _req(path, torch.int32, "path", (n_rows,))
+    _req(n_accepted, torch.int32, "n_accepted", (n_req,))
+    new_lens = torch.empty((n_req,), dtype=torch.int32, device=dev) if new_lens is None else new_lens
+    _req(new_lens, torch.int32, "new_lens", (n_req,))
+    err_word = new_err_word(dev) if err_word is None else err_word
+    _same_device(dev, v_new=v_new, kidx_new=kidx_new, k_cache=k_cache, v_cache=v_cache, kidx_cache=kidx_cache,
+                 block_table=block_table, ctx_lens=ctx_lens, node_off=node_off, path=path, n_accepted=n_accepted,
+                 new_lens=new_lens, err_word=err_word)
+    d = dims.c()
+    _call_on(dev, "msa_commit_tree", _ptr(k_new), _ptr(v_new), _ptr(kidx_new), L, _ptr(k_cache), _ptr(v_cache),
+             _ptr(kidx_cache), _ptr(block_table), _ptr(ctx_lens), _ptr(node_off), _ptr(path), _ptr(n_accepted), n_rows,
+             n_req, n_pages, ctypes.byref(d), _ptr(new_lens), _ptr(err_word), _stream(dev))
+    return new_lens
+
+
 # ------------------------------------------------------------------ whole-path helpers
 
 def dims_of(case) -> Dims:
@@ -820,3 +1012,59 @@ class MixedStep:
         self.prefill(pre_q, pre_q_idx, k_cache, v_cache, kidx_cache, pre_block_table, pre_q_req, pre_q_pos)
         main.wait_stream(self._side)                 # the decode results are complete on the caller's stream
         return self.decode.out, self.decode.lse, self.prefill.out, self.prefill.lse
+
+
+class TreeStep:
+    """One speculative decode step over drafted trees, with preallocated buffers: layout() once per
+    step, attend() once per layer, then verify() and commit().
+
+    n_rows is the largest number of drafted tokens of a step, over all requests; node_off (int32
+    [n_req + 1]) and parents (int32 [n_rows]) say which rows are in use, so one captured step serves
+    trees of any shape: rows at or past node_off[n_req] are padding.  Every node sees what it would
+    see in a sequential decode along its path, block selection included."""
+
+    def __init__(self, dims: Dims, n_rows: int, n_req: int, device):
+        self.dims, self.n_rows, self.n_req = dims, n_rows, n_req
+        f = dict(device=device)
+        self.q_req = torch.empty((n_rows,), dtype=torch.int32, **f)
+        self.q_pos = torch.empty((n_rows,), dtype=torch.int32, **f)
+        self.anc = torch.empty((n_rows,), dtype=torch.int64, **f)
+        self.scores = torch.empty((n_rows, dims.G, dims.max_blocks), dtype=torch.float32, **f)
+        self.sel = torch.empty((n_rows, dims.G, dims.topk), dtype=torch.int32, **f)
+        self.out = torch.zeros((n_rows, dims.Hq, dims.D), dtype=torch.bfloat16, **f)
+        self.lse = torch.zeros((n_rows, dims.Hq), dtype=torch.float32, **f)
+        self.workspace = torch.empty((max(1, msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims)),),
+                                     dtype=torch.uint8, **f)
+        self.path = torch.full((n_rows,), -1, dtype=torch.int32, **f)
+        self.n_accepted = torch.zeros((n_req,), dtype=torch.int32, **f)
+        self.next_token = torch.zeros((n_req,), dtype=torch.int32, **f)
+        self.new_lens = torch.zeros((n_req,), dtype=torch.int32, **f)
+        self.err = new_err_word(device)
+
+    def layout(self, node_off, parents, ctx_lens):
+        """Positions and ancestors of this step's rows, shared by every layer."""
+        self.node_off, self.parents, self.ctx_lens = node_off, parents, ctx_lens
+        return msa_tree_rows(node_off, parents, ctx_lens, self.dims, self.q_req, self.q_pos, self.anc,
+                             err_word=self.err)
+
+    def attend(self, q, q_idx, k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache, block_table, out=None, lse=None):
+        """One layer: block scores, top-k, attention -> (out, lse); the step's buffers unless given."""
+        out = self.out if out is None else out
+        lse = self.lse if lse is None else lse
+        msa_tree_index_score(q_idx, kidx_cache, kidx_new, block_table, self.ctx_lens, self.node_off, self.anc,
+                             self.dims, self.scores, err_word=self.err)
+        msa_topk_blocks(self.scores, self.q_pos, self.dims, sel=self.sel, err_word=self.err)
+        return msa_sparse_attn_tree(q, k_cache, v_cache, k_new, v_new, block_table, self.ctx_lens, self.node_off,
+                                    self.anc, self.sel, self.dims, out, lse, self.workspace, err_word=self.err)
+
+    def verify(self, target_probs, draft_probs, tokens, u_accept, u_next):
+        """-> (path, n_accepted, next_token) of this step's trees."""
+        return msa_verify_tree(target_probs, draft_probs, tokens, self.node_off, self.parents, u_accept, u_next,
+                               self.path, self.n_accepted, self.next_token, err_word=self.err)
+
+    def commit(self, k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache, block_table):
+        """Append the accepted paths to all layers' caches; -> new context lengths (the next step's
+        ctx_lens, after a copy: the buffer is written again by the next commit)."""
+        return msa_commit_tree(k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache, block_table, self.ctx_lens,
+                               self.node_off, self.path, self.n_accepted, self.dims, self.new_lens,
+                               err_word=self.err)

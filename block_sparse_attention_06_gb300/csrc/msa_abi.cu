@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "msa.h"
@@ -84,6 +85,14 @@ msa_status_t check_dims(const msa_dims_t *d, bool need_attn, bool need_index, Sh
     do {                                                         \
         if (!(cond)) return fail(MSA_ERR_INVALID_ARG, __VA_ARGS__); \
     } while (0)
+
+constexpr int kTreeMaxRequests = 65535;   // requests are a grid dimension of the tree calls
+
+bool misaligned16(std::initializer_list<const void *> ps) {
+    uintptr_t bits = 0;
+    for (const void *p : ps) bits |= reinterpret_cast<uintptr_t>(p);
+    return (bits & 15u) != 0;
+}
 
 }  // namespace
 
@@ -471,6 +480,109 @@ msa_status_t msa_decode_step(const void *q, const void *q_idx, const void *k_cac
     return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_decode_step (attention)");
 }
 
+msa_status_t msa_tree_rows(const int32_t *node_off, const int32_t *parents, const int32_t *ctx_lens, int32_t n_rows,
+                           int32_t n_req, const msa_dims_t *dims, int32_t *q_req, int32_t *q_pos, uint64_t *anc,
+                           int32_t *err_word, msa_stream_t stream) {
+    Shape s;
+    msa_status_t st = check_dims(dims, false, false, &s, "msa_tree_rows");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(n_rows >= 0 && n_req > 0, "msa_tree_rows: bad sizes");
+    if (n_rows == 0) return MSA_OK;
+    MSA_REQUIRE(node_off && parents && ctx_lens && q_req && q_pos && anc && err_word, "msa_tree_rows: NULL pointer");
+    if (n_req > kTreeMaxRequests) return fail(MSA_ERR_UNSUPPORTED, "msa_tree_rows: n_req > %d", kTreeMaxRequests);
+    cudaError_t e = launch_tree_rows(node_off, parents, ctx_lens, n_rows, n_req, s.max_blocks, q_req, q_pos, anc,
+                                     err_word, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_tree_rows");
+}
+
+msa_status_t msa_tree_index_score(const void *q_idx, const void *kidx_cache, const void *kidx_new,
+                                  const int32_t *block_table, const int32_t *ctx_lens, const int32_t *node_off,
+                                  const uint64_t *anc, int32_t n_rows, int32_t n_req, int32_t n_pages,
+                                  const msa_dims_t *dims, float *scores, int32_t *err_word, msa_stream_t stream) {
+    Shape s;
+    msa_status_t st = check_dims(dims, false, true, &s, "msa_tree_index_score");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(n_rows >= 0 && n_req > 0 && n_pages > 0, "msa_tree_index_score: bad sizes");
+    if (n_rows == 0) return MSA_OK;
+    MSA_REQUIRE(q_idx && kidx_cache && kidx_new && block_table && ctx_lens && node_off && anc && scores && err_word,
+                "msa_tree_index_score: NULL pointer");
+    if (n_req > kTreeMaxRequests)
+        return fail(MSA_ERR_UNSUPPORTED, "msa_tree_index_score: n_req > %d", kTreeMaxRequests);
+    if (s.max_blocks > 65535) return fail(MSA_ERR_UNSUPPORTED, "msa_tree_index_score: max_blocks > 65535");
+    if (misaligned16({q_idx, kidx_cache, kidx_new}))
+        return fail(MSA_ERR_INVALID_ARG, "msa_tree_index_score: q_idx and the index keys must be 16-byte aligned");
+    cudaError_t e = launch_score_tree(q_idx, kidx_cache, kidx_new, block_table, ctx_lens, node_off, anc, n_rows, n_req,
+                                      n_pages, s, scores, err_word, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_tree_index_score");
+}
+
+msa_status_t msa_sparse_attn_tree(const void *q, const void *k_cache, const void *v_cache, const void *k_new,
+                                  const void *v_new, const int32_t *block_table, const int32_t *ctx_lens,
+                                  const int32_t *node_off, const uint64_t *anc, const int32_t *sel, int32_t n_rows,
+                                  int32_t n_req, int32_t n_pages, const msa_dims_t *dims, void *out, float *lse,
+                                  void *workspace, size_t workspace_bytes, int32_t *err_word, msa_stream_t stream) {
+    Shape s;
+    msa_status_t st = check_dims(dims, true, false, &s, "msa_sparse_attn_tree");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(n_rows >= 0 && n_req > 0 && n_pages > 0, "msa_sparse_attn_tree: bad sizes");
+    if (n_rows == 0) return MSA_OK;
+    MSA_REQUIRE(q && k_cache && v_cache && k_new && v_new && block_table && ctx_lens && node_off && anc && sel && out &&
+                    lse && err_word,
+                "msa_sparse_attn_tree: NULL pointer");
+    if (s.max_blocks > 16384) return fail(MSA_ERR_UNSUPPORTED, "msa_sparse_attn_tree: max_blocks > 16384");
+    if (n_req > kTreeMaxRequests)
+        return fail(MSA_ERR_UNSUPPORTED, "msa_sparse_attn_tree: n_req > %d", kTreeMaxRequests);
+    if (1.0 * n_rows * s.G * s.topk > 2147483647.0)
+        return fail(MSA_ERR_UNSUPPORTED, "msa_sparse_attn_tree: more than 2^31 selected blocks");
+    if (misaligned16({q, k_cache, v_cache, k_new, v_new, out, workspace}))
+        return fail(MSA_ERR_INVALID_ARG, "msa_sparse_attn_tree: tensors and workspace must be 16-byte aligned");
+    const size_t need = tree_workspace_bytes(n_rows, n_req, s);
+    if (!workspace || workspace_bytes < need)
+        return fail(MSA_ERR_WORKSPACE, "msa_sparse_attn_tree: workspace needs %zu bytes", need);
+    cudaError_t e = launch_attn_tree(q, k_cache, v_cache, k_new, v_new, block_table, ctx_lens, node_off, anc, sel,
+                                     n_rows, n_req, n_pages, s, out, lse, workspace, err_word,
+                                     static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_sparse_attn_tree");
+}
+
+msa_status_t msa_verify_tree(const float *target_probs, const float *draft_probs, int32_t vocab,
+                             const int32_t *tokens, const int32_t *node_off, const int32_t *parents,
+                             const float *u_accept, const float *u_next, int32_t n_rows, int32_t n_req, int32_t *path,
+                             int32_t *n_accepted, int32_t *next_token, int32_t *err_word, msa_stream_t stream) {
+    MSA_REQUIRE(n_rows >= 0 && n_req > 0 && vocab > 0, "msa_verify_tree: bad sizes");
+    MSA_REQUIRE(n_accepted && next_token && node_off && err_word, "msa_verify_tree: NULL pointer");
+    MSA_REQUIRE(n_rows == 0 || (target_probs && tokens && parents && u_accept && u_next && path),
+                "msa_verify_tree: NULL pointer");
+    if (n_req > kTreeMaxRequests) return fail(MSA_ERR_UNSUPPORTED, "msa_verify_tree: n_req > %d", kTreeMaxRequests);
+    cudaError_t e = launch_verify_tree(target_probs, draft_probs, vocab, tokens, node_off, parents, u_accept, u_next,
+                                       n_rows, n_req, path, n_accepted, next_token, err_word,
+                                       static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_verify_tree");
+}
+
+msa_status_t msa_commit_tree(const void *k_new, const void *v_new, const void *kidx_new, int32_t n_layers,
+                             void *k_cache, void *v_cache, void *kidx_cache, const int32_t *block_table,
+                             const int32_t *ctx_lens, const int32_t *node_off, const int32_t *path,
+                             const int32_t *n_accepted, int32_t n_rows, int32_t n_req, int32_t n_pages,
+                             const msa_dims_t *dims, int32_t *new_lens, int32_t *err_word, msa_stream_t stream) {
+    Shape s;
+    msa_status_t st = check_dims(dims, true, true, &s, "msa_commit_tree");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(n_layers > 0 && n_rows >= 0 && n_req > 0 && n_pages > 0, "msa_commit_tree: bad sizes");
+    MSA_REQUIRE(ctx_lens && node_off && n_accepted && new_lens && err_word, "msa_commit_tree: NULL pointer");
+    MSA_REQUIRE(n_rows == 0 || (k_new && v_new && kidx_new && k_cache && v_cache && kidx_cache && block_table && path),
+                "msa_commit_tree: NULL pointer");
+    MSA_REQUIRE(new_lens != ctx_lens, "msa_commit_tree: new_lens must not be ctx_lens");
+    if (n_layers > 65535 || n_req > kTreeMaxRequests)
+        return fail(MSA_ERR_UNSUPPORTED, "msa_commit_tree: more than 65535 layers or %d requests", kTreeMaxRequests);
+    if (misaligned16({k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache}))
+        return fail(MSA_ERR_INVALID_ARG, "msa_commit_tree: rows and caches must be 16-byte aligned");
+    cudaError_t e = launch_commit_tree(k_new, v_new, kidx_new, n_layers, k_cache, v_cache, kidx_cache, block_table,
+                                       ctx_lens, node_off, path, n_accepted, n_rows, n_req, n_pages, s, new_lens,
+                                       err_word, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_commit_tree");
+}
+
 size_t msa_workspace_bytes(int32_t op, int32_t n_rows, int32_t n_req, const msa_dims_t *dims) {
     Shape s;
     if (n_rows < 0) return 0;
@@ -493,6 +605,10 @@ size_t msa_workspace_bytes(int32_t op, int32_t n_rows, int32_t n_req, const msa_
     if (op == MSA_OP_SELECT_INVERT_PREFILL) {
         if (check_dims(dims, false, true, &s, "msa_workspace_bytes") != MSA_OK || n_req <= 0) return 0;
         return select_lists_bytes(n_rows, s) + invert_workspace_bytes(n_rows, n_req, s);
+    }
+    if (op == MSA_OP_TREE) {
+        if (check_dims(dims, true, false, &s, "msa_workspace_bytes") != MSA_OK || n_req <= 0) return 0;
+        return tree_workspace_bytes(n_rows, n_req, s);
     }
     return 0;
 }
@@ -529,7 +645,7 @@ const char *msa_status_str(msa_status_t status) {
 
 const char *msa_last_error(void) { return g_last_error; }
 
-int32_t msa_version(void) { return 300; }
+int32_t msa_version(void) { return 400; }
 
 msa_status_t msa_selftest_timeout(int32_t *err_word, msa_stream_t stream) {
     MSA_REQUIRE(err_word, "msa_selftest_timeout: NULL err_word");

@@ -324,6 +324,25 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// ------------------------------------------------------------------ drafted trees
+
+// Rows of request b's tree: returns the node count (0 for a bad range, with its flag raised where
+// `report` is set) and the first row.
+__device__ __forceinline__ int tree_rows_of(const int32_t *__restrict__ node_off, int b, int n_rows, int32_t *err,
+                                            bool report, int *row0) {
+    const int r0 = node_off[b], r1 = node_off[b + 1];
+    *row0 = r0;
+    if (r0 < 0 || r1 < r0 || r1 > n_rows || (b == 0 && r0 != 0)) {
+        if (report) raise_flag(err, MSA_FLAG_BOUNDS);
+        return 0;
+    }
+    if (r1 - r0 > 64) {
+        if (report) raise_flag(err, MSA_FLAG_UNSUPPORTED);
+        return 0;
+    }
+    return r1 - r0;
+}
+
 // ------------------------------------------------------------------ misc
 
 __device__ __forceinline__ int32_t warp_sum_i(int32_t v) {

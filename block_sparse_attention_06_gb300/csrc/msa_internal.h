@@ -129,6 +129,30 @@ cudaError_t launch_score_decode_seq(const void *q_idx, const void *kidx, const i
                                     const int32_t *seq_lens, int B, int n_pages, const Shape &s,
                                     float *scores, int32_t *err, cudaStream_t st, bool pdl = false);
 
+// Drafted trees (speculative decode): layout, scoring, attention, verification, commit.
+constexpr int kTreeMaxNodes = 64;   // nodes per request (one bit each in a row's ancestor word)
+cudaError_t launch_tree_rows(const int32_t *node_off, const int32_t *parents, const int32_t *ctx_lens, int n_rows,
+                             int n_req, int max_blocks, int32_t *q_req, int32_t *q_pos, uint64_t *anc, int32_t *err,
+                             cudaStream_t st);
+cudaError_t launch_score_tree(const void *q_idx, const void *kidx, const void *kidx_new, const int32_t *block_table,
+                              const int32_t *ctx_lens, const int32_t *node_off, const uint64_t *anc, int n_rows,
+                              int n_req, int n_pages, const Shape &s, float *scores, int32_t *err, cudaStream_t st);
+size_t tree_workspace_bytes(int n_rows, int n_req, const Shape &s);
+cudaError_t launch_attn_tree(const void *q, const void *k_cache, const void *v_cache, const void *k_new,
+                             const void *v_new, const int32_t *block_table, const int32_t *ctx_lens,
+                             const int32_t *node_off, const uint64_t *anc, const int32_t *sel, int n_rows, int n_req,
+                             int n_pages, const Shape &s, void *out, float *lse, void *ws, int32_t *err,
+                             cudaStream_t st);
+cudaError_t launch_verify_tree(const float *p, const float *q, int vocab, const int32_t *tokens,
+                               const int32_t *node_off, const int32_t *parents, const float *u_accept,
+                               const float *u_next, int n_rows, int n_req, int32_t *path, int32_t *n_acc,
+                               int32_t *next_token, int32_t *err, cudaStream_t st);
+cudaError_t launch_commit_tree(const void *k_new, const void *v_new, const void *kidx_new, int n_layers, void *k_cache,
+                               void *v_cache, void *kidx_cache, const int32_t *block_table, const int32_t *ctx_lens,
+                               const int32_t *node_off, const int32_t *path, const int32_t *n_acc, int n_rows,
+                               int n_req, int n_pages, const Shape &s, int32_t *new_lens, int32_t *err,
+                               cudaStream_t st);
+
 // Tensor-map creation through the driver entry point (no libcuda link dependency).
 bool encode_tensor_map(void *map, int rank, const void *base, const uint64_t *dims,
                        const uint64_t *strides_bytes, const uint32_t *box, int swizzle_bytes,

@@ -92,6 +92,7 @@ typedef void *msa_stream_t;
 #define MSA_OP_PREFILL 2
 #define MSA_OP_SELECT_PREFILL 3
 #define MSA_OP_SELECT_INVERT_PREFILL 4
+#define MSA_OP_TREE 5
 
 /*
  * msa_index_score -- block scores for every (row, group, candidate block).
@@ -418,10 +419,140 @@ msa_status_t msa_sparse_attn_decode_noalloc(const void *q, const void *k_cache, 
                                             int32_t *err_word, msa_stream_t stream);
 
 /*
+ * Drafted trees (speculative decode).  The pages name multi-token decode as a
+ * use of the index scan ([T-zh 解码索引评分内核优化], MSA_PHASE_DECODE_MULTI); the
+ * five calls below carry it through a whole step.  Request b has ctx_lens[b]
+ * cached tokens and a tree of n = node_off[b+1] - node_off[b] <= 64 drafted
+ * tokens, rows node_off[b] .. node_off[b+1]-1 (row = node_off[b] + node number):
+ *
+ *   node_off  int32 [n_req + 1]  ascending from 0; node_off[n_req] <= n_rows.  Rows
+ *             at or past node_off[n_req] belong to no request (padding, for a step
+ *             captured at its largest size): no result of theirs is written, but
+ *             see msa_tree_rows.  A request may have no node.
+ *   parents   int32 [n_rows]     -1 for node 0, the root (the last sampled token,
+ *             not cached yet); for node i > 0 a number in [0, i).
+ *
+ * Node i stands at position ctx_lens[b] + depth(i) (depth 0: the root) and sees
+ * exactly what the same token would see in a sequential decode along its path: the
+ * cached tokens, its ancestors and itself.  Blocks are counted by position, so a
+ * drafted token belongs to block (ctx_lens[b] + depth) / 128.  K, V and index keys
+ * of the drafted tokens come as dense rows ([n_rows][G][D] and [n_rows][G][Di]),
+ * not through the caches; msa_commit_tree writes the accepted ones there.
+ *
+ * msa_tree_rows -- positions and ancestors of every row, shared by all layers of a step.
+ *   ctx_lens  int32 [n_req]
+ *   q_req, q_pos  int32 [n_rows]  out: request and position, as the other calls take
+ *                 them; padding rows get -1 and 0 (valid input to msa_topk_blocks)
+ *   anc       uint64 [n_rows]     out: bit m set where node m of the same request is
+ *                 an ancestor of the row or the row itself; 0 for padding rows
+ * A bad node_off or parent, a negative context or a position past max_blocks * 128
+ * raises MSA_FLAG_BOUNDS, more than 64 nodes MSA_FLAG_UNSUPPORTED; the rows of that
+ * request are then written as padding.
+ */
+msa_status_t msa_tree_rows(const int32_t *node_off, const int32_t *parents, const int32_t *ctx_lens, int32_t n_rows,
+                           int32_t n_req, const msa_dims_t *dims, int32_t *q_req, int32_t *q_pos, uint64_t *anc,
+                           int32_t *err_word, msa_stream_t stream);
+
+/*
+ * msa_tree_index_score -- msa_index_score for the nodes of drafted trees: the score
+ * of block j is the MAX of the raw dot products over the cached tokens of the block
+ * (positions < ctx_lens[b]) and the drafted ancestors (and the row itself) whose
+ * position lies in it.
+ *   q_idx      bf16 [n_rows][G][Di];  kidx_cache bf16 [n_pages][128][G][Di]
+ *   kidx_new   bf16 [n_rows][G][Di]   index keys of the drafted tokens
+ *   anc        uint64 [n_rows]        from msa_tree_rows
+ *   scores     fp32 [n_rows][G][max_blocks]  out; -inf for blocks past the row's own;
+ *              padding rows are not written
+ * Each request's k-index is read once for every 16 of its nodes.  A page id outside
+ * [0, n_pages) raises MSA_FLAG_BOUNDS.  max_blocks <= 65535.
+ */
+msa_status_t msa_tree_index_score(const void *q_idx, const void *kidx_cache, const void *kidx_new,
+                                  const int32_t *block_table, const int32_t *ctx_lens, const int32_t *node_off,
+                                  const uint64_t *anc, int32_t n_rows, int32_t n_req, int32_t n_pages,
+                                  const msa_dims_t *dims, float *scores, int32_t *err_word, msa_stream_t stream);
+
+/*
+ * msa_sparse_attn_tree -- sparse attention of the nodes of drafted trees.  Row r of
+ * group g attends the cached tokens (positions < ctx_lens[b]) of the blocks in
+ * sel[r][g], and of its ancestors and itself those whose block is in sel[r][g].
+ *   q          bf16 [n_rows][Hq][D];  k_cache, v_cache bf16 [n_pages][128][G][D]
+ *   k_new, v_new  bf16 [n_rows][G][D] the drafted tokens' K and V
+ *   sel        int32 [n_rows][G][topk] distinct block ids, -1 padding (msa_topk_blocks
+ *              with the q_pos of msa_tree_rows, or any other choice)
+ *   out        bf16 [n_rows][Hq][D]  out;  lse fp32 [n_rows][Hq]  out.  A row that sees
+ *              no token gets 0 and -inf.  Padding rows are not written.
+ *   workspace  device scratch of msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims)
+ *              bytes, 16-byte aligned
+ * What a row does not see does not reach its result, whatever its bits (unwritten
+ * page tails, other branches, padding rows).  A block id >= max_blocks, or a page
+ * outside [0, n_pages) of a block that holds cached tokens, raises MSA_FLAG_BOUNDS.
+ * Limits: max_blocks <= 16384; all tensors 16-byte aligned.
+ */
+msa_status_t msa_sparse_attn_tree(const void *q, const void *k_cache, const void *v_cache, const void *k_new,
+                                  const void *v_new, const int32_t *block_table, const int32_t *ctx_lens,
+                                  const int32_t *node_off, const uint64_t *anc, const int32_t *sel, int32_t n_rows,
+                                  int32_t n_req, int32_t n_pages, const msa_dims_t *dims, void *out, float *lse,
+                                  void *workspace, size_t workspace_bytes, int32_t *err_word, msa_stream_t stream);
+
+/*
+ * msa_verify_tree -- accept drafted tokens against the target's probabilities by
+ * rejection, from given random numbers, so that the emitted tokens have exactly the
+ * target's distribution.  From the root on, the children x of the current node v
+ * are tried in order of their number: with p, q the target and draft distributions
+ * of row v, r = max(p - c q, 0) and M the mass of r (c = 0, M = 1 at first),
+ *   x is accepted  iff  u_accept[x] * q(tok_x) * M < r(tok_x);
+ *   on rejection   c += M, M = sum_t max(p(t) - c q(t), 0)
+ * which is the chain "accept with min(1, r/(M q)), else go on with the normalised
+ * residual".  It is exact for children drawn independently from q (their parent's
+ * row of draft_probs).  With draft_probs == NULL the children are any distinct
+ * tokens chosen without chance (a lookup, the likeliest ones): x is accepted iff
+ * u_accept[x] * M < r(tok_x), where a rejected token leaves r (and M).
+ * At the first node whose children are all rejected, or that has none, the next
+ * token is the smallest t with r(0) + .. + r(t) > u_next[b] * (r(0) + .. + r(V-1)).
+ * A residual without mass is replaced by p.  Negative and NaN entries count as 0.
+ *   target_probs, draft_probs  fp32 [n_rows][vocab]; row v: the token after node v
+ *   tokens    int32 [n_rows]  the nodes' tokens (the root's is not read)
+ *   u_accept  fp32 [n_rows], u_next fp32 [n_req]  uniform in [0, 1); the roots'
+ *             u_accept is not read
+ *   path      int32 [n_rows]  out: the accepted node numbers of request b, root
+ *             first, from row node_off[b] on; -1 behind them; padding rows are not written
+ *   n_accepted int32 [n_req]  out: nodes accepted, the root among them (0 without nodes)
+ *   next_token int32 [n_req]  out; -1 for a request without nodes
+ * Sums and comparisons are carried at 48 bits or more.  A token outside [0, vocab) or a bad
+ * parent raises MSA_FLAG_BOUNDS (that node is never accepted); a row of target_probs
+ * without finite positive mass raises MSA_FLAG_NAN (next_token -1).
+ */
+msa_status_t msa_verify_tree(const float *target_probs, const float *draft_probs, int32_t vocab,
+                             const int32_t *tokens, const int32_t *node_off, const int32_t *parents,
+                             const float *u_accept, const float *u_next, int32_t n_rows, int32_t n_req, int32_t *path,
+                             int32_t *n_accepted, int32_t *next_token, int32_t *err_word, msa_stream_t stream);
+
+/*
+ * msa_commit_tree -- append the accepted paths to the caches of all layers: for k <
+ * n_accepted[b] and every layer l, the K, V and index key of row node_off[b] +
+ * path[node_off[b] + k] go to position ctx_lens[b] + k of request b.
+ *   layer stride of the dense rows: n_rows * G * D (K, V), n_rows * G * Di (k-index)
+ *   elements; of the caches: n_pages * 128 * G * D and n_pages * 128 * G * Di
+ *   k_new, v_new  bf16 [n_layers][n_rows][G][D];  kidx_new bf16 [n_layers][n_rows][G][Di]
+ *   k_cache, v_cache  bf16 [n_layers][n_pages][128][G][D];  kidx_cache likewise with Di
+ *   block_table   int32 [n_req][max_blocks], the same for every layer
+ *   path, n_accepted  from msa_verify_tree
+ *   new_lens      int32 [n_req]  out: ctx_lens[b] + n_accepted[b]; not ctx_lens itself
+ * A page outside [0, n_pages), a position past max_blocks * 128 or a bad path entry
+ * raises MSA_FLAG_BOUNDS and that token is not written.
+ */
+msa_status_t msa_commit_tree(const void *k_new, const void *v_new, const void *kidx_new, int32_t n_layers,
+                             void *k_cache, void *v_cache, void *kidx_cache, const int32_t *block_table,
+                             const int32_t *ctx_lens, const int32_t *node_off, const int32_t *path,
+                             const int32_t *n_accepted, int32_t n_rows, int32_t n_req, int32_t n_pages,
+                             const msa_dims_t *dims, int32_t *new_lens, int32_t *err_word, msa_stream_t stream);
+
+/*
  * msa_workspace_bytes -- device scratch needed by an operation:
  *   MSA_OP_INVERT: n_rows query rows, n_req requests;
  *   MSA_OP_DECODE: n_rows = B decode requests (n_req ignored);
- *   MSA_OP_PREFILL: n_rows query rows, n_req requests.
+ *   MSA_OP_PREFILL: n_rows query rows, n_req requests;
+ *   MSA_OP_TREE: n_rows rows of drafted trees (padding included), n_req requests.
  * Returns 0 for invalid arguments.
  */
 size_t msa_workspace_bytes(int32_t op, int32_t n_rows, int32_t n_req, const msa_dims_t *dims);
