@@ -1,173 +1,984 @@
-// Sparse attention of drafted trees over the paged cache.
+// Sparse attention of drafted trees over the paged cache, on the 5th-generation tensor cores.
 //
-// Row r of group g attends, with one softmax, the cached tokens of its selected blocks and those of
-// its ancestors (and itself) whose block is selected:
+// Row (node i, head h) of group g attends, with one softmax, the cached tokens of the blocks that node i
+// selected and those of its ancestors (and itself) whose block it selected:
 //   o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),  s_t = sm_scale * q . k_t,  m = max_t s_t.
-// One CTA per (row, group), one thread per token of a 128-token block, an online softmax over blocks.
+//
+// The nodes of a tree agree on many blocks, so the work goes by the union of their selections: each
+// (request, group, up to 256 / HPG nodes) is a tile, its items are the selected blocks (each with the word of
+// the nodes that selected it) and one item for the drafted tokens, and each item's K and V are read once
+// for all nodes of the tile.  That read bounds the kernel as long as several nodes share a block.
+//
+// k_tree_plan, one CTA per tile: the union through a bitmap over blocks in shared memory, ranked by
+// popcounts, hence in ascending block order and the same whatever order its threads run in.
+//
+// k_attn_tree, one persistent CTA per SM: the items of all tiles, in order, are cut into one range per CTA,
+// so one long tile is spread over many SMs and many short ones share them.  The part of a tile inside a
+// range is a segment; it keeps one online softmax.  A tile cut by a range's end leaves partials (unnormalised
+// O, max and sum, in 32 bits) in the workspace, and the CTA that completes the tile joins them in the order
+// of the ranges.  Warps:
+//   0      K/V producer: TMA boxes of 64 columns x 128 tokens (128B swizzle) into a ring of tiles;
+//   2      Q loader: one box of 64 columns x HPG heads x 128/HPG nodes is a whole 128-row tile of Q;
+//   1      MMA issuer: S = Q K^T into the TMEM buffer of a softmax group, then, one unit later, O += P V with
+//          P in TMEM (over S) and V as an MN-major shared-memory operand;
+//   4-7, 8-11  two softmax groups, one thread per row.  With up to 128 rows in the tile they take alternate
+//          items, each with an O of its own, joined at the segment's end; with more, each has half the
+//          rows.  The running maximum is raised only when a logit passes it by 8 (in powers of two), so
+//          that O, in TMEM, is seldom rescaled: P is then at most 2^8, and its rounding to bf16 is relative;
+//   12-15  finite check of V: a row that does not see a token has P = 0 there, and 0 * NaN would still reach its
+//          O through the MMA, so what is not finite is replaced by 0 before the MMA reads it.  Rows that
+//          do see such a value get it back at the segment's end (add_nonfinite), off the hot path.
+// TMEM: S0 | S1 | O0 | O1 (128 + 128 + D + D of 512 columns).  Every wait is bounded.
 #include "msa_device.cuh"
 #include "msa_internal.h"
+
+#include <algorithm>
 
 namespace msa {
 namespace {
 
+constexpr int kThreads = 512;
+constexpr int kMaxCtas = 160;           // partial slots in the workspace; at most one CTA per SM
+constexpr int kOkRing = 8;              // finite-check barriers, by item
+constexpr int kDraftBit = 1 << 30;      // of a tile's item count: its last item is the drafted tokens
+constexpr float kRaise = 8.0f;          // raise the running maximum past this (log2 units)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// One block of a tile's union: its page, the number of cached tokens in it, the nodes that selected it.
+struct __align__(16) Item {
+    int32_t page, n_tok;
+    uint32_t nodes[2];
+};
+
+struct Layout {
+    int per_tile;       // nodes of a tile
+    int chunks;         // tiles per (request, group)
+    int cap;            // items of a tile, at most
+    long long tiles;
+    size_t count, done, dmask, items, part, bytes;
+};
+
+__host__ __device__ constexpr size_t part_floats(int D) { return size_t(256) * D + 512; }   // O, then (m, l) per row
+
+inline Layout layout(int n_rows, int n_req, const Shape &s) {
+    Layout w;
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    w.per_tile = 256 / s.hpg;
+    const int nodes = std::min(n_rows, kTreeMaxNodes);
+    w.chunks = std::max(1, (nodes + w.per_tile - 1) / w.per_tile);
+    w.cap = int(std::min<long long>(1LL * std::min(nodes, w.per_tile) * s.topk, s.max_blocks)) + 1;
+    w.tiles = 1LL * n_req * w.chunks * s.G;
+    w.count = 0;
+    w.done = up(size_t(w.tiles) * 4);
+    w.dmask = w.done + up(size_t(w.tiles) * 4);
+    w.items = w.dmask + up(size_t(n_rows) * s.G * 8);
+    w.part = w.items + up(size_t(w.tiles) * w.cap * sizeof(Item));
+    w.bytes = w.part + size_t(2 * kMaxCtas) * part_floats(s.D) * 4;
+    return w;
+}
+
+// ------------------------------------------------------------------ plan
+
+constexpr int kPlanThreads = 256;
+constexpr int kMaxWords = 16384 / 32;   // bitmap over blocks
+
 template <int D, int HPG>
-__global__ void __launch_bounds__(128) k_attn_tree(
-    const uint16_t *__restrict__ q, const uint16_t *__restrict__ k_cache, const uint16_t *__restrict__ v_cache,
-    const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new, const int32_t *__restrict__ block_table,
-    const int32_t *__restrict__ ctx_lens, const int32_t *__restrict__ node_off, const uint64_t *__restrict__ anc,
-    const int32_t *__restrict__ sel, int n_rows, int n_req, int n_pages, int G, int topk, int max_blocks,
-    float sm_scale, uint16_t *__restrict__ out, float *__restrict__ lse, int32_t *err) {
-    __shared__ float q_s[HPG][D], p_s[HPG][128], red[HPG][4];
-    __shared__ uint8_t see_s[128];
-    const int r = blockIdx.x / G, g = blockIdx.x % G, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int lo = 0, hi = n_req;   // the request: the last b with node_off[b] <= r
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (node_off[mid + 1] <= r) lo = mid + 1;
-        else hi = mid;
-    }
-    if (lo >= n_req) return;   // padding
+__global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
+    const int32_t *__restrict__ sel, const int32_t *__restrict__ block_table, const int32_t *__restrict__ ctx_lens,
+    const int32_t *__restrict__ node_off, const uint64_t *__restrict__ anc, int n_rows, int n_pages, int G, int topk,
+    int max_blocks, int chunks, int cap, int32_t *__restrict__ count, int32_t *__restrict__ done,
+    unsigned long long *__restrict__ dmask, Item *__restrict__ items, uint4 *__restrict__ out,
+    float *__restrict__ lse, int32_t *err) {
+    constexpr int PER = 256 / HPG;                     // nodes of a tile, at most 64
+    constexpr int CAP = PER * 32;                      // items, at most
+    __shared__ uint32_t bits[kMaxWords];
+    __shared__ uint32_t rank[kMaxWords];               // set bits below the word
+    __shared__ uint32_t nodes_of[CAP][PER / 32];
+    __shared__ unsigned long long in_first, in_second; // nodes whose block is ctx / 128, or the next one
+    __shared__ uint32_t has[PER];                      // bit 0 / 1: the node selected that block
+    __shared__ uint32_t draft_nodes[2];
+    __shared__ int wsum[kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tile = blockIdx.x, g = tile % G, chunk = (tile / G) % chunks, b = tile / G / chunks;
+    pdl_wait();
+    pdl_trigger();
     int row0;
-    const int b = lo, n = tree_rows_of(node_off, b, n_rows, err, tid == 0, &row0);
-    if (r < row0 || r >= row0 + n) return;
+    const int n = tree_rows_of(node_off, b, n_rows, err, tid == 0 && g == 0 && chunk == 0, &row0);
+    const int first = chunk * PER, nt = min(PER, n - first);   // this tile's nodes
     const int ctx = ctx_lens[b];
-    if (ctx < 0) {
-        if (tid == 0) raise_flag(err, MSA_FLAG_BOUNDS);
+    if (nt <= 0 || ctx < 0) {
+        if (tid == 0) {
+            if (n > 0 && ctx < 0) raise_flag(err, MSA_FLAG_BOUNDS);
+            count[tile] = 0;
+            done[tile] = 0;
+        }
         return;
     }
-    for (int i = tid; i < HPG * D; i += 128)
-        q_s[i / D][i % D] = bf16_lo(q[(size_t(r) * G + g) * HPG * D + i]);
-    const uint64_t path = anc[r];
-    const int32_t *srow = sel + (size_t(r) * G + g) * topk;
-    constexpr int PER = HPG * D / 128;   // outputs per thread: column d, heads h0, h0 + step, ...
-    const int d = tid % D, h0 = tid / D;
-    constexpr int STEP = 128 / D;
-    float o[PER], m[HPG], l[HPG];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = 0.f;
-#pragma unroll
-    for (int h = 0; h < HPG; ++h) m[h] = -INFINITY, l[h] = 0.f;
+    const int words = (max_blocks + 31) >> 5;
+    for (int i = tid; i < words; i += kPlanThreads) bits[i] = 0;
+    for (int i = tid; i < CAP * (PER / 32); i += kPlanThreads) (&nodes_of[0][0])[i] = 0;
+    if (tid < PER) has[tid] = 0;
+    if (tid == 0) in_first = in_second = 0, draft_nodes[0] = draft_nodes[1] = 0;
     __syncthreads();
-    for (int x = 0; x <= topk; ++x) {   // the selected blocks, then the drafted tokens
-        const uint16_t *kb = nullptr, *vb = nullptr;
-        bool see = false;
-        if (x < topk) {
-            const int j = srow[x];
-            if (j < 0) continue;
-            if (j >= max_blocks) {
-                if (tid == 0) raise_flag(err, MSA_FLAG_BOUNDS);
-                continue;
-            }
-            if (j * 128 >= ctx) continue;
-            const int page = block_table[size_t(b) * max_blocks + j];
-            if (page < 0 || page >= n_pages) {
-                if (tid == 0) raise_flag(err, MSA_FLAG_BOUNDS);
-                continue;
-            }
-            see = j * 128 + tid < ctx;
-            kb = k_cache + (size_t(page) * 128 * G + g) * D;
-            vb = v_cache + (size_t(page) * 128 * G + g) * D;
-        } else {
-            if (tid < n && (path >> tid & 1)) {
-                const int blk = (ctx + __popcll(anc[row0 + tid]) - 1) >> 7;
-                for (int s = 0; s < topk; ++s) see = see || srow[s] == blk;
-            }
-            kb = k_new + (size_t(row0) * G + g) * D;
-            vb = v_new + (size_t(row0) * G + g) * D;
+    const int j0 = ctx >> 7;
+    if (tid < n) {
+        const int j = (ctx + __popcll(anc[row0 + tid]) - 1) >> 7;
+        if (j == j0) atomicOr(&in_first, 1ull << tid);
+        else if (j == j0 + 1) atomicOr(&in_second, 1ull << tid);
+    }
+    const int n_ent = nt * topk;
+    auto entry = [&](int e) { return sel[(size_t(row0 + first + e / topk) * G + g) * topk + e % topk]; };
+    for (int e = tid; e < n_ent; e += kPlanThreads) {
+        const int j = entry(e);
+        if (j < 0) continue;
+        if (j >= max_blocks) {
+            raise_flag(err, MSA_FLAG_BOUNDS);
+            continue;
         }
-        float s[HPG];
+        if (j < j0 || (j == j0 && (ctx & 127))) atomicOr(&bits[j >> 5], 1u << (j & 31));
+        if (j == j0) atomicOr(&has[e / topk], 1u);
+        else if (j == j0 + 1) atomicOr(&has[e / topk], 2u);
+    }
+    __syncthreads();
+    // rank of every word: a scan of the popcounts, two words per thread
+    const int w0 = 2 * tid, w1 = w0 + 1;
+    const int p0 = w0 < words ? __popc(bits[w0]) : 0, p1 = w1 < words ? __popc(bits[w1]) : 0;
+    int incl = p0 + p1;
 #pragma unroll
-        for (int h = 0; h < HPG; ++h) s[h] = 0.f;
-        if (see) {
-            const uint16_t *kt = kb + size_t(tid) * G * D;
-            for (int c = 0; c < D; c += 8) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(kt + c);
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int before = incl - p0 - p1, total = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before += wsum[w];
+        total += wsum[w];
+    }
+    if (w0 < words) rank[w0] = before;
+    if (w1 < words) rank[w1] = before + p0;
+    // the drafted tokens that each node sees
+    if (tid < nt) {
+        unsigned long long m = 0;
+        if (has[tid] & 1) m |= in_first;
+        if (has[tid] & 2) m |= in_second;
+        const int r = row0 + first + tid;
+        m &= anc[r] & (n == 64 ? ~0ull : (1ull << n) - 1);
+        dmask[size_t(r) * G + g] = m;
+        if (m) atomicOr(&draft_nodes[tid >> 5], 1u << (tid & 31));
+    }
+    __syncthreads();
+    for (int e = tid; e < n_ent; e += kPlanThreads) {
+        const int j = entry(e), i = e / topk;
+        if (j < 0 || j >= max_blocks) continue;
+        const uint32_t word = bits[j >> 5];
+        if (!(word >> (j & 31) & 1)) continue;   // a block without cached tokens
+        const int k = rank[j >> 5] + __popc(word & ((1u << (j & 31)) - 1));
+        atomicOr(&nodes_of[k][i >> 5], 1u << (i & 31));
+    }
+    __syncthreads();
+    Item *list = items + size_t(tile) * cap;
+    for (int w = tid; w < words; w += kPlanThreads) {
+        uint32_t word = bits[w];
+        int k = rank[w];
+        while (word) {
+            const int j = w * 32 + __ffs(word) - 1;
+            word &= word - 1;
+            Item it;
+            it.page = block_table[size_t(b) * max_blocks + j];
+            it.n_tok = min(128, ctx - j * 128);
+            it.nodes[0] = nodes_of[k][0];
+            it.nodes[1] = PER > 32 ? nodes_of[k][PER / 32 - 1] : 0u;
+            if (it.page < 0 || it.page >= n_pages) {   // refused: seen by no row
+                raise_flag(err, MSA_FLAG_BOUNDS);
+                it.page = 0;
+                it.nodes[0] = it.nodes[1] = 0;
+            }
+            list[k++] = it;
+        }
+    }
+    const bool drafts = draft_nodes[0] | draft_nodes[1];
+    if (tid == 0) {
+        if (drafts) {
+            Item it;
+            it.page = 0;
+            it.n_tok = n;
+            it.nodes[0] = draft_nodes[0];
+            it.nodes[1] = draft_nodes[1];
+            list[total] = it;
+        }
+        count[tile] = drafts ? (total + 1) | kDraftBit : total;
+        done[tile] = 0;
+    }
+    if (total == 0 && !drafts) {   // nothing is seen: the rows' results are written here
+        constexpr int CH = HPG * D / 8;
+        for (int i = tid; i < nt * CH; i += kPlanThreads)
+            out[(size_t(row0 + first + i / CH) * G + g) * CH + i % CH] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < nt * HPG; i += kPlanThreads)
+            lse[(size_t(row0 + first + i / HPG) * G + g) * HPG + i % HPG] = -INFINITY;
+    }
+}
+
+// ------------------------------------------------------------------ attention
+
+template <int D>
+struct TreeSmem {
+    static constexpr int NSLOT = D == 128 ? 5 : 10;
+    alignas(1024) uint8_t q[2][128 * D * 2];
+    alignas(1024) uint8_t kv[NSLOT][128 * D * 2];   // K and V tiles, alternating
+    float2 join[128];              // the second group's (max, sum), then both groups' weights
+    uint64_t q_full, q_empty;
+    uint64_t full[NSLOT], empty[NSLOT];
+    uint64_t v_ok[kOkRing];
+    uint64_t s_full[2], p_ready[2], o_done[2];
+    uint64_t o_free, drain;
+    int wsum[kThreads / 32];
+    int tile0, off0;
+    uint32_t tmem_base;
+    int abort, nonfinite, last;
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {   // MUFU.EX2, relative error about 2^-22
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// KSTEPS MMAs of S = Q K^T (K = 16 each), A and B K-major with 128-byte swizzle: a k-step advances 32 bytes
+// within a 64-column box and 16 KB between boxes (+2 / +1024 in the descriptors' units of 16 bytes).
+template <int KSTEPS>
+__device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+    for (int k = 0; k < KSTEPS; ++k) {
+        const uint64_t o = uint64_t((k & 3) * 2 + (k >> 2) * 1024);
+        mma_bf16(d, a + o, b + o, idesc, k > 0);
+    }
+}
+
+// O (+)= P V over 64 tokens: A = P in TMEM (8 columns per 16 tokens), B = V (2 KB per 16 tokens).
+__device__ __forceinline__ void mma_pv64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&r)[32]) {
+    uint32_t lo[16], hi[16];
 #pragma unroll
-                    for (int h = 0; h < HPG; ++h) {
-                        s[h] = fmaf(q_s[h][c + 2 * e], bf16_lo(ws[e]), s[h]);
-                        s[h] = fmaf(q_s[h][c + 2 * e + 1], bf16_hi(ws[e]), s[h]);
+    for (int i = 0; i < 16; ++i) lo[i] = __float_as_uint(r[i]), hi[i] = __float_as_uint(r[i + 16]);
+    tmem_st16(taddr, lo);
+    tmem_st16(taddr + 16, hi);
+}
+
+// Both softmax groups.
+__device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+__device__ __forceinline__ long long range_begin(int c, long long n, int C) { return c * n / C; }
+__device__ __forceinline__ int range_owner(long long x, long long n, int C) { return int(((x + 1) * C - 1) / n); }
+
+// The CTA's segments in order; every role walks them for itself.
+struct Walk {
+    const int32_t *count;
+    long long x, x1;
+    int tile, off, end, n_items, seg;
+    bool drafts;
+    __device__ __forceinline__ bool next() {   // the next segment: items off .. end-1 of `tile`, n_items in it
+        if (seg >= 0) {
+            x += end - off;
+            ++tile;
+            off = 0;
+        }
+        if (x >= x1) return false;
+        int c;
+        while (!((c = count[tile]) & ~kDraftBit)) ++tile;
+        n_items = c & ~kDraftBit;
+        drafts = c & kDraftBit;
+        end = int(min((long long)n_items, off + (x1 - x)));
+        ++seg;
+        return true;
+    }
+};
+
+// What a tile is of: request, group, nodes.
+struct TileOf {
+    int b, g, row, nt, n, row0;
+    __device__ __forceinline__ TileOf(int tile, int G, int chunks, int per, const int32_t *node_off) {
+        g = tile % G;
+        const int chunk = tile / G % chunks;
+        b = tile / G / chunks;
+        row0 = node_off[b];
+        n = node_off[b + 1] - row0;
+        row = row0 + chunk * per;
+        nt = min(per, n - chunk * per);
+    }
+};
+
+__device__ __forceinline__ uint32_t exp_all_ones(uint32_t w) {   // 0x8000 in each half that is inf or NaN
+    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
+template <int D, int HPG>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
+    const uint16_t *__restrict__ q, const __grid_constant__ CUtensorMap qmap,
+    const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+    const __grid_constant__ CUtensorMap knmap, const __grid_constant__ CUtensorMap vnmap,
+    const uint16_t *__restrict__ k_cache, const uint16_t *__restrict__ v_cache, const uint16_t *__restrict__ k_new,
+    const uint16_t *__restrict__ v_new, const int32_t *__restrict__ node_off, int G, int chunks, int cap, int n_tiles,
+    float sm_scale, const int32_t *__restrict__ count, int32_t *__restrict__ done,
+    const unsigned long long *__restrict__ dmask, const Item *__restrict__ items, float *__restrict__ part,
+    uint16_t *__restrict__ out, float *__restrict__ lse, int32_t *err) {
+    using Smem = TreeSmem<D>;
+    constexpr int NSLOT = Smem::NSLOT;
+    constexpr int NSUB = D / 64;
+    constexpr int PER = 256 / HPG;     // nodes of a tile
+    constexpr int NPM = 128 / HPG;     // nodes of a 128-row MMA tile
+    constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t kIdescS64 = make_idesc_bf16(128, 64, 0, 0);
+    constexpr uint32_t kIdescO = make_idesc_bf16(128, D, 0, 1);
+    extern __shared__ uint8_t smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_empty, 1);
+        for (int i = 0; i < NSLOT; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < kOkRing; ++i) mbar_init(&sm.v_ok[i], 4);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&sm.s_full[w], 1);
+            mbar_init(&sm.p_ready[w], 4);
+            mbar_init(&sm.o_done[w], 1);
+        }
+        mbar_init(&sm.o_free, 8);
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        sm.nonfinite = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+        tma_prefetch_desc(&qmap);
+    }
+    pdl_wait();   // the plan
+    // this CTA's range: a scan of the tiles' item counts, a run of tiles per thread
+    const int t_lo = int((long long)tid * n_tiles / kThreads), t_hi = int((long long)(tid + 1) * n_tiles / kThreads);
+    int mine = 0;
+    for (int t = t_lo; t < t_hi; ++t) mine += count[t] & ~kDraftBit;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sm.wsum[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long before = incl - mine, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sm.wsum[w];
+        total += sm.wsum[w];
+    }
+    const int C = int(min((long long)gridDim.x, max(total, 1LL))), cta = blockIdx.x;   // no range is empty
+    const long long x0 = cta < C ? range_begin(cta, total, C) : total;
+    const long long x1 = cta < C ? range_begin(cta + 1, total, C) : total;
+    if (x0 < x1 && x0 >= before && x0 < before + mine) {
+        int t = t_lo;
+        long long at = before;
+        for (;; ++t) {
+            const int c = count[t] & ~kDraftBit;
+            if (x0 < at + c) break;
+            at += c;
+        }
+        sm.tile0 = t;
+        sm.off0 = int(x0 - at);
+    }
+    __syncthreads();
+    const uint32_t tmem = sm.tmem_base;
+    Walk wk{count, x0, x1, x0 < x1 ? sm.tile0 : 0, x0 < x1 ? sm.off0 : 0, 0, 0, -1, false};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ K/V producer (lane 0)
+        if (lane == 0) {
+            int seq = 0;
+            bool ok = true;
+            while (ok && wk.next()) {
+                const TileOf t(wk.tile, G, chunks, PER, node_off);
+                const Item *list = items + size_t(wk.tile) * cap;
+                int page = list[wk.off].page;
+                for (int i = wk.off; ok && i < wk.end; ++i) {
+                    const int page_i = page;
+                    if (i + 1 < wk.end) page = list[i + 1].page;   // one ahead
+                    const bool draft = wk.drafts && i == wk.n_items - 1;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++seq) {
+                        const int slot = seq % NSLOT;
+                        if (seq >= NSLOT && !mbar_wait(&sm.empty[slot], (seq / NSLOT - 1) & 1, err, &sm.abort)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&sm.full[slot], draft ? 64 * D * 2 : 128 * D * 2);
+#pragma unroll
+                        for (int c = 0; c < NSUB; ++c) {
+                            uint8_t *dst = sm.kv[slot] + c * 16384;
+                            if (draft) tma_load_3d(dst, kv ? &vnmap : &knmap, &sm.full[slot], c * 64, t.g, t.row0);
+                            else tma_load_4d(dst, kv ? &vmap : &kmap, &sm.full[slot], c * 64, t.g, 0, page_i);
+                        }
                     }
+                }
+            }
+            if (sm.abort)   // the copies still in flight land before the CTA exits
+                for (int s = max(0, seq - NSLOT); s < seq; ++s)
+                    mbar_wait(&sm.full[s % NSLOT], (s / NSLOT) & 1, err, nullptr);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ Q loader (lane 0)
+        if (lane == 0) {
+            int loads = 0;
+            while (wk.next()) {
+                if (wk.seg > 0 && !mbar_wait(&sm.q_empty, (wk.seg - 1) & 1, err, &sm.abort)) break;
+                const TileOf t(wk.tile, G, chunks, PER, node_off);
+                const int nm = t.nt > NPM ? 2 : 1;
+                mbar_arrive_expect_tx(&sm.q_full, nm * 128 * D * 2);
+                for (int m = 0; m < nm; ++m)
+#pragma unroll
+                    for (int c = 0; c < NSUB; ++c)
+                        tma_load_3d(sm.q[m] + c * 16384, &qmap, &sm.q_full, c * 64, t.g * HPG, t.row + m * NPM);
+                ++loads;
+            }
+            if (sm.abort && loads) mbar_wait(&sm.q_full, (loads - 1) & 1, err, nullptr);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (lane 0)
+        if (lane == 0) {
+            int it = 0;                       // items of this CTA so far
+            int units[2] = {0, 0};            // PV units issued per group
+            bool ok = true;
+            struct Unit {
+                int w, it, acc;
+                bool draft, first_of_item, last_of_item;
+            } pend{};
+            bool have = false, o_wait = false;
+            auto issue_pv = [&]() -> bool {
+                const int w = pend.w, seq = 2 * pend.it + 1, slot = seq % NSLOT;
+                if (o_wait) {                 // both groups have read the O of the segment before
+                    if (!mbar_wait(&sm.o_free, (wk.seg - 1) & 1, err, &sm.abort)) return false;
+                    o_wait = false;
+                }
+                if (pend.first_of_item &&
+                    !mbar_wait(&sm.v_ok[pend.it % kOkRing], (pend.it / kOkRing) & 1, err, &sm.abort))
+                    return false;
+                if (!mbar_wait(&sm.p_ready[w], units[w] & 1, err, &sm.abort)) return false;
+                ++units[w];
+                tc_fence_after();
+                const uint64_t vd = make_smem_desc(smem_u32(sm.kv[slot]), 16384, 1024, 2);
+                const uint32_t d = tmem + uint32_t(256 + w * D), a = tmem + uint32_t(w * 128);
+                mma_pv64(d, a, vd, kIdescO, pend.acc);
+                if (!pend.draft) mma_pv64(d, a + 32, vd + 512, kIdescO, 1u);
+                mma_commit(&sm.o_done[w]);
+                if (pend.last_of_item) mma_commit(&sm.empty[slot]);
+                have = false;
+                return true;
+            };
+            while (ok && wk.next()) {
+                const TileOf t(wk.tile, G, chunks, PER, node_off);
+                const int nm = t.nt > NPM ? 2 : 1;
+                o_wait = wk.seg > 0;
+                if (!mbar_wait(&sm.q_full, wk.seg & 1, err, &sm.abort)) break;
+                int u = 0;                    // units of this segment
+                for (int i = wk.off; ok && i < wk.end; ++i, ++it) {
+                    const bool draft = wk.drafts && i == wk.n_items - 1;
+                    const int seq = 2 * it, slot = seq % NSLOT;
+                    if (!mbar_wait(&sm.full[slot], (seq / NSLOT) & 1, err, &sm.abort)) {
+                        ok = false;
+                        break;
+                    }
+                    for (int m = 0; m < nm; ++m, ++u) {
+                        const int w = u & 1;
+                        tc_fence_after();
+                        mma_s<D / 16>(tmem + uint32_t(w * 128), make_smem_desc(smem_u32(sm.q[m]), 16, 1024, 2),
+                                      make_smem_desc(smem_u32(sm.kv[slot]), 16, 1024, 2), draft ? kIdescS64 : kIdescS);
+                        mma_commit(&sm.s_full[w]);
+                        if (m == nm - 1) mma_commit(&sm.empty[slot]);
+                        if (m == nm - 1 && i == wk.end - 1) mma_commit(&sm.q_empty);
+                        if (have && !issue_pv()) {
+                            ok = false;
+                            break;
+                        }
+                        pend.w = w;
+                        pend.it = it;
+                        pend.acc = u >= 2;
+                        pend.draft = draft;
+                        pend.first_of_item = m == 0;
+                        pend.last_of_item = m == nm - 1;
+                        have = true;
+                    }
+                }
+                if (ok && have && !issue_pv()) ok = false;
+            }
+            mma_commit(&sm.drain);
+            mbar_wait(&sm.drain, 0, err, nullptr);
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------ finite check of V
+        const int th = tid - 12 * 32;
+        int it = 0;
+        bool ok = true;
+        while (ok && wk.next()) {
+            for (int i = wk.off; i < wk.end; ++i, ++it) {
+                const bool draft = wk.drafts && i == wk.n_items - 1;
+                const int seq = 2 * it + 1, slot = seq % NSLOT;
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[slot], (seq / NSLOT) & 1, err, &sm.abort))) {
+                    ok = false;
+                    break;
+                }
+                const int per_box = draft ? 512 : 1024;   // 16-byte chunks of a box
+                uint32_t acc = 0;
+#pragma unroll
+                for (int c = 0; c < NSUB; ++c) {
+                    const uint4 *box = reinterpret_cast<const uint4 *>(sm.kv[slot] + c * 16384);
+#pragma unroll 4
+                    for (int k = th; k < per_box; k += 128) {
+                        const uint4 v = box[k];
+                        acc |= exp_all_ones(v.x) | exp_all_ones(v.y) | exp_all_ones(v.z) | exp_all_ones(v.w);
+                    }
+                }
+                if (acc) {
+                    const int n_tok = items[size_t(wk.tile) * cap + i].n_tok;
+                    for (int c = 0; c < NSUB; ++c) {
+                        uint32_t *box = reinterpret_cast<uint32_t *>(sm.kv[slot] + c * 16384);
+                        for (int k = th; k < per_box; k += 128)
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t v = box[4 * k + e], hit = exp_all_ones(v);
+                                if (!hit) continue;
+                                box[4 * k + e] = v & ~((hit >> 15) * 0xffffu);
+                                if (k / 8 < n_tok) sm.nonfinite = 1;   // 8 chunks of a box per token
+                            }
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.v_ok[it % kOkRing]);
             }
         }
-        see_s[tid] = see;
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ softmax groups (warps 4-11)
+        const int w = (warp - 4) >> 2;
+        const int quad = warp & 3;                 // TMEM lanes this warp may access
+        const int row = quad * 32 + lane;
+        const uint32_t lane_off = uint32_t(quad * 32) << 16;
+        const uint32_t t_s = tmem + lane_off + uint32_t(w * 128);
+        const uint32_t t_o = tmem + lane_off + 256u;   // + group * D
+        const float scale = sm_scale * kLog2e;
+        int units[2] = {0, 0};                     // units of both groups so far
+        bool ok = true;   // once a wait has run out the groups only keep in step, so that no barrier is missed
+        while (wk.next()) {
+            const TileOf t(wk.tile, G, chunks, PER, node_off);
+            const int nm = t.nt > NPM ? 2 : 1;
+            const Item *list = items + size_t(wk.tile) * cap;
+            const int mt = nm == 2 ? w : 0;
+            const int node = mt * NPM + row / HPG;                 // within the tile
+            const bool live = node < t.nt;
+            const bool warp_live = mt * NPM + quad * 32 / HPG < t.nt;
+            const unsigned long long dm = live ? dmask[size_t(t.row + node) * G + t.g] : 0ull;
+            const int len = wk.end - wk.off;
+            const int step = nm == 2 ? 1 : 2, i0 = wk.off + (nm == 2 ? 0 : w);
+            float m = -INFINITY, l = 0.f;
+            int mine_n = 0;
+            Item next = i0 < wk.end ? list[i0] : Item{};
+            for (int i = i0; ok && i < wk.end; i += step, ++mine_n) {
+                const Item item = next;
+                if (i + step < wk.end) next = list[i + step];
+                const bool draft = wk.drafts && i == wk.n_items - 1;
+                const bool sees = live && (item.nodes[node >> 5] >> (node & 31) & 1);
+                // the tokens of 32 columns from c on that this row sees
+                auto seen = [&](int c) -> uint32_t {
+                    if (draft) return c < 64 ? uint32_t(dm >> c) : 0u;
+                    if (!sees || item.n_tok <= c) return 0u;
+                    return item.n_tok - c >= 32 ? ~0u : (1u << (item.n_tok - c)) - 1u;
+                };
+                const int k = units[w] + mine_n;
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[w], k & 1, err, &sm.abort))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (warp_live) {
+                    const int cols = draft ? 64 : 128;
+                    if (!__any_sync(0xffffffffu, sees)) {
+                        const uint32_t z[16] = {};
+#pragma unroll 1
+                        for (int c = 0; c < cols; c += 32) tmem_st16(t_s + uint32_t(c >> 1), z);
+                    } else {
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < cols; c += 32) {
+                            const uint32_t see = seen(c);
+                            if (!__any_sync(0xffffffffu, see)) continue;
+                            uint32_t v[32];
+                            tmem_ld32(t_s + uint32_t(c), v);
+                            tmem_ld_wait();
+                            if (__all_sync(0xffffffffu, see == ~0u || see == 0u)) {
+                                float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < HPG; ++h) {
-            s[h] = see ? s[h] * sm_scale : -INFINITY;
-            float v = s[h];
-            for (int off = 16; off; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-            if (lane == 0) red[h][warp] = v;
+                                for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x)
+                                        a[x] = fmax3(a[x], __uint_as_float(v[e + x]), __uint_as_float(v[e + 4 + x]));
+                                if (see) mx = fmaxf(mx, fmax3(fmaxf(a[0], a[1]), a[2], a[3]));
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    mx = fmaxf(mx, see >> e & 1 ? __uint_as_float(v[e]) : -INFINITY);
+                            }
+                        }
+                        const float top = mx * scale;      // -inf: nothing seen in this item
+                        const bool raise = top > m + kRaise || (m == -INFINITY && top > m);
+                        // O of a row that has seen nothing yet is 0 and needs no rescaling
+                        const float fac = raise && m != -INFINITY ? fast_exp2(m - top) : 1.f;
+                        if (raise) m = top;
+                        l *= fac;
+                        if (mine_n > 0 && __any_sync(0xffffffffu, fac != 1.f)) {
+                            if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_done[w], (k - 1) & 1, err, &sm.abort))) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t v[32];
+                                tmem_ld32(t_o + uint32_t(w * D + c), v);
+                                tmem_ld_wait();
+                                float o[32];
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * fac;
+                                tmem_st32(t_o + uint32_t(w * D + c), o);
+                            }
+                        }
+                        const float nm_ = m == -INFINITY ? 0.f : -m;
+#pragma unroll 1
+                        for (int c = 0; c < cols; c += 32) {
+                            const uint32_t see = seen(c);
+                            uint32_t p[16];
+                            if (!__any_sync(0xffffffffu, see)) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) p[e] = 0u;
+                            } else {
+                                uint32_t v[32];
+                                tmem_ld32(t_s + uint32_t(c), v);
+                                tmem_ld_wait();
+                                float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                                if (__all_sync(0xffffffffu, see == ~0u || see == 0u)) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        const float pa = fast_exp2(fmaf(__uint_as_float(v[2 * e]), scale, nm_));
+                                        const float pb = fast_exp2(fmaf(__uint_as_float(v[2 * e + 1]), scale, nm_));
+                                        s4[(2 * e) & 3] += pa;
+                                        s4[(2 * e + 1) & 3] += pb;
+                                        p[e] = see ? pack_bf16x2(pa, pb) : 0u;
+                                    }
+                                    if (see) l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        float pa = fast_exp2(fmaf(__uint_as_float(v[2 * e]), scale, nm_));
+                                        float pb = fast_exp2(fmaf(__uint_as_float(v[2 * e + 1]), scale, nm_));
+                                        pa = see >> (2 * e) & 1 ? pa : 0.f;
+                                        pb = see >> (2 * e + 1) & 1 ? pb : 0.f;
+                                        s4[(2 * e) & 3] += pa;
+                                        s4[(2 * e + 1) & 3] += pb;
+                                        p[e] = pack_bf16x2(pa, pb);
+                                    }
+                                    l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                                }
+                            }
+                            tmem_st16(t_s + uint32_t(c >> 1), p);
+                        }
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_ready[w]);
+            }
+            // units of both groups in this segment
+            const int n0 = nm == 2 ? len : (len + 1) / 2, n1 = nm == 2 ? len : len / 2;
+            units[0] += n0;
+            units[1] += n1;
+            ok = __all_sync(0xffffffffu, ok && (n0 == 0 || mbar_wait(&sm.o_done[0], (units[0] - 1) & 1, err, &sm.abort)) &&
+                                             (n1 == 0 || mbar_wait(&sm.o_done[1], (units[1] - 1) & 1, err, &sm.abort)));
+            tc_fence_after();
+            // The segment's (max, sum) of the row and the weights of the two O's.
+            float wa = 1.f, wb = 0.f;      // of O0 and O1 (nm == 1), or of the group's own O (nm == 2)
+            if (nm == 1) {
+                if (w == 1) sm.join[row] = make_float2(m, l);
+                groups_sync();
+                if (w == 0) {
+                    const float2 o = sm.join[row];
+                    const float top = fmaxf(m, o.x);
+                    wa = m == -INFINITY ? 0.f : fast_exp2(m - top);
+                    wb = o.x == -INFINITY ? 0.f : fast_exp2(o.x - top);
+                    l = l * wa + o.y * wb;
+                    m = top;
+                    sm.join[row] = make_float2(wa, wb);
+                }
+                groups_sync();
+                if (w == 1) {
+                    const float2 o = sm.join[row];
+                    wa = o.x;
+                    wb = o.y;
+                }
+            }
+            const long long seg_x = wk.x;                               // first item of the segment
+            const long long tile_x = seg_x - wk.off;                    // first item of the tile
+            const bool whole = wk.off == 0 && wk.end == wk.n_items;
+            const int c_lo = nm == 2 ? 0 : w * (D / 2), c_hi = nm == 2 ? D : c_lo + D / 2;
+            float *slot = part + size_t(2 * cta + (wk.off > 0 ? 0 : 1)) * part_floats(D);
+            float2 *slot_ml = reinterpret_cast<float2 *>(slot + 256 * D);
+            const size_t orow = (size_t(t.row + node) * G + t.g) * HPG + row % HPG;
+            if (nm == 1) {                         // group 0's total for group 1
+                groups_sync();                     // the weights have been read
+                if (w == 0) sm.join[row] = make_float2(m, l);
+                groups_sync();
+                if (w == 1) {
+                    m = sm.join[row].x;
+                    l = sm.join[row].y;
+                }
+            }
+            const bool fix = *reinterpret_cast<volatile int *>(&sm.nonfinite);
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            if (warp_live && ok) {
+#pragma unroll 1
+                for (int c = c_lo; c < c_hi; c += 32) {
+                    __syncwarp();
+                    uint32_t va[32];
+                    float o[32];
+                    if (nm == 2) {
+                        tmem_ld32(t_o + uint32_t(w * D + c), va);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(va[e]);
+                    } else {
+                        tmem_ld32(t_o + uint32_t(c), va);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = wa == 0.f ? 0.f : __uint_as_float(va[e]) * wa;
+                        if (n1 > 0) {
+                            tmem_ld32(t_o + uint32_t(D + c), va);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = wb == 0.f ? o[e] : fmaf(__uint_as_float(va[e]), wb, o[e]);
+                        }
+                    }
+                    if (fix && live) {
+                        // values that are not finite were taken out of V: p * v of those this row sees
+                        for (int i = wk.off; i < wk.end; ++i) {
+                            const Item item = list[i];
+                            const bool draft = wk.drafts && i == wk.n_items - 1;
+                            if (!(item.nodes[node >> 5] >> (node & 31) & 1)) continue;
+                            for (int tok = 0; tok < item.n_tok; ++tok) {
+                                if (draft && !(dm >> tok & 1)) continue;
+                                const size_t at = draft ? (size_t(t.row0 + tok) * G + t.g) * D
+                                                        : ((size_t(item.page) * 128 + tok) * G + t.g) * D;
+                                const uint4 *v4 = reinterpret_cast<const uint4 *>((draft ? v_new : v_cache) + at + c);
+                                const uint4 x[4] = {v4[0], v4[1], v4[2], v4[3]};
+                                uint32_t any = 0;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    any |= exp_all_ones(x[y].x) | exp_all_ones(x[y].y) | exp_all_ones(x[y].z) |
+                                           exp_all_ones(x[y].w);
+                                if (!any) continue;
+                                const uint16_t *kr = (draft ? k_new : k_cache) + at, *qr = q + orow * D;
+                                float s = 0.f;
+                                for (int d = 0; d < D; ++d) s = fmaf(bf16_lo(qr[d]), bf16_lo(kr[d]), s);
+                                const float p = fast_exp2(fmaf(s, scale, -m));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const uint4 &y = x[e >> 3];
+                                    const uint32_t word = (e >> 1 & 3) == 0   ? y.x
+                                                          : (e >> 1 & 3) == 1 ? y.y
+                                                          : (e >> 1 & 3) == 2 ? y.z
+                                                                              : y.w;
+                                    const float val = e & 1 ? bf16_hi(word) : bf16_lo(word);
+                                    if (isinf(val) || isnan(val)) o[e] = fmaf(p, val, o[e]);
+                                }
+                            }
+                        }
+                    }
+                    if (whole) {
+                        if (live) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                *reinterpret_cast<uint4 *>(out + orow * D + c + e) =
+                                    make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv),
+                                               pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                               pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
+                                               pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+                        }
+                    } else {
+                        // partial: 16-byte chunks, rows innermost, so that a warp stores whole lines
+                        float4 *po = reinterpret_cast<float4 *>(slot) + size_t(mt * (D / 4) + c / 4) * 128 + row;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            po[size_t(e / 4) * 128] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                if (nm == 2 || w == 0) {
+                    if (!whole) slot_ml[mt * 128 + row] = make_float2(m, l);
+                    else if (live) lse[orow] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.o_free);
+            if (whole) continue;
+            // a cut tile: the CTA that completes it joins the partials of all its ranges
+            groups_sync();   // every partial store of this CTA precedes the release below
+            if (tid == 4 * 32) {
+                __threadfence();
+                sm.last = atomicAdd(done + wk.tile, len) + len == wk.n_items;
+                __threadfence();
+            }
+            groups_sync();
+            if (!*reinterpret_cast<volatile int *>(&sm.last)) continue;
+            if (!warp_live) continue;
+            const int ca = range_owner(tile_x, total, C), cb = range_owner(tile_x + wk.n_items - 1, total, C);
+            auto slot_of = [&](int c) {
+                return part + size_t(2 * c + (range_begin(c, total, C) > tile_x ? 0 : 1)) * part_floats(D);
+            };
+            float top = -INFINITY;
+            for (int c = ca; c <= cb; ++c)
+                top = fmaxf(top, __ldcg(reinterpret_cast<const float2 *>(slot_of(c) + 256 * D) + mt * 128 + row).x);
+            const float ntop = top == -INFINITY ? 0.f : -top;
+            float sum = 0.f;
+            for (int c = ca; c <= cb; ++c) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot_of(c) + 256 * D) + mt * 128 + row);
+                sum += ml.y * fast_exp2(ml.x + ntop);
+            }
+            const float rcp = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+#pragma unroll 1
+            for (int cc = c_lo; cc < c_hi; cc += 32) {
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                for (int c = ca; c <= cb; ++c) {
+                    const float *base = slot_of(c);
+                    const float wgt =
+                        fast_exp2(__ldcg(reinterpret_cast<const float2 *>(base + 256 * D) + mt * 128 + row).x + ntop);
+                    const float4 *po = reinterpret_cast<const float4 *>(base) + size_t(mt * (D / 4) + cc / 4) * 128 + row;
+                    float4 v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = __ldcg(po + size_t(e) * 128);
+                    if (wgt == 0.f) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        o[4 * e] = fmaf(wgt, v[e].x, o[4 * e]);
+                        o[4 * e + 1] = fmaf(wgt, v[e].y, o[4 * e + 1]);
+                        o[4 * e + 2] = fmaf(wgt, v[e].z, o[4 * e + 2]);
+                        o[4 * e + 3] = fmaf(wgt, v[e].w, o[4 * e + 3]);
+                    }
+                }
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(out + orow * D + cc + e) = make_uint4(
+                            pack_bf16x2(o[e] * rcp, o[e + 1] * rcp), pack_bf16x2(o[e + 2] * rcp, o[e + 3] * rcp),
+                            pack_bf16x2(o[e + 4] * rcp, o[e + 5] * rcp), pack_bf16x2(o[e + 6] * rcp, o[e + 7] * rcp));
+                }
+            }
+            if (live && (nm == 2 || w == 0)) lse[orow] = sum > 0.f || sum != sum ? (top + log2f(sum)) * kLn2 : -INFINITY;
         }
-        __syncthreads();
-        float alpha[HPG];
-#pragma unroll
-        for (int h = 0; h < HPG; ++h) {
-            const float mn = fmaxf(m[h], fmaxf(fmaxf(red[h][0], red[h][1]), fmaxf(red[h][2], red[h][3])));
-            alpha[h] = mn == -INFINITY ? 1.f : expf(m[h] - mn);
-            m[h] = mn;
-            p_s[h][tid] = see ? expf(s[h] - mn) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < HPG; ++h) l[h] *= alpha[h];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            float a = 1.f;
-#pragma unroll
-            for (int h = 0; h < HPG; ++h) a = h == h0 + i * STEP ? alpha[h] : a;
-            o[i] *= a;
-        }
-        for (int t = 0; t < 128; ++t) {
-            if (!see_s[t]) continue;
-            const float v = bf16_lo(vb[size_t(t) * G * D + d]);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) o[i] = fmaf(p_s[h0 + i * STEP][t], v, o[i]);
-#pragma unroll
-            for (int h = 0; h < HPG; ++h) l[h] += p_s[h][t];
-        }
-        __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int h = h0 + i * STEP;
-        float lh = 0.f, mh = 0.f;
-#pragma unroll
-        for (int e = 0; e < HPG; ++e)
-            if (e == h) lh = l[e], mh = m[e];
-        const size_t row = (size_t(r) * G + g) * HPG + h;
-        out[row * D + d] = uint16_t(pack_bf16x2(lh > 0.f || lh != lh ? o[i] / lh : 0.f, 0.f) & 0xffffu);
-        if (d == 0) lse[row] = lh > 0.f || lh != lh ? mh + logf(lh) : -INFINITY;
-    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 template <int D, int HPG>
 cudaError_t launch_t(const void *q, const void *k_cache, const void *v_cache, const void *k_new, const void *v_new,
                      const int32_t *bt, const int32_t *ctx, const int32_t *node_off, const uint64_t *anc,
                      const int32_t *sel, int n_rows, int n_req, int n_pages, const Shape &s, void *out, float *lse,
-                     int32_t *err, cudaStream_t st) {
-    k_attn_tree<D, HPG><<<unsigned(n_rows) * unsigned(s.G), 128, 0, st>>>(
-        static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k_cache),
-        static_cast<const uint16_t *>(v_cache), static_cast<const uint16_t *>(k_new),
-        static_cast<const uint16_t *>(v_new), bt, ctx, node_off, anc, sel, n_rows, n_req, n_pages, s.G, s.topk,
-        s.max_blocks, s.sm_scale, static_cast<uint16_t *>(out), lse, err);
-    return cudaGetLastError();
+                     void *ws, int32_t *err, cudaStream_t st) {
+    const Layout w = layout(n_rows, n_req, s);
+    if (w.tiles * w.cap > 0x3fffffffLL) return cudaErrorNotSupported;
+    alignas(64) CUtensorMap qm, km, vm, kn, vn;
+    const char *why = nullptr;
+    {
+        const uint64_t dims[3] = {uint64_t(D), uint64_t(s.Hq), uint64_t(n_rows)};
+        const uint64_t strides[2] = {uint64_t(D) * 2, uint64_t(s.Hq) * D * 2};
+        const uint32_t box[3] = {64u, uint32_t(HPG), uint32_t(128 / HPG)};
+        if (!encode_tensor_map(&qm, 3, q, dims, strides, box, 128, &why)) return cudaErrorInvalidValue;
+    }
+    {
+        const uint64_t dims[4] = {uint64_t(D), uint64_t(s.G), 128ull, uint64_t(n_pages)};
+        const uint64_t strides[3] = {uint64_t(D) * 2, uint64_t(s.G) * D * 2, 128ull * s.G * D * 2};
+        const uint32_t box[4] = {64u, 1u, 128u, 1u};
+        if (!encode_tensor_map(&km, 4, k_cache, dims, strides, box, 128, &why)) return cudaErrorInvalidValue;
+        if (!encode_tensor_map(&vm, 4, v_cache, dims, strides, box, 128, &why)) return cudaErrorInvalidValue;
+    }
+    {
+        const uint64_t dims[3] = {uint64_t(D), uint64_t(s.G), uint64_t(n_rows)};
+        const uint64_t strides[2] = {uint64_t(D) * 2, uint64_t(s.G) * D * 2};
+        const uint32_t box[3] = {64u, 1u, 64u};
+        if (!encode_tensor_map(&kn, 3, k_new, dims, strides, box, 128, &why)) return cudaErrorInvalidValue;
+        if (!encode_tensor_map(&vn, 3, v_new, dims, strides, box, 128, &why)) return cudaErrorInvalidValue;
+    }
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    int32_t *count = reinterpret_cast<int32_t *>(base + w.count), *done = reinterpret_cast<int32_t *>(base + w.done);
+    auto *dmask = reinterpret_cast<unsigned long long *>(base + w.dmask);
+    Item *items = reinterpret_cast<Item *>(base + w.items);
+    float *part = reinterpret_cast<float *>(base + w.part);
+    cudaError_t e = launch_kernel(k_tree_plan<D, HPG>, dim3(unsigned(w.tiles)), dim3(kPlanThreads), 0, st, true, sel, bt,
+                                  ctx, node_off, anc, n_rows, n_pages, s.G, s.topk, s.max_blocks, w.chunks, w.cap,
+                                  count, done, dmask, items, static_cast<uint4 *>(out), lse, err);
+    if (e != cudaSuccess) return e;
+    const size_t smem = sizeof(TreeSmem<D>) + 1024;
+    static_assert(sizeof(TreeSmem<D>) + 1024 <= 232448, "shared memory of a CTA");
+    e = cudaFuncSetAttribute(k_attn_tree<D, HPG>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    const int grid = std::min(sm_count(), kMaxCtas);
+    return launch_kernel(k_attn_tree<D, HPG>, dim3(unsigned(grid)), dim3(kThreads), smem, st, true,
+                         static_cast<const uint16_t *>(q), qm, km, vm, kn, vn, static_cast<const uint16_t *>(k_cache),
+                         static_cast<const uint16_t *>(v_cache), static_cast<const uint16_t *>(k_new),
+                         static_cast<const uint16_t *>(v_new), node_off, s.G, w.chunks, w.cap, int(w.tiles), s.sm_scale,
+                         static_cast<const int32_t *>(count), done, static_cast<const unsigned long long *>(dmask),
+                         static_cast<const Item *>(items), part, static_cast<uint16_t *>(out), lse, err);
 }
 
 }  // namespace
 
-size_t tree_workspace_bytes(int, int, const Shape &) { return 16; }
+size_t tree_workspace_bytes(int n_rows, int n_req, const Shape &s) { return layout(n_rows, n_req, s).bytes; }
 
 cudaError_t launch_attn_tree(const void *q, const void *k_cache, const void *v_cache, const void *k_new,
                              const void *v_new, const int32_t *block_table, const int32_t *ctx_lens,
                              const int32_t *node_off, const uint64_t *anc, const int32_t *sel, int n_rows, int n_req,
-                             int n_pages, const Shape &s, void *out, float *lse, void *, int32_t *err,
+                             int n_pages, const Shape &s, void *out, float *lse, void *ws, int32_t *err,
                              cudaStream_t st) {
 #define MSA_AT_CASE(DD, HH)                                                                                      \
     if (s.D == DD && s.hpg == HH)                                                                                \
         return launch_t<DD, HH>(q, k_cache, v_cache, k_new, v_new, block_table, ctx_lens, node_off, anc, sel, n_rows, \
-                                n_req, n_pages, s, out, lse, err, st);
+                                n_req, n_pages, s, out, lse, ws, err, st);
     MSA_AT_CASE(128, 8) MSA_AT_CASE(128, 4) MSA_AT_CASE(64, 8) MSA_AT_CASE(64, 4)
 #undef MSA_AT_CASE
     return cudaErrorNotSupported;
