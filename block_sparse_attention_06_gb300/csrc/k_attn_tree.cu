@@ -15,8 +15,9 @@
 // k_attn_tree, one persistent CTA per SM: the items of all tiles, in order, are cut into one range per CTA,
 // so one long tile is spread over many SMs and many short ones share them.  The part of a tile inside a
 // range is a segment; it keeps one online softmax.  A tile cut by a range's end leaves partials (unnormalised
-// O, max and sum, in 32 bits) in the workspace, and the CTA that completes the tile joins them in the order
-// of the ranges.  Warps:
+// O, max and sum, in 32 bits) in the workspace, and k_tree_join joins them in the order of the ranges: a
+// kernel of its own, because one CTA reading all partials of a tile took longer than the attention
+// itself (13 partials of 40 rows: 20 us of 35).  Warps:
 //   0      K/V producer: TMA boxes of 64 columns x 128 tokens (128B swizzle) into a ring of tiles;
 //   2      Q loader: one box of 64 columns x HPG heads x 128/HPG nodes is a whole 128-row tile of Q;
 //   1      MMA issuer: S = Q K^T into the TMEM buffer of a softmax group, then, one unit later, O += P V with
@@ -51,12 +52,19 @@ struct __align__(16) Item {
     uint32_t nodes[2];
 };
 
+// What the plan says of a tile; n_items 0: nothing to do.
+struct __align__(16) Tile {
+    int32_t n_items;    // | kDraftBit
+    int32_t row, nodes; // its first row and its nodes
+    int32_t row0;       // the request's first row
+};
+
 struct Layout {
     int per_tile;       // nodes of a tile
     int chunks;         // tiles per (request, group)
     int cap;            // items of a tile, at most
     long long tiles;
-    size_t count, done, dmask, items, part, bytes;
+    size_t tile, cut, dmask, items, part, bytes;
 };
 
 __host__ __device__ constexpr size_t part_floats(int D) { return size_t(256) * D + 512; }   // O, then (m, l) per row
@@ -69,9 +77,9 @@ inline Layout layout(int n_rows, int n_req, const Shape &s) {
     w.chunks = std::max(1, (nodes + w.per_tile - 1) / w.per_tile);
     w.cap = int(std::min<long long>(1LL * std::min(nodes, w.per_tile) * s.topk, s.max_blocks)) + 1;
     w.tiles = 1LL * n_req * w.chunks * s.G;
-    w.count = 0;
-    w.done = up(size_t(w.tiles) * 4);
-    w.dmask = w.done + up(size_t(w.tiles) * 4);
+    w.tile = 0;
+    w.cut = up(size_t(w.tiles) * sizeof(Tile));
+    w.dmask = w.cut + up(size_t(w.tiles) * sizeof(int2));
     w.items = w.dmask + up(size_t(n_rows) * s.G * 8);
     w.part = w.items + up(size_t(w.tiles) * w.cap * sizeof(Item));
     w.bytes = w.part + size_t(2 * kMaxCtas) * part_floats(s.D) * 4;
@@ -87,7 +95,7 @@ template <int D, int HPG>
 __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
     const int32_t *__restrict__ sel, const int32_t *__restrict__ block_table, const int32_t *__restrict__ ctx_lens,
     const int32_t *__restrict__ node_off, const uint64_t *__restrict__ anc, int n_rows, int n_pages, int G, int topk,
-    int max_blocks, int chunks, int cap, int32_t *__restrict__ count, int32_t *__restrict__ done,
+    int max_blocks, int chunks, int cap, Tile *__restrict__ tiles, int2 *__restrict__ cut,
     unsigned long long *__restrict__ dmask, Item *__restrict__ items, uint4 *__restrict__ out,
     float *__restrict__ lse, int32_t *err) {
     constexpr int PER = 256 / HPG;                     // nodes of a tile, at most 64
@@ -110,8 +118,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
     if (nt <= 0 || ctx < 0) {
         if (tid == 0) {
             if (n > 0 && ctx < 0) raise_flag(err, MSA_FLAG_BOUNDS);
-            count[tile] = 0;
-            done[tile] = 0;
+            tiles[tile] = Tile{0, 0, 0, 0};
+            cut[tile] = make_int2(0, -1);
         }
         return;
     }
@@ -209,8 +217,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
             it.nodes[1] = draft_nodes[1];
             list[total] = it;
         }
-        count[tile] = drafts ? (total + 1) | kDraftBit : total;
-        done[tile] = 0;
+        tiles[tile] = Tile{drafts ? (total + 1) | kDraftBit : total, row0 + first, nt, row0};
+        cut[tile] = make_int2(0, -1);
     }
     if (total == 0 && !drafts) {   // nothing is seen: the rows' results are written here
         constexpr int CH = HPG * D / 8;
@@ -237,7 +245,7 @@ struct TreeSmem {
     int wsum[kThreads / 32];
     int tile0, off0;
     uint32_t tmem_base;
-    int abort, nonfinite, last;
+    int abort, nonfinite;
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {   // MUFU.EX2, relative error about 2^-22
@@ -288,9 +296,10 @@ __device__ __forceinline__ int range_owner(long long x, long long n, int C) { re
 
 // The CTA's segments in order; every role walks them for itself.
 struct Walk {
-    const int32_t *count;
+    const Tile *tiles;
     long long x, x1;
     int tile, off, end, n_items, seg;
+    Tile t;
     bool drafts;
     __device__ __forceinline__ bool next() {   // the next segment: items off .. end-1 of `tile`, n_items in it
         if (seg >= 0) {
@@ -299,27 +308,16 @@ struct Walk {
             off = 0;
         }
         if (x >= x1) return false;
-        int c;
-        while (!((c = count[tile]) & ~kDraftBit)) ++tile;
-        n_items = c & ~kDraftBit;
-        drafts = c & kDraftBit;
+        for (;; ++tile) {
+            const int4 v = *reinterpret_cast<const int4 *>(tiles + tile);
+            t = Tile{v.x, v.y, v.z, v.w};
+            n_items = t.n_items & ~kDraftBit;
+            if (n_items) break;
+        }
+        drafts = t.n_items & kDraftBit;
         end = int(min((long long)n_items, off + (x1 - x)));
         ++seg;
         return true;
-    }
-};
-
-// What a tile is of: request, group, nodes.
-struct TileOf {
-    int b, g, row, nt, n, row0;
-    __device__ __forceinline__ TileOf(int tile, int G, int chunks, int per, const int32_t *node_off) {
-        g = tile % G;
-        const int chunk = tile / G % chunks;
-        b = tile / G / chunks;
-        row0 = node_off[b];
-        n = node_off[b + 1] - row0;
-        row = row0 + chunk * per;
-        nt = min(per, n - chunk * per);
     }
 };
 
@@ -333,14 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
     const __grid_constant__ CUtensorMap knmap, const __grid_constant__ CUtensorMap vnmap,
     const uint16_t *__restrict__ k_cache, const uint16_t *__restrict__ v_cache, const uint16_t *__restrict__ k_new,
-    const uint16_t *__restrict__ v_new, const int32_t *__restrict__ node_off, int G, int chunks, int cap, int n_tiles,
-    float sm_scale, const int32_t *__restrict__ count, int32_t *__restrict__ done,
+    const uint16_t *__restrict__ v_new, int G, int cap, int n_tiles, float sm_scale,
+    const Tile *__restrict__ tiles, int2 *__restrict__ cut,
     const unsigned long long *__restrict__ dmask, const Item *__restrict__ items, float *__restrict__ part,
     uint16_t *__restrict__ out, float *__restrict__ lse, int32_t *err) {
     using Smem = TreeSmem<D>;
     constexpr int NSLOT = Smem::NSLOT;
     constexpr int NSUB = D / 64;
-    constexpr int PER = 256 / HPG;     // nodes of a tile
     constexpr int NPM = 128 / HPG;     // nodes of a 128-row MMA tile
     constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t kIdescS64 = make_idesc_bf16(128, 64, 0, 0);
@@ -378,10 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
         tma_prefetch_desc(&qmap);
     }
     pdl_wait();   // the plan
+    pdl_trigger();
     // this CTA's range: a scan of the tiles' item counts, a run of tiles per thread
     const int t_lo = int((long long)tid * n_tiles / kThreads), t_hi = int((long long)(tid + 1) * n_tiles / kThreads);
     int mine = 0;
-    for (int t = t_lo; t < t_hi; ++t) mine += count[t] & ~kDraftBit;
+    for (int t = t_lo; t < t_hi; ++t) mine += tiles[t].n_items & ~kDraftBit;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -404,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
         int t = t_lo;
         long long at = before;
         for (;; ++t) {
-            const int c = count[t] & ~kDraftBit;
+            const int c = tiles[t].n_items & ~kDraftBit;
             if (x0 < at + c) break;
             at += c;
         }
@@ -413,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     }
     __syncthreads();
     const uint32_t tmem = sm.tmem_base;
-    Walk wk{count, x0, x1, x0 < x1 ? sm.tile0 : 0, x0 < x1 ? sm.off0 : 0, 0, 0, -1, false};
+    Walk wk{tiles, x0, x1, x0 < x1 ? sm.tile0 : 0, x0 < x1 ? sm.off0 : 0, 0, 0, -1, Tile{}, false};
 
     if (warp == 0) {
         // ------------------------------------------------------------ K/V producer (lane 0)
@@ -421,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             int seq = 0;
             bool ok = true;
             while (ok && wk.next()) {
-                const TileOf t(wk.tile, G, chunks, PER, node_off);
+                const int g = wk.tile % G;
                 const Item *list = items + size_t(wk.tile) * cap;
                 int page = list[wk.off].page;
                 for (int i = wk.off; ok && i < wk.end; ++i) {
@@ -439,8 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
 #pragma unroll
                         for (int c = 0; c < NSUB; ++c) {
                             uint8_t *dst = sm.kv[slot] + c * 16384;
-                            if (draft) tma_load_3d(dst, kv ? &vnmap : &knmap, &sm.full[slot], c * 64, t.g, t.row0);
-                            else tma_load_4d(dst, kv ? &vmap : &kmap, &sm.full[slot], c * 64, t.g, 0, page_i);
+                            if (draft) tma_load_3d(dst, kv ? &vnmap : &knmap, &sm.full[slot], c * 64, g, wk.t.row0);
+                            else tma_load_4d(dst, kv ? &vmap : &kmap, &sm.full[slot], c * 64, g, 0, page_i);
                         }
                     }
                 }
@@ -455,13 +453,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             int loads = 0;
             while (wk.next()) {
                 if (wk.seg > 0 && !mbar_wait(&sm.q_empty, (wk.seg - 1) & 1, err, &sm.abort)) break;
-                const TileOf t(wk.tile, G, chunks, PER, node_off);
-                const int nm = t.nt > NPM ? 2 : 1;
+                const int nm = wk.t.nodes > NPM ? 2 : 1;
                 mbar_arrive_expect_tx(&sm.q_full, nm * 128 * D * 2);
                 for (int m = 0; m < nm; ++m)
 #pragma unroll
                     for (int c = 0; c < NSUB; ++c)
-                        tma_load_3d(sm.q[m] + c * 16384, &qmap, &sm.q_full, c * 64, t.g * HPG, t.row + m * NPM);
+                        tma_load_3d(sm.q[m] + c * 16384, &qmap, &sm.q_full, c * 64, wk.tile % G * HPG,
+                                    wk.t.row + m * NPM);
                 ++loads;
             }
             if (sm.abort && loads) mbar_wait(&sm.q_full, (loads - 1) & 1, err, nullptr);
@@ -499,8 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                 return true;
             };
             while (ok && wk.next()) {
-                const TileOf t(wk.tile, G, chunks, PER, node_off);
-                const int nm = t.nt > NPM ? 2 : 1;
+                const int nm = wk.t.nodes > NPM ? 2 : 1;
                 o_wait = wk.seg > 0;
                 if (!mbar_wait(&sm.q_full, wk.seg & 1, err, &sm.abort)) break;
                 int u = 0;                    // units of this segment
@@ -591,14 +588,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
         int units[2] = {0, 0};                     // units of both groups so far
         bool ok = true;   // once a wait has run out the groups only keep in step, so that no barrier is missed
         while (wk.next()) {
-            const TileOf t(wk.tile, G, chunks, PER, node_off);
-            const int nm = t.nt > NPM ? 2 : 1;
+            const int g = wk.tile % G, nt = wk.t.nodes;
+            const int nm = nt > NPM ? 2 : 1;
             const Item *list = items + size_t(wk.tile) * cap;
             const int mt = nm == 2 ? w : 0;
             const int node = mt * NPM + row / HPG;                 // within the tile
-            const bool live = node < t.nt;
-            const bool warp_live = mt * NPM + quad * 32 / HPG < t.nt;
-            const unsigned long long dm = live ? dmask[size_t(t.row + node) * G + t.g] : 0ull;
+            const bool live = node < nt;
+            const bool warp_live = mt * NPM + quad * 32 / HPG < nt;
+            const unsigned long long dm = live ? dmask[size_t(wk.t.row + node) * G + g] : 0ull;
             const int len = wk.end - wk.off;
             const int step = nm == 2 ? 1 : 2, i0 = wk.off + (nm == 2 ? 0 : w);
             float m = -INFINITY, l = 0.f;
@@ -747,13 +744,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                     wb = o.y;
                 }
             }
-            const long long seg_x = wk.x;                               // first item of the segment
-            const long long tile_x = seg_x - wk.off;                    // first item of the tile
             const bool whole = wk.off == 0 && wk.end == wk.n_items;
             const int c_lo = nm == 2 ? 0 : w * (D / 2), c_hi = nm == 2 ? D : c_lo + D / 2;
             float *slot = part + size_t(2 * cta + (wk.off > 0 ? 0 : 1)) * part_floats(D);
             float2 *slot_ml = reinterpret_cast<float2 *>(slot + 256 * D);
-            const size_t orow = (size_t(t.row + node) * G + t.g) * HPG + row % HPG;
+            const size_t orow = (size_t(wk.t.row + node) * G + g) * HPG + row % HPG;
             if (nm == 1) {                         // group 0's total for group 1
                 groups_sync();                     // the weights have been read
                 if (w == 0) sm.join[row] = make_float2(m, l);
@@ -797,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                             if (!(item.nodes[node >> 5] >> (node & 31) & 1)) continue;
                             for (int tok = 0; tok < item.n_tok; ++tok) {
                                 if (draft && !(dm >> tok & 1)) continue;
-                                const size_t at = draft ? (size_t(t.row0 + tok) * G + t.g) * D
-                                                        : ((size_t(item.page) * 128 + tok) * G + t.g) * D;
+                                const size_t at = draft ? (size_t(wk.t.row0 + tok) * G + g) * D
+                                                        : ((size_t(item.page) * 128 + tok) * G + g) * D;
                                 const uint4 *v4 = reinterpret_cast<const uint4 *>((draft ? v_new : v_cache) + at + c);
                                 const uint4 x[4] = {v4[0], v4[1], v4[2], v4[3]};
                                 uint32_t any = 0;
@@ -850,62 +845,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_free);
-            if (whole) continue;
-            // a cut tile: the CTA that completes it joins the partials of all its ranges
-            groups_sync();   // every partial store of this CTA precedes the release below
-            if (tid == 4 * 32) {
-                __threadfence();
-                sm.last = atomicAdd(done + wk.tile, len) + len == wk.n_items;
-                __threadfence();
-            }
-            groups_sync();
-            if (!*reinterpret_cast<volatile int *>(&sm.last)) continue;
-            if (!warp_live) continue;
-            const int ca = range_owner(tile_x, total, C), cb = range_owner(tile_x + wk.n_items - 1, total, C);
-            auto slot_of = [&](int c) {
-                return part + size_t(2 * c + (range_begin(c, total, C) > tile_x ? 0 : 1)) * part_floats(D);
-            };
-            float top = -INFINITY;
-            for (int c = ca; c <= cb; ++c)
-                top = fmaxf(top, __ldcg(reinterpret_cast<const float2 *>(slot_of(c) + 256 * D) + mt * 128 + row).x);
-            const float ntop = top == -INFINITY ? 0.f : -top;
-            float sum = 0.f;
-            for (int c = ca; c <= cb; ++c) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot_of(c) + 256 * D) + mt * 128 + row);
-                sum += ml.y * fast_exp2(ml.x + ntop);
-            }
-            const float rcp = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-#pragma unroll 1
-            for (int cc = c_lo; cc < c_hi; cc += 32) {
-                float o[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                for (int c = ca; c <= cb; ++c) {
-                    const float *base = slot_of(c);
-                    const float wgt =
-                        fast_exp2(__ldcg(reinterpret_cast<const float2 *>(base + 256 * D) + mt * 128 + row).x + ntop);
-                    const float4 *po = reinterpret_cast<const float4 *>(base) + size_t(mt * (D / 4) + cc / 4) * 128 + row;
-                    float4 v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = __ldcg(po + size_t(e) * 128);
-                    if (wgt == 0.f) continue;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        o[4 * e] = fmaf(wgt, v[e].x, o[4 * e]);
-                        o[4 * e + 1] = fmaf(wgt, v[e].y, o[4 * e + 1]);
-                        o[4 * e + 2] = fmaf(wgt, v[e].z, o[4 * e + 2]);
-                        o[4 * e + 3] = fmaf(wgt, v[e].w, o[4 * e + 3]);
-                    }
-                }
-                if (live) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>(out + orow * D + cc + e) = make_uint4(
-                            pack_bf16x2(o[e] * rcp, o[e + 1] * rcp), pack_bf16x2(o[e + 2] * rcp, o[e + 3] * rcp),
-                            pack_bf16x2(o[e + 4] * rcp, o[e + 5] * rcp), pack_bf16x2(o[e + 6] * rcp, o[e + 7] * rcp));
-                }
-            }
-            if (live && (nm == 2 || w == 0)) lse[orow] = sum > 0.f || sum != sum ? (top + log2f(sum)) * kLn2 : -INFINITY;
+            if (!whole && wk.off == 0 && tid == 4 * 32)   // the ranges that hold the tile
+                cut[wk.tile] = make_int2(cta, range_owner(wk.x + wk.n_items - 1, total, C));
         }
     }
 
@@ -913,6 +854,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ join
+//
+// The partials of a cut tile: O = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over its ranges c.  One thread
+// per row and 8 columns, eight ranges' loads in flight.
+template <int D, int HPG>
+__global__ void __launch_bounds__(256) k_tree_join(const Tile *__restrict__ tiles, const int2 *__restrict__ cut,
+                                                   const float *__restrict__ part, int G, uint16_t *__restrict__ out,
+                                                   float *__restrict__ lse) {
+    const int tile = blockIdx.x, col = blockIdx.y * 8, row = threadIdx.x;   // rows 128.. : the second 128-row half
+    pdl_wait();
+    const int2 range = cut[tile];
+    if (range.x > range.y) return;   // not cut
+    const int node = row / HPG;
+    const int4 tv = *reinterpret_cast<const int4 *>(tiles + tile);
+    if (node >= tv.z) return;
+    const float *base = part + size_t(2 * range.x + 1) * part_floats(D);   // the first range's second slot
+    float m = -INFINITY, l = 0.f, o[8] = {};
+    for (int c0 = range.x; c0 <= range.y; c0 += 8) {
+        float2 ml[8];
+        float4 v[8][2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = c0 + i;
+            if (c > range.y) break;
+            const float *p = c == range.x ? base : part + size_t(2 * c) * part_floats(D);
+            ml[i] = __ldcg(reinterpret_cast<const float2 *>(p + 256 * D) + row);
+            const float4 *po = reinterpret_cast<const float4 *>(p) + size_t((row >> 7) * (D / 4) + col / 4) * 128 +
+                               (row & 127);
+            v[i][0] = __ldcg(po);
+            v[i][1] = __ldcg(po + 128);
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c0 + i <= range.y) top = fmaxf(top, ml[i].x);
+        const float nt = top == -INFINITY ? 0.f : -top;
+        const float f = fast_exp2(m + nt);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c0 + i > range.y) break;
+            const float w = fast_exp2(ml[i].x + nt);
+            l = fmaf(ml[i].y, w, l);
+            if (w == 0.f) continue;
+            o[0] = fmaf(w, v[i][0].x, o[0]);
+            o[1] = fmaf(w, v[i][0].y, o[1]);
+            o[2] = fmaf(w, v[i][0].z, o[2]);
+            o[3] = fmaf(w, v[i][0].w, o[3]);
+            o[4] = fmaf(w, v[i][1].x, o[4]);
+            o[5] = fmaf(w, v[i][1].y, o[5]);
+            o[6] = fmaf(w, v[i][1].z, o[6]);
+            o[7] = fmaf(w, v[i][1].w, o[7]);
+        }
+    }
+    const bool any = l > 0.f || l != l;
+    const float r = any ? 1.f / l : 0.f;
+    const size_t orow = (size_t(tv.y + node) * G + tile % G) * HPG + row % HPG;
+    *reinterpret_cast<uint4 *>(out + orow * D + col) =
+        make_uint4(pack_bf16x2(o[0] * r, o[1] * r), pack_bf16x2(o[2] * r, o[3] * r), pack_bf16x2(o[4] * r, o[5] * r),
+                   pack_bf16x2(o[6] * r, o[7] * r));
+    if (col == 0) lse[orow] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <int D, int HPG>
@@ -945,25 +952,30 @@ cudaError_t launch_t(const void *q, const void *k_cache, const void *v_cache, co
         if (!encode_tensor_map(&vn, 3, v_new, dims, strides, box, 128, &why)) return cudaErrorInvalidValue;
     }
     uint8_t *base = static_cast<uint8_t *>(ws);
-    int32_t *count = reinterpret_cast<int32_t *>(base + w.count), *done = reinterpret_cast<int32_t *>(base + w.done);
+    Tile *tiles = reinterpret_cast<Tile *>(base + w.tile);
+    int2 *cut = reinterpret_cast<int2 *>(base + w.cut);
     auto *dmask = reinterpret_cast<unsigned long long *>(base + w.dmask);
     Item *items = reinterpret_cast<Item *>(base + w.items);
     float *part = reinterpret_cast<float *>(base + w.part);
     cudaError_t e = launch_kernel(k_tree_plan<D, HPG>, dim3(unsigned(w.tiles)), dim3(kPlanThreads), 0, st, true, sel, bt,
                                   ctx, node_off, anc, n_rows, n_pages, s.G, s.topk, s.max_blocks, w.chunks, w.cap,
-                                  count, done, dmask, items, static_cast<uint4 *>(out), lse, err);
+                                  tiles, cut, dmask, items, static_cast<uint4 *>(out), lse, err);
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(TreeSmem<D>) + 1024;
     static_assert(sizeof(TreeSmem<D>) + 1024 <= 232448, "shared memory of a CTA");
     e = cudaFuncSetAttribute(k_attn_tree<D, HPG>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     const int grid = std::min(sm_count(), kMaxCtas);
-    return launch_kernel(k_attn_tree<D, HPG>, dim3(unsigned(grid)), dim3(kThreads), smem, st, true,
-                         static_cast<const uint16_t *>(q), qm, km, vm, kn, vn, static_cast<const uint16_t *>(k_cache),
-                         static_cast<const uint16_t *>(v_cache), static_cast<const uint16_t *>(k_new),
-                         static_cast<const uint16_t *>(v_new), node_off, s.G, w.chunks, w.cap, int(w.tiles), s.sm_scale,
-                         static_cast<const int32_t *>(count), done, static_cast<const unsigned long long *>(dmask),
-                         static_cast<const Item *>(items), part, static_cast<uint16_t *>(out), lse, err);
+    e = launch_kernel(k_attn_tree<D, HPG>, dim3(unsigned(grid)), dim3(kThreads), smem, st, true,
+                      static_cast<const uint16_t *>(q), qm, km, vm, kn, vn, static_cast<const uint16_t *>(k_cache),
+                      static_cast<const uint16_t *>(v_cache), static_cast<const uint16_t *>(k_new),
+                      static_cast<const uint16_t *>(v_new), s.G, w.cap, int(w.tiles), s.sm_scale,
+                      static_cast<const Tile *>(tiles), cut, static_cast<const unsigned long long *>(dmask),
+                      static_cast<const Item *>(items), part, static_cast<uint16_t *>(out), lse, err);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(k_tree_join<D, HPG>, dim3(unsigned(w.tiles), D / 8), dim3(256), 0, st, true,
+                         static_cast<const Tile *>(tiles), static_cast<const int2 *>(cut),
+                         static_cast<const float *>(part), s.G, static_cast<uint16_t *>(out), lse);
 }
 
 }  // namespace
