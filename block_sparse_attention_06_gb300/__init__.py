@@ -63,6 +63,17 @@ class Dims:
         sc = self.sm_scale if self.sm_scale is not None else 1.0 / math.sqrt(self.D)
         return msa_dims_t(self.Hq, self.G, self.D, self.Di, self.page_size, self.topk, self.max_blocks, sc)
 
+    def ref(self):
+        """A ctypes reference to c(), made once (the fields are frozen and the library only reads them)."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = ctypes.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
+
+    def __getstate__(self):   # copies and pickles make their own
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
 
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
@@ -518,51 +529,66 @@ def msa_decode_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, seq_len
 
 # ------------------------------------------------------------------ drafted trees (speculative decode)
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _arg(t, dtype, shape, index: int, name: str) -> int:
+    """The address of a tensor argument on device `index`, checked as _req does (which words the
+    refusal).  A decode step makes these calls per layer, so the checks that pass are kept short."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == index):
+        return t.data_ptr()
+    _req(t, dtype, name, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _call_on(dev, name: str, *args):
-    """_call with the tensors' device current (kernels launch on the current device)."""
-    if dev.index == torch.cuda.current_device():
-        _call(name, *args)
-    else:
-        with torch.cuda.device(dev):
-            _call(name, *args)
+def _lead(t, name: str) -> int:
+    """The device index of the argument that decides where a call runs."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
-def _req_tree(node_off, ctx_lens=None):
-    _req(node_off, torch.int32, "node_off")
-    if node_off.dim() != 1 or node_off.shape[0] < 2:
+def _ndim(t, n: int, name: str, what: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must be {what}")
+    return t.shape
+
+
+def _n_req(node_off) -> int:
+    n = _ndim(node_off, 1, "node_off", "[n_req + 1]")[0] - 1
+    if n < 1:
         raise ValueError("node_off must be [n_req + 1]")
-    n_req = node_off.shape[0] - 1
-    if ctx_lens is not None:
-        _req(ctx_lens, torch.int32, "ctx_lens", (n_req,))
-    return n_req
+    return n
+
+
+def _launch(index: int, name: str, *args):
+    """_call on the current stream of device `index`, with that device current."""
+    if index == torch.cuda.current_device():
+        _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
+
+
+_I32, _I64, _F32, _BF16, _U8 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
 
 
 def msa_tree_rows(node_off, parents, ctx_lens, dims: Dims, q_req=None, q_pos=None, anc=None, err_word=None):
     """Positions and ancestors of the rows of drafted trees -> (q_req, q_pos, anc); anc is int64,
     bit m of a row's word set where node m is the row's ancestor or the row itself."""
-    n_req = _req_tree(node_off, ctx_lens)
-    _req(parents, torch.int32, "parents")
-    if parents.dim() != 1:
-        raise ValueError("parents must be [n_rows]")
-    n_rows, dev = parents.shape[0], parents.device
-    f = dict(device=dev)
-    q_req = torch.empty((n_rows,), dtype=torch.int32, **f) if q_req is None else q_req
-    q_pos = torch.empty((n_rows,), dtype=torch.int32, **f) if q_pos is None else q_pos
-    anc = torch.empty((n_rows,), dtype=torch.int64, **f) if anc is None else anc
-    _req(q_req, torch.int32, "q_req", (n_rows,))
-    _req(q_pos, torch.int32, "q_pos", (n_rows,))
-    _req(anc, torch.int64, "anc", (n_rows,))
-    err_word = new_err_word(dev) if err_word is None else err_word
-    _same_device(dev, node_off=node_off, ctx_lens=ctx_lens, q_req=q_req, q_pos=q_pos, anc=anc, err_word=err_word)
-    d = dims.c()
-    _call_on(dev, "msa_tree_rows", _ptr(node_off), _ptr(parents), _ptr(ctx_lens), n_rows, n_req, ctypes.byref(d),
-             _ptr(q_req), _ptr(q_pos), _ptr(anc), _ptr(err_word), _stream(dev))
+    dev = _lead(parents, "parents")
+    n_req = _n_req(node_off)
+    rows = _ndim(parents, 1, "parents", "[n_rows]")
+    q_req = parents.new_empty(rows) if q_req is None else q_req
+    q_pos = parents.new_empty(rows) if q_pos is None else q_pos
+    anc = parents.new_empty(rows, dtype=_I64) if anc is None else anc
+    err_word = new_err_word(parents.device) if err_word is None else err_word
+    _launch(dev, "msa_tree_rows", _arg(node_off, _I32, (n_req + 1,), dev, "node_off"),
+            _arg(parents, _I32, rows, dev, "parents"), _arg(ctx_lens, _I32, (n_req,), dev, "ctx_lens"), rows[0], n_req,
+            dims.ref(), _arg(q_req, _I32, rows, dev, "q_req"), _arg(q_pos, _I32, rows, dev, "q_pos"),
+            _arg(anc, _I64, rows, dev, "anc"), _arg(err_word, _I32, (1,), dev, "err_word"))
     return q_req, q_pos, anc
 
 
@@ -570,25 +596,21 @@ def msa_tree_index_score(q_idx, kidx_cache, kidx_new, block_table, ctx_lens, nod
                          err_word=None):
     """Block scores of the nodes of drafted trees: msa_index_score over the cached tokens and each
     node's drafted ancestors (anc from msa_tree_rows)."""
-    n_req = _req_tree(node_off, ctx_lens)
-    n_rows, dev = q_idx.shape[0], q_idx.device
-    _req(q_idx, torch.bfloat16, "q_idx", (n_rows, dims.G, dims.Di))
-    _req(kidx_cache, torch.bfloat16, "kidx_cache")
-    if kidx_cache.dim() != 4 or tuple(kidx_cache.shape[1:]) != (dims.page_size, dims.G, dims.Di):
-        raise ValueError("kidx_cache must be [n_pages][128][G][Di]")
-    _req(kidx_new, torch.bfloat16, "kidx_new", (n_rows, dims.G, dims.Di))
-    _req(block_table, torch.int32, "block_table", (n_req, dims.max_blocks))
-    _req(anc, torch.int64, "anc", (n_rows,))
+    dev = _lead(q_idx, "q_idx")
+    n_req, n_rows = _n_req(node_off), _ndim(q_idx, 3, "q_idx", "[n_rows][G][Di]")[0]
+    n_pages = _ndim(kidx_cache, 4, "kidx_cache", "[n_pages][128][G][Di]")[0]
+    index = (n_rows, dims.G, dims.Di)
     if scores is None:
-        scores = torch.empty((n_rows, dims.G, dims.max_blocks), dtype=torch.float32, device=dev)
-    _req(scores, torch.float32, "scores", (n_rows, dims.G, dims.max_blocks))
-    err_word = new_err_word(dev) if err_word is None else err_word
-    _same_device(dev, kidx_cache=kidx_cache, kidx_new=kidx_new, block_table=block_table, ctx_lens=ctx_lens,
-                 node_off=node_off, anc=anc, scores=scores, err_word=err_word)
-    d = dims.c()
-    _call_on(dev, "msa_tree_index_score", _ptr(q_idx), _ptr(kidx_cache), _ptr(kidx_new), _ptr(block_table),
-             _ptr(ctx_lens), _ptr(node_off), _ptr(anc), n_rows, n_req, kidx_cache.shape[0], ctypes.byref(d),
-             _ptr(scores), _ptr(err_word), _stream(dev))
+        scores = q_idx.new_empty((n_rows, dims.G, dims.max_blocks), dtype=_F32)
+    err_word = new_err_word(q_idx.device) if err_word is None else err_word
+    _launch(dev, "msa_tree_index_score", _arg(q_idx, _BF16, index, dev, "q_idx"),
+            _arg(kidx_cache, _BF16, (n_pages, dims.page_size, dims.G, dims.Di), dev, "kidx_cache"),
+            _arg(kidx_new, _BF16, index, dev, "kidx_new"),
+            _arg(block_table, _I32, (n_req, dims.max_blocks), dev, "block_table"),
+            _arg(ctx_lens, _I32, (n_req,), dev, "ctx_lens"), _arg(node_off, _I32, (n_req + 1,), dev, "node_off"),
+            _arg(anc, _I64, (n_rows,), dev, "anc"), n_rows, n_req, n_pages, dims.ref(),
+            _arg(scores, _F32, (n_rows, dims.G, dims.max_blocks), dev, "scores"),
+            _arg(err_word, _I32, (1,), dev, "err_word"))
     return scores
 
 
@@ -596,36 +618,25 @@ def msa_sparse_attn_tree(q, k_cache, v_cache, k_new, v_new, block_table, ctx_len
                          out=None, lse=None, workspace=None, err_word=None):
     """Sparse attention of the nodes of drafted trees: the cached tokens of each row's selected
     blocks and the row's drafted ancestors whose block is selected -> (out, lse)."""
-    n_req = _req_tree(node_off, ctx_lens)
-    n_rows, dev = q.shape[0], q.device
-    _req(q, torch.bfloat16, "q", (n_rows, dims.Hq, dims.D))
-    _req(k_cache, torch.bfloat16, "k_cache")
-    _req(v_cache, torch.bfloat16, "v_cache", tuple(k_cache.shape))
-    if k_cache.dim() != 4 or tuple(k_cache.shape[1:]) != (dims.page_size, dims.G, dims.D):
-        raise ValueError("k_cache must be [n_pages][128][G][D]")
-    _req(k_new, torch.bfloat16, "k_new", (n_rows, dims.G, dims.D))
-    _req(v_new, torch.bfloat16, "v_new", (n_rows, dims.G, dims.D))
-    _req(block_table, torch.int32, "block_table", (n_req, dims.max_blocks))
-    _req(anc, torch.int64, "anc", (n_rows,))
-    _req(sel, torch.int32, "sel", (n_rows, dims.G, dims.topk))
-    if out is None:
-        out = torch.empty((n_rows, dims.Hq, dims.D), dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.empty((n_rows, dims.Hq), dtype=torch.float32, device=dev)
-    _req(out, torch.bfloat16, "out", (n_rows, dims.Hq, dims.D))
-    _req(lse, torch.float32, "lse", (n_rows, dims.Hq))
+    dev = _lead(q, "q")
+    n_req, n_rows = _n_req(node_off), _ndim(q, 3, "q", "[n_rows][Hq][D]")[0]
+    n_pages = _ndim(k_cache, 4, "k_cache", "[n_pages][128][G][D]")[0]
+    heads, cache = (n_rows, dims.Hq, dims.D), (n_pages, dims.page_size, dims.G, dims.D)
+    rows = (n_rows, dims.G, dims.D)
+    out = q.new_empty(heads) if out is None else out
+    lse = q.new_empty(heads[:2], dtype=_F32) if lse is None else lse
     if workspace is None:
-        need = msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims)
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
-    _req(workspace, torch.uint8, "workspace")
-    err_word = new_err_word(dev) if err_word is None else err_word
-    _same_device(dev, k_cache=k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new, block_table=block_table,
-                 ctx_lens=ctx_lens, node_off=node_off, anc=anc, sel=sel, out=out, lse=lse, workspace=workspace,
-                 err_word=err_word)
-    d = dims.c()
-    _call_on(dev, "msa_sparse_attn_tree", _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_new), _ptr(v_new),
-             _ptr(block_table), _ptr(ctx_lens), _ptr(node_off), _ptr(anc), _ptr(sel), n_rows, n_req, k_cache.shape[0],
-             ctypes.byref(d), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err_word), _stream(dev))
+        workspace = q.new_empty((max(msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims), 1),), dtype=_U8)
+    err_word = new_err_word(q.device) if err_word is None else err_word
+    ws_bytes = _ndim(workspace, 1, "workspace", "a uint8 vector")
+    _launch(dev, "msa_sparse_attn_tree", _arg(q, _BF16, heads, dev, "q"), _arg(k_cache, _BF16, cache, dev, "k_cache"),
+            _arg(v_cache, _BF16, cache, dev, "v_cache"), _arg(k_new, _BF16, rows, dev, "k_new"),
+            _arg(v_new, _BF16, rows, dev, "v_new"),
+            _arg(block_table, _I32, (n_req, dims.max_blocks), dev, "block_table"),
+            _arg(ctx_lens, _I32, (n_req,), dev, "ctx_lens"), _arg(node_off, _I32, (n_req + 1,), dev, "node_off"),
+            _arg(anc, _I64, (n_rows,), dev, "anc"), _arg(sel, _I32, (n_rows, dims.G, dims.topk), dev, "sel"), n_rows,
+            n_req, n_pages, dims.ref(), _arg(out, _BF16, heads, dev, "out"), _arg(lse, _F32, heads[:2], dev, "lse"),
+            _arg(workspace, _U8, ws_bytes, dev, "workspace"), ws_bytes[0], _arg(err_word, _I32, (1,), dev, "err_word"))
     return out, lse
 
 
@@ -633,30 +644,22 @@ def msa_verify_tree(target_probs, draft_probs, tokens, node_off, parents, u_acce
                     n_accepted=None, next_token=None, err_word=None):
     """Accept drafted tokens against the target's probabilities from given random numbers ->
     (path, n_accepted, next_token); draft_probs None: drafts chosen without chance."""
-    n_req = _req_tree(node_off)
-    _req(target_probs, torch.float32, "target_probs")
-    if target_probs.dim() != 2 or target_probs.shape[1] < 1:
+    dev = _lead(target_probs, "target_probs")
+    n_req, probs = _n_req(node_off), _ndim(target_probs, 2, "target_probs", "[n_rows][vocab]")
+    n_rows, vocab = probs
+    if vocab < 1:
         raise ValueError("target_probs must be [n_rows][vocab]")
-    (n_rows, vocab), dev = target_probs.shape, target_probs.device
-    if draft_probs is not None:
-        _req(draft_probs, torch.float32, "draft_probs", (n_rows, vocab))
-    _req(tokens, torch.int32, "tokens", (n_rows,))
-    _req(parents, torch.int32, "parents", (n_rows,))
-    _req(u_accept, torch.float32, "u_accept", (n_rows,))
-    _req(u_next, torch.float32, "u_next", (n_req,))
-    f = dict(dtype=torch.int32, device=dev)
-    path = torch.empty((n_rows,), **f) if path is None else path
-    n_accepted = torch.empty((n_req,), **f) if n_accepted is None else n_accepted
-    next_token = torch.empty((n_req,), **f) if next_token is None else next_token
-    _req(path, torch.int32, "path", (n_rows,))
-    _req(n_accepted, torch.int32, "n_accepted", (n_req,))
-    _req(next_token, torch.int32, "next_token", (n_req,))
-    err_word = new_err_word(dev) if err_word is None else err_word
-    _same_device(dev, draft_probs=draft_probs, tokens=tokens, node_off=node_off, parents=parents, u_accept=u_accept,
-                 u_next=u_next, path=path, n_accepted=n_accepted, next_token=next_token, err_word=err_word)
-    _call_on(dev, "msa_verify_tree", _ptr(target_probs), _ptr(draft_probs), vocab, _ptr(tokens), _ptr(node_off),
-             _ptr(parents), _ptr(u_accept), _ptr(u_next), n_rows, n_req, _ptr(path), _ptr(n_accepted),
-             _ptr(next_token), _ptr(err_word), _stream(dev))
+    path = target_probs.new_empty((n_rows,), dtype=_I32) if path is None else path
+    n_accepted = target_probs.new_empty((n_req,), dtype=_I32) if n_accepted is None else n_accepted
+    next_token = target_probs.new_empty((n_req,), dtype=_I32) if next_token is None else next_token
+    err_word = new_err_word(target_probs.device) if err_word is None else err_word
+    _launch(dev, "msa_verify_tree", _arg(target_probs, _F32, probs, dev, "target_probs"),
+            None if draft_probs is None else _arg(draft_probs, _F32, probs, dev, "draft_probs"), vocab,
+            _arg(tokens, _I32, (n_rows,), dev, "tokens"), _arg(node_off, _I32, (n_req + 1,), dev, "node_off"),
+            _arg(parents, _I32, (n_rows,), dev, "parents"), _arg(u_accept, _F32, (n_rows,), dev, "u_accept"),
+            _arg(u_next, _F32, (n_req,), dev, "u_next"), n_rows, n_req, _arg(path, _I32, (n_rows,), dev, "path"),
+            _arg(n_accepted, _I32, (n_req,), dev, "n_accepted"), _arg(next_token, _I32, (n_req,), dev, "next_token"),
+            _arg(err_word, _I32, (1,), dev, "err_word"))
     return path, n_accepted, next_token
 
 
@@ -670,34 +673,24 @@ def msa_commit_tree(k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache, block_
     """Append the accepted paths to the caches of all layers (in place) -> new_lens.  Rows are
     [n_layers][n_rows][G][D], caches [n_layers][n_pages][128][G][D] (the k-index with Di); for one
     layer the leading dimension may be left out."""
-    n_req = _req_tree(node_off, ctx_lens)
+    dev = _lead(k_new, "k_new")
+    n_req = _n_req(node_off)
     k_new, v_new, kidx_new = _layers(k_new, 3), _layers(v_new, 3), _layers(kidx_new, 3)
     k_cache, v_cache, kidx_cache = _layers(k_cache, 4), _layers(v_cache, 4), _layers(kidx_cache, 4)
-    _req(k_new, torch.bfloat16, "k_new")
-    _req(k_cache, torch.bfloat16, "k_cache")
-    if k_new.dim() != 4 or tuple(k_new.shape[2:]) != (dims.G, dims.D):
-        raise ValueError("k_new must be [n_layers][n_rows][G][D]")
-    L, n_rows, dev = k_new.shape[0], k_new.shape[1], k_new.device
-    if k_cache.dim() != 5 or k_cache.shape[0] != L or tuple(k_cache.shape[2:]) != (dims.page_size, dims.G, dims.D):
-        raise ValueError("k_cache must be [n_layers][n_pages][128][G][D]")
-    n_pages = k_cache.shape[1]
-    _req(v_new, torch.bfloat16, "v_new", tuple(k_new.shape))
-    _req(kidx_new, torch.bfloat16, "kidx_new", (L, n_rows, dims.G, dims.Di))
-    _req(v_cache, torch.bfloat16, "v_cache", tuple(k_cache.shape))
-    _req(kidx_cache, torch.bfloat16, "kidx_cache", (L, n_pages, dims.page_size, dims.G, dims.Di))
-    _req(block_table, torch.int32, "block_table", (n_req, dims.max_blocks))
-    _req(path, torch.int32, "path", (n_rows,))
-    _req(n_accepted, torch.int32, "n_accepted", (n_req,))
-    new_lens = torch.empty((n_req,), dtype=torch.int32, device=dev) if new_lens is None else new_lens
-    _req(new_lens, torch.int32, "new_lens", (n_req,))
-    err_word = new_err_word(dev) if err_word is None else err_word
-    _same_device(dev, v_new=v_new, kidx_new=kidx_new, k_cache=k_cache, v_cache=v_cache, kidx_cache=kidx_cache,
-                 block_table=block_table, ctx_lens=ctx_lens, node_off=node_off, path=path, n_accepted=n_accepted,
-                 new_lens=new_lens, err_word=err_word)
-    d = dims.c()
-    _call_on(dev, "msa_commit_tree", _ptr(k_new), _ptr(v_new), _ptr(kidx_new), L, _ptr(k_cache), _ptr(v_cache),
-             _ptr(kidx_cache), _ptr(block_table), _ptr(ctx_lens), _ptr(node_off), _ptr(path), _ptr(n_accepted), n_rows,
-             n_req, n_pages, ctypes.byref(d), _ptr(new_lens), _ptr(err_word), _stream(dev))
+    L, n_rows = _ndim(k_new, 4, "k_new", "[n_layers][n_rows][G][D]")[:2]
+    n_pages = _ndim(k_cache, 5, "k_cache", "[n_layers][n_pages][128][G][D]")[1]
+    rows, cache = (L, n_rows, dims.G, dims.D), (L, n_pages, dims.page_size, dims.G, dims.D)
+    new_lens = k_new.new_empty((n_req,), dtype=_I32) if new_lens is None else new_lens
+    err_word = new_err_word(k_new.device) if err_word is None else err_word
+    _launch(dev, "msa_commit_tree", _arg(k_new, _BF16, rows, dev, "k_new"), _arg(v_new, _BF16, rows, dev, "v_new"),
+            _arg(kidx_new, _BF16, (L, n_rows, dims.G, dims.Di), dev, "kidx_new"), L,
+            _arg(k_cache, _BF16, cache, dev, "k_cache"), _arg(v_cache, _BF16, cache, dev, "v_cache"),
+            _arg(kidx_cache, _BF16, (L, n_pages, dims.page_size, dims.G, dims.Di), dev, "kidx_cache"),
+            _arg(block_table, _I32, (n_req, dims.max_blocks), dev, "block_table"),
+            _arg(ctx_lens, _I32, (n_req,), dev, "ctx_lens"), _arg(node_off, _I32, (n_req + 1,), dev, "node_off"),
+            _arg(path, _I32, (n_rows,), dev, "path"), _arg(n_accepted, _I32, (n_req,), dev, "n_accepted"), n_rows,
+            n_req, n_pages, dims.ref(), _arg(new_lens, _I32, (n_req,), dev, "new_lens"),
+            _arg(err_word, _I32, (1,), dev, "err_word"))
     return new_lens
 
 

@@ -19,14 +19,16 @@
 // kernel of its own, because one CTA reading all partials of a tile took longer than the attention
 // itself (13 partials of 40 rows: 20 us of 35).  Warps:
 //   0      K/V producer: TMA boxes of 64 columns x 128 tokens (128B swizzle) into a ring of tiles;
-//   2      Q loader: one box of 64 columns x HPG heads x 128/HPG nodes is a whole 128-row tile of Q;
 //   1      MMA issuer: S = Q K^T into the TMEM buffer of a softmax group, then, one unit later, O += P V with
 //          P in TMEM (over S) and V as an MN-major shared-memory operand;
 //   4-7, 8-11  two softmax groups, one thread per row.  With up to 128 rows in the tile they take alternate
 //          items, each with an O of its own, joined at the segment's end; with more, each has half the
-//          rows.  The running maximum is raised only when a logit passes it by 8 (in powers of two), so
-//          that O, in TMEM, is seldom rescaled: P is then at most 2^8, and its rounding to bf16 is relative;
-//   12-15  finite check of V: a row that does not see a token has P = 0 there, and 0 * NaN would still reach its
+//          rows.  P = 2^(s - m) for a reference m that is the row's first maximum (rounded up to a whole
+//          power of two) until a logit passes it by 2^40: P, sums and O are floating point of 8 exponent bits
+//          throughout, so a reference below the true maximum costs no precision, S is read once, and O, in
+//          TMEM, is next to never rescaled (by a power of two then, exactly);
+//   2, 3   Q loads (one box of 64 columns x HPG heads x 128/HPG nodes is a whole 128-row tile of Q), and the
+//          finite check of V: a row that does not see a token has P = 0 there, and 0 * NaN would still reach its
 //          O through the MMA, so what is not finite is replaced by 0 before the MMA reads it.  Rows that
 //          do see such a value get it back at the segment's end (add_nonfinite), off the hot path.
 // TMEM: S0 | S1 | O0 | O1 (128 + 128 + D + D of 512 columns).  Every wait is bounded.
@@ -38,11 +40,12 @@
 namespace msa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;           // 168 registers a thread
 constexpr int kMaxCtas = 160;           // partial slots in the workspace; at most one CTA per SM
 constexpr int kOkRing = 8;              // finite-check barriers, by item
 constexpr int kDraftBit = 1 << 30;      // of a tile's item count: its last item is the drafted tokens
-constexpr float kRaise = 8.0f;          // raise the running maximum past this (log2 units)
+constexpr float kRaise = 40.0f;         // raise the reference once a logit is this far above (log2 units)
+constexpr float kRaiseSum = 1099511627776.0f;   // 2^kRaise
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -103,6 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
     __shared__ uint32_t bits[kMaxWords];
     __shared__ uint32_t rank[kMaxWords];               // set bits below the word
     __shared__ uint32_t nodes_of[CAP][PER / 32];
+    __shared__ uint16_t block_of[CAP];
     __shared__ unsigned long long in_first, in_second; // nodes whose block is ctx / 128, or the next one
     __shared__ uint32_t has[PER];                      // bit 0 / 1: the node selected that block
     __shared__ uint32_t draft_nodes[2];
@@ -135,18 +139,28 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
         if (j == j0) atomicOr(&in_first, 1ull << tid);
         else if (j == j0 + 1) atomicOr(&in_second, 1ull << tid);
     }
+    // this thread's entries of the selection, loaded together (-1 where there is none)
+    constexpr int EPT = CAP / kPlanThreads;
     const int n_ent = nt * topk;
-    auto entry = [&](int e) { return sel[(size_t(row0 + first + e / topk) * G + g) * topk + e % topk]; };
-    for (int e = tid; e < n_ent; e += kPlanThreads) {
-        const int j = entry(e);
+    int ent[EPT];
+#pragma unroll
+    for (int x = 0; x < EPT; ++x) {
+        const int e = tid + x * kPlanThreads;
+        ent[x] = e < n_ent ? sel[(size_t(row0 + first + e / topk) * G + g) * topk + e % topk] : -1;
+    }
+#pragma unroll
+    for (int x = 0; x < EPT; ++x) {
+        const int j = ent[x], i = (tid + x * kPlanThreads) / topk;
         if (j < 0) continue;
         if (j >= max_blocks) {
             raise_flag(err, MSA_FLAG_BOUNDS);
+            ent[x] = -1;
             continue;
         }
+        if (j == j0) atomicOr(&has[i], 1u);
+        else if (j == j0 + 1) atomicOr(&has[i], 2u);
         if (j < j0 || (j == j0 && (ctx & 127))) atomicOr(&bits[j >> 5], 1u << (j & 31));
-        if (j == j0) atomicOr(&has[e / topk], 1u);
-        else if (j == j0 + 1) atomicOr(&has[e / topk], 2u);
+        else ent[x] = -1;   // a block without cached tokens
     }
     __syncthreads();
     // rank of every word: a scan of the popcounts, two words per thread
@@ -178,34 +192,29 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
         if (m) atomicOr(&draft_nodes[tid >> 5], 1u << (tid & 31));
     }
     __syncthreads();
-    for (int e = tid; e < n_ent; e += kPlanThreads) {
-        const int j = entry(e), i = e / topk;
-        if (j < 0 || j >= max_blocks) continue;
-        const uint32_t word = bits[j >> 5];
-        if (!(word >> (j & 31) & 1)) continue;   // a block without cached tokens
-        const int k = rank[j >> 5] + __popc(word & ((1u << (j & 31)) - 1));
+#pragma unroll
+    for (int x = 0; x < EPT; ++x) {
+        const int j = ent[x], i = (tid + x * kPlanThreads) / topk;
+        if (j < 0) continue;
+        const int k = rank[j >> 5] + __popc(bits[j >> 5] & ((1u << (j & 31)) - 1));
         atomicOr(&nodes_of[k][i >> 5], 1u << (i & 31));
+        block_of[k] = uint16_t(j);   // the same from every node that selected it
     }
     __syncthreads();
     Item *list = items + size_t(tile) * cap;
-    for (int w = tid; w < words; w += kPlanThreads) {
-        uint32_t word = bits[w];
-        int k = rank[w];
-        while (word) {
-            const int j = w * 32 + __ffs(word) - 1;
-            word &= word - 1;
-            Item it;
-            it.page = block_table[size_t(b) * max_blocks + j];
-            it.n_tok = min(128, ctx - j * 128);
-            it.nodes[0] = nodes_of[k][0];
-            it.nodes[1] = PER > 32 ? nodes_of[k][PER / 32 - 1] : 0u;
-            if (it.page < 0 || it.page >= n_pages) {   // refused: seen by no row
-                raise_flag(err, MSA_FLAG_BOUNDS);
-                it.page = 0;
-                it.nodes[0] = it.nodes[1] = 0;
-            }
-            list[k++] = it;
+    for (int k = tid; k < total; k += kPlanThreads) {
+        const int j = block_of[k];
+        Item it;
+        it.page = block_table[size_t(b) * max_blocks + j];
+        it.n_tok = min(128, ctx - j * 128);
+        it.nodes[0] = nodes_of[k][0];
+        it.nodes[1] = PER > 32 ? nodes_of[k][PER / 32 - 1] : 0u;
+        if (it.page < 0 || it.page >= n_pages) {   // refused: seen by no row
+            raise_flag(err, MSA_FLAG_BOUNDS);
+            it.page = 0;
+            it.nodes[0] = it.nodes[1] = 0;
         }
+        list[k] = it;
     }
     const bool drafts = draft_nodes[0] | draft_nodes[1];
     if (tid == 0) {
@@ -254,14 +263,42 @@ __device__ __forceinline__ float fast_exp2(float x) {   // MUFU.EX2, relative er
     return y;
 }
 
-// KSTEPS MMAs of S = Q K^T (K = 16 each), A and B K-major with 128-byte swizzle: a k-step advances 32 bytes
-// within a 64-column box and 16 KB between boxes (+2 / +1024 in the descriptors' units of 16 bytes).
-template <int KSTEPS>
+// D / 16 MMAs of S = Q K^T (K = 16 each), A and B K-major with 128-byte swizzle: a k-step advances 32 bytes within
+// a 64-column box and 16 KB between boxes (+2 / +1024 in the descriptors' units of 16 bytes).  One asm block: MMAs
+// issued one by one lose issue slots to the softmax warps of the sub-partition.  (Issued by a converged
+// warp with one lane predicated, the kernel was 8 % slower: 32 lanes polled each barrier.)
+template <int D>
 __device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-#pragma unroll
-    for (int k = 0; k < KSTEPS; ++k) {
-        const uint64_t o = uint64_t((k & 3) * 2 + (k >> 2) * 1024);
-        mma_bf16(d, a + o, b + o, idesc, k > 0);
+    if constexpr (D == 128) {
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+            "setp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
+            "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 1024;\n\t"
+            "add.s64 b5, %2, 1026;\n\tadd.s64 b6, %2, 1028;\n\tadd.s64 b7, %2, 1030;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+            "setp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
+            : "memory");
     }
 }
 
@@ -280,12 +317,33 @@ __device__ __forceinline__ void mma_pv64(uint32_t d, uint32_t a, uint64_t b, uin
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&r)[32]) {
-    uint32_t lo[16], hi[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) lo[i] = __float_as_uint(r[i]), hi[i] = __float_as_uint(r[i + 16]);
-    tmem_st16(taddr, lo);
-    tmem_st16(taddr + 16, hi);
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Two fp32 lanes per instruction; b2 and c2 hold one value in both halves.
+__device__ __forceinline__ uint64_t dup2(float x) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void ffma2(float &d0, float &d1, float a0, float a1, uint64_t b2, uint64_t c2) {
+    asm("{\n\t.reg .b64 x, d;\n\tmov.b64 x, {%2, %3};\n\tfma.rn.f32x2 d, x, %4, %5;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "l"(b2), "l"(c2));
+}
+__device__ __forceinline__ void fadd2_acc(uint64_t &acc2, float a0, float a1) {
+    asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tadd.rn.f32x2 %0, %0, x;\n\t}" : "+l"(acc2) : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float sum2(uint64_t acc2) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(acc2));
+    return a + b;
 }
 
 // Both softmax groups.
@@ -353,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
         }
-        for (int i = 0; i < kOkRing; ++i) mbar_init(&sm.v_ok[i], 4);
+        for (int i = 0; i < kOkRing; ++i) mbar_init(&sm.v_ok[i], 2);
         for (int w = 0; w < 2; ++w) {
             mbar_init(&sm.s_full[w], 1);
             mbar_init(&sm.p_ready[w], 4);
@@ -390,21 +448,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    long long before = incl - mine, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sm.wsum[w];
-        total += sm.wsum[w];
-    }
+    int sums = lane < kThreads / 32 ? sm.wsum[lane] : 0;
+    const int before = warp_sum_i(lane < warp ? sums : 0) + incl - mine;
+    const long long total = warp_sum_i(sums);
     const int C = int(min((long long)gridDim.x, max(total, 1LL))), cta = blockIdx.x;   // no range is empty
     const long long x0 = cta < C ? range_begin(cta, total, C) : total;
     const long long x1 = cta < C ? range_begin(cta + 1, total, C) : total;
     if (x0 < x1 && x0 >= before && x0 < before + mine) {
-        int t = t_lo;
-        long long at = before;
-        for (;; ++t) {
+        int t = t_lo, at = before;
+        while (t + 1 < t_hi) {
             const int c = tiles[t].n_items & ~kDraftBit;
             if (x0 < at + c) break;
             at += c;
+            ++t;
         }
         sm.tile0 = t;
         sm.off0 = int(x0 - at);
@@ -447,26 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                 for (int s = max(0, seq - NSLOT); s < seq; ++s)
                     mbar_wait(&sm.full[s % NSLOT], (s / NSLOT) & 1, err, nullptr);
         }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ Q loader (lane 0)
-        if (lane == 0) {
-            int loads = 0;
-            while (wk.next()) {
-                if (wk.seg > 0 && !mbar_wait(&sm.q_empty, (wk.seg - 1) & 1, err, &sm.abort)) break;
-                const int nm = wk.t.nodes > NPM ? 2 : 1;
-                mbar_arrive_expect_tx(&sm.q_full, nm * 128 * D * 2);
-                for (int m = 0; m < nm; ++m)
-#pragma unroll
-                    for (int c = 0; c < NSUB; ++c)
-                        tma_load_3d(sm.q[m] + c * 16384, &qmap, &sm.q_full, c * 64, wk.tile % G * HPG,
-                                    wk.t.row + m * NPM);
-                ++loads;
-            }
-            if (sm.abort && loads) mbar_wait(&sm.q_full, (loads - 1) & 1, err, nullptr);
-        }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (lane 0)
         if (lane == 0) {
+            auto wait = [&](uint64_t *bar, int phase) { return mbar_wait(bar, uint32_t(phase & 1), err, &sm.abort); };
             int it = 0;                       // items of this CTA so far
             int units[2] = {0, 0};            // PV units issued per group
             bool ok = true;
@@ -478,13 +518,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             auto issue_pv = [&]() -> bool {
                 const int w = pend.w, seq = 2 * pend.it + 1, slot = seq % NSLOT;
                 if (o_wait) {                 // both groups have read the O of the segment before
-                    if (!mbar_wait(&sm.o_free, (wk.seg - 1) & 1, err, &sm.abort)) return false;
+                    if (!wait(&sm.o_free, wk.seg - 1)) return false;
                     o_wait = false;
                 }
-                if (pend.first_of_item &&
-                    !mbar_wait(&sm.v_ok[pend.it % kOkRing], (pend.it / kOkRing) & 1, err, &sm.abort))
-                    return false;
-                if (!mbar_wait(&sm.p_ready[w], units[w] & 1, err, &sm.abort)) return false;
+                if (pend.first_of_item && !wait(&sm.v_ok[pend.it % kOkRing], pend.it / kOkRing)) return false;
+                if (!wait(&sm.p_ready[w], units[w])) return false;
                 ++units[w];
                 tc_fence_after();
                 const uint64_t vd = make_smem_desc(smem_u32(sm.kv[slot]), 16384, 1024, 2);
@@ -499,20 +537,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             while (ok && wk.next()) {
                 const int nm = wk.t.nodes > NPM ? 2 : 1;
                 o_wait = wk.seg > 0;
-                if (!mbar_wait(&sm.q_full, wk.seg & 1, err, &sm.abort)) break;
+                if (!wait(&sm.q_full, wk.seg)) break;
                 int u = 0;                    // units of this segment
                 for (int i = wk.off; ok && i < wk.end; ++i, ++it) {
                     const bool draft = wk.drafts && i == wk.n_items - 1;
                     const int seq = 2 * it, slot = seq % NSLOT;
-                    if (!mbar_wait(&sm.full[slot], (seq / NSLOT) & 1, err, &sm.abort)) {
+                    if (!wait(&sm.full[slot], seq / NSLOT)) {
                         ok = false;
                         break;
                     }
                     for (int m = 0; m < nm; ++m, ++u) {
                         const int w = u & 1;
                         tc_fence_after();
-                        mma_s<D / 16>(tmem + uint32_t(w * 128), make_smem_desc(smem_u32(sm.q[m]), 16, 1024, 2),
-                                      make_smem_desc(smem_u32(sm.kv[slot]), 16, 1024, 2), draft ? kIdescS64 : kIdescS);
+                        const uint64_t qd = make_smem_desc(smem_u32(sm.q[m]), 16, 1024, 2);
+                        const uint64_t kd = make_smem_desc(smem_u32(sm.kv[slot]), 16, 1024, 2);
+                        mma_s<D>(tmem + uint32_t(w * 128), qd, kd, draft ? kIdescS64 : kIdescS);
                         mma_commit(&sm.s_full[w]);
                         if (m == nm - 1) mma_commit(&sm.empty[slot]);
                         if (m == nm - 1 && i == wk.end - 1) mma_commit(&sm.q_empty);
@@ -534,12 +573,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             mma_commit(&sm.drain);
             mbar_wait(&sm.drain, 0, err, nullptr);
         }
-    } else if (warp >= 12) {
-        // ------------------------------------------------------------ finite check of V
-        const int th = tid - 12 * 32;
-        int it = 0;
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ Q loader (warp 2, lane 0), finite check of V
+        const int th = tid - 64;
+        int it = 0, loads = 0;
         bool ok = true;
         while (ok && wk.next()) {
+            if (tid == 64 && (wk.seg == 0 || mbar_wait(&sm.q_empty, (wk.seg - 1) & 1, err, &sm.abort))) {
+                const int nm = wk.t.nodes > NPM ? 2 : 1;
+                mbar_arrive_expect_tx(&sm.q_full, nm * 128 * D * 2);
+                for (int m = 0; m < nm; ++m)
+#pragma unroll
+                    for (int c = 0; c < NSUB; ++c)
+                        tma_load_3d(sm.q[m] + c * 16384, &qmap, &sm.q_full, c * 64, wk.tile % G * HPG,
+                                    wk.t.row + m * NPM);
+                ++loads;
+            }
+            __syncwarp();
             for (int i = wk.off; i < wk.end; ++i, ++it) {
                 const bool draft = wk.drafts && i == wk.n_items - 1;
                 const int seq = 2 * it + 1, slot = seq % NSLOT;
@@ -552,8 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
 #pragma unroll
                 for (int c = 0; c < NSUB; ++c) {
                     const uint4 *box = reinterpret_cast<const uint4 *>(sm.kv[slot] + c * 16384);
-#pragma unroll 4
-                    for (int k = th; k < per_box; k += 128) {
+#pragma unroll 8
+                    for (int k = th; k < per_box; k += 64) {
                         const uint4 v = box[k];
                         acc |= exp_all_ones(v.x) | exp_all_ones(v.y) | exp_all_ones(v.z) | exp_all_ones(v.w);
                     }
@@ -562,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                     const int n_tok = items[size_t(wk.tile) * cap + i].n_tok;
                     for (int c = 0; c < NSUB; ++c) {
                         uint32_t *box = reinterpret_cast<uint32_t *>(sm.kv[slot] + c * 16384);
-                        for (int k = th; k < per_box; k += 128)
+                        for (int k = th; k < per_box; k += 64)
                             for (int e = 0; e < 4; ++e) {
                                 const uint32_t v = box[4 * k + e], hit = exp_all_ones(v);
                                 if (!hit) continue;
@@ -576,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                 if (lane == 0) mbar_arrive(&sm.v_ok[it % kOkRing]);
             }
         }
-    } else if (warp >= 4) {
+        if (loads && sm.abort) mbar_wait(&sm.q_full, (loads - 1) & 1, err, nullptr);   // lands before the CTA exits
+    } else {
         // ------------------------------------------------------------ softmax groups (warps 4-11)
         const int w = (warp - 4) >> 2;
         const int quad = warp & 3;                 // TMEM lanes this warp may access
@@ -620,96 +671,154 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                 tc_fence_after();
                 if (warp_live) {
                     const int cols = draft ? 64 : 128;
-                    if (!__any_sync(0xffffffffu, sees)) {
+                    uint64_t acc2[4] = {0, 0, 0, 0};
+                    bool done = false;
+                    const bool any = __any_sync(0xffffffffu, sees);
+                    if (!any) {
                         const uint32_t z[16] = {};
-#pragma unroll 1
                         for (int c = 0; c < cols; c += 32) tmem_st16(t_s + uint32_t(c >> 1), z);
-                    } else {
-                        float mx = -INFINITY;
-#pragma unroll 1
-                        for (int c = 0; c < cols; c += 32) {
-                            const uint32_t see = seen(c);
-                            if (!__any_sync(0xffffffffu, see)) continue;
-                            uint32_t v[32];
-                            tmem_ld32(t_s + uint32_t(c), v);
-                            tmem_ld_wait();
-                            if (__all_sync(0xffffffffu, see == ~0u || see == 0u)) {
-                                float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        done = true;
+                    } else if (!draft && item.n_tok == 128) {
+                        // A whole block.  A row without a reference takes the maximum of its first 32 tokens for one;
+                        // no other maximum is taken (a sum past 2^kRaise tells that a logit may be far above the
+                        // reference; S is still whole then, and the loop below starts over).  P stays in
+                        // registers until the end, so that nothing waits between the chunks and the loads run ahead.
+                        uint32_t u[4][32], p[4][16];
+                        uint64_t sum[4] = {0, 0, 0, 0};
+                        uint64_t nm2;
+                        const uint64_t scale2 = dup2(scale);
+                        auto chunk = [&](int i) {
 #pragma unroll
-                                for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                                    for (int x = 0; x < 4; ++x)
-                                        a[x] = fmax3(a[x], __uint_as_float(v[e + x]), __uint_as_float(v[e + 4 + x]));
-                                if (see) mx = fmaxf(mx, fmax3(fmaxf(a[0], a[1]), a[2], a[3]));
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    mx = fmaxf(mx, see >> e & 1 ? __uint_as_float(v[e]) : -INFINITY);
+                            for (int e = 0; e < 16; ++e) {
+                                float pa, pb;
+                                ffma2(pa, pb, __uint_as_float(u[i][2 * e]), __uint_as_float(u[i][2 * e + 1]), scale2, nm2);
+                                pa = fast_exp2(pa);
+                                pb = fast_exp2(pb);
+                                fadd2_acc(sum[e & 3], pa, pb);
+                                p[i][e] = pack_bf16x2(pa, pb);
                             }
+                        };
+                        tmem_ld32(t_s, u[0]);
+                        tmem_ld32(t_s + 32u, u[1]);
+                        tmem_ld_wait();
+                        if (__any_sync(0xffffffffu, sees && m == -INFINITY)) {
+                            float a[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) a[x] = __uint_as_float(u[0][x]);
+#pragma unroll
+                            for (int e = 4; e < 28; e += 8)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    a[x] = fmax3(a[x], __uint_as_float(u[0][e + x]), __uint_as_float(u[0][e + 4 + x]));
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) a[x] = fmaxf(a[x], __uint_as_float(u[0][28 + x]));
+                            const float top = fmaxf(fmax3(a[0], a[1], a[2]), a[3]) * scale;
+                            if (sees && m == -INFINITY && top > m) m = ceilf(top);
                         }
-                        const float top = mx * scale;      // -inf: nothing seen in this item
-                        const bool raise = top > m + kRaise || (m == -INFINITY && top > m);
-                        // O of a row that has seen nothing yet is 0 and needs no rescaling
-                        const float fac = raise && m != -INFINITY ? fast_exp2(m - top) : 1.f;
-                        if (raise) m = top;
-                        l *= fac;
-                        if (mine_n > 0 && __any_sync(0xffffffffu, fac != 1.f)) {
-                            if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_done[w], (k - 1) & 1, err, &sm.abort))) {
-                                ok = false;
-                                break;
+                        tmem_ld32(t_s + 64u, u[2]);
+                        nm2 = dup2(m == -INFINITY ? 0.f : -m);
+                        chunk(0);
+                        tmem_ld_wait();
+                        tmem_ld32(t_s + 96u, u[3]);
+                        chunk(1);
+                        chunk(2);
+                        tmem_ld_wait();
+                        chunk(3);
+                        const float add = (sum2(sum[0]) + sum2(sum[1])) + (sum2(sum[2]) + sum2(sum[3]));
+                        done = !__any_sync(0xffffffffu, sees && add > kRaiseSum);
+                        if (done) {
+                            if (!__all_sync(0xffffffffu, sees)) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) p[i][e] = sees ? p[i][e] : 0u;
                             }
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t v[32];
-                                tmem_ld32(t_o + uint32_t(w * D + c), v);
-                                tmem_ld_wait();
-                                float o[32];
+                            if (sees) l += add;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * fac;
-                                tmem_st32(t_o + uint32_t(w * D + c), o);
-                            }
-                        }
-                        const float nm_ = m == -INFINITY ? 0.f : -m;
-#pragma unroll 1
-                        for (int c = 0; c < cols; c += 32) {
-                            const uint32_t see = seen(c);
-                            uint32_t p[16];
-                            if (!__any_sync(0xffffffffu, see)) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) p[e] = 0u;
-                            } else {
-                                uint32_t v[32];
-                                tmem_ld32(t_s + uint32_t(c), v);
-                                tmem_ld_wait();
-                                float s4[4] = {0.f, 0.f, 0.f, 0.f};
-                                if (__all_sync(0xffffffffu, see == ~0u || see == 0u)) {
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        const float pa = fast_exp2(fmaf(__uint_as_float(v[2 * e]), scale, nm_));
-                                        const float pb = fast_exp2(fmaf(__uint_as_float(v[2 * e + 1]), scale, nm_));
-                                        s4[(2 * e) & 3] += pa;
-                                        s4[(2 * e + 1) & 3] += pb;
-                                        p[e] = see ? pack_bf16x2(pa, pb) : 0u;
-                                    }
-                                    if (see) l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                                } else {
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        float pa = fast_exp2(fmaf(__uint_as_float(v[2 * e]), scale, nm_));
-                                        float pb = fast_exp2(fmaf(__uint_as_float(v[2 * e + 1]), scale, nm_));
-                                        pa = see >> (2 * e) & 1 ? pa : 0.f;
-                                        pb = see >> (2 * e + 1) & 1 ? pb : 0.f;
-                                        s4[(2 * e) & 3] += pa;
-                                        s4[(2 * e + 1) & 3] += pb;
-                                        p[e] = pack_bf16x2(pa, pb);
-                                    }
-                                    l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                                }
-                            }
-                            tmem_st16(t_s + uint32_t(c >> 1), p);
+                            for (int i = 0; i < 4; ++i) tmem_st16(t_s + uint32_t(16 * i), p[i]);
                         }
                     }
+#pragma unroll 1
+                    for (int c = done ? cols : 0; c < cols; c += 32) {
+                        const uint32_t see = seen(c);
+                        uint32_t p[16];
+                        if (!__any_sync(0xffffffffu, see)) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) p[e] = 0u;
+                            tmem_st16(t_s + uint32_t(c >> 1), p);
+                            continue;
+                        }
+                        uint32_t u[32];
+                        tmem_ld32(t_s + uint32_t(c), u);
+                        tmem_ld_wait();
+                        float v[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[e]);
+                        if (!__all_sync(0xffffffffu, see == ~0u)) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = see >> e & 1 ? v[e] : -INFINITY;
+                        }
+                        float a[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) a[x] = fmaxf(v[x], v[4 + x]);
+#pragma unroll
+                        for (int e = 8; e < 32; e += 8)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) a[x] = fmax3(a[x], v[e + x], v[e + 4 + x]);
+                        const float top = fmaxf(fmax3(a[0], a[1], a[2]), a[3]) * scale;   // -inf: nothing seen here
+                        if (__any_sync(0xffffffffu, top > m + kRaise || (m == -INFINITY && top > m))) {
+                            // a row's first tokens (its O and P are 0 so far), or a logit far above its reference
+                            const bool up = top > m + kRaise || (m == -INFINITY && top > m);
+                            const float fac = up && m != -INFINITY ? fast_exp2(m - ceilf(top)) : 1.f;
+                            if (up) m = ceilf(top);
+                            if (__any_sync(0xffffffffu, fac != 1.f)) {
+                                l *= fac;
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    l += sum2(acc2[x]) * fac;
+                                    acc2[x] = 0;
+                                }
+                                if (mine_n > 0) {
+                                    if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_done[w], (k - 1) & 1, err, &sm.abort))) {
+                                        ok = false;
+                                        break;
+                                    }
+                                    tc_fence_after();
+#pragma unroll 1
+                                    for (int d = 0; d < D; d += 16) {
+                                        uint32_t x[16];
+                                        tmem_ld16(t_o + uint32_t(w * D + d), x);
+                                        tmem_ld_wait();
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * fac);
+                                        tmem_st16(t_o + uint32_t(w * D + d), x);
+                                    }
+                                }
+#pragma unroll 1
+                                for (int d = 0; d < (c >> 1); d += 16) {   // this item's P so far
+                                    uint32_t x[16];
+                                    tmem_ld16(t_s + uint32_t(d), x);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) x[e] = pack_bf16x2(bf16_lo(x[e]) * fac, bf16_hi(x[e]) * fac);
+                                    tmem_st16(t_s + uint32_t(d), x);
+                                }
+                                tmem_st_wait();
+                            }
+                        }
+                        const uint64_t scale2 = dup2(scale), nm2 = dup2(m == -INFINITY ? 0.f : -m);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float pa, pb;
+                            ffma2(pa, pb, v[2 * e], v[2 * e + 1], scale2, nm2);
+                            pa = fast_exp2(pa);
+                            pb = fast_exp2(pb);
+                            fadd2_acc(acc2[e & 3], pa, pb);
+                            p[e] = pack_bf16x2(pa, pb);
+                        }
+                        tmem_st16(t_s + uint32_t(c >> 1), p);
+                    }
+                    l += (sum2(acc2[0]) + sum2(acc2[1])) + (sum2(acc2[2]) + sum2(acc2[3]));
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -858,39 +967,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
 
 // ------------------------------------------------------------------ join
 //
-// The partials of a cut tile: O = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over its ranges c.  One thread
-// per row and 8 columns, eight ranges' loads in flight.
+// The partials of a cut tile: O = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over its ranges c.  A CTA has 128
+// rows of a tile and 16 columns, one thread per row and 8 columns, four ranges' loads in flight.
 template <int D, int HPG>
-__global__ void __launch_bounds__(256) k_tree_join(const Tile *__restrict__ tiles, const int2 *__restrict__ cut,
-                                                   const float *__restrict__ part, int G, uint16_t *__restrict__ out,
-                                                   float *__restrict__ lse) {
-    const int tile = blockIdx.x, col = blockIdx.y * 8, row = threadIdx.x;   // rows 128.. : the second 128-row half
+__global__ void __launch_bounds__(256, 4) k_tree_join(const Tile *__restrict__ tiles, const int2 *__restrict__ cut,
+                                                      const float *__restrict__ part, int G,
+                                                      uint16_t *__restrict__ out, float *__restrict__ lse) {
+    const int tile = blockIdx.x >> 1, half = blockIdx.x & 1, r = threadIdx.x & 127;
+    const int col = blockIdx.y * 16 + (threadIdx.x >> 7) * 8;
     pdl_wait();
     const int2 range = cut[tile];
-    if (range.x > range.y) return;   // not cut
-    const int node = row / HPG;
     const int4 tv = *reinterpret_cast<const int4 *>(tiles + tile);
-    if (node >= tv.z) return;
-    const float *base = part + size_t(2 * range.x + 1) * part_floats(D);   // the first range's second slot
+    const int node = half * (128 / HPG) + r / HPG;
+    if (range.x > range.y || node >= tv.z) return;   // not cut; no such row
+    const float *first = part + size_t(2 * range.x + 1) * part_floats(D);   // the first range's second slot
     float m = -INFINITY, l = 0.f, o[8] = {};
-    for (int c0 = range.x; c0 <= range.y; c0 += 8) {
-        float2 ml[8];
-        float4 v[8][2];
+    for (int c0 = range.x; c0 <= range.y; c0 += 4) {
+        float2 ml[4];
+        float4 v[4][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + i;
-            if (c > range.y) break;
-            const float *p = c == range.x ? base : part + size_t(2 * c) * part_floats(D);
-            ml[i] = __ldcg(reinterpret_cast<const float2 *>(p + 256 * D) + row);
-            const float4 *po = reinterpret_cast<const float4 *>(p) + size_t((row >> 7) * (D / 4) + col / 4) * 128 +
-                               (row & 127);
+        for (int i = 0; i < 4; ++i) {
+            const int c = min(c0 + i, range.y);
+            const float *p = c == range.x ? first : part + size_t(2 * c) * part_floats(D);
+            ml[i] = __ldcg(reinterpret_cast<const float2 *>(p + 256 * D) + half * 128 + r);
+            const float4 *po = reinterpret_cast<const float4 *>(p) + size_t(half * (D / 4) + col / 4) * 128 + r;
             v[i][0] = __ldcg(po);
             v[i][1] = __ldcg(po + 128);
+            if (c0 + i > range.y) ml[i] = make_float2(-INFINITY, 0.f);
         }
-        float top = m;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c0 + i <= range.y) top = fmaxf(top, ml[i].x);
+        const float top = fmaxf(fmax3(m, ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
         const float nt = top == -INFINITY ? 0.f : -top;
         const float f = fast_exp2(m + nt);
         m = top;
@@ -898,11 +1003,10 @@ __global__ void __launch_bounds__(256) k_tree_join(const Tile *__restrict__ tile
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] *= f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (c0 + i > range.y) break;
+        for (int i = 0; i < 4; ++i) {
             const float w = fast_exp2(ml[i].x + nt);
             l = fmaf(ml[i].y, w, l);
-            if (w == 0.f) continue;
+            if (w == 0.f) continue;   // nothing seen there (its O may hold anything)
             o[0] = fmaf(w, v[i][0].x, o[0]);
             o[1] = fmaf(w, v[i][0].y, o[1]);
             o[2] = fmaf(w, v[i][0].z, o[2]);
@@ -914,11 +1018,11 @@ __global__ void __launch_bounds__(256) k_tree_join(const Tile *__restrict__ tile
         }
     }
     const bool any = l > 0.f || l != l;
-    const float r = any ? 1.f / l : 0.f;
-    const size_t orow = (size_t(tv.y + node) * G + tile % G) * HPG + row % HPG;
+    const float rcp = any ? 1.f / l : 0.f;
+    const size_t orow = (size_t(tv.y + node) * G + tile % G) * HPG + r % HPG;
     *reinterpret_cast<uint4 *>(out + orow * D + col) =
-        make_uint4(pack_bf16x2(o[0] * r, o[1] * r), pack_bf16x2(o[2] * r, o[3] * r), pack_bf16x2(o[4] * r, o[5] * r),
-                   pack_bf16x2(o[6] * r, o[7] * r));
+        make_uint4(pack_bf16x2(o[0] * rcp, o[1] * rcp), pack_bf16x2(o[2] * rcp, o[3] * rcp),
+                   pack_bf16x2(o[4] * rcp, o[5] * rcp), pack_bf16x2(o[6] * rcp, o[7] * rcp));
     if (col == 0) lse[orow] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
@@ -973,7 +1077,7 @@ cudaError_t launch_t(const void *q, const void *k_cache, const void *v_cache, co
                       static_cast<const Tile *>(tiles), cut, static_cast<const unsigned long long *>(dmask),
                       static_cast<const Item *>(items), part, static_cast<uint16_t *>(out), lse, err);
     if (e != cudaSuccess) return e;
-    return launch_kernel(k_tree_join<D, HPG>, dim3(unsigned(w.tiles), D / 8), dim3(256), 0, st, true,
+    return launch_kernel(k_tree_join<D, HPG>, dim3(unsigned(2 * w.tiles), D / 16), dim3(256), 0, st, true,
                          static_cast<const Tile *>(tiles), static_cast<const int2 *>(cut),
                          static_cast<const float *>(part), s.G, static_cast<uint16_t *>(out), lse);
 }

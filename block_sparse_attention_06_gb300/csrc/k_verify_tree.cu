@@ -2,8 +2,19 @@
 //
 // With r_c(t) = max(p(t) - c q(t), 0) the residual after any number of rejections is r_c / M, M its
 // sum: rejecting a child takes p' to max(p' - q, 0) normalised, i.e. r_c / M to r_{c + M} / M'.  So a
-// node's state is two scalars, and a rejection costs one pass over the node's two rows.
-// One CTA per request walks the path; sums and comparisons are in 64 bits.
+// node's state is two scalars, a test of a child reads two probabilities, and a rejection costs one pass
+// over the node's two rows.  The last pass at the last node also holds the sums that the next token
+// is found by.
+//
+// A cluster of up to 8 CTAs has one request, because a single SM would take tens of microseconds for a
+// pass over a large vocabulary: each warp of the cluster has a contiguous run of tokens, leaves the
+// run's sum in every CTA's shared memory, and after one cluster barrier warp 0 of each CTA goes on with the
+// walk by itself, all of them with the same numbers and so the same decisions.  The next token is then
+// found in the one run that holds it.
+//
+// A rounding of a sum or of p - c q moves a border between two tokens, so both are carried to about 48 bits:
+// as unevaluated sums of two fp32 numbers in the passes (64-bit arithmetic runs at 1/64 of the fp32 rate
+// on this GPU), in 64 bits from the run sums on.
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
@@ -12,165 +23,366 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 
-__device__ __forceinline__ double warp_sum_d(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
+// What warp 0 asks of its CTA.
+enum { kPass, kSelect, kDone };
 
 struct Smem {
-    int parent[kTreeMaxNodes], tok[kTreeMaxNodes];
+    unsigned long long kids[kTreeMaxNodes];                       // children of a node, by number
+    int tok[kTreeMaxNodes];
     float u[kTreeMaxNodes], p[kTreeMaxNodes], q[kTreeMaxNodes];   // at the node's token in its parent's rows
     int gone[kTreeMaxNodes];                                      // tokens taken out (no draft distribution)
-    double part[kWarps];
-    int found;
+    double run[2][kMaxCluster * kWarps];                          // run sums of the cluster, two passes
+    double c, before, want;
+    int cmd, at, n_gone, slot;
 };
 
-__device__ double residual(const float *__restrict__ p, const float *__restrict__ q, double c, const int *gone,
-                           int n_gone, int t) {
-    double r = double(p[t]);
-    if (q) r -= c * double(q[t]);
-    for (int i = 0; i < n_gone; ++i)
-        if (gone[i] == t) r = 0.0;
-    return r > 0.0 ? r : 0.0;
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kThreads) k_verify_tree(
+__device__ __forceinline__ void st_cluster_f64(double *local, uint32_t rank, double v) {
+    uint32_t addr;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+// (h, l) += x + y, |y| far below |x|: the rounding of h + x goes to l.
+__device__ __forceinline__ void add2(float &h, float &l, float x, float y) {
+    const float s = __fadd_rn(h, x), b = __fsub_rn(s, h);
+    l = __fadd_rn(l, __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(x, b)), y));
+    h = s;
+}
+
+struct Residual {
+    float chi, clo;   // c
+    bool draft;
+    // max(p - c q, 0) as hi + lo
+    __device__ __forceinline__ void operator()(float p, float q, float &hi, float &lo) const {
+        if (!draft) {
+            hi = fmaxf(p, 0.f);   // NaN counts as 0
+            lo = 0.f;
+            return;
+        }
+        const float th = __fmul_rn(chi, q), tl = fmaf(clo, q, fmaf(chi, q, -th));
+        const float d = __fsub_rn(p, th), b = __fsub_rn(d, p);
+        const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(th, b)), tl);
+        hi = __fadd_rn(d, e);
+        lo = __fsub_rn(e, __fsub_rn(hi, d));
+        if (!(hi > 0.f)) hi = lo = 0.f;
+        if (p > 3.402823466e38f) hi = p, lo = 0.f;   // an infinite mass is reported, not lost
+    }
+};
+
+template <int VEC>
+struct Chunk {
+    float v[VEC];
+    __device__ __forceinline__ void load(const float *__restrict__ row, int t, int vocab) {
+        if constexpr (VEC == 4) {
+            const float4 x = t < vocab ? __ldg(reinterpret_cast<const float4 *>(row + t)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+            v[0] = t < vocab ? __ldg(row + t) : 0.f;
+        }
+    }
+};
+
+// VEC = 4: rows are 16-byte aligned (vocab a multiple of 4), a lane has four neighbouring tokens; else one.
+template <int VEC>
+__global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
     const float *__restrict__ probs, const float *__restrict__ drafts, int vocab, const int32_t *__restrict__ tokens,
     const int32_t *__restrict__ node_off, const int32_t *__restrict__ parents, const float *__restrict__ u_accept,
-    const float *__restrict__ u_next, int n_rows, int32_t *__restrict__ path, int32_t *__restrict__ n_acc,
-    int32_t *__restrict__ next_token, int32_t *err) {
+    const float *__restrict__ u_next, int n_rows, int cluster, int32_t *__restrict__ path,
+    int32_t *__restrict__ n_acc, int32_t *__restrict__ next_token, int32_t *err) {
+    constexpr int TILE = 32 * VEC;
     __shared__ Smem sm;
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int row0;
-    const int n = tree_rows_of(node_off, b, n_rows, err, tid == 0, &row0);
-    if (n == 0) {
-        if (tid == 0) {
+    const int n = tree_rows_of(node_off, b, n_rows, err, tid == 0 && rank == 0, &row0);
+    if (n == 0) {   // the whole cluster
+        if (tid == 0 && rank == 0) {
             n_acc[b] = 0;
             next_token[b] = -1;
         }
         return;
     }
+    if (tid < n) sm.kids[tid] = 0;
+    __syncthreads();
     if (tid < n) {
         const int par = parents[row0 + tid], tok = tokens[row0 + tid];
         const bool ok = tid > 0 && par >= 0 && par < tid && tok >= 0 && tok < vocab;
-        if (tid == 0 ? par != -1 : !ok) raise_flag(err, MSA_FLAG_BOUNDS);
-        sm.parent[tid] = ok ? par : -1;
-        sm.tok[tid] = tok;
+        if (rank == 0 && (tid == 0 ? par != -1 : !ok)) raise_flag(err, MSA_FLAG_BOUNDS);
         if (ok) {
+            sm.tok[tid] = tok;
             sm.u[tid] = u_accept[row0 + tid];
             sm.p[tid] = probs[size_t(row0 + par) * vocab + tok];
             if (drafts) sm.q[tid] = drafts[size_t(row0 + par) * vocab + tok];
+            atomicOr(&sm.kids[par], 1ull << tid);
         }
-        path[row0 + tid] = -1;
+        if (rank == 0) path[row0 + tid] = -1;
     }
-    __syncthreads();
-    // a contiguous range of the vocabulary per thread
-    const int t0 = int((long long)tid * vocab / kThreads), t1 = int((long long)(tid + 1) * vocab / kThreads);
-    auto block_sum = [&](double v) {
-        v = warp_sum_d(v);
-        __syncthreads();
-        if (lane == 0) sm.part[warp] = v;
-        __syncthreads();
-        double s = 0.0;
-        for (int w = 0; w < kWarps; ++w) s += sm.part[w];
-        return s;
-    };
-    int at = 0, count = 0;
-    double c, mass;
-    int n_gone;
-    const float *p, *q;
+    const int slots = cluster * kWarps, my_slot = rank * kWarps + warp;
+    const int tiles = (vocab + TILE - 1) / TILE;
+    const int tile0 = int((long long)my_slot * tiles / slots), tile1 = int((long long)(my_slot + 1) * tiles / slots);
+    if (cluster > 1) cluster_sync();   // every CTA of the cluster runs before its shared memory is written
+    else __syncthreads();
+
+    // walk state, the same in every lane of warp 0 of every CTA of the cluster
+    int at = 0, count = 0, n_gone = 0, buf = 0;
+    unsigned long long kids = sm.kids[0];
+    double c = 0.0, mass = 1.0;
+    bool whole = false;      // the pass is over p itself (nothing is left of the residual)
+    bool summed = false;     // sm.run[buf ^ 1] holds the run sums of the state (at, c, gone)
+    bool entered = false;    // `at` is in the path
     for (;;) {
-        if (tid == 0) path[row0 + count] = at;
-        ++count;
-        c = 0.0;
-        mass = 1.0;
-        n_gone = 0;
-        p = probs + size_t(row0 + at) * vocab;
-        q = drafts ? drafts + size_t(row0 + at) * vocab : nullptr;
-        int next = -1;
-        for (int x = at + 1; x < n && next < 0; ++x) {
-            if (sm.parent[x] != at) continue;
-            const double qx = q ? double(sm.q[x]) : 1.0;
-            double r = double(sm.p[x]) - (q ? c * qx : 0.0);
-            for (int i = 0; i < n_gone; ++i)
-                if (sm.gone[i] == sm.tok[x]) r = 0.0;
-            if (!(r > 0.0)) r = 0.0;
-            if (double(sm.u[x]) * qx * mass < r) {
-                next = x;
-            } else if (q) {
-                c += mass;
-                double v = 0.0;
-                for (int t = t0; t < t1; ++t) v += residual(p, q, c, nullptr, 0, t);
-                mass = block_sum(v);
-            } else {
-                mass = fmax(mass - r, 0.0);   // rounding of p may leave less than nothing
-                if (tid == 0) sm.gone[n_gone] = sm.tok[x];
-                ++n_gone;
-                __syncthreads();
+        if (warp == 0) {
+            int cmd = -1;
+            while (cmd < 0) {
+                if (!entered) {
+                    if (rank == 0 && lane == 0) path[row0 + count] = at;
+                    ++count;
+                    entered = true;
+                }
+                if (kids && !whole) {
+                    const int x = __ffsll(kids) - 1;
+                    kids &= kids - 1;
+                    const int tok = sm.tok[x];
+                    const double qx = drafts ? double(sm.q[x]) : 1.0;
+                    double r = double(sm.p[x]) - (drafts ? c * qx : 0.0);
+                    if (!(r > 0.0)) r = 0.0;
+                    if (!drafts)
+                        for (int i = 0; i < n_gone; ++i)
+                            if (sm.gone[i] == tok) r = 0.0;
+                    if (double(sm.u[x]) * qx * mass < r) {
+                        at = x;
+                        kids = sm.kids[x];
+                        c = 0.0;
+                        mass = 1.0;
+                        n_gone = 0;
+                        summed = entered = false;
+                    } else if (drafts) {
+                        c += mass;
+                        cmd = kPass;
+                    } else {
+                        mass = fmax(mass - r, 0.0);   // rounding of p may leave less than nothing
+                        if (lane == 0) sm.gone[n_gone] = tok;
+                        ++n_gone;
+                        __syncwarp();
+                    }
+                } else {
+                    cmd = summed ? kSelect : kPass;
+                }
+            }
+            if (cmd == kSelect) {
+                // the run in which the running sum passes u * total; four runs per lane
+                const double *run = sm.run[buf ^ 1];
+                double own[kMaxCluster * kWarps / 32], incl = 0.0;
+#pragma unroll
+                for (int i = 0; i < kMaxCluster * kWarps / 32; ++i) {
+                    const int s = lane * (kMaxCluster * kWarps / 32) + i;
+                    own[i] = s < slots ? run[s] : 0.0;
+                    incl += own[i];
+                }
+                double scan = incl;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double y = __shfl_up_sync(0xffffffffu, scan, o);
+                    if (lane >= o) scan += y;
+                }
+                const double total = __shfl_sync(0xffffffffu, scan, 31);
+                if (!(total > 0.0) || isinf(total)) {
+                    if (!whole && !(isinf(total))) {   // nothing is left of the residual: p itself
+                        whole = true;
+                        c = 0.0;
+                        n_gone = 0;
+                        cmd = kPass;
+                    } else {
+                        if (rank == 0 && lane == 0) {
+                            raise_flag(err, MSA_FLAG_NAN);
+                            next_token[b] = -1;
+                            n_acc[b] = count;
+                        }
+                        cmd = kDone;
+                    }
+                } else {
+                    const double want = double(u_next[b]) * total;
+                    double run_before = scan - incl, found_before = 0.0;
+                    int found = slots;
+#pragma unroll
+                    for (int i = kMaxCluster * kWarps / 32 - 1; i >= 0; --i) {
+                        double bef = run_before;
+#pragma unroll
+                        for (int k = 0; k < kMaxCluster * kWarps / 32; ++k)
+                            if (k < i) bef += own[k];
+                        // the first run whose end passes `want`; an empty run holds no token
+                        if (own[i] > 0.0 && bef + own[i] > want) {
+                            found = lane * (kMaxCluster * kWarps / 32) + i;
+                            found_before = bef;
+                        }
+                    }
+                    const uint32_t hit = __ballot_sync(0xffffffffu, found < slots);
+                    if (hit) {
+                        const int src = __ffs(hit) - 1;
+                        found = __shfl_sync(0xffffffffu, found, src);
+                        found_before = __shfl_sync(0xffffffffu, found_before, src);
+                    } else {   // rounding left the total short: the last run with mass
+                        int last = -1;
+#pragma unroll
+                        for (int i = 0; i < kMaxCluster * kWarps / 32; ++i)
+                            if (own[i] > 0.0) last = lane * (kMaxCluster * kWarps / 32) + i;
+                        found = __reduce_max_sync(0xffffffffu, last);
+                        found_before = 0.0;
+                    }
+                    if (rank == 0 && lane == 0) n_acc[b] = count;
+                    if (lane == 0) {
+                        sm.slot = found;
+                        sm.before = found_before;
+                        sm.want = hit ? want : INFINITY;
+                    }
+                }
+            }
+            if (lane == 0) {
+                sm.cmd = cmd;
+                sm.at = at;
+                sm.c = c;
+                sm.n_gone = n_gone;
             }
         }
-        if (next < 0) break;
-        at = next;
-        __syncthreads();   // sm.gone is free again
-    }
-    // the next token from the residual, or from p where nothing is left of it
-    double mine = 0.0, total = 0.0;
-    for (int attempt = 0; attempt < 2; ++attempt) {
-        if (attempt) q = nullptr, n_gone = 0;
-        mine = 0.0;
-        for (int t = t0; t < t1; ++t) mine += residual(p, q, c, sm.gone, n_gone, t);
-        total = block_sum(mine);
-        if (total > 0.0) break;
-    }
-    if (!(total > 0.0) || isinf(total)) {
-        if (tid == 0) {
-            raise_flag(err, MSA_FLAG_NAN);
-            next_token[b] = -1;
-            n_acc[b] = count;
-        }
-        return;
-    }
-    const double want = double(u_next[b]) * total;
-    // exclusive prefix of this thread's range
-    double incl = mine;
+        __syncthreads();
+        const int cmd = sm.cmd;
+        if (cmd == kDone) break;
+        const float *p = probs + size_t(row0 + sm.at) * vocab;
+        const Residual res{float(sm.c), float(sm.c - double(float(sm.c))), drafts != nullptr && sm.c != 0.0};
+        const float *q = res.draft ? drafts + size_t(row0 + sm.at) * vocab : p;
+        const int gone_n = sm.n_gone;
+        if (cmd == kSelect) {
+            if (sm.slot != my_slot) break;
+            // this warp's run holds the token
+            double before = sm.before;
+            const double want = sm.want;
+            int token = -1;
+            for (int tile = tile0; tile < tile1 && token < 0; ++tile) {
+                const int t = tile * TILE + lane * VEC;
+                Chunk<VEC> cp, cq;
+                cp.load(p, t, vocab);
+                cq.load(q, t, vocab);
+                double r[VEC], incl = 0.0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    __syncthreads();
-    if (lane == 31) sm.part[warp] = incl;
-    if (tid == 0) sm.found = vocab;
-    __syncthreads();
-    double before = incl - mine;
-    for (int w = 0; w < warp; ++w) before += sm.part[w];
-    double run = before;
-    int last = -1;
-    for (int t = t0; t < t1; ++t) {
-        const double r = residual(p, q, c, sm.gone, n_gone, t);
-        run += r;
-        if (r > 0.0) last = t;
-        if (run > want) {
-            atomicMin(&sm.found, t);
+                for (int e = 0; e < VEC; ++e) {
+                    float hi, lo;
+                    res(cp.v[e], cq.v[e], hi, lo);
+                    r[e] = double(hi) + double(lo);
+                    for (int i = 0; i < gone_n; ++i)
+                        if (sm.gone[i] == t + e) r[e] = 0.0;
+                    incl += r[e];
+                }
+                double scan = incl;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double y = __shfl_up_sync(0xffffffffu, scan, o);
+                    if (lane >= o) scan += y;
+                }
+                double run = before + (scan - incl);
+                int mine = vocab;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    run += r[e];
+                    if (mine == vocab && r[e] > 0.0 && run > want) mine = t + e;
+                }
+                const int first = __reduce_min_sync(0xffffffffu, mine);
+                if (first < vocab) token = first;
+                before += __shfl_sync(0xffffffffu, scan, 31);
+            }
+            if (token < 0) {   // rounding: the run's last token with mass
+                for (int tile = tile1 - 1; tile >= tile0 && token < 0; --tile) {
+                    const int t = tile * TILE + lane * VEC;
+                    Chunk<VEC> cp, cq;
+                    cp.load(p, t, vocab);
+                    cq.load(q, t, vocab);
+                    int mine = -1;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        float hi, lo;
+                        res(cp.v[e], cq.v[e], hi, lo);
+                        bool out = false;
+                        for (int i = 0; i < gone_n; ++i) out = out || sm.gone[i] == t + e;
+                        if (hi > 0.f && !out) mine = t + e;
+                    }
+                    token = __reduce_max_sync(0xffffffffu, mine);
+                }
+            }
+            if (lane == 0) next_token[b] = token;
             break;
         }
+        // a pass: this warp's run sum
+        float h = 0.f, l = 0.f;
+        constexpr int U = 8 / VEC;   // tiles in flight
+        for (int tile = tile0; tile < tile1; tile += U) {
+            Chunk<VEC> cp[U], cq[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int t = tile + k < tile1 ? (tile + k) * TILE + lane * VEC : vocab;
+                cp[k].load(p, t, vocab);
+                if (res.draft) cq[k].load(q, t, vocab);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    float hi, lo;
+                    res(cp[k].v[e], cq[k].v[e], hi, lo);
+                    if (gone_n > 0) {
+                        const int t = (tile + k) * TILE + lane * VEC + e;
+                        for (int i = 0; i < gone_n; ++i)
+                            if (sm.gone[i] == t) hi = lo = 0.f;
+                    }
+                    add2(h, l, hi, lo);
+                }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, h, o), y = __shfl_xor_sync(0xffffffffu, l, o);
+            add2(h, l, x, y);
+        }
+        const double sum = double(__shfl_sync(0xffffffffu, h, 0)) + double(__shfl_sync(0xffffffffu, l, 0));
+        if (cluster > 1) {
+            if (lane < cluster) st_cluster_f64(&sm.run[buf][my_slot], uint32_t(lane), sum);
+            cluster_sync();
+        } else {
+            if (lane == 0) sm.run[buf][my_slot] = sum;
+            __syncthreads();
+        }
+        buf ^= 1;
+        if (warp == 0) {   // the residual's mass
+            double s = 0.0;
+            for (int i = lane; i < slots; i += 32) s += sm.run[buf ^ 1][i];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            mass = s;
+            summed = true;
+        }
     }
-    __syncthreads();
-    int tok = sm.found;
-    __syncthreads();
-    if (tok == vocab) {   // rounding left the last range short: the last token with mass
-        if (tid == 0) sm.found = -1;
-        __syncthreads();
-        if (last >= 0) atomicMax(&sm.found, last);
-        __syncthreads();
-        tok = sm.found;
-    }
-    if (tid == 0) {
-        next_token[b] = tok;
-        n_acc[b] = count;
-    }
+    if (cluster > 1) cluster_sync();   // no CTA ends while another may still write its shared memory
+}
+
+template <int VEC>
+cudaError_t launch_t(const float *p, const float *q, int vocab, const int32_t *tokens, const int32_t *node_off,
+                     const int32_t *parents, const float *u_accept, const float *u_next, int n_rows, int n_req,
+                     int cluster, int32_t *path, int32_t *n_acc, int32_t *next_token, int32_t *err, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(n_req) * unsigned(cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_verify_tree<VEC>, p, q, vocab, tokens, node_off, parents, u_accept, u_next, n_rows,
+                              cluster, path, n_acc, next_token, err);
 }
 
 }  // namespace
@@ -179,9 +391,13 @@ cudaError_t launch_verify_tree(const float *p, const float *q, int vocab, const 
                                const int32_t *node_off, const int32_t *parents, const float *u_accept,
                                const float *u_next, int n_rows, int n_req, int32_t *path, int32_t *n_acc,
                                int32_t *next_token, int32_t *err, cudaStream_t st) {
-    k_verify_tree<<<unsigned(n_req), kThreads, 0, st>>>(p, q, vocab, tokens, node_off, parents, u_accept, u_next,
-                                                        n_rows, path, n_acc, next_token, err);
-    return cudaGetLastError();
+    // CTAs per request: enough that a CTA's part of a row is about 4,096 tokens (eight per thread), as long as
+    // all of the batch runs at once (two CTAs per SM)
+    int cluster = 1;
+    while (cluster < kMaxCluster && vocab / cluster > 4096 && 1LL * n_req * cluster <= sm_count()) cluster *= 2;
+    const bool vec = vocab % 4 == 0 && ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
+    return (vec ? launch_t<4> : launch_t<1>)(p, q, vocab, tokens, node_off, parents, u_accept, u_next, n_rows, n_req,
+                                             cluster, path, n_acc, next_token, err, st);
 }
 
 }  // namespace msa
