@@ -18,7 +18,7 @@
 // O, max and sum, in 32 bits) in the workspace, and k_tree_join joins them in the order of the ranges: a
 // kernel of its own, because one CTA reading all partials of a tile took longer than the attention
 // itself (13 partials of 40 rows: 20 us of 35).  Warps:
-//   0      K/V producer: TMA boxes of 64 columns x 128 tokens (128B swizzle) into a ring of tiles;
+//   0      K/V producer: TMA boxes of 64 columns x 128 tokens (128B swizzle) into a ring for each;
 //   1      MMA issuer: S = Q K^T into the TMEM buffer of a softmax group, then, one unit later, O += P V with
 //          P in TMEM (over S) and V as an MN-major shared-memory operand;
 //   4-7, 8-11  two softmax groups, one thread per row.  With up to 128 rows in the tile they take alternate
@@ -31,7 +31,8 @@
 //          finite check of V: a row that does not see a token has P = 0 there, and 0 * NaN would still reach its
 //          O through the MMA, so what is not finite is replaced by 0 before the MMA reads it.  Rows that
 //          do see such a value get it back at the segment's end (add_nonfinite), off the hot path.
-// TMEM: S0 | S1 | O0 | O1 (128 + 128 + D + D of 512 columns).  Every wait is bounded.
+// TMEM: S0 | S1 | O0 | O1 (128 + 128 + D + D of 512 columns).  Every barrier has one waiting role, which waits for each
+// of its phases in order (or, for a group's O, knows the one before to be over).  Every wait is bounded.
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
@@ -242,12 +243,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
 
 template <int D>
 struct TreeSmem {
-    static constexpr int NSLOT = D == 128 ? 5 : 10;
+    static constexpr int NK = D == 128 ? 2 : 5, NV = D == 128 ? 3 : 5;   // V waits one item longer than K
     alignas(1024) uint8_t q[2][128 * D * 2];
-    alignas(1024) uint8_t kv[NSLOT][128 * D * 2];   // K and V tiles, alternating
+    alignas(1024) uint8_t k[NK][128 * D * 2];
+    alignas(1024) uint8_t v[NV][128 * D * 2];
     float2 join[128];              // the second group's (max, sum), then both groups' weights
     uint64_t q_full, q_empty;
-    uint64_t full[NSLOT], empty[NSLOT];
+    uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV];
     uint64_t v_ok[kOkRing];
     uint64_t s_full[2], p_ready[2], o_done[2];
     uint64_t o_free, drain;
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     const unsigned long long *__restrict__ dmask, const Item *__restrict__ items, float *__restrict__ part,
     uint16_t *__restrict__ out, float *__restrict__ lse, int32_t *err) {
     using Smem = TreeSmem<D>;
-    constexpr int NSLOT = Smem::NSLOT;
+    constexpr int NK = Smem::NK, NV = Smem::NV;
     constexpr int NSUB = D / 64;
     constexpr int NPM = 128 / HPG;     // nodes of a 128-row MMA tile
     constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, 0, 0);
@@ -407,9 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     if (tid == 0) {
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1);
-        for (int i = 0; i < NSLOT; ++i) {
-            mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 1);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(&sm.k_full[i], 1);
+            mbar_init(&sm.k_empty[i], 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_empty[i], 1);
         }
         for (int i = 0; i < kOkRing; ++i) mbar_init(&sm.v_ok[i], 2);
         for (int w = 0; w < 2; ++w) {
@@ -472,36 +478,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     if (warp == 0) {
         // ------------------------------------------------------------ K/V producer (lane 0)
         if (lane == 0) {
-            int seq = 0;
+            int it = 0, v_loads = 0;
             bool ok = true;
             while (ok && wk.next()) {
                 const int g = wk.tile % G;
                 const Item *list = items + size_t(wk.tile) * cap;
                 int page = list[wk.off].page;
-                for (int i = wk.off; ok && i < wk.end; ++i) {
+                for (int i = wk.off; i < wk.end; ++i, ++it) {
                     const int page_i = page;
                     if (i + 1 < wk.end) page = list[i + 1].page;   // one ahead
                     const bool draft = wk.drafts && i == wk.n_items - 1;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++seq) {
-                        const int slot = seq % NSLOT;
-                        if (seq >= NSLOT && !mbar_wait(&sm.empty[slot], (seq / NSLOT - 1) & 1, err, &sm.abort)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&sm.full[slot], draft ? 64 * D * 2 : 128 * D * 2);
-#pragma unroll
-                        for (int c = 0; c < NSUB; ++c) {
-                            uint8_t *dst = sm.kv[slot] + c * 16384;
-                            if (draft) tma_load_3d(dst, kv ? &vnmap : &knmap, &sm.full[slot], c * 64, g, wk.t.row0);
-                            else tma_load_4d(dst, kv ? &vmap : &kmap, &sm.full[slot], c * 64, g, 0, page_i);
-                        }
+                    const uint32_t bytes = draft ? 64 * D * 2 : 128 * D * 2;
+                    const int ks = it % NK, vs = it % NV;
+                    if (it >= NK && !mbar_wait(&sm.k_empty[ks], (it / NK - 1) & 1, err, &sm.abort)) {
+                        ok = false;
+                        break;
                     }
+                    mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
+#pragma unroll
+                    for (int c = 0; c < NSUB; ++c) {
+                        if (draft) tma_load_3d(sm.k[ks] + c * 16384, &knmap, &sm.k_full[ks], c * 64, g, wk.t.row0);
+                        else tma_load_4d(sm.k[ks] + c * 16384, &kmap, &sm.k_full[ks], c * 64, g, 0, page_i);
+                    }
+                    if (it >= NV && !mbar_wait(&sm.v_empty[vs], (it / NV - 1) & 1, err, &sm.abort)) {
+                        ok = false;
+                        ++it;   // its K is in flight
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
+#pragma unroll
+                    for (int c = 0; c < NSUB; ++c) {
+                        if (draft) tma_load_3d(sm.v[vs] + c * 16384, &vnmap, &sm.v_full[vs], c * 64, g, wk.t.row0);
+                        else tma_load_4d(sm.v[vs] + c * 16384, &vmap, &sm.v_full[vs], c * 64, g, 0, page_i);
+                    }
+                    v_loads = it + 1;
                 }
             }
-            if (sm.abort)   // the copies still in flight land before the CTA exits
-                for (int s = max(0, seq - NSLOT); s < seq; ++s)
-                    mbar_wait(&sm.full[s % NSLOT], (s / NSLOT) & 1, err, nullptr);
+            if (sm.abort) {   // the copies still in flight land before the CTA exits
+                for (int s = max(0, it - NK); s < it; ++s) mbar_wait(&sm.k_full[s % NK], (s / NK) & 1, err, nullptr);
+                for (int s = max(0, v_loads - NV); s < v_loads; ++s)
+                    mbar_wait(&sm.v_full[s % NV], (s / NV) & 1, err, nullptr);
+            }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (lane 0)
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             } pend{};
             bool have = false, o_wait = false;
             auto issue_pv = [&]() -> bool {
-                const int w = pend.w, seq = 2 * pend.it + 1, slot = seq % NSLOT;
+                const int w = pend.w, slot = pend.it % NV;
                 if (o_wait) {                 // both groups have read the O of the segment before
                     if (!wait(&sm.o_free, wk.seg - 1)) return false;
                     o_wait = false;
@@ -525,12 +542,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                 if (!wait(&sm.p_ready[w], units[w])) return false;
                 ++units[w];
                 tc_fence_after();
-                const uint64_t vd = make_smem_desc(smem_u32(sm.kv[slot]), 16384, 1024, 2);
+                const uint64_t vd = make_smem_desc(smem_u32(sm.v[slot]), 16384, 1024, 2);
                 const uint32_t d = tmem + uint32_t(256 + w * D), a = tmem + uint32_t(w * 128);
                 mma_pv64(d, a, vd, kIdescO, pend.acc);
                 if (!pend.draft) mma_pv64(d, a + 32, vd + 512, kIdescO, 1u);
                 mma_commit(&sm.o_done[w]);
-                if (pend.last_of_item) mma_commit(&sm.empty[slot]);
+                if (pend.last_of_item) mma_commit(&sm.v_empty[slot]);
                 have = false;
                 return true;
             };
@@ -541,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                 int u = 0;                    // units of this segment
                 for (int i = wk.off; ok && i < wk.end; ++i, ++it) {
                     const bool draft = wk.drafts && i == wk.n_items - 1;
-                    const int seq = 2 * it, slot = seq % NSLOT;
-                    if (!wait(&sm.full[slot], seq / NSLOT)) {
+                    const int slot = it % NK;
+                    if (!wait(&sm.k_full[slot], it / NK)) {
                         ok = false;
                         break;
                     }
@@ -550,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                         const int w = u & 1;
                         tc_fence_after();
                         const uint64_t qd = make_smem_desc(smem_u32(sm.q[m]), 16, 1024, 2);
-                        const uint64_t kd = make_smem_desc(smem_u32(sm.kv[slot]), 16, 1024, 2);
+                        const uint64_t kd = make_smem_desc(smem_u32(sm.k[slot]), 16, 1024, 2);
                         mma_s<D>(tmem + uint32_t(w * 128), qd, kd, draft ? kIdescS64 : kIdescS);
                         mma_commit(&sm.s_full[w]);
-                        if (m == nm - 1) mma_commit(&sm.empty[slot]);
+                        if (m == nm - 1) mma_commit(&sm.k_empty[slot]);
                         if (m == nm - 1 && i == wk.end - 1) mma_commit(&sm.q_empty);
                         if (have && !issue_pv()) {
                             ok = false;
@@ -592,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             __syncwarp();
             for (int i = wk.off; i < wk.end; ++i, ++it) {
                 const bool draft = wk.drafts && i == wk.n_items - 1;
-                const int seq = 2 * it + 1, slot = seq % NSLOT;
-                if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[slot], (seq / NSLOT) & 1, err, &sm.abort))) {
+                const int slot = it % NV;
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm.v_full[slot], (it / NV) & 1, err, &sm.abort))) {
                     ok = false;
                     break;
                 }
@@ -601,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                 uint32_t acc = 0;
 #pragma unroll
                 for (int c = 0; c < NSUB; ++c) {
-                    const uint4 *box = reinterpret_cast<const uint4 *>(sm.kv[slot] + c * 16384);
+                    const uint4 *box = reinterpret_cast<const uint4 *>(sm.v[slot] + c * 16384);
 #pragma unroll 8
                     for (int k = th; k < per_box; k += 64) {
                         const uint4 v = box[k];
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                 if (acc) {
                     const int n_tok = items[size_t(wk.tile) * cap + i].n_tok;
                     for (int c = 0; c < NSUB; ++c) {
-                        uint32_t *box = reinterpret_cast<uint32_t *>(sm.kv[slot] + c * 16384);
+                        uint32_t *box = reinterpret_cast<uint32_t *>(sm.v[slot] + c * 16384);
                         for (int k = th; k < per_box; k += 64)
                             for (int e = 0; e < 4; ++e) {
                                 const uint32_t v = box[4 * k + e], hit = exp_all_ones(v);
@@ -829,9 +846,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             const int n0 = nm == 2 ? len : (len + 1) / 2, n1 = nm == 2 ? len : len / 2;
             units[0] += n0;
             units[1] += n1;
-            ok = __all_sync(0xffffffffu, ok && (n0 == 0 || mbar_wait(&sm.o_done[0], (units[0] - 1) & 1, err, &sm.abort)) &&
-                                             (n1 == 0 || mbar_wait(&sm.o_done[1], (units[1] - 1) & 1, err, &sm.abort)));
-            tc_fence_after();
+            // its own O is complete; the other group's is, once the groups have met
+            ok = __all_sync(0xffffffffu, ok && (mine_n == 0 || mbar_wait(&sm.o_done[w], (units[w] - 1) & 1, err, &sm.abort)));
+            tc_fence_before();
             // The segment's (max, sum) of the row and the weights of the two O's.
             float wa = 1.f, wb = 0.f;      // of O0 and O1 (nm == 1), or of the group's own O (nm == 2)
             if (nm == 1) {
@@ -867,6 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                     l = sm.join[row].y;
                 }
             }
+            tc_fence_after();
             const bool fix = *reinterpret_cast<volatile int *>(&sm.nonfinite);
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             if (warp_live && ok) {

@@ -1,15 +1,26 @@
-// Block scores for the nodes of drafted trees.
+// Block scores for the nodes of drafted trees, on the 5th-generation tensor cores.
 //
-// As the multi-token decode scan: s[i, g, j] = max_t q_idx[i, g] . k_idx[t, g] over the tokens of block j
-// that node i may see, with the block's k-index read once for all nodes.  What differs is who is seen:
-// every cached token (position < ctx), and of the drafted tokens the node's ancestors and itself, whose
-// index keys come as dense rows and whose block is (ctx + depth) / 128.  Drafts therefore touch only
-// the block that the context ends in and the one after it.
-//   - one CTA per (request, page, 16 nodes); warp w scores KV group w (and w + 8);
-//   - the warp stages its group's 128 x Di slice of the page in 32-token chunks (16-byte cp.async,
-//     double-buffered, chunk columns XOR-swizzled so that ldmatrix reads them without bank conflicts);
-//   - m16n8k16 bf16 MMAs with tokens as M and nodes as N; the max over tokens is taken on the fp32
-//     accumulators.  A CTA of a block that drafts may touch then scores the drafted keys the same way.
+// s[i, g, j] = max_t q_idx[i, g] . k_idx[t, g] over the tokens of block j that node i may see: every cached token
+// (position < ctx), and of the drafted tokens the node's ancestors and itself, whose index keys come as dense
+// rows and whose block is (ctx + depth) / 128.  Drafts touch only the block that the context ends in and the
+// one after it.
+//
+// The scan reads the k-index once for all nodes of a request, and that read bounds it (61 MB per request of 60,000
+// tokens at G = 8, Di = 64).  One persistent CTA per SM; the units (request, block, group), groups innermost, are
+// cut into one contiguous range per CTA, so that a CTA keeps its request's queries in shared memory and streams
+// whole pages.  With nodes as M (up to 64 of the 128 MMA rows; the rest is ignored) and the block's tokens as N,
+// a node's score is a maximum over one TMEM lane.  Warp-level MMAs with tokens as M, as in the multi-token
+// scan, hold 16 nodes at a time: four passes over the pages for 64 nodes, and 307 us instead of the time below.
+// Warps:
+//   0     TMA: q_idx of a request once, pages as 128-token tiles into a ring for each set, the drafted keys last;
+//   4+5, 8+9, 12+13, 16+17  epilogue sets (a warp can read only the TMEM lane quarter of its index mod 4, and 64
+//         nodes are two quarters), each with every fourth unit and a 128-column accumulator in TMEM;
+//   1, 2, 3, 6  an MMA issuer for each set: the waits and commits of a tile cost one thread about 1,500 cycles,
+//         twice what the pages' read leaves for it (one issuer: 140 us for 8 x 60,000 tokens);
+//   the others write -inf to the blocks past the drafts.
+// Every barrier has one waiting role, which waits for each of its phases in order: a role that could get a whole
+// ring ahead of another on a shared barrier would take the parity of the phase before last for its own.
+// Every wait is bounded.
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
@@ -18,214 +29,403 @@
 namespace msa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kChunkTok = 32;        // tokens per staged chunk
-constexpr int kRows = 16;            // nodes of one CTA (two n-tiles of 8)
+constexpr int kThreads = 18 * 32;
+constexpr int kSets = 4;
+constexpr int kMaxDepth = 3;      // tiles of a set's ring
+constexpr int kFillWarps = 5;
+constexpr int kSmemLimit = 232448 - 1024;   // of a CTA, less the statically declared part
 
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-                 : "r"(addr));
-}
+struct Ctl {
+    uint64_t q_full, q_free;
+    uint64_t full[kSets * kMaxDepth], empty[kSets * kMaxDepth];
+    uint64_t acc_full[kSets], acc_free[kSets];
+    uint64_t drain;   // every issuer's last MMAs
+    int wsum[kThreads / 32];
+    int b0, v0;
+    uint32_t tmem_base;
+    int abort;
+};
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+__device__ __forceinline__ long long range_begin(int c, long long n, int C) { return c * n / C; }
 
-// Position of the 16-byte chunk q of token row i in a staged chunk: rows of DI bf16, chunk index
-// XOR-swizzled so that the 8 rows an ldmatrix phase reads fall in 8 distinct bank groups.
+// A request as the scan sees it.
+struct Req {
+    int row0, n, ctx, nb;   // nb: blocks that hold cached or drafted tokens
+    __device__ __forceinline__ void load(const int32_t *__restrict__ node_off, const int32_t *__restrict__ ctx_lens,
+                                         int b, int n_rows, int max_blocks, int32_t *err, bool report) {
+        n = tree_rows_of(node_off, b, n_rows, err, report, &row0);
+        ctx = ctx_lens[b];
+        if (ctx < 0) {
+            if (report && n > 0) raise_flag(err, MSA_FLAG_BOUNDS);
+            n = 0;
+        }
+        nb = n > 0 ? int(min((long long)max_blocks, ((long long)ctx + n + 127) >> 7)) : 0;
+    }
+};
+
+// The units of a CTA's range, every STRIDE-th from the first-th on; every role walks them for itself.
+template <int STRIDE>
+struct Walk {
+    const int32_t *node_off, *ctx_lens;
+    int n_rows, max_blocks, G;
+    long long left;          // units from the present one to the range's end, this one included
+    int b, j, g;
+    int request;             // requests of the range so far, less one
+    bool begun;
+    Req r;
+    __device__ __forceinline__ void start(int b0, int v0) {
+        b = b0;
+        request = 0;
+        begun = false;
+        j = g = 0;
+        if (left <= 0) return;
+        r.load(node_off, ctx_lens, b, n_rows, max_blocks, nullptr, false);
+        j = v0 / G;
+        g = v0 - j * G;
+    }
+    __device__ __forceinline__ void move(int units) {
+        left -= units;
+        g += units;
+        while (g >= G) {
+            g -= G;
+            if (++j == r.nb) {
+                j = 0;
+                ++request;
+                do r.load(node_off, ctx_lens, ++b, n_rows, max_blocks, nullptr, false);
+                while (r.nb == 0);
+            }
+        }
+    }
+    // On false the walk stands at the range's last unit (so `request` counts all of them).
+    __device__ __forceinline__ bool next(int first = 0) {
+        const int step = begun ? STRIDE : first;
+        begun = true;
+        if (left <= step) {
+            if (left > 1) move(int(left) - 1);
+            return false;
+        }
+        move(step);
+        return true;
+    }
+    __device__ __forceinline__ int cached() const { return min(128, max(0, r.ctx - j * 128)); }
+    __device__ __forceinline__ bool drafts() const { return (j + 1) * 128 > r.ctx; }   // j < nb: some may be here
+};
+
 template <int DI>
-__device__ __forceinline__ uint32_t stage_off(int i, int q) {
-    if constexpr (DI == 64) return uint32_t(i * 128 + ((q ^ (i & 7)) << 4));
-    else return uint32_t(i * 64 + ((q ^ ((i >> 1) & 3)) << 4));
-}
-
-template <int DI>
-__global__ void __launch_bounds__(kWarps * 32) k_score_tree(
-    const uint16_t *__restrict__ q_idx, const uint8_t *__restrict__ kidx, const uint8_t *__restrict__ kidx_new,
-    const int32_t *__restrict__ block_table, const int32_t *__restrict__ ctx_lens,
-    const int32_t *__restrict__ node_off, const uint64_t *__restrict__ anc, int n_rows, int n_pages, int G,
-    int max_blocks, float *__restrict__ scores, int32_t *err) {
-    constexpr int CH = DI / 8;                     // 16-byte chunks per token row
-    constexpr int KS = DI / 16;                    // k-steps of 16
-    constexpr int STAGE = kChunkTok * DI * 2;      // bytes of one staged chunk
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int draft_blk[kTreeMaxNodes];       // block of each drafted token
-    const int b = blockIdx.x, j = blockIdx.y, n0 = blockIdx.z * kRows;
+__global__ void __launch_bounds__(kThreads, 1) k_score_tree(
+    const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+    const __grid_constant__ CUtensorMap dmap, const int32_t *__restrict__ block_table,
+    const int32_t *__restrict__ ctx_lens, const int32_t *__restrict__ node_off, const uint64_t *__restrict__ anc,
+    int n_rows, int n_req, int n_pages, int G, int max_blocks, int depth, float *__restrict__ scores,
+    int32_t *err) {
+    constexpr int TILE = 128 * DI * 2, QTILE = 64 * DI * 2;
+    constexpr uint32_t kSw = DI == 64 ? 2u : 4u;           // descriptor swizzle: 128B / 64B
+    constexpr uint32_t kSbo = 8u * DI * 2u;                // 8 rows of DI bf16
+    constexpr uint32_t kIdesc = make_idesc_bf16(128, 128, 0, 0), kIdesc64 = make_idesc_bf16(128, 64, 0, 0);
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Ctl sm;
+    uint8_t *const q_s = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *const ring = q_s + size_t(G + 1) * QTILE;     // an MMA reads 128 rows: one tile of slack
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int row0;
-    const int n = tree_rows_of(node_off, b, n_rows, err, tid == 0 && j == 0 && n0 == 0, &row0);
-    const int T = min(kRows, n - n0);
-    if (T <= 0) return;
-    const int ctx = ctx_lens[b];
-    if (ctx < 0) {
-        if (tid == 0 && j == 0) raise_flag(err, MSA_FLAG_BOUNDS);
-        return;
-    }
-    const int first = row0 + n0;
-    const int n_cached = min(128, max(0, ctx - j * 128));   // cached tokens of this block
-    const bool drafts = (j + 1) * 128 > ctx && j * 128 < ctx + n;
-    if (n_cached == 0 && !drafts) {
-        for (int i = tid; i < T * G; i += kWarps * 32)
-            scores[(size_t(first + i / G) * G + (i % G)) * max_blocks + j] = -INFINITY;
-        return;
-    }
-    int page = 0;
-    if (n_cached > 0) {
-        page = block_table[size_t(b) * max_blocks + j];
-        if (page < 0 || page >= n_pages) {
-            if (tid == 0) raise_flag(err, MSA_FLAG_BOUNDS);
-            return;
+    if (tid == 0) {
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_free, kSets);
+        for (int i = 0; i < kSets * depth; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
         }
+        for (int s = 0; s < kSets; ++s) {
+            mbar_init(&sm.acc_full[s], 1);
+            mbar_init(&sm.acc_free[s], 2);
+        }
+        mbar_init(&sm.drain, kSets);
+        sm.abort = 0;
+        fence_mbar_init();
     }
-    if (drafts && tid < n) draft_blk[tid] = (ctx + __popcll(anc[row0 + tid]) - 1) >> 7;
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, 128 * kSets);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&dmap);
+    }
+    pdl_wait();
+    pdl_trigger();
+    // this CTA's range: a scan of the requests' units, a run of requests per thread
+    const int b_lo = int((long long)tid * n_req / kThreads), b_hi = int((long long)(tid + 1) * n_req / kThreads);
+    int mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        Req r;
+        r.load(node_off, ctx_lens, b, n_rows, max_blocks, err, blockIdx.x == 0);
+        mine += r.nb * G;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sm.wsum[warp] = incl;
+    tc_fence_before();
     __syncthreads();
-
-    // this lane's accumulator columns: nodes nt * 8 + (lane & 3) * 2 + e
-    uint64_t path[2][2];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = nt * 8 + (lane & 3) * 2 + e;
-            path[nt][e] = drafts && i < T ? anc[first + i] : 0ull;
+    tc_fence_after();
+    const int sums = lane < kThreads / 32 ? sm.wsum[lane] : 0;
+    const int before = warp_sum_i(lane < warp ? sums : 0) + incl - mine;
+    const long long total = warp_sum_i(sums);
+    const int C = int(min((long long)gridDim.x, max(total, 1LL))), cta = blockIdx.x;   // no range is empty
+    const long long x0 = cta < C ? range_begin(cta, total, C) : total;
+    const long long x1 = cta < C ? range_begin(cta + 1, total, C) : total;
+    if (x0 < x1 && x0 >= before && x0 < before + mine) {
+        int b = b_lo, at = before;
+        while (b + 1 < b_hi) {
+            Req r;
+            r.load(node_off, ctx_lens, b, n_rows, max_blocks, nullptr, false);
+            if (x0 < at + r.nb * G) break;
+            at += r.nb * G;
+            ++b;
         }
-    const int NT = (T + 7) >> 3;
-    const uint32_t stage_s = smem_u32(smem + warp * 2 * STAGE);
-    const int cached_chunks = (n_cached + kChunkTok - 1) / kChunkTok;
-    const int chunks = cached_chunks + (drafts ? (n + kChunkTok - 1) / kChunkTok : 0);
+        sm.b0 = b;
+        sm.v0 = int(x0 - at);
+    }
+    __syncthreads();
+    const uint32_t tmem = sm.tmem_base;
+    const int b0 = x0 < x1 ? sm.b0 : 0, v0 = x0 < x1 ? sm.v0 : 0;
 
-    for (int g = warp; g < G; g += kWarps) {
-        // q_idx fragments (B operand, "col": k = d, n = node): b0 = k 0..7 pair, b1 = k 8..15 pair
-        uint32_t bq[2][KS][2];
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer (lane 0)
+        if (lane == 0) {
+            Walk<1> wk{node_off, ctx_lens, n_rows, max_blocks, G, x1 - x0};
+            wk.start(b0, v0);
+            int set = -1, requests = 0, j_of = -1, page = 0, page_next = 0;
+            int at[kSets] = {}, loads[kSets] = {};
+            auto page_of = [&](int j) -> int {
+                return j * 128 < wk.r.ctx ? block_table[size_t(wk.b) * max_blocks + j] : 0;
+            };
+            // the next slot of the unit's ring, once its last reader is done with it; -1 on a timeout
+            auto claim = [&](uint32_t bytes) -> int {
+                int slot = 0, n = 0;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const int i = nt * 8 + (lane >> 2);
-                const int d = ks * 16 + (lane & 3) * 2;
-                uint32_t v0 = 0, v1 = 0;
-                if (i < T) {
-                    const uint16_t *qp = q_idx + (size_t(first + i) * G + g) * DI;
-                    v0 = *reinterpret_cast<const uint32_t *>(qp + d);
-                    v1 = *reinterpret_cast<const uint32_t *>(qp + d + 8);
+                for (int s = 0; s < kSets; ++s)
+                    if (s == set) {
+                        slot = s * depth + at[s];
+                        n = loads[s]++;
+                        if (++at[s] == depth) at[s] = 0;
+                    }
+                if (n >= depth && !mbar_wait(&sm.empty[slot], (n / depth - 1) & 1, err, &sm.abort)) return -1;
+                mbar_arrive_expect_tx(&sm.full[slot], bytes);
+                return slot;
+            };
+            bool ok = true;
+            while (ok && wk.next()) {
+                set = (set + 1) % kSets;
+                if (wk.request == requests) {
+                    if (requests > 0 && !mbar_wait(&sm.q_free, (requests - 1) & 1, err, &sm.abort)) break;
+                    ++requests;
+                    mbar_arrive_expect_tx(&sm.q_full, uint32_t(G) * QTILE);
+                    for (int g = 0; g < G; ++g)
+                        tma_load_3d(q_s + size_t(g) * QTILE, &qmap, &sm.q_full, 0, g, wk.r.row0);
+                    j_of = -1;
+                    page_next = page_of(wk.j);
                 }
-                bq[nt][ks][0] = v0;
-                bq[nt][ks][1] = v1;
+                if (wk.j != j_of) {
+                    j_of = wk.j;
+                    page = page_next;
+                    if (page < 0 || page >= n_pages) {
+                        raise_flag(err, MSA_FLAG_BOUNDS);
+                        page = 0;   // a page that exists; the scores are unspecified
+                    }
+                    if (wk.j + 1 < wk.r.nb) page_next = page_of(wk.j + 1);   // one block ahead
+                }
+                if (wk.cached() > 0) {
+                    const int slot = claim(TILE);
+                    if (!(ok = slot >= 0)) break;
+                    tma_load_4d(ring + size_t(slot) * TILE, &kmap, &sm.full[slot], 0, wk.g, 0, page);
+                }
+                if (wk.drafts()) {
+                    const int slot = claim(QTILE);
+                    if (!(ok = slot >= 0)) break;
+                    tma_load_3d(ring + size_t(slot) * TILE, &dmap, &sm.full[slot], 0, wk.g, wk.r.row0);
+                }
             }
-        // chunk c: 32 cached tokens of the page, or 32 drafted ones; rows past the end repeat the last one
-        auto issue = [&](int c) {
-            const uint32_t dst = stage_s + uint32_t((c & 1) * STAGE);
-            const bool cached = c < cached_chunks;
-            const int t0 = (cached ? c : c - cached_chunks) * kChunkTok;
-            const int lim = cached ? 127 : n - 1;
-            const uint8_t *src = (cached ? kidx + size_t(page) * 128 * G * DI * 2 : kidx_new + size_t(row0) * G * DI * 2) +
-                                 size_t(g) * DI * 2;
-#pragma unroll
-            for (int k = 0; k < kChunkTok * CH / 32; ++k) {
-                const int p = lane + 32 * k;
-                const int i = p / CH, q = p % CH;
-                cp_async_16(dst + stage_off<DI>(i, q), src + size_t(min(t0 + i, lim)) * G * DI * 2 + q * 16);
+            if (sm.abort) {   // the copies still in flight land before the CTA exits
+                for (int s = 0; s < kSets; ++s) {
+                    const int done = loads[s] - (ok || s != set ? 0 : 1);   // a claim that ran out loaded nothing
+                    for (int n = max(0, done - depth); n < done; ++n)
+                        mbar_wait(&sm.full[s * depth + n % depth], (n / depth) & 1, err, nullptr);
+                }
+                if (requests > 0) mbar_wait(&sm.q_full, (requests - 1) & 1, err, nullptr);
             }
-            cp_async_commit();
-        };
-        float mx[2][2];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
-        issue(0);
-        if (chunks > 1) issue(1);
-        else cp_async_commit();
+        }
+    } else if (warp < 4 || warp == 6) {
+        // ------------------------------------------------------------ MMA issuers (lane 0)
+        if (lane == 0) {
+            const int set = warp < 4 ? warp - 1 : 3;
+            Walk<kSets> wk{node_off, ctx_lens, n_rows, max_blocks, G, x1 - x0};
+            wk.start(b0, v0);
+            int at = 0, tiles = 0, left_behind = 0;   // requests whose queries this issuer has done with
+            uint32_t phase = 0;
+            int q_of = -1;
+            // every issuer arrives once for each request of the range but the last, one phase at a time
+            auto leave = [&]() -> bool {
+                for (; left_behind < wk.request; ++left_behind) {
+                    if (left_behind > 0 && !mbar_wait(&sm.q_free, (left_behind - 1) & 1, err, &sm.abort)) return false;
+                    mma_commit(&sm.q_free);
+                }
+                return true;
+            };
+            bool ok = true;
+            while (ok && wk.next(set)) {
+                if (!(ok = leave())) break;
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            cp_async_wait<1>();   // chunk c has landed (chunk c + 1 may be in flight)
-            __syncwarp();
-            const uint32_t buf = stage_s + uint32_t((c & 1) * STAGE);
-            const bool cached = c < cached_chunks;
+                for (int part = 0; part < 2; ++part) {   // cached tokens, drafted tokens
+                    if (!(part ? wk.drafts() : wk.cached() > 0)) continue;
+                    const int slot = set * depth + at;
+                    // the tile first: once it is here, the queries' load has been issued, so that its phase is the one waited for
+                    if (!mbar_wait(&sm.full[slot], phase, err, &sm.abort) ||
+                        (q_of != wk.request && !mbar_wait(&sm.q_full, wk.request & 1, err, &sm.abort)) ||
+                        (tiles > 0 && !mbar_wait(&sm.acc_free[set], (tiles - 1) & 1, err, &sm.abort))) {
+                        ok = false;
+                        break;
+                    }
+                    q_of = wk.request;
+                    ++tiles;
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(q_s + size_t(wk.g) * QTILE);
+                    const uint32_t bb = smem_u32(ring + size_t(slot) * TILE);
 #pragma unroll
-            for (int mt = 0; mt < kChunkTok / 16; ++mt) {
-                float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    // A = 16 tokens x 16 index dims: matrices (rows 0-7 | 8-15) x (cols 0-7 | 8-15)
-                    const int r = mt * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-                    const int q = ks * 2 + (lane >> 4);
-                    uint32_t a0, a1, a2, a3;
-                    ldsm_x4(buf + stage_off<DI>(r, q), a0, a1, a2, a3);
-                    mma16816(acc[0], a0, a1, a2, a3, bq[0][ks][0], bq[0][ks][1]);
-                    if (NT > 1) mma16816(acc[1], a0, a1, a2, a3, bq[1][ks][0], bq[1][ks][1]);
+                    for (int k = 0; k < DI / 16; ++k)
+                        mma_bf16(tmem + uint32_t(set * 128), make_smem_desc(a + k * 32, 16, kSbo, kSw),
+                                 make_smem_desc(bb + k * 32, 16, kSbo, kSw), part ? kIdesc64 : kIdesc, k > 0);
+                    mma_commit(&sm.acc_full[set]);
+                    mma_commit(&sm.empty[slot]);
+                    if (++at == depth) at = 0, phase ^= 1u;
                 }
-                // accumulator: acc[nt][h * 2 + e] = token (lane >> 2) + 8 h, node nt * 8 + (lane & 3) * 2 + e
-                const int tok0 = mt * 16 + (lane >> 2);
-                if (cached) {
+            }
+            if (ok) leave();
+            mma_commit(&sm.drain);
+            mbar_wait(&sm.drain, 0, err, nullptr);
+        }
+    } else if (warp >= 4 && (warp & 3) < 2) {
+        // ------------------------------------------------------------ epilogue sets
+        const int set = (warp >> 2) - 1, quad = warp & 3, i = quad * 32 + lane;   // node i
+        const uint32_t t_s = tmem + (uint32_t(quad * 32) << 16) + uint32_t(set * 128);
+        Walk<kSets> wk{node_off, ctx_lens, n_rows, max_blocks, G, x1 - x0};
+        wk.start(b0, v0);
+        int tiles = 0, b_of = -1;
+        unsigned long long path = 0, first = 0, second = 0;   // of this node; nodes by block: the context's last, the next
+        bool ok = true;
+        while (ok && wk.next(set)) {
+            const Req &r = wk.r;
+            if (wk.drafts() && b_of != wk.b) {
+                b_of = wk.b;
+                path = i < r.n ? anc[r.row0 + i] : 0ull;
+                first = second = 0;
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
+                for (int h = 0; h < 2; ++h) {
+                    const int m = h * 32 + lane;
+                    const int blk = m < r.n ? (r.ctx + __popcll(anc[r.row0 + m]) - 1) >> 7 : -1;
+                    first |= (unsigned long long)__ballot_sync(0xffffffffu, blk == r.ctx >> 7) << (32 * h);
+                    second |= (unsigned long long)__ballot_sync(0xffffffffu, blk == (r.ctx >> 7) + 1) << (32 * h);
+                }
+            }
+            const bool warp_live = quad * 32 < r.n;
+            float best = -INFINITY;
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+                if (!(part ? wk.drafts() : wk.cached() > 0)) continue;
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm.acc_full[set], uint32_t(tiles & 1), err, &sm.abort))) {
+                    ok = false;
+                    break;
+                }
+                ++tiles;
+                tc_fence_after();
+                if (warp_live) {
+                    const unsigned long long seen = path & (wk.j == r.ctx >> 7 ? first : second);
+                    const int lim = part ? 64 : wk.cached();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < lim; c0 += 64) {
+                        uint32_t v[2][32];
+                        tmem_ld32(t_s + uint32_t(c0), v[0]);
+                        tmem_ld32(t_s + uint32_t(c0 + 32), v[1]);
+                        tmem_ld_wait();
+                        if (part || c0 + 64 > lim) {
+                            const unsigned long long see =
+                                part ? seen : lim - c0 >= 64 ? ~0ull : (1ull << (lim - c0)) - 1;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                            for (int e = 0; e < 64; ++e)
+                                if (see >> e & 1) best = fmaxf(best, __uint_as_float(v[e >> 5][e & 31]));
+                        } else {
+                            float a[4] = {best, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (c * kChunkTok + tok0 + 8 * h < n_cached)
-                                    mx[nt][e] = fmaxf(mx[nt][e], acc[nt][h * 2 + e]);
-                } else {
+                            for (int e = 0; e < 64; e += 8)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int t = (c - cached_chunks) * kChunkTok + tok0 + 8 * h;
-                        if (t >= n || draft_blk[t] != j) continue;
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (path[nt][e] >> t & 1) mx[nt][e] = fmaxf(mx[nt][e], acc[nt][h * 2 + e]);
+                                for (int x = 0; x < 4; ++x)
+                                    a[x] = fmax3(a[x], __uint_as_float(v[e >> 5][(e & 31) + x]),
+                                                 __uint_as_float(v[e >> 5][(e & 31) + 4 + x]));
+                            best = fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
+                        }
                     }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.acc_free[set]);
             }
-            __syncwarp();
-            if (c + 2 < chunks) issue(c + 2);
-            else cp_async_commit();   // keep one group per chunk so that wait<1> stays exact
+            if (ok && i < r.n) scores[(size_t(r.row0 + i) * G + wk.g) * max_blocks + wk.j] = best;
         }
-        cp_async_wait<0>();
-        // max over the 8 lanes that share the columns
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float v = mx[nt][e];
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                mx[nt][e] = v;
-            }
-        if (lane < 4) {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = nt * 8 + lane * 2 + e;
-                    if (i < T) scores[(size_t(first + i) * G + g) * max_blocks + j] = mx[nt][e];
+    } else {
+        // ------------------------------------------------------------ -inf past the drafts (warps 7, 10, 11, 14, 15)
+        const int fill = (warp >> 2) * 2 + (warp & 1) - 3;
+        {
+            const int W = int(gridDim.x) * kFillWarps;
+            int at = cta * kFillWarps + fill;   // (row, group) pairs of all requests, dealt to the warps in turn
+            for (int b = 0; b < n_req; ++b) {
+                Req r;
+                r.load(node_off, ctx_lens, b, n_rows, max_blocks, nullptr, false);
+                const int pairs = r.n * G;
+                for (; at < pairs; at += W) {
+                    float *row = scores + (size_t(r.row0) * G + at) * max_blocks;
+                    for (int j = r.nb + lane; j < max_blocks; j += 32) row[j] = -INFINITY;
                 }
+                at -= pairs;
+            }
         }
-        __syncwarp();   // the stage buffers are reused by the next group
     }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 128 * kSets);
 }
 
 template <int DI>
 cudaError_t launch_di(const void *q_idx, const void *kidx, const void *kidx_new, const int32_t *bt, const int32_t *ctx,
                       const int32_t *node_off, const uint64_t *anc, int n_rows, int n_req, int n_pages, const Shape &s,
                       float *scores, int32_t *err, cudaStream_t st) {
-    const size_t smem = size_t(kWarps) * 2 * kChunkTok * DI * 2;
+    alignas(64) CUtensorMap qm, km, dm;
+    const char *why = nullptr;
+    {
+        const uint64_t dims[3] = {uint64_t(DI), uint64_t(s.G), uint64_t(n_rows)};
+        const uint64_t strides[2] = {uint64_t(DI) * 2, uint64_t(s.G) * DI * 2};
+        const uint32_t box[3] = {uint32_t(DI), 1u, 64u};
+        if (!encode_tensor_map(&qm, 3, q_idx, dims, strides, box, DI * 2, &why)) return cudaErrorInvalidValue;
+        if (!encode_tensor_map(&dm, 3, kidx_new, dims, strides, box, DI * 2, &why)) return cudaErrorInvalidValue;
+    }
+    {
+        const uint64_t dims[4] = {uint64_t(DI), uint64_t(s.G), 128ull, uint64_t(n_pages)};
+        const uint64_t strides[3] = {uint64_t(DI) * 2, uint64_t(s.G) * DI * 2, 128ull * s.G * DI * 2};
+        const uint32_t box[4] = {uint32_t(DI), 1u, 128u, 1u};
+        if (!encode_tensor_map(&km, 4, kidx, dims, strides, box, DI * 2, &why)) return cudaErrorInvalidValue;
+    }
+    if (1.0 * n_req * s.max_blocks * s.G > 2147483647.0) return cudaErrorNotSupported;
+    const size_t q_bytes = size_t(s.G + 1) * 64 * DI * 2, tile = 128 * DI * 2;
+    const int depth = int(std::min<size_t>(kMaxDepth, (kSmemLimit - 1024 - q_bytes) / (kSets * tile)));
+    const size_t smem = 1024 + q_bytes + size_t(depth) * kSets * tile;
     cudaError_t e = cudaFuncSetAttribute(k_score_tree<DI>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    const int groups = (std::min(n_rows, kTreeMaxNodes) + kRows - 1) / kRows;
-    const dim3 grid(static_cast<unsigned>(n_req), static_cast<unsigned>(s.max_blocks), static_cast<unsigned>(groups));
-    k_score_tree<DI><<<grid, kWarps * 32, smem, st>>>(
-        static_cast<const uint16_t *>(q_idx), static_cast<const uint8_t *>(kidx),
-        static_cast<const uint8_t *>(kidx_new), bt, ctx, node_off, anc, n_rows, n_pages, s.G, s.max_blocks, scores,
-        err);
-    return cudaGetLastError();
+    return launch_kernel(k_score_tree<DI>, dim3(unsigned(sm_count())), dim3(kThreads), smem, st, true, qm, km, dm, bt,
+                         ctx, node_off, anc, n_rows, n_req, n_pages, s.G, s.max_blocks, depth, scores, err);
 }
 
 }  // namespace

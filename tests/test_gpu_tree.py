@@ -110,6 +110,24 @@ def test_tree_scores(msa, ctx, counts, shape, G, Di):
     assert bool((scores[t.n_rows:] == 77.0).all()), "padding rows were written"
 
 
+@pytest.mark.parametrize("G,Di", [(1, 64), (2, 32), (4, 64), (16, 64)])
+def test_tree_scores_many_requests(msa, G, Di):
+    """Requests of one block or none, several to a range of work, so that a CTA changes its queries often."""
+    B = 700
+    t = T.make_tree([(37 * b) % 150 for b in range(B)], [(7 * b) % 5 for b in range(B)], 12)
+    q, kn = T.bf16((t.n_rows, G, Di), 1), T.bf16((t.n_rows, G, Di), 2)
+    kidx = T.bf16((t.n_pages, 128, G, Di), 3)
+    off, _, ctxd, bt, anc = t.dev(DEV)
+    err = msa.new_err_word(DEV)
+    want, tol = T.ref_scores(t, q, kidx, kn)
+    q, kn, kidx = q.to(DEV), kn.to(DEV), kidx.to(DEV)
+    for _ in range(3):
+        scores = msa.msa_tree_index_score(q, kidx, kn, bt, ctxd, off, anc, _dims(msa, t, 8 * G, G, 128, Di),
+                                          err_word=err)
+        msa.msa_check(err)
+        T.assert_within(scores, want, tol, "scores")
+
+
 def test_tree_scores_flag_bad_page(msa):
     t = T.make_tree([300], [4], 5)
     off, _, ctxd, bt, anc = t.dev(DEV)
