@@ -12,12 +12,14 @@
 // a node's score is a maximum over one TMEM lane.  Warp-level MMAs with tokens as M, as in the multi-token
 // scan, hold 16 nodes at a time: four passes over the pages for 64 nodes, and 307 us instead of the time below.
 // Warps:
-//   0     TMA: q_idx of a request once, pages as 128-token tiles into a ring for each set, the drafted keys last;
 //   4+5, 8+9, 12+13, 16+17  epilogue sets (a warp can read only the TMEM lane quarter of its index mod 4, and 64
 //         nodes are two quarters), each with every fourth unit and a 128-column accumulator in TMEM;
-//   1, 2, 3, 6  an MMA issuer for each set: the waits and commits of a tile cost one thread about 1,500 cycles,
-//         twice what the pages' read leaves for it (one issuer: 140 us for 8 x 60,000 tokens);
-//   the others write -inf to the blocks past the drafts.
+//   0, 7, 10, 11  a producer for each set: 128-token tiles of the pages into the set's ring by TMA, drafted keys last;
+//   1, 2, 3, 6  an MMA issuer for each set.  The waits, address arithmetic and commits of a tile cost one thread
+//         1,000 to 1,500 cycles, more than the 720 that the pages' read leaves for it (one issuer: 140 us for 8 x
+//         60,000 tokens; one producer: 106 us), so neither role is one thread;
+//   14    the queries of a request (all groups), by TMA;
+//   14, 15  write -inf to the blocks past the drafts.
 // Every barrier has one waiting role, which waits for each of its phases in order: a role that could get a whole
 // ring ahead of another on a shared barrier would take the parity of the phase before last for its own.
 // Every wait is bounded.
@@ -32,7 +34,7 @@ namespace {
 constexpr int kThreads = 18 * 32;
 constexpr int kSets = 4;
 constexpr int kMaxDepth = 3;      // tiles of a set's ring
-constexpr int kFillWarps = 5;
+constexpr int kFillWarps = 2;
 constexpr int kSmemLimit = 232448 - 1024;   // of a CTA, less the statically declared part
 
 struct Ctl {
@@ -193,70 +195,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_tree(
     const uint32_t tmem = sm.tmem_base;
     const int b0 = x0 < x1 ? sm.b0 : 0, v0 = x0 < x1 ? sm.v0 : 0;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer (lane 0)
+    if (warp == 0 || warp == 7 || warp == 10 || warp == 11) {
+        // ------------------------------------------------------------ TMA producers (lane 0)
         if (lane == 0) {
-            Walk<1> wk{node_off, ctx_lens, n_rows, max_blocks, G, x1 - x0};
+            const int set = warp == 0 ? 0 : warp == 7 ? 1 : warp - 8;
+            Walk<kSets> wk{node_off, ctx_lens, n_rows, max_blocks, G, x1 - x0};
             wk.start(b0, v0);
-            int set = -1, requests = 0, j_of = -1, page = 0, page_next = 0;
-            int at[kSets] = {}, loads[kSets] = {};
+            int at = 0, loads = 0, b_of = -1, j_of = -1, page = 0, j_ahead = 0, ahead = 0;
+            uint32_t phase = 1;   // of the slot's last reader, from the second round on
             auto page_of = [&](int j) -> int {
                 return j * 128 < wk.r.ctx ? block_table[size_t(wk.b) * max_blocks + j] : 0;
             };
-            // the next slot of the unit's ring, once its last reader is done with it; -1 on a timeout
-            auto claim = [&](uint32_t bytes) -> int {
-                int slot = 0, n = 0;
-#pragma unroll
-                for (int s = 0; s < kSets; ++s)
-                    if (s == set) {
-                        slot = s * depth + at[s];
-                        n = loads[s]++;
-                        if (++at[s] == depth) at[s] = 0;
-                    }
-                if (n >= depth && !mbar_wait(&sm.empty[slot], (n / depth - 1) & 1, err, &sm.abort)) return -1;
-                mbar_arrive_expect_tx(&sm.full[slot], bytes);
-                return slot;
+            // the ring's next slot, once its last reader is done with it
+            auto claim = [&](uint32_t bytes) -> bool {
+                if (loads >= depth && !mbar_wait(&sm.empty[set * depth + at], phase, err, &sm.abort)) return false;
+                mbar_arrive_expect_tx(&sm.full[set * depth + at], bytes);
+                return true;
             };
-            bool ok = true;
-            while (ok && wk.next()) {
-                set = (set + 1) % kSets;
-                if (wk.request == requests) {
-                    if (requests > 0 && !mbar_wait(&sm.q_free, (requests - 1) & 1, err, &sm.abort)) break;
-                    ++requests;
-                    mbar_arrive_expect_tx(&sm.q_full, uint32_t(G) * QTILE);
-                    for (int g = 0; g < G; ++g)
-                        tma_load_3d(q_s + size_t(g) * QTILE, &qmap, &sm.q_full, 0, g, wk.r.row0);
-                    j_of = -1;
-                    page_next = page_of(wk.j);
-                }
-                if (wk.j != j_of) {
+            auto advance = [&]() {
+                ++loads;
+                if (++at == depth) at = 0, phase ^= 1u;
+            };
+            while (wk.next(set)) {
+                if (wk.b != b_of || wk.j != j_of) {
+                    page = wk.b == b_of && wk.j == j_ahead ? ahead : page_of(wk.j);
+                    b_of = wk.b;
                     j_of = wk.j;
-                    page = page_next;
                     if (page < 0 || page >= n_pages) {
                         raise_flag(err, MSA_FLAG_BOUNDS);
                         page = 0;   // a page that exists; the scores are unspecified
                     }
-                    if (wk.j + 1 < wk.r.nb) page_next = page_of(wk.j + 1);   // one block ahead
+                    j_ahead = wk.j + max(1, kSets / G);   // the block of this set's next unit but G / 4, as a rule
+                    if (j_ahead < wk.r.nb) ahead = page_of(j_ahead);
                 }
                 if (wk.cached() > 0) {
-                    const int slot = claim(TILE);
-                    if (!(ok = slot >= 0)) break;
+                    if (!claim(TILE)) break;
+                    const int slot = set * depth + at;
                     tma_load_4d(ring + size_t(slot) * TILE, &kmap, &sm.full[slot], 0, wk.g, 0, page);
+                    advance();
                 }
                 if (wk.drafts()) {
-                    const int slot = claim(QTILE);
-                    if (!(ok = slot >= 0)) break;
+                    if (!claim(QTILE)) break;
+                    const int slot = set * depth + at;
                     tma_load_3d(ring + size_t(slot) * TILE, &dmap, &sm.full[slot], 0, wk.g, wk.r.row0);
+                    advance();
                 }
             }
-            if (sm.abort) {   // the copies still in flight land before the CTA exits
-                for (int s = 0; s < kSets; ++s) {
-                    const int done = loads[s] - (ok || s != set ? 0 : 1);   // a claim that ran out loaded nothing
-                    for (int n = max(0, done - depth); n < done; ++n)
-                        mbar_wait(&sm.full[s * depth + n % depth], (n / depth) & 1, err, nullptr);
-                }
-                if (requests > 0) mbar_wait(&sm.q_full, (requests - 1) & 1, err, nullptr);
-            }
+            if (sm.abort)   // the copies still in flight land before the CTA exits
+                for (int n = max(0, loads - depth); n < loads; ++n)
+                    mbar_wait(&sm.full[set * depth + n % depth], (n / depth) & 1, err, nullptr);
         }
     } else if (warp < 4 || warp == 6) {
         // ------------------------------------------------------------ MMA issuers (lane 0)
@@ -266,10 +253,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_tree(
             wk.start(b0, v0);
             int at = 0, tiles = 0, left_behind = 0;   // requests whose queries this issuer has done with
             uint32_t phase = 0;
-            int q_of = -1;
+            int q_of = -1;   // the request whose queries are here (waited for one by one: each issuer sees every phase)
+            auto queries = [&](int request) -> bool {
+                for (; q_of < request; ++q_of)
+                    if (!mbar_wait(&sm.q_full, (q_of + 1) & 1, err, &sm.abort)) return false;
+                return true;
+            };
             // every issuer arrives once for each request of the range but the last, one phase at a time
             auto leave = [&]() -> bool {
                 for (; left_behind < wk.request; ++left_behind) {
+                    if (!queries(left_behind)) return false;
                     if (left_behind > 0 && !mbar_wait(&sm.q_free, (left_behind - 1) & 1, err, &sm.abort)) return false;
                     mma_commit(&sm.q_free);
                 }
@@ -282,14 +275,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_tree(
                 for (int part = 0; part < 2; ++part) {   // cached tokens, drafted tokens
                     if (!(part ? wk.drafts() : wk.cached() > 0)) continue;
                     const int slot = set * depth + at;
-                    // the tile first: once it is here, the queries' load has been issued, so that its phase is the one waited for
-                    if (!mbar_wait(&sm.full[slot], phase, err, &sm.abort) ||
-                        (q_of != wk.request && !mbar_wait(&sm.q_full, wk.request & 1, err, &sm.abort)) ||
+                    if (!queries(wk.request) || !mbar_wait(&sm.full[slot], phase, err, &sm.abort) ||
                         (tiles > 0 && !mbar_wait(&sm.acc_free[set], (tiles - 1) & 1, err, &sm.abort))) {
                         ok = false;
                         break;
                     }
-                    q_of = wk.request;
                     ++tiles;
                     tc_fence_after();
                     const uint32_t a = smem_u32(q_s + size_t(wk.g) * QTILE);
@@ -375,9 +365,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_tree(
             if (ok && i < r.n) scores[(size_t(r.row0 + i) * G + wk.g) * max_blocks + wk.j] = best;
         }
     } else {
-        // ------------------------------------------------------------ -inf past the drafts (warps 7, 10, 11, 14, 15)
-        const int fill = (warp >> 2) * 2 + (warp & 1) - 3;
-        {
+        // ------------------------------------------------------------ queries (warp 14), -inf past the drafts
+        if (warp == 14 && lane == 0) {
+            Walk<1> wk{node_off, ctx_lens, n_rows, max_blocks, G, x1 - x0};
+            wk.start(b0, v0);
+            int requests = 0;
+            if (x0 < x1)
+                for (;; ++requests) {
+                    if (requests > 0 && !mbar_wait(&sm.q_free, (requests - 1) & 1, err, &sm.abort)) break;
+                    mbar_arrive_expect_tx(&sm.q_full, uint32_t(G) * QTILE);
+                    for (int g = 0; g < G; ++g)
+                        tma_load_3d(q_s + size_t(g) * QTILE, &qmap, &sm.q_full, 0, g, wk.r.row0);
+                    const long long rest = 1LL * wk.r.nb * G - (1LL * wk.j * G + wk.g);   // units to the request's end
+                    if (rest >= wk.left) {
+                        ++requests;
+                        break;
+                    }
+                    wk.move(int(rest));
+                }
+            if (requests > 0 && sm.abort) mbar_wait(&sm.q_full, (requests - 1) & 1, err, nullptr);
+        }
+        __syncwarp();
+        if (warp >= 14) {
+            const int fill = warp - 14;
             const int W = int(gridDim.x) * kFillWarps;
             int at = cta * kFillWarps + fill;   // (row, group) pairs of all requests, dealt to the warps in turn
             for (int b = 0; b < n_req; ++b) {
