@@ -13,14 +13,17 @@
 // popcounts, hence in ascending block order and the same whatever order its threads run in.
 //
 // k_attn_tree, one persistent CTA per SM: the items of all tiles, in order, are cut into one range per CTA,
-// so one long tile is spread over many SMs and many short ones share them.  The part of a tile inside a
+// so one long tile is spread over many SMs and many short ones share them.  Leaving one tile for the next costs
+// a CTA about the time of kTileCost items (its output, and no attention meanwhile), so each tile counts
+// for so many items more where the ranges are cut (one, where a range is a few items and latency counts).  The part of a tile inside a
 // range is a segment; it keeps one online softmax.  A tile cut by a range's end leaves partials (unnormalised
 // O, max and sum, in 32 bits) in the workspace, and k_tree_join joins them in the order of the ranges: a
 // kernel of its own, because one CTA reading all partials of a tile took longer than the attention
 // itself (13 partials of 40 rows: 20 us of 35).  Warps:
 //   0      K/V producer: TMA boxes of 64 columns x 128 tokens (128B swizzle) into a ring for each;
 //   1      MMA issuer: S = Q K^T into the TMEM buffer of a softmax group, then, one unit later, O += P V with
-//          P in TMEM (over S) and V as an MN-major shared-memory operand;
+//          P in TMEM (over S) and V as an MN-major shared-memory operand (an issuer for each was no faster, and
+//          its warp is worth more to the check of V: 16 nodes, 57 us against 52);
 //   4-7, 8-11  two softmax groups, one thread per row.  With up to 128 rows in the tile they take alternate
 //          items, each with an O of its own, joined at the segment's end; with more, each has half the
 //          rows.  P = 2^(s - m) for a reference m that is the row's first maximum (rounded up to a whole
@@ -44,6 +47,7 @@ namespace {
 constexpr int kThreads = 384;           // 168 registers a thread
 constexpr int kMaxCtas = 160;           // partial slots in the workspace; at most one CTA per SM
 constexpr int kOkRing = 8;              // finite-check barriers, by item
+constexpr int kTileCost = 3;           // of a tile, in items, where the ranges are cut
 constexpr int kDraftBit = 1 << 30;      // of a tile's item count: its last item is the drafted tokens
 constexpr float kRaise = 40.0f;         // raise the reference once a logit is this far above (log2 units)
 constexpr float kRaiseSum = 1099511627776.0f;   // 2^kRaise
@@ -63,12 +67,17 @@ struct __align__(16) Tile {
     int32_t row0;       // the request's first row
 };
 
+// 128 rows of a cut tile: the ranges (CTAs) that hold it, its group, first row and nodes.
+struct __align__(16) Cut {
+    int32_t first, last, half, g, row, nodes, pad[2];
+};
+
 struct Layout {
     int per_tile;       // nodes of a tile
     int chunks;         // tiles per (request, group)
     int cap;            // items of a tile, at most
     long long tiles;
-    size_t tile, cut, dmask, items, part, bytes;
+    size_t tile, cut, n_cut, dmask, items, part, bytes;
 };
 
 __host__ __device__ constexpr size_t part_floats(int D) { return size_t(256) * D + 512; }   // O, then (m, l) per row
@@ -83,7 +92,8 @@ inline Layout layout(int n_rows, int n_req, const Shape &s) {
     w.tiles = 1LL * n_req * w.chunks * s.G;
     w.tile = 0;
     w.cut = up(size_t(w.tiles) * sizeof(Tile));
-    w.dmask = w.cut + up(size_t(w.tiles) * sizeof(int2));
+    w.n_cut = w.cut + up(size_t(w.tiles) * 2 * sizeof(Cut));
+    w.dmask = w.n_cut + 256;
     w.items = w.dmask + up(size_t(n_rows) * s.G * 8);
     w.part = w.items + up(size_t(w.tiles) * w.cap * sizeof(Item));
     w.bytes = w.part + size_t(2 * kMaxCtas) * part_floats(s.D) * 4;
@@ -99,7 +109,7 @@ template <int D, int HPG>
 __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
     const int32_t *__restrict__ sel, const int32_t *__restrict__ block_table, const int32_t *__restrict__ ctx_lens,
     const int32_t *__restrict__ node_off, const uint64_t *__restrict__ anc, int n_rows, int n_pages, int G, int topk,
-    int max_blocks, int chunks, int cap, Tile *__restrict__ tiles, int2 *__restrict__ cut,
+    int max_blocks, int chunks, int cap, Tile *__restrict__ tiles, int32_t *__restrict__ n_cut,
     unsigned long long *__restrict__ dmask, Item *__restrict__ items, uint4 *__restrict__ out,
     float *__restrict__ lse, int32_t *err) {
     constexpr int PER = 256 / HPG;                     // nodes of a tile, at most 64
@@ -116,15 +126,15 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
     const int tile = blockIdx.x, g = tile % G, chunk = (tile / G) % chunks, b = tile / G / chunks;
     pdl_wait();
     pdl_trigger();
+    if (tile == 0 && tid == 0) *n_cut = 0;
     int row0;
+    const int ctx = ctx_lens[b];
     const int n = tree_rows_of(node_off, b, n_rows, err, tid == 0 && g == 0 && chunk == 0, &row0);
     const int first = chunk * PER, nt = min(PER, n - first);   // this tile's nodes
-    const int ctx = ctx_lens[b];
     if (nt <= 0 || ctx < 0) {
         if (tid == 0) {
             if (n > 0 && ctx < 0) raise_flag(err, MSA_FLAG_BOUNDS);
             tiles[tile] = Tile{0, 0, 0, 0};
-            cut[tile] = make_int2(0, -1);
         }
         return;
     }
@@ -228,7 +238,6 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
             list[total] = it;
         }
         tiles[tile] = Tile{drafts ? (total + 1) | kDraftBit : total, row0 + first, nt, row0};
-        cut[tile] = make_int2(0, -1);
     }
     if (total == 0 && !drafts) {   // nothing is seen: the rows' results are written here
         constexpr int CH = HPG * D / 8;
@@ -253,8 +262,8 @@ struct TreeSmem {
     uint64_t v_ok[kOkRing];
     uint64_t s_full[2], p_ready[2], o_done[2];
     uint64_t o_free, drain;
-    int wsum[kThreads / 32];
-    int tile0, off0;
+    int2 wsum[kThreads / 32];
+    int tile0, at0;
     uint32_t tmem_base;
     int abort, nonfinite;
 };
@@ -351,31 +360,36 @@ __device__ __forceinline__ float sum2(uint64_t acc2) {
 // Both softmax groups.
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-__device__ __forceinline__ long long range_begin(int c, long long n, int C) { return c * n / C; }
-__device__ __forceinline__ int range_owner(long long x, long long n, int C) { return int(((x + 1) * C - 1) / n); }
+// Ranges are cut in units of cost: a tile has `extra` units before its items.  The first unit of range c:
+__device__ __forceinline__ int range_begin(int c, int n, int C) {
+    if (n < 1 << 24) return int(uint32_t(c) * uint32_t(n) / uint32_t(C));   // c <= kMaxCtas: within 32 bits
+    return int((long long)c * n / C);
+}
+__device__ __forceinline__ int range_owner(int x, int n, int C) { return int(((long long)(x + 1) * C - 1) / n); }
 
 // The CTA's segments in order; every role walks them for itself.
 struct Walk {
     const Tile *tiles;
-    long long x, x1;
+    int x, x1;               // the present tile's first unit of cost; the range's end
+    int extra;               // a tile's cost beside its items
     int tile, off, end, n_items, seg;
     Tile t;
     bool drafts;
     __device__ __forceinline__ bool next() {   // the next segment: items off .. end-1 of `tile`, n_items in it
         if (seg >= 0) {
-            x += end - off;
+            x += n_items + extra;
             ++tile;
             off = 0;
         }
-        if (x >= x1) return false;
         for (;; ++tile) {
+            if (x + extra >= x1) return false;   // no item of the next tile, if any, lies before the end
             const int4 v = *reinterpret_cast<const int4 *>(tiles + tile);
             t = Tile{v.x, v.y, v.z, v.w};
             n_items = t.n_items & ~kDraftBit;
             if (n_items) break;
         }
         drafts = t.n_items & kDraftBit;
-        end = int(min((long long)n_items, off + (x1 - x)));
+        end = min(n_items, x1 - x - extra);
         ++seg;
         return true;
     }
@@ -392,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     const __grid_constant__ CUtensorMap knmap, const __grid_constant__ CUtensorMap vnmap,
     const uint16_t *__restrict__ k_cache, const uint16_t *__restrict__ v_cache, const uint16_t *__restrict__ k_new,
     const uint16_t *__restrict__ v_new, int G, int cap, int n_tiles, float sm_scale,
-    const Tile *__restrict__ tiles, int2 *__restrict__ cut,
+    const Tile *__restrict__ tiles, Cut *__restrict__ cut, int32_t *__restrict__ n_cut,
     const unsigned long long *__restrict__ dmask, const Item *__restrict__ items, float *__restrict__ part,
     uint16_t *__restrict__ out, float *__restrict__ lse, int32_t *err) {
     using Smem = TreeSmem<D>;
@@ -442,38 +456,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     pdl_trigger();
     // this CTA's range: a scan of the tiles' item counts, a run of tiles per thread
     const int t_lo = int((long long)tid * n_tiles / kThreads), t_hi = int((long long)(tid + 1) * n_tiles / kThreads);
-    int mine = 0;
-    for (int t = t_lo; t < t_hi; ++t) mine += tiles[t].n_items & ~kDraftBit;
-    int incl = mine;
+    int mine = 0, mine_t = 0;   // items and tiles
+    for (int t = t_lo; t < t_hi; ++t) {
+        const int c = tiles[t].n_items & ~kDraftBit;
+        mine += c;
+        mine_t += c > 0;
+    }
+    int incl = mine, incl_t = mine_t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const int y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, incl_t, o);
+        if (lane >= o) incl += y, incl_t += z;
     }
-    if (lane == 31) sm.wsum[warp] = incl;
+    if (lane == 31) sm.wsum[warp] = make_int2(incl, incl_t);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int sums = lane < kThreads / 32 ? sm.wsum[lane] : 0;
-    const int before = warp_sum_i(lane < warp ? sums : 0) + incl - mine;
-    const long long total = warp_sum_i(sums);
-    const int C = int(min((long long)gridDim.x, max(total, 1LL))), cta = blockIdx.x;   // no range is empty
-    const long long x0 = cta < C ? range_begin(cta, total, C) : total;
-    const long long x1 = cta < C ? range_begin(cta + 1, total, C) : total;
-    if (x0 < x1 && x0 >= before && x0 < before + mine) {
+    const int2 sums = lane < kThreads / 32 ? sm.wsum[lane] : make_int2(0, 0);
+    const int n_items = warp_sum_i(sums.x), n_live = warp_sum_i(sums.y);
+    const int extra = n_items >= 4 * int(gridDim.x) ? kTileCost : 1;
+    const int before = warp_sum_i(lane < warp ? sums.x + extra * sums.y : 0) + incl - mine + extra * (incl_t - mine_t);
+    const int total = n_items + extra * n_live;
+    // every range holds an item (it is longer than a tile's extra cost), so that a cut tile's ranges are consecutive CTAs
+    const int C = min(int(gridDim.x), max(total / (extra + 1), 1)), cta = blockIdx.x;
+    const int x0 = cta < C ? range_begin(cta, total, C) : total, x1 = cta < C ? range_begin(cta + 1, total, C) : total;
+    if (x0 < x1 && x0 >= before && x0 < before + mine + extra * mine_t) {
         int t = t_lo, at = before;
         while (t + 1 < t_hi) {
             const int c = tiles[t].n_items & ~kDraftBit;
-            if (x0 < at + c) break;
-            at += c;
+            if (c && x0 < at + c + extra) break;
+            at += c ? c + extra : 0;
             ++t;
         }
         sm.tile0 = t;
-        sm.off0 = int(x0 - at);
+        sm.at0 = at;
     }
     __syncthreads();
     const uint32_t tmem = sm.tmem_base;
-    Walk wk{tiles, x0, x1, x0 < x1 ? sm.tile0 : 0, x0 < x1 ? sm.off0 : 0, 0, 0, -1, Tile{}, false};
+    // a range that begins within a tile's cost has the tile from its first item on
+    const int at0 = x0 < x1 ? sm.at0 : total;
+    Walk wk{tiles, at0, x1, extra, x0 < x1 ? sm.tile0 : 0, max(0, x0 - at0 - extra), 0, 0, -1, Tile{}, false};
 
     if (warp == 0) {
         // ------------------------------------------------------------ K/V producer (lane 0)
@@ -591,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             mbar_wait(&sm.drain, 0, err, nullptr);
         }
     } else if (warp < 4) {
-        // ------------------------------------------------------------ Q loader (warp 2, lane 0), finite check of V
+        // ------------------------------------------------------------ Q loads (warp 2, lane 0), finite check of V
         const int th = tid - 64;
         int it = 0, loads = 0;
         bool ok = true;
@@ -973,7 +995,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_free);
             if (!whole && wk.off == 0 && tid == 4 * 32)   // the ranges that hold the tile
-                cut[wk.tile] = make_int2(cta, range_owner(wk.x + wk.n_items - 1, total, C));
+                for (int h = 0; h < nm; ++h)
+                    cut[atomicAdd(n_cut, 1)] = Cut{cta, range_owner(wk.x + extra + wk.n_items - 1, total, C), h, g,
+                                                   wk.t.row + h * NPM, nt - h * NPM, {0, 0}};
         }
     }
 
@@ -986,62 +1010,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
 // ------------------------------------------------------------------ join
 //
 // The partials of a cut tile: O = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over its ranges c.  A CTA has 128
-// rows of a tile and 16 columns, one thread per row and 8 columns, four ranges' loads in flight.
+// rows of a tile and 16 columns at a time, one thread per row and 8 columns, with four ranges' loads in
+// flight: latency bounds it.  The list of cut tiles is in no order; the results do not depend on it.
 template <int D, int HPG>
-__global__ void __launch_bounds__(256, 4) k_tree_join(const Tile *__restrict__ tiles, const int2 *__restrict__ cut,
+__global__ void __launch_bounds__(256, 3) k_tree_join(const Cut *__restrict__ cut, const int32_t *__restrict__ n_cut,
                                                       const float *__restrict__ part, int G,
                                                       uint16_t *__restrict__ out, float *__restrict__ lse) {
-    const int tile = blockIdx.x >> 1, half = blockIdx.x & 1, r = threadIdx.x & 127;
-    const int col = blockIdx.y * 16 + (threadIdx.x >> 7) * 8;
+    constexpr int SLABS = D / 16;
+    const int r = threadIdx.x & 127;
     pdl_wait();
-    const int2 range = cut[tile];
-    const int4 tv = *reinterpret_cast<const int4 *>(tiles + tile);
-    const int node = half * (128 / HPG) + r / HPG;
-    if (range.x > range.y || node >= tv.z) return;   // not cut; no such row
-    const float *first = part + size_t(2 * range.x + 1) * part_floats(D);   // the first range's second slot
-    float m = -INFINITY, l = 0.f, o[8] = {};
-    for (int c0 = range.x; c0 <= range.y; c0 += 4) {
-        float2 ml[4];
-        float4 v[4][2];
+    const int tasks = *n_cut * SLABS;
+    for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const int4 *cv = reinterpret_cast<const int4 *>(cut + task / SLABS);
+        const int4 c0v = cv[0], c1v = cv[1];
+        const int first = c0v.x, last = c0v.y, half = c0v.z;
+        const int node = r / HPG, col = task % SLABS * 16 + (threadIdx.x >> 7) * 8;
+        if (node >= c1v.y) continue;
+        float m = -INFINITY, l = 0.f, o[8] = {};
+        for (int c0 = first; c0 <= last; c0 += 4) {
+            float2 ml[4];
+            float4 v[4][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = min(c0 + i, range.y);
-            const float *p = c == range.x ? first : part + size_t(2 * c) * part_floats(D);
-            ml[i] = __ldcg(reinterpret_cast<const float2 *>(p + 256 * D) + half * 128 + r);
-            const float4 *po = reinterpret_cast<const float4 *>(p) + size_t(half * (D / 4) + col / 4) * 128 + r;
-            v[i][0] = __ldcg(po);
-            v[i][1] = __ldcg(po + 128);
-            if (c0 + i > range.y) ml[i] = make_float2(-INFINITY, 0.f);
+            for (int i = 0; i < 4; ++i) {
+                const int c = min(c0 + i, last);
+                // a tile's first range left it in its second slot, the others in their first
+                const float *p = part + size_t(2 * c + (c == first)) * part_floats(D);
+                ml[i] = __ldcg(reinterpret_cast<const float2 *>(p + 256 * D) + half * 128 + r);
+                const float4 *po = reinterpret_cast<const float4 *>(p) + size_t(half * (D / 4) + col / 4) * 128 + r;
+                if (c0 + i <= last) {
+                    v[i][0] = __ldcg(po);
+                    v[i][1] = __ldcg(po + 128);
+                } else {
+                    ml[i] = make_float2(-INFINITY, 0.f);
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, ml[i].x);
+            const float nt = top == -INFINITY ? 0.f : -top;
+            const float f = fast_exp2(m + nt);
+            m = top;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w = fast_exp2(ml[i].x + nt);
+                l = fmaf(ml[i].y, w, l);
+                if (w == 0.f) continue;   // nothing seen there (its O may hold anything)
+                o[0] = fmaf(w, v[i][0].x, o[0]);
+                o[1] = fmaf(w, v[i][0].y, o[1]);
+                o[2] = fmaf(w, v[i][0].z, o[2]);
+                o[3] = fmaf(w, v[i][0].w, o[3]);
+                o[4] = fmaf(w, v[i][1].x, o[4]);
+                o[5] = fmaf(w, v[i][1].y, o[5]);
+                o[6] = fmaf(w, v[i][1].z, o[6]);
+                o[7] = fmaf(w, v[i][1].w, o[7]);
+            }
         }
-        const float top = fmaxf(fmax3(m, ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-        const float nt = top == -INFINITY ? 0.f : -top;
-        const float f = fast_exp2(m + nt);
-        m = top;
-        l *= f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float w = fast_exp2(ml[i].x + nt);
-            l = fmaf(ml[i].y, w, l);
-            if (w == 0.f) continue;   // nothing seen there (its O may hold anything)
-            o[0] = fmaf(w, v[i][0].x, o[0]);
-            o[1] = fmaf(w, v[i][0].y, o[1]);
-            o[2] = fmaf(w, v[i][0].z, o[2]);
-            o[3] = fmaf(w, v[i][0].w, o[3]);
-            o[4] = fmaf(w, v[i][1].x, o[4]);
-            o[5] = fmaf(w, v[i][1].y, o[5]);
-            o[6] = fmaf(w, v[i][1].z, o[6]);
-            o[7] = fmaf(w, v[i][1].w, o[7]);
-        }
+        const bool any = l > 0.f || l != l;
+        const float rcp = any ? 1.f / l : 0.f;
+        const size_t orow = (size_t(c1v.x + node) * G + c0v.w) * HPG + r % HPG;
+        *reinterpret_cast<uint4 *>(out + orow * D + col) =
+            make_uint4(pack_bf16x2(o[0] * rcp, o[1] * rcp), pack_bf16x2(o[2] * rcp, o[3] * rcp),
+                       pack_bf16x2(o[4] * rcp, o[5] * rcp), pack_bf16x2(o[6] * rcp, o[7] * rcp));
+        if (col == 0) lse[orow] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
-    const bool any = l > 0.f || l != l;
-    const float rcp = any ? 1.f / l : 0.f;
-    const size_t orow = (size_t(tv.y + node) * G + tile % G) * HPG + r % HPG;
-    *reinterpret_cast<uint4 *>(out + orow * D + col) =
-        make_uint4(pack_bf16x2(o[0] * rcp, o[1] * rcp), pack_bf16x2(o[2] * rcp, o[3] * rcp),
-                   pack_bf16x2(o[4] * rcp, o[5] * rcp), pack_bf16x2(o[6] * rcp, o[7] * rcp));
-    if (col == 0) lse[orow] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <int D, int HPG>
@@ -1050,7 +1084,7 @@ cudaError_t launch_t(const void *q, const void *k_cache, const void *v_cache, co
                      const int32_t *sel, int n_rows, int n_req, int n_pages, const Shape &s, void *out, float *lse,
                      void *ws, int32_t *err, cudaStream_t st) {
     const Layout w = layout(n_rows, n_req, s);
-    if (w.tiles * w.cap > 0x3fffffffLL) return cudaErrorNotSupported;
+    if (w.tiles * (w.cap + kTileCost) > 0x3fffffffLL) return cudaErrorNotSupported;
     alignas(64) CUtensorMap qm, km, vm, kn, vn;
     const char *why = nullptr;
     {
@@ -1075,13 +1109,14 @@ cudaError_t launch_t(const void *q, const void *k_cache, const void *v_cache, co
     }
     uint8_t *base = static_cast<uint8_t *>(ws);
     Tile *tiles = reinterpret_cast<Tile *>(base + w.tile);
-    int2 *cut = reinterpret_cast<int2 *>(base + w.cut);
+    Cut *cut = reinterpret_cast<Cut *>(base + w.cut);
+    int32_t *n_cut = reinterpret_cast<int32_t *>(base + w.n_cut);
     auto *dmask = reinterpret_cast<unsigned long long *>(base + w.dmask);
     Item *items = reinterpret_cast<Item *>(base + w.items);
     float *part = reinterpret_cast<float *>(base + w.part);
     cudaError_t e = launch_kernel(k_tree_plan<D, HPG>, dim3(unsigned(w.tiles)), dim3(kPlanThreads), 0, st, true, sel, bt,
                                   ctx, node_off, anc, n_rows, n_pages, s.G, s.topk, s.max_blocks, w.chunks, w.cap,
-                                  tiles, cut, dmask, items, static_cast<uint4 *>(out), lse, err);
+                                  tiles, n_cut, dmask, items, static_cast<uint4 *>(out), lse, err);
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(TreeSmem<D>) + 1024;
     static_assert(sizeof(TreeSmem<D>) + 1024 <= 232448, "shared memory of a CTA");
@@ -1092,11 +1127,11 @@ cudaError_t launch_t(const void *q, const void *k_cache, const void *v_cache, co
                       static_cast<const uint16_t *>(q), qm, km, vm, kn, vn, static_cast<const uint16_t *>(k_cache),
                       static_cast<const uint16_t *>(v_cache), static_cast<const uint16_t *>(k_new),
                       static_cast<const uint16_t *>(v_new), s.G, w.cap, int(w.tiles), s.sm_scale,
-                      static_cast<const Tile *>(tiles), cut, static_cast<const unsigned long long *>(dmask),
+                      static_cast<const Tile *>(tiles), cut, n_cut, static_cast<const unsigned long long *>(dmask),
                       static_cast<const Item *>(items), part, static_cast<uint16_t *>(out), lse, err);
     if (e != cudaSuccess) return e;
-    return launch_kernel(k_tree_join<D, HPG>, dim3(unsigned(2 * w.tiles), D / 16), dim3(256), 0, st, true,
-                         static_cast<const Tile *>(tiles), static_cast<const int2 *>(cut),
+    return launch_kernel(k_tree_join<D, HPG>, dim3(unsigned(4 * grid)), dim3(256), 0, st, true, static_cast<const Cut *>(cut),
+                         static_cast<const int32_t *>(n_cut),
                          static_cast<const float *>(part), s.G, static_cast<uint16_t *>(out), lse);
 }
 
