@@ -532,9 +532,11 @@ def msa_decode_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, seq_len
 def _arg(t, dtype, shape, index: int, name: str) -> int:
     """The address of a tensor argument on device `index`, checked as _req does (which words the
     refusal).  A decode step makes these calls per layer, so the checks that pass are kept short."""
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == index):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _req(t, dtype, name, shape)
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 

@@ -100,13 +100,36 @@ __global__ void __launch_bounds__(256) k_commit_tree(
     const int per = 2 * kv + ix;
     const size_t new_kv = size_t(layer) * n_rows * kv, new_ix = size_t(layer) * n_rows * ix;
     const size_t pool_kv = size_t(layer) * n_pages * 128 * kv, pool_ix = size_t(layer) * n_pages * 128 * ix;
-    for (int i = tid; i < acc * per; i += 256) {
+    // where 16-byte chunk i of the accepted tokens comes from and goes to; null: not written
+    auto chunk = [&](int i, const uint4 *&from, uint4 *&to) {
+        from = nullptr;
+        if (i >= acc * per) return;
         const int t = i / per, c = i - t * per;
         const long long src = src_s[t], dst = dst_s[t];
-        if (src < 0) continue;
-        if (c < kv) k_cache[pool_kv + size_t(dst) * kv + c] = k_new[new_kv + size_t(src) * kv + c];
-        else if (c < 2 * kv) v_cache[pool_kv + size_t(dst) * kv + c - kv] = v_new[new_kv + size_t(src) * kv + c - kv];
-        else ix_cache[pool_ix + size_t(dst) * ix + c - 2 * kv] = ix_new[new_ix + size_t(src) * ix + c - 2 * kv];
+        if (src < 0) return;
+        if (c < kv) {
+            from = k_new + new_kv + size_t(src) * kv + c;
+            to = k_cache + pool_kv + size_t(dst) * kv + c;
+        } else if (c < 2 * kv) {
+            from = v_new + new_kv + size_t(src) * kv + c - kv;
+            to = v_cache + pool_kv + size_t(dst) * kv + c - kv;
+        } else {
+            from = ix_new + new_ix + size_t(src) * ix + c - 2 * kv;
+            to = ix_cache + pool_ix + size_t(dst) * ix + c - 2 * kv;
+        }
+    };
+    // four loads in flight per thread: one at a time, a layer's few tokens take several times the latency
+    for (int i = tid; i < acc * per; i += 4 * 256) {
+        const uint4 *from[4];
+        uint4 *to[4], v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            chunk(i + x * 256, from[x], to[x]);
+            if (from[x]) v[x] = __ldg(from[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (from[x]) *to[x] = v[x];
     }
 }
 

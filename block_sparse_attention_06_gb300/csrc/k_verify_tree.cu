@@ -12,9 +12,11 @@
 // walk by itself, all of them with the same numbers and so the same decisions.  The next token is then
 // found in the one run that holds it.
 //
-// A rounding of a sum or of p - c q moves a border between two tokens, so both are carried to about 48 bits:
-// as unevaluated sums of two fp32 numbers in the passes (64-bit arithmetic runs at 1/64 of the fp32 rate
-// on this GPU), in 64 bits from the run sums on.
+// A rounding of a sum moves a border between two tokens, so sums are carried to more than 40 bits of the whole mass.
+// 64-bit arithmetic runs at 1/64 of the fp32 rate on this GPU and pairs of fp32 numbers for each residual made the
+// pass bound by its arithmetic (3.6 us of 131,072 tokens on 8 CTAs).  A residual's mass is A - c B, A and B the sums
+// of p and q over the tokens with p > c q, and those are sums of given fp32 numbers: each is split at 2^-22 into a
+// part whose sums are exact in fp32 up to 4 and a rest below 2^-23.  Everything from the run sums on is in 64 bits.
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
@@ -24,6 +26,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kInFlight = 8;    // tokens of each row that a thread has in flight
 
 // What warp 0 asks of its CTA.
 enum { kPass, kSelect, kDone };
@@ -33,6 +36,7 @@ struct Smem {
     int tok[kTreeMaxNodes];
     float u[kTreeMaxNodes], p[kTreeMaxNodes], q[kTreeMaxNodes];   // at the node's token in its parent's rows
     int gone[kTreeMaxNodes];                                      // tokens taken out (no draft distribution)
+    float4 part[kWarps];                                          // A and B of each warp's run, split
     double run[2][kMaxCluster * kWarps];                          // run sums of the cluster, two passes
     double c, before, want;
     int cmd, at, n_gone, slot;
@@ -48,30 +52,53 @@ __device__ __forceinline__ void st_cluster_f64(double *local, uint32_t rank, dou
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
 
-// (h, l) += x + y, |y| far below |x|: the rounding of h + x goes to l.
-__device__ __forceinline__ void add2(float &h, float &l, float x, float y) {
-    const float s = __fadd_rn(h, x), b = __fsub_rn(s, h);
-    l = __fadd_rn(l, __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(x, b)), y));
-    h = s;
+// Two fp32 lanes per instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// h + l += v in both lanes: h holds multiples of 2^-22 (exact while the sum of a row stays below 4), l what is left.
+__device__ __forceinline__ void add_split(uint64_t &h, uint64_t &l, uint64_t v) {
+    const uint64_t hi = add2(add2(v, pack2(3.0f, 3.0f)), pack2(-3.0f, -3.0f));
+    h = add2(h, hi);
+    l = add2(l, fma2(hi, pack2(-1.0f, -1.0f), v));
+}
+
+__device__ __forceinline__ float warp_sum_f(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
 struct Residual {
+    double c;
     float chi, clo;   // c
     bool draft;
-    // max(p - c q, 0) as hi + lo
-    __device__ __forceinline__ void operator()(float p, float q, float &hi, float &lo) const {
-        if (!draft) {
-            hi = fmaxf(p, 0.f);   // NaN counts as 0
-            lo = 0.f;
-            return;
-        }
-        const float th = __fmul_rn(chi, q), tl = fmaf(clo, q, fmaf(chi, q, -th));
-        const float d = __fsub_rn(p, th), b = __fsub_rn(d, p);
-        const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(th, b)), tl);
-        hi = __fadd_rn(d, e);
-        lo = __fsub_rn(e, __fsub_rn(hi, d));
-        if (!(hi > 0.f)) hi = lo = 0.f;
-        if (p > 3.402823466e38f) hi = p, lo = 0.f;   // an infinite mass is reported, not lost
+    // whether p - c q > 0 (NaN: no)
+    __device__ __forceinline__ bool positive(float p, float q) const {
+        return draft ? fmaf(-clo, q, fmaf(-chi, q, p)) > 0.f : p > 0.f;
+    }
+    __device__ __forceinline__ double value(float p, float q) const {
+        if (!positive(p, q)) return 0.0;
+        const double r = draft ? double(p) - c * double(q) : double(p);
+        return r > 0.0 ? r : 0.0;
     }
 };
 
@@ -208,18 +235,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
                     }
                 } else {
                     const double want = double(u_next[b]) * total;
-                    double run_before = scan - incl, found_before = 0.0;
+                    double end = scan - incl, found_before = 0.0;
                     int found = slots;
 #pragma unroll
-                    for (int i = kMaxCluster * kWarps / 32 - 1; i >= 0; --i) {
-                        double bef = run_before;
-#pragma unroll
-                        for (int k = 0; k < kMaxCluster * kWarps / 32; ++k)
-                            if (k < i) bef += own[k];
+                    for (int i = 0; i < kMaxCluster * kWarps / 32; ++i) {
                         // the first run whose end passes `want`; an empty run holds no token
-                        if (own[i] > 0.0 && bef + own[i] > want) {
+                        const double begin = end;
+                        end += own[i];
+                        if (found == slots && own[i] > 0.0 && end > want) {
                             found = lane * (kMaxCluster * kWarps / 32) + i;
-                            found_before = bef;
+                            found_before = begin;
                         }
                     }
                     const uint32_t hit = __ballot_sync(0xffffffffu, found < slots);
@@ -254,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
         const int cmd = sm.cmd;
         if (cmd == kDone) break;
         const float *p = probs + size_t(row0 + sm.at) * vocab;
-        const Residual res{float(sm.c), float(sm.c - double(float(sm.c))), drafts != nullptr && sm.c != 0.0};
+        const Residual res{sm.c, float(sm.c), float(sm.c - double(float(sm.c))), drafts != nullptr && sm.c != 0.0};
         const float *q = res.draft ? drafts + size_t(row0 + sm.at) * vocab : p;
         const int gone_n = sm.n_gone;
         if (cmd == kSelect) {
@@ -271,9 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
                 double r[VEC], incl = 0.0;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    float hi, lo;
-                    res(cp.v[e], cq.v[e], hi, lo);
-                    r[e] = double(hi) + double(lo);
+                    r[e] = res.value(cp.v[e], cq.v[e]);
                     for (int i = 0; i < gone_n; ++i)
                         if (sm.gone[i] == t + e) r[e] = 0.0;
                     incl += r[e];
@@ -304,11 +327,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
                     int mine = -1;
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        float hi, lo;
-                        res(cp.v[e], cq.v[e], hi, lo);
                         bool out = false;
                         for (int i = 0; i < gone_n; ++i) out = out || sm.gone[i] == t + e;
-                        if (hi > 0.f && !out) mine = t + e;
+                        if (res.value(cp.v[e], cq.v[e]) > 0.0 && !out) mine = t + e;
                     }
                     token = __reduce_max_sync(0xffffffffu, mine);
                 }
@@ -316,9 +337,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
             if (lane == 0) next_token[b] = token;
             break;
         }
-        // a pass: this warp's run sum
-        float h = 0.f, l = 0.f;
-        constexpr int U = 8 / VEC;   // tiles in flight
+        // a pass: this warp's run sum, A - c B
+        uint64_t ah2 = 0, al2 = 0, bh2 = 0, bl2 = 0;
+        const uint64_t nchi2 = pack2(-res.chi, -res.chi), nclo2 = pack2(-res.clo, -res.clo);
+        constexpr int U = kInFlight / VEC;   // tiles in flight
         for (int tile = tile0; tile < tile1; tile += U) {
             Chunk<VEC> cp[U], cq[U];
 #pragma unroll
@@ -327,33 +349,53 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
                 cp[k].load(p, t, vocab);
                 if (res.draft) cq[k].load(q, t, vocab);
             }
+            if (gone_n > 0) {
 #pragma unroll
-            for (int k = 0; k < U; ++k)
+                for (int k = 0; k < U; ++k)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    float hi, lo;
-                    res(cp[k].v[e], cq[k].v[e], hi, lo);
-                    if (gone_n > 0) {
-                        const int t = (tile + k) * TILE + lane * VEC + e;
+                    for (int e = 0; e < VEC; ++e)
                         for (int i = 0; i < gone_n; ++i)
-                            if (sm.gone[i] == t) hi = lo = 0.f;
-                    }
-                    add2(h, l, hi, lo);
-                }
-        }
+                            if (sm.gone[i] == (tile + k) * TILE + lane * VEC + e) cp[k].v[e] = 0.f;
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float x = __shfl_xor_sync(0xffffffffu, h, o), y = __shfl_xor_sync(0xffffffffu, l, o);
-            add2(h, l, x, y);
+            for (int x = 0; x < U * VEC; x += 2) {
+                const float p0 = cp[x / VEC].v[x % VEC], p1 = cp[(x + 1) / VEC].v[(x + 1) % VEC];
+                if (res.draft) {
+                    const float q0 = cq[x / VEC].v[x % VEC], q1 = cq[(x + 1) / VEC].v[(x + 1) % VEC];
+                    const uint64_t q2 = pack2(q0, q1);
+                    const float2 r = unpack2(fma2(nclo2, q2, fma2(nchi2, q2, pack2(p0, p1))));
+                    add_split(ah2, al2, pack2(r.x > 0.f ? p0 : 0.f, r.y > 0.f ? p1 : 0.f));
+                    add_split(bh2, bl2, pack2(r.x > 0.f ? q0 : 0.f, r.y > 0.f ? q1 : 0.f));
+                } else {
+                    add_split(ah2, al2, pack2(fmaxf(p0, 0.f), fmaxf(p1, 0.f)));   // NaN counts as 0
+                }
+            }
         }
-        const double sum = double(__shfl_sync(0xffffffffu, h, 0)) + double(__shfl_sync(0xffffffffu, l, 0));
-        if (cluster > 1) {
-            if (lane < cluster) st_cluster_f64(&sm.run[buf][my_slot], uint32_t(lane), sum);
-            cluster_sync();
-        } else {
-            if (lane == 0) sm.run[buf][my_slot] = sum;
-            __syncthreads();
+        auto both = [](uint64_t v) {
+            const float2 x = unpack2(v);
+            return x.x + x.y;
+        };
+        float ah = both(ah2), al = both(al2), bh = both(bh2), bl = both(bl2);
+        ah = warp_sum_f(ah);
+        al = warp_sum_f(al);
+        if (res.draft) {
+            bh = warp_sum_f(bh);
+            bl = warp_sum_f(bl);
         }
+        if (lane == 0) sm.part[warp] = make_float4(ah, al, bh, bl);
+        __syncthreads();
+        // one warp joins them: the SM has two 64-bit operations a cycle, and 16 warps would queue up for them
+        if (warp == 0 && lane < kWarps) {
+            const float4 v = sm.part[lane];
+            double sum = double(v.x) + double(v.y);
+            if (res.draft) sum -= res.c * (double(v.z) + double(v.w));
+            if (sum < 0.0) sum = 0.0;   // a rounding of nothing (NaN stays)
+            if (cluster == 1) sm.run[buf][lane] = sum;
+            else
+                for (int r = 0; r < cluster; ++r) st_cluster_f64(&sm.run[buf][rank * kWarps + lane], uint32_t(r), sum);
+        }
+        if (cluster > 1) cluster_sync();
+        else __syncthreads();
         buf ^= 1;
         if (warp == 0) {   // the residual's mass
             double s = 0.0;
