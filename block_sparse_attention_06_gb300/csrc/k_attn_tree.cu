@@ -9,8 +9,12 @@
 // the nodes that selected it) and one item for the drafted tokens, and each item's K and V are read once
 // for all nodes of the tile.  That read bounds the kernel as long as several nodes share a block.
 //
-// k_tree_plan, one CTA per tile: the union through a bitmap over blocks in shared memory, ranked by
-// popcounts, hence in ascending block order and the same whatever order its threads run in.
+// k_tree_plan, one CTA per (request, group): the union through a bitmap over blocks in shared memory, ranked by
+// popcounts, hence in ascending block order and the same whatever order its threads run in.  With HPG = 8 and more
+// than 16 nodes, nodes of like selections become neighbours: they are ordered by the least hash of their blocks that
+// not most nodes have, which is the same for two nodes the more likely the more of their blocks they share.  Tiles
+// then have smaller unions, and the 128-row halves of a tile skip the items that none of their nodes selected
+// (8 x 60,000 tokens, 64 nodes that share windows of 7 blocks by fives: 233 us in the trees' own order).
 //
 // k_attn_tree, one persistent CTA per SM: the items of all tiles, in order, are cut into one range per CTA,
 // so one long tile is spread over many SMs and many short ones share them.  Leaving one tile for the next costs
@@ -48,6 +52,7 @@ constexpr int kThreads = 384;           // 168 registers a thread
 constexpr int kMaxCtas = 160;           // partial slots in the workspace; at most one CTA per SM
 constexpr int kOkRing = 8;              // finite-check barriers, by item
 constexpr int kTileCost = 3;           // of a tile, in items, where the ranges are cut
+constexpr int kSortedBit = 1 << 30;     // of a tile's place in `order`: not the nodes' own order
 constexpr int kDraftBit = 1 << 30;      // of a tile's item count: its last item is the drafted tokens
 constexpr float kRaise = 40.0f;         // raise the reference once a logit is this far above (log2 units)
 constexpr float kRaiseSum = 1099511627776.0f;   // 2^kRaise
@@ -63,13 +68,13 @@ struct __align__(16) Item {
 // What the plan says of a tile; n_items 0: nothing to do.
 struct __align__(16) Tile {
     int32_t n_items;    // | kDraftBit
-    int32_t row, nodes; // its first row and its nodes
-    int32_t row0;       // the request's first row
+    int32_t nodes, row0;   // its nodes, the request's first row
+    int32_t ord;        // where its nodes' numbers begin in `order` | kSortedBit
 };
 
-// 128 rows of a cut tile: the ranges (CTAs) that hold it, its group, first row and nodes.
+// 128 rows of a cut tile: the ranges (CTAs) that hold it, and whose rows they are.
 struct __align__(16) Cut {
-    int32_t first, last, half, g, row, nodes, pad[2];
+    int32_t first, last, half, g, row0, nodes, ord, pad;
 };
 
 struct Layout {
@@ -77,7 +82,7 @@ struct Layout {
     int chunks;         // tiles per (request, group)
     int cap;            // items of a tile, at most
     long long tiles;
-    size_t tile, cut, n_cut, dmask, items, part, bytes;
+    size_t tile, cut, n_cut, order, dmask, items, part, bytes;
 };
 
 __host__ __device__ constexpr size_t part_floats(int D) { return size_t(256) * D + 512; }   // O, then (m, l) per row
@@ -93,7 +98,8 @@ inline Layout layout(int n_rows, int n_req, const Shape &s) {
     w.tile = 0;
     w.cut = up(size_t(w.tiles) * sizeof(Tile));
     w.n_cut = w.cut + up(size_t(w.tiles) * 2 * sizeof(Cut));
-    w.dmask = w.n_cut + 256;
+    w.order = w.n_cut + 256;
+    w.dmask = w.order + up(size_t(n_req) * s.G * kTreeMaxNodes);
     w.items = w.dmask + up(size_t(n_rows) * s.G * 8);
     w.part = w.items + up(size_t(w.tiles) * w.cap * sizeof(Item));
     w.bytes = w.part + size_t(2 * kMaxCtas) * part_floats(s.D) * 4;
@@ -105,59 +111,83 @@ inline Layout layout(int n_rows, int n_req, const Shape &s) {
 constexpr int kPlanThreads = 256;
 constexpr int kMaxWords = 16384 / 32;   // bitmap over blocks
 
+// Exclusive prefix of v over the CTA's threads; *total gets the sum.
+__device__ __forceinline__ int plan_scan(int v, int *wsum, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int before = incl - v, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        const int x = wsum[w];
+        if (w < warp) before += x;
+        sum += x;
+    }
+    *total = sum;
+    return before;
+}
+
 template <int D, int HPG>
-__global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
+__global__ void __launch_bounds__(kPlanThreads, 2) k_tree_plan(
     const int32_t *__restrict__ sel, const int32_t *__restrict__ block_table, const int32_t *__restrict__ ctx_lens,
     const int32_t *__restrict__ node_off, const uint64_t *__restrict__ anc, int n_rows, int n_pages, int G, int topk,
     int max_blocks, int chunks, int cap, Tile *__restrict__ tiles, int32_t *__restrict__ n_cut,
-    unsigned long long *__restrict__ dmask, Item *__restrict__ items, uint4 *__restrict__ out,
-    float *__restrict__ lse, int32_t *err) {
+    uint8_t *__restrict__ order, unsigned long long *__restrict__ dmask, Item *__restrict__ items,
+    uint4 *__restrict__ out, float *__restrict__ lse, int32_t *err) {
     constexpr int PER = 256 / HPG;                     // nodes of a tile, at most 64
-    constexpr int CAP = PER * 32;                      // items, at most
+    constexpr int NPM = 128 / HPG;                     // nodes of 128 rows
+    constexpr int CAP = kTreeMaxNodes * 32;            // selected blocks, at most
+    constexpr int EPT = CAP / kPlanThreads;
     __shared__ uint32_t bits[kMaxWords];
     __shared__ uint32_t rank[kMaxWords];               // set bits below the word
-    __shared__ uint32_t nodes_of[CAP][PER / 32];
+    __shared__ uint32_t nodes_of[CAP][2];              // by the nodes' numbers, then by their places
     __shared__ uint16_t block_of[CAP];
     __shared__ unsigned long long in_first, in_second; // nodes whose block is ctx / 128, or the next one
-    __shared__ uint32_t has[PER];                      // bit 0 / 1: the node selected that block
-    __shared__ uint32_t draft_nodes[2];
-    __shared__ int wsum[kPlanThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tile = blockIdx.x, g = tile % G, chunk = (tile / G) % chunks, b = tile / G / chunks;
+    __shared__ uint32_t has[kTreeMaxNodes];            // bit 0 / 1: the node selected that block
+    __shared__ uint32_t key[kTreeMaxNodes];
+    __shared__ uint8_t place[kTreeMaxNodes];
+    __shared__ uint32_t draft_at[2];                   // places whose nodes see drafted tokens
+    __shared__ int wsum[2][kPlanThreads / 32];
+    const int tid = threadIdx.x;
+    const int b = blockIdx.x / G, g = blockIdx.x - b * G;
     pdl_wait();
     pdl_trigger();
-    if (tile == 0 && tid == 0) *n_cut = 0;
+    if (blockIdx.x == 0 && tid == 0) *n_cut = 0;
     int row0;
     const int ctx = ctx_lens[b];
-    const int n = tree_rows_of(node_off, b, n_rows, err, tid == 0 && g == 0 && chunk == 0, &row0);
-    const int first = chunk * PER, nt = min(PER, n - first);   // this tile's nodes
-    if (nt <= 0 || ctx < 0) {
-        if (tid == 0) {
-            if (n > 0 && ctx < 0) raise_flag(err, MSA_FLAG_BOUNDS);
-            tiles[tile] = Tile{0, 0, 0, 0};
-        }
+    const int n = tree_rows_of(node_off, b, n_rows, err, tid == 0 && g == 0, &row0);
+    auto tile_of = [&](int chunk) { return (b * chunks + chunk) * G + g; };
+    if (n <= 0 || ctx < 0) {
+        if (n > 0 && tid == 0) raise_flag(err, MSA_FLAG_BOUNDS);
+        if (tid < chunks) tiles[tile_of(tid)] = Tile{0, 0, 0, 0};
         return;
     }
-    const int words = (max_blocks + 31) >> 5;
-    for (int i = tid; i < words; i += kPlanThreads) bits[i] = 0;
-    for (int i = tid; i < CAP * (PER / 32); i += kPlanThreads) (&nodes_of[0][0])[i] = 0;
-    if (tid < PER) has[tid] = 0;
-    if (tid == 0) in_first = in_second = 0, draft_nodes[0] = draft_nodes[1] = 0;
-    __syncthreads();
-    const int j0 = ctx >> 7;
-    if (tid < n) {
-        const int j = (ctx + __popcll(anc[row0 + tid]) - 1) >> 7;
-        if (j == j0) atomicOr(&in_first, 1ull << tid);
-        else if (j == j0 + 1) atomicOr(&in_second, 1ull << tid);
-    }
     // this thread's entries of the selection, loaded together (-1 where there is none)
-    constexpr int EPT = CAP / kPlanThreads;
-    const int n_ent = nt * topk;
+    const int n_ent = n * topk;
     int ent[EPT];
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
         const int e = tid + x * kPlanThreads;
-        ent[x] = e < n_ent ? sel[(size_t(row0 + first + e / topk) * G + g) * topk + e % topk] : -1;
+        ent[x] = e < n_ent ? sel[(size_t(row0 + e / topk) * G + g) * topk + e % topk] : -1;
+    }
+    const unsigned long long path = tid < n ? anc[row0 + tid] : 0ull;
+    const int words = (max_blocks + 31) >> 5;
+    for (int i = tid; i < words; i += kPlanThreads) bits[i] = 0;
+    for (int i = tid; i < 2 * min(n_ent, CAP); i += kPlanThreads) (&nodes_of[0][0])[i] = 0;
+    if (tid < kTreeMaxNodes) has[tid] = 0, key[tid] = ~0u;
+    if (tid == 0) in_first = in_second = 0, draft_at[0] = draft_at[1] = 0;
+    __syncthreads();
+    const int j0 = ctx >> 7;
+    if (tid < n) {
+        const int j = (ctx + __popcll(path) - 1) >> 7;
+        if (j == j0) atomicOr(&in_first, 1ull << tid);
+        else if (j == j0 + 1) atomicOr(&in_second, 1ull << tid);
     }
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
@@ -174,77 +204,107 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(
         else ent[x] = -1;   // a block without cached tokens
     }
     __syncthreads();
-    // rank of every word: a scan of the popcounts, two words per thread
+    // rank of every word, two words per thread; every selected block's place in the union and its nodes
     const int w0 = 2 * tid, w1 = w0 + 1;
     const int p0 = w0 < words ? __popc(bits[w0]) : 0, p1 = w1 < words ? __popc(bits[w1]) : 0;
-    int incl = p0 + p1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    int before = incl - p0 - p1, total = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) before += wsum[w];
-        total += wsum[w];
-    }
+    int total;
+    const int before = plan_scan(p0 + p1, wsum[0], &total);
     if (w0 < words) rank[w0] = before;
     if (w1 < words) rank[w1] = before + p0;
-    // the drafted tokens that each node sees
-    if (tid < nt) {
-        unsigned long long m = 0;
-        if (has[tid] & 1) m |= in_first;
-        if (has[tid] & 2) m |= in_second;
-        const int r = row0 + first + tid;
-        m &= anc[r] & (n == 64 ? ~0ull : (1ull << n) - 1);
-        dmask[size_t(r) * G + g] = m;
-        if (m) atomicOr(&draft_nodes[tid >> 5], 1u << (tid & 31));
-    }
+    if (tid < n) place[tid] = uint8_t(tid);
     __syncthreads();
+    const bool sorted = HPG == 8 && n > NPM;   // (with HPG = 4, Q comes in boxes of neighbouring rows)
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
         const int j = ent[x], i = (tid + x * kPlanThreads) / topk;
         if (j < 0) continue;
         const int k = rank[j >> 5] + __popc(bits[j >> 5] & ((1u << (j & 31)) - 1));
+        ent[x] = k;              // from here on: the block's place in the union
         atomicOr(&nodes_of[k][i >> 5], 1u << (i & 31));
         block_of[k] = uint16_t(j);   // the same from every node that selected it
     }
     __syncthreads();
-    Item *list = items + size_t(tile) * cap;
-    for (int k = tid; k < total; k += kPlanThreads) {
-        const int j = block_of[k];
-        Item it;
-        it.page = block_table[size_t(b) * max_blocks + j];
-        it.n_tok = min(128, ctx - j * 128);
-        it.nodes[0] = nodes_of[k][0];
-        it.nodes[1] = PER > 32 ? nodes_of[k][PER / 32 - 1] : 0u;
-        if (it.page < 0 || it.page >= n_pages) {   // refused: seen by no row
-            raise_flag(err, MSA_FLAG_BOUNDS);
-            it.page = 0;
-            it.nodes[0] = it.nodes[1] = 0;
+    if (sorted) {
+#pragma unroll
+        for (int x = 0; x < EPT; ++x) {
+            const int k = ent[x], i = (tid + x * kPlanThreads) / topk;
+            if (k < 0 || 2 * (__popc(nodes_of[k][0]) + __popc(nodes_of[k][1])) > n) continue;
+            atomicMin(&key[i], (uint32_t(block_of[k]) + 1u) * 2654435761u);
         }
-        list[k] = it;
+        __syncthreads();
+        if (tid < n) {
+            const uint32_t mine = key[tid];
+            int p = 0;
+            for (int m = 0; m < n; ++m) p += key[m] < mine || (key[m] == mine && m < tid);
+            place[tid] = uint8_t(p);
+        }
+        for (int i = tid; i < 2 * total; i += kPlanThreads) (&nodes_of[0][0])[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < EPT; ++x) {
+            const int k = ent[x], i = (tid + x * kPlanThreads) / topk;
+            if (k < 0) continue;
+            const int p = place[i];
+            atomicOr(&nodes_of[k][p >> 5], 1u << (p & 31));
+        }
     }
-    const bool drafts = draft_nodes[0] | draft_nodes[1];
-    if (tid == 0) {
-        if (drafts) {
+    // the drafted tokens that each node sees, and the nodes by place
+    if (tid < n) {
+        unsigned long long m = 0;
+        if (has[tid] & 1) m |= in_first;
+        if (has[tid] & 2) m |= in_second;
+        m &= path & (n == 64 ? ~0ull : (1ull << n) - 1);
+        dmask[size_t(row0 + tid) * G + g] = m;
+        const int p = place[tid];
+        if (m) atomicOr(&draft_at[p >> 5], 1u << (p & 31));
+        order[size_t(blockIdx.x) * kTreeMaxNodes + p] = uint8_t(tid);
+    }
+    __syncthreads();
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+        const int tile = tile_of(chunk), nt = min(PER, n - chunk * PER);
+        if (nt <= 0) {
+            if (tid == 0) tiles[tile] = Tile{0, 0, 0, 0};
+            continue;
+        }
+        auto nodes_at = [&](const uint32_t (&w)[2], int h) { return PER == 64 ? w[h] : h ? 0u : w[chunk & 1]; };
+        // the union's blocks that a node of this tile selected: a run of them per thread, counted, then written
+        const int k0 = tid * total / kPlanThreads, k1 = (tid + 1) * total / kPlanThreads;
+        int mine = 0, n_blocks;
+        for (int k = k0; k < k1; ++k) mine += (nodes_at(nodes_of[k], 0) | nodes_at(nodes_of[k], 1)) != 0;
+        int at = plan_scan(mine, wsum[(chunk + 1) & 1], &n_blocks);
+        Item *list = items + size_t(tile) * cap;
+        for (int k = k0; k < k1; ++k) {
             Item it;
-            it.page = 0;
-            it.n_tok = n;
-            it.nodes[0] = draft_nodes[0];
-            it.nodes[1] = draft_nodes[1];
-            list[total] = it;
+            it.nodes[0] = nodes_at(nodes_of[k], 0);
+            it.nodes[1] = nodes_at(nodes_of[k], 1);
+            if (!(it.nodes[0] | it.nodes[1])) continue;
+            const int j = block_of[k];
+            it.page = block_table[size_t(b) * max_blocks + j];
+            it.n_tok = min(128, ctx - j * 128);
+            if (it.page < 0 || it.page >= n_pages) {   // refused: seen by no row
+                raise_flag(err, MSA_FLAG_BOUNDS);
+                it.page = 0;
+                it.nodes[0] = it.nodes[1] = 0;
+            }
+            list[at++] = it;
         }
-        tiles[tile] = Tile{drafts ? (total + 1) | kDraftBit : total, row0 + first, nt, row0};
-    }
-    if (total == 0 && !drafts) {   // nothing is seen: the rows' results are written here
-        constexpr int CH = HPG * D / 8;
-        for (int i = tid; i < nt * CH; i += kPlanThreads)
-            out[(size_t(row0 + first + i / CH) * G + g) * CH + i % CH] = make_uint4(0, 0, 0, 0);
-        for (int i = tid; i < nt * HPG; i += kPlanThreads)
-            lse[(size_t(row0 + first + i / HPG) * G + g) * HPG + i % HPG] = -INFINITY;
+        const uint32_t d0 = nodes_at(draft_at, 0), d1 = nodes_at(draft_at, 1);
+        const bool drafts = d0 | d1;
+        if (tid == 0) {
+            if (drafts) list[n_blocks] = Item{0, n, {d0, d1}};
+            tiles[tile] = Tile{drafts ? (n_blocks + 1) | kDraftBit : n_blocks, nt, row0,
+                               (int(blockIdx.x) * kTreeMaxNodes + chunk * PER) | (sorted ? kSortedBit : 0)};
+        }
+        if (n_blocks == 0 && !drafts) {   // nothing is seen: the rows' results are written here
+            constexpr int CH = HPG * D / 8;
+            auto row_of = [&](int i) {   // the row of the node at the tile's place i
+                int m = 0;
+                while (place[m] != chunk * PER + i) ++m;
+                return size_t(row0 + m) * G + g;
+            };
+            for (int i = tid; i < nt * CH; i += kPlanThreads) out[row_of(i / CH) * CH + i % CH] = make_uint4(0, 0, 0, 0);
+            for (int i = tid; i < nt * HPG; i += kPlanThreads) lse[row_of(i / HPG) * HPG + i % HPG] = -INFINITY;
+        }
     }
 }
 
@@ -367,6 +427,13 @@ __device__ __forceinline__ int range_begin(int c, int n, int C) {
 }
 __device__ __forceinline__ int range_owner(int x, int n, int C) { return int(((long long)(x + 1) * C - 1) / n); }
 
+// Which 128-row halves of a tile an item's nodes are in.
+template <int HPG>
+__device__ __forceinline__ uint32_t half_bits(const Item &it) {
+    if constexpr (HPG == 4) return (it.nodes[0] ? 1u : 0u) | (it.nodes[1] ? 2u : 0u);
+    return (it.nodes[0] & 0xffffu ? 1u : 0u) | (it.nodes[0] >> 16 ? 2u : 0u);
+}
+
 // The CTA's segments in order; every role walks them for itself.
 struct Walk {
     const Tile *tiles;
@@ -374,7 +441,7 @@ struct Walk {
     int extra;               // a tile's cost beside its items
     int tile, off, end, n_items, seg;
     Tile t;
-    bool drafts;
+    bool drafts, sorted;
     __device__ __forceinline__ bool next() {   // the next segment: items off .. end-1 of `tile`, n_items in it
         if (seg >= 0) {
             x += n_items + extra;
@@ -384,7 +451,8 @@ struct Walk {
         for (;; ++tile) {
             if (x + extra >= x1) return false;   // no item of the next tile, if any, lies before the end
             const int4 v = *reinterpret_cast<const int4 *>(tiles + tile);
-            t = Tile{v.x, v.y, v.z, v.w};
+            t = Tile{v.x, v.y, v.z, v.w & ~kSortedBit};
+            sorted = v.w & kSortedBit;
             n_items = t.n_items & ~kDraftBit;
             if (n_items) break;
         }
@@ -401,12 +469,12 @@ __device__ __forceinline__ uint32_t exp_all_ones(uint32_t w) {   // 0x8000 in ea
 
 template <int D, int HPG>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
-    const uint16_t *__restrict__ q, const __grid_constant__ CUtensorMap qmap,
+    const uint16_t *__restrict__ q, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qnode,
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
     const __grid_constant__ CUtensorMap knmap, const __grid_constant__ CUtensorMap vnmap,
     const uint16_t *__restrict__ k_cache, const uint16_t *__restrict__ v_cache, const uint16_t *__restrict__ k_new,
     const uint16_t *__restrict__ v_new, int G, int cap, int n_tiles, float sm_scale,
-    const Tile *__restrict__ tiles, Cut *__restrict__ cut, int32_t *__restrict__ n_cut,
+    const uint8_t *__restrict__ order, const Tile *__restrict__ tiles, Cut *__restrict__ cut, int32_t *__restrict__ n_cut,
     const unsigned long long *__restrict__ dmask, const Item *__restrict__ items, float *__restrict__ part,
     uint16_t *__restrict__ out, float *__restrict__ lse, int32_t *err) {
     using Smem = TreeSmem<D>;
@@ -495,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
     const uint32_t tmem = sm.tmem_base;
     // a range that begins within a tile's cost has the tile from its first item on
     const int at0 = x0 < x1 ? sm.at0 : total;
-    Walk wk{tiles, at0, x1, extra, x0 < x1 ? sm.tile0 : 0, max(0, x0 - at0 - extra), 0, 0, -1, Tile{}, false};
+    Walk wk{tiles, at0, x1, extra, x0 < x1 ? sm.tile0 : 0, max(0, x0 - at0 - extra), 0, 0, -1, Tile{}, false, false};
 
     if (warp == 0) {
         // ------------------------------------------------------------ K/V producer (lane 0)
@@ -547,86 +615,140 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
         if (lane == 0) {
             auto wait = [&](uint64_t *bar, int phase) { return mbar_wait(bar, uint32_t(phase & 1), err, &sm.abort); };
             int it = 0;                       // items of this CTA so far
-            int units[2] = {0, 0};            // PV units issued per group
-            bool ok = true;
-            struct Unit {
-                int w, it, acc;
-                bool draft, first_of_item, last_of_item;
-            } pend{};
-            bool have = false, o_wait = false;
-            auto issue_pv = [&]() -> bool {
-                const int w = pend.w, slot = pend.it % NV;
-                if (o_wait) {                 // both groups have read the O of the segment before
-                    if (!wait(&sm.o_free, wk.seg - 1)) return false;
-                    o_wait = false;
-                }
-                if (pend.first_of_item && !wait(&sm.v_ok[pend.it % kOkRing], pend.it / kOkRing)) return false;
-                if (!wait(&sm.p_ready[w], units[w])) return false;
-                ++units[w];
+            uint32_t units = 0;               // parity of the PV units issued for each group (bit w)
+            bool ok = true, o_wait = false;
+            const uint64_t q_desc = make_smem_desc(smem_u32(sm.q[0]), 16, 1024, 2);
+            const uint64_t k_desc = make_smem_desc(smem_u32(sm.k[0]), 16, 1024, 2);
+            const uint64_t v_desc = make_smem_desc(smem_u32(sm.v[0]), 16384, 1024, 2);
+            constexpr uint64_t kTileStep = sizeof(sm.k[0]) / 16;   // between tiles, in the descriptors' units
+            auto issue_s = [&](int w, int m, int slot, bool draft) {
                 tc_fence_after();
-                const uint64_t vd = make_smem_desc(smem_u32(sm.v[slot]), 16384, 1024, 2);
+                mma_s<D>(tmem + uint32_t(w * 128), q_desc + m * kTileStep, k_desc + slot * kTileStep,
+                         draft ? kIdescS64 : kIdescS);
+                mma_commit(&sm.s_full[w]);
+            };
+            // O += P V of a unit of item x: both groups have read the O of the segment before, V is checked, P is there
+            auto issue_pv = [&](int w, int x, bool acc, bool draft, bool first, bool last) -> bool {
+                if (o_wait && !wait(&sm.o_free, wk.seg - 1)) return false;
+                o_wait = false;
+                if (first && !wait(&sm.v_ok[x % kOkRing], x / kOkRing)) return false;
+                if (!wait(&sm.p_ready[w], units >> w)) return false;
+                units ^= 1u << w;
+                tc_fence_after();
+                const int slot = x % NV;
+                const uint64_t vd = v_desc + slot * kTileStep;
                 const uint32_t d = tmem + uint32_t(256 + w * D), a = tmem + uint32_t(w * 128);
-                mma_pv64(d, a, vd, kIdescO, pend.acc);
-                if (!pend.draft) mma_pv64(d, a + 32, vd + 512, kIdescO, 1u);
+                mma_pv64(d, a, vd, kIdescO, acc);
+                if (!draft) mma_pv64(d, a + 32, vd + 512, kIdescO, 1u);
                 mma_commit(&sm.o_done[w]);
-                if (pend.last_of_item) mma_commit(&sm.v_empty[slot]);
-                have = false;
+                if (last) mma_commit(&sm.v_empty[slot]);
                 return true;
             };
             while (ok && wk.next()) {
-                const int nm = wk.t.nodes > NPM ? 2 : 1;
                 o_wait = wk.seg > 0;
                 if (!wait(&sm.q_full, wk.seg)) break;
-                int u = 0;                    // units of this segment
-                for (int i = wk.off; ok && i < wk.end; ++i, ++it) {
-                    const bool draft = wk.drafts && i == wk.n_items - 1;
-                    const int slot = it % NK;
-                    if (!wait(&sm.k_full[slot], it / NK)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int m = 0; m < nm; ++m, ++u) {
-                        const int w = u & 1;
-                        tc_fence_after();
-                        const uint64_t qd = make_smem_desc(smem_u32(sm.q[m]), 16, 1024, 2);
-                        const uint64_t kd = make_smem_desc(smem_u32(sm.k[slot]), 16, 1024, 2);
-                        mma_s<D>(tmem + uint32_t(w * 128), qd, kd, draft ? kIdescS64 : kIdescS);
-                        mma_commit(&sm.s_full[w]);
-                        if (m == nm - 1) mma_commit(&sm.k_empty[slot]);
-                        if (m == nm - 1 && i == wk.end - 1) mma_commit(&sm.q_empty);
-                        if (have && !issue_pv()) {
-                            ok = false;
-                            break;
+                const int len = wk.end - wk.off;
+                const bool ends = wk.drafts && wk.end == wk.n_items;   // the last item is the drafted tokens
+                if (wk.t.nodes <= NPM) {
+                    // one half: every item is a unit, of the groups in turn; S of a unit goes before P V of the one before
+                    for (int x = 0; x <= len; ++x) {
+                        if (x < len) {
+                            const int slot = (it + x) % NK;
+                            if (!(ok = wait(&sm.k_full[slot], (it + x) / NK))) break;
+                            issue_s(x & 1, 0, slot, ends && x == len - 1);
+                            mma_commit(&sm.k_empty[slot]);
+                            if (x == len - 1) mma_commit(&sm.q_empty);
                         }
-                        pend.w = w;
-                        pend.it = it;
-                        pend.acc = u >= 2;
-                        pend.draft = draft;
-                        pend.first_of_item = m == 0;
-                        pend.last_of_item = m == nm - 1;
-                        have = true;
+                        if (x > 0 && !(ok = issue_pv((x - 1) & 1, it + x - 1, x > 2, ends && x == len, true, true))) break;
+                    }
+                    it += len;
+                    continue;
+                }
+                // two halves: a unit is an item and a half of which a node selected it
+                const Item *list = items + size_t(wk.tile) * cap;
+                auto halves_of = [&](int x) { return x < len ? half_bits<HPG>(list[wk.off + x]) : 0u; };
+                uint32_t a0 = halves_of(0), a1 = halves_of(1), a2 = halves_of(2), a3 = halves_of(3);   // four items ahead
+                uint32_t begun = 0;                          // halves whose O holds something of this segment
+                int w_p = -1, x_p = 0;                       // the unit whose P V is to come, its item
+                bool first_p = false, last_p = false;
+                for (int x = 0; ok && x <= len; ++x) {       // one round more than items, for the last unit's P V
+                    const uint32_t halves = a0;
+                    a0 = a1;
+                    a1 = a2;
+                    a2 = a3;
+                    a3 = halves_of(x + 4);
+                    const int slot = (it + x) % NK;
+                    if (x < len && !(ok = wait(&sm.k_full[slot], (it + x) / NK))) break;
+#pragma unroll 1
+                    for (int m = 0; ok && m < 2; ++m) {
+                        const bool s = halves >> m & 1;
+                        if (!s && (halves || m)) continue;   // (an item of nobody and the tail come by once, for the P V)
+                        // S of one half goes before P V of the other's unit; its own P lies where its next S will
+                        const bool last = m || !(halves & 2);
+                        auto do_s = [&]() {
+                            issue_s(m, m, slot, ends && x == len - 1);
+                            if (last) mma_commit(&sm.k_empty[slot]);
+                            if (last && x == len - 1) mma_commit(&sm.q_empty);
+                        };
+                        const bool early = s && w_p != m;
+                        if (early) do_s();
+                        if (w_p >= 0) {
+                            ok = issue_pv(w_p, it + x_p, begun >> w_p & 1, ends && x_p == len - 1, first_p, last_p);
+                            if (!ok) break;
+                            begun |= 1u << w_p;
+                            w_p = -1;
+                        }
+                        if (!s) break;
+                        if (!early) do_s();
+                        first_p = !(m && (halves & 1));
+                        last_p = last;
+                        w_p = m;
+                        x_p = x;
+                    }
+                    if (!ok || x == len) break;
+                    if (!halves) {   // nobody's item (a refused page): its K is let go, and its V in turn
+                        mma_commit(&sm.k_empty[slot]);
+                        if (x == len - 1) mma_commit(&sm.q_empty);
+                        if (!(ok = wait(&sm.v_ok[(it + x) % kOkRing], (it + x) / kOkRing))) break;
+                        mma_commit(&sm.v_empty[(it + x) % NV]);
                     }
                 }
-                if (ok && have && !issue_pv()) ok = false;
+                it += len;
+                if (ok && o_wait) ok = wait(&sm.o_free, wk.seg - 1);   // a segment without units
             }
             mma_commit(&sm.drain);
             mbar_wait(&sm.drain, 0, err, nullptr);
         }
     } else if (warp < 4) {
-        // ------------------------------------------------------------ Q loads (warp 2, lane 0), finite check of V
+        // ------------------------------------------------------------ Q loads (warp 2), finite check of V
         const int th = tid - 64;
         int it = 0, loads = 0;
         bool ok = true;
         while (ok && wk.next()) {
-            if (tid == 64 && (wk.seg == 0 || mbar_wait(&sm.q_empty, (wk.seg - 1) & 1, err, &sm.abort))) {
-                const int nm = wk.t.nodes > NPM ? 2 : 1;
-                mbar_arrive_expect_tx(&sm.q_full, nm * 128 * D * 2);
-                for (int m = 0; m < nm; ++m)
+            if (warp == 2) {
+                bool free_q = true;
+                if (lane == 0 && wk.seg > 0) free_q = mbar_wait(&sm.q_empty, (wk.seg - 1) & 1, err, &sm.abort);
+                if (__shfl_sync(0xffffffffu, free_q, 0)) {
+                    const int nt = wk.t.nodes, g = wk.tile % G;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&sm.q_full, wk.sorted ? nt * (HPG * D * 2) : (nt > NPM ? 2 : 1) * (128 * D * 2));
+                    __syncwarp();
+                    if (wk.sorted) {   // (HPG = 8) a node's heads are a whole 1024-byte swizzle atom: a box for each node
+                        if (lane < nt) {
+                            const int row = wk.t.row0 + order[wk.t.ord + lane];
 #pragma unroll
-                    for (int c = 0; c < NSUB; ++c)
-                        tma_load_3d(sm.q[m] + c * 16384, &qmap, &sm.q_full, c * 64, wk.tile % G * HPG,
-                                    wk.t.row + m * NPM);
-                ++loads;
+                            for (int c = 0; c < NSUB; ++c)
+                                tma_load_3d(sm.q[lane / NPM] + c * 16384 + (lane % NPM) * (HPG * 128), &qnode, &sm.q_full,
+                                            c * 64, g * HPG, row);
+                        }
+                    } else if (lane < (nt > NPM ? 2 : 1)) {   // nodes in their own order: one box of 128 rows
+                        const int row = wk.t.row0 + wk.t.ord % kTreeMaxNodes + lane * NPM;
+#pragma unroll
+                        for (int c = 0; c < NSUB; ++c)
+                            tma_load_3d(sm.q[lane] + c * 16384, &qmap, &sm.q_full, c * 64, g * HPG, row);
+                    }
+                    ++loads;
+                }
             }
             __syncwarp();
             for (int i = wk.off; i < wk.end; ++i, ++it) {
@@ -675,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
         const uint32_t t_s = tmem + lane_off + uint32_t(w * 128);
         const uint32_t t_o = tmem + lane_off + 256u;   // + group * D
         const float scale = sm_scale * kLog2e;
-        int units[2] = {0, 0};                     // units of both groups so far
+        int units = 0;                             // units of this group so far
         bool ok = true;   // once a wait has run out the groups only keep in step, so that no barrier is missed
         while (wk.next()) {
             const int g = wk.tile % G, nt = wk.t.nodes;
@@ -685,24 +807,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             const int node = mt * NPM + row / HPG;                 // within the tile
             const bool live = node < nt;
             const bool warp_live = mt * NPM + quad * 32 / HPG < nt;
-            const unsigned long long dm = live ? dmask[size_t(wk.t.row + node) * G + g] : 0ull;
-            const int len = wk.end - wk.off;
-            const int step = nm == 2 ? 1 : 2, i0 = wk.off + (nm == 2 ? 0 : w);
+            auto row_of = [&]() { return wk.t.row0 + int(order[wk.t.ord + node]); };   // of a live row
+            auto drafts_seen = [&]() { return live ? dmask[size_t(row_of()) * G + g] : 0ull; };
             float m = -INFINITY, l = 0.f;
             int mine_n = 0;
-            Item next = i0 < wk.end ? list[i0] : Item{};
-            for (int i = i0; ok && i < wk.end; i += step, ++mine_n) {
-                const Item item = next;
-                if (i + step < wk.end) next = list[i + step];
+            // This group's items: every second one, or (nm == 2) those that a node of its rows selected, found 32 at a time.
+            uint32_t todo = 0;
+            int base = wk.off - 32;
+            auto step = [&](int i) -> int {
+                if (nm == 1) return i < 0 ? wk.off + w : i + 2;
+                while (!todo) {
+                    base += 32;
+                    if (base >= wk.end) return wk.end;
+                    const int x = base + lane;
+                    todo = __ballot_sync(0xffffffffu, x < wk.end && (half_bits<HPG>(list[min(x, wk.end - 1)]) >> mt & 1));
+                }
+                const int x = base + __ffs(todo) - 1;
+                todo &= todo - 1;
+                return x;
+            };
+            int i_next = step(-1);
+            int tok_next = 0;        // its cached tokens and the nodes that selected it, one item ahead
+            uint32_t nodes_next = 0;
+            auto fetch = [&]() {
+                if (i_next >= wk.end) return;
+                tok_next = list[i_next].n_tok;
+                nodes_next = list[i_next].nodes[HPG == 4 ? mt : 0];
+            };
+            fetch();
+            while (ok && i_next < wk.end) {
+                const int i = i_next, n_tok = tok_next;
+                const bool sees = live && (nodes_next >> (node & 31) & 1);
+                i_next = step(i);
+                fetch();
                 const bool draft = wk.drafts && i == wk.n_items - 1;
-                const bool sees = live && (item.nodes[node >> 5] >> (node & 31) & 1);
+                const unsigned long long dm = draft ? drafts_seen() : 0ull;
                 // the tokens of 32 columns from c on that this row sees
                 auto seen = [&](int c) -> uint32_t {
                     if (draft) return c < 64 ? uint32_t(dm >> c) : 0u;
-                    if (!sees || item.n_tok <= c) return 0u;
-                    return item.n_tok - c >= 32 ? ~0u : (1u << (item.n_tok - c)) - 1u;
+                    if (!sees || n_tok <= c) return 0u;
+                    return n_tok - c >= 32 ? ~0u : (1u << (n_tok - c)) - 1u;
                 };
-                const int k = units[w] + mine_n;
+                const int k = units + mine_n;
+                ++mine_n;
                 if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[w], k & 1, err, &sm.abort))) {
                     ok = false;
                     break;
@@ -717,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                         const uint32_t z[16] = {};
                         for (int c = 0; c < cols; c += 32) tmem_st16(t_s + uint32_t(c >> 1), z);
                         done = true;
-                    } else if (!draft && item.n_tok == 128) {
+                    } else if (!draft && n_tok == 128) {
                         // A whole block.  A row without a reference takes the maximum of its first 32 tokens for one;
                         // no other maximum is taken (a sum past 2^kRaise tells that a logit may be far above the
                         // reference; S is still whole then, and the loop below starts over).  P stays in
@@ -817,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                                     l += sum2(acc2[x]) * fac;
                                     acc2[x] = 0;
                                 }
-                                if (mine_n > 0) {
+                                if (mine_n > 1) {
                                     if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_done[w], (k - 1) & 1, err, &sm.abort))) {
                                         ok = false;
                                         break;
@@ -864,12 +1011,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_ready[w]);
             }
-            // units of both groups in this segment
-            const int n0 = nm == 2 ? len : (len + 1) / 2, n1 = nm == 2 ? len : len / 2;
-            units[0] += n0;
-            units[1] += n1;
+            units += mine_n;
+            const int n1 = (wk.end - wk.off) / 2;   // the second group's units (nm == 1)
             // its own O is complete; the other group's is, once the groups have met
-            ok = __all_sync(0xffffffffu, ok && (mine_n == 0 || mbar_wait(&sm.o_done[w], (units[w] - 1) & 1, err, &sm.abort)));
+            ok = __all_sync(0xffffffffu, ok && (mine_n == 0 || mbar_wait(&sm.o_done[w], (units - 1) & 1, err, &sm.abort)));
             tc_fence_before();
             // The segment's (max, sum) of the row and the weights of the two O's.
             float wa = 1.f, wb = 0.f;      // of O0 and O1 (nm == 1), or of the group's own O (nm == 2)
@@ -896,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             const int c_lo = nm == 2 ? 0 : w * (D / 2), c_hi = nm == 2 ? D : c_lo + D / 2;
             float *slot = part + size_t(2 * cta + (wk.off > 0 ? 0 : 1)) * part_floats(D);
             float2 *slot_ml = reinterpret_cast<float2 *>(slot + 256 * D);
-            const size_t orow = (size_t(wk.t.row + node) * G + g) * HPG + row % HPG;
+            const size_t orow = (size_t(live ? row_of() : wk.t.row0) * G + g) * HPG + row % HPG;
             if (nm == 1) {                         // group 0's total for group 1
                 groups_sync();                     // the weights have been read
                 if (w == 0) sm.join[row] = make_float2(m, l);
@@ -919,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                         tmem_ld32(t_o + uint32_t(w * D + c), va);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(va[e]);
+                        for (int e = 0; e < 32; ++e) o[e] = mine_n > 0 ? __uint_as_float(va[e]) : 0.f;
                     } else {
                         tmem_ld32(t_o + uint32_t(c), va);
                         tmem_ld_wait();
@@ -934,6 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                         }
                     }
                     if (fix && live) {
+                        const unsigned long long dm = wk.drafts ? drafts_seen() : 0ull;
                         // values that are not finite were taken out of V: p * v of those this row sees
                         for (int i = wk.off; i < wk.end; ++i) {
                             const Item item = list[i];
@@ -997,7 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
             if (!whole && wk.off == 0 && tid == 4 * 32)   // the ranges that hold the tile
                 for (int h = 0; h < nm; ++h)
                     cut[atomicAdd(n_cut, 1)] = Cut{cta, range_owner(wk.x + extra + wk.n_items - 1, total, C), h, g,
-                                                   wk.t.row + h * NPM, nt - h * NPM, {0, 0}};
+                                                   wk.t.row0, nt - h * NPM, wk.t.ord + h * NPM, 0};
         }
     }
 
@@ -1014,6 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
 // flight: latency bounds it.  The list of cut tiles is in no order; the results do not depend on it.
 template <int D, int HPG>
 __global__ void __launch_bounds__(256, 3) k_tree_join(const Cut *__restrict__ cut, const int32_t *__restrict__ n_cut,
+                                                      const uint8_t *__restrict__ order,
                                                       const float *__restrict__ part, int G,
                                                       uint16_t *__restrict__ out, float *__restrict__ lse) {
     constexpr int SLABS = D / 16;
@@ -1070,7 +1217,7 @@ __global__ void __launch_bounds__(256, 3) k_tree_join(const Cut *__restrict__ cu
         }
         const bool any = l > 0.f || l != l;
         const float rcp = any ? 1.f / l : 0.f;
-        const size_t orow = (size_t(c1v.x + node) * G + c0v.w) * HPG + r % HPG;
+        const size_t orow = (size_t(c1v.x + order[c1v.z + node]) * G + c0v.w) * HPG + r % HPG;
         *reinterpret_cast<uint4 *>(out + orow * D + col) =
             make_uint4(pack_bf16x2(o[0] * rcp, o[1] * rcp), pack_bf16x2(o[2] * rcp, o[3] * rcp),
                        pack_bf16x2(o[4] * rcp, o[5] * rcp), pack_bf16x2(o[6] * rcp, o[7] * rcp));
@@ -1085,13 +1232,14 @@ cudaError_t launch_t(const void *q, const void *k_cache, const void *v_cache, co
                      void *ws, int32_t *err, cudaStream_t st) {
     const Layout w = layout(n_rows, n_req, s);
     if (w.tiles * (w.cap + kTileCost) > 0x3fffffffLL) return cudaErrorNotSupported;
-    alignas(64) CUtensorMap qm, km, vm, kn, vn;
+    alignas(64) CUtensorMap qm, qn, km, vm, kn, vn;
     const char *why = nullptr;
     {
         const uint64_t dims[3] = {uint64_t(D), uint64_t(s.Hq), uint64_t(n_rows)};
         const uint64_t strides[2] = {uint64_t(D) * 2, uint64_t(s.Hq) * D * 2};
-        const uint32_t box[3] = {64u, uint32_t(HPG), uint32_t(128 / HPG)};
+        const uint32_t box[3] = {64u, uint32_t(HPG), uint32_t(128 / HPG)}, one[3] = {64u, uint32_t(HPG), 1u};
         if (!encode_tensor_map(&qm, 3, q, dims, strides, box, 128, &why)) return cudaErrorInvalidValue;
+        if (!encode_tensor_map(&qn, 3, q, dims, strides, one, 128, &why)) return cudaErrorInvalidValue;
     }
     {
         const uint64_t dims[4] = {uint64_t(D), uint64_t(s.G), 128ull, uint64_t(n_pages)};
@@ -1111,12 +1259,13 @@ cudaError_t launch_t(const void *q, const void *k_cache, const void *v_cache, co
     Tile *tiles = reinterpret_cast<Tile *>(base + w.tile);
     Cut *cut = reinterpret_cast<Cut *>(base + w.cut);
     int32_t *n_cut = reinterpret_cast<int32_t *>(base + w.n_cut);
+    uint8_t *order = base + w.order;
     auto *dmask = reinterpret_cast<unsigned long long *>(base + w.dmask);
     Item *items = reinterpret_cast<Item *>(base + w.items);
     float *part = reinterpret_cast<float *>(base + w.part);
-    cudaError_t e = launch_kernel(k_tree_plan<D, HPG>, dim3(unsigned(w.tiles)), dim3(kPlanThreads), 0, st, true, sel, bt,
+    cudaError_t e = launch_kernel(k_tree_plan<D, HPG>, dim3(unsigned(n_req) * unsigned(s.G)), dim3(kPlanThreads), 0, st, true, sel, bt,
                                   ctx, node_off, anc, n_rows, n_pages, s.G, s.topk, s.max_blocks, w.chunks, w.cap,
-                                  tiles, n_cut, dmask, items, static_cast<uint4 *>(out), lse, err);
+                                  tiles, n_cut, order, dmask, items, static_cast<uint4 *>(out), lse, err);
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(TreeSmem<D>) + 1024;
     static_assert(sizeof(TreeSmem<D>) + 1024 <= 232448, "shared memory of a CTA");
@@ -1124,14 +1273,14 @@ cudaError_t launch_t(const void *q, const void *k_cache, const void *v_cache, co
     if (e != cudaSuccess) return e;
     const int grid = std::min(sm_count(), kMaxCtas);
     e = launch_kernel(k_attn_tree<D, HPG>, dim3(unsigned(grid)), dim3(kThreads), smem, st, true,
-                      static_cast<const uint16_t *>(q), qm, km, vm, kn, vn, static_cast<const uint16_t *>(k_cache),
+                      static_cast<const uint16_t *>(q), qm, qn, km, vm, kn, vn, static_cast<const uint16_t *>(k_cache),
                       static_cast<const uint16_t *>(v_cache), static_cast<const uint16_t *>(k_new),
                       static_cast<const uint16_t *>(v_new), s.G, w.cap, int(w.tiles), s.sm_scale,
-                      static_cast<const Tile *>(tiles), cut, n_cut, static_cast<const unsigned long long *>(dmask),
+                      static_cast<const uint8_t *>(order), static_cast<const Tile *>(tiles), cut, n_cut, static_cast<const unsigned long long *>(dmask),
                       static_cast<const Item *>(items), part, static_cast<uint16_t *>(out), lse, err);
     if (e != cudaSuccess) return e;
     return launch_kernel(k_tree_join<D, HPG>, dim3(unsigned(4 * grid)), dim3(256), 0, st, true, static_cast<const Cut *>(cut),
-                         static_cast<const int32_t *>(n_cut),
+                         static_cast<const int32_t *>(n_cut), static_cast<const uint8_t *>(order),
                          static_cast<const float *>(part), s.G, static_cast<uint16_t *>(out), lse);
 }
 
