@@ -111,21 +111,29 @@ inline Layout layout(int n_rows, int n_req, const Shape &s) {
 constexpr int kPlanThreads = 256;
 constexpr int kMaxWords = 16384 / 32;   // bitmap over blocks
 
+// Which 128-row halves of a tile an item's nodes are in.
+template <int HPG>
+__device__ __forceinline__ uint32_t half_bits(const Item &it) {
+    if constexpr (HPG == 4) return (it.nodes[0] ? 1u : 0u) | (it.nodes[1] ? 2u : 0u);
+    return (it.nodes[0] & 0xffffu ? 1u : 0u) | (it.nodes[0] >> 16 ? 2u : 0u);
+}
+
 // Exclusive prefix of v over the CTA's threads; *total gets the sum.
-__device__ __forceinline__ int plan_scan(int v, int *wsum, int *total) {
+template <class T>
+__device__ __forceinline__ T plan_scan(T v, T *wsum, T *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = v;
+    T incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        const T y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    int before = incl - v, sum = 0;
+    T before = incl - v, sum = 0;
 #pragma unroll
     for (int w = 0; w < kPlanThreads / 32; ++w) {
-        const int x = wsum[w];
+        const T x = wsum[w];
         if (w < warp) before += x;
         sum += x;
     }
@@ -153,7 +161,8 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_tree_plan(
     __shared__ uint32_t key[kTreeMaxNodes];
     __shared__ uint8_t place[kTreeMaxNodes];
     __shared__ uint32_t draft_at[2];                   // places whose nodes see drafted tokens
-    __shared__ int wsum[2][kPlanThreads / 32];
+    __shared__ int wsum[kPlanThreads / 32];
+    __shared__ unsigned long long wsum3[2][kPlanThreads / 32];
     const int tid = threadIdx.x;
     const int b = blockIdx.x / G, g = blockIdx.x - b * G;
     pdl_wait();
@@ -208,7 +217,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_tree_plan(
     const int w0 = 2 * tid, w1 = w0 + 1;
     const int p0 = w0 < words ? __popc(bits[w0]) : 0, p1 = w1 < words ? __popc(bits[w1]) : 0;
     int total;
-    const int before = plan_scan(p0 + p1, wsum[0], &total);
+    const int before = plan_scan(p0 + p1, wsum, &total);
     if (w0 < words) rank[w0] = before;
     if (w1 < words) rank[w1] = before + p0;
     if (tid < n) place[tid] = uint8_t(tid);
@@ -267,17 +276,32 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_tree_plan(
             continue;
         }
         auto nodes_at = [&](const uint32_t (&w)[2], int h) { return PER == 64 ? w[h] : h ? 0u : w[chunk & 1]; };
-        // the union's blocks that a node of this tile selected: a run of them per thread, counted, then written
+        // The union's blocks that a node of this tile selected, in three classes: of the first 128 rows alone, of the
+        // second alone, of both.  A run of blocks per thread is counted, then written.
         const int k0 = tid * total / kPlanThreads, k1 = (tid + 1) * total / kPlanThreads;
-        int mine = 0, n_blocks;
-        for (int k = k0; k < k1; ++k) mine += (nodes_at(nodes_of[k], 0) | nodes_at(nodes_of[k], 1)) != 0;
-        int at = plan_scan(mine, wsum[(chunk + 1) & 1], &n_blocks);
+        auto item_of = [&](int k) { return Item{0, 0, {nodes_at(nodes_of[k], 0), nodes_at(nodes_of[k], 1)}}; };
+        unsigned long long mine = 0, sums;   // 21 bits per class
+        for (int k = k0; k < k1; ++k) {
+            const uint32_t h = half_bits<HPG>(item_of(k));
+            if (h) mine += 1ull << (21 * (h - 1));
+        }
+        unsigned long long before = plan_scan(mine, wsum3[chunk & 1], &sums);
+        const int cnt[3] = {int(sums & 0x1fffff), int(sums >> 21 & 0x1fffff), int(sums >> 42)};
+        const int n_blocks = cnt[0] + cnt[1] + cnt[2];
         Item *list = items + size_t(tile) * cap;
         for (int k = k0; k < k1; ++k) {
-            Item it;
-            it.nodes[0] = nodes_at(nodes_of[k], 0);
-            it.nodes[1] = nodes_at(nodes_of[k], 1);
-            if (!(it.nodes[0] | it.nodes[1])) continue;
+            Item it = item_of(k);
+            const uint32_t h = half_bits<HPG>(it);
+            if (!h) continue;
+            // The classes are merged evenly, each in ascending order, so that the halves take turns and a CTA's range
+            // has its share of each: item r of class q goes by (2 r + 1) / (2 cnt[q]), ties by class.
+            const int q = int(h) - 1, r = int(before >> (21 * q) & 0x1fffff);
+            before += 1ull << (21 * q);
+            const int cnt_q = q == 0 ? cnt[0] : q == 1 ? cnt[1] : cnt[2];
+            int at = r;
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                if (p != q && cnt[p]) at += (((2 * r + 1) * cnt[p] - (p < q ? 0 : 1)) / cnt_q + 1) >> 1;
             const int j = block_of[k];
             it.page = block_table[size_t(b) * max_blocks + j];
             it.n_tok = min(128, ctx - j * 128);
@@ -286,7 +310,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_tree_plan(
                 it.page = 0;
                 it.nodes[0] = it.nodes[1] = 0;
             }
-            list[at++] = it;
+            list[at] = it;
         }
         const uint32_t d0 = nodes_at(draft_at, 0), d1 = nodes_at(draft_at, 1);
         const bool drafts = d0 | d1;
@@ -427,13 +451,6 @@ __device__ __forceinline__ int range_begin(int c, int n, int C) {
 }
 __device__ __forceinline__ int range_owner(int x, int n, int C) { return int(((long long)(x + 1) * C - 1) / n); }
 
-// Which 128-row halves of a tile an item's nodes are in.
-template <int HPG>
-__device__ __forceinline__ uint32_t half_bits(const Item &it) {
-    if constexpr (HPG == 4) return (it.nodes[0] ? 1u : 0u) | (it.nodes[1] ? 2u : 0u);
-    return (it.nodes[0] & 0xffffu ? 1u : 0u) | (it.nodes[0] >> 16 ? 2u : 0u);
-}
-
 // The CTA's segments in order; every role walks them for itself.
 struct Walk {
     const Tile *tiles;
@@ -570,6 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
         if (lane == 0) {
             int it = 0, v_loads = 0;
             bool ok = true;
+            // Pages leave L2 first (16 nodes: 48 us, 52 without; 64 nodes, whose two tiles read most pages at about the
+            // same time: 146 us and 148).
+            const uint64_t policy = l2_policy_evict_first();
             while (ok && wk.next()) {
                 const int g = wk.tile % G;
                 const Item *list = items + size_t(wk.tile) * cap;
@@ -588,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
 #pragma unroll
                     for (int c = 0; c < NSUB; ++c) {
                         if (draft) tma_load_3d(sm.k[ks] + c * 16384, &knmap, &sm.k_full[ks], c * 64, g, wk.t.row0);
-                        else tma_load_4d(sm.k[ks] + c * 16384, &kmap, &sm.k_full[ks], c * 64, g, 0, page_i);
+                        else tma_load_4d_hint(sm.k[ks] + c * 16384, &kmap, &sm.k_full[ks], c * 64, g, 0, page_i, policy);
                     }
                     if (it >= NV && !mbar_wait(&sm.v_empty[vs], (it / NV - 1) & 1, err, &sm.abort)) {
                         ok = false;
@@ -599,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
 #pragma unroll
                     for (int c = 0; c < NSUB; ++c) {
                         if (draft) tma_load_3d(sm.v[vs] + c * 16384, &vnmap, &sm.v_full[vs], c * 64, g, wk.t.row0);
-                        else tma_load_4d(sm.v[vs] + c * 16384, &vmap, &sm.v_full[vs], c * 64, g, 0, page_i);
+                        else tma_load_4d_hint(sm.v[vs] + c * 16384, &vmap, &sm.v_full[vs], c * 64, g, 0, page_i, policy);
                     }
                     v_loads = it + 1;
                 }

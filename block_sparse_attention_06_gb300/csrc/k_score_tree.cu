@@ -51,17 +51,6 @@ struct Ctl {
 
 __device__ __forceinline__ long long range_begin(int c, long long n, int C) { return c * n / C; }
 
-// tma_load_4d with an L2 policy.  The pages are read once, and evicted first they leave the block scores, whose
-// 32-byte sectors fill up over eight blocks, in L2 until they are whole (64 nodes: 98 us without).
-__device__ __forceinline__ void tma_load_4d_hint(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t c0,
-                                                 int32_t c1, int32_t c2, int32_t c3, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
-
 // A request as the scan sees it.
 struct Req {
     int row0, n, ctx, nb;   // nb: blocks that hold cached or drafted tokens
@@ -214,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_tree(
             Walk<kSets> wk{node_off, ctx_lens, n_rows, max_blocks, G, x1 - x0};
             wk.start(b0, v0);
             int at = 0, loads = 0, b_of = -1, j_of = -1, page = 0, j_ahead = 0, ahead = 0;
+            // The pages are read once, and evicted first they leave the block scores, whose 32-byte sectors fill up
+            // over eight blocks, in L2 until they are whole (64 nodes: 98 us without).
             const uint64_t policy = l2_policy_evict_first();
             uint32_t phase = 1;   // of the slot's last reader, from the second round on
             auto page_of = [&](int j) -> int {
