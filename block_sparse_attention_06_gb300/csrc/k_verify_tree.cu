@@ -91,11 +91,12 @@ struct Residual {
     double c;
     float chi, clo;   // c
     bool draft;
-    // whether p - c q > 0 (NaN: no)
+    // whether p - c q > 0 (NaN: no), for q >= 0: entries of q below 0 and NaN count as 0 (fmaxf)
     __device__ __forceinline__ bool positive(float p, float q) const {
         return draft ? fmaf(-clo, q, fmaf(-chi, q, p)) > 0.f : p > 0.f;
     }
     __device__ __forceinline__ double value(float p, float q) const {
+        q = fmaxf(q, 0.f);
         if (!positive(p, q)) return 0.0;
         const double r = draft ? double(p) - c * double(q) : double(p);
         return r > 0.0 ? r : 0.0;
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
             sm.tok[tid] = tok;
             sm.u[tid] = u_accept[row0 + tid];
             sm.p[tid] = probs[size_t(row0 + par) * vocab + tok];
-            if (drafts) sm.q[tid] = drafts[size_t(row0 + par) * vocab + tok];
+            if (drafts) sm.q[tid] = fmaxf(drafts[size_t(row0 + par) * vocab + tok], 0.f);
             atomicOr(&sm.kids[par], 1ull << tid);
         }
         if (rank == 0) path[row0 + tid] = -1;
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
             for (int x = 0; x < U * VEC; x += 2) {
                 const float p0 = cp[x / VEC].v[x % VEC], p1 = cp[(x + 1) / VEC].v[(x + 1) % VEC];
                 if (res.draft) {
-                    const float q0 = cq[x / VEC].v[x % VEC], q1 = cq[(x + 1) / VEC].v[(x + 1) % VEC];
+                    const float q0 = fmaxf(cq[x / VEC].v[x % VEC], 0.f), q1 = fmaxf(cq[(x + 1) / VEC].v[(x + 1) % VEC], 0.f);
                     const uint64_t q2 = pack2(q0, q1);
                     const float2 r = unpack2(fma2(nclo2, q2, fma2(nchi2, q2, pack2(p0, p1))));
                     add_split(ah2, al2, pack2(r.x > 0.f ? p0 : 0.f, r.y > 0.f ? p1 : 0.f));

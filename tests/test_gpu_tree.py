@@ -637,3 +637,24 @@ def test_two_steps_at_once(msa):
         for (a, b), (c, d), r in zip(got, want, runs):
             assert torch.equal(a, c) and torch.equal(b, d)
             msa.msa_check(r[7])
+
+
+# ------------------------------------------------------------------ calls at the edges of what is documented
+
+def test_verify_counts_bad_draft_entries_as_zero(msa):
+    """Draft entries that are negative or not a number, anywhere in a row and at the drafted tokens."""
+    t = T.make_tree([0] * 8, [5] * 8, 55, "star")
+    V = 1003
+    p, q, tok, ua, un = T.verify_inputs(t, V, 74, True)
+    q[::2, 3::7] = float("nan")
+    q[1::2, 2::5] = -0.25
+    q[:, 11] = -float("inf")
+    for b in range(8):
+        q[t.off[b], tok[t.off[b] + 1].long()] = float("nan") if b % 2 else -1.0
+    off, par, _, _, _ = t.dev(DEV)
+    err = msa.new_err_word(DEV)
+    got = msa.msa_verify_tree(p.to(DEV), q.to(DEV), tok.to(DEV), off, par, ua.to(DEV), un.to(DEV), err_word=err)
+    msa.msa_check(err)
+    want = T.ref_verify(t, p, torch.nan_to_num(q, nan=0.0, neginf=0.0).clamp(min=0), tok, ua, un)
+    for g, w in zip(got, want):
+        assert torch.equal(g.cpu(), w), (g.tolist(), w.tolist())
