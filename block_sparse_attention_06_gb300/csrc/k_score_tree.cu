@@ -460,7 +460,6 @@ cudaError_t launch_di(const void *q_idx, const void *kidx, const void *kidx_new,
         const uint32_t box[4] = {uint32_t(DI), 1u, 128u, 1u};
         if (!encode_tensor_map(&km, 4, kidx, dims, strides, box, DI * 2, &why)) return cudaErrorInvalidValue;
     }
-    if (1.0 * n_req * s.max_blocks * s.G > 2147483647.0) return cudaErrorNotSupported;
     const size_t q_bytes = size_t(s.G + 1) * 64 * DI * 2, tile = 128 * DI * 2;
     const size_t stages = size_t(2 * kSets) * kStage * sizeof(float);
     const int depth = int(std::min<size_t>(kMaxDepth, (kSmemLimit - 1024 - q_bytes - stages) / (kSets * tile)));

@@ -509,6 +509,8 @@ msa_status_t msa_tree_index_score(const void *q_idx, const void *kidx_cache, con
     if (n_req > kTreeMaxRequests)
         return fail(MSA_ERR_UNSUPPORTED, "msa_tree_index_score: n_req > %d", kTreeMaxRequests);
     if (s.max_blocks > 65535) return fail(MSA_ERR_UNSUPPORTED, "msa_tree_index_score: max_blocks > 65535");
+    if (1.0 * n_req * s.max_blocks * s.G > 2147483647.0)
+        return fail(MSA_ERR_UNSUPPORTED, "msa_tree_index_score: n_req * max_blocks * G >= 2^31");
     if (misaligned16({q_idx, kidx_cache, kidx_new}))
         return fail(MSA_ERR_INVALID_ARG, "msa_tree_index_score: q_idx and the index keys must be 16-byte aligned");
     cudaError_t e = launch_score_tree(q_idx, kidx_cache, kidx_new, block_table, ctx_lens, node_off, anc, n_rows, n_req,
@@ -554,6 +556,7 @@ msa_status_t msa_verify_tree(const float *target_probs, const float *draft_probs
     MSA_REQUIRE(n_rows == 0 || (target_probs && tokens && parents && u_accept && u_next && path),
                 "msa_verify_tree: NULL pointer");
     if (n_req > kTreeMaxRequests) return fail(MSA_ERR_UNSUPPORTED, "msa_verify_tree: n_req > %d", kTreeMaxRequests);
+    if (vocab > (1 << 30)) return fail(MSA_ERR_UNSUPPORTED, "msa_verify_tree: vocab > 2^30");
     cudaError_t e = launch_verify_tree(target_probs, draft_probs, vocab, tokens, node_off, parents, u_accept, u_next,
                                        n_rows, n_req, path, n_accepted, next_token, err_word,
                                        static_cast<cudaStream_t>(stream));

@@ -463,8 +463,9 @@ msa_status_t msa_tree_rows(const int32_t *node_off, const int32_t *parents, cons
  *   anc        uint64 [n_rows]        from msa_tree_rows
  *   scores     fp32 [n_rows][G][max_blocks]  out; -inf for blocks past the row's own;
  *              padding rows are not written
- * Each request's k-index is read once for every 16 of its nodes.  A page id outside
- * [0, n_pages) raises MSA_FLAG_BOUNDS.  max_blocks <= 65535.
+ * Each request's k-index is read once for all of its nodes.  A page id outside
+ * [0, n_pages) raises MSA_FLAG_BOUNDS.  Limits: max_blocks <= 65535, n_req *
+ * max_blocks * G < 2^31; q_idx and the index keys 16-byte aligned.
  */
 msa_status_t msa_tree_index_score(const void *q_idx, const void *kidx_cache, const void *kidx_new,
                                   const int32_t *block_table, const int32_t *ctx_lens, const int32_t *node_off,
@@ -477,8 +478,9 @@ msa_status_t msa_tree_index_score(const void *q_idx, const void *kidx_cache, con
  * sel[r][g], and of its ancestors and itself those whose block is in sel[r][g].
  *   q          bf16 [n_rows][Hq][D];  k_cache, v_cache bf16 [n_pages][128][G][D]
  *   k_new, v_new  bf16 [n_rows][G][D] the drafted tokens' K and V
- *   sel        int32 [n_rows][G][topk] distinct block ids, -1 padding (msa_topk_blocks
- *              with the q_pos of msa_tree_rows, or any other choice)
+ *   sel        int32 [n_rows][G][topk] block ids in any order, -1 padding (msa_topk_blocks
+ *              with the q_pos of msa_tree_rows, or any other choice); a set: a block
+ *              named twice counts once
  *   out        bf16 [n_rows][Hq][D]  out;  lse fp32 [n_rows][Hq]  out.  A row that sees
  *              no token gets 0 and -inf.  Padding rows are not written.
  *   workspace  device scratch of msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims)
@@ -518,7 +520,8 @@ msa_status_t msa_sparse_attn_tree(const void *q, const void *k_cache, const void
  *             first, from row node_off[b] on; -1 behind them; padding rows are not written
  *   n_accepted int32 [n_req]  out: nodes accepted, the root among them (0 without nodes)
  *   next_token int32 [n_req]  out; -1 for a request without nodes
- * Sums and comparisons are carried at 48 bits or more.  A token outside [0, vocab) or a bad
+ * Sums are carried to more than 40 bits of the whole mass of a row (its entries
+ * are taken to sum to less than 4), comparisons in 64 bits.  vocab <= 2^30.  A token outside [0, vocab) or a bad
  * parent raises MSA_FLAG_BOUNDS (that node is never accepted); a row of target_probs
  * without finite positive mass raises MSA_FLAG_NAN (next_token -1).
  */

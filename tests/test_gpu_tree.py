@@ -658,3 +658,117 @@ def test_verify_counts_bad_draft_entries_as_zero(msa):
     want = T.ref_verify(t, p, torch.nan_to_num(q, nan=0.0, neginf=0.0).clamp(min=0), tok, ua, un)
     for g, w in zip(got, want):
         assert torch.equal(g.cpu(), w), (g.tolist(), w.tolist())
+
+
+@pytest.mark.parametrize("Hq,G,D", [(16, 2, 128), (8, 2, 64), (128, 16, 128)])
+def test_tree_attention_refused_page_of_wide_trees(msa, Hq, G, D):
+    """A bad page is reported and the rows that did not select its block are as without it, also where the page
+    leaves a tile's item without any node."""
+    t = T.make_tree([900, 1700], [60, 23], 28)
+    x = _attn_inputs(t, Hq, G, D, 38)
+    sel = T.random_sel(t, G, 5, 45, drop_own=0.2, empty=0.05)
+    off, _, ctxd, bt, anc = t.dev(DEV)
+    bt[0, 3], bt[1, 0] = -5, t.n_pages
+    err = msa.new_err_word(DEV)
+    out, lse = msa.msa_sparse_attn_tree(*[v.to(DEV) for v in x], bt, ctxd, off, anc, sel.to(DEV),
+                                        _dims(msa, t, Hq, G, D, 64, 5), err_word=err)
+    with pytest.raises(msa.MsaError, match="BOUNDS"):
+        msa.msa_check(err)
+    ro, rl, bo, bl = T.ref_attend(t, *x, sel, D ** -0.5)
+    bad = torch.where(torch.arange(t.n_rows) < t.off[1], 3, 0)[:, None, None]
+    keep = (~(sel == bad).any(-1)).repeat_interleave(Hq // G, 1)          # [n_rows][Hq]
+    assert 0.2 < float(keep.float().mean()) < 0.98
+    T.assert_within(lse[keep.to(DEV)], rl[keep], bl[keep], "lse")
+    T.assert_within(out[keep.to(DEV)], ro[keep], bo[keep], "out")
+
+
+def test_tree_attention_block_named_twice(msa):
+    """The selection is a set."""
+    t = T.make_tree([700], [20], 29)
+    x = _attn_inputs(t, 16, 2, 128, 39)
+    sel = T.random_sel(t, 2, 3, 46)
+    dims = _dims(msa, t, topk=6)
+    once = torch.cat([sel, torch.full_like(sel, -1)], -1)
+    a = _attend(msa, t, dims, *x, once)
+    b = _attend(msa, t, dims, *x, torch.cat([sel, sel.flip(-1)], -1))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("Hq,G,D,Di", [(128, 16, 128, 64), (4, 1, 64, 32)])
+def test_largest_tree_at_the_longest_context(msa, Hq, G, D, Di):
+    """64 nodes with 32 blocks each that end at the last position of the largest table of the attention; the pages
+    repeat, so the cache is small."""
+    MB, n_pages = 16384, 96
+    ctx = MB * 128 - 64
+    t = T.make_tree([ctx % 8192 + 64], [64], 30, "chain")     # for its parents alone
+    g = torch.Generator().manual_seed(40)
+    bt = torch.randint(n_pages, (1, MB), generator=g, dtype=torch.int32)
+    off, par = torch.tensor([0, 64], dtype=torch.int32, device=DEV), torch.tensor(t.parents, dtype=torch.int32, device=DEV)
+    ctxd = torch.tensor([ctx], dtype=torch.int32, device=DEV)
+    dims = msa.Dims(Hq, G, D, Di, 32, MB)
+    step = msa.TreeStep(dims, 64, 1, DEV)
+    step.layout(off, par, ctxd)
+    assert int(step.q_pos[-1]) == MB * 128 - 1
+    q, qi = T.bf16((64, Hq, D), 47), T.bf16((64, G, Di), 48)
+    kc, vc, ic = T.bf16((n_pages, 128, G, D), 49), T.bf16((n_pages, 128, G, D), 50), T.bf16((n_pages, 128, G, Di), 51)
+    kn, vn, ixn = T.bf16((64, G, D), 52), T.bf16((64, G, D), 53), T.bf16((64, G, Di), 54)
+    dev = [v.to(DEV) for v in (q, qi, kn, vn, ixn, kc, vc, ic, bt)]
+    out, lse = step.attend(*dev)
+    msa.msa_check(step.err)
+    # scores of the repeated pages: one product per page
+    dots = torch.einsum("rgd,ptgd->rgpt", qi.double(), ic.double())
+    per_page = dots.amax(-1)
+    want = per_page[..., bt[0].long()]
+    tail = ctx % 128                                          # cached tokens of the last block
+    drafted = torch.einsum("rgd,mgd->rgm", qi.double(), ixn.double())
+    drafted.masked_fill_(~torch.ones(64, 64).tril().bool()[:, None], -torch.inf)
+    want[..., -1] = torch.maximum(dots[:, :, bt[0, -1].long(), :tail].amax(-1), drafted.amax(-1))
+    # |dot - its fp32 sum| <= Di ulps of the sum of the products' sizes
+    size = torch.einsum("rgd,ptgd->rgpt", qi.double().abs(), ic.double().abs()).amax() + \
+        torch.einsum("rgd,mgd->rgm", qi.double().abs(), ixn.double().abs()).amax()
+    assert bool(((step.scores.cpu().double() - want).abs() <= Di * 2.0 ** -23 * float(size)).all())
+    sel = step.sel.cpu()
+    assert bool((sel[..., 0] >= 0).all()) and int(sel.max()) == MB - 1
+    # the attention of three rows, by the selection that was made
+    for r in (0, 31, 63):
+        for h in range(0, Hq, Hq // G):
+            grp = h // (Hq // G)
+            ks, vs = [], []
+            for j in sel[r, grp].tolist():
+                if j < 0:
+                    continue
+                lim = tail if j == MB - 1 else 128
+                ks.append(kc[bt[0, j], :lim, grp])
+                vs.append(vc[bt[0, j], :lim, grp])
+                if j == MB - 1:
+                    ks.append(kn[:r + 1, grp])
+                    vs.append(vn[:r + 1, grp])
+            k, v = torch.cat(ks).double(), torch.cat(vs).double()
+            s = (k @ q[r, h].double()) * D ** -0.5
+            w = torch.softmax(s, 0)
+            # P and the output rounded to bf16 (half a step each), and the logits' fp32 sums
+            slack = D * 2.0 ** -23 * float((k.abs() @ q[r, h].double().abs()).max()) * D ** -0.5 + 1e-5
+            bound = (2.0 ** -8 + 2 * slack) * (w @ v.abs()) * (1 + 2.0 ** -8) + 2.0 ** -8 * (w @ v).abs()
+            assert bool(((out[r, h].cpu().double() - w @ v).abs() <= bound).all()), (r, h)
+            assert abs(float(lse[r, h]) - float(s.logsumexp(0))) <= slack + 2.0 ** -22 * abs(float(s.logsumexp(0)))
+
+
+def test_step_with_padding_and_old_scores(msa):
+    """Scores that an earlier use of the buffers left, NaN among them, do not reach a padded step."""
+    t = T.make_tree([500, 90], [9, 4], 31)
+    pad = 7
+    off, par, ctxd, bt, _ = t.dev(DEV, pad)
+    dims = _dims(msa, t)
+    x = _attn_inputs(t, 16, 2, 128, 41, pad)
+    qi, ic, ixn = T.bf16((t.n_rows + pad, 2, 64), 42), T.bf16((t.n_pages, 128, 2, 64), 43), T.bf16((t.n_rows + pad, 2, 64), 44)
+    got = []
+    for fill in (0.0, float("nan")):
+        step = msa.TreeStep(dims, t.n_rows + pad, 2, DEV)
+        step.scores.fill_(fill)
+        step.layout(off, par, ctxd)
+        q, kc, vc, kn, vn = [v.to(DEV) for v in x]
+        out, lse = step.attend(q, qi.to(DEV), kn, vn, ixn.to(DEV), kc, vc, ic.to(DEV), bt)
+        msa.msa_check(step.err)
+        got.append((out.clone(), lse.clone()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert bool((got[0][0][t.n_rows:] == 0).all())

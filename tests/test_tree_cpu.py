@@ -53,6 +53,13 @@ def test_unsupported_shapes(lib):  # noqa: F811
     assert _verify(lib, n_req=65536) == 2
 
 
+def test_refuses_sizes_past_32_bits(lib):  # noqa: F811
+    """Index arithmetic that would leave 32 bits is refused before anything is launched."""
+    assert _verify(lib, vocab=(1 << 30) + 1) == 2
+    assert _score(lib, good_dims(Hq=128, G=16, max_blocks=65535), n_rows=4000, n_req=4000) == 2
+    assert _attn(lib, good_dims(Hq=128, G=16, topk=32, max_blocks=16384), n_rows=65535, n_req=65535) == 2
+
+
 def test_bad_sizes_and_pointers(lib):  # noqa: F811
     d = good_dims()
     for call in (_rows, _score, _attn, _commit):
