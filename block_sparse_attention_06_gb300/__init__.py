@@ -567,7 +567,7 @@ def _n_req(node_off) -> int:
 
 def _launch(index: int, name: str, *args):
     """_call on the current stream of device `index`, with that device current."""
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
@@ -583,9 +583,9 @@ def msa_tree_rows(node_off, parents, ctx_lens, dims: Dims, q_req=None, q_pos=Non
     dev = _lead(parents, "parents")
     n_req = _n_req(node_off)
     rows = _ndim(parents, 1, "parents", "[n_rows]")
-    q_req = parents.new_empty(rows) if q_req is None else q_req
-    q_pos = parents.new_empty(rows) if q_pos is None else q_pos
-    anc = parents.new_empty(rows, dtype=_I64) if anc is None else anc
+    q_req = torch.empty_like(parents) if q_req is None else q_req
+    q_pos = torch.empty_like(parents) if q_pos is None else q_pos
+    anc = torch.empty_like(parents, dtype=_I64) if anc is None else anc
     err_word = new_err_word(parents.device) if err_word is None else err_word
     _launch(dev, "msa_tree_rows", _arg(node_off, _I32, (n_req + 1,), dev, "node_off"),
             _arg(parents, _I32, rows, dev, "parents"), _arg(ctx_lens, _I32, (n_req,), dev, "ctx_lens"), rows[0], n_req,
@@ -603,7 +603,7 @@ def msa_tree_index_score(q_idx, kidx_cache, kidx_new, block_table, ctx_lens, nod
     n_pages = _ndim(kidx_cache, 4, "kidx_cache", "[n_pages][128][G][Di]")[0]
     index = (n_rows, dims.G, dims.Di)
     if scores is None:
-        scores = q_idx.new_empty((n_rows, dims.G, dims.max_blocks), dtype=_F32)
+        scores = torch.empty((n_rows, dims.G, dims.max_blocks), dtype=_F32, device=q_idx.device)
     err_word = new_err_word(q_idx.device) if err_word is None else err_word
     _launch(dev, "msa_tree_index_score", _arg(q_idx, _BF16, index, dev, "q_idx"),
             _arg(kidx_cache, _BF16, (n_pages, dims.page_size, dims.G, dims.Di), dev, "kidx_cache"),
@@ -625,10 +625,10 @@ def msa_sparse_attn_tree(q, k_cache, v_cache, k_new, v_new, block_table, ctx_len
     n_pages = _ndim(k_cache, 4, "k_cache", "[n_pages][128][G][D]")[0]
     heads, cache = (n_rows, dims.Hq, dims.D), (n_pages, dims.page_size, dims.G, dims.D)
     rows = (n_rows, dims.G, dims.D)
-    out = q.new_empty(heads) if out is None else out
-    lse = q.new_empty(heads[:2], dtype=_F32) if lse is None else lse
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty(heads[:2], dtype=_F32, device=q.device) if lse is None else lse
     if workspace is None:
-        workspace = q.new_empty((max(msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims), 1),), dtype=_U8)
+        workspace = torch.empty(max(msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims), 1), dtype=_U8, device=q.device)
     err_word = new_err_word(q.device) if err_word is None else err_word
     ws_bytes = _ndim(workspace, 1, "workspace", "a uint8 vector")
     _launch(dev, "msa_sparse_attn_tree", _arg(q, _BF16, heads, dev, "q"), _arg(k_cache, _BF16, cache, dev, "k_cache"),
@@ -651,9 +651,10 @@ def msa_verify_tree(target_probs, draft_probs, tokens, node_off, parents, u_acce
     n_rows, vocab = probs
     if vocab < 1:
         raise ValueError("target_probs must be [n_rows][vocab]")
-    path = target_probs.new_empty((n_rows,), dtype=_I32) if path is None else path
-    n_accepted = target_probs.new_empty((n_req,), dtype=_I32) if n_accepted is None else n_accepted
-    next_token = target_probs.new_empty((n_req,), dtype=_I32) if next_token is None else next_token
+    new = dict(dtype=_I32, device=target_probs.device)
+    path = torch.empty(n_rows, **new) if path is None else path
+    n_accepted = torch.empty(n_req, **new) if n_accepted is None else n_accepted
+    next_token = torch.empty(n_req, **new) if next_token is None else next_token
     err_word = new_err_word(target_probs.device) if err_word is None else err_word
     _launch(dev, "msa_verify_tree", _arg(target_probs, _F32, probs, dev, "target_probs"),
             None if draft_probs is None else _arg(draft_probs, _F32, probs, dev, "draft_probs"), vocab,
@@ -682,7 +683,7 @@ def msa_commit_tree(k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache, block_
     L, n_rows = _ndim(k_new, 4, "k_new", "[n_layers][n_rows][G][D]")[:2]
     n_pages = _ndim(k_cache, 5, "k_cache", "[n_layers][n_pages][128][G][D]")[1]
     rows, cache = (L, n_rows, dims.G, dims.D), (L, n_pages, dims.page_size, dims.G, dims.D)
-    new_lens = k_new.new_empty((n_req,), dtype=_I32) if new_lens is None else new_lens
+    new_lens = torch.empty(n_req, dtype=_I32, device=k_new.device) if new_lens is None else new_lens
     err_word = new_err_word(k_new.device) if err_word is None else err_word
     _launch(dev, "msa_commit_tree", _arg(k_new, _BF16, rows, dev, "k_new"), _arg(v_new, _BF16, rows, dev, "v_new"),
             _arg(kidx_new, _BF16, (L, n_rows, dims.G, dims.Di), dev, "kidx_new"), L,
