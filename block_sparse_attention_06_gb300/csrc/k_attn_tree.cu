@@ -1,29 +1,33 @@
 // Sparse attention of drafted trees over the paged cache, on the 5th-generation tensor cores.
 //
-// Row (node i, head h) of group g attends, with one softmax, the cached tokens of the blocks that node i
-// selected and those of its ancestors (and itself) whose block it selected:
+// Row (node i, head h) of group g attends, with one softmax, the cached tokens of the blocks that node i selected
+// and those of its ancestors (and itself) whose block it selected:
 //   o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),  s_t = sm_scale * q . k_t,  m = max_t s_t.
 //
-// The nodes of a tree agree on many blocks, so the work goes by the union of their selections: each
-// (request, group, up to 256 / HPG nodes) is a tile, its items are the selected blocks (each with the word of
-// the nodes that selected it) and one item for the drafted tokens, and each item's K and V are read once
-// for all nodes of the tile.  That read bounds the kernel as long as several nodes share a block.
+// The nodes of a tree agree on many blocks, so the work goes by the union of their selections: each (request,
+// group, up to 256 / HPG nodes) is a tile, its items are the selected blocks (each with the word of the nodes that
+// selected it) and one item for the drafted tokens, and each item's K and V are read once for all nodes of the
+// tile.  With up to 128 rows in a tile that read bounds the loop (8 x 60,000 tokens of 16 nodes: 174 MB in 26 us,
+// 6.6 TB/s; 47 us with the plan, the first loads, the last output and the join).  With two halves of 128 rows it
+// is the chain S, softmax, P V of each half, 1.7 us for a unit, that bounds it (64 nodes: 499 MB, 138 us in all;
+// the same time with every page in L2).
 //
 // k_tree_plan, one CTA per (request, group): the union through a bitmap over blocks in shared memory, ranked by
-// popcounts, hence in ascending block order and the same whatever order its threads run in.  With HPG = 8 and more
-// than 16 nodes, nodes of like selections become neighbours: they are ordered by the least hash of their blocks that
-// not most nodes have, which is the same for two nodes the more likely the more of their blocks they share.  Tiles
-// then have smaller unions, and the 128-row halves of a tile skip the items that none of their nodes selected
-// (8 x 60,000 tokens, 64 nodes that share windows of 7 blocks by fives: 233 us in the trees' own order).
+// popcounts, hence the same whatever order its threads run in.  With HPG = 8 and more than 16 nodes, nodes of like
+// selections become neighbours: they are ordered by the least hash of their blocks that not most nodes have, which
+// is the same for two nodes the more likely the more of their blocks they share.  Tiles then have smaller unions,
+// and the 128-row halves of a tile skip the items that none of their nodes selected (8 x 60,000 tokens, 64 nodes
+// that share windows of 7 blocks by fives: 147 us, and 233 in the trees' own order). A tile's items are then
+// merged so that the halves take turns (143 us).
 //
-// k_attn_tree, one persistent CTA per SM: the items of all tiles, in order, are cut into one range per CTA,
-// so one long tile is spread over many SMs and many short ones share them.  Leaving one tile for the next costs
-// a CTA about the time of kTileCost items (its output, and no attention meanwhile), so each tile counts
-// for so many items more where the ranges are cut (one, where a range is a few items and latency counts).  The part of a tile inside a
-// range is a segment; it keeps one online softmax.  A tile cut by a range's end leaves partials (unnormalised
-// O, max and sum, in 32 bits) in the workspace, and k_tree_join joins them in the order of the ranges: a
-// kernel of its own, because one CTA reading all partials of a tile took longer than the attention
-// itself (13 partials of 40 rows: 20 us of 35).  Warps:
+// k_attn_tree, one persistent CTA per SM: the items of all tiles, in order, are cut into one range per CTA, so one
+// long tile is spread over many SMs and many short ones share them.  Leaving one tile for the next costs a CTA
+// about the time of kTileCost items (its output, and no attention meanwhile), so each tile counts for so many
+// items more where the ranges are cut (one, where a range is a few items and latency counts).  The part of a tile
+// inside a range is a segment; it keeps one online softmax.  A tile cut by a range's end leaves partials
+// (unnormalised O, max and sum, in 32 bits: in 16 they would cost a rounding more) in the workspace, and
+// k_tree_join joins them in the order of the ranges: a kernel of its own, because one CTA reading all partials of
+// a tile took longer than the attention itself (13 partials of 40 rows: 20 us of 35).  Warps:
 //   0      K/V producer: TMA boxes of 64 columns x 128 tokens (128B swizzle) into a ring for each;
 //   1      MMA issuer: S = Q K^T into the TMEM buffer of a softmax group, then, one unit later, O += P V with
 //          P in TMEM (over S) and V as an MN-major shared-memory operand (an issuer for each was no faster, and
@@ -33,13 +37,14 @@
 //          rows.  P = 2^(s - m) for a reference m that is the row's first maximum (rounded up to a whole
 //          power of two) until a logit passes it by 2^40: P, sums and O are floating point of 8 exponent bits
 //          throughout, so a reference below the true maximum costs no precision, S is read once, and O, in
-//          TMEM, is next to never rescaled (by a power of two then, exactly);
+//          TMEM, is next to never rescaled (by a power of two then, exactly).  P is rounded to bf16, as the
+//          operand of the MMA: half a step, 2^-8 of each weight, as large as the rounding of the output;
 //   2, 3   Q loads (one box of 64 columns x HPG heads x 128/HPG nodes is a whole 128-row tile of Q), and the
 //          finite check of V: a row that does not see a token has P = 0 there, and 0 * NaN would still reach its
 //          O through the MMA, so what is not finite is replaced by 0 before the MMA reads it.  Rows that
-//          do see such a value get it back at the segment's end (add_nonfinite), off the hot path.
-// TMEM: S0 | S1 | O0 | O1 (128 + 128 + D + D of 512 columns).  Every barrier has one waiting role, which waits for each
-// of its phases in order (or, for a group's O, knows the one before to be over).  Every wait is bounded.
+//          do see such a value get it back at the segment's end, off the hot path.
+// TMEM: S0 | S1 | O0 | O1 (128 + 128 + D + D of 512 columns).  Every barrier has one waiting role, which waits for
+// each of its phases in order (or, for a group's O, knows the one before to be over).  Every wait is bounded.
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
@@ -51,7 +56,7 @@ namespace {
 constexpr int kThreads = 384;           // 168 registers a thread
 constexpr int kMaxCtas = 160;           // partial slots in the workspace; at most one CTA per SM
 constexpr int kOkRing = 8;              // finite-check barriers, by item
-constexpr int kTileCost = 3;           // of a tile, in items, where the ranges are cut
+constexpr int kTileCost = 3;            // of a tile, in items, where the ranges are cut
 constexpr int kSortedBit = 1 << 30;     // of a tile's place in `order`: not the nodes' own order
 constexpr int kDraftBit = 1 << 30;      // of a tile's item count: its last item is the drafted tokens
 constexpr float kRaise = 40.0f;         // raise the reference once a logit is this far above (log2 units)
