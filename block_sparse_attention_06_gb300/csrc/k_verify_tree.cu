@@ -180,13 +180,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
                     const int x = __ffsll(kids) - 1;
                     kids &= kids - 1;
                     const int tok = sm.tok[x];
-                    const double qx = drafts ? double(sm.q[x]) : 1.0;
-                    double r = double(sm.p[x]) - (drafts ? c * qx : 0.0);
-                    if (!(r > 0.0)) r = 0.0;
+                    const float px = sm.p[x], qx = drafts ? sm.q[x] : 1.f, ux = sm.u[x];
+                    bool gone = false;
                     if (!drafts)
-                        for (int i = 0; i < n_gone; ++i)
-                            if (sm.gone[i] == tok) r = 0.0;
-                    if (double(sm.u[x]) * qx * mass < r) {
+                        for (int i = 0; i < n_gone; ++i) gone = gone || sm.gone[i] == tok;
+                    auto left = [&]() {   // of the token in the residual
+                        const double r = double(px) - (drafts ? c * double(qx) : 0.0);
+                        return r > 0.0 && !gone ? r : 0.0;
+                    };
+                    // In fp32 first, whose roundings stay below 2^-21 of the terms, and in 64 bits where that does not
+                    // tell (a 64-bit operation is slow here, and the walk is one after another).
+                    const float cf = float(c), rf = gone ? 0.f : fmaxf(drafts ? fmaf(-cf, qx, px) : px, 0.f);
+                    const float lf = ux * qx * float(mass);
+                    const float slack = fmaf(0x1p-20f, fabsf(px) + cf * qx + fabsf(lf), 1e-36f);
+                    if (fabsf(lf - rf) > slack ? lf < rf : double(ux) * double(qx) * mass < left()) {
                         at = x;
                         kids = sm.kids[x];
                         c = 0.0;
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
                         c += mass;
                         cmd = kPass;
                     } else {
-                        mass = fmax(mass - r, 0.0);   // rounding of p may leave less than nothing
+                        mass = fmax(mass - left(), 0.0);   // rounding of p may leave less than nothing
                         if (lane == 0) sm.gone[n_gone] = tok;
                         ++n_gone;
                         __syncwarp();
@@ -402,8 +409,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
         else __syncthreads();
         buf ^= 1;
         if (warp == 0) {   // the residual's mass
-            double s = 0.0;
-            for (int i = lane; i < slots; i += 32) s += sm.run[buf ^ 1][i];
+            double own[kMaxCluster * kWarps / 32];
+#pragma unroll
+            for (int i = 0; i < kMaxCluster * kWarps / 32; ++i)
+                own[i] = lane + 32 * i < slots ? sm.run[buf ^ 1][lane + 32 * i] : 0.0;
+            double s = (own[0] + own[1]) + (own[2] + own[3]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             mass = s;
