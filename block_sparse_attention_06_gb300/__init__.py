@@ -1017,7 +1017,8 @@ class TreeStep:
     n_rows is the largest number of drafted tokens of a step, over all requests; node_off (int32
     [n_req + 1]) and parents (int32 [n_rows]) say which rows are in use, so one captured step serves
     trees of any shape: rows at or past node_off[n_req] are padding.  Every node sees what it would
-    see in a sequential decode along its path, block selection included."""
+    see in a sequential decode along its path, block selection included.  Steps that may run at once
+    need a TreeStep each."""
 
     def __init__(self, dims: Dims, n_rows: int, n_req: int, device):
         self.dims, self.n_rows, self.n_req = dims, n_rows, n_req
@@ -1036,6 +1037,7 @@ class TreeStep:
         self.next_token = torch.zeros((n_req,), dtype=torch.int32, **f)
         self.new_lens = torch.zeros((n_req,), dtype=torch.int32, **f)
         self.err = new_err_word(device)
+        self.node_off = self.parents = self.ctx_lens = None   # of the step in hand, from layout()
 
     def layout(self, node_off, parents, ctx_lens):
         """Positions and ancestors of this step's rows, shared by every layer."""

@@ -484,7 +484,7 @@ msa_status_t msa_tree_index_score(const void *q_idx, const void *kidx_cache, con
  *   out        bf16 [n_rows][Hq][D]  out;  lse fp32 [n_rows][Hq]  out.  A row that sees
  *              no token gets 0 and -inf.  Padding rows are not written.
  *   workspace  device scratch of msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims)
- *              bytes, 16-byte aligned
+ *              bytes, 16-byte aligned; calls that may run at once need one each
  * What a row does not see does not reach its result, whatever its bits (unwritten
  * page tails, other branches, padding rows).  A block id >= max_blocks, or a page
  * outside [0, n_pages) of a block that holds cached tokens, raises MSA_FLAG_BOUNDS.
@@ -540,7 +540,7 @@ msa_status_t msa_verify_tree(const float *target_probs, const float *draft_probs
  *   k_cache, v_cache  bf16 [n_layers][n_pages][128][G][D];  kidx_cache likewise with Di
  *   block_table   int32 [n_req][max_blocks], the same for every layer
  *   path, n_accepted  from msa_verify_tree
- *   new_lens      int32 [n_req]  out: ctx_lens[b] + n_accepted[b]; not ctx_lens itself
+ *   new_lens      int32 [n_req]  out: ctx_lens[b] + n_accepted[b]; not over ctx_lens
  * A page outside [0, n_pages), a position past max_blocks * 128 or a bad path entry
  * raises MSA_FLAG_BOUNDS and that token is not written.
  */

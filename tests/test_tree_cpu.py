@@ -77,6 +77,13 @@ def test_bad_sizes_and_pointers(lib):  # noqa: F811
     assert b"new_lens" in lib.msa_last_error()
 
 
+def test_commit_refuses_lengths_that_overlap(lib):  # noqa: F811
+    """A CTA of one layer would write a length that another has still to read."""
+    d = good_dims()
+    for shift in (-4, 4):
+        assert _commit(lib, d, n_req=2, lens=ctypes.c_void_p(FAKE.value + shift)) == 1
+
+
 def test_nothing_to_do(lib):  # noqa: F811
     d = good_dims()
     assert _rows(lib, d, n_rows=0) == 0 and _score(lib, d, n_rows=0) == 0 and _attn(lib, d, n_rows=0) == 0
