@@ -575,11 +575,11 @@ msa_status_t msa_commit_tree(const void *k_new, const void *v_new, const void *k
     MSA_REQUIRE(ctx_lens && node_off && n_accepted && new_lens && err_word, "msa_commit_tree: NULL pointer");
     MSA_REQUIRE(n_rows == 0 || (k_new && v_new && kidx_new && k_cache && v_cache && kidx_cache && block_table && path),
                 "msa_commit_tree: NULL pointer");
+    if (n_layers > 65535 || n_req > kTreeMaxRequests)
+        return fail(MSA_ERR_UNSUPPORTED, "msa_commit_tree: more than 65535 layers or %d requests", kTreeMaxRequests);
     // every layer's CTAs read the old lengths
     MSA_REQUIRE(new_lens >= ctx_lens + n_req || ctx_lens >= new_lens + n_req,
                 "msa_commit_tree: new_lens must not overlap ctx_lens");
-    if (n_layers > 65535 || n_req > kTreeMaxRequests)
-        return fail(MSA_ERR_UNSUPPORTED, "msa_commit_tree: more than 65535 layers or %d requests", kTreeMaxRequests);
     if (misaligned16({k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache}))
         return fail(MSA_ERR_INVALID_ARG, "msa_commit_tree: rows and caches must be 16-byte aligned");
     cudaError_t e = launch_commit_tree(k_new, v_new, kidx_new, n_layers, k_cache, v_cache, kidx_cache, block_table,
