@@ -11,9 +11,9 @@
 // run's sum in every CTA's shared memory, and after one cluster barrier warp 0 of each CTA goes on with the
 // walk by itself, all of them with the same numbers and so the same decisions.  The next token is then
 // found in the one run that holds it.
-// 32 requests x 131,072 tokens: 38 us, about five passes of 33 MB for the slowest request (a rejection decides the next
-// test, so the passes of a request follow one another; a pass is 4 us of loads and 2 us of sums and cluster barrier).
-// One request: 12 us.
+// 32 requests x 131,072 tokens: 37 us, about five passes of 33 MB for the slowest request (a rejection decides the next
+// test, so the passes of a request follow one another; a pass is 3 to 5 us of loads, 1.5 of sums and cluster barrier and 1 of the decision).
+// One request: 11 us.
 //
 // A rounding of a sum moves a border between two tokens, so sums are carried to more than 40 bits of the whole mass.
 // 64-bit arithmetic runs at 1/64 of the fp32 rate on this GPU and pairs of fp32 numbers for each residual made the

@@ -437,7 +437,8 @@ msa_status_t msa_sparse_attn_decode_noalloc(const void *q, const void *k_cache, 
  * cached tokens, its ancestors and itself.  Blocks are counted by position, so a
  * drafted token belongs to block (ctx_lens[b] + depth) / 128.  K, V and index keys
  * of the drafted tokens come as dense rows ([n_rows][G][D] and [n_rows][G][Di]),
- * not through the caches; msa_commit_tree writes the accepted ones there.
+ * not through the caches; msa_commit_tree writes the accepted ones there.  No output
+ * may lie over an input, but for the caches that msa_commit_tree writes.
  *
  * msa_tree_rows -- positions and ancestors of every row, shared by all layers of a step.
  *   ctx_lens  int32 [n_req]
