@@ -1016,6 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                                         tmem_st16(t_o + uint32_t(w * D + d), x);
                                     }
                                 }
+                                tmem_st_wait();   // the rounds before may still be storing it
 #pragma unroll 1
                                 for (int d = 0; d < (c >> 1); d += 16) {   // this item's P so far
                                     uint32_t x[16];
