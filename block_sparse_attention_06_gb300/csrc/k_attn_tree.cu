@@ -923,7 +923,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                         tmem_ld32(t_s, u[0]);
                         tmem_ld32(t_s + 32u, u[1]);
                         tmem_ld_wait();
-                        if (__any_sync(0xffffffffu, sees && m == -INFINITY)) {
+                        bool based = !__any_sync(0xffffffffu, sees && m == -INFINITY);
+                        if (!based) {
                             float a[4];
 #pragma unroll
                             for (int x = 0; x < 4; ++x) a[x] = __uint_as_float(u[0][x]);
@@ -936,28 +937,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(
                             for (int x = 0; x < 4; ++x) a[x] = fmaxf(a[x], __uint_as_float(u[0][28 + x]));
                             const float top = fmaxf(fmax3(a[0], a[1], a[2]), a[3]) * scale;
                             if (sees && m == -INFINITY && top > m) m = ceilf(top);
+                            based = !__any_sync(0xffffffffu, sees && m == -INFINITY);
                         }
-                        tmem_ld32(t_s + 64u, u[2]);
-                        nm2 = dup2(m == -INFINITY ? 0.f : -m);
-                        chunk(0);
-                        tmem_ld_wait();
-                        tmem_ld32(t_s + 96u, u[3]);
-                        chunk(1);
-                        chunk(2);
-                        tmem_ld_wait();
-                        chunk(3);
-                        const float add = (sum2(sum[0]) + sum2(sum[1])) + (sum2(sum[2]) + sum2(sum[3]));
-                        done = !__any_sync(0xffffffffu, sees && add > kRaiseSum);
-                        if (done) {
-                            if (!__all_sync(0xffffffffu, sees)) {
+                        // Where a row's first 32 logits are all -inf or NaN it has no reference yet, and the loop below
+                        // takes the block: it sets one at the first chunk that has a maximum.
+                        if (based) {
+                            tmem_ld32(t_s + 64u, u[2]);
+                            nm2 = dup2(m == -INFINITY ? 0.f : -m);
+                            chunk(0);
+                            tmem_ld_wait();
+                            tmem_ld32(t_s + 96u, u[3]);
+                            chunk(1);
+                            chunk(2);
+                            tmem_ld_wait();
+                            chunk(3);
+                            const float add = (sum2(sum[0]) + sum2(sum[1])) + (sum2(sum[2]) + sum2(sum[3]));
+                            done = !__any_sync(0xffffffffu, sees && add > kRaiseSum);
+                            if (done) {
+                                if (!__all_sync(0xffffffffu, sees)) {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
+                                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) p[i][e] = sees ? p[i][e] : 0u;
+                                        for (int e = 0; e < 16; ++e) p[i][e] = sees ? p[i][e] : 0u;
+                                }
+                                if (sees) l += add;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) tmem_st16(t_s + uint32_t(16 * i), p[i]);
                             }
-                            if (sees) l += add;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) tmem_st16(t_s + uint32_t(16 * i), p[i]);
                         }
                     }
 #pragma unroll 1
