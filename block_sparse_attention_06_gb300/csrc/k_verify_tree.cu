@@ -11,15 +11,19 @@
 // run's sum in every CTA's shared memory, and after one cluster barrier warp 0 of each CTA goes on with the
 // walk by itself, all of them with the same numbers and so the same decisions.  The next token is then
 // found in the one run that holds it.
-// 32 requests x 131,072 tokens: 37 us, about five passes of 33 MB for the slowest request (a rejection decides the next
-// test, so the passes of a request follow one another; a pass is 3 to 5 us of loads, 1.5 of sums and cluster barrier and 1 of the decision).
+// 32 requests x 131,072 tokens: 38 us, about five passes of 33 MB for the slowest request (a rejection decides the next
+// test, so the passes of a request follow one another; a pass is 3 to 5 us of loads, 2 of sums and cluster barrier and 1 of the decision).
 // One request: 11 us.
 //
-// A rounding of a sum moves a border between two tokens, so sums are carried to more than 40 bits of the whole mass.
-// 64-bit arithmetic runs at 1/64 of the fp32 rate on this GPU and pairs of fp32 numbers for each residual made the
+// A rounding of a sum moves a border between two tokens, and the residual may be a flat tail of a row whose likely
+// token was rejected, so sums have to be good to a small part of themselves, whatever is in the row.  64-bit
+// arithmetic runs at 1/64 of the fp32 rate on this GPU and pairs of fp32 numbers for each residual made the
 // pass bound by its arithmetic (3.6 us of 131,072 tokens on 8 CTAs).  A residual's mass is A - c B, A and B the sums
-// of p and q over the tokens with p > c q, and those are sums of given fp32 numbers: each is split at 2^-22 into a
-// part whose sums are exact in fp32 up to 4 and a rest below 2^-23.  Everything from the run sums on is in 64 bits.
+// of p and q over the tokens with p > c q, and those are sums of given fp32 numbers that are not negative: each is
+// carried as h + l with the exact error of every addition to h added to l, and l is brought below a step of h after
+// every four.  Four of a lane's additions then lose at most 14 * 2^-48 of its sum and the join of the lanes 66 * 2^-48,
+// so a sum is off by less than (n + 20) 2^-46 of itself with n tokens per half lane, vocab / (1024 * CTAs of the request):
+// 2^-40 for 131,072 tokens on 8 CTAs, 2^-38 on one.  Everything from the run sums on is in 64 bits.
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
@@ -39,7 +43,7 @@ struct Smem {
     int tok[kTreeMaxNodes];
     float u[kTreeMaxNodes], p[kTreeMaxNodes], q[kTreeMaxNodes];   // at the node's token in its parent's rows
     int gone[kTreeMaxNodes];                                      // tokens taken out (no draft distribution)
-    float4 part[kWarps];                                          // A and B of each warp's run, split
+    float4 part[kWarps];                                          // A and B of each warp's run, h and l
     double run[2][kMaxCluster * kWarps];                          // run sums of the cluster, two passes
     double c, before, want;
     int cmd, at, n_gone, slot;
@@ -71,23 +75,28 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 
-// h + l += v in both lanes: h holds multiples of 2^-22 (exact while the sum of a row stays below 4), l what is left.
-__device__ __forceinline__ void add_split(uint64_t &h, uint64_t &l, uint64_t v) {
-    const uint64_t hi = add2(add2(v, pack2(3.0f, 3.0f)), pack2(-3.0f, -3.0f));
-    h = add2(h, hi);
-    l = add2(l, fma2(hi, pack2(-1.0f, -1.0f), v));
+// h + l += v in both lanes: the exact error of h + v goes to l.
+__device__ __forceinline__ void add_pair(uint64_t &h, uint64_t &l, uint64_t v) {
+    const uint64_t s = add2(h, v), w = sub2(s, h);
+    l = add2(l, add2(sub2(h, sub2(s, w)), sub2(v, w)));
+    h = s;
 }
-
-__device__ __forceinline__ float warp_sum_f(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// h takes what of l it can hold.
+__device__ __forceinline__ void settle(uint64_t &h, uint64_t &l) {
+    const uint64_t s = add2(h, l);
+    l = sub2(l, sub2(s, h));
+    h = s;
 }
 
 struct Residual {
@@ -349,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
             break;
         }
         // a pass: this warp's run sum, A - c B
-        uint64_t ah2 = 0, al2 = 0, bh2 = 0, bl2 = 0;
+        uint64_t ah = 0, al = 0, bh = 0, bl = 0;   // two tokens' sums each
         const uint64_t nchi2 = pack2(-res.chi, -res.chi), nclo2 = pack2(-res.clo, -res.clo);
         constexpr int U = kInFlight / VEC;   // tiles in flight
         for (int tile = tile0; tile < tile1; tile += U) {
@@ -375,25 +384,30 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
                     const float q0 = fmaxf(cq[x / VEC].v[x % VEC], 0.f), q1 = fmaxf(cq[(x + 1) / VEC].v[(x + 1) % VEC], 0.f);
                     const uint64_t q2 = pack2(q0, q1);
                     const float2 r = unpack2(fma2(nclo2, q2, fma2(nchi2, q2, pack2(p0, p1))));
-                    add_split(ah2, al2, pack2(r.x > 0.f ? p0 : 0.f, r.y > 0.f ? p1 : 0.f));
-                    add_split(bh2, bl2, pack2(r.x > 0.f ? q0 : 0.f, r.y > 0.f ? q1 : 0.f));
+                    add_pair(ah, al, pack2(r.x > 0.f ? p0 : 0.f, r.y > 0.f ? p1 : 0.f));
+                    add_pair(bh, bl, pack2(r.x > 0.f ? q0 : 0.f, r.y > 0.f ? q1 : 0.f));
                 } else {
-                    add_split(ah2, al2, pack2(fmaxf(p0, 0.f), fmaxf(p1, 0.f)));   // NaN counts as 0
+                    add_pair(ah, al, pack2(fmaxf(p0, 0.f), fmaxf(p1, 0.f)));   // NaN counts as 0
                 }
             }
+            settle(ah, al);
+            if (res.draft) settle(bh, bl);
         }
-        auto both = [](uint64_t v) {
-            const float2 x = unpack2(v);
-            return x.x + x.y;
-        };
-        float ah = both(ah2), al = both(al2), bh = both(bh2), bl = both(bl2);
-        ah = warp_sum_f(ah);
-        al = warp_sum_f(al);
-        if (res.draft) {
-            bh = warp_sum_f(bh);
-            bl = warp_sum_f(bl);
+        // the two halves and the lanes, A beside B
+        const float2 a_h = unpack2(ah), a_l = unpack2(al), b_h = unpack2(bh), b_l = unpack2(bl);
+        uint64_t h = pack2(a_h.x, b_h.x), l = pack2(a_l.x, b_l.x);
+        add_pair(h, l, pack2(a_h.y, b_h.y));
+        l = add2(l, pack2(a_l.y, b_l.y));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const uint64_t h_o = __shfl_xor_sync(0xffffffffu, h, o), l_o = __shfl_xor_sync(0xffffffffu, l, o);
+            add_pair(h, l, h_o);
+            l = add2(l, l_o);
         }
-        if (lane == 0) sm.part[warp] = make_float4(ah, al, bh, bl);
+        if (lane == 0) {
+            const float2 hs = unpack2(h), ls = unpack2(l);
+            sm.part[warp] = make_float4(hs.x, ls.x, hs.y, ls.y);
+        }
         __syncthreads();
         // one warp joins them: the SM has two 64-bit operations a cycle, and 16 warps would queue up for them
         if (warp == 0 && lane < kWarps) {

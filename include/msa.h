@@ -521,8 +521,10 @@ msa_status_t msa_sparse_attn_tree(const void *q, const void *k_cache, const void
  *             first, from row node_off[b] on; -1 behind them; padding rows are not written
  *   n_accepted int32 [n_req]  out: nodes accepted, the root among them (0 without nodes)
  *   next_token int32 [n_req]  out; -1 for a request without nodes
- * Sums are carried to more than 40 bits of the whole mass of a row (its entries
- * are taken to sum to less than 4), comparisons in 64 bits.  vocab <= 2^30.  A token outside [0, vocab) or a bad
+ * A sum over a row of p or q is off by less than (vocab / 1024 + 32) * 2^-46 of itself
+ * (2^-38 of it at 131,072 tokens), whatever the row holds; with a draft distribution
+ * a residual's mass is one such sum less c times another.  Comparisons in 64 bits.
+ * vocab <= 2^30.  A token outside [0, vocab) or a bad
  * parent raises MSA_FLAG_BOUNDS (that node is never accepted); a row of target_probs
  * without finite positive mass raises MSA_FLAG_NAN (next_token -1).
  */

@@ -141,3 +141,115 @@ def test_rows_whose_logits_are_all_infinite(msa):
     alone = T.make_tree([256], [3], 98, "star")
     alone.block_table, alone.n_pages = t.block_table, t.n_pages
     _check_finite(alone, out[1::2], lse[1::2], x, torch.full((3, 1, 2), 1, dtype=torch.int32), 128)
+
+
+# ------------------------------------------------------------------ verification: sums of flat tails, rows of any mass
+
+def _flat_tail(V, head, x1, x2):
+    """A likely token and a flat tail: x1 in its first half, x2 in the second.  Returns the row, and the tail's entries
+    as whole numbers of 2^-60 with their sum (fp32 numbers from 2^-36 on are whole numbers of 2^-60)."""
+    x = torch.full((V,), x1, dtype=torch.float32)
+    x[V // 2:] = x2
+    x[head] = 0.0
+    units = (x.double() * 2.0 ** 60).long()
+    row = x.clone()
+    row[head] = 1.0 - float(x.double().sum())
+    return row, units, int(units.sum())
+
+
+def _border(cum, total, u):
+    """The smallest t with cum[t] > u * total, exactly (u an fp32 number: a whole number of 2^-24 over [0, 1))."""
+    n = int(float(u) * 2 ** 48)
+    assert n == float(u) * 2 ** 48
+    want = n * total
+    lo, hi = 0, len(cum) - 1
+    while lo < hi:
+        mid = (lo + hi) // 2
+        lo, hi = (lo, mid) if (int(cum[mid]) << 48) > want else (mid + 1, hi)
+    return lo
+
+
+@pytest.mark.parametrize("B", [3, 200])                         # clusters of CTAs, and more requests than SMs
+@pytest.mark.parametrize("V", [131072, 130999])
+@pytest.mark.parametrize("drafts", [True, False])
+def test_sums_of_a_flat_tail(msa, V, B, drafts):
+    """A likely token was drafted and rejected: the flat tail behind it is all that is left, and the next token's
+    border is placed a small part of a token's share away from a token's end."""
+    head = 777
+    row, units, total = _flat_tail(V, head, 2.0 ** -23, 1.1920e-7)
+    cum = units.cumsum(0)
+    g = torch.Generator().manual_seed(101)
+    # borders half a hundredth of a share and more away from a token's end, on both sides
+    ends = torch.randint(V // 8, V // 2 - 2, (B,), generator=g)
+    share = cum[ends].double() / total
+    u = (share + torch.where(torch.arange(B) % 2 == 0, 1.0, -1.0) * 2.0 ** -17 / 40).float()
+    want = [_border(cum, total, x) for x in u]
+    tok = torch.tensor([0, head], dtype=torch.int32).repeat(B)
+    ua = torch.tensor([0.0, 1 - 2.0 ** -24]).repeat(B)
+    off = torch.arange(0, 2 * B + 1, 2, dtype=torch.int32, device=DEV)
+    par = torch.tensor([-1, 0], dtype=torch.int32, device=DEV).repeat(B)
+    P = row.to(DEV).expand(2 * B, V).contiguous()
+    Q = None
+    if drafts:
+        Q = torch.zeros(V)
+        Q[head] = 1.0
+        Q = Q.to(DEV).expand(2 * B, V).contiguous()
+    err = msa.new_err_word(DEV)
+    path, acc, nxt = msa.msa_verify_tree(P, Q, tok.to(DEV), off, par, ua.to(DEV), u.to(DEV), err_word=err)
+    msa.msa_check(err)
+    assert acc.tolist() == [1] * B
+    assert nxt.tolist() == want
+
+
+@pytest.mark.parametrize("B", [4, 200])
+def test_mass_of_a_flat_tail(msa, B):
+    """The second child is held to the mass of that tail: accepted just below the border, rejected just above it."""
+    V, head, tok = 131072, 5, 100000
+    row, units, total = _flat_tail(V, head, 2.0 ** -23, 1.1920e-7)
+    mass = total * 2.0 ** -60                                   # of the residual once the head is rejected, but for q
+    q = torch.zeros(V)
+    q[head] = 1.0
+    q[tok] = float(row[tok]) / (1 + mass / 2)                   # r(tok) is about half of mass * q(tok)
+    qt = int(float(q[tok].double() * 2.0 ** 60))
+    left, rest = int(units[tok]) - qt, total - qt               # whole numbers of 2^-60: r(tok) and M
+    border = left * 2 ** 60 / (qt * rest)
+    assert 0.4 < border < 0.6
+    u0 = torch.tensor([border], dtype=torch.float64).float()
+    step = 2.0 ** -24                                           # fp32 numbers in [0.5, 1); half of it below
+    u = torch.stack([u0 + k * step for k in (-3, -2, 2, 3)]).flatten().repeat(B // 4)
+    want = [2 if int(float(x) * 2 ** 48) * qt * rest < left << 108 else 1 for x in u]
+    assert sorted(set(want)) == [1, 2]
+    off = torch.arange(0, 3 * B + 1, 3, dtype=torch.int32, device=DEV)
+    par = torch.tensor([-1, 0, 0], dtype=torch.int32, device=DEV).repeat(B)
+    toks = torch.tensor([0, head, tok], dtype=torch.int32, device=DEV).repeat(B)
+    ua = torch.stack([torch.zeros(B), torch.full((B,), 1 - 2.0 ** -24), u], 1).flatten().to(DEV)
+    P, Q = row.to(DEV).expand(3 * B, V).contiguous(), q.to(DEV).expand(3 * B, V).contiguous()
+    err = msa.new_err_word(DEV)
+    path, acc, _ = msa.msa_verify_tree(P, Q, toks, off, par, ua, torch.full((B,), 0.5, device=DEV), err_word=err)
+    msa.msa_check(err)
+    assert acc.tolist() == want
+    assert path.view(B, 3)[:, 1].tolist() == [2 if w == 2 else -1 for w in want]
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 10, 2.0 ** -20])
+def test_next_token_of_rows_of_any_mass(msa, scale):
+    """Weights that do not sum to one: the next token goes by their share all the same."""
+    V, B = 5003, 64
+    g = torch.Generator().manual_seed(102)
+    w = torch.randint(1, 2 ** 20, (V,), generator=g)
+    row = (w.double() * 2.0 ** -20 * scale).float()             # exact
+    cum = w.cumsum(0)
+    u = torch.rand(B, generator=g)
+    # a border between two tokens, from either side
+    ends = torch.randint(V // 8, V, (B,), generator=g)
+    near = cum[ends].double() / int(cum[-1])
+    u[::2] = (near + torch.where(torch.arange(B) % 4 == 0, 1.0, -1.0) * 2.0 ** -23).clamp(max=1 - 2.0 ** -24).float()[::2]
+    want = [_border(cum, int(cum[-1]), x) for x in u]
+    off = torch.arange(B + 1, dtype=torch.int32, device=DEV)
+    par = torch.full((B,), -1, dtype=torch.int32, device=DEV)
+    zero = torch.zeros(B, device=DEV)
+    err = msa.new_err_word(DEV)
+    _, acc, nxt = msa.msa_verify_tree(row.to(DEV).expand(B, V).contiguous(), None, par * 0, off, par, zero, u.to(DEV),
+                                      err_word=err)
+    msa.msa_check(err)
+    assert acc.tolist() == [1] * B and nxt.tolist() == want
