@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_tree(
                     for (int e = 0; e < VEC; ++e) {
                         bool out = false;
                         for (int i = 0; i < gone_n; ++i) out = out || sm.gone[i] == t + e;
-                        if (res.value(cp.v[e], cq.v[e]) > 0.0 && !out) mine = t + e;
+                        // (as the pass decided: a run with mass has such a token)
+                        if (res.positive(cp.v[e], fmaxf(cq.v[e], 0.f)) && !out) mine = t + e;
                     }
                     token = __reduce_max_sync(0xffffffffu, mine);
                 }
