@@ -1247,7 +1247,7 @@ __global__ void __launch_bounds__(256, 3) k_tree_join(const Cut *__restrict__ cu
             for (int i = 0; i < 4; ++i) {
                 const float w = fast_exp2(ml[i].x + nt);
                 l = fmaf(ml[i].y, w, l);
-                if (w == 0.f) continue;   // nothing seen there (its O may hold anything)
+                if (ml[i].x == -INFINITY) continue;   // nothing seen there (its O may hold anything)
                 o[0] = fmaf(w, v[i][0].x, o[0]);
                 o[1] = fmaf(w, v[i][0].y, o[1]);
                 o[2] = fmaf(w, v[i][0].z, o[2]);

@@ -253,3 +253,29 @@ def test_next_token_of_rows_of_any_mass(msa, scale):
                                       err_word=err)
     msa.msa_check(err)
     assert acc.tolist() == [1] * B and nxt.tolist() == want
+
+
+# ------------------------------------------------------------------ attention: values that are not finite, next to no weight
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("nodes,ctx", [(3, 256), (3, 512), (3, 1024), (3, 2048), (40, 2048)])
+def test_seen_nonfinite_values_of_no_weight(msa, bad, nodes, ctx):
+    """A value that is not finite reaches the rows that see it, however little its token weighs, whether or not the
+    token's block and the heavy one fall to the same range of work."""
+    t = T.make_tree([ctx], [nodes], 103, "star")
+    x = _inputs(t, 8, 1, 128, 104)
+    q, kc, vc = x[:3]
+    q[..., 0] = 8.0
+    kc[..., 0] = 0.0
+    x[3][..., 0] = 0.0
+    kc[int(t.block_table[0, ctx // 128 - 1]), 60, :, 0] = 160.0   # 113 above the others: e^-113 is 0 in 32 bits
+    vc[int(t.block_table[0, 0]), 3, 0, 7] = bad
+    sel = torch.arange(16, dtype=torch.int32).repeat(nodes, 1, 1)
+    sel[sel >= ctx // 128] = -1
+    sel[1, :, 0] = -1                                             # node 1 does not see it
+    out, lse = _attend(msa, t, msa.Dims(8, 1, 128, 64, 16, t.max_blocks), x, sel)
+    hit = ~torch.isfinite(out.cpu())
+    want = torch.zeros_like(hit)
+    want[:, :, 7] = True
+    want[1] = False
+    assert torch.equal(hit, want) and bool(torch.isfinite(lse).all())
