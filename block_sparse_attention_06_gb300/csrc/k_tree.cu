@@ -9,6 +9,41 @@
 namespace msa {
 namespace {
 
+// The rows of no request, by one CTA: those behind the last request, or, where a range is refused (they may then
+// overlap or leave gaps anywhere), every row that no good range holds, found through a bitmap of them.
+__device__ __forceinline__ void pad_rows(const int32_t *__restrict__ node_off, int n_rows, int n_req,
+                                         int32_t *__restrict__ q_req, int32_t *__restrict__ q_pos,
+                                         uint64_t *__restrict__ anc) {
+    constexpr int kWindow = 32768;   // rows looked at together
+    __shared__ uint32_t held[kWindow / 32];
+    const int i = threadIdx.x;
+    int r0, r1;
+    bool bad = false;
+    for (int x = i; x < n_req; x += kTreeMaxNodes) bad |= tree_range(node_off, x, n_rows, &r0, &r1) != 0;
+    bad = __syncthreads_or(bad);
+    // (without a bad range node_off rises from 0 to n_rows at most)
+    for (long long w0 = bad ? 0 : node_off[n_req]; w0 < n_rows; w0 += kWindow) {
+        const int rows = int(min((long long)kWindow, n_rows - w0));
+        if (bad) {
+            for (int x = i; x < kWindow / 32; x += kTreeMaxNodes) held[x] = 0;
+            __syncthreads();
+            for (int x = i; x < n_req; x += kTreeMaxNodes) {
+                if (tree_range(node_off, x, n_rows, &r0, &r1)) continue;
+                const int lo = int(max(0LL, r0 - w0)), hi = int(min((long long)rows, r1 - w0));
+                for (int r = lo; r < hi; ++r) atomicOr(&held[r >> 5], 1u << (r & 31));
+            }
+            __syncthreads();
+        }
+        for (int r = i; r < rows; r += kTreeMaxNodes) {
+            if (bad && (held[r >> 5] >> (r & 31) & 1)) continue;
+            q_req[w0 + r] = -1;
+            q_pos[w0 + r] = 0;
+            anc[w0 + r] = 0;
+        }
+        __syncthreads();
+    }
+}
+
 // CTA b < n_req: request b, one thread per node.  CTA n_req: the padding rows.
 __global__ void __launch_bounds__(kTreeMaxNodes) k_tree_rows(
     const int32_t *__restrict__ node_off, const int32_t *__restrict__ parents, const int32_t *__restrict__ ctx_lens,
@@ -19,25 +54,12 @@ __global__ void __launch_bounds__(kTreeMaxNodes) k_tree_rows(
     const int b = blockIdx.x, i = threadIdx.x;
     pdl_trigger();
     if (b == n_req) {
-        for (int r = max(0, node_off[n_req]) + i; r < n_rows; r += kTreeMaxNodes) {
-            q_req[r] = -1;
-            q_pos[r] = 0;
-            anc[r] = 0;
-        }
+        pad_rows(node_off, n_rows, n_req, q_req, q_pos, anc);
         return;
     }
     int row0;
     const int n = tree_rows_of(node_off, b, n_rows, err, i == 0, &row0);
-    if (n == 0) {
-        const int r1 = min(node_off[b + 1], n_rows);   // rows of a refused request: padding
-        if (row0 >= 0)
-            for (int r = row0 + i; r < r1; r += kTreeMaxNodes) {
-                q_req[r] = -1;
-                q_pos[r] = 0;
-                anc[r] = 0;
-            }
-        return;
-    }
+    if (n == 0) return;   // no rows, or those of a refused request: padding
     // up: the node that this node's word reaches next (itself at the root)
     const int p = i < n ? parents[row0 + i] : 0;
     bool bad = i < n && (i == 0 ? p != -1 : (p < 0 || p >= i));

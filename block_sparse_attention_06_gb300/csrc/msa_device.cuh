@@ -335,21 +335,26 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 
 // ------------------------------------------------------------------ drafted trees
 
+// Rows r0 .. r1-1 of request b's tree; what is wrong with the range (0: nothing, a flag otherwise).
+__device__ __forceinline__ int32_t tree_range(const int32_t *__restrict__ node_off, int b, int n_rows, int *r0,
+                                              int *r1) {
+    *r0 = node_off[b];
+    *r1 = node_off[b + 1];
+    if (*r0 < 0 || *r1 < *r0 || *r1 > n_rows || (b == 0 && *r0 != 0)) return MSA_FLAG_BOUNDS;
+    return *r1 - *r0 > 64 ? MSA_FLAG_UNSUPPORTED : 0;
+}
+
 // Rows of request b's tree: returns the node count (0 for a bad range, with its flag raised where
 // `report` is set) and the first row.
 __device__ __forceinline__ int tree_rows_of(const int32_t *__restrict__ node_off, int b, int n_rows, int32_t *err,
                                             bool report, int *row0) {
-    const int r0 = node_off[b], r1 = node_off[b + 1];
-    *row0 = r0;
-    if (r0 < 0 || r1 < r0 || r1 > n_rows || (b == 0 && r0 != 0)) {
-        if (report) raise_flag(err, MSA_FLAG_BOUNDS);
+    int r1;
+    const int32_t flag = tree_range(node_off, b, n_rows, row0, &r1);
+    if (flag) {
+        if (report) raise_flag(err, flag);
         return 0;
     }
-    if (r1 - r0 > 64) {
-        if (report) raise_flag(err, MSA_FLAG_UNSUPPORTED);
-        return 0;
-    }
-    return r1 - r0;
+    return r1 - *row0;
 }
 
 // ------------------------------------------------------------------ misc

@@ -448,7 +448,8 @@ msa_status_t msa_sparse_attn_decode_noalloc(const void *q, const void *k_cache, 
  *                 an ancestor of the row or the row itself; 0 for padding rows
  * A bad node_off or parent, a negative context or a position past max_blocks * 128
  * raises MSA_FLAG_BOUNDS, more than 64 nodes MSA_FLAG_UNSUPPORTED; the rows of that
- * request are then written as padding.
+ * request are then written as padding, and so is every row that a bad node_off
+ * leaves to no request.
  */
 msa_status_t msa_tree_rows(const int32_t *node_off, const int32_t *parents, const int32_t *ctx_lens, int32_t n_rows,
                            int32_t n_req, const msa_dims_t *dims, int32_t *q_req, int32_t *q_pos, uint64_t *anc,

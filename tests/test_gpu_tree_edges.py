@@ -279,3 +279,65 @@ def test_seen_nonfinite_values_of_no_weight(msa, bad, nodes, ctx):
     want[:, :, 7] = True
     want[1] = False
     assert torch.equal(hit, want) and bool(torch.isfinite(lse).all())
+
+
+# ------------------------------------------------------------------ layouts that are refused
+
+@pytest.mark.parametrize("off,good", [
+    ([1, 5, 9], (5, 9)),            # does not begin at 0
+    ([7, 5, 9], (5, 9)),
+    ([0, 12, 9], ()),               # past the rows, then down
+    ([0, 5, 10], (0, 5)),           # past the rows
+    ([0, 5, 3], (0, 5)),            # down
+    ([-3, 5, 9], (5, 9)),           # below 0
+    ([0, -2, 4], ()),
+    ([2, 2, 2], ()),                # no node at all, but rows before the first request
+    ([20, 30, 40], ()),
+    ([-3, -3, -3], ()),
+    ([0, 5, 12, 9], (0, 5)),        # past the rows, then down, behind a good one
+])
+def test_every_row_of_a_bad_layout_is_written(msa, off, good):
+    """Rows that a bad node_off leaves to no good request are padding, whatever the buffers held: the calls that follow
+    read them."""
+    ctx = [10, 20, 30][:len(off) - 1]
+    old = [torch.full((9,), 77, dtype=d, device=DEV) for d in (torch.int32, torch.int32, torch.int64)]
+    par = torch.arange(9, dtype=torch.int32) - 1 - (good[0] if good else 0)
+    if good:
+        par[good[0]] = -1
+    err = msa.new_err_word(DEV)
+    q_req, q_pos, anc = msa.msa_tree_rows(torch.tensor(off, dtype=torch.int32, device=DEV), par.to(DEV),
+                                          torch.tensor(ctx, dtype=torch.int32, device=DEV),
+                                          msa.Dims(16, 2, 128, 64, 4, 3), *old, err_word=err)
+    with pytest.raises(msa.MsaError, match="BOUNDS"):
+        msa.msa_check(err)
+    b = off.index(good[0]) if good else 0
+    for r in range(9):
+        mine = bool(good) and good[0] <= r < good[1]
+        k = r - good[0] if mine else 0
+        assert int(q_req[r]) == (b if mine else -1), r
+        assert int(q_pos[r]) == (ctx[b] + k if mine else 0), r
+        assert int(anc[r]) == ((2 << k) - 1 if mine else 0), r
+
+
+def test_a_refused_request_among_many(msa):
+    """One request with too many nodes in the middle of 40,000 rows, and padding behind the last."""
+    counts = [40] * 1000
+    counts[819] = 70                                             # rows 32,760 to 32,829
+    off = [0]
+    for n in counts:
+        off.append(off[-1] + n)
+    R = off[-1] + 100
+    node = torch.cat([torch.arange(n) for n in counts] + [torch.zeros(100, dtype=torch.long)])
+    req = torch.cat([torch.full((n,), b) for b, n in enumerate(counts)] + [torch.full((100,), -1)])
+    req[off[819]:off[820]] = -1
+    old = [torch.full((R,), 77, dtype=d, device=DEV) for d in (torch.int32, torch.int32, torch.int64)]
+    err = msa.new_err_word(DEV)
+    q_req, q_pos, anc = msa.msa_tree_rows(torch.tensor(off, dtype=torch.int32, device=DEV), (node - 1).int().to(DEV),
+                                          torch.arange(1000, dtype=torch.int32, device=DEV),
+                                          msa.Dims(16, 2, 128, 64, 4, 9), *old, err_word=err)
+    with pytest.raises(msa.MsaError, match="UNSUPPORTED"):
+        msa.msa_check(err)
+    live = req >= 0
+    assert torch.equal(q_req.cpu().long(), req)
+    assert torch.equal(q_pos.cpu().long(), torch.where(live, req + node, 0))
+    assert torch.equal(anc.cpu(), torch.where(live, (2 << node.clamp(max=61)) - 1, 0))
