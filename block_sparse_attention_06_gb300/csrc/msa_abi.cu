@@ -536,6 +536,8 @@ msa_status_t msa_sparse_attn_tree(const void *q, const void *k_cache, const void
         return fail(MSA_ERR_UNSUPPORTED, "msa_sparse_attn_tree: n_req > %d", kTreeMaxRequests);
     if (1.0 * n_rows * s.G * s.topk > 2147483647.0)
         return fail(MSA_ERR_UNSUPPORTED, "msa_sparse_attn_tree: more than 2^31 selected blocks");
+    if (1LL * n_req * s.G > 1 << 24)   // 64 nodes each: their numbers' places are kept in 30 bits
+        return fail(MSA_ERR_UNSUPPORTED, "msa_sparse_attn_tree: n_req * G > 2^24");
     if (misaligned16({q, k_cache, v_cache, k_new, v_new, out, workspace}))
         return fail(MSA_ERR_INVALID_ARG, "msa_sparse_attn_tree: tensors and workspace must be 16-byte aligned");
     const size_t need = tree_workspace_bytes(n_rows, n_req, s);

@@ -490,7 +490,7 @@ msa_status_t msa_tree_index_score(const void *q_idx, const void *kidx_cache, con
  * What a row does not see does not reach its result, whatever its bits (unwritten
  * page tails, other branches, padding rows).  A block id >= max_blocks, or a page
  * outside [0, n_pages) of a block that holds cached tokens, raises MSA_FLAG_BOUNDS.
- * Limits: max_blocks <= 16384; all tensors 16-byte aligned.
+ * Limits: max_blocks <= 16384, n_req * G <= 2^24; all tensors 16-byte aligned.
  */
 msa_status_t msa_sparse_attn_tree(const void *q, const void *k_cache, const void *v_cache, const void *k_new,
                                   const void *v_new, const int32_t *block_table, const int32_t *ctx_lens,

@@ -172,3 +172,12 @@ def test_reference_verification_keeps_the_targets_distribution():
                         mass[tok] += w / N ** 3
     # the grid's own error: at most one cell per comparison
     assert bool(((mass - p[0].double()).abs() <= 3 / N).all()) and float(mass[3]) == 0.0
+
+
+def test_attention_refuses_more_requests_and_groups_than_its_records_number(lib):  # noqa: F811
+    """A (request, group)'s place in the workspace is kept in 30 bits, 64 nodes each."""
+    big = dict(n_rows=1, n_req=65535, n_pages=1)
+    assert _attn(lib, good_dims(Hq=4 * 257, G=257, topk=1), **big) == 2
+    lib.msa_workspace_bytes.restype = ctypes.c_size_t
+    small = good_dims(Hq=4 * 256, G=256, topk=1)
+    assert _attn(lib, small, **big, ws_bytes=ctypes.c_size_t(0)) == 6   # 2^24 - 256 of them: only the workspace is short
