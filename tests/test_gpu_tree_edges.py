@@ -341,3 +341,58 @@ def test_a_refused_request_among_many(msa):
     assert torch.equal(q_req.cpu().long(), req)
     assert torch.equal(q_pos.cpu().long(), torch.where(live, req + node, 0))
     assert torch.equal(anc.cpu(), torch.where(live, (2 << node.clamp(max=61)) - 1, 0))
+
+
+# ------------------------------------------------------------------ a step against a sequential decode, to the rounding
+
+def test_tree_step_and_decode_within_the_rounding(msa):
+    """The attention of every accepted node, from the tree and from decoding its path token by token, lies within the
+    roundings of the 64-bit result over the selection that both made; a reference without one drafted token on the
+    path, or with another value for it, does not."""
+    t = T.make_tree([700, 250, 0, 126], [9, 20, 4, 12], 105, extra_blocks=1)
+    Hq, G, D, Di, topk = 16, 2, 128, 64, 4
+    dims = msa.Dims(Hq, G, D, Di, topk, t.max_blocks)
+    q, kc, vc, kn, vn = _inputs(t, Hq, G, D, 106)
+    qi, ic, ixn = T.bf16((t.n_rows, G, Di), 111), T.bf16((t.n_pages, 128, G, Di), 112), T.bf16((t.n_rows, G, Di), 113)
+    off, par, ctx, bt, _ = t.dev(DEV)
+    step = msa.TreeStep(dims, t.n_rows, 4, DEV)
+    step.layout(off, par, ctx)
+    dev = [v.to(DEV) for v in (kn, vn, ixn, kc, vc, ic)]
+    out, lse = step.attend(q.to(DEV), qi.to(DEV), *dev, bt)
+    msa.msa_check(step.err)
+    sel = step.sel.cpu()
+    x = [q, kc, vc, kn, vn]
+    _check(t, out, lse, x, sel, D)
+    # the deepest path of each tree, appended and decoded token by token
+    ro, rl, bo, bl = T.ref_attend(t, *x, sel, D ** -0.5)
+    dec = msa.DecodeStep(dims, 1, 1, t.n_pages, DEV)
+    nodes = []
+    for b in range(4):
+        best = max(t.rows(b), key=lambda r: t.depth[r])
+        rows = [r for r in t.rows(b) if t.anc[best] >> (r - t.off[b]) & 1]
+        nodes += rows[-1:] if len(rows) > 2 else []
+        for k, r in enumerate(rows):
+            page, at = int(t.block_table[b, (t.ctx[b] + k) // 128]), (t.ctx[b] + k) % 128
+            for c, n in zip(dev[3:], dev[:3]):
+                c[page, at] = n[r]
+            n = torch.tensor([t.ctx[b] + k + 1], dtype=torch.int32, device=DEV)
+            o, s = dec(q[r:r + 1].to(DEV), qi[r:r + 1].to(DEV), *dev[3:], bt[b:b + 1].contiguous(), n)
+            msa.msa_check(dec.err)
+            assert torch.equal(dec.sel[0].cpu(), sel[r])
+            T.assert_within(o[0], ro[r], bo[r], "decoded out")
+            T.assert_within(s[0], rl[r], bl[r], "decoded lse")
+    # mistakes planted in the reference
+    assert len(nodes) >= 3
+    for what in ("dropped", "value"):
+        for r in nodes:
+            b = t.q_req()[r]
+            up = t.off[b] + t.parents[r]
+            bad = T.Tree(t.off, t.parents, t.ctx, t.depth, list(t.anc), t.block_table, t.n_pages)
+            vn2 = vn.clone()
+            if what == "dropped":
+                bad.anc[r] &= ~(1 << t.parents[r])
+            else:
+                vn2[up] += 1
+            o2, l2, _, _ = T.ref_attend(bad, q, kc, vc, kn, vn2, sel, D ** -0.5)
+            miss = (out[r].cpu().double() - o2[r]).abs() > bo[r]
+            assert bool(miss.any()), (what, r)
