@@ -8,17 +8,19 @@
 // group, up to 256 / HPG nodes) is a tile, its items are the selected blocks (each with the word of the nodes that
 // selected it) and one item for the drafted tokens, and each item's K and V are read once for all nodes of the
 // tile.  With up to 128 rows in a tile that read bounds the loop (8 x 60,000 tokens of 16 nodes: 174 MB in 26 us,
-// 6.6 TB/s; 47 us with the plan, the first loads, the last output and the join).  With two halves of 128 rows it
-// is the chain S, softmax, P V of each half, 1.7 us for a unit, that bounds it (64 nodes: 499 MB, 138 us in all;
+// 6.6 TB/s; 48 us with the plan, the first loads, the last output and the join).  With two halves of 128 rows it
+// is the chain S, softmax, P V of each half, 1.7 us for a unit, that bounds it (64 nodes: 499 MB, 140 us in all;
 // the same time with every page in L2).
 //
 // k_tree_plan, one CTA per (request, group): the union through a bitmap over blocks in shared memory, ranked by
-// popcounts, hence the same whatever order its threads run in.  With HPG = 8 and more than 16 nodes, nodes of like
-// selections become neighbours: they are ordered by the least hash of their blocks that not most nodes have, which
-// is the same for two nodes the more likely the more of their blocks they share.  Tiles then have smaller unions,
-// and the 128-row halves of a tile skip the items that none of their nodes selected (8 x 60,000 tokens, 64 nodes
-// that share windows of 7 blocks by fives: 147 us, and 233 in the trees' own order). A tile's items are then
-// merged so that the halves take turns (143 us).
+// popcounts, hence the same whatever order its threads run in.  With HPG = 8 and more than 16 nodes the nodes' order
+// matters: a tile reads what any of its nodes selected, and its 128-row halves skip the items that none of theirs did.
+// Two orders are counted, items and units of halves together, and the cheaper one is taken: the tree's own, and one by
+// the least hash of a node's blocks that not most nodes have, which is the same for two nodes the more likely the
+// more of their blocks they share.  8 x 60,000 tokens, 64 nodes: windows of 7 blocks that nodes far apart share, 256 us
+// in the tree's own order and 137 hashed; children that keep all but one of their parent's blocks, 122 and 155 in a
+// chain, 130 and 151 with parents among the four nodes before, 138 and 138 with four children a node in breadth order
+// (counting both costs 2 us).  A tile's items are then merged so that the halves take turns (143 us, and 147 without).
 //
 // k_attn_tree, one persistent CTA per SM: the items of all tiles, in order, are cut into one range per CTA, so one
 // long tile is spread over many SMs and many short ones share them.  Leaving one tile for the next costs a CTA
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_tree_plan(
     constexpr int EPT = CAP / kPlanThreads;
     __shared__ uint32_t bits[kMaxWords];
     __shared__ uint32_t rank[kMaxWords];               // set bits below the word
-    __shared__ uint32_t nodes_of[CAP][2];              // by the nodes' numbers, then by their places
+    __shared__ uint32_t words_of[2][CAP][2];           // nodes of the union's blocks: by number, by the hashed places
     __shared__ uint16_t block_of[CAP];
     __shared__ unsigned long long in_first, in_second; // nodes whose block is ctx / 128, or the next one
     __shared__ uint32_t has[kTreeMaxNodes];            // bit 0 / 1: the node selected that block
@@ -197,7 +199,8 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_tree_plan(
     const unsigned long long path = tid < n ? anc[row0 + tid] : 0ull;
     const int words = (max_blocks + 31) >> 5;
     for (int i = tid; i < words; i += kPlanThreads) bits[i] = 0;
-    for (int i = tid; i < 2 * min(n_ent, CAP); i += kPlanThreads) (&nodes_of[0][0])[i] = 0;
+    uint32_t(*nodes_of)[2] = words_of[0];              // in the order that is taken
+    for (int i = tid; i < 2 * min(n_ent, CAP); i += kPlanThreads) (&words_of[0][0][0])[i] = (&words_of[1][0][0])[i] = 0;
     if (tid < kTreeMaxNodes) has[tid] = 0, key[tid] = ~0u;
     if (tid == 0) in_first = in_second = 0, draft_at[0] = draft_at[1] = 0;
     __syncthreads();
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_tree_plan(
     if (w1 < words) rank[w1] = before + p0;
     if (tid < n) place[tid] = uint8_t(tid);
     __syncthreads();
-    const bool sorted = HPG == 8 && n > NPM;   // (with HPG = 4, Q comes in boxes of neighbouring rows)
+    bool sorted = HPG == 8 && n > NPM;   // (with HPG = 4, Q comes in boxes of neighbouring rows)
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
         const int j = ent[x], i = (tid + x * kPlanThreads) / topk;
@@ -256,15 +259,28 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_tree_plan(
             for (int m = 0; m < n; ++m) p += key[m] < mine || (key[m] == mine && m < tid);
             place[tid] = uint8_t(p);
         }
-        for (int i = tid; i < 2 * total; i += kPlanThreads) (&nodes_of[0][0])[i] = 0;
         __syncthreads();
 #pragma unroll
         for (int x = 0; x < EPT; ++x) {
             const int k = ent[x], i = (tid + x * kPlanThreads) / topk;
             if (k < 0) continue;
             const int p = place[i];
-            atomicOr(&nodes_of[k][p >> 5], 1u << (p & 31));
+            atomicOr(&words_of[1][k][p >> 5], 1u << (p & 31));
         }
+        __syncthreads();
+        // What either order costs: tiles that read a block, and 128-row halves that it is a unit of.
+        unsigned long long cost = 0, costs;   // by number in the low word
+        for (int k = tid; k < total; k += kPlanThreads)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint32_t w = words_of[y >> 1][k][y & 1];
+                cost += (unsigned long long)((w != 0) + ((w & 0xffffu) != 0) + (w >> 16 != 0)) << (32 * (y >> 1));
+            }
+        plan_scan(cost, wsum3[0], &costs);
+        sorted = uint32_t(costs >> 32) < uint32_t(costs);
+        if (sorted) nodes_of = words_of[1];
+        else if (tid < n) place[tid] = uint8_t(tid);
+        __syncthreads();
     }
     // the drafted tokens that each node sees, and the nodes by place
     if (tid < n) {

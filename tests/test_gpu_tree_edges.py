@@ -396,3 +396,64 @@ def test_tree_step_and_decode_within_the_rounding(msa):
             o2, l2, _, _ = T.ref_attend(bad, q, kc, vc, kn, vn2, sel, D ** -0.5)
             miss = (out[r].cpu().double() - o2[r]).abs() > bo[r]
             assert bool(miss.any()), (what, r)
+
+
+# ------------------------------------------------------------------ attention: the order of a tile's nodes
+
+def _inherited(n, G, full, seed, changed):
+    """15 blocks a node: seven that all nodes have, and eight of its parent's, `changed` of them new."""
+    g = torch.Generator().manual_seed(seed)
+    rnd = lambda k: int(torch.randint(k, (1,), generator=g))
+    sel = []
+    for _ in range(G):
+        ids = torch.randperm(full, generator=g).tolist()
+        core, rest, own = ids[:7], ids[7:], []
+        for i in range(n):
+            s = list(own[i - 1]) if i else rest[:8]
+            for _ in range(changed if i else 0):
+                s[rnd(8)] = [j for j in rest if j not in s][rnd(len(rest) - 8)]
+            own.append(s)
+        sel.append([sorted(core + s) for s in own])
+    return torch.tensor(sel, dtype=torch.int32).permute(1, 0, 2)
+
+
+def _windows(n, G, full, seed):
+    """The same, but of eight blocks one after another in a pool of 96: nodes twelve apart have the same."""
+    g = torch.Generator().manual_seed(seed)
+    sel = []
+    for _ in range(G):
+        ids = torch.randperm(full, generator=g).tolist()
+        sel.append([sorted(ids[:7] + [ids[7 + (8 * i + k) % 80] for k in range(8)]) for i in range(n)])
+    return torch.tensor(sel, dtype=torch.int32).permute(1, 0, 2)
+
+
+@pytest.mark.parametrize("pattern", ["inherited", "inherited_2", "windows"])
+def test_nodes_keep_their_order_where_it_reads_less(msa, pattern):
+    """A tile reads the blocks that any of its 32 nodes selected.  Where a child keeps most of its parent's blocks the
+    tree's own order makes the smaller tiles, where like nodes lie far apart another one does; the plan's tiles are
+    never larger than those of the tree's own order."""
+    n, G, Hq, D = 64, 2, 16, 128
+    t = T.make_tree([12000, 11990], [n, n], 107, "chain")
+    full = 93
+    both = [_windows(n, G, full, 108 + b) if pattern == "windows" else
+            _inherited(n, G, full, 108 + b, 2 if pattern == "inherited_2" else 1) for b in range(2)]
+    sel = torch.full((2 * n, G, 16), -1, dtype=torch.int32)
+    sel[:, :, :15] = torch.cat(both)
+    sel[:, :, 15] = (torch.tensor(t.q_pos()) // 128)[:, None]
+    x = _inputs(t, Hq, G, D, 109)
+    dims = msa.Dims(Hq, G, D, 64, 16, t.max_blocks)
+    ws = torch.empty(msa.msa_workspace_bytes(msa.MSA_OP_TREE, 2 * n, 2, dims), dtype=torch.uint8, device=DEV)
+    off, _, ctx, bt, anc = t.dev(DEV)
+    err = msa.new_err_word(DEV)
+    out, lse = msa.msa_sparse_attn_tree(*[v.to(DEV) for v in x], bt, ctx, off, anc, sel.to(DEV), dims, workspace=ws,
+                                        err_word=err)
+    msa.msa_check(err)
+    _check(t, out, lse, x, sel, D)
+    # the plan's records: a tile's items in the first word, 2^30 for the item of the drafted tokens
+    tiles = 2 * 2 * G
+    items = ws[:16 * tiles].view(torch.int32).view(tiles, 4)[:, 0].cpu()
+    assert bool((items >> 30 == 1).all())
+    blocks = (items & (1 << 30) - 1) - 1
+    own = sum(len({int(j) for j in sel[r0:r0 + 32, g].flatten() if 0 <= int(j) * 128 < t.ctx[r0 // n]})
+              for r0 in range(0, 2 * n, 32) for g in range(G))
+    assert int(blocks.sum()) < own if pattern == "windows" else int(blocks.sum()) <= own
