@@ -457,3 +457,26 @@ def test_nodes_keep_their_order_where_it_reads_less(msa, pattern):
     own = sum(len({int(j) for j in sel[r0:r0 + 32, g].flatten() if 0 <= int(j) * 128 < t.ctx[r0 // n]})
               for r0 in range(0, 2 * n, 32) for g in range(G))
     assert int(blocks.sum()) < own if pattern == "windows" else int(blocks.sum()) <= own
+
+
+@pytest.mark.parametrize("Hq,G,D", [(16, 2, 128), (8, 1, 64)])
+@pytest.mark.parametrize("counts", [[17, 31], [33, 16], [40, 63], [48, 1]])
+def test_wide_trees_in_their_own_order(msa, counts, Hq, G, D):
+    """Selections that follow the tree, at sizes that leave a tile's second half or a second tile partly filled; the
+    rows behind each tree belong to the next one, or are padding full of NaN."""
+    t = T.make_tree([2900, 2950], counts, 110, "chain")
+    full = 22
+    sel = torch.cat([_inherited(n, G, full, 111 + b, 1) for b, n in enumerate(counts)])
+    own = (torch.tensor(t.q_pos()) // 128)[:, None, None].expand(-1, G, 1).int()
+    sel = torch.cat([sel, own], -1).contiguous()
+    x = _inputs(t, Hq, G, D, 112)
+    pad = 9
+    wide = [torch.cat([v, torch.full((pad, *v.shape[1:]), float("nan"), dtype=v.dtype)]) if i in (0, 3, 4) else v
+            for i, v in enumerate(x)]
+    off, _, ctx, bt, anc = t.dev(DEV, pad)
+    err = msa.new_err_word(DEV)
+    out, lse = msa.msa_sparse_attn_tree(*[v.to(DEV) for v in wide], bt, ctx, off, anc,
+                                        torch.cat([sel, torch.full((pad, G, 16), -1, dtype=torch.int32)]).to(DEV),
+                                        msa.Dims(Hq, G, D, 64, 16, t.max_blocks), err_word=err)
+    msa.msa_check(err)
+    _check(t, out[:t.n_rows], lse[:t.n_rows], x, sel, D)
