@@ -11,9 +11,9 @@
 // run's sum in every CTA's shared memory, and after one cluster barrier warp 0 of each CTA goes on with the
 // walk by itself, all of them with the same numbers and so the same decisions.  The next token is then
 // found in the one run that holds it.
-// 32 requests x 131,072 tokens: 38 us, about five passes of 33 MB for the slowest request (a rejection decides the next
+// 32 requests x 131,072 tokens: 39 us, about five passes of 33 MB for the slowest request (a rejection decides the next
 // test, so the passes of a request follow one another; a pass is 3 to 5 us of loads, 2 of sums and cluster barrier and 1 of the decision).
-// One request: 11 us.
+// One request of 32,000 tokens: 12 us.
 //
 // A rounding of a sum moves a border between two tokens, and the residual may be a flat tail of a row whose likely
 // token was rejected, so sums have to be good to a small part of themselves, whatever is in the row.  64-bit

@@ -488,7 +488,8 @@ msa_status_t msa_tree_index_score(const void *q_idx, const void *kidx_cache, con
  *   workspace  device scratch of msa_workspace_bytes(MSA_OP_TREE, n_rows, n_req, dims)
  *              bytes, 16-byte aligned; calls that may run at once need one each
  * What a row does not see does not reach its result, whatever its bits (unwritten
- * page tails, other branches, padding rows).  A block id >= max_blocks, or a page
+ * page tails, other branches, padding rows); what it sees with a logit of -inf weighs
+ * nothing.  A block id >= max_blocks, or a page
  * outside [0, n_pages) of a block that holds cached tokens, raises MSA_FLAG_BOUNDS.
  * Limits: max_blocks <= 16384, n_req * G <= 2^24; all tensors 16-byte aligned.
  */
@@ -525,9 +526,9 @@ msa_status_t msa_sparse_attn_tree(const void *q, const void *k_cache, const void
  * A sum over a row of p or q is off by less than (vocab / 1024 + 32) * 2^-46 of itself
  * (2^-38 of it at 131,072 tokens), whatever the row holds; with a draft distribution
  * a residual's mass is one such sum less c times another.  Comparisons in 64 bits.
- * vocab <= 2^30.  A token outside [0, vocab) or a bad
- * parent raises MSA_FLAG_BOUNDS (that node is never accepted); a row of target_probs
- * without finite positive mass raises MSA_FLAG_NAN (next_token -1).
+ * vocab <= 2^30.  A token outside [0, vocab) or a bad parent raises MSA_FLAG_BOUNDS
+ * (that node is never accepted); a row of target_probs without finite positive mass
+ * raises MSA_FLAG_NAN (next_token -1).
  */
 msa_status_t msa_verify_tree(const float *target_probs, const float *draft_probs, int32_t vocab,
                              const int32_t *tokens, const int32_t *node_off, const int32_t *parents,
