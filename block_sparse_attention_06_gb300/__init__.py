@@ -48,6 +48,20 @@ class msa_dims_t(ctypes.Structure):
                 ("max_blocks", ctypes.c_int32), ("sm_scale", ctypes.c_float)]
 
 
+class msa_cache_q8_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "k_scale", "v", "v_scale", "kidx", "kidx_scale")]
+
+
+class msa_rows_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "q_idx", "k_idx")]
+                + [(n + "_stride", ctypes.c_int64) for n in ("q", "k", "v", "q_idx", "k_idx")])
+
+
+class msa_rope_t(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("rot_idx", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("gain", ctypes.c_float), ("inv_freq", ctypes.c_void_p), ("inv_freq_idx", ctypes.c_void_p)]
+
+
 @dataclass(frozen=True)
 class Dims:
     Hq: int
@@ -98,6 +112,13 @@ def _load() -> ctypes.CDLL:
         "msa_sparse_attn_tree": [P, P, P, P, P, P, P, P, P, P, I, I, I, D, P, P, P, S, P, P],
         "msa_verify_tree": [P, P, I, P, P, P, P, P, I, I, P, P, P, P, P],
         "msa_commit_tree": [P, P, P, I, P, P, P, P, P, P, P, P, I, I, I, D, P, P, P],
+        "msa_rope_append": [P, P, P, P, P, I, I, I, D, P, P, P, P, P, P, P],
+        "msa_rope_append_q8": [P, P, P, P, P, I, I, I, D, P, P, P, P, P],
+        "msa_cache_read_q8": [P, P, P, P, I, I, I, D, P, P, P, P, P],
+        "msa_index_score_q8": [P, P, P, P, P, I, I, I, D, P, P, P],
+        "msa_sparse_attn_decode_q8": [P, P, P, P, I, I, D, P, P, P, P],
+        "msa_decode_step_q8": [P, P, P, P, P, I, I, D, P, P, P, P, P, P, P, P],
+        "msa_window_attn_q8": [P, P, P, P, P, I, I, I, I, I, D, I, P, P, P, P],
         "msa_check": [P, P],
     }
     for name, argt in sigs.items():
@@ -697,6 +718,279 @@ def msa_commit_tree(k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache, block_
     return new_lens
 
 
+# ------------------------------------------------------------------ appending, and 8-bit caches
+
+_E4M3, _E8M0, _F64 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.float64
+
+
+@dataclass(frozen=True)
+class CacheQ8:
+    """The 8-bit caches of one layer: e4m3 codes [n_pages][G][128][D] (k, v) and [n_pages][G][128][Di] (kidx), and
+    the rows' power-of-two scales, e8m0 [n_pages][G][128]; value = code * scale.  kidx may be left out where no
+    call needs it (window layers), and so may any of them that a call does not read."""
+    k: Optional[torch.Tensor]
+    k_scale: Optional[torch.Tensor]
+    v: Optional[torch.Tensor]
+    v_scale: Optional[torch.Tensor]
+    kidx: Optional[torch.Tensor] = None
+    kidx_scale: Optional[torch.Tensor] = None
+
+    @classmethod
+    def zeros(cls, dims: Dims, n_pages: int, device, index: bool = True) -> "CacheQ8":
+        """Caches of n_pages pages of zeros."""
+        line = (n_pages, dims.G, dims.page_size)
+
+        def one(width):
+            return (torch.zeros((*line, width), dtype=torch.uint8, device=device).view(_E4M3),
+                    torch.full(line, 127, dtype=torch.uint8, device=device).view(_E8M0))
+        return cls(*one(dims.D), *one(dims.D), *(one(dims.Di) if index else (None, None)))
+
+    def _struct(self, dims: Dims, dev: int, kv: bool, index: bool):
+        """(reference to the C struct, n_pages), with what the call needs checked."""
+        first = self.k if kv else self.kidx
+        n_pages = _ndim(first, 4, "cache.k" if kv else "cache.kidx", "[n_pages][G][128][width]")[0]
+        line = (n_pages, dims.G, dims.page_size)
+        p = [None] * 6
+        if kv:
+            p[0] = _arg(self.k, _E4M3, (*line, dims.D), dev, "cache.k")
+            p[1] = _arg(self.k_scale, _E8M0, line, dev, "cache.k_scale")
+            p[2] = _arg(self.v, _E4M3, (*line, dims.D), dev, "cache.v")
+            p[3] = _arg(self.v_scale, _E8M0, line, dev, "cache.v_scale")
+        if index:
+            p[4] = _arg(self.kidx, _E4M3, (*line, dims.Di), dev, "cache.kidx")
+            p[5] = _arg(self.kidx_scale, _E8M0, line, dev, "cache.kidx_scale")
+        return ctypes.byref(msa_cache_q8_t(*p)), n_pages
+
+
+def rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original_len: int = 0,
+                  beta_fast: float = 32.0, beta_slow: float = 1.0) -> Tuple[torch.Tensor, float]:
+    """Radians per position of the rot // 2 pairs (float64, CPU), and the gain, of rotary positions scaled for long
+    contexts: "none"; "linear" (positions divided by the factor); "ntk" (the base raised so that the lowest
+    frequency is divided by the factor and the highest kept); "yarn" (pairs that turn more than beta_fast times
+    over original_len positions kept, fewer than beta_slow times divided by the factor, in between blended; gain
+    0.1 ln(factor) + 1)."""
+    if rot < 0 or rot % 2:
+        raise ValueError("rot must be even and not negative")
+    if factor < 1.0:
+        raise ValueError("factor must be at least 1")
+    i = torch.arange(rot // 2, dtype=_F64)
+    if scaling == "ntk":
+        base = base * factor ** (rot / max(rot - 2, 1))
+    f = base ** (-2.0 * i / max(rot, 1))
+    if scaling in ("none", "ntk"):
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling != "yarn":
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if original_len < 1:
+        raise ValueError("yarn needs original_len")
+
+    def pair_of(turns):   # the pair that turns so often over original_len positions
+        return rot * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+    lo, hi = max(math.floor(pair_of(beta_fast)), 0), min(math.ceil(pair_of(beta_slow)), rot - 1)
+    ramp = ((i - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+    return f / factor * ramp + f * (1 - ramp), 0.1 * math.log(factor) + 1.0
+
+
+class Rope:
+    """Rotary positions of a layer's heads: of each q and k head the first `rot` components turn (pair i by
+    inv_freq[i] radians a position; float64 on the GPU), of each index vector the first `rot_idx`.  Pairs are
+    components (i, i + rot/2), or (2i, 2i + 1) where interleaved.  `gain` multiplies what turns."""
+
+    def __init__(self, rot: int, inv_freq=None, rot_idx: int = 0, inv_freq_idx=None, interleaved: bool = False,
+                 gain: float = 1.0):
+        for n, f, name in ((rot, inv_freq, "inv_freq"), (rot_idx, inv_freq_idx, "inv_freq_idx")):
+            if n < 0 or n % 16:
+                raise ValueError("rot and rot_idx must be multiples of 16")
+            if n:
+                _req(f, _F64, name, (n // 2,))
+        self.rot, self.rot_idx, self.interleaved, self.gain = rot, rot_idx, bool(interleaved), float(gain)
+        self.inv_freq, self.inv_freq_idx = inv_freq, inv_freq_idx
+
+    @classmethod
+    def of_base(cls, rot: int, rot_idx: int = 0, interleaved: bool = False, device="cuda", **scaling) -> "Rope":
+        """Frequencies of rope_inv_freq (its arguments as keywords) for both."""
+        f, gain = rope_inv_freq(rot, **scaling)
+        g, _ = rope_inv_freq(rot_idx, **scaling)
+        return cls(rot, f.to(device), rot_idx, g.to(device), interleaved, gain)
+
+    def _struct(self, dev: int):
+        p = [_arg(f, _F64, (n // 2,), dev, name) if n else None
+             for n, f, name in ((self.rot, self.inv_freq, "inv_freq"), (self.rot_idx, self.inv_freq_idx, "inv_freq_idx"))]
+        return ctypes.byref(msa_rope_t(self.rot, self.rot_idx, self.interleaved, self.gain, *p))
+
+
+def _part(t, shape, index: int, name: str):
+    """Address and row stride of rows [n][heads][width] whose heads are dense behind one another."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if (st[2] != 1 and shape[2] > 1) or (st[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a row must be dense behind one another")
+    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _append_args(q, k, v, q_idx, k_idx, q_req, q_pos, rope, dims, q_out, q_idx_out, err_word):
+    dev = _lead(q, "q")
+    n = _ndim(q, 3, "q", "[n_rows][Hq][D]")[0]
+    heads, kv, idx = (n, dims.Hq, dims.D), (n, dims.G, dims.D), (n, dims.G, dims.Di)
+    parts = [_part(q, heads, dev, "q"), _part(k, kv, dev, "k"), _part(v, kv, dev, "v")]
+    index = q_idx is not None or k_idx is not None
+    parts += [_part(q_idx, idx, dev, "q_idx"), _part(k_idx, idx, dev, "k_idx")] if index else [(None, 0)] * 2
+    q_out = torch.empty(heads, dtype=_BF16, device=q.device) if q_out is None else q_out
+    if index and q_idx_out is None:
+        q_idx_out = torch.empty(idx, dtype=_BF16, device=q.device)
+    err_word = new_err_word(q.device) if err_word is None else err_word
+    rows = ctypes.byref(msa_rows_t(*(p for p, _ in parts), *(s for _, s in parts)))
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    front = (rows, rope._struct(dev))
+    back = (_arg(q_out, _BF16, heads, dev, "q_out"),
+            _arg(q_idx_out, _BF16, idx, dev, "q_idx_out") if index else None)
+    return dev, n, index, front, back, q_out, q_idx_out if index else None, err_word
+
+
+def msa_rope_append(q, k, v, q_idx, k_idx, k_cache, v_cache, kidx_cache, block_table, q_req, q_pos, rope: Rope,
+                    dims: Dims, q_out=None, q_idx_out=None, err_word=None):
+    """Rotate a layer's new rows to their positions and append k, v and k_idx to its bf16 caches -> (q, q_idx)
+    rotated.  Row r is the token at q_pos[r] of request q_req[r] (-1: a padding row, nothing of it is written).
+    The rows may be parts of one wider tensor (any row stride); q_idx, k_idx and kidx_cache may be None."""
+    dev, n, index, front, back, q_out, q_idx_out, err_word = _append_args(
+        q, k, v, q_idx, k_idx, q_req, q_pos, rope, dims, q_out, q_idx_out, err_word)
+    n_req = _ndim(block_table, 2, "block_table", "[n_req][max_blocks]")[0]
+    n_pages = _ndim(k_cache, 4, "k_cache", "[n_pages][128][G][D]")[0]
+    page = (n_pages, dims.page_size, dims.G)
+    _launch(dev, "msa_rope_append", *front, _arg(block_table, _I32, (n_req, dims.max_blocks), dev, "block_table"),
+            _arg(q_req, _I32, (n,), dev, "q_req"), _arg(q_pos, _I32, (n,), dev, "q_pos"), n, n_req, n_pages, dims.ref(),
+            *back, _arg(k_cache, _BF16, (*page, dims.D), dev, "k_cache"),
+            _arg(v_cache, _BF16, (*page, dims.D), dev, "v_cache"),
+            _arg(kidx_cache, _BF16, (*page, dims.Di), dev, "kidx_cache") if index else None,
+            _arg(err_word, _I32, (1,), dev, "err_word"))
+    return q_out, q_idx_out
+
+
+def msa_rope_append_q8(q, k, v, q_idx, k_idx, cache: CacheQ8, block_table, q_req, q_pos, rope: Rope, dims: Dims,
+                       q_out=None, q_idx_out=None, err_word=None):
+    """msa_rope_append into 8-bit caches (quantised as they are written) -> (q, q_idx) rotated."""
+    dev, n, index, front, back, q_out, q_idx_out, err_word = _append_args(
+        q, k, v, q_idx, k_idx, q_req, q_pos, rope, dims, q_out, q_idx_out, err_word)
+    n_req = _ndim(block_table, 2, "block_table", "[n_req][max_blocks]")[0]
+    c, n_pages = cache._struct(dims, dev, True, index)
+    _launch(dev, "msa_rope_append_q8", *front, _arg(block_table, _I32, (n_req, dims.max_blocks), dev, "block_table"),
+            _arg(q_req, _I32, (n,), dev, "q_req"), _arg(q_pos, _I32, (n,), dev, "q_pos"), n, n_req, n_pages, dims.ref(),
+            *back, c, _arg(err_word, _I32, (1,), dev, "err_word"))
+    return q_out, q_idx_out
+
+
+def msa_cache_read_q8(cache: CacheQ8, block_table, out_table, lens, dims: Dims, k_cache, v_cache, kidx_cache=None,
+                      err_word=None):
+    """Blocks of 8-bit caches as bf16 pages, exactly -> (k_cache, v_cache, kidx_cache): block j of request b goes to
+    page out_table[b][j] (-1: not wanted), its tokens below lens[b] only.  With out_table as block table and these
+    caches the prefill calls run on what the 8-bit caches hold."""
+    dev = _lead(k_cache, "k_cache")
+    n_req = _ndim(block_table, 2, "block_table", "[n_req][max_blocks]")[0]
+    n_out = _ndim(k_cache, 4, "k_cache", "[n_out_pages][128][G][D]")[0]
+    page, table = (n_out, dims.page_size, dims.G), (n_req, dims.max_blocks)
+    err_word = new_err_word(k_cache.device) if err_word is None else err_word
+    c, n_pages = cache._struct(dims, dev, True, kidx_cache is not None)
+    _launch(dev, "msa_cache_read_q8", c, _arg(block_table, _I32, table, dev, "block_table"),
+            _arg(out_table, _I32, table, dev, "out_table"), _arg(lens, _I32, (n_req,), dev, "lens"), n_req, n_pages, n_out,
+            dims.ref(), _arg(k_cache, _BF16, (*page, dims.D), dev, "k_cache"),
+            _arg(v_cache, _BF16, (*page, dims.D), dev, "v_cache"),
+            None if kidx_cache is None else _arg(kidx_cache, _BF16, (*page, dims.Di), dev, "kidx_cache"),
+            _arg(err_word, _I32, (1,), dev, "err_word"))
+    return k_cache, v_cache, kidx_cache
+
+
+def msa_index_score_q8(q_idx, cache: CacheQ8, block_table, q_req, q_pos, dims: Dims, scores=None, err_word=None):
+    """Block scores of decode rows over 8-bit index keys: msa_index_score with MSA_PHASE_DECODE."""
+    dev = _lead(q_idx, "q_idx")
+    n = _ndim(q_idx, 3, "q_idx", "[n_rows][G][Di]")[0]
+    n_req = _ndim(block_table, 2, "block_table", "[n_req][max_blocks]")[0]
+    shape = (n, dims.G, dims.max_blocks)
+    scores = torch.empty(shape, dtype=_F32, device=q_idx.device) if scores is None else scores
+    err_word = new_err_word(q_idx.device) if err_word is None else err_word
+    c, n_pages = cache._struct(dims, dev, False, True)
+    _launch(dev, "msa_index_score_q8", _arg(q_idx, _BF16, (n, dims.G, dims.Di), dev, "q_idx"), c,
+            _arg(block_table, _I32, (n_req, dims.max_blocks), dev, "block_table"), _arg(q_req, _I32, (n,), dev, "q_req"),
+            _arg(q_pos, _I32, (n,), dev, "q_pos"), n, n_req, n_pages, dims.ref(), _arg(scores, _F32, shape, dev, "scores"),
+            _arg(err_word, _I32, (1,), dev, "err_word"))
+    return scores
+
+
+def msa_sparse_attn_decode_q8(q, cache: CacheQ8, page_table, row_len, dims: Dims, out=None, lse=None, err_word=None):
+    """Decode attention over 8-bit caches and per-(request, group) page tables -> (out, lse): msa_sparse_attn_decode,
+    without a workspace."""
+    dev = _lead(q, "q")
+    B = _ndim(q, 3, "q", "[B][Hq][D]")[0]
+    heads = (B, dims.Hq, dims.D)
+    out = torch.empty(heads, dtype=_BF16, device=q.device) if out is None else out
+    lse = torch.empty(heads[:2], dtype=_F32, device=q.device) if lse is None else lse
+    err_word = new_err_word(q.device) if err_word is None else err_word
+    c, n_pages = cache._struct(dims, dev, True, False)
+    _launch(dev, "msa_sparse_attn_decode_q8", _arg(q, _BF16, heads, dev, "q"), c,
+            _arg(page_table, _I32, (B * dims.G, dims.topk), dev, "page_table"),
+            _arg(row_len, _I32, (B * dims.G,), dev, "row_len"), B, n_pages, dims.ref(), _arg(out, _BF16, heads, dev, "out"),
+            _arg(lse, _F32, heads[:2], dev, "lse"), _arg(err_word, _I32, (1,), dev, "err_word"))
+    return out, lse
+
+
+def msa_decode_step_q8(q, q_idx, cache: CacheQ8, block_table, seq_lens, dims: Dims, scores=None, sel=None,
+                       page_table=None, row_len=None, out=None, lse=None, err_word=None):
+    """One whole decode step over 8-bit caches (index scan, top-k, page tables, attention) in one call -> (out, lse,
+    sel, page_table, row_len, scores); out and lse may be page-locked host memory."""
+    dev = _lead(q, "q")
+    B = _ndim(q, 3, "q", "[B][Hq][D]")[0]
+    heads, f = (B, dims.Hq, dims.D), dict(device=q.device)
+    scores = torch.empty((B, dims.G, dims.max_blocks), dtype=_F32, **f) if scores is None else scores
+    sel = torch.empty((B, dims.G, dims.topk), dtype=_I32, **f) if sel is None else sel
+    page_table = torch.empty((B * dims.G, dims.topk), dtype=_I32, **f) if page_table is None else page_table
+    row_len = torch.empty((B * dims.G,), dtype=_I32, **f) if row_len is None else row_len
+    out = torch.empty(heads, dtype=_BF16, **f) if out is None else out
+    lse = torch.empty(heads[:2], dtype=_F32, **f) if lse is None else lse
+    err_word = new_err_word(q.device) if err_word is None else err_word
+    c, n_pages = cache._struct(dims, dev, True, True)
+    res = [t.data_ptr() if t.is_cuda is False and _req_result(t, dt, name, shape) is t else _arg(t, dt, shape, dev, name)
+           for t, dt, name, shape in ((out, _BF16, "out", heads), (lse, _F32, "lse", heads[:2]))]
+    _launch(dev, "msa_decode_step_q8", _arg(q, _BF16, heads, dev, "q"),
+            _arg(q_idx, _BF16, (B, dims.G, dims.Di), dev, "q_idx"), c,
+            _arg(block_table, _I32, (B, dims.max_blocks), dev, "block_table"),
+            _arg(seq_lens, _I32, (B,), dev, "seq_lens"), B, n_pages, dims.ref(),
+            _arg(scores, _F32, (B, dims.G, dims.max_blocks), dev, "scores"),
+            _arg(sel, _I32, (B, dims.G, dims.topk), dev, "sel"),
+            _arg(page_table, _I32, (B * dims.G, dims.topk), dev, "page_table"),
+            _arg(row_len, _I32, (B * dims.G,), dev, "row_len"), *res, _arg(err_word, _I32, (1,), dev, "err_word"))
+    return out, lse, sel, page_table, row_len, scores
+
+
+def msa_window_attn_q8(q, cache: CacheQ8, block_table, q_req, q_pos, window: int, n_sink: int, dims: Dims, phase: int,
+                       out=None, lse=None, err_word=None):
+    """Attention over 8-bit caches of each row (the token at q_pos[r] of request q_req[r]; -1: padding, nothing of it
+    is written) to the last `window` tokens and the first n_sink -> (out, lse).  phase: MSA_PHASE_DECODE (single rows)
+    or MSA_PHASE_PREFILL (chunks)."""
+    dev = _lead(q, "q")
+    n = _ndim(q, 3, "q", "[n_rows][Hq][D]")[0]
+    n_req = _ndim(block_table, 2, "block_table", "[n_req][max_blocks]")[0]
+    heads = (n, dims.Hq, dims.D)
+    out = torch.empty(heads, dtype=_BF16, device=q.device) if out is None else out
+    lse = torch.empty(heads[:2], dtype=_F32, device=q.device) if lse is None else lse
+    err_word = new_err_word(q.device) if err_word is None else err_word
+    c, n_pages = cache._struct(dims, dev, True, False)
+    _launch(dev, "msa_window_attn_q8", _arg(q, _BF16, heads, dev, "q"), c,
+            _arg(block_table, _I32, (n_req, dims.max_blocks), dev, "block_table"), _arg(q_req, _I32, (n,), dev, "q_req"),
+            _arg(q_pos, _I32, (n,), dev, "q_pos"), n, n_req, n_pages, window, n_sink, dims.ref(), phase,
+            _arg(out, _BF16, heads, dev, "out"), _arg(lse, _F32, heads[:2], dev, "lse"),
+            _arg(err_word, _I32, (1,), dev, "err_word"))
+    return out, lse
+
+
 # ------------------------------------------------------------------ whole-path helpers
 
 def dims_of(case) -> Dims:
@@ -1008,6 +1302,62 @@ class MixedStep:
         self.prefill(pre_q, pre_q_idx, k_cache, v_cache, kidx_cache, pre_block_table, pre_q_req, pre_q_pos)
         main.wait_stream(self._side)                 # the decode results are complete on the caller's stream
         return self.decode.out, self.decode.lse, self.prefill.out, self.prefill.lse
+
+
+class DecodeStepQ8:
+    """A decode step over 8-bit caches with preallocated buffers: step() takes one new row per request as the
+    projections give them, rotates it to q_pos, appends it to the caches and attends; append() and the call itself
+    are its two halves.  capture() records a step() into a CUDA graph and replay() reruns it on what its tensors
+    then hold.  Steps that may run at once need a DecodeStepQ8 each."""
+
+    def __init__(self, dims: Dims, B: int, device, rope: Optional[Rope] = None):
+        self.dims, self.B, self.rope = dims, B, rope
+        f = dict(device=device)
+        self.q = torch.empty((B, dims.Hq, dims.D), dtype=torch.bfloat16, **f)
+        self.q_idx = torch.empty((B, dims.G, dims.Di), dtype=torch.bfloat16, **f)
+        self.scores = torch.empty((B, dims.G, dims.max_blocks), dtype=torch.float32, **f)
+        self.sel = torch.empty((B, dims.G, dims.topk), dtype=torch.int32, **f)
+        self.page_table = torch.empty((B * dims.G, dims.topk), dtype=torch.int32, **f)
+        self.row_len = torch.empty((B * dims.G,), dtype=torch.int32, **f)
+        self.out = torch.empty((B, dims.Hq, dims.D), dtype=torch.bfloat16, **f)
+        self.lse = torch.empty((B, dims.Hq), dtype=torch.float32, **f)
+        self.q_req = torch.arange(B, dtype=torch.int32, **f)
+        self.err = new_err_word(device)
+        self.kernel_launches = 4   # append, index scan, selection (top-k + page table), attention
+
+    def append(self, q, k, v, q_idx, k_idx, cache: CacheQ8, block_table, q_pos):
+        """Row b is the token at q_pos[b] of request b -> (q, q_idx) rotated, in the step's buffers."""
+        rope = self.rope if self.rope is not None else Rope(0)
+        return msa_rope_append_q8(q, k, v, q_idx, k_idx, cache, block_table, self.q_req, q_pos, rope, self.dims, self.q,
+                                  self.q_idx, err_word=self.err)
+
+    def __call__(self, q, q_idx, cache: CacheQ8, block_table, seq_lens, out=None, lse=None):
+        """Index scan, selection and attention of rows that are in the caches already (seq_lens counts them)."""
+        out, lse = self.out if out is None else out, self.lse if lse is None else lse
+        msa_decode_step_q8(q, q_idx, cache, block_table, seq_lens, self.dims, self.scores, self.sel, self.page_table,
+                           self.row_len, out, lse, err_word=self.err)
+        return out, lse
+
+    def step(self, q, k, v, q_idx, k_idx, cache: CacheQ8, block_table, q_pos, seq_lens):
+        """append() of the new rows, then the step over caches that hold them: seq_lens = q_pos + 1."""
+        self.append(q, k, v, q_idx, k_idx, cache, block_table, q_pos)
+        return self(self.q, self.q_idx, cache, block_table, seq_lens)
+
+    def capture(self, q, k, v, q_idx, k_idx, cache: CacheQ8, block_table, q_pos, seq_lens):
+        """Record step() on these tensors (one eager step runs first); write new values into them, then replay()."""
+        args = (q, k, v, q_idx, k_idx, cache, block_table, q_pos, seq_lens)
+        self.step(*args)
+        torch.cuda.synchronize(q.device)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            self.step(*args)
+        self._graph, self._graph_args = graph, args
+        return graph
+
+    def replay(self):
+        """Replay the captured step on the current stream -> its (out, lse)."""
+        self._graph.replay()
+        return self.out, self.lse
 
 
 class TreeStep:

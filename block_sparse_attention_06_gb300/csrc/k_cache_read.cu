@@ -1,0 +1,95 @@
+// 8-bit pages read back as bf16 pages: value = code * 2^(b - 127), a bf16 number already, so nothing is
+// rounded.  The prefill kernels take bf16 pages; a chunk's context is read back once per layer and chunk.
+//
+// Pure streaming: 16 codes (16 bytes) per lane and load, 32 bytes per lane and store.  Lanes follow the
+// output's order ([token][group][width]), so a warp stores whole lines; its loads are runs of `width` bytes.
+#include "msa_internal.h"
+#include "msa_q8.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Args {
+    const uint8_t *code[3], *scale[3];
+    uint8_t *out[3];
+    const int32_t *bt_in, *bt_out, *lens;
+    int n_pages, n_pages_out, max_blocks, G, width[3];
+    int32_t *err;
+};
+
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t codes, float s) {
+    const float2 f = unpack_e4m3x2(codes);
+    return pack_bf16x2(f.x * s, f.y * s);
+}
+
+__global__ void __launch_bounds__(kThreads) k_cache_read(const __grid_constant__ Args a) {
+    const int b = blockIdx.x / a.max_blocks, j = blockIdx.x - b * a.max_blocks;
+    const int which = blockIdx.y;
+    const int to = a.bt_out[blockIdx.x];
+    const int n_tok = min(128, a.lens[b] - j * 128);
+    if (to < 0 || n_tok <= 0) return;
+    const int from = a.bt_in[blockIdx.x];
+    if (from < 0 || from >= a.n_pages || to >= a.n_pages_out) {
+        if (threadIdx.x == 0 && which == 0) raise_flag(a.err, MSA_FLAG_BOUNDS);
+        return;
+    }
+    const int width = a.width[which], cpv = width >> 4, per_tok = a.G * cpv;   // chunks of 16 per vector, per token
+    const uint8_t *code = a.code[which] + size_t(from) * a.G * 128 * width;
+    const uint8_t *scale = a.scale[which] + size_t(from) * a.G * 128;
+    uint8_t *out = a.out[which] + size_t(to) * 128 * a.G * width * 2;
+    const int n = n_tok * per_tok;
+    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kThreads) {
+        uint4 w[4];
+        float s[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i < n) {
+                const int t = i / per_tok, g = (i - t * per_tok) / cpv, c = i - t * per_tok - g * cpv;
+                w[u] = ldg_stream_v4(code + (size_t(g) * 128 + t) * width + c * 16);
+                s[u] = q8_scale(__ldg(scale + g * 128 + t));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i < n) {
+                uint4 *p = reinterpret_cast<uint4 *>(out + size_t(i) * 32);
+                p[0] = make_uint4(bf16_pair(w[u].x, s[u]), bf16_pair(w[u].x >> 16, s[u]), bf16_pair(w[u].y, s[u]),
+                                  bf16_pair(w[u].y >> 16, s[u]));
+                p[1] = make_uint4(bf16_pair(w[u].z, s[u]), bf16_pair(w[u].z >> 16, s[u]), bf16_pair(w[u].w, s[u]),
+                                  bf16_pair(w[u].w >> 16, s[u]));
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_read(const CacheQ8 &c, const int32_t *bt_in, const int32_t *bt_out, const int32_t *lens,
+                              int n_req, int n_pages, int n_pages_out, const Shape &s, void *k, void *v, void *kidx,
+                              int32_t *err, cudaStream_t st) {
+    Args a = {};
+    const void *code[3] = {c.k, c.v, c.kidx}, *scale[3] = {c.k_scale, c.v_scale, c.kidx_scale};
+    void *out[3] = {k, v, kidx};
+    for (int i = 0; i < 3; ++i) {
+        a.code[i] = static_cast<const uint8_t *>(code[i]);
+        a.scale[i] = static_cast<const uint8_t *>(scale[i]);
+        a.out[i] = static_cast<uint8_t *>(out[i]);
+        a.width[i] = i == 2 ? s.Di : s.D;
+    }
+    a.bt_in = bt_in;
+    a.bt_out = bt_out;
+    a.lens = lens;
+    a.n_pages = n_pages;
+    a.n_pages_out = n_pages_out;
+    a.max_blocks = s.max_blocks;
+    a.G = s.G;
+    a.err = err;
+    return launch_kernel(k_cache_read, dim3(unsigned(n_req) * unsigned(s.max_blocks), kidx ? 3u : 2u), dim3(kThreads), 0,
+                         st, false, a);
+}
+
+}  // namespace msa

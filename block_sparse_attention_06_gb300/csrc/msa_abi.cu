@@ -87,6 +87,7 @@ msa_status_t check_dims(const msa_dims_t *d, bool need_attn, bool need_index, Sh
     } while (0)
 
 constexpr int kTreeMaxRequests = 65535;   // requests are a grid dimension of the tree calls
+constexpr long long kQ8MaxRows = 1 << 26;   // (row, group) pairs: clusters of up to 16 CTAs of one grid dimension
 
 bool misaligned16(std::initializer_list<const void *> ps) {
     uintptr_t bits = 0;
@@ -590,6 +591,221 @@ msa_status_t msa_commit_tree(const void *k_new, const void *v_new, const void *k
     return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_commit_tree");
 }
 
+// The codes and scales that an operation needs, and their alignment.
+static msa_status_t check_cache_q8(const msa_cache_q8_t *c, bool kv, bool index, CacheQ8 *out, const char *who) {
+    MSA_REQUIRE(c, "%s: NULL cache", who);
+    *out = CacheQ8{c->k, c->k_scale, c->v, c->v_scale, c->kidx, c->kidx_scale};
+    MSA_REQUIRE(!kv || (c->k && c->k_scale && c->v && c->v_scale), "%s: NULL pointer in the cache", who);
+    MSA_REQUIRE(!index || (c->kidx && c->kidx_scale), "%s: NULL pointer in the cache", who);
+    MSA_REQUIRE(!misaligned16({kv ? c->k : nullptr, kv ? c->v : nullptr, index ? c->kidx : nullptr}),
+                "%s: codes must be 16-byte aligned", who);
+    const uintptr_t sc = (kv ? reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale) : 0) |
+                         (index ? reinterpret_cast<uintptr_t>(c->kidx_scale) : 0);
+    MSA_REQUIRE((sc & 3u) == 0, "%s: scales must be 4-byte aligned", who);
+    return MSA_OK;
+}
+
+static msa_status_t rope_append(const msa_rows_t *rows, const msa_rope_t *rope, const int32_t *block_table,
+                                const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
+                                int32_t n_pages, const msa_dims_t *dims, void *q_out, void *q_idx_out,
+                                void *const (&dst)[3], void *const (&scale)[3], int32_t *err_word, msa_stream_t stream,
+                                const char *who) {
+    MSA_REQUIRE(rows && rope, "%s: NULL rows or rope", who);
+    const bool index = rows->q_idx || rows->k_idx;
+    Shape s;
+    msa_status_t st = check_dims(dims, true, index, &s, who);
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(n_rows >= 0 && n_req > 0 && n_pages > 0, "%s: bad sizes", who);
+    MSA_REQUIRE(rope->rot >= 0 && rope->rot <= s.D && rope->rot_idx >= 0 && (!index || rope->rot_idx <= s.Di),
+                "%s: rot outside the head", who);
+    if (rope->rot % 16 || rope->rot_idx % 16) return fail(MSA_ERR_UNSUPPORTED, "%s: rot must be a multiple of 16", who);
+    MSA_REQUIRE(rope->interleaved == 0 || rope->interleaved == 1, "%s: interleaved must be 0 or 1", who);
+    if (n_rows == 0) return MSA_OK;
+    MSA_REQUIRE(rows->q && rows->k && rows->v && block_table && q_req && q_pos && q_out && dst[0] && dst[1] && err_word,
+                "%s: NULL pointer", who);
+    MSA_REQUIRE(!index || (rows->q_idx && rows->k_idx && q_idx_out && dst[2]), "%s: NULL pointer of the index", who);
+    MSA_REQUIRE((rope->rot == 0 || rope->inv_freq) && (!index || rope->rot_idx == 0 || rope->inv_freq_idx),
+                "%s: NULL inv_freq", who);
+    MSA_REQUIRE(!misaligned16({rows->q, rows->k, rows->v, q_out, dst[0], dst[1]}) &&
+                    (!index || !misaligned16({rows->q_idx, rows->k_idx, q_idx_out, dst[2]})),
+                "%s: rows, outputs and caches must be 16-byte aligned", who);
+    const int64_t stride[5] = {rows->q_stride, rows->k_stride, rows->v_stride, rows->q_idx_stride, rows->k_idx_stride};
+    for (int i = 0; i < (index ? 5 : 3); ++i) {
+        const int64_t least = i == 0 ? int64_t(s.Hq) * s.D : i < 3 ? int64_t(s.G) * s.D : int64_t(s.G) * s.Di;
+        MSA_REQUIRE(stride[i] % 8 == 0 && (stride[i] >= least || n_rows == 1),
+                    "%s: row strides must be multiples of 8 and no rows may overlap", who);
+    }
+    RopeAppend p = {};
+    const void *src[5] = {rows->q, rows->k, rows->v, index ? rows->q_idx : nullptr, index ? rows->k_idx : nullptr};
+    for (int i = 0; i < 5; ++i) {
+        p.src[i] = src[i];
+        p.stride[i] = stride[i];
+    }
+    p.q_out = q_out;
+    p.q_idx_out = q_idx_out;
+    for (int i = 0; i < 3; ++i) {
+        p.dst[i] = dst[i];
+        p.scale[i] = scale[i];
+    }
+    p.inv_freq = rope->inv_freq;
+    p.inv_freq_idx = rope->inv_freq_idx;
+    p.block_table = block_table;
+    p.q_req = q_req;
+    p.q_pos = q_pos;
+    p.n_rows = n_rows;
+    p.n_req = n_req;
+    p.n_pages = n_pages;
+    p.rot = rope->rot;
+    p.rot_idx = rope->rot_idx;
+    p.interleaved = rope->interleaved;
+    p.gain = rope->gain;
+    p.err = err_word;
+    const cudaError_t e = launch_rope_append(p, s, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, who);
+}
+
+msa_status_t msa_rope_append(const msa_rows_t *rows, const msa_rope_t *rope, const int32_t *block_table,
+                             const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
+                             int32_t n_pages, const msa_dims_t *dims, void *q_out, void *q_idx_out, void *k_cache,
+                             void *v_cache, void *kidx_cache, int32_t *err_word, msa_stream_t stream) {
+    return rope_append(rows, rope, block_table, q_req, q_pos, n_rows, n_req, n_pages, dims, q_out, q_idx_out,
+                       {k_cache, v_cache, kidx_cache}, {nullptr, nullptr, nullptr}, err_word, stream,
+                       "msa_rope_append");
+}
+
+msa_status_t msa_rope_append_q8(const msa_rows_t *rows, const msa_rope_t *rope, const int32_t *block_table,
+                                const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
+                                int32_t n_pages, const msa_dims_t *dims, void *q_out, void *q_idx_out,
+                                const msa_cache_q8_t *cache, int32_t *err_word, msa_stream_t stream) {
+    MSA_REQUIRE(rows, "msa_rope_append_q8: NULL rows");
+    CacheQ8 c;
+    if (n_rows != 0) {
+        const msa_status_t st = check_cache_q8(cache, true, rows->q_idx || rows->k_idx, &c, "msa_rope_append_q8");
+        if (st != MSA_OK) return st;
+    } else {
+        c = CacheQ8{};
+    }
+    return rope_append(rows, rope, block_table, q_req, q_pos, n_rows, n_req, n_pages, dims, q_out, q_idx_out,
+                       {c.k, c.v, c.kidx}, {c.k_scale, c.v_scale, c.kidx_scale}, err_word, stream,
+                       "msa_rope_append_q8");
+}
+
+msa_status_t msa_cache_read_q8(const msa_cache_q8_t *cache, const int32_t *block_table, const int32_t *out_table,
+                               const int32_t *lens, int32_t n_req, int32_t n_pages, int32_t n_out_pages,
+                               const msa_dims_t *dims, void *k_cache, void *v_cache, void *kidx_cache,
+                               int32_t *err_word, msa_stream_t stream) {
+    Shape s;
+    msa_status_t st = check_dims(dims, true, kidx_cache != nullptr, &s, "msa_cache_read_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(n_req >= 0 && n_pages > 0 && n_out_pages > 0, "msa_cache_read_q8: bad sizes");
+    if (n_req == 0) return MSA_OK;
+    CacheQ8 c;
+    st = check_cache_q8(cache, true, kidx_cache != nullptr, &c, "msa_cache_read_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(block_table && out_table && lens && k_cache && v_cache && err_word, "msa_cache_read_q8: NULL pointer");
+    MSA_REQUIRE(!misaligned16({k_cache, v_cache, kidx_cache}), "msa_cache_read_q8: caches must be 16-byte aligned");
+    if (1LL * n_req * s.max_blocks > 0x7fffffffLL)
+        return fail(MSA_ERR_UNSUPPORTED, "msa_cache_read_q8: n_req * max_blocks >= 2^31");
+    const cudaError_t e = launch_cache_read(c, block_table, out_table, lens, n_req, n_pages, n_out_pages, s, k_cache,
+                                            v_cache, kidx_cache, err_word, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_cache_read_q8");
+}
+
+msa_status_t msa_index_score_q8(const void *q_idx, const msa_cache_q8_t *cache, const int32_t *block_table,
+                                const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
+                                int32_t n_pages, const msa_dims_t *dims, float *scores, int32_t *err_word,
+                                msa_stream_t stream) {
+    Shape s;
+    msa_status_t st = check_dims(dims, false, true, &s, "msa_index_score_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(n_rows >= 0 && n_req > 0 && n_pages > 0, "msa_index_score_q8: bad sizes");
+    if (n_rows == 0) return MSA_OK;
+    CacheQ8 c;
+    st = check_cache_q8(cache, false, true, &c, "msa_index_score_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(q_idx && block_table && q_req && q_pos && scores && err_word, "msa_index_score_q8: NULL pointer");
+    MSA_REQUIRE(!misaligned16({q_idx}), "msa_index_score_q8: q_idx must be 16-byte aligned");
+    if (1LL * n_rows * s.max_blocks > 0x7fffffffLL)
+        return fail(MSA_ERR_UNSUPPORTED, "msa_index_score_q8: n_rows * max_blocks >= 2^31");
+    const cudaError_t e = launch_score_q8(q_idx, c, block_table, q_req, q_pos, nullptr, n_rows, n_req, n_pages, s,
+                                          scores, err_word, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_index_score_q8");
+}
+
+msa_status_t msa_sparse_attn_decode_q8(const void *q, const msa_cache_q8_t *cache, const int32_t *page_table,
+                                       const int32_t *row_len, int32_t B, int32_t n_pages, const msa_dims_t *dims,
+                                       void *out, float *lse, int32_t *err_word, msa_stream_t stream) {
+    Shape s;
+    msa_status_t st = check_dims(dims, true, false, &s, "msa_sparse_attn_decode_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(B >= 0 && n_pages > 0, "msa_sparse_attn_decode_q8: bad sizes");
+    if (B == 0) return MSA_OK;
+    CacheQ8 c;
+    st = check_cache_q8(cache, true, false, &c, "msa_sparse_attn_decode_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(q && page_table && row_len && out && lse && err_word, "msa_sparse_attn_decode_q8: NULL pointer");
+    MSA_REQUIRE(!misaligned16({q, out}), "msa_sparse_attn_decode_q8: q and out must be 16-byte aligned");
+    if (1LL * B * s.G > kQ8MaxRows) return fail(MSA_ERR_UNSUPPORTED, "msa_sparse_attn_decode_q8: B*G > 2^26");
+    const cudaError_t e = launch_attn_decode_q8(q, c, page_table, row_len, B, n_pages, s, out, lse, err_word,
+                                                static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_sparse_attn_decode_q8");
+}
+
+msa_status_t msa_decode_step_q8(const void *q, const void *q_idx, const msa_cache_q8_t *cache,
+                                const int32_t *block_table, const int32_t *seq_lens, int32_t B, int32_t n_pages,
+                                const msa_dims_t *dims, float *scores, int32_t *sel, int32_t *page_table,
+                                int32_t *row_len, void *out, float *lse, int32_t *err_word, msa_stream_t stream) {
+    Shape s;
+    msa_status_t st = check_dims(dims, true, true, &s, "msa_decode_step_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(B >= 0 && n_pages > 0, "msa_decode_step_q8: bad sizes");
+    if (B == 0) return MSA_OK;
+    CacheQ8 c;
+    st = check_cache_q8(cache, true, true, &c, "msa_decode_step_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(q && q_idx && block_table && seq_lens && scores && sel && page_table && row_len && out && lse && err_word,
+                "msa_decode_step_q8: NULL pointer");
+    MSA_REQUIRE(!misaligned16({q, q_idx, out}), "msa_decode_step_q8: q, q_idx and out must be 16-byte aligned");
+    if (1LL * B * s.G > 65535) return fail(MSA_ERR_UNSUPPORTED, "msa_decode_step_q8: B*G > 65535");
+    if (s.max_blocks > 16384) return fail(MSA_ERR_UNSUPPORTED, "msa_decode_step_q8: max_blocks > 16384");
+    void *out_d = nullptr, *lse_d = nullptr;
+    if ((st = result_ptr(out, &out_d, "msa_decode_step_q8")) != MSA_OK) return st;
+    if ((st = result_ptr(lse, &lse_d, "msa_decode_step_q8")) != MSA_OK) return st;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_score_q8(q_idx, c, block_table, nullptr, nullptr, seq_lens, B, B, n_pages, s, scores,
+                                    err_word, cs, true);
+    if (e != cudaSuccess) return cuda_fail(e, "msa_decode_step_q8 (index scan)");
+    e = launch_decode_select(scores, seq_lens, block_table, B, n_pages, s, sel, page_table, row_len, nullptr, err_word,
+                             cs, true);
+    if (e != cudaSuccess) return cuda_fail(e, "msa_decode_step_q8 (selection)");
+    e = launch_attn_decode_q8(q, c, page_table, row_len, B, n_pages, s, out_d, static_cast<float *>(lse_d), err_word, cs,
+                              true);
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_decode_step_q8 (attention)");
+}
+
+msa_status_t msa_window_attn_q8(const void *q, const msa_cache_q8_t *cache, const int32_t *block_table,
+                                const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
+                                int32_t n_pages, int32_t window, int32_t n_sink, const msa_dims_t *dims,
+                                int32_t phase, void *out, float *lse, int32_t *err_word, msa_stream_t stream) {
+    Shape s;
+    msa_status_t st = check_dims(dims, true, false, &s, "msa_window_attn_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(n_rows >= 0 && n_req > 0 && n_pages > 0, "msa_window_attn_q8: bad sizes");
+    MSA_REQUIRE(window >= 1 && n_sink >= 0, "msa_window_attn_q8: window < 1 or n_sink < 0");
+    MSA_REQUIRE(phase == MSA_PHASE_DECODE || phase == MSA_PHASE_PREFILL, "msa_window_attn_q8: unknown phase %d", phase);
+    if (n_rows == 0) return MSA_OK;
+    CacheQ8 c;
+    st = check_cache_q8(cache, true, false, &c, "msa_window_attn_q8");
+    if (st != MSA_OK) return st;
+    MSA_REQUIRE(q && block_table && q_req && q_pos && out && lse && err_word, "msa_window_attn_q8: NULL pointer");
+    MSA_REQUIRE(!misaligned16({q, out}), "msa_window_attn_q8: q and out must be 16-byte aligned");
+    if (s.max_blocks > 1 << 24) return fail(MSA_ERR_UNSUPPORTED, "msa_window_attn_q8: max_blocks > 2^24");
+    if (1LL * n_rows * s.G > kQ8MaxRows) return fail(MSA_ERR_UNSUPPORTED, "msa_window_attn_q8: n_rows*G > 2^26");
+    const cudaError_t e = launch_window_decode_q8(q, c, block_table, q_req, q_pos, n_rows, n_req, n_pages, window,
+                                                  n_sink, s, out, lse, err_word, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_window_attn_q8");
+}
+
 size_t msa_workspace_bytes(int32_t op, int32_t n_rows, int32_t n_req, const msa_dims_t *dims) {
     Shape s;
     if (n_rows < 0) return 0;
@@ -629,7 +845,7 @@ msa_status_t msa_check(int32_t *err_word, msa_stream_t stream) {
     if (e == cudaSuccess) e = cudaMemsetAsync(err_word, 0, sizeof h, cs);
     if (e != cudaSuccess) return cuda_fail(e, "msa_check");
     if (h & MSA_FLAG_BOUNDS) return fail(MSA_ERR_DEVICE_BOUNDS, "device: index out of range (word 0x%x)", h);
-    if (h & MSA_FLAG_NAN) return fail(MSA_ERR_DEVICE_BOUNDS, "device: NaN block score (word 0x%x)", h);
+    if (h & MSA_FLAG_NAN) return fail(MSA_ERR_DEVICE_BOUNDS, "device: NaN block score, or a NaN or infinity stored in 8 bits (word 0x%x)", h);
     if (h & MSA_FLAG_TIMEOUT) return fail(MSA_ERR_TIMEOUT, "device: bounded wait expired (word 0x%x)", h);
     if (h & MSA_FLAG_UNSUPPORTED)
         return fail(MSA_ERR_DEVICE_UNSUPPORTED, "device: unsupported layout (word 0x%x)", h);
@@ -652,7 +868,7 @@ const char *msa_status_str(msa_status_t status) {
 
 const char *msa_last_error(void) { return g_last_error; }
 
-int32_t msa_version(void) { return 400; }
+int32_t msa_version(void) { return 500; }
 
 msa_status_t msa_selftest_timeout(int32_t *err_word, msa_stream_t stream) {
     MSA_REQUIRE(err_word, "msa_selftest_timeout: NULL err_word");

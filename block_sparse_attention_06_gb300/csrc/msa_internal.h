@@ -153,6 +153,41 @@ cudaError_t launch_commit_tree(const void *k_new, const void *v_new, const void 
                                int n_req, int n_pages, const Shape &s, int32_t *new_lens, int32_t *err,
                                cudaStream_t st);
 
+// 8-bit caches of one layer: e4m3 codes [n_pages][G][128][width] and scale bytes [n_pages][G][128].
+struct CacheQ8 {
+    void *k, *k_scale, *v, *v_scale, *kidx, *kidx_scale;
+};
+
+// Rotary positions and the append of a layer's new rows: q, k, v, q_idx, k_idx (the last two may be absent);
+// scale[0] says whether the caches are 8-bit.
+struct RopeAppend {
+    const void *src[5];
+    long long stride[5];
+    void *q_out, *q_idx_out;
+    void *dst[3], *scale[3];
+    const double *inv_freq, *inv_freq_idx;
+    const int32_t *block_table, *q_req, *q_pos;
+    int n_rows, n_req, n_pages, rot, rot_idx, interleaved;
+    float gain;
+    int32_t *err;
+};
+cudaError_t launch_rope_append(const RopeAppend &p, const Shape &s, cudaStream_t st);
+// Blocks of 8-bit caches as bf16 pages; kidx may be null.
+cudaError_t launch_cache_read(const CacheQ8 &c, const int32_t *bt_in, const int32_t *bt_out, const int32_t *lens,
+                              int n_req, int n_pages, int n_pages_out, const Shape &s, void *k, void *v, void *kidx,
+                              int32_t *err, cudaStream_t st);
+// Decode index scan over 8-bit index keys: rows by (q_req, q_pos), or the requests at seq_lens - 1.
+cudaError_t launch_score_q8(const void *q_idx, const CacheQ8 &c, const int32_t *block_table, const int32_t *q_req,
+                            const int32_t *q_pos, const int32_t *seq_lens, int n_rows, int n_req, int n_pages,
+                            const Shape &s, float *scores, int32_t *err, cudaStream_t st, bool pdl = false);
+// Decode attention over 8-bit caches: the pages of a table, or a window and the first tokens.
+cudaError_t launch_attn_decode_q8(const void *q, const CacheQ8 &c, const int32_t *page_table, const int32_t *row_len,
+                                  int B, int n_pages, const Shape &s, void *out, float *lse, int32_t *err,
+                                  cudaStream_t st, bool pdl = false);
+cudaError_t launch_window_decode_q8(const void *q, const CacheQ8 &c, const int32_t *block_table, const int32_t *q_req,
+                                    const int32_t *q_pos, int n_rows, int n_req, int n_pages, int window, int n_sink,
+                                    const Shape &s, void *out, float *lse, int32_t *err, cudaStream_t st);
+
 // Tensor-map creation through the driver entry point (no libcuda link dependency).
 bool encode_tensor_map(void *map, int rank, const void *base, const uint64_t *dims,
                        const uint64_t *strides_bytes, const uint32_t *box, int swizzle_bytes,

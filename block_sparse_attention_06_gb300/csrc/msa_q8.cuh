@@ -1,0 +1,93 @@
+// The 8-bit cache format, shared by its writer and its readers.
+//
+// A row (one token of one group) is `width` e4m3 codes and one scale byte b: value = code * 2^(b - 127).
+// The scale is the smallest power of two under which the row's largest magnitude is at most 448, the
+// largest e4m3 number, and at least 2^-100; a row of zeros has scale 1, a row that holds a NaN or an
+// infinity has b = 255 (NaN).  e4m3 has four significant bits and the scale is a power of two, so every
+// stored value is also a bf16 number: a bf16 contraction over the stored values rounds nothing further.
+#pragma once
+
+#include "msa_device.cuh"
+
+namespace msa {
+
+constexpr int kQ8LowestExp = -100;   // of a scale that the writer gives
+
+// 2^(b - 127); NaN for b = 255 (b = 0, which the writer never gives, is 2^-127).
+__device__ __forceinline__ float q8_scale(uint32_t b) {
+    const uint32_t bits = b == 255u ? 0x7fffffffu : b == 0u ? 0x00400000u : b << 23;
+    return __uint_as_float(bits);
+}
+
+// Exponent of the scale of a row whose largest magnitude has the bits `amax` (not a NaN or an infinity).
+// amax = m 2^E with m in [0.5, 1) and 448 = 0.875 * 2^9, so amax / 2^e <= 448 for e = E - 9 where
+// m <= 0.875 and for E - 8 elsewhere.  A magnitude under 2^-126 ends at the lowest exponent.
+__device__ __forceinline__ int q8_exponent(uint32_t amax) {
+    if (amax == 0u) return 0;
+    const int e = int(amax >> 23) - 126 - 9 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return max(e, kQ8LowestExp);
+}
+
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }   // -126 <= e <= 127
+
+// Two fp32 numbers as e4m3, round to nearest even (b in the upper byte).
+__device__ __forceinline__ uint32_t pack_e4m3x2(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Two e4m3 codes (the lower 16 bits) as fp32.
+__device__ __forceinline__ float2 unpack_e4m3x2(uint32_t w) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(w)));
+    float2 f;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+}
+
+// A vector of bf16 numbers as the sum of three vectors of e4m3 numbers, so that its products with cached
+// codes run on the 8-bit tensor cores without rounding either side: with x = q 2^-e, |x| <= 448,
+//   hi = e4m3(x),  lo = e4m3((x - hi) 2^4),  re = e4m3((x - hi - lo 2^-4) 2^22).
+// bf16 has eight significant bits and e4m3 four, so hi + lo 2^-4 is x itself where |x| >= 2^-6 (2^-14 of
+// the largest), re takes what is below, and nothing above 2^-40 of the largest is lost.
+constexpr float kQ8LoScale = 0x1p-4f, kQ8ReScale = 0x1p-22f;
+
+// Pieces of four numbers x (already scaled) as words of four codes, first number in the lowest byte.
+__device__ __forceinline__ void q8_pieces(const float (&x)[4], uint32_t &hi, uint32_t &lo, uint32_t &re) {
+    uint32_t h[2], l[2], r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        h[i] = pack_e4m3x2(a, b);
+        const float2 hf = unpack_e4m3x2(h[i]);
+        const float ra = (a - hf.x) * 0x1p4f, rb = (b - hf.y) * 0x1p4f;
+        l[i] = pack_e4m3x2(ra, rb);
+        const float2 lf = unpack_e4m3x2(l[i]);
+        r[i] = pack_e4m3x2((ra - lf.x) * 0x1p18f, (rb - lf.y) * 0x1p18f);
+    }
+    hi = h[0] | h[1] << 16;
+    lo = l[0] | l[1] << 16;
+    re = r[0] | r[1] << 16;
+}
+
+// D += A B, e4m3 with fp32 accumulation: m16 (rows of A: cached tokens), n8, k32.
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+}  // namespace msa

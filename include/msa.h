@@ -556,6 +556,136 @@ msa_status_t msa_commit_tree(const void *k_new, const void *v_new, const void *k
                              const msa_dims_t *dims, int32_t *new_lens, int32_t *err_word, msa_stream_t stream);
 
 /*
+ * Appending to the caches, and 8-bit caches.  A layer's projections give one row of q, k, v
+ * (and q_idx, k_idx) per new token; msa_rope_append turns q, k and the index vectors to
+ * their positions and writes k, v and k_idx into the paged caches.  The caches are bf16
+ * (the layout at the top of this file) or 8-bit, in which half the bytes are read:
+ *
+ *   codes   e4m3 [n_pages][G][128][D] (k, v) and [n_pages][G][128][Di] (kidx): the slice
+ *           of one page and group is one contiguous run
+ *   scales  uint8 [n_pages][G][128]: byte b of a (token, group) row stands for 2^(b - 127)
+ *           (255: NaN); value = code * 2^(b - 127)
+ *
+ * The scale is the smallest power of two under which the row's largest magnitude is at most
+ * 448 (the largest code), at least 2^-100, and 1 for a row of zeros.  Values are rounded
+ * once, to the nearest code (ties to even), so a value is off by at most 2^-4 of itself where
+ * its code is normal, and by 2^-18 of the row's largest magnitude below; each stored
+ * value is also a bf16 number.  A row of k, v or k_idx that holds a NaN or an infinity is stored as
+ * a row of NaN and raises MSA_FLAG_NAN.  The 8-bit pages are those of the same page ids and
+ * block tables as the bf16 ones.  Codes and bf16 rows are 16-byte aligned, scales 4-byte.
+ */
+typedef struct {
+    void *k, *k_scale;          /* codes and scales of K                                   */
+    void *v, *v_scale;          /* of V                                                    */
+    void *kidx, *kidx_scale;    /* of the index keys; NULL where a call does not need them */
+} msa_cache_q8_t;
+
+/* A layer's new rows: row r of x at x + r * stride elements, its heads dense behind one another, so the
+ * five may be parts of one projection's output.  Strides are multiples of 8, pointers 16-byte aligned. */
+typedef struct {
+    const void *q, *k, *v;      /* bf16 [n_rows][Hq][D], [n_rows][G][D], [n_rows][G][D]    */
+    const void *q_idx, *k_idx;  /* bf16 [n_rows][G][Di] both, or both NULL                 */
+    int64_t q_stride, k_stride, v_stride, q_idx_stride, k_idx_stride;
+} msa_rows_t;
+
+/* Rotary positions.  Of each head the first `rot` components turn, in pairs (i, i + rot/2) or, interleaved,
+ * (2i, 2i + 1): (a, b) -> gain * (a cos w - b sin w, b cos w + a sin w), w = q_pos * inv_freq[i].  Index
+ * vectors likewise with rot_idx and inv_freq_idx.  Positions scaled for long contexts are a matter of
+ * inv_freq and gain.  The angle is exact to 2^-40 turns at any position. */
+typedef struct {
+    int32_t rot, rot_idx;       /* multiples of 16 in [0, D] and [0, Di]                   */
+    int32_t interleaved;        /* 0 or 1                                                  */
+    float gain;                 /* 1 where positions are not scaled                        */
+    const double *inv_freq, *inv_freq_idx;   /* device, [rot/2] and [rot_idx/2], radians   */
+} msa_rope_t;
+
+/*
+ * msa_rope_append -- rotate a layer's new rows and append them to its bf16 caches.
+ *   rows, rope      see above
+ *   block_table     int32 [n_req][max_blocks];  q_req, q_pos int32 [n_rows]: row r is the token at
+ *                   position q_pos[r] of request q_req[r]; q_req -1 marks a padding row, of which
+ *                   nothing is written
+ *   q_out           bf16 [n_rows][Hq][D] out;  q_idx_out bf16 [n_rows][G][Di] out: the rotated vectors.
+ *                   They may be the rows' own q and q_idx where those are dense, and lie over no other
+ *                   input.  Without q_idx and k_idx, q_idx_out and kidx_cache are not used.
+ * A position outside the table, a request outside [0, n_req) or a page outside [0, n_pages) raises
+ * MSA_FLAG_BOUNDS and nothing of that row is written.  No two rows may be the same token.
+ */
+msa_status_t msa_rope_append(const msa_rows_t *rows, const msa_rope_t *rope, const int32_t *block_table,
+                             const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
+                             int32_t n_pages, const msa_dims_t *dims, void *q_out, void *q_idx_out, void *k_cache,
+                             void *v_cache, void *kidx_cache, int32_t *err_word, msa_stream_t stream);
+
+/* msa_rope_append_q8 -- the same into 8-bit caches, quantised from the fp32 rotation. */
+msa_status_t msa_rope_append_q8(const msa_rows_t *rows, const msa_rope_t *rope, const int32_t *block_table,
+                                const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
+                                int32_t n_pages, const msa_dims_t *dims, void *q_out, void *q_idx_out,
+                                const msa_cache_q8_t *cache, int32_t *err_word, msa_stream_t stream);
+
+/*
+ * msa_cache_read_q8 -- blocks of 8-bit caches as bf16 pages, exactly: what the prefill calls
+ * take.  Block j of request b is written to page out_table[b][j] where that is >= 0 and the block
+ * holds a token below lens[b]; tokens at or past lens[b] are left as they are.
+ *   block_table, out_table  int32 [n_req][max_blocks];  lens int32 [n_req]
+ *   k_cache, v_cache  bf16 [n_out_pages][128][G][D] out;  kidx_cache bf16 [n_out_pages][128][G][Di] out,
+ *                     or NULL (then cache->kidx is not read)
+ * A page outside [0, n_pages) of a block to be written, or an out_table entry >= n_out_pages, raises
+ * MSA_FLAG_BOUNDS and that block is not written.  No two blocks may go to the same page.
+ */
+msa_status_t msa_cache_read_q8(const msa_cache_q8_t *cache, const int32_t *block_table, const int32_t *out_table,
+                               const int32_t *lens, int32_t n_req, int32_t n_pages, int32_t n_out_pages,
+                               const msa_dims_t *dims, void *k_cache, void *v_cache, void *kidx_cache,
+                               int32_t *err_word, msa_stream_t stream);
+
+/*
+ * msa_index_score_q8 -- msa_index_score (MSA_PHASE_DECODE: each row reads its own candidate pages) over 8-bit
+ * index keys.  Arguments as there.  A NaN among a block's visible tokens gives a NaN score.
+ * q_idx is finite (else its scores are NaN); components below 2^-40 of the largest of their group count as 0.
+ */
+msa_status_t msa_index_score_q8(const void *q_idx, const msa_cache_q8_t *cache, const int32_t *block_table,
+                                const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
+                                int32_t n_pages, const msa_dims_t *dims, float *scores, int32_t *err_word,
+                                msa_stream_t stream);
+
+/*
+ * msa_sparse_attn_decode_q8 -- msa_sparse_attn_decode over 8-bit caches, without a workspace.
+ *   q bf16 [B][Hq][D];  page_table int32 [B*G][topk];  row_len int32 [B*G]
+ *   out bf16 [B][Hq][D] out;  lse fp32 [B][Hq] out.  A row that sees nothing gets 0 and -inf.
+ * What a row does not see does not reach it, whatever its bits; a NaN that it sees makes it NaN.  q is finite
+ * (else its row is NaN); components below 2^-40 of a head's largest count as 0.  V's scales are at most 2^87.
+ */
+msa_status_t msa_sparse_attn_decode_q8(const void *q, const msa_cache_q8_t *cache, const int32_t *page_table,
+                                       const int32_t *row_len, int32_t B, int32_t n_pages, const msa_dims_t *dims,
+                                       void *out, float *lse, int32_t *err_word, msa_stream_t stream);
+
+/*
+ * msa_decode_step_q8 -- msa_decode_step over 8-bit caches: index scan, selection and page tables, attention,
+ * with the results of the separate calls.  Arguments and limits as there; no workspace.
+ */
+msa_status_t msa_decode_step_q8(const void *q, const void *q_idx, const msa_cache_q8_t *cache,
+                                const int32_t *block_table, const int32_t *seq_lens, int32_t B, int32_t n_pages,
+                                const msa_dims_t *dims, float *scores, int32_t *sel, int32_t *page_table,
+                                int32_t *row_len, void *out, float *lse, int32_t *err_word, msa_stream_t stream);
+
+/*
+ * msa_window_attn_q8 -- attention over 8-bit caches to the last tokens and the first ones: a row at position p
+ * attends the tokens t <= p of its request with t > p - window or t < n_sink.  A window of at least p + 1 is
+ * dense causal attention.  dims->topk is not used.
+ *   q bf16 [n_rows][Hq][D];  block_table int32 [n_req][max_blocks];  q_req, q_pos int32 [n_rows]
+ *   window >= 1, n_sink >= 0
+ *   phase  MSA_PHASE_DECODE: each row reads its own tokens.  MSA_PHASE_PREFILL: runs of 128/(Hq/G) consecutive
+ *          rows share their reads, on the tensor cores; any rows, but it suits chunks of neighbouring tokens.
+ *   out bf16 [n_rows][Hq][D] out;  lse fp32 [n_rows][Hq] out.  A row with q_req -1 is padding: nothing of it is
+ *          written.
+ * A bad request or position, or a page outside [0, n_pages) of a block that a row sees, raises
+ * MSA_FLAG_BOUNDS.  What is said of q, V and NaN at msa_sparse_attn_decode_q8 holds here.
+ */
+msa_status_t msa_window_attn_q8(const void *q, const msa_cache_q8_t *cache, const int32_t *block_table,
+                                const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
+                                int32_t n_pages, int32_t window, int32_t n_sink, const msa_dims_t *dims,
+                                int32_t phase, void *out, float *lse, int32_t *err_word, msa_stream_t stream);
+
+/*
  * msa_workspace_bytes -- device scratch needed by an operation:
  *   MSA_OP_INVERT: n_rows query rows, n_req requests;
  *   MSA_OP_DECODE: n_rows = B decode requests (n_req ignored);
