@@ -15,8 +15,9 @@
 // they are, q is three e4m3 pieces that sum to it (msa_q8.cuh); the token's scale and the head's factor multiply
 // the fp32 result.  O^T = V^T P^T runs on bf16 MMAs (m16n8k16, components = M): a code seeeemmm becomes the
 // bf16 number s0000eeeemmm0000 = code * 2^-120 by shifts and masks (subnormal codes included, and no code gives
-// a NaN or an infinity, so tokens that a row does not see cannot reach it), and P carries the token's scale:
-// P_t = p_t 2^(e_t + 40).  That range is bf16's: scales up to 2^87.  P is rounded to bf16, once.
+// a NaN or an infinity, so tokens that a row does not see cannot reach it), and P carries the token's scale
+// relative to the largest that the warp has seen: P_t = p_t 2^(e_t - E + 100), so O is held times 2^(-20 - E) and
+// scales of any size fit, with 100 binades between the largest and what is lost.  P is rounded to bf16, once.
 //
 // Layout.  In a unit lane (r, c) = (lane / 4, lane % 4) reads tokens 4r .. 4r+3 of K (its quad covers the row,
 // a quarter each) and tokens 8c .. 8c+7 of V (D/8 components each): whole lines per load.  The C fragment of S^T
@@ -60,6 +61,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // Codes in bytes 0 and 2, or 1 and 3, of w as two bf16 numbers code * 2^-120.
 __device__ __forceinline__ uint32_t bf16_even(uint32_t w) { return ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u); }
 __device__ __forceinline__ uint32_t bf16_odd(uint32_t w) { return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u); }
+
+// 2^d for d <= 0, 0 below 2^-126.
+__device__ __forceinline__ float pow2_down(int d) { return __uint_as_float(uint32_t(max(d + 127, 0)) << 23); }
+
+// out = (x 2^20) 2^E for x = O 2^(-20 - E) / l, with E as a scale byte.
+__device__ __forceinline__ float unscaled(float x, int e) { return x * 0x1p20f * q8_scale(uint32_t(e)); }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -131,8 +138,10 @@ template <int D>
 struct Smem {
     alignas(16) float o[kWarps][8][D + 4];
     float m[kWarps][8], l[kWarps][8];
+    int e[kWarps];
     alignas(16) float po[8][D];       // of the CTA, read by the cluster
     float pm[8], pl[8];
+    int pe;
 };
 
 template <int D, int HPG, bool WINDOW>
@@ -254,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
 #pragma unroll
     for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // heads 2c, 2c + 1; l over this lane's tokens
+    int emax = 0;                    // largest scale byte of V so far (255 aside): E + 127
 
     for (; u < rw.units; u += step) {
         int page_n = -1, t_n = 0, v0_n = 0, v1_n = 0;
@@ -284,19 +294,33 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
             if (page_n >= 0) load_k(page_n, t_n);
             const bool whole = v0 <= 0 && v1 >= kUnit;
             float mx0 = -INFINITY, mx1 = -INFINITY;
-            float f[4];              // the token's scale in P (0: not visible)
+            int eb[4];               // scale bytes of V (-1: not visible)
+            int etop = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float ks = q8_scale((kb >> (8 * i)) & 255u);
-                f[i] = q8_scale((vb >> (8 * i)) & 255u) * 0x1p40f;
+                eb[i] = int((vb >> (8 * i)) & 255u);
                 s[i][0] = s[i][0] * ks * hq0;
                 s[i][1] = s[i][1] * ks * hq1;
                 if (!whole && (4 * r + i < v0 || 4 * r + i >= v1)) {
                     s[i][0] = s[i][1] = -INFINITY;
-                    f[i] = 0.f;
+                    eb[i] = -1;
                 }
+                etop = max(etop, eb[i] == 255 ? 0 : eb[i]);
                 mx0 = fmaxf(mx0, s[i][0]);
                 mx1 = fmaxf(mx1, s[i][1]);
+            }
+            etop = __reduce_max_sync(0xffffffffu, etop);
+            if (etop > emax) {       // uniform in the warp
+                const float al = pow2_down(emax - etop);
+                emax = etop;
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    o[t][0] *= al;
+                    o[t][1] *= al;
+                    o[t][2] *= al;
+                    o[t][3] *= al;
+                }
             }
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
@@ -326,7 +350,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
                 const float p0 = fast_exp2(s[i][0] - r0), p1 = fast_exp2(s[i][1] - r1);
                 l0 += p0;
                 l1 += p1;
-                pt[i] = transpose8(pack_bf16x2(p0 * f[i], p1 * f[i]));
+                // 2^(e - E + 100): 0 for tokens that are not visible, NaN for a NaN row
+                const int x = max(eb[i] - emax + 227, 0) << 23;
+                const float f = eb[i] < 0 ? 0.f : __uint_as_float(eb[i] == 255 ? 0x7fffffffu : uint32_t(x));
+                pt[i] = transpose8(pack_bf16x2(p0 * f, p1 * f));
             }
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
@@ -357,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
         sm.m[warp][2 * c + 1] = m1;
         sm.l[warp][2 * c] = l0;
         sm.l[warp][2 * c + 1] = l1;
+        if (lane == 0) sm.e[warp] = emax;
     }
 #pragma unroll
     for (int t = 0; t < MT; t += 2) {
@@ -367,28 +395,31 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
     __syncthreads();
     constexpr int PAIRS = HPG * D / 2;
     const size_t head0 = size_t(b) * a.G * HPG + size_t(g) * HPG;
-    auto weights = [](const float *m, int n, int stride, float *w) {   // of n partials against their largest
-        float top = -INFINITY;
-        for (int i = 0; i < n; ++i) top = fmaxf(top, m[i * stride]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        for (int i = 0; i < n; ++i) w[i] = fast_exp2(m[i * stride] - ref);
-        return top;
+    int ecta = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) ecta = max(ecta, sm.e[i]);
+    // a pair of output components from the sums over all partials
+    auto finish = [&](int h, int d, float top, float l, float x, float y, int e) {
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        *reinterpret_cast<uint32_t *>(a.out + (head0 + h) * D + d) = pack_bf16x2(unscaled(x * inv, e), unscaled(y * inv, e));
+        if (d == 0) a.lse[head0 + h] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
     };
-    for (int e = tid; e < PAIRS; e += kThreads) {
-        const int h = e / (D / 2), d = (e - h * (D / 2)) * 2;
-        float w[kWarps];
-        const float top = weights(&sm.m[0][h], kWarps, 8, w);
+    for (int i = tid; i < PAIRS; i += kThreads) {
+        const int h = i / (D / 2), d = (i - h * (D / 2)) * 2;
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sm.m[k][h]);
+        const float ref = top == -INFINITY ? 0.f : top;
         float l = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            l += w[i] * sm.l[i][h];
-            x += w[i] * sm.o[i][h][d];
-            y += w[i] * sm.o[i][h][d + 1];
+        for (int k = 0; k < kWarps; ++k) {
+            const float w = fast_exp2(sm.m[k][h] - ref), wo = w * pow2_down(sm.e[k] - ecta);
+            l += w * sm.l[k][h];
+            x += wo * sm.o[k][h][d];
+            y += wo * sm.o[k][h][d + 1];
         }
         if (a.cluster == 1) {
-            const float inv = l == 0.f ? 0.f : 0x1p80f / l;
-            *reinterpret_cast<uint32_t *>(a.out + (head0 + h) * D + d) = pack_bf16x2(x * inv, y * inv);
-            if (d == 0) a.lse[head0 + h] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+            finish(h, d, top, l, x, y, ecta);
         } else {
             *reinterpret_cast<float2 *>(&sm.po[h][d]) = make_float2(x, y);
             if (d == 0) {
@@ -398,12 +429,16 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
         }
     }
     if (a.cluster == 1) return;
+    if (tid == 0) sm.pe = ecta;
     cluster_arrive();
     cluster_wait();
+    const uint32_t pe = smem_u32(&sm.pe);
+    int ec = 0;
+    for (int k = 0; k < a.cluster; ++k) ec = max(ec, __float_as_int(ld_cluster(cluster_map(pe, k))));
     const int share = PAIRS / a.cluster;   // a power of two, at least 8
     for (int i = tid; i < share; i += kThreads) {
-        const int e = rank * share + i;
-        const int h = e / (D / 2), d = (e - h * (D / 2)) * 2;
+        const int j = rank * share + i;
+        const int h = j / (D / 2), d = (j - h * (D / 2)) * 2;
         const uint32_t pm = smem_u32(&sm.pm[h]), pl = smem_u32(&sm.pl[h]), po = smem_u32(&sm.po[h][d]);
         float top = -INFINITY;
         for (int k = 0; k < a.cluster; ++k) top = fmaxf(top, ld_cluster(cluster_map(pm, k)));
@@ -411,14 +446,13 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
         float l = 0.f, x = 0.f, y = 0.f;
         for (int k = 0; k < a.cluster; ++k) {
             const float w = fast_exp2(ld_cluster(cluster_map(pm, k)) - ref);
+            const float wo = w * pow2_down(__float_as_int(ld_cluster(cluster_map(pe, k))) - ec);
             const float2 v = ld_cluster2(cluster_map(po, k));
             l += w * ld_cluster(cluster_map(pl, k));
-            x += w * v.x;
-            y += w * v.y;
+            x += wo * v.x;
+            y += wo * v.y;
         }
-        const float inv = l == 0.f ? 0.f : 0x1p80f / l;
-        *reinterpret_cast<uint32_t *>(a.out + (head0 + h) * D + d) = pack_bf16x2(x * inv, y * inv);
-        if (d == 0) a.lse[head0 + h] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+        finish(h, d, top, l, x, y, ec);
     }
     cluster_arrive();                // no CTA leaves while another reads its partials
     cluster_wait();

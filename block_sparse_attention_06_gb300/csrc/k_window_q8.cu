@@ -1,0 +1,716 @@
+// Window attention of a chunk's rows over 8-bit caches, on the 5th-generation tensor cores.
+//
+// Row r (position p of its request) attends the tokens t <= p with t > p - window or t < n_sink.  A tile is
+// 128/HPG consecutive rows times the HPG heads of one KV group = the 128 rows of an MMA's M; an item is two such
+// tiles (A, B) of one group, whose rows need nearly the same pages, and its steps are those pages:
+//   S = Q K^T  (128 x 128 x D),  P = 2^(S scale - ref),  O += P V  (128 x D x 128),  l += row sums of P.
+// ref is a row's reference: its maximum so far, raised only when a logit passes it by 2^8, so O is next to never
+// rescaled; out = O / l, lse = ref + log l.
+//
+// K and V come as codes and scales; four warps turn a page into bf16 tiles in shared memory, exactly (a code
+// becomes code * 2^-120 by shifts and masks, one multiplication by a power of two gives the value), so the MMAs
+// round nothing of the cache.  A row of V that is NaN is written as zeros and the rows that see it are made NaN
+// at the end: what a row does not see cannot reach it, whatever its bits.
+//
+// What bounds it: per step and pair of tiles 2048 cycles of MMAs, about as much of shared memory (the MMAs read 192
+// KB of operands, the converters write 64 KB), and a good half of that of ALU work (exponentials and masks of 2 x 128 x
+// 128 logits, conversion of 32 KB of codes).  So the two tiles take turns: while one's softmax runs, the tensor cores
+// work on the other's S and P V.
+//
+// One CTA per SM, 16 warps, persistent over items:
+//   warp 0     planner: for each item the pages that any of its rows sees, in a ring of step descriptors;
+//   warp 1     MMA issuer and TMEM owner: S_A(s), P V of B(s-1), S_B(s), P V of A(s), ...;
+//   warp 2     Q loader (TMA, one box per tile and 64 columns);   warp 3  idle;
+//   warps 4-7, 8-11   softmax of tiles A and B, one row per thread; each also writes its tile's results;
+//   warps 12-15  converters: K and V of the next page wait in registers while this one's are written.
+// TMEM: S_A | S_B | O_A | O_B (128 + 128 + D + D columns); P is written over S.
+// Every wait is bounded; a timeout raises MSA_FLAG_TIMEOUT and every role drains.
+#include "msa_internal.h"
+#include "msa_q8.cuh"
+
+#include <algorithm>
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRing = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRaise = 8.f;        // log2 units by which a logit may pass its row's reference
+
+constexpr int kFirst = 1, kLast = 2, kEnd = 4, kNan = 8;
+
+struct Step {
+    int32_t flags;
+    int32_t page;          // physical page
+    int32_t base;          // position of its first token
+    int32_t req;
+    int32_t row0, g;       // the item: its first row, its group
+    uint32_t nan_v[4];     // tokens whose V row is NaN (kNan)
+};
+
+template <int D>
+struct Smem {
+    alignas(1024) uint8_t q[2][128 * D * 2];
+    alignas(1024) uint8_t k[2][128 * D * 2];
+    alignas(1024) uint8_t v[2][128 * D * 2];
+    Step step[kRing];
+    uint64_t desc_full[kRing], desc_empty[kRing];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2];   // per tile
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct Args {
+    const uint8_t *k, *k_scale, *v, *v_scale;
+    const int32_t *block_table, *q_req, *q_pos;
+    int n_rows, n_req, n_pages, max_blocks, Hq, G, window, n_sink, n_items;
+    float sm_scale;
+    uint16_t *out;
+    float *lse;
+    int32_t *err;
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two fp32 lanes per instruction; b2 and c2 hold one value in both halves.
+__device__ __forceinline__ uint64_t dup2(float x) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void ffma2(float &d0, float &d1, float a0, float a1, uint64_t b2, uint64_t c2) {
+    asm("{\n\t.reg .b64 x, d;\n\tmov.b64 x, {%2, %3};\n\tfma.rn.f32x2 d, x, %4, %5;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "l"(b2), "l"(c2));
+}
+__device__ __forceinline__ void fadd2_acc(uint64_t &acc2, float a0, float a1) {
+    asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tadd.rn.f32x2 %0, %0, x;\n\t}" : "+l"(acc2) : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float sum2(uint64_t acc2) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(acc2));
+    return a + b;
+}
+
+// D/16 MMAs of S = Q K^T, both operands K-major with the 128-byte swizzle: a k-step of 16 columns is 32 bytes
+// further in a sub-tile of 64 columns, and sub-tiles are 16 KB apart.
+template <int D>
+__device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        const uint64_t off = uint64_t((i >> 2) * 1024 + (i & 3) * 2);
+        mma_bf16(d, a + off, b + off, idesc, i > 0);
+    }
+}
+
+// Eight MMAs of O (+)= P V: P in TMEM (bf16 pairs, 8 columns per 16 tokens), V MN-major, 16 tokens 2 KB apart.
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t accumulate) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(p + uint32_t(i * 8)), "l"(v + uint64_t(i * 128)), "r"(idesc), "r"(i > 0 ? 1u : accumulate)
+            : "memory");
+    }
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// 16 codes as 16 bf16 values.  f: 2^(120 + min(e, 0)) in both halves; up: 2^max(e, 0), applied where `big`.
+__device__ __forceinline__ void convert16(const uint4 &w, uint32_t f, uint32_t up, bool big, uint32_t (&o)[8]) {
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // codes 0, 1 and 2, 3 side by side: bytes 0 and 2, then 1 and 3, of a word in the order 0, 2, 1, 3
+        const uint32_t x = __byte_perm(ww[i], 0u, 0x3120);
+        o[2 * i] = mul_bf16x2(((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u), f);
+        o[2 * i + 1] = mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), f);
+    }
+    if (big) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], up);
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16x2_exp2(int e) { return uint32_t((e + 127) << 7) * 0x10001u; }
+
+template <int D, int HPG>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_window_q8(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap qmap) {
+    constexpr int EPT = 128 / HPG;       // rows per tile
+    constexpr int NSUB = D / 64;         // 64-column sub-tiles
+    constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t kIdescO = make_idesc_bf16(128, D, 0, 1);
+    extern __shared__ uint8_t smem_raw[];
+    Smem<D> &sm = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t *const err = a.err;
+
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&sm.desc_full[i], 32);
+            mbar_init(&sm.desc_empty[i], 14);   // issuer, Q loader, 8 softmax warps, 4 converter warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1);
+            mbar_init(&sm.k_full[i], 4);
+            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.v_full[i], 4);
+            mbar_init(&sm.v_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_full[i], 1);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (warp == 2 && lane == 0) tma_prefetch_desc(&qmap);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    const volatile Step *const steps = sm.step;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ planner
+        int s = 0;                       // steps published
+        bool ok = true, pending = false;
+        Step st = {};                    // the step in hand: published with the next one, when its scales are here
+        uint32_t vs = 0u;                // its V scales, four tokens a lane
+        auto publish = [&](int more) {
+            const int slot = s % kRing;
+            if (s >= kRing) {
+                bool w = true;
+                if (lane == 0) w = mbar_wait(&sm.desc_empty[slot], ((s / kRing) - 1) & 1, err, &sm.abort);
+                if (!__shfl_sync(0xffffffffu, w, 0)) {
+                    ok = false;
+                    return;
+                }
+            }
+            uint32_t nib = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nib |= ((vs >> (8 * i)) & 255u) == 255u ? 1u << i : 0u;
+            const bool nan = __any_sync(0xffffffffu, nib != 0u);
+            if (nan) {
+                uint32_t m = nib << (4 * (lane & 7));
+                m |= __shfl_xor_sync(0xffffffffu, m, 1);
+                m |= __shfl_xor_sync(0xffffffffu, m, 2);
+                m |= __shfl_xor_sync(0xffffffffu, m, 4);
+                if ((lane & 7) == 0) sm.step[slot].nan_v[lane >> 3] = m;
+            }
+            if (lane == 0) {
+                Step &d = sm.step[slot];
+                d.flags = st.flags | more | (nan ? kNan : 0);
+                d.page = st.page;
+                d.base = st.base;
+                d.req = st.req;
+                d.row0 = st.row0;
+                d.g = st.g;
+            }
+            mbar_arrive(&sm.desc_full[slot]);
+            ++s;
+        };
+        for (int item = blockIdx.x; ok && item < a.n_items; item += gridDim.x) {
+            const int pair = item / a.G, g = item - pair * a.G;
+            const int row0 = pair * 2 * EPT;
+            // the item's rows, EPT / 16 a lane
+            constexpr int RPL = 2 * EPT / 32;
+            int rq[RPL], rp[RPL];
+#pragma unroll
+            for (int i = 0; i < RPL; ++i) {
+                const int r = row0 + i * 32 + lane;
+                rq[i] = r < a.n_rows ? a.q_req[r] : -1;
+                rp[i] = r < a.n_rows ? a.q_pos[r] : 0;
+                if (rq[i] != -1 && (rq[i] < 0 || rq[i] >= a.n_req || rp[i] < 0 || (rp[i] >> 7) >= a.max_blocks)) {
+                    if (g == 0) raise_flag(err, MSA_FLAG_BOUNDS);
+                    rq[i] = -1;
+                }
+            }
+            int flags = kFirst;
+            auto next_req = [&]() {      // the lowest request that is left, -1 for none
+                int m = 0x7fffffff;
+#pragma unroll
+                for (int i = 0; i < RPL; ++i) m = min(m, rq[i] < 0 ? 0x7fffffff : rq[i]);
+                m = __reduce_min_sync(0xffffffffu, m);
+                return m == 0x7fffffff ? -1 : m;
+            };
+            for (int req = next_req(); ok && req >= 0;) {
+                int pmin = 0x7fffffff, pmax = -1;
+#pragma unroll
+                for (int i = 0; i < RPL; ++i)
+                    if (rq[i] == req) {
+                        pmin = min(pmin, rp[i]);
+                        pmax = max(pmax, rp[i]);
+                    }
+                pmin = __reduce_min_sync(0xffffffffu, pmin);
+                pmax = __reduce_max_sync(0xffffffffu, pmax);
+                const int32_t *table = a.block_table + size_t(req) * a.max_blocks;
+                const int sink = min(a.n_sink, pmax + 1);
+                const int n_sp = (sink + 127) >> 7;                       // blocks with tokens that stay visible
+                const int lo = max(n_sp, max(0, pmin - (a.window - 1)) >> 7);
+                const int n_w = max(0, (pmax >> 7) - lo + 1);
+                for (int x0 = 0; ok && x0 < n_sp + n_w; x0 += 32) {       // 32 blocks at a time, one a lane
+                    const int x = x0 + lane;
+                    const int j = x < n_sp ? x : lo + (x - n_sp);
+                    const bool in = x < n_sp + n_w;
+                    int page = in ? table[j] : -1;
+                    bool need = false;                                    // does any row of the request see a token of it?
+#pragma unroll
+                    for (int i = 0; i < RPL; ++i)
+                        for (int l = 0; l < 32; ++l) {
+                            const int q = __shfl_sync(0xffffffffu, rq[i], l), p = __shfl_sync(0xffffffffu, rp[i], l);
+                            need |= q == req && j * 128 <= p &&
+                                    (j * 128 + 127 > p - a.window || j * 128 < a.n_sink);
+                        }
+                    need = need && in;
+                    if (need && (page < 0 || page >= a.n_pages)) {
+                        raise_flag(err, MSA_FLAG_BOUNDS);
+                        need = false;
+                    }
+                    uint32_t left = __ballot_sync(0xffffffffu, need);
+                    while (ok && left) {
+                        const int l = __ffs(left) - 1;
+                        left &= left - 1u;
+                        const int pg = __shfl_sync(0xffffffffu, page, l), jj = __shfl_sync(0xffffffffu, j, l);
+                        const uint32_t vn = __ldg(
+                            reinterpret_cast<const uint32_t *>(a.v_scale + (size_t(pg) * a.G + g) * 128) + lane);
+                        if (pending) publish(0);
+                        st.flags = flags;
+                        st.page = pg;
+                        st.base = jj * 128;
+                        st.req = req;
+                        st.row0 = row0;
+                        st.g = g;
+                        vs = vn;
+                        flags = 0;
+                        pending = true;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < RPL; ++i)
+                    if (rq[i] == req) rq[i] = -1;
+                req = next_req();
+            }
+            if (ok && pending) {
+                publish(kLast);
+                pending = false;
+            }
+            if (ok && flags == kFirst) {   // no row of the item sees a page that exists: zeros
+                for (int i = lane; i < 2 * EPT * HPG; i += 32) {
+                    const int r = row0 + i / HPG;
+                    if (r >= a.n_rows || a.q_req[r] == -1) continue;
+                    const size_t h = size_t(r) * a.Hq + g * HPG + i % HPG;
+                    for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.out + h * D + d) = make_uint4(0u, 0u, 0u, 0u);
+                    a.lse[h] = -INFINITY;
+                }
+            }
+        }
+        if (ok) {
+            st.flags = kEnd;
+            vs = 0u;
+            publish(0);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (lane 0)
+        if (lane == 0) {
+            const uint64_t qd[2] = {make_smem_desc(smem_u32(sm.q[0]), 16, 1024, 2),
+                                    make_smem_desc(smem_u32(sm.q[1]), 16, 1024, 2)};
+            const uint64_t kd[2] = {make_smem_desc(smem_u32(sm.k[0]), 16, 1024, 2),
+                                    make_smem_desc(smem_u32(sm.k[1]), 16, 1024, 2)};
+            const uint64_t vd[2] = {make_smem_desc(smem_u32(sm.v[0]), 16384, 1024, 2),
+                                    make_smem_desc(smem_u32(sm.v[1]), 16384, 1024, 2)};
+            // P V of tile x at step s; `first`: overwrite O
+            auto issue_pv = [&](int x, int s, bool first) -> bool {
+                if (!mbar_wait(&sm.p_full[x], s & 1, err, &sm.abort)) return false;
+                if (x == 0 && !mbar_wait(&sm.v_full[s & 1], (s >> 1) & 1, err, &sm.abort)) return false;
+                tc_fence_after();
+                mma_pv(tmem + 256u + uint32_t(x * D), tmem + uint32_t(x * 128), vd[s & 1], kIdescO, first ? 0u : 1u);
+                mma_commit(&sm.o_full[x]);
+                if (x == 1) mma_commit(&sm.v_empty[s & 1]);
+                return true;
+            };
+            int items = 0;               // whose Q has been waited for
+            bool b_pending = false, b_first = false;
+            for (int s = 0;; ++s) {
+                const int slot = s % kRing;
+                if (!mbar_wait(&sm.desc_full[slot], (s / kRing) & 1, err, &sm.abort)) break;
+                const int flags = steps[slot].flags;
+                mbar_arrive(&sm.desc_empty[slot]);
+                if (flags & kEnd) break;
+                const bool first = flags & kFirst, last = flags & kLast;
+                if (!mbar_wait(&sm.k_full[s & 1], (s >> 1) & 1, err, &sm.abort)) break;
+                if (first && !mbar_wait(&sm.q_full[0], items & 1, err, &sm.abort)) break;
+                tc_fence_after();
+                mma_s<D>(tmem, qd[0], kd[s & 1], kIdescS);
+                mma_commit(&sm.s_full[0]);
+                if (last) mma_commit(&sm.q_empty[0]);
+                if (b_pending) {
+                    b_pending = false;
+                    if (!issue_pv(1, s - 1, b_first)) break;
+                }
+                if (first && !mbar_wait(&sm.q_full[1], items & 1, err, &sm.abort)) break;
+                if (first) ++items;
+                tc_fence_after();
+                mma_s<D>(tmem + 128u, qd[1], kd[s & 1], kIdescS);
+                mma_commit(&sm.s_full[1]);
+                mma_commit(&sm.k_empty[s & 1]);
+                if (last) mma_commit(&sm.q_empty[1]);
+                if (!issue_pv(0, s, first)) break;
+                b_pending = true;
+                b_first = first;
+                if (last) {              // the item's results wait for it, and the next item's Q is still on its way
+                    b_pending = false;
+                    if (!issue_pv(1, s, first)) break;
+                }
+            }
+            mma_commit(&sm.drain);
+            mbar_wait(&sm.drain, 0, err, nullptr);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ Q loader (lane 0)
+        if (lane == 0) {
+            int items = 0, loaded[2] = {0, 0};
+            for (int s = 0;; ++s) {
+                const int slot = s % kRing;
+                if (!mbar_wait(&sm.desc_full[slot], (s / kRing) & 1, err, &sm.abort)) break;
+                const int flags = steps[slot].flags, row0 = steps[slot].row0, g = steps[slot].g;
+                mbar_arrive(&sm.desc_empty[slot]);
+                if (flags & kEnd) break;
+                if (!(flags & kFirst)) continue;
+                bool ok = true;
+                for (int x = 0; ok && x < 2; ++x) {
+                    if (items > 0 && !mbar_wait(&sm.q_empty[x], (items - 1) & 1, err, &sm.abort)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&sm.q_full[x], 128 * D * 2);
+#pragma unroll
+                    for (int i = 0; i < NSUB; ++i)   // rows past the last read as zeros
+                        tma_load_3d(sm.q[x] + i * 16384, &qmap, &sm.q_full[x], i * 64, g * HPG, row0 + x * EPT);
+                    loaded[x] = items + 1;
+                }
+                if (!ok) break;
+                ++items;
+            }
+            if (sm.abort)                // copies in flight land before the CTA exits
+                for (int x = 0; x < 2; ++x)
+                    if (loaded[x] > 0) mbar_wait(&sm.q_full[x], (loaded[x] - 1) & 1, err, nullptr);
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------ converters
+        // A thread takes TPT consecutive tokens, 16 codes of each (its lane's column); a quarter warp's stores
+        // fill eight different 16-byte columns: the upper four lanes store their two in the other order.
+        constexpr int LPT = D / 16;      // lanes per token
+        constexpr int TPT = LPT;         // tokens per thread (128 threads, 128 tokens)
+        const int w = warp - 12;
+        const int col = lane % LPT, tok0 = (w * (32 / LPT) + lane / LPT) * TPT;
+        const int swap = (lane >> 2) & 1;
+        const uint32_t sub = uint32_t(col >> 2) * 16384u;   // sub-tile of 64 columns
+        const int ch = (col & 3) * 2;                       // its first 16-byte chunk
+        uint4 kc[TPT], vc[TPT];
+        uint32_t ks[TPT / 4], vsc[TPT / 4];
+        auto load = [&](const uint8_t *codes, const uint8_t *scales, int page, int g, uint4 (&c)[TPT],
+                        uint32_t (&sc)[TPT / 4]) {
+            const size_t line = (size_t(page) * a.G + g) * 128 + tok0;
+#pragma unroll
+            for (int i = 0; i < TPT; ++i) c[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (line + i) * D + col * 16));
+#pragma unroll
+            for (int i = 0; i < TPT / 4; ++i) sc[i] = __ldg(reinterpret_cast<const uint32_t *>(scales + line) + i);
+        };
+        auto store = [&](uint8_t *tile, const uint4 (&c)[TPT], const uint32_t (&sc)[TPT / 4], bool values) {
+            const uint32_t base = smem_u32(tile) + sub;
+#pragma unroll
+            for (int i = 0; i < TPT; ++i) {
+                const int t = tok0 + i;
+                const uint32_t b = (sc[i / 4] >> (8 * (i & 3))) & 255u;
+                const int e = int(b) - 127;
+                uint32_t f = bf16x2_exp2(120 + min(max(e, -126 - 120), 0));
+                // a NaN row: of K NaN, so the logits of the rows that see it are; of V zeros (see above)
+                if (b == 255u) f = values ? 0u : 0x7fff7fffu;
+                uint32_t o[8];
+                convert16(c[i], f, bf16x2_exp2(min(max(e, 0), 127)), e > 0 && b != 255u, o);
+                const uint32_t row = base + uint32_t(t * 128);
+                const int x0 = (ch + swap) ^ (t & 7), x1 = (ch + 1 - swap) ^ (t & 7);
+                const uint32_t p0 = row + uint32_t(x0 << 4), p1 = row + uint32_t(x1 << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0), "r"(swap ? o[4] : o[0]),
+                             "r"(swap ? o[5] : o[1]), "r"(swap ? o[6] : o[2]), "r"(swap ? o[7] : o[3]) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p1), "r"(swap ? o[0] : o[4]),
+                             "r"(swap ? o[1] : o[5]), "r"(swap ? o[2] : o[6]), "r"(swap ? o[3] : o[7]) : "memory");
+            }
+        };
+        // descriptor of step s: its flags, with page and group
+        auto desc = [&](int s, int *flags, int *page, int *g) -> bool {
+            const int slot = s % kRing;
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm.desc_full[slot], (s / kRing) & 1, err, &sm.abort))) return false;
+            *flags = steps[slot].flags;
+            *page = steps[slot].page;
+            *g = steps[slot].g;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.desc_empty[slot]);
+            return true;
+        };
+        int flags, page, g;
+        bool ok = desc(0, &flags, &page, &g);
+        if (ok && !(flags & kEnd)) {
+            load(a.k, a.k_scale, page, g, kc, ks);
+            load(a.v, a.v_scale, page, g, vc, vsc);
+        }
+        for (int s = 0; ok && !(flags & kEnd); ++s) {
+            const int b = s & 1;
+            if (s >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.k_empty[b], ((s >> 1) - 1) & 1, err, &sm.abort))) break;
+            store(sm.k[b], kc, ks, false);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.k_full[b]);
+            ok = desc(s + 1, &flags, &page, &g);
+            const bool more = ok && !(flags & kEnd);
+            if (more) load(a.k, a.k_scale, page, g, kc, ks);
+            if (s >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.v_empty[b], ((s >> 1) - 1) & 1, err, &sm.abort))) break;
+            store(sm.v[b], vc, vsc, true);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_full[b]);
+            if (more) load(a.v, a.v_scale, page, g, vc, vsc);
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ softmax (warps 4-7: A, 8-11: B)
+        const int x = (warp - 4) >> 2;
+        const int quad = warp & 3;                          // TMEM lanes this warp may access
+        const int trow = quad * 32 + lane;
+        const int e = trow / HPG, h = trow - e * HPG;
+        const uint32_t t_s = tmem + (uint32_t(quad * 32) << 16) + uint32_t(x * 128);
+        const uint32_t t_o = tmem + (uint32_t(quad * 32) << 16) + 256u + uint32_t(x * D);
+        const float scale = a.sm_scale * kLog2e;
+        const uint64_t scale2 = dup2(scale);
+        int row = -1, req = -1, pos = -1;                   // of this thread, in the item at hand
+        float ref = -INFINITY, l = 0.f;
+        bool poison = false;
+        for (int s = 0;; ++s) {
+            const int slot = s % kRing;
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm.desc_full[slot], (s / kRing) & 1, err, &sm.abort))) break;
+            const int flags = steps[slot].flags, base = steps[slot].base, sreq = steps[slot].req;
+            const int row0 = steps[slot].row0, g = steps[slot].g;
+            uint32_t nan_v[4] = {0u, 0u, 0u, 0u};
+            if (flags & kNan) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) nan_v[i] = steps[slot].nan_v[i];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.desc_empty[slot]);
+            if (flags & kEnd) break;
+            if (flags & kFirst) {
+                row = row0 + x * EPT + e;
+                req = row < a.n_rows ? a.q_req[row] : -1;
+                pos = row < a.n_rows ? a.q_pos[row] : 0;
+                ref = -INFINITY;
+                l = 0.f;
+                poison = false;
+            }
+            // tokens c of the page with c <= hi and (c >= lo or c < sk) are visible
+            const int hi = req == sreq ? pos - base : -1;
+            const int lo = pos - (a.window - 1) - base, sk = min(a.n_sink - base, 128);
+            const bool whole = hi >= 127 && (lo <= 0 || sk >= 128);
+            const bool all_whole = __all_sync(0xffffffffu, whole);
+            if (flags & kNan) {
+#pragma unroll 1
+                for (int c = 0; c < 128; ++c)
+                    if (nan_v[c >> 5] >> (c & 31) & 1u) poison |= c <= hi && (c >= lo || c < sk);
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], s & 1, err, &sm.abort))) break;
+            tc_fence_after();
+            // pass 1: the row's maximum
+            float mx[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll 1
+            for (int c0 = 0; c0 < 128; c0 += 64) {
+                uint32_t vv[2][32];
+                tmem_ld32(t_s + uint32_t(c0), vv[0]);
+                tmem_ld32(t_s + uint32_t(c0 + 32), vv[1]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int c = c0 + 32 * hh;
+                    const uint32_t(&v)[32] = vv[hh];
+                    if (all_whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 16)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                mx[j] = fmax3(mx[j], __uint_as_float(v[i + j]), __uint_as_float(v[i + 8 + j]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const bool see = c + i <= hi && (c + i >= lo || c + i < sk);
+                            mx[i & 7] = fmaxf(mx[i & 7], see ? __uint_as_float(v[i]) : -INFINITY);
+                        }
+                    }
+                }
+            }
+            const float m = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * scale;
+            // raise the reference where a logit passes it too far; O so far is brought to the new one
+            const bool raise = m > ref + kRaise;            // false for rows that see nothing
+            if (__any_sync(0xffffffffu, raise)) {
+                const float nref = raise ? m : ref;
+                const float al = ref == -INFINITY || !raise ? 1.f : fast_exp2(ref - nref);
+                ref = nref;
+                l *= al;
+                if (!(flags & kFirst)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_full[x], (s - 1) & 1, err, &sm.abort))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        asm volatile(
+                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+                            "%12, %13, %14, %15}, [%16];"
+                            : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                              "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
+                              "=r"(o[14]), "=r"(o[15])
+                            : "r"(t_o + uint32_t(c)));
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                        tmem_st16(t_o + uint32_t(c), o);
+                    }
+                }
+            }
+            // pass 2: P as bf16 over the columns already read, and its sum
+            const uint64_t nref2 = dup2(ref == -INFINITY ? 0.f : -ref);
+            uint64_t acc2[4] = {0, 0, 0, 0};
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(t_s + uint32_t(c), v);
+                tmem_ld_wait();
+                if (!all_whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const bool see = c + i <= hi && (c + i >= lo || c + i < sk);
+                        v[i] = see ? v[i] : 0xff800000u;
+                    }
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float xa, xb;
+                    ffma2(xa, xb, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), scale2, nref2);
+                    const float pa = fast_exp2(xa), pb = fast_exp2(xb);
+                    w[i] = pack_bf16x2(pa, pb);
+                    fadd2_acc(acc2[i & 3], pa, pb);
+                }
+                tmem_st16(t_s + uint32_t(c >> 1), w);
+            }
+            l += (sum2(acc2[0]) + sum2(acc2[1])) + (sum2(acc2[2]) + sum2(acc2[3]));
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[x]);
+            if (flags & kLast) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_full[x], s & 1, err, &sm.abort))) break;
+                tc_fence_after();
+                const bool live = row < a.n_rows && req != -1;
+                const size_t head = live ? size_t(row) * a.Hq + g * HPG + h : 0;
+                float inv = l == 0.f ? 0.f : 1.0f / l;
+                if (poison) inv = __uint_as_float(0x7fffffffu);
+                uint16_t *o_out = a.out + head * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(t_o + uint32_t(c), o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint4 w;
+                        w.x = pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+                        w.y = pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                        w.z = pack_bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+                        w.w = pack_bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+                        if (live) *reinterpret_cast<uint4 *>(o_out + c + i) = w;
+                    }
+                }
+                if (live) a.lse[head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+                tc_fence_before();
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D, int HPG>
+cudaError_t launch_t(const void *q, Args a, const Shape &s, cudaStream_t st) {
+    alignas(64) CUtensorMap qm;
+    const char *why = nullptr;
+    const uint64_t dims[3] = {uint64_t(D), uint64_t(s.Hq), uint64_t(a.n_rows)};
+    const uint64_t strides[2] = {uint64_t(D) * 2, uint64_t(s.Hq) * D * 2};
+    const uint32_t box[3] = {64u, uint32_t(HPG), uint32_t(128 / HPG)};
+    if (!encode_tensor_map(&qm, 3, q, dims, strides, box, 128, &why)) return cudaErrorInvalidValue;
+    constexpr int kRows = 2 * 128 / HPG;
+    const long long items = ((a.n_rows + kRows - 1LL) / kRows) * s.G;
+    if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    a.n_items = int(items);
+    const size_t smem = sizeof(Smem<D>) + 1024;
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_window_q8<D, HPG>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    return launch_kernel(k_window_q8<D, HPG>, dim3(unsigned(std::min<long long>(items, sm_count()))), dim3(kThreads), smem,
+                         st, false, a, qm);
+}
+
+}  // namespace
+
+cudaError_t launch_window_prefill_q8(const void *q, const CacheQ8 &c, const int32_t *block_table, const int32_t *q_req,
+                                     const int32_t *q_pos, int n_rows, int n_req, int n_pages, int window, int n_sink,
+                                     const Shape &s, void *out, float *lse, int32_t *err, cudaStream_t st) {
+    Args a = {};
+    a.k = static_cast<const uint8_t *>(c.k);
+    a.k_scale = static_cast<const uint8_t *>(c.k_scale);
+    a.v = static_cast<const uint8_t *>(c.v);
+    a.v_scale = static_cast<const uint8_t *>(c.v_scale);
+    a.block_table = block_table;
+    a.q_req = q_req;
+    a.q_pos = q_pos;
+    a.n_rows = n_rows;
+    a.n_req = n_req;
+    a.n_pages = n_pages;
+    a.max_blocks = s.max_blocks;
+    a.Hq = s.Hq;
+    a.G = s.G;
+    a.window = window;
+    a.n_sink = n_sink;
+    a.sm_scale = s.sm_scale;
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.err = err;
+#define MSA_WQ_CASE(DD, HH) \
+    if (s.D == DD && s.hpg == HH) return launch_t<DD, HH>(q, a, s, st);
+    MSA_WQ_CASE(128, 8) MSA_WQ_CASE(128, 4) MSA_WQ_CASE(64, 8) MSA_WQ_CASE(64, 4)
+#undef MSA_WQ_CASE
+    return cudaErrorNotSupported;
+}
+
+}  // namespace msa

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -799,10 +800,14 @@ msa_status_t msa_window_attn_q8(const void *q, const msa_cache_q8_t *cache, cons
     if (st != MSA_OK) return st;
     MSA_REQUIRE(q && block_table && q_req && q_pos && out && lse && err_word, "msa_window_attn_q8: NULL pointer");
     MSA_REQUIRE(!misaligned16({q, out}), "msa_window_attn_q8: q and out must be 16-byte aligned");
-    if (s.max_blocks > 1 << 24) return fail(MSA_ERR_UNSUPPORTED, "msa_window_attn_q8: max_blocks > 2^24");
+    if (s.max_blocks > 1 << 22) return fail(MSA_ERR_UNSUPPORTED, "msa_window_attn_q8: max_blocks > 2^22");
     if (1LL * n_rows * s.G > kQ8MaxRows) return fail(MSA_ERR_UNSUPPORTED, "msa_window_attn_q8: n_rows*G > 2^26");
-    const cudaError_t e = launch_window_decode_q8(q, c, block_table, q_req, q_pos, n_rows, n_req, n_pages, window,
-                                                  n_sink, s, out, lse, err_word, static_cast<cudaStream_t>(stream));
+    // a window or a number of sinks past the longest context says no more than that one, and stays in 30 bits
+    window = std::min(window, s.max_blocks * 128);
+    n_sink = std::min(n_sink, s.max_blocks * 128);
+    auto launch = phase == MSA_PHASE_DECODE ? launch_window_decode_q8 : launch_window_prefill_q8;
+    const cudaError_t e = launch(q, c, block_table, q_req, q_pos, n_rows, n_req, n_pages, window, n_sink, s, out, lse,
+                                 err_word, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_window_attn_q8");
 }
 

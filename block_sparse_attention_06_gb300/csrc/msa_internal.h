@@ -187,6 +187,10 @@ cudaError_t launch_attn_decode_q8(const void *q, const CacheQ8 &c, const int32_t
 cudaError_t launch_window_decode_q8(const void *q, const CacheQ8 &c, const int32_t *block_table, const int32_t *q_req,
                                     const int32_t *q_pos, int n_rows, int n_req, int n_pages, int window, int n_sink,
                                     const Shape &s, void *out, float *lse, int32_t *err, cudaStream_t st);
+// The same window attention with runs of consecutive rows sharing their reads, on the tensor cores.
+cudaError_t launch_window_prefill_q8(const void *q, const CacheQ8 &c, const int32_t *block_table, const int32_t *q_req,
+                                     const int32_t *q_pos, int n_rows, int n_req, int n_pages, int window, int n_sink,
+                                     const Shape &s, void *out, float *lse, int32_t *err, cudaStream_t st);
 
 // Tensor-map creation through the driver entry point (no libcuda link dependency).
 bool encode_tensor_map(void *map, int rank, const void *base, const uint64_t *dims,

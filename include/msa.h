@@ -564,7 +564,8 @@ msa_status_t msa_commit_tree(const void *k_new, const void *v_new, const void *k
  *   codes   e4m3 [n_pages][G][128][D] (k, v) and [n_pages][G][128][Di] (kidx): the slice
  *           of one page and group is one contiguous run
  *   scales  uint8 [n_pages][G][128]: byte b of a (token, group) row stands for 2^(b - 127)
- *           (255: NaN); value = code * 2^(b - 127)
+ *           (255: NaN); value = code * 2^(b - 127).  The codes of a NaN (0x7f, 0xff) stand
+ *           in rows of scale 255 only
  *
  * The scale is the smallest power of two under which the row's largest magnitude is at most
  * 448 (the largest code), at least 2^-100, and 1 for a row of zeros.  Values are rounded
@@ -652,7 +653,7 @@ msa_status_t msa_index_score_q8(const void *q_idx, const msa_cache_q8_t *cache, 
  *   q bf16 [B][Hq][D];  page_table int32 [B*G][topk];  row_len int32 [B*G]
  *   out bf16 [B][Hq][D] out;  lse fp32 [B][Hq] out.  A row that sees nothing gets 0 and -inf.
  * What a row does not see does not reach it, whatever its bits; a NaN that it sees makes it NaN.  q is finite
- * (else its row is NaN); components below 2^-40 of a head's largest count as 0.  V's scales are at most 2^87.
+ * (else its row is NaN); components below 2^-40 of a head's largest count as 0.
  */
 msa_status_t msa_sparse_attn_decode_q8(const void *q, const msa_cache_q8_t *cache, const int32_t *page_table,
                                        const int32_t *row_len, int32_t B, int32_t n_pages, const msa_dims_t *dims,
@@ -678,7 +679,7 @@ msa_status_t msa_decode_step_q8(const void *q, const void *q_idx, const msa_cach
  *   out bf16 [n_rows][Hq][D] out;  lse fp32 [n_rows][Hq] out.  A row with q_req -1 is padding: nothing of it is
  *          written.
  * A bad request or position, or a page outside [0, n_pages) of a block that a row sees, raises
- * MSA_FLAG_BOUNDS.  What is said of q, V and NaN at msa_sparse_attn_decode_q8 holds here.
+ * MSA_FLAG_BOUNDS.  What is said of q, V and NaN at msa_sparse_attn_decode_q8 holds here.  max_blocks <= 2^22.
  */
 msa_status_t msa_window_attn_q8(const void *q, const msa_cache_q8_t *cache, const int32_t *block_table,
                                 const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,

@@ -530,6 +530,45 @@ def test_window(msa, phase, Hq, G, D, ctx, n, window, sinks, pad):
 
 
 @pytest.mark.parametrize("phase", [0, 1])
+@pytest.mark.parametrize("exp", [-100, -7, 0, 9, 60])
+def test_window_all_codes(msa, phase, exp):
+    """Every finite code in V, subnormal ones among them, under small and large scales: rows that see one token."""
+    dims = msa.Dims(8, 1, 128, 64, 1, 2)
+    codes = torch.tensor([c for c in range(256) if c & 0x7f != 0x7f], dtype=torch.uint8)
+    k = torch.zeros((2, 1, 128, 128), dtype=torch.uint8)
+    v = k.clone()
+    v[0, 0, 0], v[1, 0, 0, :126] = codes[:128], codes[128:]
+    sc = torch.full((2, 1, 128), 127 + exp, dtype=torch.uint8)
+    cache = msa.CacheQ8(k.view(E4M3).cuda(), sc.view(E8M0).cuda(), v.view(E4M3).cuda(), sc.view(E8M0).cuda())
+    q = Q.normal((2, 8, 128), 1).cuda()
+    out, lse = msa.msa_window_attn_q8(q, cache, i32([[0, 1]]).cuda(), i32([0, 0]).cuda(), i32([0, 128]).cuda(), 1, 0, dims,
+                                      phase)
+    want = v.view(E4M3).float()[:, 0, 0] * 2.0 ** exp
+    assert torch.equal(out.float().cpu(), want[:, None].expand(2, 8, 128))
+    assert float(lse.abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("phase", [0, 1])
+def test_window_all_key_codes(msa, phase):
+    """Every finite code in K: the log-sum of a row that sees one token is its logit."""
+    dims = msa.Dims(8, 1, 128, 64, 1, 2, 1.0)
+    codes = torch.tensor([c for c in range(256) if c & 0x7f != 0x7f], dtype=torch.uint8)
+    k = torch.zeros((2, 1, 128, 128), dtype=torch.uint8)
+    flat = k[:, 0].reshape(-1, 128)
+    flat[torch.arange(254), torch.arange(254) % 128] = codes
+    one = torch.full((2, 1, 128), 127, dtype=torch.uint8)
+    cache = msa.CacheQ8(k.view(E4M3).cuda(), one.view(E8M0).cuda(), torch.zeros_like(k).view(E4M3).cuda(),
+                        one.view(E8M0).cuda())
+    q = torch.zeros((254, 8, 128), dtype=torch.bfloat16)
+    q[torch.arange(254), :, torch.arange(254) % 128] = 1.0
+    out, lse = msa.msa_window_attn_q8(q.cuda(), cache, i32([[0, 1]]).cuda(), i32([0] * 254).cuda(),
+                                      torch.arange(254, dtype=torch.int32).cuda(), 1, 0, dims, phase)
+    want = codes.view(E4M3).float()[:, None].expand(254, 8)
+    assert float((lse.cpu() - want).abs().max() / 448) < 2.0 ** -22 and bool((out == 0).all())
+    assert float(((lse.cpu() - want).abs() / want.abs().clamp(min=2.0 ** -9)).max()) < 2.0 ** -20
+
+
+@pytest.mark.parametrize("phase", [0, 1])
 def test_window_rows_in_any_order(msa, phase):
     """Rows of several requests, shuffled, with padding among them; one row twice."""
     bt, pool = Q.tables([400, 260, 150], 1)
