@@ -7,7 +7,7 @@
 // ref is a row's reference: its maximum so far, raised only when a logit passes it by 2^8, so O is next to never
 // rescaled; out = O / l, lse = ref + log l.
 //
-// K and V come as codes and scales; four warps turn a page into bf16 tiles in shared memory, exactly (a code
+// K and V come as codes and scales; eight warps turn a page into bf16 tiles in shared memory, exactly (a code
 // becomes code * 2^-120 by shifts and masks, one multiplication by a power of two gives the value), so the MMAs
 // round nothing of the cache.  A row of V that is NaN is written as zeros and the rows that see it are made NaN
 // at the end: what a row does not see cannot reach it, whatever its bits.
@@ -17,12 +17,12 @@
 // 128 logits, conversion of 32 KB of codes).  So the two tiles take turns: while one's softmax runs, the tensor cores
 // work on the other's S and P V.
 //
-// One CTA per SM, 16 warps, persistent over items:
+// One CTA per SM, 20 warps, persistent over items:
 //   warp 0     planner: for each item the pages that any of its rows sees, in a ring of step descriptors;
 //   warp 1     MMA issuer and TMEM owner: S_A(s), P V of B(s-1), S_B(s), P V of A(s), ...;
 //   warp 2     Q loader (TMA, one box per tile and 64 columns);   warp 3  idle;
 //   warps 4-7, 8-11   softmax of tiles A and B, one row per thread; each also writes its tile's results;
-//   warps 12-15  converters: K and V of the next page wait in registers while this one's are written.
+//   warps 12-19  converters: K and V of the next two pages wait in registers while this one's are written.
 // TMEM: S_A | S_B | O_A | O_B (128 + 128 + D + D columns); P is written over S.
 // Every wait is bounded; a timeout raises MSA_FLAG_TIMEOUT and every role drains.
 #include "msa_internal.h"
@@ -33,7 +33,7 @@
 namespace msa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 896;
 constexpr int kRing = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -60,6 +60,7 @@ struct Smem {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], o_full[2];   // per tile
+    float part[2][2][128];       // per tile and half of the page: a row's maximum, at the end its sum
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -101,27 +102,67 @@ __device__ __forceinline__ float sum2(uint64_t acc2) {
     return a + b;
 }
 
+// The lowest n bits set, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t ones_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // D/16 MMAs of S = Q K^T, both operands K-major with the 128-byte swizzle: a k-step of 16 columns is 32 bytes
 // further in a sub-tile of 64 columns, and sub-tiles are 16 KB apart.
+// One asm block, so that the issuing thread spends as few issue slots as it can.
 template <int D>
 __device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-        const uint64_t off = uint64_t((i >> 2) * 1024 + (i & 3) * 2);
-        mma_bf16(d, a + off, b + off, idesc, i > 0);
+    if constexpr (D == 128) {
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+            "setp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
+            "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 1024;\n\t"
+            "add.s64 b5, %2, 1026;\n\tadd.s64 b6, %2, 1028;\n\tadd.s64 b7, %2, 1030;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+            "setp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
+            : "memory");
     }
 }
 
-// Eight MMAs of O (+)= P V: P in TMEM (bf16 pairs, 8 columns per 16 tokens), V MN-major, 16 tokens 2 KB apart.
+// Eight MMAs of O (+)= P V: P in TMEM (bf16 pairs, 8 columns per 16 tokens, the halves of 64 tokens 64 columns
+// apart), V MN-major, 16 tokens 2 KB apart.
 __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t accumulate) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(p + uint32_t(i * 8)), "l"(v + uint64_t(i * 128)), "r"(idesc), "r"(i > 0 ? 1u : accumulate)
-            : "memory");
-    }
+    asm volatile(
+        "{\n\t.reg .pred f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+        "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 64;\n\t"
+        "add.s32 a5, %1, 72;\n\tadd.s32 a6, %1, 80;\n\tadd.s32 a7, %1, 88;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
+        "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
+        "r"(p), "l"(v), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -130,8 +171,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// 16 codes as 16 bf16 values.  f: 2^(120 + min(e, 0)) in both halves; up: 2^max(e, 0), applied where `big`.
-__device__ __forceinline__ void convert16(const uint4 &w, uint32_t f, uint32_t up, bool big, uint32_t (&o)[8]) {
+// 16 codes as 16 bf16 numbers code * 2^-120 * f (f: a bf16 number in both halves).
+__device__ __forceinline__ void convert16(const uint4 &w, uint32_t f, uint32_t (&o)[8]) {
     const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -140,13 +181,17 @@ __device__ __forceinline__ void convert16(const uint4 &w, uint32_t f, uint32_t u
         o[2 * i] = mul_bf16x2(((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u), f);
         o[2 * i + 1] = mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), f);
     }
-    if (big) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], up);
-    }
 }
 
-__device__ __forceinline__ uint32_t bf16x2_exp2(int e) { return uint32_t((e + 127) << 7) * 0x10001u; }
+// 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 
 template <int D, int HPG>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -163,17 +208,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sm.desc_full[i], 32);
-            mbar_init(&sm.desc_empty[i], 14);   // issuer, Q loader, 8 softmax warps, 4 converter warps
+            mbar_init(&sm.desc_empty[i], 26);   // issuer, Q loader, 16 softmax warps, 8 converter warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_empty[i], 1);
-            mbar_init(&sm.k_full[i], 4);
+            mbar_init(&sm.k_full[i], 8);
             mbar_init(&sm.k_empty[i], 1);
-            mbar_init(&sm.v_full[i], 4);
+            mbar_init(&sm.v_full[i], 8);
             mbar_init(&sm.v_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.p_full[i], 8);
             mbar_init(&sm.o_full[i], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -184,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&sm.tmem_base, 512);
         tmem_relinquish();
     }
-    if (warp == 2 && lane == 0) tma_prefetch_desc(&qmap);
+    if (warp == 21 && lane == 0) tma_prefetch_desc(&qmap);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -340,12 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t vd[2] = {make_smem_desc(smem_u32(sm.v[0]), 16384, 1024, 2),
                                     make_smem_desc(smem_u32(sm.v[1]), 16384, 1024, 2)};
             // P V of tile x at step s; `first`: overwrite O
-            auto issue_pv = [&](int x, int s, bool first) -> bool {
+            auto issue_pv = [&](int x, int s, bool first, bool last) -> bool {
                 if (!mbar_wait(&sm.p_full[x], s & 1, err, &sm.abort)) return false;
                 if (x == 0 && !mbar_wait(&sm.v_full[s & 1], (s >> 1) & 1, err, &sm.abort)) return false;
                 tc_fence_after();
                 mma_pv(tmem + 256u + uint32_t(x * D), tmem + uint32_t(x * 128), vd[s & 1], kIdescO, first ? 0u : 1u);
-                mma_commit(&sm.o_full[x]);
+                if (last) mma_commit(&sm.o_full[x]);
                 if (x == 1) mma_commit(&sm.v_empty[s & 1]);
                 return true;
             };
@@ -366,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (last) mma_commit(&sm.q_empty[0]);
                 if (b_pending) {
                     b_pending = false;
-                    if (!issue_pv(1, s - 1, b_first)) break;
+                    if (!issue_pv(1, s - 1, b_first, false)) break;
                 }
                 if (first && !mbar_wait(&sm.q_full[1], items & 1, err, &sm.abort)) break;
                 if (first) ++items;
@@ -375,18 +420,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(&sm.s_full[1]);
                 mma_commit(&sm.k_empty[s & 1]);
                 if (last) mma_commit(&sm.q_empty[1]);
-                if (!issue_pv(0, s, first)) break;
+                if (!issue_pv(0, s, first, last)) break;
                 b_pending = true;
                 b_first = first;
                 if (last) {              // the item's results wait for it, and the next item's Q is still on its way
                     b_pending = false;
-                    if (!issue_pv(1, s, first)) break;
+                    if (!issue_pv(1, s, first, last)) break;
                 }
             }
             mma_commit(&sm.drain);
             mbar_wait(&sm.drain, 0, err, nullptr);
         }
-    } else if (warp == 2) {
+    } else if (warp == 21) {
         // ------------------------------------------------------------ Q loader (lane 0)
         if (lane == 0) {
             int items = 0, loaded[2] = {0, 0};
@@ -416,108 +461,125 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < 2; ++x)
                     if (loaded[x] > 0) mbar_wait(&sm.q_full[x], (loaded[x] - 1) & 1, err, nullptr);
         }
-    } else if (warp >= 12) {
+    } else if (warp == 25) {
+        // idle: it would share the MMA issuer's sub-partition
+    } else if (warp >= 20 || warp == 2 || warp == 3) {
         // ------------------------------------------------------------ converters
-        // A thread takes TPT consecutive tokens, 16 codes of each (its lane's column); a quarter warp's stores
-        // fill eight different 16-byte columns: the upper four lanes store their two in the other order.
+        // A thread takes TPT consecutive tokens, 16 codes of each (its lane's column).  The upper four lanes of a
+        // quarter warp take them in the order 1, 0, 3, 2: the swizzle then puts the eight stores of a quarter warp
+        // into eight different 16-byte columns.
         constexpr int LPT = D / 16;      // lanes per token
-        constexpr int TPT = LPT;         // tokens per thread (128 threads, 128 tokens)
-        const int w = warp - 12;
+        constexpr int TPT = LPT / 2;     // tokens per thread (256 threads, 128 tokens)
+        // warps 2, 3, 20, 22, 23, 24, 26, 27: none in the MMA issuer's sub-partition (warp index mod 4 = 1)
+        const int w = warp < 4 ? warp - 2 : warp == 20 ? 2 : warp < 24 ? warp - 19 : warp == 24 ? 5 : warp - 20;
         const int col = lane % LPT, tok0 = (w * (32 / LPT) + lane / LPT) * TPT;
         const int swap = (lane >> 2) & 1;
         const uint32_t sub = uint32_t(col >> 2) * 16384u;   // sub-tile of 64 columns
         const int ch = (col & 3) * 2;                       // its first 16-byte chunk
-        uint4 kc[TPT], vc[TPT];
-        uint32_t ks[TPT / 4], vsc[TPT / 4];
-        auto load = [&](const uint8_t *codes, const uint8_t *scales, int page, int g, uint4 (&c)[TPT],
-                        uint32_t (&sc)[TPT / 4]) {
+        struct Rows {
+            uint4 c[TPT];
+            uint32_t sc;                 // scale bytes in the order of c
+        };
+        auto load = [&](const uint8_t *codes, const uint8_t *scales, int page, int g, Rows &x) {
             const size_t line = (size_t(page) * a.G + g) * 128 + tok0;
 #pragma unroll
-            for (int i = 0; i < TPT; ++i) c[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (line + i) * D + col * 16));
-#pragma unroll
-            for (int i = 0; i < TPT / 4; ++i) sc[i] = __ldg(reinterpret_cast<const uint32_t *>(scales + line) + i);
+            for (int i = 0; i < TPT; ++i)
+                x.c[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (line + (i ^ swap)) * D + col * 16));
+            uint32_t sc;
+            if constexpr (TPT == 4) sc = __ldg(reinterpret_cast<const uint32_t *>(scales + line));
+            else sc = __ldg(reinterpret_cast<const uint16_t *>(scales + line));
+            x.sc = swap ? __byte_perm(sc, 0u, 0x2301) : sc;
         };
-        auto store = [&](uint8_t *tile, const uint4 (&c)[TPT], const uint32_t (&sc)[TPT / 4], bool values) {
+        auto store = [&](uint8_t *tile, const Rows &x, bool values) {
             const uint32_t base = smem_u32(tile) + sub;
+            const bool usual = (x.sc & 0x80808080u) == 0u;   // no scale above 1, no NaN row
 #pragma unroll
             for (int i = 0; i < TPT; ++i) {
-                const int t = tok0 + i;
-                const uint32_t b = (sc[i / 4] >> (8 * (i & 3))) & 255u;
-                const int e = int(b) - 127;
-                uint32_t f = bf16x2_exp2(120 + min(max(e, -126 - 120), 0));
-                // a NaN row: of K NaN, so the logits of the rows that see it are; of V zeros (see above)
-                if (b == 255u) f = values ? 0u : 0x7fff7fffu;
+                const int t = tok0 + (i ^ swap);
+                const uint32_t b = (x.sc >> (8 * i)) & 255u;
                 uint32_t o[8];
-                convert16(c[i], f, bf16x2_exp2(min(max(e, 0), 127)), e > 0 && b != 255u, o);
+                if (usual) {             // 2^(120 + e), e = b - 127
+                    convert16(x.c[i], (b + 120u) * 0x00800080u, o);
+                } else {
+                    // 2^120 and then 2^e where e > 0; a NaN row: of K NaN, so the logits of the rows that see it are; of
+                    // V zeros (see above)
+                    const uint32_t f = b == 255u ? (values ? 0u : 0x7fff7fffu) : (min(b, 127u) + 120u) * 0x00800080u;
+                    const uint32_t up = b == 255u ? 0x3f803f80u : max(b, 127u) * 0x00800080u;
+                    convert16(x.c[i], f, o);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], up);
+                }
                 const uint32_t row = base + uint32_t(t * 128);
-                const int x0 = (ch + swap) ^ (t & 7), x1 = (ch + 1 - swap) ^ (t & 7);
-                const uint32_t p0 = row + uint32_t(x0 << 4), p1 = row + uint32_t(x1 << 4);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0), "r"(swap ? o[4] : o[0]),
-                             "r"(swap ? o[5] : o[1]), "r"(swap ? o[6] : o[2]), "r"(swap ? o[7] : o[3]) : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p1), "r"(swap ? o[0] : o[4]),
-                             "r"(swap ? o[1] : o[5]), "r"(swap ? o[2] : o[6]), "r"(swap ? o[3] : o[7]) : "memory");
+                const uint32_t p0 = row + uint32_t((ch ^ (t & 7)) << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                             "r"(o[3]) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0 ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]),
+                             "r"(o[7]) : "memory");
             }
+            fence_proxy_async_smem();
+            __syncwarp();
         };
-        // descriptor of step s: its flags, with page and group
-        auto desc = [&](int s, int *flags, int *page, int *g) -> bool {
-            const int slot = s % kRing;
-            if (!__all_sync(0xffffffffu, mbar_wait(&sm.desc_full[slot], (s / kRing) & 1, err, &sm.abort))) return false;
-            *flags = steps[slot].flags;
-            *page = steps[slot].page;
-            *g = steps[slot].g;
+        // the next step's descriptor; false at the end
+        int sd = 0, page = 0, g = 0;
+        auto desc = [&]() -> bool {
+            const int slot = sd % kRing;
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm.desc_full[slot], (sd / kRing) & 1, err, &sm.abort))) return false;
+            const int flags = steps[slot].flags;
+            page = steps[slot].page;
+            g = steps[slot].g;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.desc_empty[slot]);
-            return true;
+            ++sd;
+            return !(flags & kEnd);
         };
-        int flags, page, g;
-        bool ok = desc(0, &flags, &page, &g);
-        if (ok && !(flags & kEnd)) {
-            load(a.k, a.k_scale, page, g, kc, ks);
-            load(a.v, a.v_scale, page, g, vc, vsc);
+        Rows kc, vc;
+        bool more = desc();              // there is a step that is not written yet
+        if (more) {
+            load(a.k, a.k_scale, page, g, kc);
+            load(a.v, a.v_scale, page, g, vc);
         }
-        for (int s = 0; ok && !(flags & kEnd); ++s) {
+        for (int s = 0; more; ++s) {
             const int b = s & 1;
             if (s >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.k_empty[b], ((s >> 1) - 1) & 1, err, &sm.abort))) break;
-            store(sm.k[b], kc, ks, false);
-            fence_proxy_async_smem();
-            __syncwarp();
+            store(sm.k[b], kc, false);
             if (lane == 0) mbar_arrive(&sm.k_full[b]);
-            ok = desc(s + 1, &flags, &page, &g);
-            const bool more = ok && !(flags & kEnd);
-            if (more) load(a.k, a.k_scale, page, g, kc, ks);
+            more = desc();
+            if (more) load(a.k, a.k_scale, page, g, kc);
             if (s >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.v_empty[b], ((s >> 1) - 1) & 1, err, &sm.abort))) break;
-            store(sm.v[b], vc, vsc, true);
-            fence_proxy_async_smem();
-            __syncwarp();
+            store(sm.v[b], vc, true);
             if (lane == 0) mbar_arrive(&sm.v_full[b]);
-            if (more) load(a.v, a.v_scale, page, g, vc, vsc);
+            if (more) load(a.v, a.v_scale, page, g, vc);
         }
     } else if (warp >= 4) {
-        // ------------------------------------------------------------ softmax (warps 4-7: A, 8-11: B)
-        const int x = (warp - 4) >> 2;
+        // ------------------------------------------------------------ softmax (warps 4-11: A, 12-19: B)
+        // A row is two threads, 64 tokens of the page each: their warps read the same TMEM lanes.
+        const int x = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1;
         const int quad = warp & 3;                          // TMEM lanes this warp may access
         const int trow = quad * 32 + lane;
         const int e = trow / HPG, h = trow - e * HPG;
-        const uint32_t t_s = tmem + (uint32_t(quad * 32) << 16) + uint32_t(x * 128);
-        const uint32_t t_o = tmem + (uint32_t(quad * 32) << 16) + 256u + uint32_t(x * D);
+        const uint32_t t_s = tmem + (uint32_t(quad * 32) << 16) + uint32_t(x * 128 + hf * 64);
+        const uint32_t t_o = tmem + (uint32_t(quad * 32) << 16) + 256u + uint32_t(x * D + hf * (D / 2));
         const float scale = a.sm_scale * kLog2e;
         const uint64_t scale2 = dup2(scale);
+        float *const mine = &sm.part[x][hf][trow];
+        const volatile float *const other = &sm.part[x][hf ^ 1][trow];
+        auto meet = [&]() {              // the two warps of these rows
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + x * 4 + quad) : "memory");
+        };
         int row = -1, req = -1, pos = -1;                   // of this thread, in the item at hand
+        int items = 0;                   // done
         float ref = -INFINITY, l = 0.f;
         bool poison = false;
         for (int s = 0;; ++s) {
             const int slot = s % kRing;
-            if (!__all_sync(0xffffffffu, mbar_wait(&sm.desc_full[slot], (s / kRing) & 1, err, &sm.abort))) break;
-            const int flags = steps[slot].flags, base = steps[slot].base, sreq = steps[slot].req;
+            bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.desc_full[slot], (s / kRing) & 1, err, &sm.abort));
+            const int flags = steps[slot].flags, base = steps[slot].base + hf * 64, sreq = steps[slot].req;
             const int row0 = steps[slot].row0, g = steps[slot].g;
-            uint32_t nan_v[4] = {0u, 0u, 0u, 0u};
-            if (flags & kNan) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) nan_v[i] = steps[slot].nan_v[i];
-            }
+            uint64_t nan_v = 0u;
+            if (flags & kNan) nan_v = uint64_t(steps[slot].nan_v[2 * hf + 1]) << 32 | steps[slot].nan_v[2 * hf];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.desc_empty[slot]);
-            if (flags & kEnd) break;
+            if (ok && lane == 0) mbar_arrive(&sm.desc_empty[slot]);
+            if (!ok || (flags & kEnd)) break;
             if (flags & kFirst) {
                 row = row0 + x * EPT + e;
                 req = row < a.n_rows ? a.q_req[row] : -1;
@@ -526,48 +588,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = 0.f;
                 poison = false;
             }
-            // tokens c of the page with c <= hi and (c >= lo or c < sk) are visible
+            // Tokens c of this half with c <= hi and (c >= lo or c < sk) are visible: bit c % 32 of word c / 32.  Rows of
+            // a tile are near one another, so most words are all ones or all zeros in the whole warp.
             const int hi = req == sreq ? pos - base : -1;
-            const int lo = pos - (a.window - 1) - base, sk = min(a.n_sink - base, 128);
-            const bool whole = hi >= 127 && (lo <= 0 || sk >= 128);
-            const bool all_whole = __all_sync(0xffffffffu, whole);
-            if (flags & kNan) {
-#pragma unroll 1
-                for (int c = 0; c < 128; ++c)
-                    if (nan_v[c >> 5] >> (c & 31) & 1u) poison |= c <= hi && (c >= lo || c < sk);
+            const int lo = pos - (a.window - 1) - base, sk = a.n_sink - base;
+            uint32_t see[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t below = ones_below(hi + 1 - 32 * k);
+                see[k] = below & (~ones_below(lo - 32 * k) | ones_below(sk - 32 * k));
             }
-            if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], s & 1, err, &sm.abort))) break;
+            if (nan_v) {
+                poison |= (uint32_t(nan_v) & see[0]) != 0u || (uint32_t(nan_v >> 32) & see[1]) != 0u;
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], s & 1, err, &sm.abort));
             tc_fence_after();
-            // pass 1: the row's maximum
+            // pass 1: the row's maximum, over both halves
             float mx[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
 #pragma unroll 1
-            for (int c0 = 0; c0 < 128; c0 += 64) {
-                uint32_t vv[2][32];
-                tmem_ld32(t_s + uint32_t(c0), vv[0]);
-                tmem_ld32(t_s + uint32_t(c0 + 32), vv[1]);
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t bits = k ? see[1] : see[0];
+                if (!__any_sync(0xffffffffu, bits != 0u)) continue;
+                uint32_t v[32];
+                tmem_ld32(t_s + uint32_t(32 * k), v);
                 tmem_ld_wait();
+                if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int c = c0 + 32 * hh;
-                    const uint32_t(&v)[32] = vv[hh];
-                    if (all_whole) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 16)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                mx[j] = fmax3(mx[j], __uint_as_float(v[i + j]), __uint_as_float(v[i + 8 + j]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const bool see = c + i <= hi && (c + i >= lo || c + i < sk);
-                            mx[i & 7] = fmaxf(mx[i & 7], see ? __uint_as_float(v[i]) : -INFINITY);
-                        }
-                    }
+                    for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1u ? v[i] : 0xff800000u;
                 }
+#pragma unroll
+                for (int i = 0; i < 32; i += 16)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        mx[j] = fmax3(mx[j], __uint_as_float(v[i + j]), __uint_as_float(v[i + 8 + j]));
             }
-            const float m = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * scale;
+            float m = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * scale;
+            *mine = m;
+            meet();
+            m = fmaxf(m, *other);
             // raise the reference where a logit passes it too far; O so far is brought to the new one
             const bool raise = m > ref + kRaise;            // false for rows that see nothing
             if (__any_sync(0xffffffffu, raise)) {
@@ -575,19 +635,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float al = ref == -INFINITY || !raise ? 1.f : fast_exp2(ref - nref);
                 ref = nref;
                 l *= al;
-                if (!(flags & kFirst)) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_full[x], (s - 1) & 1, err, &sm.abort))) break;
-                    tc_fence_after();
+                if (!(flags & kFirst)) {   // S of this step came behind the P V before it: O is complete up to there
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
+                    for (int c = 0; c < D / 2; c += 16) {
                         uint32_t o[16];
-                        asm volatile(
-                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-                            "%12, %13, %14, %15}, [%16];"
-                            : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
-                              "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
-                              "=r"(o[14]), "=r"(o[15])
-                            : "r"(t_o + uint32_t(c)));
+                        tmem_ld16(t_o + uint32_t(c), o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
@@ -599,48 +651,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t nref2 = dup2(ref == -INFINITY ? 0.f : -ref);
             uint64_t acc2[4] = {0, 0, 0, 0};
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                uint32_t v[32];
-                tmem_ld32(t_s + uint32_t(c), v);
-                tmem_ld_wait();
-                if (!all_whole) {
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t bits = k ? see[1] : see[0];
+                uint32_t w[16];
+                if (!__any_sync(0xffffffffu, bits != 0u)) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const bool see = c + i <= hi && (c + i >= lo || c + i < sk);
-                        v[i] = see ? v[i] : 0xff800000u;
+                    for (int i = 0; i < 16; ++i) w[i] = 0u;
+                } else {
+                    uint32_t v[32];
+                    tmem_ld32(t_s + uint32_t(32 * k), v);
+                    tmem_ld_wait();
+                    if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1u ? v[i] : 0xff800000u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float xa, xb;
+                        ffma2(xa, xb, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), scale2, nref2);
+                        const float pa = fast_exp2(xa), pb = fast_exp2(xb);
+                        w[i] = pack_bf16x2(pa, pb);
+                        fadd2_acc(acc2[i & 3], pa, pb);
                     }
                 }
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float xa, xb;
-                    ffma2(xa, xb, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), scale2, nref2);
-                    const float pa = fast_exp2(xa), pb = fast_exp2(xb);
-                    w[i] = pack_bf16x2(pa, pb);
-                    fadd2_acc(acc2[i & 3], pa, pb);
-                }
-                tmem_st16(t_s + uint32_t(c >> 1), w);
+                tmem_st16(t_s + uint32_t(16 * k), w);
             }
             l += (sum2(acc2[0]) + sum2(acc2[1])) + (sum2(acc2[2]) + sum2(acc2[3]));
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[x]);
+            if (ok && lane == 0) mbar_arrive(&sm.p_full[x]);
             if (flags & kLast) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_full[x], s & 1, err, &sm.abort))) break;
+                meet();                  // both have read the maxima
+                *mine = poison ? -l : l;                    // the sign bit says that V was NaN
+                meet();
+                const float l2 = *other, sum = l + fabsf(l2);
+                const bool bad = poison || (__float_as_uint(l2) >> 31);
+                meet();                  // both have read the sums
+                ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[x], items & 1, err, &sm.abort)) && ok;
+                ++items;
                 tc_fence_after();
-                const bool live = row < a.n_rows && req != -1;
+                const bool live = ok && row < a.n_rows && req != -1;
                 const size_t head = live ? size_t(row) * a.Hq + g * HPG + h : 0;
-                float inv = l == 0.f ? 0.f : 1.0f / l;
-                if (poison) inv = __uint_as_float(0x7fffffffu);
-                uint16_t *o_out = a.out + head * D;
+                const float inv = bad ? __uint_as_float(0x7fffffffu) : sum == 0.f ? 0.f : 1.0f / sum;
+                uint16_t *o_out = a.out + head * D + hf * (D / 2);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(t_o + uint32_t(c), o);
+                for (int c = 0; c < D / 2; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(t_o + uint32_t(c), o);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
+                    for (int i = 0; i < 16; i += 8) {
                         uint4 w;
                         w.x = pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
                         w.y = pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
@@ -649,9 +710,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (live) *reinterpret_cast<uint4 *>(o_out + c + i) = w;
                     }
                 }
-                if (live) a.lse[head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+                if (live && hf == 0) a.lse[head] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
                 tc_fence_before();
             }
+            if (!ok) break;
         }
     }
 
