@@ -602,7 +602,7 @@ static msa_status_t check_cache_q8(const msa_cache_q8_t *c, bool kv, bool index,
                 "%s: codes must be 16-byte aligned", who);
     const uintptr_t sc = (kv ? reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale) : 0) |
                          (index ? reinterpret_cast<uintptr_t>(c->kidx_scale) : 0);
-    MSA_REQUIRE((sc & 3u) == 0, "%s: scales must be 4-byte aligned", who);
+    MSA_REQUIRE((sc & 15u) == 0, "%s: scales must be 16-byte aligned", who);
     return MSA_OK;
 }
 

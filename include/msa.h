@@ -573,7 +573,7 @@ msa_status_t msa_commit_tree(const void *k_new, const void *v_new, const void *k
  * its code is normal, and by 2^-18 of the row's largest magnitude below; each stored
  * value is also a bf16 number.  A row of k, v or k_idx that holds a NaN or an infinity is stored as
  * a row of NaN and raises MSA_FLAG_NAN.  The 8-bit pages are those of the same page ids and
- * block tables as the bf16 ones.  Codes and bf16 rows are 16-byte aligned, scales 4-byte.
+ * block tables as the bf16 ones.  Codes, scales and bf16 rows are 16-byte aligned.
  */
 typedef struct {
     void *k, *k_scale;          /* codes and scales of K                                   */

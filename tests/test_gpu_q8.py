@@ -308,6 +308,28 @@ def test_score(msa, G, Di, lens, more):
     Q.assert_within(got, want, tol, "scores")
 
 
+def test_score_many_rows(msa):
+    """More rows than a warp has lanes, bad ones among them: every range of units starts in its own row."""
+    lens = [1 + 37 * (i % 19) for i in range(300)]
+    bt, pool = Q.tables([max(lens)], 1)
+    dims = msa.Dims(8, 2, 64, 64, 2, bt.shape[1] + 1)
+    bt = torch.cat([bt, i32([[-1]])], 1)
+    cache, _ = make_cache(msa, dims, pool, 3)
+    q = Q.normal((300, 2, 64), 9)
+    pos = i32([n - 1 for n in lens])
+    req = i32([0] * 300)
+    err = msa.new_err_word("cuda")
+    got = msa.msa_index_score_q8(q.cuda(), cache, *cuda(bt, req, pos), dims, err_word=err)
+    msa.msa_check(err)
+    want, tol = Q.ref_scores(q, cache.kidx.cpu(), cache.kidx_scale.cpu(), bt, req, pos)
+    Q.assert_within(got, want, tol, "scores")
+    req[7], pos[200] = 1, -1
+    got = msa.msa_index_score_q8(q.cuda(), cache, *cuda(bt, req, pos), dims, err_word=err)
+    assert int(err) == 1
+    want[7], want[200] = -math.inf, -math.inf
+    Q.assert_within(got, want, tol, "scores")
+
+
 def test_score_small_components_count(msa):
     """Components 2^-16 and 2^-30 of the largest, alone with a key: the third piece holds them."""
     dims = msa.Dims(4, 1, 64, 32, 1, 1)

@@ -111,11 +111,11 @@ def test_bad_sizes_and_pointers(lib):  # noqa: F811
     for name in ("k", "k_scale", "v", "v_scale"):
         for call in (_append8, _read, _attn, _step, _window):
             assert call(lib, d, c=cache(**{name: None})) == 1, name
-            assert call(lib, d, c=cache(**{name: 0x1002})) == 1, name
+            assert call(lib, d, c=cache(**{name: 0x1004})) == 1, name
     for name in ("kidx", "kidx_scale"):
         for call in (_append8, _read, _score, _step):
             assert call(lib, d, c=cache(**{name: None})) == 1, name
-            assert call(lib, d, c=cache(**{name: 0x1002})) == 1, name
+            assert call(lib, d, c=cache(**{name: 0x1004})) == 1, name
     assert _append(lib, d, kidx=None) == 1
 
 
