@@ -5,24 +5,27 @@
 //
 // What bounds it is the read of K and V (one byte per component, and two scale bytes per token), and with
 // few rows the latency of a chain: table, K, softmax, join.  So:
-//   - a unit is 32 tokens of one page, and one warp takes a unit on its own, from global memory straight into
-//     MMA operands, with its own running maximum and sum: no shared memory, no barrier until the row's end.  K
-//     and V of a unit are loaded together, K of the next one while this one's softmax and P V run.
-//   - a row's units are dealt to the warps of a cluster of CTAs (more CTAs where there are few rows), whose
-//     partials are joined through distributed shared memory, always in the same order: no workspace, no atomics.
+//   - a unit is 32 tokens of one page, and each warp streams its units through a ring of its own in shared
+//     memory by asynchronous copies, with its own running sums: no barrier between warps until the row's end;
+//   - a row's units are dealt to the warps of a cluster of CTAs (more CTAs where there are few rows).  At the end
+//     every warp writes its partial into the shared memory of the CTAs that own a share of the row's output; one
+//     cluster barrier, and each CTA joins its share, always in the same order: no workspace, no atomics.
 //
-// S^T = K q^T runs on the 8-bit tensor cores (m16n8k32, tokens = M, heads = N): K's codes are the A operand as
-// they are, q is three e4m3 pieces that sum to it (msa_q8.cuh); the token's scale and the head's factor multiply
-// the fp32 result.  O^T = V^T P^T runs on bf16 MMAs (m16n8k16, components = M): a code seeeemmm becomes the
-// bf16 number s0000eeeemmm0000 = code * 2^-120 by shifts and masks (subnormal codes included, and no code gives
-// a NaN or an infinity, so tokens that a row does not see cannot reach it), and P carries the token's scale
-// relative to the largest that the warp has seen: P_t = p_t 2^(e_t - E + 100), so O is held times 2^(-20 - E) and
-// scales of any size fit, with 100 binades between the largest and what is lost.  P is rounded to bf16, once.
+// Both contractions run on f16 MMAs (m16n8k16, heads = N): a code is an f16 number.
+//   S^T = K q^T (tokens = M): q is f16 times a power of two (msa_q8.cuh), so nothing is rounded; the token's scale and
+//   the head's factor multiply the fp32 result.
+//   O^T = V^T P^T (components = M): P carries the token's scale, P_t = 2^(x_t - rx + 12) with x_t = (s_t - rs) + e_t,
+//   and is rounded to f16, 2^-12 of itself or 2^-37 of the largest, whichever is more; the weights 2^(s_t - rs) are
+//   summed in fp32.  rs is raised where a weight would pass 2^60, rx where P would pass 2^15.9, which is rare: a unit
+//   costs no shuffle for them.  (x counts from rs, so logits of any size lose nothing to the exponent.)
+// What a row does not see cannot reach it: its P is 0, and its bytes of V are cleared (a code may be a NaN).
+// (The 8-bit MMA of warps takes codes as they are, but is no faster: it unpacks its operands itself, every time, and
+// needs P and q in pieces.)
 //
-// Layout.  In a unit lane (r, c) = (lane / 4, lane % 4) reads tokens 4r .. 4r+3 of K (its quad covers the row,
-// a quarter each) and tokens 8c .. 8c+7 of V (D/8 components each): whole lines per load.  The C fragment of S^T
-// then has the tokens 4r+i, i = 0 .. 3; packed over two heads and transposed by movmatrix it is the B fragment of
-// P V for tokens 8c+i and 8c+4+i, which are two of the lane's eight.
+// Layout.  A unit's K and V are 32 rows of D bytes, swizzled by the copy (128- or 64-byte pattern).  Lane (r, c) =
+// (lane / 4, lane % 4) reads a quarter of K's rows 8i + r, i = 0 .. 3, and an eighth of V's rows 8i + 2c and 8i + 2c + 1:
+// with the swizzle both take distinct banks (D = 128).  The C fragment of S^T then has the tokens 8i + r; P packed over
+// two heads and transposed by movmatrix is the B fragment of P V for tokens 8i + 2c and 8i + 2c + 1.
 #include "msa_internal.h"
 #include "msa_q8.cuh"
 
@@ -36,6 +39,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;            // tokens
+constexpr float kShift = 12.f;       // P is at most 2^12 where its reference was set ...
+constexpr float kRaiseP = 3.9f;      // ... and its reference is raised where it would pass 2^15.9 (f16 ends below 2^16)
+constexpr float kRaiseL = 60.f;      // a weight may pass its reference by 2^60
 
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
@@ -43,30 +49,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-
-// Codes in bytes 0 and 2, or 1 and 3, of w as two bf16 numbers code * 2^-120.
-__device__ __forceinline__ uint32_t bf16_even(uint32_t w) { return ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u); }
-__device__ __forceinline__ uint32_t bf16_odd(uint32_t w) { return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u); }
-
-// 2^d for d <= 0, 0 below 2^-126.
-__device__ __forceinline__ float pow2_down(int d) { return __uint_as_float(uint32_t(max(d + 127, 0)) << 23); }
-
-// out = (x 2^20) 2^E for x = O 2^(-20 - E) / l, with E as a scale byte.
-__device__ __forceinline__ float unscaled(float x, int e) { return x * 0x1p20f * q8_scale(uint32_t(e)); }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -76,15 +63,16 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t smem, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float x, float y, float z, float w) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+
+// 4-byte global -> shared copy.
+__device__ __forceinline__ void cp_async_4(uint32_t smem_dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_dst), "l"(src) : "memory");
 }
 
 struct Args {
@@ -134,23 +122,35 @@ struct Row {
     }
 };
 
-template <int D>
+constexpr int kMaxCluster = 16;
+
+template <int D, int HPG>
 struct Smem {
-    alignas(16) float o[kWarps][8][D + 4];
-    float m[kWarps][8], l[kWarps][8];
-    int e[kWarps];
-    alignas(16) float po[8][D];       // of the CTA, read by the cluster
-    float pm[8], pl[8];
-    int pe;
+    static constexpr int NST = D == 128 ? 2 : 4;      // stages per warp
+    alignas(1024) uint8_t kv[kWarps][NST][2][kUnit * D];
+    alignas(16) uint8_t scale[kWarps][NST][2][kUnit];
+    // this CTA's share of the partials of all warps of the cluster (its HPG * D / cluster components), and their
+    // references and sums
+    alignas(16) float part[kWarps * HPG * D];
+    float rx[kMaxCluster * kWarps][8], rs[kMaxCluster * kWarps][8], l[kMaxCluster * kWarps][8];
 };
 
+// Byte offset of 16-byte column `ch` of row t of a unit.
+template <int D>
+__device__ __forceinline__ uint32_t unit_off(int t, int ch) {
+    return uint32_t(t * D + ((D == 128 ? ch ^ (t & 7) : ch ^ ((t >> 1) & 3)) << 4));
+}
+
 template <int D, int HPG, bool WINDOW>
-__global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads)
+    k_attn_q8(const __grid_constant__ Args a) {
+    using S = Smem<D, HPG>;
+    constexpr int NST = S::NST;
     constexpr int KW = D / 16;       // words of K a lane reads per token
     constexpr int VW = D / 32;       // words of V a lane reads per token
-    constexpr int KS = D / 32;       // k32 steps of S
     constexpr int MT = D / 16;       // m16 tiles of O
-    __shared__ Smem<D> sm;
+    extern __shared__ uint8_t smem_raw[];
+    S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     const int row = blockIdx.x / a.cluster, rank = blockIdx.x - row * a.cluster;
     const int b = row / a.G, g = row - b * a.G;
@@ -175,55 +175,50 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
         rw.table = a.page_table + size_t(row) * a.topk;
     }
 
-    uint32_t kw[4][KW], vw[8][VW];   // codes of the unit at hand (K: of the next one from the softmax on)
-    uint32_t ksb, vsb;               // scale bytes of tokens 4r .. 4r+3
-    auto load_k = [&](int page, int t_in) {
-        const size_t line = (size_t(page) * a.G + g) * 128 + t_in;
-        const uint8_t *kp = a.k + (line + 4 * r) * D + c * (D / 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int w = 0; w < KW; w += 4) {
-                const uint4 x = ldg_stream_v4(kp + i * D + w * 4);
-                kw[i][w] = x.x;
-                kw[i][w + 1] = x.y;
-                kw[i][w + 2] = x.z;
-                kw[i][w + 3] = x.w;
-            }
-        ksb = __ldg(reinterpret_cast<const uint32_t *>(a.k_scale + line) + r);
-    };
-    auto load_v = [&](int page, int t_in) {
-        const size_t line = (size_t(page) * a.G + g) * 128 + t_in;
-        const uint8_t *vp = a.v + (line + 8 * c) * D + r * (D / 8);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (VW == 4) {
-                const uint4 x = ldg_stream_v4(vp + i * D);
-                vw[i][0] = x.x;
-                vw[i][1] = x.y;
-                vw[i][2] = x.z;
-                vw[i][3] = x.w;
-            } else {
-                asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                             : "=r"(vw[i][0]), "=r"(vw[i][1]) : "l"(vp + i * D));
-            }
-        }
-        vsb = __ldg(reinterpret_cast<const uint32_t *>(a.v_scale + line) + r);
-    };
+    cluster_arrive();                // waited for before this CTA writes into the others: they have started by then
 
-    const int step = a.cluster * kWarps;
-    int u = rank * kWarps + warp;
-    int t_in = 0, v0 = 0, v1 = 0, page = -1;
-    if (u < rw.units) {
-        page = rw.unit(u, a.n_pages, &t_in, &v0, &v1, a.err);
-        if (page >= 0) {
-            load_k(page, t_in);
-            load_v(page, t_in);
+    // This warp's units: first, first + step, ...  Lane l looks up the l-th of 32 at a time.
+    const int step = a.cluster * kWarps, first = rank * kWarps + warp;
+    const int n = first < rw.units ? (rw.units - first + step - 1) / step : 0;
+    int u_page = -1, u_at = 0;       // the page, and t_in | v0 << 8 | v1 << 16 (v0, v1 in 0 .. 32)
+    auto look_up = [&](int i0) {
+        u_page = -1;
+        if (i0 + lane < n) {
+            int t_in, v0, v1;
+            u_page = rw.unit(first + (i0 + lane) * step, a.n_pages, &t_in, &v0, &v1, a.err);
+            u_at = t_in | max(v0, 0) << 8 | min(max(v1, 0), kUnit) << 16;
         }
+    };
+    int st_page = -1, st_at = 0;     // lane l: what stage l holds (page -1: nothing)
+    auto issue = [&](int i, int stage) {
+        if ((i & 31) == 0) look_up(i);
+        const int page = __shfl_sync(0xffffffffu, u_page, i & 31), at = __shfl_sync(0xffffffffu, u_at, i & 31);
+        if (lane == stage) {
+            st_page = page;
+            st_at = at;
+        }
+        if (page >= 0) {
+            constexpr int CPR = D / 16;                  // 16-byte columns of a row
+            const size_t line = (size_t(page) * a.G + g) * 128 + (at & 127);
+            const uint8_t *const kp = a.k + line * D + lane * 16, *const vp = a.v + line * D + lane * 16;
+            const uint32_t kd = smem_u32(sm.kv[warp][stage][0]), vd = smem_u32(sm.kv[warp][stage][1]);
+#pragma unroll
+            for (int k = 0; k < CPR; ++k) cp_async_16(kd + unit_off<D>((lane + 32 * k) / CPR, lane % CPR), kp + k * 512);
+#pragma unroll
+            for (int k = 0; k < CPR; ++k) cp_async_16(vd + unit_off<D>((lane + 32 * k) / CPR, lane % CPR), vp + k * 512);
+            if (lane < 16)
+                cp_async_4(smem_u32(sm.scale[warp][stage][lane >> 3]) + (lane & 7) * 4,
+                           (lane < 8 ? a.k_scale : a.v_scale) + line + (lane & 7) * 4);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+        if (i < n) issue(i, i);
+        cp_async_commit();
     }
 
-    // q of head r in pieces (a quarter of the components per lane), and the factor of heads 2c, 2c + 1
-    uint32_t qh[KW], ql[KW], qr[KW];
+    // q of head r (a quarter of the components per lane), and the factor of heads 2c, 2c + 1
+    uint32_t q[KW][2];
     float hq0, hq1;
     {
         float x[D / 4];
@@ -245,14 +240,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const bool finite = amax < 0x7f800000u;
-        const int e = finite ? q8_exponent(amax) : 0;
+        const int e = finite ? f16_exponent(amax) : 0;
         const float inv = exp2i(-e);
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
-            float y[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) y[h] = x[4 * i + h] * inv;
-            q8_pieces(y, qh[i], ql[i], qr[i]);
+            q[i][0] = pack_f16x2(x[4 * i] * inv, x[4 * i + 1] * inv);
+            q[i][1] = pack_f16x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv);
         }
         const float hq = finite ? a.sm_scale * kLog2e * exp2i(e) : __uint_as_float(0x7fffffffu);
         hq0 = __shfl_sync(0xffffffffu, hq, 8 * c);
@@ -262,218 +255,238 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_q8(const __grid_constant__
     float o[MT][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // heads 2c, 2c + 1; l over this lane's tokens
-    int emax = 0;                    // largest scale byte of V so far (255 aside): E + 127
+    // heads 2c, 2c + 1: references of P and of the weights, the weights' sum over this lane's tokens
+    float rx[2] = {-INFINITY, -INFINITY}, rs[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    for (; u < rw.units; u += step) {
-        int page_n = -1, t_n = 0, v0_n = 0, v1_n = 0;
-        if (u + step < rw.units) page_n = rw.unit(u + step, a.n_pages, &t_n, &v0_n, &v1_n, a.err);
-        if (page < 0) {              // nothing to read: only the next unit's loads
-            if (page_n >= 0) {
-                load_k(page_n, t_n);
-                load_v(page_n, t_n);
+    int stage = 0;
+    for (int i = 0; i < n; ++i) {
+        cp_async_wait<NST - 1>();
+        __syncwarp();                // every lane's part of the stage is there
+        const int page = __shfl_sync(0xffffffffu, st_page, stage), at = __shfl_sync(0xffffffffu, st_at, stage);
+        if (page >= 0) {
+            const uint8_t *const ku = sm.kv[warp][stage][0], *const vu = sm.kv[warp][stage][1];
+            // scales: of token `lane` here, of tokens 8k + r by shuffles
+            const int v0 = at >> 8 & 255, v1 = at >> 16;
+            const uint32_t vb = sm.scale[warp][stage][1][lane];
+            const bool seen = lane >= v0 && lane < v1;
+            const float kf = q8_scale(sm.scale[warp][stage][0][lane]);
+            // the exponent of V's scale, -inf where the token is not visible, NaN for a NaN row
+            const float ve = !seen ? -INFINITY : vb == 255u ? __uint_as_float(0x7fffffffu) : float(int(vb) - 127);
+            float s[4][2], x[4][2];  // logits in log2 units, and x (see above): token 8k + r, head 2c + h
+            const float base[2] = {rs[0] == -INFINITY ? 0.f : rs[0], rs[1] == -INFINITY ? 0.f : rs[1]};
+            float y[2][2][4];        // four chains of MMAs: their latency counts
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[mt][0][k] = y[mt][1][k] = 0.f;
+#pragma unroll
+            for (int j = 0; j < KW; j += 4) {
+                uint32_t kw[2][2][4];
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(
+                            ku + unit_off<D>(16 * mt + 8 * k + r, c * (KW / 4) + j / 4));
+                        kw[mt][k][0] = x.x;
+                        kw[mt][k][1] = x.y;
+                        kw[mt][k][2] = x.z;
+                        kw[mt][k][3] = x.w;
+                    }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+                        mma_f16(y[mt][k & 1], f16_of_low(kw[mt][0][k]), f16_of_low(kw[mt][1][k]),
+                                f16_of_high(kw[mt][0][k]), f16_of_high(kw[mt][1][k]), q[j + k][0], q[j + k][1]);
             }
-        } else {
-            float s[4][2];           // logits in log2 units: token 4r + i, head 2c + h
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-                float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const uint32_t a0 = kw[2 * mt][2 * ks], a1 = kw[2 * mt + 1][2 * ks];
-                    const uint32_t a2 = kw[2 * mt][2 * ks + 1], a3 = kw[2 * mt + 1][2 * ks + 1];
-                    mma_e4m3(x, a0, a1, a2, a3, qh[2 * ks], qh[2 * ks + 1]);
-                    mma_e4m3(y, a0, a1, a2, a3, ql[2 * ks], ql[2 * ks + 1]);
-                    mma_e4m3(z, a0, a1, a2, a3, qr[2 * ks], qr[2 * ks + 1]);
+                for (int k = 0; k < 2; ++k) {
+                    const float f = __shfl_sync(0xffffffffu, kf, 16 * mt + 8 * k + r);
+                    const float e = __shfl_sync(0xffffffffu, ve, 16 * mt + 8 * k + r);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int i = 2 * k + h;
+                        float v = (y[mt][0][i] + y[mt][1][i]) * f * (h ? hq1 : hq0);
+                        if (e == -INFINITY) v = -INFINITY;           // not visible, whatever K holds
+                        s[2 * mt + k][h] = v;
+                        x[2 * mt + k][h] = (v - base[h]) + e;
+                    }
+                }
+            bool raise = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float mx = fmaxf(fmaxf(x[0][h], x[1][h]), fmaxf(x[2][h], x[3][h]));
+                const float ms = fmaxf(fmaxf(s[0][h], s[1][h]), fmaxf(s[2][h], s[3][h]));
+                raise |= mx > rx[h] + kRaiseP || ms > rs[h] + kRaiseL;
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float ms = fmaxf(fmaxf(s[0][h], s[1][h]), fmaxf(s[2][h], s[3][h]));
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, k));
+                    ms = fmaxf(ms, rs[h]);
+                    const float down = rs[h] == -INFINITY ? 0.f : ms - rs[h];   // by which what counts from rs falls
+                    rs[h] = ms;
+                    l[h] *= fast_exp2(-down);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float e = __shfl_sync(0xffffffffu, ve, 8 * k + r);
+                        x[k][h] = (s[k][h] - (ms == -INFINITY ? 0.f : ms)) + e;
+                        mx = fmaxf(mx, x[k][h]);
+                    }
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+                    const float old = rx[h] - down;
+                    mx = fmaxf(mx, old);
+                    const float ax = mx == -INFINITY ? 1.f : fast_exp2(old - mx);
+                    rx[h] = mx;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        o[t][h] *= ax;
+                        o[t][2 + h] *= ax;
+                    }
+                }
+            }
+            uint32_t pt[4];          // P of tokens 8k + 2c, 8k + 2c + 1 and head r
+            {
+                const float bx0 = rx[0] == -INFINITY ? 0.f : rx[0] - kShift, bx1 = rx[1] == -INFINITY ? 0.f : rx[1] - kShift;
+                const float bs0 = rs[0] == -INFINITY ? 0.f : rs[0], bs1 = rs[1] == -INFINITY ? 0.f : rs[1];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    l[0] += fast_exp2(s[k][0] - bs0);
+                    l[1] += fast_exp2(s[k][1] - bs1);
+                    pt[k] = transpose8(pack_f16x2(fast_exp2(x[k][0] - bx0), fast_exp2(x[k][1] - bx1)));
+                }
+            }
+            uint32_t vw[8][VW];      // tokens 8 (k / 2) + 2c + k % 2
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int t = 8 * (k >> 1) + 2 * c + (k & 1);
+                if constexpr (VW == 4) {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(vu + unit_off<D>(t, r));
+                    vw[k][0] = y.x;
+                    vw[k][1] = y.y;
+                    vw[k][2] = y.z;
+                    vw[k][3] = y.w;
+                } else {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(vu + unit_off<D>(t, r >> 1) + (r & 1) * 8);
+                    vw[k][0] = y.x;
+                    vw[k][1] = y.y;
+                }
+            }
+            if (v0 > 0 || v1 < kUnit) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int t = 8 * (k >> 1) + 2 * c + (k & 1);
+                    if (t < v0 || t >= v1) {
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) vw[k][j] = 0u;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+                uint32_t av[4][4];   // components 4j .. 4j + 3 of the four pairs of tokens
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t t0 = __byte_perm(vw[2 * k][j], vw[2 * k + 1][j], 0x5140);
+                    const uint32_t t1 = __byte_perm(vw[2 * k][j], vw[2 * k + 1][j], 0x7362);
+                    av[k][0] = f16_of_low(t0);
+                    av[k][1] = f16_of_high(t0);
+                    av[k][2] = f16_of_low(t1);
+                    av[k][3] = f16_of_high(t1);
                 }
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    s[2 * mt + (h >> 1)][h & 1] = x[h] + (y[h] * kQ8LoScale + z[h] * kQ8ReScale);
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        mma_f16(o[2 * j + k], av[2 * kk][2 * k], av[2 * kk][2 * k + 1], av[2 * kk + 1][2 * k],
+                                av[2 * kk + 1][2 * k + 1], pt[2 * kk], pt[2 * kk + 1]);
             }
-            const uint32_t kb = ksb, vb = vsb;
-            if (page_n >= 0) load_k(page_n, t_n);
-            const bool whole = v0 <= 0 && v1 >= kUnit;
-            float mx0 = -INFINITY, mx1 = -INFINITY;
-            int eb[4];               // scale bytes of V (-1: not visible)
-            int etop = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float ks = q8_scale((kb >> (8 * i)) & 255u);
-                eb[i] = int((vb >> (8 * i)) & 255u);
-                s[i][0] = s[i][0] * ks * hq0;
-                s[i][1] = s[i][1] * ks * hq1;
-                if (!whole && (4 * r + i < v0 || 4 * r + i >= v1)) {
-                    s[i][0] = s[i][1] = -INFINITY;
-                    eb[i] = -1;
-                }
-                etop = max(etop, eb[i] == 255 ? 0 : eb[i]);
-                mx0 = fmaxf(mx0, s[i][0]);
-                mx1 = fmaxf(mx1, s[i][1]);
-            }
-            etop = __reduce_max_sync(0xffffffffu, etop);
-            if (etop > emax) {       // uniform in the warp
-                const float al = pow2_down(emax - etop);
-                emax = etop;
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    o[t][0] *= al;
-                    o[t][1] *= al;
-                    o[t][2] *= al;
-                    o[t][3] *= al;
-                }
-            }
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
-            }
-            if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
-                const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-                const float al0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
-                const float al1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
-                m0 = n0;
-                m1 = n1;
-                l0 *= al0;
-                l1 *= al1;
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    o[t][0] *= al0;
-                    o[t][1] *= al1;
-                    o[t][2] *= al0;
-                    o[t][3] *= al1;
-                }
-            }
-            const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-            uint32_t pt[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p0 = fast_exp2(s[i][0] - r0), p1 = fast_exp2(s[i][1] - r1);
-                l0 += p0;
-                l1 += p1;
-                // 2^(e - E + 100): 0 for tokens that are not visible, NaN for a NaN row
-                const int x = max(eb[i] - emax + 227, 0) << 23;
-                const float f = eb[i] < 0 ? 0.f : __uint_as_float(eb[i] == 255 ? 0x7fffffffu : uint32_t(x));
-                pt[i] = transpose8(pack_bf16x2(p0 * f, p1 * f));
-            }
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const uint32_t sel = t & 1 ? 0x7632u : 0x5410u;
-                    const uint32_t x = __byte_perm(vw[2 * kk][t >> 1], vw[2 * kk + 4][t >> 1], sel);
-                    const uint32_t y = __byte_perm(vw[2 * kk + 1][t >> 1], vw[2 * kk + 5][t >> 1], sel);
-                    mma_bf16_16816(o[t], bf16_even(x), bf16_odd(x), bf16_even(y), bf16_odd(y), pt[2 * kk],
-                                   pt[2 * kk + 1]);
-                }
-            if (page_n >= 0) load_v(page_n, t_n);
         }
-        page = page_n;
-        t_in = t_n;
-        v0 = v0_n;
-        v1 = v1_n;
+        __syncwarp();                // the stage has been read
+        if (i + NST < n) issue(i + NST, stage);
+        cp_async_commit();
+        stage = stage + 1 == NST ? 0 : stage + 1;
     }
+    cp_async_wait<0>();
 
-    // ---------------------------------------------------------------- join: warps, then CTAs
+    // ---------------------------------------------------------------- join
 #pragma unroll
-    for (int x = 4; x < 32; x <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    for (int k = 4; k < 32; k <<= 1) {
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
+        l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
     }
-    if (r == 0) {
-        sm.m[warp][2 * c] = m0;
-        sm.m[warp][2 * c + 1] = m1;
-        sm.l[warp][2 * c] = l0;
-        sm.l[warp][2 * c + 1] = l1;
-        if (lane == 0) sm.e[warp] = emax;
-    }
+    cluster_wait();
+    // The row's HPG * D components are shared out in equal runs; a lane's D / 8 of a head fall to one CTA.
+    const int share = HPG * D / a.cluster, wid = rank * kWarps + warp;
+    const uint32_t part = smem_u32(sm.part) + uint32_t(wid * share) * 4u;
 #pragma unroll
-    for (int t = 0; t < MT; t += 2) {
-        const int d = r * (D / 8) + 2 * t;
-        *reinterpret_cast<float4 *>(&sm.o[warp][2 * c][d]) = make_float4(o[t][0], o[t][2], o[t + 1][0], o[t + 1][2]);
-        *reinterpret_cast<float4 *>(&sm.o[warp][2 * c + 1][d]) = make_float4(o[t][1], o[t][3], o[t + 1][1], o[t + 1][3]);
-    }
-    __syncthreads();
-    constexpr int PAIRS = HPG * D / 2;
-    const size_t head0 = size_t(b) * a.G * HPG + size_t(g) * HPG;
-    int ecta = 0;
+    for (int h = 0; h < 2; ++h) {
+        const int e = (2 * c + h) * D + r * (D / 8);
+        if (2 * c + h < HPG) {
+            const uint32_t dst = cluster_map(part + uint32_t(e % share) * 4u, e / share);
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) ecta = max(ecta, sm.e[i]);
-    // a pair of output components from the sums over all partials
-    auto finish = [&](int h, int d, float top, float l, float x, float y, int e) {
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-        *reinterpret_cast<uint32_t *>(a.out + (head0 + h) * D + d) = pack_bf16x2(unscaled(x * inv, e), unscaled(y * inv, e));
-        if (d == 0) a.lse[head0 + h] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
-    };
-    for (int i = tid; i < PAIRS; i += kThreads) {
-        const int h = i / (D / 2), d = (i - h * (D / 2)) * 2;
-        float top = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sm.m[k][h]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float l = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            const float w = fast_exp2(sm.m[k][h] - ref), wo = w * pow2_down(sm.e[k] - ecta);
-            l += w * sm.l[k][h];
-            x += wo * sm.o[k][h][d];
-            y += wo * sm.o[k][h][d + 1];
-        }
-        if (a.cluster == 1) {
-            finish(h, d, top, l, x, y, ecta);
-        } else {
-            *reinterpret_cast<float2 *>(&sm.po[h][d]) = make_float2(x, y);
-            if (d == 0) {
-                sm.pm[h] = top;
-                sm.pl[h] = l;
-            }
+            for (int t = 0; t < MT; t += 2)
+                st_cluster4(dst + t * 8, o[t][h], o[t][2 + h], o[t + 1][h], o[t + 1][2 + h]);
         }
     }
-    if (a.cluster == 1) return;
-    if (tid == 0) sm.pe = ecta;
+    for (int k = r; k < a.cluster; k += 8) {             // lanes of r take the CTAs in turn
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            st_cluster(cluster_map(smem_u32(&sm.rx[wid][2 * c + h]), k), rx[h]);
+            st_cluster(cluster_map(smem_u32(&sm.rs[wid][2 * c + h]), k), rs[h]);
+            st_cluster(cluster_map(smem_u32(&sm.l[wid][2 * c + h]), k), l[h]);
+        }
+    }
     cluster_arrive();
     cluster_wait();
-    const uint32_t pe = smem_u32(&sm.pe);
-    int ec = 0;
-    for (int k = 0; k < a.cluster; ++k) ec = max(ec, __float_as_int(ld_cluster(cluster_map(pe, k))));
-    const int share = PAIRS / a.cluster;   // a power of two, at least 8
-    for (int i = tid; i < share; i += kThreads) {
-        const int j = rank * share + i;
-        const int h = j / (D / 2), d = (j - h * (D / 2)) * 2;
-        const uint32_t pm = smem_u32(&sm.pm[h]), pl = smem_u32(&sm.pl[h]), po = smem_u32(&sm.po[h][d]);
-        float top = -INFINITY;
-        for (int k = 0; k < a.cluster; ++k) top = fmaxf(top, ld_cluster(cluster_map(pm, k)));
-        const float ref = top == -INFINITY ? 0.f : top;
-        float l = 0.f, x = 0.f, y = 0.f;
-        for (int k = 0; k < a.cluster; ++k) {
-            const float w = fast_exp2(ld_cluster(cluster_map(pm, k)) - ref);
-            const float wo = w * pow2_down(__float_as_int(ld_cluster(cluster_map(pe, k))) - ec);
-            const float2 v = ld_cluster2(cluster_map(po, k));
-            l += w * ld_cluster(cluster_map(pl, k));
-            x += wo * v.x;
-            y += wo * v.y;
+    const size_t head0 = size_t(b) * a.G * HPG + size_t(g) * HPG;
+    const int n_part = a.cluster * kWarps;
+    auto weight = [](float ref, float top) { return top == -INFINITY ? 0.f : fast_exp2(ref - top); };
+    for (int i = tid * 2; i < share; i += kThreads * 2) {
+        const int e = rank * share + i, h = e / D, d = e - h * D;
+        float ts = -INFINITY;            // the largest rs: what every partial is brought to
+        for (int k = 0; k < n_part; ++k) ts = fmaxf(ts, sm.rs[k][h]);
+        auto rx_of = [&](int k) { return sm.rs[k][h] == -INFINITY ? -INFINITY : sm.rx[k][h] + (sm.rs[k][h] - ts); };
+        float tx = -INFINITY;
+        for (int k = 0; k < n_part; ++k) tx = fmaxf(tx, rx_of(k));
+        float sum = 0.f, x = 0.f, y = 0.f;
+        for (int k = 0; k < n_part; ++k) {
+            const float wx = weight(rx_of(k), tx);
+            const float2 v = *reinterpret_cast<const float2 *>(&sm.part[k * share + i]);
+            sum += weight(sm.rs[k][h], ts) * sm.l[k][h];
+            x += wx * v.x;
+            y += wx * v.y;
         }
-        finish(h, d, top, l, x, y, ec);
+        const float f = sum == 0.f ? 0.f : weight(tx - kShift, 0.f) / sum;
+        *reinterpret_cast<uint32_t *>(a.out + (head0 + h) * D + d) = pack_bf16x2(x * f, y * f);
+        if (d == 0) a.lse[head0 + h] = sum == 0.f ? -INFINITY : (ts + log2f(sum)) * kLn2;
     }
-    cluster_arrive();                // no CTA leaves while another reads its partials
-    cluster_wait();
 }
 
 template <int D, int HPG, bool WINDOW>
 cudaError_t launch_t(Args a, long long rows, int units, cudaStream_t st, bool pdl) {
-    // Enough CTAs to have three on every SM, as long as every warp of the cluster has a unit.
-    const long long want = 3LL * sm_count();
+    // As many CTAs as fit the SMs at two each, as long as every warp of the cluster has two units.
+    const long long want = 2LL * sm_count();
     int cs = 1;
-    while (cs < 16 && rows * cs * 2 <= want && cs * 2 * kWarps <= units) cs *= 2;
+    while (cs < kMaxCluster && rows * cs * 2 <= want && cs * 4 * kWarps <= units) cs *= 2;
     a.cluster = cs;
     if (rows * cs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     auto k = k_attn_q8<D, HPG, WINDOW>;
-    if (cs > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
+    const size_t smem = sizeof(Smem<D, HPG>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e == cudaSuccess && cs > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(rows * cs));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -1,11 +1,11 @@
 // Decode index scan over 8-bit index keys: score = max over a block's visible tokens of q_idx . kidx.
 //
 // A token and group is Di codes and a scale byte, half of the bf16 scan's bytes, and the scan is bound by
-// them.  The dot products run on the 8-bit tensor cores (mma.sync m16n8k32, tokens = M): the codes are the A
-// operand as they are, and q_idx is the B operand in three e4m3 pieces whose sum is q_idx (msa_q8.cuh), so neither
-// side is rounded.  hi and lo pieces fill the even and odd columns of the eight, so every lane of a quad holds the
-// whole result of its tokens; which lane goes on with a tile's tokens is dealt by turns.  Components are summed in
-// the order that suits the loads: the four lanes of a quad take a quarter of the vector each.
+// them.  The dot products run on f16 MMAs (m16n8k16, tokens = M): a code is an f16 number, and q_idx is one times a
+// power of two (msa_q8.cuh), so neither side is rounded.  All eight columns hold q_idx, so every lane of a quad has the
+// results of its tokens; which lane goes on with a tile's tokens is dealt by turns.  Components are summed in the
+// order that suits the loads: the four lanes of a quad take a quarter of the vector each.  (The 8-bit MMA of warps
+// takes the codes as they are, but is three times as many instructions: it unpacks its operands itself, every time.)
 //
 // A unit is the slice of one block and group, one contiguous run of 128 Di codes and one of 128 scales.  One CTA per
 // SM; each of its warps streams a contiguous range of the units that exist (row, then group, then block) through
@@ -74,8 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_q8(const uint16_t *__rest
                                                           int n_pages, float *__restrict__ scores, int32_t *err) {
     using S = Smem<DI>;
     constexpr int NST = S::NST;
-    constexpr int NW = DI / 16;      // words of a lane per token
-    constexpr int KS = DI / 32;      // MMAs per tile and piece
+    constexpr int NW = DI / 16;      // words of a lane per token, MMAs per tile
     extern __shared__ uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -190,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_q8(const uint16_t *__rest
     }
 
     const int rr = lane >> 2, c = lane & 3;
-    uint32_t bh[NW], br[NW];             // columns: hi (even) or lo (odd); the rest (even) or nothing (odd)
+    uint32_t q[NW][2];                   // q_idx: four components per word of the codes
     float qs = 0.f;
     bool fresh = true;                   // q_idx is to be read
     int lim = 0, j0 = 0, stage = 0;
@@ -202,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_q8(const uint16_t *__rest
             fresh = false;
             j0 = at.j;
             lim = rows.pos(at.r);
-            // this lane's quarter of q_idx in pieces
+            // this lane's quarter of q_idx
             float x[DI / 4];
             const uint4 *qp = reinterpret_cast<const uint4 *>(q_idx + (size_t(at.r) * G + at.g) * DI + c * (DI / 4));
             uint32_t amax = 0u;
@@ -221,18 +220,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_q8(const uint16_t *__rest
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             const bool finite = amax < 0x7f800000u;
-            const int e = finite ? q8_exponent(amax) : 0;
+            const int e = finite ? f16_exponent(amax) : 0;
             const float inv = exp2i(-e);
             qs = finite ? exp2i(e) : __uint_as_float(0x7fffffffu);
 #pragma unroll
             for (int k = 0; k < NW; ++k) {
-                float y[4];
-#pragma unroll
-                for (int h = 0; h < 4; ++h) y[h] = x[4 * k + h] * inv;
-                uint32_t hi, lo, re;
-                q8_pieces(y, hi, lo, re);
-                bh[k] = rr & 1 ? lo : hi;
-                br[k] = rr & 1 ? 0u : re;
+                q[k][0] = pack_f16x2(x[4 * k] * inv, x[4 * k + 1] * inv);
+                q[k][1] = pack_f16x2(x[4 * k + 2] * inv, x[4 * k + 3] * inv);
             }
         }
         float best = -INFINITY;
@@ -257,15 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_score_q8(const uint16_t *__rest
                     k0[0] = x.x, k0[1] = x.y;
                     k1[0] = y.x, k1[1] = y.y;
                 }
-                float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+                float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    mma_e4m3(a, k0[2 * ks], k1[2 * ks], k0[2 * ks + 1], k1[2 * ks + 1], bh[2 * ks], bh[2 * ks + 1]);
-                    mma_e4m3(b, k0[2 * ks], k1[2 * ks], k0[2 * ks + 1], k1[2 * ks + 1], br[2 * ks], br[2 * ks + 1]);
-                }
+                for (int k = 0; k < NW; ++k)
+                    mma_f16(a, f16_of_low(k0[k]), f16_of_low(k1[k]), f16_of_high(k0[k]), f16_of_high(k1[k]), q[k][0],
+                            q[k][1]);
                 if ((m & 3) == c) {      // a select: every lane runs the MMAs
-                    s[2 * (m >> 2)] = a[0] + (a[1] * kQ8LoScale + b[0] * kQ8ReScale);
-                    s[2 * (m >> 2) + 1] = a[2] + (a[3] * kQ8LoScale + b[2] * kQ8ReScale);
+                    s[2 * (m >> 2)] = a[0];
+                    s[2 * (m >> 2) + 1] = a[2];
                 }
             }
             const int left = lim - at.j * 128;           // tokens t <= left are visible

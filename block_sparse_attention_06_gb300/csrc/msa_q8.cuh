@@ -48,36 +48,34 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t w) {
     return f;
 }
 
-// A vector of bf16 numbers as the sum of three vectors of e4m3 numbers, so that its products with cached
-// codes run on the 8-bit tensor cores without rounding either side: with x = q 2^-e, |x| <= 448,
-//   hi = e4m3(x),  lo = e4m3((x - hi) 2^4),  re = e4m3((x - hi - lo 2^-4) 2^22).
-// bf16 has eight significant bits and e4m3 four, so hi + lo 2^-4 is x itself where |x| >= 2^-6 (2^-14 of
-// the largest), re takes what is below, and nothing above 2^-40 of the largest is lost.
-constexpr float kQ8LoScale = 0x1p-4f, kQ8ReScale = 0x1p-22f;
-
-// Pieces of four numbers x (already scaled) as words of four codes, first number in the lowest byte.
-__device__ __forceinline__ void q8_pieces(const float (&x)[4], uint32_t &hi, uint32_t &lo, uint32_t &re) {
-    uint32_t h[2], l[2], r[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        h[i] = pack_e4m3x2(a, b);
-        const float2 hf = unpack_e4m3x2(h[i]);
-        const float ra = (a - hf.x) * 0x1p4f, rb = (b - hf.y) * 0x1p4f;
-        l[i] = pack_e4m3x2(ra, rb);
-        const float2 lf = unpack_e4m3x2(l[i]);
-        r[i] = pack_e4m3x2((ra - lf.x) * 0x1p18f, (rb - lf.y) * 0x1p18f);
-    }
-    hi = h[0] | h[1] << 16;
-    lo = l[0] | l[1] << 16;
-    re = r[0] | r[1] << 16;
+// Codes as f16, exactly (e4m3's range lies in f16's): what the MMAs below read.  A NaN code stays a NaN.
+__device__ __forceinline__ uint32_t f16_of_low(uint32_t w) {    // codes 0 and 1 of a word
+    uint32_t h;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(h) : "r"(w));
+    return h;
+}
+__device__ __forceinline__ uint32_t f16_of_high(uint32_t w) {   // codes 2 and 3
+    uint32_t h;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}" : "=r"(h) : "r"(w));
+    return h;
 }
 
-// D += A B, e4m3 with fp32 accumulation: m16 (rows of A: cached tokens), n8, k32.
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A vector of bf16 numbers as f16 times a power of two: q = x 2^e with the largest |x| in [2^14, 2^15).  f16 holds the
+// eight bits of a bf16 number down to 2^-31 of the largest, and nothing above 2^-39 of it is lost.  amax: the bits of
+// the largest magnitude, finite.
+__device__ __forceinline__ int f16_exponent(uint32_t amax) { return max(int(amax >> 23) - 127, -100) - 14; }
+
+// D += A B, f16 with fp32 accumulation: m16, n8, k16.
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));

@@ -641,7 +641,7 @@ msa_status_t msa_cache_read_q8(const msa_cache_q8_t *cache, const int32_t *block
 /*
  * msa_index_score_q8 -- msa_index_score (MSA_PHASE_DECODE: each row reads its own candidate pages) over 8-bit
  * index keys.  Arguments as there.  A NaN among a block's visible tokens gives a NaN score.
- * q_idx is finite (else its scores are NaN); components below 2^-40 of the largest of their group count as 0.
+ * q_idx is finite (else its scores are NaN); components below 2^-39 of the largest of their group count as 0.
  */
 msa_status_t msa_index_score_q8(const void *q_idx, const msa_cache_q8_t *cache, const int32_t *block_table,
                                 const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,
@@ -653,7 +653,7 @@ msa_status_t msa_index_score_q8(const void *q_idx, const msa_cache_q8_t *cache, 
  *   q bf16 [B][Hq][D];  page_table int32 [B*G][topk];  row_len int32 [B*G]
  *   out bf16 [B][Hq][D] out;  lse fp32 [B][Hq] out.  A row that sees nothing gets 0 and -inf.
  * What a row does not see does not reach it, whatever its bits; a NaN that it sees makes it NaN.  q is finite
- * (else its row is NaN); components below 2^-40 of a head's largest count as 0.
+ * (else its row is NaN); components below 2^-39 of a head's largest count as 0.
  */
 msa_status_t msa_sparse_attn_decode_q8(const void *q, const msa_cache_q8_t *cache, const int32_t *page_table,
                                        const int32_t *row_len, int32_t B, int32_t n_pages, const msa_dims_t *dims,

@@ -124,7 +124,8 @@ def ref_scores(q_idx, kidx, kscale, bt, req, pos):
             n = min(PAGE, int(pos[r]) + 1 - j * PAGE)
             x = k[int(bt[req[r], j]), :, :n]
             s[r, :, j] = torch.einsum("gd,gtd->gt", q, x).amax(-1)
-            # two pieces of a bf16 number sum to it, the third takes what is under 2^-14 of the largest; fp32 sums
+            # q in f16, the largest component in [2^14, 2^15): half of the lowest step, 2^-25, is under 2^-39 of it;
+            # fp32 sums
             mag = torch.einsum("gd,gtd->gt", q.abs(), x.abs()) * 1.2 * (Di + 8) * 2.0 ** -23
             lost = q.abs().amax(-1)[:, None] * x.abs().sum(-1) * 2.0 ** -39
             tol[r, :, j] = (mag + lost).amax(-1)

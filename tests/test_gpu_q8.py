@@ -422,6 +422,24 @@ def test_attend_rows_of_unlike_scale(msa, spread):
     Q.assert_within(lse, s, bs, "lse")
 
 
+@pytest.mark.parametrize("scale", [2.0 ** 10, 2.0 ** 20, 2.0 ** 40])
+def test_attend_huge_logits(msa, scale):
+    """Logits whose steps in fp32 are whole numbers or more: the output stays a mean of values that the row sees (here
+    mostly one token's), whatever the scales of V."""
+    dims, table, lens, cache, (k, v), q = _paged(msa, 16, 2, 128, 4, [500, 130], 2, 3.0)
+    dims = msa.Dims(16, 2, 128, 64, 4, 4, scale)
+    out, lse = msa.msa_sparse_attn_decode_q8(q.cuda(), cache, *cuda(table, lens), dims)
+    o, s, bo, bs = Q.ref_paged(q, k, v, table, lens, scale)
+    Q.assert_within(out, o, bo, "out")
+    assert bool(torch.isfinite(lse).all())
+    for r in range(4):
+        idx = [(int(p), t) for j, p in enumerate(table[r]) for t in range(min(128, int(lens[r]) - j * 128))]
+        seen = v[[p for p, _ in idx], r % 2, [t for _, t in idx]]
+        got = out[r // 2, r % 2 * 8:r % 2 * 8 + 8].double().cpu()
+        top, low = seen.amax(0) * (1 + seen.amax(0).sign() * 2.0 ** -7), seen.amin(0) * (1 - seen.amin(0).sign() * 2.0 ** -7)
+        assert bool((got <= top).all()) and bool((got >= low).all())
+
+
 def test_attend_all_codes(msa):
     """Every finite code, subnormal ones among them, reaches the output: one token seen at a time."""
     dims = msa.Dims(8, 1, 128, 64, 1, 1)
