@@ -721,6 +721,7 @@ def msa_commit_tree(k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache, block_
 # ------------------------------------------------------------------ appending, and 8-bit caches
 
 _E4M3, _E8M0, _F64 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.float64
+_NO_KV = (None, None, None, None)
 
 
 @dataclass(frozen=True)
@@ -746,20 +747,34 @@ class CacheQ8:
         return cls(*one(dims.D), *one(dims.D), *(one(dims.Di) if index else (None, None)))
 
     def _struct(self, dims: Dims, dev: int, kv: bool, index: bool):
-        """(reference to the C struct, n_pages), with what the call needs checked."""
+        """(reference to the C struct, n_pages), with what the call needs checked: types, shapes and devices once for
+        each kind of call (the fields are frozen), addresses every time."""
+        key = (dims.page_size, dims.G, dims.D, dims.Di, dev, kv, index)
+        n_pages = self.__dict__.get(key)
+        if n_pages is None:
+            n_pages = self._check(dims, dev, kv, index)
+            self.__dict__[key] = n_pages
+        p = (self.k.data_ptr(), self.k_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr()) if kv else _NO_KV
+        if index:
+            p += (self.kidx.data_ptr(), self.kidx_scale.data_ptr())
+        return ctypes.byref(msa_cache_q8_t(*p)), n_pages
+
+    def __getstate__(self):   # copies and pickles are checked anew
+        return {k: v for k, v in self.__dict__.items() if isinstance(k, str)}
+
+    def _check(self, dims: Dims, dev: int, kv: bool, index: bool) -> int:
         first = self.k if kv else self.kidx
         n_pages = _ndim(first, 4, "cache.k" if kv else "cache.kidx", "[n_pages][G][128][width]")[0]
         line = (n_pages, dims.G, dims.page_size)
-        p = [None] * 6
         if kv:
-            p[0] = _arg(self.k, _E4M3, (*line, dims.D), dev, "cache.k")
-            p[1] = _arg(self.k_scale, _E8M0, line, dev, "cache.k_scale")
-            p[2] = _arg(self.v, _E4M3, (*line, dims.D), dev, "cache.v")
-            p[3] = _arg(self.v_scale, _E8M0, line, dev, "cache.v_scale")
+            _arg(self.k, _E4M3, (*line, dims.D), dev, "cache.k")
+            _arg(self.k_scale, _E8M0, line, dev, "cache.k_scale")
+            _arg(self.v, _E4M3, (*line, dims.D), dev, "cache.v")
+            _arg(self.v_scale, _E8M0, line, dev, "cache.v_scale")
         if index:
-            p[4] = _arg(self.kidx, _E4M3, (*line, dims.Di), dev, "cache.kidx")
-            p[5] = _arg(self.kidx_scale, _E8M0, line, dev, "cache.kidx_scale")
-        return ctypes.byref(msa_cache_q8_t(*p)), n_pages
+            _arg(self.kidx, _E4M3, (*line, dims.Di), dev, "cache.kidx")
+            _arg(self.kidx_scale, _E8M0, line, dev, "cache.kidx_scale")
+        return n_pages
 
 
 def rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original_len: int = 0,
@@ -931,7 +946,7 @@ def msa_sparse_attn_decode_q8(q, cache: CacheQ8, page_table, row_len, dims: Dims
     dev = _lead(q, "q")
     B = _ndim(q, 3, "q", "[B][Hq][D]")[0]
     heads = (B, dims.Hq, dims.D)
-    out = torch.empty(heads, dtype=_BF16, device=q.device) if out is None else out
+    out = torch.empty_like(q) if out is None else out
     lse = torch.empty(heads[:2], dtype=_F32, device=q.device) if lse is None else lse
     err_word = new_err_word(q.device) if err_word is None else err_word
     c, n_pages = cache._struct(dims, dev, True, False)
@@ -979,7 +994,7 @@ def msa_window_attn_q8(q, cache: CacheQ8, block_table, q_req, q_pos, window: int
     n = _ndim(q, 3, "q", "[n_rows][Hq][D]")[0]
     n_req = _ndim(block_table, 2, "block_table", "[n_req][max_blocks]")[0]
     heads = (n, dims.Hq, dims.D)
-    out = torch.empty(heads, dtype=_BF16, device=q.device) if out is None else out
+    out = torch.empty_like(q) if out is None else out
     lse = torch.empty(heads[:2], dtype=_F32, device=q.device) if lse is None else lse
     err_word = new_err_word(q.device) if err_word is None else err_word
     c, n_pages = cache._struct(dims, dev, True, False)

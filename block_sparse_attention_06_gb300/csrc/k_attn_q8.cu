@@ -480,8 +480,8 @@ cudaError_t launch_t(Args a, long long rows, int units, cudaStream_t st, bool pd
     if (rows * cs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     auto k = k_attn_q8<D, HPG, WINDOW>;
     const size_t smem = sizeof(Smem<D, HPG>) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e == cudaSuccess && cs > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_once(allowed, reinterpret_cast<const void *>(k), smem, true);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(rows * cs));

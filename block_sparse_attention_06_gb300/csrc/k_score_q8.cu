@@ -295,7 +295,8 @@ template <int DI>
 cudaError_t launch_t(const void *q_idx, const CacheQ8 &c, const int32_t *block_table, const Rows &rows, int G, int n_pages,
                      float *scores, int32_t *err, cudaStream_t st, bool pdl) {
     const size_t smem = sizeof(Smem<DI>) + 128;
-    const cudaError_t e = cudaFuncSetAttribute(k_score_q8<DI>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_once(allowed, reinterpret_cast<const void *>(k_score_q8<DI>), smem);
     if (e != cudaSuccess) return e;
     const long long units = 1LL * rows.n_rows * rows.max_blocks * G;
     const int grid = int(std::min<long long>((units + kWarps - 1) / kWarps, sm_count()));

@@ -736,8 +736,8 @@ cudaError_t launch_t(const void *q, Args a, const Shape &s, cudaStream_t st) {
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.n_items = int(items);
     const size_t smem = sizeof(Smem<D>) + 1024;
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_window_q8<D, HPG>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_once(allowed, reinterpret_cast<const void *>(k_window_q8<D, HPG>), smem);
     if (e != cudaSuccess) return e;
     return launch_kernel(k_window_q8<D, HPG>, dim3(unsigned(std::min<long long>(items, sm_count()))), dim3(kThreads), smem,
                          st, false, a, qm);

@@ -7,6 +7,7 @@
 
 #include "msa.h"
 
+#include <atomic>
 #include <utility>
 
 namespace msa {
@@ -198,6 +199,10 @@ bool encode_tensor_map(void *map, int rank, const void *base, const uint64_t *di
                        const char **why);
 
 int sm_count();
+
+// The attributes of a kernel that takes `smem` bytes (and clusters of more than 8 CTAs), set at its first launch on
+// a device; `done` is the kernel's own.
+cudaError_t allow_once(std::atomic<uint64_t> &done, const void *kernel, size_t smem, bool large_clusters = false);
 
 // One thread waits on an mbarrier that nothing arrives on (the device timeout path).
 cudaError_t launch_selftest_timeout(int32_t *err, cudaStream_t st);
