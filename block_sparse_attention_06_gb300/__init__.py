@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 from typing import Optional, Tuple
 
 import torch
@@ -735,6 +735,7 @@ class CacheQ8:
     v_scale: Optional[torch.Tensor]
     kidx: Optional[torch.Tensor] = None
     kidx_scale: Optional[torch.Tensor] = None
+    _checked: dict = field(default_factory=dict, init=False, repr=False, compare=False)
 
     @classmethod
     def zeros(cls, dims: Dims, n_pages: int, device, index: bool = True) -> "CacheQ8":
@@ -750,17 +751,13 @@ class CacheQ8:
         """(reference to the C struct, n_pages), with what the call needs checked: types, shapes and devices once for
         each kind of call (the fields are frozen), addresses every time."""
         key = (dims.page_size, dims.G, dims.D, dims.Di, dev, kv, index)
-        n_pages = self.__dict__.get(key)
+        n_pages = self._checked.get(key)
         if n_pages is None:
-            n_pages = self._check(dims, dev, kv, index)
-            self.__dict__[key] = n_pages
+            n_pages = self._checked[key] = self._check(dims, dev, kv, index)
         p = (self.k.data_ptr(), self.k_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr()) if kv else _NO_KV
         if index:
             p += (self.kidx.data_ptr(), self.kidx_scale.data_ptr())
         return ctypes.byref(msa_cache_q8_t(*p)), n_pages
-
-    def __getstate__(self):   # copies and pickles are checked anew
-        return {k: v for k, v in self.__dict__.items() if isinstance(k, str)}
 
     def _check(self, dims: Dims, dev: int, kv: bool, index: bool) -> int:
         first = self.k if kv else self.kidx

@@ -24,13 +24,22 @@ __device__ __forceinline__ uint32_t bf16_pair(uint32_t codes, float s) {
     return pack_bf16x2(f.x * s, f.y * s);
 }
 
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// EVEN: a token's chunks divide the CTA's threads, so a thread keeps its group and column and steps over tokens.
+template <bool EVEN>
 __global__ void __launch_bounds__(kThreads) k_cache_read(const __grid_constant__ Args a) {
+    constexpr int U = 8;                 // loads in flight per lane
     const int b = blockIdx.x / a.max_blocks, j = blockIdx.x - b * a.max_blocks;
     const int which = blockIdx.y;
     const int to = a.bt_out[blockIdx.x];
+    const int from = a.bt_in[blockIdx.x];
     const int n_tok = min(128, a.lens[b] - j * 128);
     if (to < 0 || n_tok <= 0) return;
-    const int from = a.bt_in[blockIdx.x];
     if (from < 0 || from >= a.n_pages || to >= a.n_pages_out) {
         if (threadIdx.x == 0 && which == 0) raise_flag(a.err, MSA_FLAG_BOUNDS);
         return;
@@ -40,27 +49,34 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(const __grid_constant__
     const uint8_t *scale = a.scale[which] + size_t(from) * a.G * 128;
     uint8_t *out = a.out[which] + size_t(to) * 128 * a.G * width * 2;
     const int n = n_tok * per_tok;
-    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kThreads) {
-        uint4 w[4];
-        float s[4];
+    const int t0 = threadIdx.x / per_tok, g0 = (threadIdx.x - t0 * per_tok) / cpv;
+    const int c0 = threadIdx.x - t0 * per_tok - g0 * cpv, dt = kThreads / per_tok;
+    for (int i0 = threadIdx.x, t1 = t0; i0 < n; i0 += U * kThreads, t1 += U * dt) {
+        uint4 w[U];
+        uint8_t s[U];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int i = i0 + u * kThreads;
             if (i < n) {
-                const int t = i / per_tok, g = (i - t * per_tok) / cpv, c = i - t * per_tok - g * cpv;
-                w[u] = ldg_stream_v4(code + (size_t(g) * 128 + t) * width + c * 16);
-                s[u] = q8_scale(__ldg(scale + g * 128 + t));
+                int t = t1 + u * dt, g = g0, c = c0;
+                if constexpr (!EVEN) {
+                    t = i / per_tok;
+                    g = (i - t * per_tok) / cpv;
+                    c = i - t * per_tok - g * cpv;
+                }
+                w[u] = ldg_stream_v4(code + (g * 128 + t) * width + c * 16);
+                s[u] = __ldg(scale + g * 128 + t);
             }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int i = i0 + u * kThreads;
             if (i < n) {
-                uint4 *p = reinterpret_cast<uint4 *>(out + size_t(i) * 32);
-                p[0] = make_uint4(bf16_pair(w[u].x, s[u]), bf16_pair(w[u].x >> 16, s[u]), bf16_pair(w[u].y, s[u]),
-                                  bf16_pair(w[u].y >> 16, s[u]));
-                p[1] = make_uint4(bf16_pair(w[u].z, s[u]), bf16_pair(w[u].z >> 16, s[u]), bf16_pair(w[u].w, s[u]),
-                                  bf16_pair(w[u].w >> 16, s[u]));
+                const float f = q8_scale(s[u]);
+                const uint32_t o[8] = {bf16_pair(w[u].x, f), bf16_pair(w[u].x >> 16, f), bf16_pair(w[u].y, f),
+                                       bf16_pair(w[u].y >> 16, f), bf16_pair(w[u].z, f), bf16_pair(w[u].z >> 16, f),
+                                       bf16_pair(w[u].w, f), bf16_pair(w[u].w >> 16, f)};
+                st_global_v8(out + size_t(i) * 32, o);
             }
         }
     }
@@ -88,7 +104,8 @@ cudaError_t launch_cache_read(const CacheQ8 &c, const int32_t *bt_in, const int3
     a.max_blocks = s.max_blocks;
     a.G = s.G;
     a.err = err;
-    return launch_kernel(k_cache_read, dim3(unsigned(n_req) * unsigned(s.max_blocks), kidx ? 3u : 2u), dim3(kThreads), 0,
+    const bool even = kThreads % (s.G * (s.D / 16)) == 0 && (!kidx || kThreads % (s.G * (s.Di / 16)) == 0);
+    return launch_kernel(even ? k_cache_read<true> : k_cache_read<false>, dim3(unsigned(n_req) * unsigned(s.max_blocks), kidx ? 3u : 2u), dim3(kThreads), 0,
                          st, false, a);
 }
 

@@ -36,12 +36,55 @@ struct Args {
     int32_t *err;
 };
 
+// (y0, y1) = (y0, y1) (c0, c1) + (p0, p1) (s0, s1), two fp32 lanes per instruction.
+__device__ __forceinline__ void turn2(float &y0, float &y1, float p0, float p1, float c0, float c1, float s0, float s1) {
+    asm("{\n\t.reg .b64 y, p, c, s;\n\tmov.b64 y, {%0, %1};\n\tmov.b64 p, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\t"
+        "mov.b64 s, {%6, %7};\n\tmul.rn.f32x2 y, y, c;\n\tfma.rn.f32x2 y, p, s, y;\n\tmov.b64 {%0, %1}, y;\n\t}"
+        : "+f"(y0), "+f"(y1)
+        : "f"(p0), "f"(p1), "f"(c0), "f"(c1), "f"(s0), "f"(s1));
+}
+
 template <bool Q8, int RPC>
-__global__ void __launch_bounds__(kThreads) k_rope_append(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 4) k_rope_append(const __grid_constant__ Args a) {
     __shared__ __align__(16) float cos_s[RPC][kMaxPairs], sin_s[RPC][kMaxPairs];
     __shared__ int page_s[RPC], slot_s[RPC];   // page -1: nothing of the row is written
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row0 = blockIdx.x * RPC;
+
+    const int nq = a.Hq * a.D / 256, nk = (a.G * a.D + 255) / 256, ni = a.index ? (a.G * a.Di + 255) / 256 : 0;
+    const int n_tasks = nq + 2 * nk + 2 * ni;
+    struct Task {
+        int sec, chunk, width, heads;    // section: 0 q, 1 k, 2 v, 3 q_idx, 4 k_idx; the lane's chunk in it
+    };
+    auto task = [&](int t) {
+        Task x;
+        int first;
+        if (t < nq) x.sec = 0, first = 0;
+        else if (t < nq + nk) x.sec = 1, first = nq;
+        else if (t < nq + 2 * nk) x.sec = 2, first = nq + nk;
+        else if (t < nq + 2 * nk + ni) x.sec = 3, first = nq + 2 * nk;
+        else x.sec = 4, first = nq + 2 * nk + ni;
+        x.chunk = (t - first) * 32 + lane;
+        x.width = x.sec >= 3 ? a.Di : a.D;
+        x.heads = x.sec == 0 ? a.Hq : a.G;
+        return x;
+    };
+    auto load = [&](const Task &x, uint4 (&v)[RPC]) {
+        const bool in = x.chunk < x.heads * (x.width >> 3);
+        const uint16_t *src = a.src[x.sec] + size_t(x.chunk) * 8 + (long long)row0 * a.stride[x.sec];
+#pragma unroll
+        for (int k = 0; k < RPC; ++k) {
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (in && row0 + k < a.n_rows) v[k] = ldg_stream_v4(src + k * a.stride[x.sec]);
+        }
+    };
+    uint4 v[RPC];
+    int t = blockIdx.y * (kThreads / 32) + warp;
+    Task x = {};
+    if (t < n_tasks) {                   // on their way while the angles are worked out
+        x = task(t);
+        load(x, v);
+    }
 
     if (tid < RPC) {
         const int r = row0 + tid;
@@ -73,48 +116,41 @@ __global__ void __launch_bounds__(kThreads) k_rope_append(const __grid_constant_
             const unsigned long long pos = r < a.n_rows ? (unsigned long long)(long long)a.q_pos[r] : 0ull;
             float s, c;
             sincospif(__ll2float_rn((long long)(turn * pos)) * 0x1p-63f, &s, &c);   // half turns in [-1, 1]
-            const int at = i < half ? i : i - half + 64;
+            // Half-split pairs come eight to a chunk: the first four of all chunks, then the second four, so that the
+            // lanes of a vector read neighbouring 16 bytes.
+            const bool idx = i >= half;
+            const int j = idx ? i - half : i, quarter = (idx ? a.rot_idx : a.rot) >> 2;
+            const int at = (idx ? 64 : 0) + (a.interleaved ? j : (j >> 2 & 1) * quarter + (j >> 3) * 4 + (j & 3));
             cos_s[k][at] = c * a.gain;
             sin_s[k][at] = s * a.gain;
         }
     }
     __syncthreads();
 
-    const int nq = a.Hq * a.D / 256, nk = (a.G * a.D + 255) / 256, ni = a.index ? (a.G * a.Di + 255) / 256 : 0;
-    const int n_tasks = nq + 2 * nk + 2 * ni;
-    for (int t = blockIdx.y * (kThreads / 32) + warp; t < n_tasks; t += gridDim.y * (kThreads / 32)) {
-        // section: 0 q, 1 k, 2 v, 3 q_idx, 4 k_idx
-        int sec, first;
-        if (t < nq) sec = 0, first = 0;
-        else if (t < nq + nk) sec = 1, first = nq;
-        else if (t < nq + 2 * nk) sec = 2, first = nq + nk;
-        else if (t < nq + 2 * nk + ni) sec = 3, first = nq + 2 * nk;
-        else sec = 4, first = nq + 2 * nk + ni;
-        const int width = sec >= 3 ? a.Di : a.D, heads = sec == 0 ? a.Hq : a.G;
-        const int lpv = width >> 3;                          // lanes of one vector: 4, 8 or 16
-        const int chunk = (t - first) * 32 + lane;           // of 8 components
-        const bool in = chunk < heads * lpv;
-        const int head = chunk / lpv, cpos = chunk - head * lpv;
+    while (t < n_tasks) {
+        const int sec = x.sec, chunk = x.chunk;
+        const int lv = __ffs(x.width) - 4, lpv = 1 << lv;    // lanes of one vector: 4, 8 or 16
+        const bool in = chunk < x.heads << lv;
+        const int head = chunk >> lv, cpos = chunk & (lpv - 1);
         const int rot = sec == 2 ? 0 : sec >= 3 ? a.rot_idx : a.rot;
-        const uint16_t *src = a.src[sec] + size_t(chunk) * 8;
-
-        uint4 v[RPC];
-#pragma unroll
-        for (int k = 0; k < RPC; ++k) {
-            v[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (in && page_s[k] >= 0)
-                v[k] = ldg_stream_v4(src + (long long)(row0 + k) * a.stride[sec]);
-        }
+        const bool cached = sec == 1 || sec == 2 || sec == 4;
+        const int which = sec == 4 ? 2 : sec - 1;            // of the caches
         // which lane holds the partners, and which cosines turn this chunk
         const int hc = rot >> 4;                             // chunks of half the rotated part
         const bool turned = cpos < 2 * hc;
         const bool upper = !a.interleaved && turned && cpos >= hc;
         const int partner = a.interleaved || !turned ? lane : upper ? lane - hc : lane + hc;
-        const int at = (sec >= 3 ? 64 : 0) + (a.interleaved ? cpos * 4 : (upper ? cpos - hc : cpos) * 8);
+        const uint32_t flip = upper ? 0u : 0x80008000u;      // (a, b) -> (a cos - b sin, b cos + a sin)
+        const int at = (sec >= 3 ? 64 : 0) + (upper ? cpos - hc : cpos) * 4;
 #pragma unroll
         for (int k = 0; k < RPC; ++k) {
-            float x[8] = {bf16_lo(v[k].x), bf16_hi(v[k].x), bf16_lo(v[k].y), bf16_hi(v[k].y),
-                          bf16_lo(v[k].z), bf16_hi(v[k].z), bf16_lo(v[k].w), bf16_hi(v[k].w)};
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[2 * i] = bf16_lo(w[i]);
+                y[2 * i + 1] = bf16_hi(w[i]);
+            }
             if (rot > 0) {   // uniform in the warp
                 if (a.interleaved) {
                     if (turned) {
@@ -123,66 +159,66 @@ __global__ void __launch_bounds__(kThreads) k_rope_append(const __grid_constant_
                         const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float u = x[2 * i], w = x[2 * i + 1];
-                            x[2 * i] = u * cc[i] - w * ss[i];
-                            x[2 * i + 1] = w * cc[i] + u * ss[i];
+                            const float u = y[2 * i], z = y[2 * i + 1];
+                            y[2 * i] = u * cc[i] - z * ss[i];
+                            y[2 * i + 1] = z * cc[i] + u * ss[i];
                         }
                     }
                 } else {
-                    uint32_t p[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                    uint32_t p[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = __shfl_sync(0xffffffffu, p[i], partner);
+                    for (int i = 0; i < 4; ++i) p[i] = __shfl_sync(0xffffffffu, w[i], partner) ^ flip;
                     if (turned) {
-                        const float sign = upper ? 1.f : -1.f;
 #pragma unroll
-                        for (int i = 0; i < 8; i += 4) {
-                            const float4 c = *reinterpret_cast<const float4 *>(&cos_s[k][at + i]);
-                            const float4 s = *reinterpret_cast<const float4 *>(&sin_s[k][at + i]);
-                            x[i] = x[i] * c.x + sign * bf16_lo(p[i / 2]) * s.x;
-                            x[i + 1] = x[i + 1] * c.y + sign * bf16_hi(p[i / 2]) * s.y;
-                            x[i + 2] = x[i + 2] * c.z + sign * bf16_lo(p[i / 2 + 1]) * s.z;
-                            x[i + 3] = x[i + 3] * c.w + sign * bf16_hi(p[i / 2 + 1]) * s.w;
+                        for (int i = 0; i < 4; i += 2) {
+                            const float4 c = *reinterpret_cast<const float4 *>(&cos_s[k][at + (i >> 1) * (rot >> 2)]);
+                            const float4 s = *reinterpret_cast<const float4 *>(&sin_s[k][at + (i >> 1) * (rot >> 2)]);
+                            turn2(y[2 * i], y[2 * i + 1], bf16_lo(p[i]), bf16_hi(p[i]), c.x, c.y, s.x, s.y);
+                            turn2(y[2 * i + 2], y[2 * i + 3], bf16_lo(p[i + 1]), bf16_hi(p[i + 1]), c.z, c.w, s.z, s.w);
                         }
                     }
                 }
             }
             const int page = page_s[k], slot = slot_s[k];
             const bool live = in && page >= 0;
-            const bool cached = sec == 1 || sec == 2 || sec == 4;
             if (Q8 && cached) {
-                const int which = sec == 4 ? 2 : sec - 1;
                 uint32_t amax = 0u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+                for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7fffffffu);
                 for (int o = 1; o < lpv; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                 const bool bad = amax >= 0x7f800000u;        // a NaN or an infinity among the components
                 const int e = bad ? 0 : q8_exponent(amax);
                 const float inv = exp2i(-e);
                 uint2 code;
-                code.x = pack_e4m3x2(x[0] * inv, x[1] * inv) | pack_e4m3x2(x[2] * inv, x[3] * inv) << 16;
-                code.y = pack_e4m3x2(x[4] * inv, x[5] * inv) | pack_e4m3x2(x[6] * inv, x[7] * inv) << 16;
+                code.x = pack_e4m3x2(y[0] * inv, y[1] * inv) | pack_e4m3x2(y[2] * inv, y[3] * inv) << 16;
+                code.y = pack_e4m3x2(y[4] * inv, y[5] * inv) | pack_e4m3x2(y[6] * inv, y[7] * inv) << 16;
                 if (bad) code = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
                 if (live) {
                     const size_t line = (size_t(page) * a.G + head) * 128 + slot;
-                    *reinterpret_cast<uint2 *>(a.dst[which] + line * width + cpos * 8) = code;
+                    *reinterpret_cast<uint2 *>(a.dst[which] + line * x.width + cpos * 8) = code;
                     if (cpos == 0) {
                         a.scale[which][line] = bad ? uint8_t(255) : uint8_t(e + 127);
                         if (bad) raise_flag(a.err, MSA_FLAG_NAN);
                     }
                 }
             } else if (live) {
-                const uint4 w = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                           pack_bf16x2(x[6], x[7]));
-                if (sec == 0) {
-                    *reinterpret_cast<uint4 *>(a.q_out + size_t(row0 + k) * a.Hq * a.D + size_t(chunk) * 8) = w;
-                } else if (sec == 3) {
-                    *reinterpret_cast<uint4 *>(a.q_idx_out + size_t(row0 + k) * a.G * a.Di + size_t(chunk) * 8) = w;
-                } else {
-                    uint16_t *dst = reinterpret_cast<uint16_t *>(a.dst[sec == 4 ? 2 : sec - 1]);
-                    *reinterpret_cast<uint4 *>(dst + ((size_t(page) * 128 + slot) * a.G + head) * width + cpos * 8) =
-                        sec == 2 ? v[k] : w;
-                }
+                uint4 o = v[k];                              // what does not turn goes on as it is
+                if (turned)
+                    o = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                   pack_bf16x2(y[6], y[7]));
+                uint16_t *dst;
+                if (sec == 0) dst = a.q_out + size_t(row0 + k) * a.Hq * a.D + size_t(chunk) * 8;
+                else if (sec == 3) dst = a.q_idx_out + size_t(row0 + k) * a.G * a.Di + size_t(chunk) * 8;
+                else
+                    dst = reinterpret_cast<uint16_t *>(a.dst[which]) +
+                          ((size_t(page) * 128 + slot) * a.G + head) * x.width + cpos * 8;
+                *reinterpret_cast<uint4 *>(dst) = o;
             }
+        }
+        t += gridDim.y * (kThreads / 32);
+        if (t < n_tasks) {
+            x = task(t);
+            load(x, v);
         }
     }
 }

@@ -720,7 +720,9 @@ msa_status_t msa_cache_read_q8(const msa_cache_q8_t *cache, const int32_t *block
     st = check_cache_q8(cache, true, kidx_cache != nullptr, &c, "msa_cache_read_q8");
     if (st != MSA_OK) return st;
     MSA_REQUIRE(block_table && out_table && lens && k_cache && v_cache && err_word, "msa_cache_read_q8: NULL pointer");
-    MSA_REQUIRE(!misaligned16({k_cache, v_cache, kidx_cache}), "msa_cache_read_q8: caches must be 16-byte aligned");
+    const uintptr_t at = reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
+                         reinterpret_cast<uintptr_t>(kidx_cache);
+    MSA_REQUIRE((at & 31u) == 0, "msa_cache_read_q8: the bf16 caches must be 32-byte aligned");
     if (1LL * n_req * s.max_blocks > 0x7fffffffLL)
         return fail(MSA_ERR_UNSUPPORTED, "msa_cache_read_q8: n_req * max_blocks >= 2^31");
     const cudaError_t e = launch_cache_read(c, block_table, out_table, lens, n_req, n_pages, n_out_pages, s, k_cache,

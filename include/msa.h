@@ -631,7 +631,8 @@ msa_status_t msa_rope_append_q8(const msa_rows_t *rows, const msa_rope_t *rope, 
  *   k_cache, v_cache  bf16 [n_out_pages][128][G][D] out;  kidx_cache bf16 [n_out_pages][128][G][Di] out,
  *                     or NULL (then cache->kidx is not read)
  * A page outside [0, n_pages) of a block to be written, or an out_table entry >= n_out_pages, raises
- * MSA_FLAG_BOUNDS and that block is not written.  No two blocks may go to the same page.
+ * MSA_FLAG_BOUNDS and that block is not written.  No two blocks may go to the same page.  The bf16 caches are
+ * 32-byte aligned.
  */
 msa_status_t msa_cache_read_q8(const msa_cache_q8_t *cache, const int32_t *block_table, const int32_t *out_table,
                                const int32_t *lens, int32_t n_req, int32_t n_pages, int32_t n_out_pages,

@@ -84,9 +84,10 @@ def test_append(msa, q8, Hq, G, D, Di, rot, rot_idx, inter, ctx, n, pad, fused, 
         cache, _ = make_cache(msa, dims, pool, 11)
         if not index:
             cache = msa.CacheQ8(cache.k, cache.k_scale, cache.v, cache.v_scale)
-        before = [None if x is None else u8(x).clone() for x in vars(cache).values()]
+        parts8 = (cache.k, cache.k_scale, cache.v, cache.v_scale, cache.kidx, cache.kidx_scale)
+        before = [None if x is None else u8(x).clone() for x in parts8]
         out = msa.msa_rope_append_q8(*parts, cache, *t, rope, dims, q_out, qi_out, err_word=err)
-        after = [None if x is None else u8(x) for x in vars(cache).values()]
+        after = [None if x is None else u8(x) for x in parts8]
     else:
         caches = [Q.normal((pool, 128, G, w), 20 + w).cuda() for w in (D, D, Di)]
         before = [x.clone() for x in caches]

@@ -102,6 +102,7 @@ def test_bad_sizes_and_pointers(lib):  # noqa: F811
     for call in ALL:
         assert call(lib, d, n_pages=0) == 1
     assert _read(lib, d, n_req=-1) == 1 and _read(lib, d, n_out=0) == 1 and _read(lib, d, k=None) == 1
+    assert _read(lib, d, k=ctypes.c_void_p(0x1010)) == 1 and _read(lib, d, kidx=ctypes.c_void_p(0x1010)) == 1
     assert _attn(lib, d, B=-1) == 1 and _step(lib, d, B=-1) == 1
     for call in (_score, _attn, _step, _window):
         assert call(lib, d, q=None) == 1 and call(lib, d, q=ODD) == 1
