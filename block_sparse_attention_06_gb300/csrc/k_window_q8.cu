@@ -50,14 +50,15 @@ struct Step {
     uint32_t nan_v[4];     // tokens whose V row is NaN (kNan)
 };
 
-template <int D>
+template <int D, bool PAIR>
 struct Smem {
+    static constexpr int TILE = 128 * D * 2 / (PAIR ? 2 : 1);   // a CTA's part of a page's K or V
     alignas(1024) uint8_t q[2][128 * D * 2];
-    alignas(1024) uint8_t k[2][128 * D * 2];
-    alignas(1024) uint8_t v[2][128 * D * 2];
+    alignas(1024) uint8_t k[2][TILE];
+    alignas(1024) uint8_t v[2][TILE];
     Step step[kRing];
     uint64_t desc_full[kRing], desc_empty[kRing];
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_tma[2], q_full[2], q_empty[2];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], o_full[2];   // per tile
     float part[2][2][128];       // per tile and half of the page: a row's maximum, at the end its sum
@@ -106,11 +107,30 @@ __device__ __forceinline__ float sum2(uint64_t acc2) {
 __device__ __forceinline__ uint32_t ones_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // D/16 MMAs of S = Q K^T, both operands K-major with the 128-byte swizzle: a k-step of 16 columns is 32 bytes
-// further in a sub-tile of 64 columns, and sub-tiles are 16 KB apart.
-// One asm block, so that the issuing thread spends as few issue slots as it can.
-template <int D>
+// further in a sub-tile of 64 columns; sub-tiles are 16 KB apart (a pair's halves of K: 8 KB).  One asm block, so that
+// the issuing thread spends as few issue slots as it can.
+template <int D, bool PAIR>
 __device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-    if constexpr (D == 128) {
+    static_assert(D == 128 || !PAIR, "pairs have D = 128");
+    if constexpr (PAIR) {
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+            "setp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
+            "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 512;\n\t"
+            "add.s64 b5, %2, 514;\n\tadd.s64 b6, %2, 516;\n\tadd.s64 b7, %2, 518;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], a4, b4, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], a5, b5, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], a6, b6, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
+            : "memory");
+    } else if constexpr (D == 128) {
         asm volatile(
             "{\n\t.reg .pred f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
             "setp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
@@ -145,24 +165,105 @@ __device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32
 
 // Eight MMAs of O (+)= P V: P in TMEM (bf16 pairs, 8 columns per 16 tokens, the halves of 64 tokens 64 columns
 // apart), V MN-major, 16 tokens 2 KB apart.
+template <bool PAIR>
 __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (PAIR) {
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+            "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+            "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 64;\n\t"
+            "add.s32 a5, %1, 72;\n\tadd.s32 a6, %1, 80;\n\tadd.s32 a7, %1, 88;\n\t"
+            "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
+            "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a4], b4, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a5], b5, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a6], b6, %3, t;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
+            "r"(p), "l"(v), "r"(idesc), "r"(accumulate)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+            "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+            "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 64;\n\t"
+            "add.s32 a5, %1, 72;\n\tadd.s32 a6, %1, 80;\n\tadd.s32 a7, %1, 88;\n\t"
+            "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
+            "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
+            "r"(p), "l"(v), "r"(idesc), "r"(accumulate)
+            : "memory");
+    }
+}
+
+// A pair of CTAs: MMAs of M = 256 over both SMs, issued by the first CTA.  Barriers that the issuer waits on are the
+// first CTA's; its commits arrive in both CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                         smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+    else
+        mma_commit(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void arrive_first(uint64_t *bar) {
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+                     "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar)) : "memory");
+    else
+        mbar_arrive(bar);
+}
+
+// mbar_wait for arrivals of both CTAs.
+static __device__ __noinline__ bool wait_pair_slow(uint64_t *bar, uint32_t parity, int32_t *err, volatile int *abort);
+
+__device__ __forceinline__ bool try_wait_pair(uint64_t *bar, uint32_t parity, uint32_t hint_ns) {
+    uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
-        "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 64;\n\t"
-        "add.s32 a5, %1, 72;\n\tadd.s32 a6, %1, 80;\n\tadd.s32 a7, %1, 88;\n\t"
-        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
-        "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
-        "r"(p), "l"(v), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
         : "memory");
+    return ok != 0;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ bool wait_both(uint64_t *bar, uint32_t parity, int32_t *err, volatile int *abort) {
+    if constexpr (PAIR) return try_wait_pair(bar, parity, 0) || wait_pair_slow(bar, parity, err, abort);
+    else return mbar_wait(bar, parity, err, abort);
+}
+
+static __device__ __noinline__ bool wait_pair_slow(uint64_t *bar, uint32_t parity, int32_t *err, volatile int *abort) {
+    const uint64_t t0 = global_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (try_wait_pair(bar, parity, kWaitSleepNs)) return true;
+        if ((it & 15u) == 0u) {
+            if (abort && *abort) return false;
+            if (global_ns() - t0 > kWaitLimitNs) {
+                raise_flag(err, MSA_FLAG_TIMEOUT);
+                if (abort) *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -193,15 +294,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
-template <int D, int HPG>
+template <int D, int HPG, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     k_window_q8(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap qmap) {
     constexpr int EPT = 128 / HPG;       // rows per tile
     constexpr int NSUB = D / 64;         // 64-column sub-tiles
-    constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, 0, 0);
-    constexpr uint32_t kIdescO = make_idesc_bf16(128, D, 0, 1);
+    constexpr int CT = PAIR ? 2 : 1;     // CTAs that work on an item
+    constexpr uint32_t kIdescS = make_idesc_bf16(CT * 128, 128, 0, 0);
+    constexpr uint32_t kIdescO = make_idesc_bf16(CT * 128, D, 0, 1);
+    using S = Smem<D, PAIR>;
     extern __shared__ uint8_t smem_raw[];
-    Smem<D> &sm = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int rank = PAIR ? blockIdx.x & 1 : 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int32_t *const err = a.err;
 
@@ -211,14 +315,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.desc_empty[i], 26);   // issuer, Q loader, 16 softmax warps, 8 converter warps
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_tma[i], 1);
+            mbar_init(&sm.q_full[i], CT);
             mbar_init(&sm.q_empty[i], 1);
-            mbar_init(&sm.k_full[i], 8);
+            mbar_init(&sm.k_full[i], 8 * CT);
             mbar_init(&sm.k_empty[i], 1);
-            mbar_init(&sm.v_full[i], 8);
+            mbar_init(&sm.v_full[i], 8 * CT);
             mbar_init(&sm.v_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 8);
+            mbar_init(&sm.p_full[i], 8 * CT);
             mbar_init(&sm.o_full[i], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -226,12 +331,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(&sm.tmem_base, 512);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                         "r"(512) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            tmem_alloc(&sm.tmem_base, 512);
+            tmem_relinquish();
+        }
     }
     if (warp == 21 && lane == 0) tma_prefetch_desc(&qmap);
     tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are there too
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     const volatile Step *const steps = sm.step;
@@ -275,11 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&sm.desc_full[slot]);
             ++s;
         };
-        for (int item = blockIdx.x; ok && item < a.n_items; item += gridDim.x) {
-            const int pair = item / a.G, g = item - pair * a.G;
-            const int row0 = pair * 2 * EPT;
-            // the item's rows, EPT / 16 a lane
-            constexpr int RPL = 2 * EPT / 32;
+        for (int item = blockIdx.x / CT; ok && item < a.n_items; item += gridDim.x / CT) {
+            const int set = item / a.G, g = item - set * a.G;
+            const int row0 = set * 2 * CT * EPT, mine0 = row0 + rank * 2 * EPT;
+            // the item's rows (both CTAs of a pair plan the same steps), 2 CT EPT / 32 a lane
+            constexpr int RPL = 2 * CT * EPT / 32;
             int rq[RPL], rp[RPL];
 #pragma unroll
             for (int i = 0; i < RPL; ++i) {
@@ -344,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         st.page = pg;
                         st.base = jj * 128;
                         st.req = req;
-                        st.row0 = row0;
+                        st.row0 = mine0;
                         st.g = g;
                         vs = vn;
                         flags = 0;
@@ -362,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (ok && flags == kFirst) {   // no row of the item sees a page that exists: zeros
                 for (int i = lane; i < 2 * EPT * HPG; i += 32) {
-                    const int r = row0 + i / HPG;
+                    const int r = mine0 + i / HPG;
                     if (r >= a.n_rows || a.q_req[r] == -1) continue;
                     const size_t h = size_t(r) * a.Hq + g * HPG + i % HPG;
                     for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.out + h * D + d) = make_uint4(0u, 0u, 0u, 0u);
@@ -386,12 +498,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     make_smem_desc(smem_u32(sm.v[1]), 16384, 1024, 2)};
             // P V of tile x at step s; `first`: overwrite O
             auto issue_pv = [&](int x, int s, bool first, bool last) -> bool {
-                if (!mbar_wait(&sm.p_full[x], s & 1, err, &sm.abort)) return false;
-                if (x == 0 && !mbar_wait(&sm.v_full[s & 1], (s >> 1) & 1, err, &sm.abort)) return false;
+                if (!wait_both<PAIR>(&sm.p_full[x], s & 1, err, &sm.abort)) return false;
+                if (x == 0 && !wait_both<PAIR>(&sm.v_full[s & 1], (s >> 1) & 1, err, &sm.abort)) return false;
                 tc_fence_after();
-                mma_pv(tmem + 256u + uint32_t(x * D), tmem + uint32_t(x * 128), vd[s & 1], kIdescO, first ? 0u : 1u);
-                if (last) mma_commit(&sm.o_full[x]);
-                if (x == 1) mma_commit(&sm.v_empty[s & 1]);
+                mma_pv<PAIR>(tmem + 256u + uint32_t(x * D), tmem + uint32_t(x * 128), vd[s & 1], kIdescO, first ? 0u : 1u);
+                if (last) commit<PAIR>(&sm.o_full[x]);
+                if (x == 1) commit<PAIR>(&sm.v_empty[s & 1]);
                 return true;
             };
             int items = 0;               // whose Q has been waited for
@@ -402,24 +514,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int flags = steps[slot].flags;
                 mbar_arrive(&sm.desc_empty[slot]);
                 if (flags & kEnd) break;
+                if (rank != 0) continue;     // the first CTA issues for both
                 const bool first = flags & kFirst, last = flags & kLast;
-                if (!mbar_wait(&sm.k_full[s & 1], (s >> 1) & 1, err, &sm.abort)) break;
-                if (first && !mbar_wait(&sm.q_full[0], items & 1, err, &sm.abort)) break;
+                if (!wait_both<PAIR>(&sm.k_full[s & 1], (s >> 1) & 1, err, &sm.abort)) break;
+                if (first && !wait_both<PAIR>(&sm.q_full[0], items & 1, err, &sm.abort)) break;
                 tc_fence_after();
-                mma_s<D>(tmem, qd[0], kd[s & 1], kIdescS);
-                mma_commit(&sm.s_full[0]);
-                if (last) mma_commit(&sm.q_empty[0]);
+                mma_s<D, PAIR>(tmem, qd[0], kd[s & 1], kIdescS);
+                commit<PAIR>(&sm.s_full[0]);
+                if (last) commit<PAIR>(&sm.q_empty[0]);
                 if (b_pending) {
                     b_pending = false;
                     if (!issue_pv(1, s - 1, b_first, false)) break;
                 }
-                if (first && !mbar_wait(&sm.q_full[1], items & 1, err, &sm.abort)) break;
+                if (first && !wait_both<PAIR>(&sm.q_full[1], items & 1, err, &sm.abort)) break;
                 if (first) ++items;
                 tc_fence_after();
-                mma_s<D>(tmem + 128u, qd[1], kd[s & 1], kIdescS);
-                mma_commit(&sm.s_full[1]);
-                mma_commit(&sm.k_empty[s & 1]);
-                if (last) mma_commit(&sm.q_empty[1]);
+                mma_s<D, PAIR>(tmem + 128u, qd[1], kd[s & 1], kIdescS);
+                commit<PAIR>(&sm.s_full[1]);
+                commit<PAIR>(&sm.k_empty[s & 1]);
+                if (last) commit<PAIR>(&sm.q_empty[1]);
                 if (!issue_pv(0, s, first, last)) break;
                 b_pending = true;
                 b_first = first;
@@ -428,8 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!issue_pv(1, s, first, last)) break;
                 }
             }
-            mma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0, err, nullptr);
+            if (rank == 0) {
+                if constexpr (PAIR)
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                     smem_u32(&sm.drain)) : "memory");
+                else
+                    mma_commit(&sm.drain);
+                mbar_wait(&sm.drain, 0, err, nullptr);
+            }
         }
     } else if (warp == 21) {
         // ------------------------------------------------------------ Q loader (lane 0)
@@ -448,75 +567,97 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sm.q_full[x], 128 * D * 2);
+                    uint64_t *bar = PAIR ? &sm.q_tma[x] : &sm.q_full[x];
+                    mbar_arrive_expect_tx(bar, 128 * D * 2);
 #pragma unroll
                     for (int i = 0; i < NSUB; ++i)   // rows past the last read as zeros
-                        tma_load_3d(sm.q[x] + i * 16384, &qmap, &sm.q_full[x], i * 64, g * HPG, row0 + x * EPT);
+                        tma_load_3d(sm.q[x] + i * 16384, &qmap, bar, i * 64, g * HPG, row0 + x * EPT);
                     loaded[x] = items + 1;
                 }
                 if (!ok) break;
+                if constexpr (PAIR) {
+                    for (int x = 0; ok && x < 2; ++x) {
+                        ok = mbar_wait(&sm.q_tma[x], items & 1, err, &sm.abort);
+                        if (ok) arrive_first<PAIR>(&sm.q_full[x]);
+                    }
+                    if (!ok) break;
+                }
                 ++items;
             }
             if (sm.abort)                // copies in flight land before the CTA exits
                 for (int x = 0; x < 2; ++x)
-                    if (loaded[x] > 0) mbar_wait(&sm.q_full[x], (loaded[x] - 1) & 1, err, nullptr);
+                    if (loaded[x] > 0) mbar_wait(PAIR ? &sm.q_tma[x] : &sm.q_full[x], (loaded[x] - 1) & 1, err, nullptr);
         }
     } else if (warp == 25) {
         // idle: it would share the MMA issuer's sub-partition
     } else if (warp >= 20 || warp == 2 || warp == 3) {
         // ------------------------------------------------------------ converters
-        // A thread takes TPT consecutive tokens, 16 codes of each (its lane's column).  The upper four lanes of a
-        // quarter warp take them in the order 1, 0, 3, 2: the swizzle then puts the eight stores of a quarter warp
-        // into eight different 16-byte columns.
-        constexpr int LPT = D / 16;      // lanes per token
-        constexpr int TPT = LPT / 2;     // tokens per thread (256 threads, 128 tokens)
+        // A thread takes a few consecutive tokens, 16 codes of each (its lane's column).  The upper four lanes of a
+        // quarter warp take them in the order 1, 0, 3, 2: the swizzle then puts the eight stores of a quarter warp into
+        // eight different 16-byte columns.  A pair of CTAs shares a page: each converts half of K's tokens and half of
+        // V's columns, which is what the MMAs of pairs read of it.
         // warps 2, 3, 20, 22, 23, 24, 26, 27: none in the MMA issuer's sub-partition (warp index mod 4 = 1)
         const int w = warp < 4 ? warp - 2 : warp == 20 ? 2 : warp < 24 ? warp - 19 : warp == 24 ? 5 : warp - 20;
-        const int col = lane % LPT, tok0 = (w * (32 / LPT) + lane / LPT) * TPT;
         const int swap = (lane >> 2) & 1;
-        const uint32_t sub = uint32_t(col >> 2) * 16384u;   // sub-tile of 64 columns
-        const int ch = (col & 3) * 2;                       // its first 16-byte chunk
-        struct Rows {
-            uint4 c[TPT];
-            uint32_t sc;                 // scale bytes in the order of c
+        constexpr int KL = D / 16, KT = KL / 2 / CT;         // K: lanes per token, tokens per thread
+        constexpr int VL = D / 16 / CT, VT = D / 32 / CT;    // V
+        using Lane = struct {
+            int col, tok0;                                   // 16 codes of tokens tok0 ..
+            uint32_t at;                                     // their sub-tile of 64 columns
+            int ch;                                          // their first 16-byte chunk in it
+            size_t off;                                      // bytes from the page's first row
         };
-        auto load = [&](const uint8_t *codes, const uint8_t *scales, int page, int g, Rows &x) {
-            const size_t line = (size_t(page) * a.G + g) * 128 + tok0;
+        auto lane_of = [&](int lanes, int toks, int row_first, int col_first, uint32_t sub_bytes) {
+            Lane x;
+            x.col = lane % lanes;
+            x.tok0 = (w * (32 / lanes) + lane / lanes) * toks;
+            x.at = uint32_t(x.col >> 2) * sub_bytes;
+            x.ch = (x.col & 3) * 2;
+            x.off = size_t(row_first + x.tok0) * D + col_first + x.col * 16;
+            return x;
+        };
+        const Lane kl = lane_of(KL, KT, PAIR ? rank * 64 : 0, 0, PAIR ? 8192u : 16384u);
+        const Lane vl = lane_of(VL, VT, 0, PAIR ? rank * 64 : 0, 16384u);
+        // codes c[i] of token tok0 + (i ^ swap); returns the scale bytes in that order
+        auto load = [&](const uint8_t *codes, const uint8_t *scales, size_t page_line, const Lane &x, int row_first, auto &c) {
+            constexpr int T = sizeof(c) / sizeof(uint4);
+            const uint8_t *p = codes + page_line * D + x.off;
 #pragma unroll
-            for (int i = 0; i < TPT; ++i)
-                x.c[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (line + (i ^ swap)) * D + col * 16));
+            for (int i = 0; i < T; ++i) c[i] = __ldg(reinterpret_cast<const uint4 *>(p + (i ^ swap) * D));
+            const uint8_t *sp = scales + page_line + row_first + x.tok0;
             uint32_t sc;
-            if constexpr (TPT == 4) sc = __ldg(reinterpret_cast<const uint32_t *>(scales + line));
-            else sc = __ldg(reinterpret_cast<const uint16_t *>(scales + line));
-            x.sc = swap ? __byte_perm(sc, 0u, 0x2301) : sc;
+            if constexpr (T == 4) sc = __ldg(reinterpret_cast<const uint32_t *>(sp));
+            else sc = __ldg(reinterpret_cast<const uint16_t *>(sp));
+            return swap ? __byte_perm(sc, 0u, 0x2301) : sc;
         };
-        auto store = [&](uint8_t *tile, const Rows &x, bool values) {
-            const uint32_t base = smem_u32(tile) + sub;
-            const bool usual = (x.sc & 0x80808080u) == 0u;   // no scale above 1, no NaN row
+        auto store = [&](uint8_t *tile, const Lane &x, const auto &c, uint32_t sc, bool values) {
+            constexpr int T = sizeof(c) / sizeof(uint4);
+            const uint32_t base = smem_u32(tile) + x.at;
+            const bool usual = (sc & 0x80808080u) == 0u;     // no scale above 1, no NaN row
 #pragma unroll
-            for (int i = 0; i < TPT; ++i) {
-                const int t = tok0 + (i ^ swap);
-                const uint32_t b = (x.sc >> (8 * i)) & 255u;
+            for (int i = 0; i < T; ++i) {
+                const int t = x.tok0 + (i ^ swap);
+                const uint32_t b = (sc >> (8 * i)) & 255u;
                 uint32_t o[8];
                 if (usual) {             // 2^(120 + e), e = b - 127
-                    convert16(x.c[i], (b + 120u) * 0x00800080u, o);
+                    convert16(c[i], (b + 120u) * 0x00800080u, o);
                 } else {
                     // 2^120 and then 2^e where e > 0; a NaN row: of K NaN, so the logits of the rows that see it are; of
                     // V zeros (see above)
                     const uint32_t f = b == 255u ? (values ? 0u : 0x7fff7fffu) : (min(b, 127u) + 120u) * 0x00800080u;
                     const uint32_t up = b == 255u ? 0x3f803f80u : max(b, 127u) * 0x00800080u;
-                    convert16(x.c[i], f, o);
+                    convert16(c[i], f, o);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], up);
                 }
-                const uint32_t row = base + uint32_t(t * 128);
-                const uint32_t p0 = row + uint32_t((ch ^ (t & 7)) << 4);
+                const uint32_t p0 = base + uint32_t(t * 128) + uint32_t((x.ch ^ (t & 7)) << 4);
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0), "r"(o[0]), "r"(o[1]), "r"(o[2]),
                              "r"(o[3]) : "memory");
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0 ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]),
                              "r"(o[7]) : "memory");
             }
-            fence_proxy_async_smem();
+            if constexpr (PAIR) asm volatile("fence.proxy.async;" ::: "memory");   // read by MMAs of both SMs
+            else fence_proxy_async_smem();
             __syncwarp();
         };
         // the next step's descriptor; false at the end
@@ -532,23 +673,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++sd;
             return !(flags & kEnd);
         };
-        Rows kc, vc;
+        uint4 kc[KT], vc[VT];
+        uint32_t ks = 0u, vs = 0u;
+        auto load_k = [&]() { ks = load(a.k, a.k_scale, (size_t(page) * a.G + g) * 128, kl, PAIR ? rank * 64 : 0, kc); };
+        auto load_v = [&]() { vs = load(a.v, a.v_scale, (size_t(page) * a.G + g) * 128, vl, 0, vc); };
         bool more = desc();              // there is a step that is not written yet
         if (more) {
-            load(a.k, a.k_scale, page, g, kc);
-            load(a.v, a.v_scale, page, g, vc);
+            load_k();
+            load_v();
         }
         for (int s = 0; more; ++s) {
             const int b = s & 1;
             if (s >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.k_empty[b], ((s >> 1) - 1) & 1, err, &sm.abort))) break;
-            store(sm.k[b], kc, false);
-            if (lane == 0) mbar_arrive(&sm.k_full[b]);
+            store(sm.k[b], kl, kc, ks, false);
+            if (lane == 0) arrive_first<PAIR>(&sm.k_full[b]);
             more = desc();
-            if (more) load(a.k, a.k_scale, page, g, kc);
+            if (more) load_k();
             if (s >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.v_empty[b], ((s >> 1) - 1) & 1, err, &sm.abort))) break;
-            store(sm.v[b], vc, true);
-            if (lane == 0) mbar_arrive(&sm.v_full[b]);
-            if (more) load(a.v, a.v_scale, page, g, vc);
+            store(sm.v[b], vl, vc, vs, true);
+            if (lane == 0) arrive_first<PAIR>(&sm.v_full[b]);
+            if (more) load_v();
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax (warps 4-11: A, 12-19: B)
@@ -680,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&sm.p_full[x]);
+            if (ok && lane == 0) arrive_first<PAIR>(&sm.p_full[x]);
             if (flags & kLast) {
                 meet();                  // both have read the maxima
                 *mine = poison ? -l : l;                    // the sign bit says that V was NaN
@@ -718,12 +862,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // neither CTA leaves while the other's MMAs or arrivals may reach it
+    else __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) {
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        else
+            tmem_dealloc(tmem, 512);
+    }
 }
 
-template <int D, int HPG>
+template <int D, int HPG, bool PAIR>
 cudaError_t launch_t(const void *q, Args a, const Shape &s, cudaStream_t st) {
     alignas(64) CUtensorMap qm;
     const char *why = nullptr;
@@ -731,16 +881,27 @@ cudaError_t launch_t(const void *q, Args a, const Shape &s, cudaStream_t st) {
     const uint64_t strides[2] = {uint64_t(D) * 2, uint64_t(s.Hq) * D * 2};
     const uint32_t box[3] = {64u, uint32_t(HPG), uint32_t(128 / HPG)};
     if (!encode_tensor_map(&qm, 3, q, dims, strides, box, 128, &why)) return cudaErrorInvalidValue;
-    constexpr int kRows = 2 * 128 / HPG;
+    constexpr int CT = PAIR ? 2 : 1, kRows = 2 * CT * 128 / HPG;
     const long long items = ((a.n_rows + kRows - 1LL) / kRows) * s.G;
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.n_items = int(items);
-    const size_t smem = sizeof(Smem<D>) + 1024;
+    const size_t smem = sizeof(Smem<D, PAIR>) + 1024;
+    auto k = k_window_q8<D, HPG, PAIR>;
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_once(allowed, reinterpret_cast<const void *>(k_window_q8<D, HPG>), smem);
+    const cudaError_t e = allow_once(allowed, reinterpret_cast<const void *>(k), smem);
     if (e != cudaSuccess) return e;
-    return launch_kernel(k_window_q8<D, HPG>, dim3(unsigned(std::min<long long>(items, sm_count()))), dim3(kThreads), smem,
-                         st, false, a, qm);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min<long long>(items, sm_count() / CT) * CT));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CT;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a, qm);
 }
 
 }  // namespace
@@ -769,7 +930,7 @@ cudaError_t launch_window_prefill_q8(const void *q, const CacheQ8 &c, const int3
     a.lse = lse;
     a.err = err;
 #define MSA_WQ_CASE(DD, HH) \
-    if (s.D == DD && s.hpg == HH) return launch_t<DD, HH>(q, a, s, st);
+    if (s.D == DD && s.hpg == HH) return launch_t<DD, HH, DD == 128>(q, a, s, st);
     MSA_WQ_CASE(128, 8) MSA_WQ_CASE(128, 4) MSA_WQ_CASE(64, 8) MSA_WQ_CASE(64, 4)
 #undef MSA_WQ_CASE
     return cudaErrorNotSupported;
