@@ -207,7 +207,9 @@ __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint3
 }
 
 // A pair of CTAs: MMAs of M = 256 over both SMs, issued by the first CTA.  Barriers that the issuer waits on are the
-// first CTA's; its commits arrive in both CTAs.
+// first CTA's; its commits arrive in both CTAs.  What these arrivals hand over is read by the tensor cores alone: the
+// fences before them (of tcgen05, of the async proxy) order it, and a release over the cluster, which would hold
+// the softmax warps up for 1500 cycles per step, is not needed.
 template <bool PAIR>
 __device__ __forceinline__ void commit(uint64_t *bar) {
     if constexpr (PAIR)
@@ -221,45 +223,9 @@ template <bool PAIR>
 __device__ __forceinline__ void arrive_first(uint64_t *bar) {
     if constexpr (PAIR)
         asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
-                     "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar)) : "memory");
+                     "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar)) : "memory");
     else
         mbar_arrive(bar);
-}
-
-// mbar_wait for arrivals of both CTAs.
-static __device__ __noinline__ bool wait_pair_slow(uint64_t *bar, uint32_t parity, int32_t *err, volatile int *abort);
-
-__device__ __forceinline__ bool try_wait_pair(uint64_t *bar, uint32_t parity, uint32_t hint_ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
-        : "memory");
-    return ok != 0;
-}
-
-template <bool PAIR>
-__device__ __forceinline__ bool wait_both(uint64_t *bar, uint32_t parity, int32_t *err, volatile int *abort) {
-    if constexpr (PAIR) return try_wait_pair(bar, parity, 0) || wait_pair_slow(bar, parity, err, abort);
-    else return mbar_wait(bar, parity, err, abort);
-}
-
-static __device__ __noinline__ bool wait_pair_slow(uint64_t *bar, uint32_t parity, int32_t *err, volatile int *abort) {
-    const uint64_t t0 = global_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (try_wait_pair(bar, parity, kWaitSleepNs)) return true;
-        if ((it & 15u) == 0u) {
-            if (abort && *abort) return false;
-            if (global_ns() - t0 > kWaitLimitNs) {
-                raise_flag(err, MSA_FLAG_TIMEOUT);
-                if (abort) *abort = 1;
-                return false;
-            }
-        }
-    }
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -498,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     make_smem_desc(smem_u32(sm.v[1]), 16384, 1024, 2)};
             // P V of tile x at step s; `first`: overwrite O
             auto issue_pv = [&](int x, int s, bool first, bool last) -> bool {
-                if (!wait_both<PAIR>(&sm.p_full[x], s & 1, err, &sm.abort)) return false;
-                if (x == 0 && !wait_both<PAIR>(&sm.v_full[s & 1], (s >> 1) & 1, err, &sm.abort)) return false;
+                if (!mbar_wait(&sm.p_full[x], s & 1, err, &sm.abort)) return false;
+                if (x == 0 && !mbar_wait(&sm.v_full[s & 1], (s >> 1) & 1, err, &sm.abort)) return false;
                 tc_fence_after();
                 mma_pv<PAIR>(tmem + 256u + uint32_t(x * D), tmem + uint32_t(x * 128), vd[s & 1], kIdescO, first ? 0u : 1u);
                 if (last) commit<PAIR>(&sm.o_full[x]);
@@ -516,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (flags & kEnd) break;
                 if (rank != 0) continue;     // the first CTA issues for both
                 const bool first = flags & kFirst, last = flags & kLast;
-                if (!wait_both<PAIR>(&sm.k_full[s & 1], (s >> 1) & 1, err, &sm.abort)) break;
-                if (first && !wait_both<PAIR>(&sm.q_full[0], items & 1, err, &sm.abort)) break;
+                if (!mbar_wait(&sm.k_full[s & 1], (s >> 1) & 1, err, &sm.abort)) break;
+                if (first && !mbar_wait(&sm.q_full[0], items & 1, err, &sm.abort)) break;
                 tc_fence_after();
                 mma_s<D, PAIR>(tmem, qd[0], kd[s & 1], kIdescS);
                 commit<PAIR>(&sm.s_full[0]);
@@ -526,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     b_pending = false;
                     if (!issue_pv(1, s - 1, b_first, false)) break;
                 }
-                if (first && !wait_both<PAIR>(&sm.q_full[1], items & 1, err, &sm.abort)) break;
+                if (first && !mbar_wait(&sm.q_full[1], items & 1, err, &sm.abort)) break;
                 if (first) ++items;
                 tc_fence_after();
                 mma_s<D, PAIR>(tmem + 128u, qd[1], kd[s & 1], kIdescS);
