@@ -33,21 +33,21 @@
 namespace msa {
 namespace {
 
-constexpr int kThreads = 896;
+constexpr int kThreads = 640;
 constexpr int kRing = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;        // log2 units by which a logit may pass its row's reference
 
-constexpr int kFirst = 1, kLast = 2, kEnd = 4, kNan = 8;
+constexpr int kFirst = 1, kLast = 2, kEnd = 4, kNan = 8, kWhole = 16;   // kWhole: every row sees every token
 
-struct Step {
+struct alignas(16) Step {
     int32_t flags;
     int32_t page;          // physical page
     int32_t base;          // position of its first token
     int32_t req;
-    int32_t row0, g;       // the item: its first row, its group
     uint32_t nan_v[4];     // tokens whose V row is NaN (kNan)
+    int32_t row0, g;       // the item: its first row, its group
 };
 
 template <int D, bool PAIR>
@@ -61,7 +61,6 @@ struct Smem {
     uint64_t q_tma[2], q_full[2], q_empty[2];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], o_full[2];   // per tile
-    float part[2][2][128];       // per tile and half of the page: a row's maximum, at the end its sum
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -163,16 +162,15 @@ __device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32
     }
 }
 
-// Eight MMAs of O (+)= P V: P in TMEM (bf16 pairs, 8 columns per 16 tokens, the halves of 64 tokens 64 columns
-// apart), V MN-major, 16 tokens 2 KB apart.
+// Eight MMAs of O (+)= P V: P in TMEM (bf16 pairs, 8 columns per 16 tokens), V MN-major, 16 tokens 2 KB apart.
 template <bool PAIR>
 __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t accumulate) {
     if constexpr (PAIR) {
         asm volatile(
             "{\n\t.reg .pred f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
             "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-            "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 64;\n\t"
-            "add.s32 a5, %1, 72;\n\tadd.s32 a6, %1, 80;\n\tadd.s32 a7, %1, 88;\n\t"
+            "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 32;\n\t"
+            "add.s32 a5, %1, 40;\n\tadd.s32 a6, %1, 48;\n\tadd.s32 a7, %1, 56;\n\t"
             "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
             "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
             "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, f;\n\t"
@@ -189,8 +187,8 @@ __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint3
         asm volatile(
             "{\n\t.reg .pred f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
             "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-            "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 64;\n\t"
-            "add.s32 a5, %1, 72;\n\tadd.s32 a6, %1, 80;\n\tadd.s32 a7, %1, 88;\n\t"
+            "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 32;\n\t"
+            "add.s32 a5, %1, 40;\n\tadd.s32 a6, %1, 48;\n\tadd.s32 a7, %1, 56;\n\t"
             "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
             "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
@@ -278,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sm.desc_full[i], 32);
-            mbar_init(&sm.desc_empty[i], 26);   // issuer, Q loader, 16 softmax warps, 8 converter warps
+            mbar_init(&sm.desc_empty[i], 18);   // issuer, Q loader, 8 softmax warps, 8 converter warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_tma[i], 1);
@@ -289,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.v_full[i], 8 * CT);
             mbar_init(&sm.v_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 8 * CT);
+            mbar_init(&sm.p_full[i], 4 * CT);
             mbar_init(&sm.o_full[i], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -306,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_relinquish();
         }
     }
-    if (warp == 21 && lane == 0) tma_prefetch_desc(&qmap);
+    if (warp == 2 && lane == 0) tma_prefetch_desc(&qmap);
     tc_fence_before();
     if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are there too
     else __syncthreads();
@@ -369,6 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rq[i] = -1;
                 }
             }
+            int rq0[RPL];
+#pragma unroll
+            for (int i = 0; i < RPL; ++i) rq0[i] = rq[i];
             int flags = kFirst;
             auto next_req = [&]() {      // the lowest request that is left, -1 for none
                 int m = 0x7fffffff;
@@ -387,6 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 pmin = __reduce_min_sync(0xffffffffu, pmin);
                 pmax = __reduce_max_sync(0xffffffffu, pmax);
+                bool alone = true;           // no row of another request
+#pragma unroll
+                for (int i = 0; i < RPL; ++i) alone &= rq0[i] == -1 || rq0[i] == req;
+                alone = __all_sync(0xffffffffu, alone);
                 const int32_t *table = a.block_table + size_t(req) * a.max_blocks;
                 const int sink = min(a.n_sink, pmax + 1);
                 const int n_sp = (sink + 127) >> 7;                       // blocks with tokens that stay visible
@@ -418,7 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t vn = __ldg(
                             reinterpret_cast<const uint32_t *>(a.v_scale + (size_t(pg) * a.G + g) * 128) + lane);
                         if (pending) publish(0);
-                        st.flags = flags;
+                        const bool whole = alone && jj * 128 + 127 <= pmin &&
+                                           (jj * 128 > pmax - a.window || jj * 128 + 128 <= a.n_sink);
+                        st.flags = flags | (whole ? kWhole : 0);
                         st.page = pg;
                         st.base = jj * 128;
                         st.req = req;
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(&sm.drain, 0, err, nullptr);
             }
         }
-    } else if (warp == 21) {
+    } else if (warp == 2) {
         // ------------------------------------------------------------ Q loader (lane 0)
         if (lane == 0) {
             int items = 0, loaded[2] = {0, 0};
@@ -554,16 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < 2; ++x)
                     if (loaded[x] > 0) mbar_wait(PAIR ? &sm.q_tma[x] : &sm.q_full[x], (loaded[x] - 1) & 1, err, nullptr);
         }
-    } else if (warp == 25) {
-        // idle: it would share the MMA issuer's sub-partition
-    } else if (warp >= 20 || warp == 2 || warp == 3) {
+    } else if (warp >= 12) {
         // ------------------------------------------------------------ converters
         // A thread takes a few consecutive tokens, 16 codes of each (its lane's column).  The upper four lanes of a
         // quarter warp take them in the order 1, 0, 3, 2: the swizzle then puts the eight stores of a quarter warp into
         // eight different 16-byte columns.  A pair of CTAs shares a page: each converts half of K's tokens and half of
         // V's columns, which is what the MMAs of pairs read of it.
-        // warps 2, 3, 20, 22, 23, 24, 26, 27: none in the MMA issuer's sub-partition (warp index mod 4 = 1)
-        const int w = warp < 4 ? warp - 2 : warp == 20 ? 2 : warp < 24 ? warp - 19 : warp == 24 ? 5 : warp - 20;
+        const int w = warp - 12;
         const int swap = (lane >> 2) & 1;
         constexpr int KL = D / 16, KT = KL / 2 / CT;         // K: lanes per token, tokens per thread
         constexpr int VL = D / 16 / CT, VT = D / 32 / CT;    // V
@@ -622,8 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0 ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]),
                              "r"(o[7]) : "memory");
             }
-            if constexpr (PAIR) asm volatile("fence.proxy.async;" ::: "memory");   // read by MMAs of both SMs
-            else fence_proxy_async_smem();
+            fence_proxy_async_smem();
             __syncwarp();
         };
         // the next step's descriptor; false at the end
@@ -661,83 +664,95 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) load_v();
         }
     } else if (warp >= 4) {
-        // ------------------------------------------------------------ softmax (warps 4-11: A, 12-19: B)
-        // A row is two threads, 64 tokens of the page each: their warps read the same TMEM lanes.
-        const int x = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1;
+        // ------------------------------------------------------------ softmax (warps 4-7: A, 8-11: B)
+        const int x = (warp - 4) >> 2;
         const int quad = warp & 3;                          // TMEM lanes this warp may access
         const int trow = quad * 32 + lane;
         const int e = trow / HPG, h = trow - e * HPG;
-        const uint32_t t_s = tmem + (uint32_t(quad * 32) << 16) + uint32_t(x * 128 + hf * 64);
-        const uint32_t t_o = tmem + (uint32_t(quad * 32) << 16) + 256u + uint32_t(x * D + hf * (D / 2));
+        const uint32_t t_s = tmem + (uint32_t(quad * 32) << 16) + uint32_t(x * 128);
+        const uint32_t t_o = tmem + (uint32_t(quad * 32) << 16) + 256u + uint32_t(x * D);
         const float scale = a.sm_scale * kLog2e;
         const uint64_t scale2 = dup2(scale);
-        float *const mine = &sm.part[x][hf][trow];
-        const volatile float *const other = &sm.part[x][hf ^ 1][trow];
-        auto meet = [&]() {              // the two warps of these rows
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + x * 4 + quad) : "memory");
-        };
-        int row = -1, req = -1, pos = -1;                   // of this thread, in the item at hand
+        int row = -1, req = -1, pos = -1, g = 0;            // of this thread, in the item at hand
         int items = 0;                   // done
         float ref = -INFINITY, l = 0.f;
         bool poison = false;
         for (int s = 0;; ++s) {
             const int slot = s % kRing;
             bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.desc_full[slot], (s / kRing) & 1, err, &sm.abort));
-            const int flags = steps[slot].flags, base = steps[slot].base + hf * 64, sreq = steps[slot].req;
-            const int row0 = steps[slot].row0, g = steps[slot].g;
-            uint64_t nan_v = 0u;
-            if (flags & kNan) nan_v = uint64_t(steps[slot].nan_v[2 * hf + 1]) << 32 | steps[slot].nan_v[2 * hf];
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&sm.desc_empty[slot]);
-            if (!ok || (flags & kEnd)) break;
+            const int4 d = *reinterpret_cast<const int4 *>(&sm.step[slot]);
+            const int flags = d.x;
+            uint32_t nan_v[4] = {0u, 0u, 0u, 0u};
+            if (flags & kNan) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) nan_v[i] = steps[slot].nan_v[i];
+            }
             if (flags & kFirst) {
-                row = row0 + x * EPT + e;
+                row = steps[slot].row0 + x * EPT + e;
+                g = steps[slot].g;
                 req = row < a.n_rows ? a.q_req[row] : -1;
                 pos = row < a.n_rows ? a.q_pos[row] : 0;
                 ref = -INFINITY;
                 l = 0.f;
                 poison = false;
             }
-            // Tokens c of this half with c <= hi and (c >= lo or c < sk) are visible: bit c % 32 of word c / 32.  Rows of
-            // a tile are near one another, so most words are all ones or all zeros in the whole warp.
-            const int hi = req == sreq ? pos - base : -1;
-            const int lo = pos - (a.window - 1) - base, sk = a.n_sink - base;
-            uint32_t see[2];
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&sm.desc_empty[slot]);
+            if (!ok || (flags & kEnd)) break;
+            // Tokens c of the page with c <= hi and (c >= lo or c < sk) are visible: bit c % 32 of word c / 32.  Rows of
+            // a tile are near one another, so where the page as a whole is not, most words are all ones or all zeros
+            // in the whole warp.
+            uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+            if (!(flags & kWhole)) {
+                const int hi = req == d.w ? pos - d.z : -1;
+                const int lo = pos - (a.window - 1) - d.z, sk = a.n_sink - d.z;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t below = ones_below(hi + 1 - 32 * k);
-                see[k] = below & (~ones_below(lo - 32 * k) | ones_below(sk - 32 * k));
+                for (int k = 0; k < 4; ++k)
+                    see[k] = ones_below(hi + 1 - 32 * k) & (~ones_below(lo - 32 * k) | ones_below(sk - 32 * k));
             }
-            if (nan_v) {
-                poison |= (uint32_t(nan_v) & see[0]) != 0u || (uint32_t(nan_v >> 32) & see[1]) != 0u;
-            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) poison |= (nan_v[k] & see[k]) != 0u;
             ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], s & 1, err, &sm.abort));
             tc_fence_after();
-            // pass 1: the row's maximum, over both halves
+            // pass 1: the row's maximum
             float mx[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+            if (flags & kWhole) {
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t bits = k ? see[1] : see[0];
-                if (!__any_sync(0xffffffffu, bits != 0u)) continue;
-                uint32_t v[32];
-                tmem_ld32(t_s + uint32_t(32 * k), v);
-                tmem_ld_wait();
-                if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
+                for (int c = 0; c < 128; c += 64) {
+                    uint32_t v[2][32];
+                    tmem_ld32(t_s + uint32_t(c), v[0]);
+                    tmem_ld32(t_s + uint32_t(c + 32), v[1]);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1u ? v[i] : 0xff800000u;
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 16)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                mx[j] = fmax3(mx[j], __uint_as_float(v[k][i + j]), __uint_as_float(v[k][i + 8 + j]));
                 }
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t bits = k < 2 ? (k ? see[1] : see[0]) : k == 2 ? see[2] : see[3];
+                    if (!__any_sync(0xffffffffu, bits != 0u)) continue;
+                    uint32_t v[32];
+                    tmem_ld32(t_s + uint32_t(32 * k), v);
+                    tmem_ld_wait();
+                    if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 16)
+                        for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1u ? v[i] : 0xff800000u;
+                    }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        mx[j] = fmax3(mx[j], __uint_as_float(v[i + j]), __uint_as_float(v[i + 8 + j]));
+                    for (int i = 0; i < 32; i += 16)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            mx[j] = fmax3(mx[j], __uint_as_float(v[i + j]), __uint_as_float(v[i + 8 + j]));
+                }
             }
-            float m = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * scale;
-            *mine = m;
-            meet();
-            m = fmaxf(m, *other);
+            const float m = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * scale;
             // raise the reference where a logit passes it too far; O so far is brought to the new one
             const bool raise = m > ref + kRaise;            // false for rows that see nothing
             if (__any_sync(0xffffffffu, raise)) {
@@ -747,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l *= al;
                 if (!(flags & kFirst)) {   // S of this step came behind the P V before it: O is complete up to there
 #pragma unroll 1
-                    for (int c = 0; c < D / 2; c += 16) {
+                    for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
                         tmem_ld16(t_o + uint32_t(c), o);
                         tmem_ld_wait();
@@ -760,58 +775,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             // pass 2: P as bf16 over the columns already read, and its sum
             const uint64_t nref2 = dup2(ref == -INFINITY ? 0.f : -ref);
             uint64_t acc2[4] = {0, 0, 0, 0};
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t bits = k ? see[1] : see[0];
-                uint32_t w[16];
-                if (!__any_sync(0xffffffffu, bits != 0u)) {
+            auto weigh = [&](const uint32_t (&v)[32], uint32_t (&w)[16]) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = 0u;
-                } else {
-                    uint32_t v[32];
-                    tmem_ld32(t_s + uint32_t(32 * k), v);
-                    tmem_ld_wait();
-                    if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1u ? v[i] : 0xff800000u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float xa, xb;
-                        ffma2(xa, xb, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), scale2, nref2);
-                        const float pa = fast_exp2(xa), pb = fast_exp2(xb);
-                        w[i] = pack_bf16x2(pa, pb);
-                        fadd2_acc(acc2[i & 3], pa, pb);
-                    }
+                for (int i = 0; i < 16; ++i) {
+                    float xa, xb;
+                    ffma2(xa, xb, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), scale2, nref2);
+                    const float pa = fast_exp2(xa), pb = fast_exp2(xb);
+                    w[i] = pack_bf16x2(pa, pb);
+                    fadd2_acc(acc2[i & 3], pa, pb);
                 }
-                tmem_st16(t_s + uint32_t(16 * k), w);
+            };
+            if (flags & kWhole) {
+                uint32_t v[2][32];       // a chunk's load is in flight while the one before it is worked on
+                tmem_ld32(t_s, v[0]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k < 3) tmem_ld32(t_s + uint32_t(32 * k + 32), v[(k + 1) & 1]);
+                    uint32_t w[16];
+                    weigh(v[k & 1], w);
+                    tmem_st16(t_s + uint32_t(16 * k), w);
+                    if (k < 3) tmem_ld_wait();
+                }
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t bits = k < 2 ? (k ? see[1] : see[0]) : k == 2 ? see[2] : see[3];
+                    uint32_t w[16];
+                    if (!__any_sync(0xffffffffu, bits != 0u)) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = 0u;
+                    } else {
+                        uint32_t v[32];
+                        tmem_ld32(t_s + uint32_t(32 * k), v);
+                        tmem_ld_wait();
+                        if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1u ? v[i] : 0xff800000u;
+                        }
+                        weigh(v, w);
+                    }
+                    tmem_st16(t_s + uint32_t(16 * k), w);
+                }
             }
-            l += (sum2(acc2[0]) + sum2(acc2[1])) + (sum2(acc2[2]) + sum2(acc2[3]));
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (ok && lane == 0) arrive_first<PAIR>(&sm.p_full[x]);
+            l += (sum2(acc2[0]) + sum2(acc2[1])) + (sum2(acc2[2]) + sum2(acc2[3]));
             if (flags & kLast) {
-                meet();                  // both have read the maxima
-                *mine = poison ? -l : l;                    // the sign bit says that V was NaN
-                meet();
-                const float l2 = *other, sum = l + fabsf(l2);
-                const bool bad = poison || (__float_as_uint(l2) >> 31);
-                meet();                  // both have read the sums
                 ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[x], items & 1, err, &sm.abort)) && ok;
                 ++items;
                 tc_fence_after();
                 const bool live = ok && row < a.n_rows && req != -1;
                 const size_t head = live ? size_t(row) * a.Hq + g * HPG + h : 0;
-                const float inv = bad ? __uint_as_float(0x7fffffffu) : sum == 0.f ? 0.f : 1.0f / sum;
-                uint16_t *o_out = a.out + head * D + hf * (D / 2);
+                const float inv = poison ? __uint_as_float(0x7fffffffu) : l == 0.f ? 0.f : 1.0f / l;
+                uint16_t *o_out = a.out + head * D;
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(t_o + uint32_t(c), o);
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(t_o + uint32_t(c), o);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 8) {
+                    for (int i = 0; i < 32; i += 8) {
                         uint4 w;
                         w.x = pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
                         w.y = pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
@@ -820,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (live) *reinterpret_cast<uint4 *>(o_out + c + i) = w;
                     }
                 }
-                if (live && hf == 0) a.lse[head] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+                if (live) a.lse[head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
                 tc_fence_before();
             }
             if (!ok) break;
