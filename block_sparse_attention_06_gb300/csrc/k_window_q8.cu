@@ -110,97 +110,98 @@ __device__ __forceinline__ uint32_t ones_below(int n) { return n >= 32 ? 0xfffff
 // further in a sub-tile of 64 columns; sub-tiles are 16 KB apart (a pair's halves of K: 8 KB).  One asm block, so that
 // the issuing thread spends as few issue slots as it can.
 template <int D, bool PAIR>
-__device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t el) {
     static_assert(D == 128 || !PAIR, "pairs have D = 128");
     if constexpr (PAIR) {
         asm volatile(
-            "{\n\t.reg .pred f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
-            "setp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+            "setp.ne.b32 e, %4, 0;\n\tsetp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
             "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
             "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
             "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 512;\n\t"
             "add.s64 b5, %2, 514;\n\tadd.s64 b6, %2, 516;\n\tadd.s64 b7, %2, 518;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, f;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], a4, b4, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], a5, b5, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], a6, b6, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc)
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a4, b4, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a5, b5, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a6, b6, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(el)
             : "memory");
     } else if constexpr (D == 128) {
         asm volatile(
-            "{\n\t.reg .pred f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
-            "setp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+            "setp.ne.b32 e, %4, 0;\n\tsetp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
             "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
             "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
             "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 1024;\n\t"
             "add.s64 b5, %2, 1026;\n\tadd.s64 b6, %2, 1028;\n\tadd.s64 b7, %2, 1030;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc)
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(el)
             : "memory");
     } else {
         asm volatile(
-            "{\n\t.reg .pred f, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-            "setp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+            "setp.ne.b32 e, %4, 0;\n\tsetp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
             "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
             "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc)
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(el)
             : "memory");
     }
 }
 
 // Eight MMAs of O (+)= P V: P in TMEM (bf16 pairs, 8 columns per 16 tokens), V MN-major, 16 tokens 2 KB apart.
 template <bool PAIR>
-__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t el) {
     if constexpr (PAIR) {
         asm volatile(
-            "{\n\t.reg .pred f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
-            "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+            "{\n\t.reg .pred e, f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+            "setp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
             "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 32;\n\t"
             "add.s32 a5, %1, 40;\n\tadd.s32 a6, %1, 48;\n\tadd.s32 a7, %1, 56;\n\t"
             "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
             "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, f;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a4], b4, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a5], b5, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a6], b6, %3, t;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
-            "r"(p), "l"(v), "r"(idesc), "r"(accumulate)
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a4], b4, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a5], b5, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a6], b6, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
+            "r"(p), "l"(v), "r"(idesc), "r"(accumulate), "r"(el)
             : "memory");
     } else {
         asm volatile(
-            "{\n\t.reg .pred f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
-            "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+            "{\n\t.reg .pred e, f, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+            "setp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
             "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 32;\n\t"
             "add.s32 a5, %1, 40;\n\tadd.s32 a6, %1, 48;\n\tadd.s32 a7, %1, 56;\n\t"
             "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
             "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
-            "r"(p), "l"(v), "r"(idesc), "r"(accumulate)
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
+            "r"(p), "l"(v), "r"(idesc), "r"(accumulate), "r"(el)
             : "memory");
     }
 }
@@ -210,12 +211,22 @@ __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint3
 // fences before them (of tcgen05, of the async proxy) order it, and a release over the cluster, which would hold
 // the softmax warps up for 1500 cycles per step, is not needed.
 template <bool PAIR>
-__device__ __forceinline__ void commit(uint64_t *bar) {
+__device__ __forceinline__ void commit(uint64_t *bar, uint32_t el) {
     if constexpr (PAIR)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                         smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+        asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+                     "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     "\n\t}" ::"r"(smem_u32(bar)), "h"(uint16_t(3)), "r"(el) : "memory");
     else
-        mma_commit(bar);
+        asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                     "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                         smem_u32(bar)), "r"(el) : "memory");
+}
+
+// 1 in one lane of the warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
 }
 
 template <bool PAIR>
@@ -461,67 +472,72 @@ __global__ void __launch_bounds__(kThreads, 1)
             publish(0);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer (lane 0)
-        if (lane == 0) {
-            const uint64_t qd[2] = {make_smem_desc(smem_u32(sm.q[0]), 16, 1024, 2),
-                                    make_smem_desc(smem_u32(sm.q[1]), 16, 1024, 2)};
-            const uint64_t kd[2] = {make_smem_desc(smem_u32(sm.k[0]), 16, 1024, 2),
-                                    make_smem_desc(smem_u32(sm.k[1]), 16, 1024, 2)};
-            const uint64_t vd[2] = {make_smem_desc(smem_u32(sm.v[0]), 16384, 1024, 2),
-                                    make_smem_desc(smem_u32(sm.v[1]), 16384, 1024, 2)};
-            // P V of tile x at step s; `first`: overwrite O
-            auto issue_pv = [&](int x, int s, bool first, bool last) -> bool {
-                if (!mbar_wait(&sm.p_full[x], s & 1, err, &sm.abort)) return false;
-                if (x == 0 && !mbar_wait(&sm.v_full[s & 1], (s >> 1) & 1, err, &sm.abort)) return false;
-                tc_fence_after();
-                mma_pv<PAIR>(tmem + 256u + uint32_t(x * D), tmem + uint32_t(x * 128), vd[s & 1], kIdescO, first ? 0u : 1u);
-                if (last) commit<PAIR>(&sm.o_full[x]);
-                if (x == 1) commit<PAIR>(&sm.v_empty[s & 1]);
-                return true;
-            };
-            int items = 0;               // whose Q has been waited for
-            bool b_pending = false, b_first = false;
-            for (int s = 0;; ++s) {
-                const int slot = s % kRing;
-                if (!mbar_wait(&sm.desc_full[slot], (s / kRing) & 1, err, &sm.abort)) break;
-                const int flags = steps[slot].flags;
-                mbar_arrive(&sm.desc_empty[slot]);
-                if (flags & kEnd) break;
-                if (rank != 0) continue;     // the first CTA issues for both
-                const bool first = flags & kFirst, last = flags & kLast;
-                if (!mbar_wait(&sm.k_full[s & 1], (s >> 1) & 1, err, &sm.abort)) break;
-                if (first && !mbar_wait(&sm.q_full[0], items & 1, err, &sm.abort)) break;
-                tc_fence_after();
-                mma_s<D, PAIR>(tmem, qd[0], kd[s & 1], kIdescS);
-                commit<PAIR>(&sm.s_full[0]);
-                if (last) commit<PAIR>(&sm.q_empty[0]);
-                if (b_pending) {
-                    b_pending = false;
-                    if (!issue_pv(1, s - 1, b_first, false)) break;
-                }
-                if (first && !mbar_wait(&sm.q_full[1], items & 1, err, &sm.abort)) break;
-                if (first) ++items;
-                tc_fence_after();
-                mma_s<D, PAIR>(tmem + 128u, qd[1], kd[s & 1], kIdescS);
-                commit<PAIR>(&sm.s_full[1]);
-                commit<PAIR>(&sm.k_empty[s & 1]);
-                if (last) commit<PAIR>(&sm.q_empty[1]);
-                if (!issue_pv(0, s, first, last)) break;
-                b_pending = true;
-                b_first = first;
-                if (last) {              // the item's results wait for it, and the next item's Q is still on its way
-                    b_pending = false;
-                    if (!issue_pv(1, s, first, last)) break;
-                }
+        // ------------------------------------------------------------ MMA issuer
+        // The warp stays together, and one lane's MMAs are predicated: descriptors then are uniform registers.
+        const uint32_t el = elect_one();
+        const uint64_t qd0 = make_smem_desc(smem_u32(sm.q[0]), 16, 1024, 2), qd1 = make_smem_desc(smem_u32(sm.q[1]), 16, 1024, 2);
+        const uint64_t kd0 = make_smem_desc(smem_u32(sm.k[0]), 16, 1024, 2);
+        const uint64_t vd0 = make_smem_desc(smem_u32(sm.v[0]), 16384, 1024, 2);
+        constexpr uint64_t kNext = Smem<D, PAIR>::TILE >> 4;      // from a descriptor to the other stage's
+        auto wait = [&](uint64_t *bar, int parity) {
+            return bool(__all_sync(0xffffffffu, mbar_wait(bar, uint32_t(parity), err, &sm.abort)));
+        };
+        // P V of tile x at step s; `first`: overwrite O
+        auto issue_pv = [&](int x, int s, bool first, bool last) -> bool {
+            if (!wait(&sm.p_full[x], s & 1)) return false;
+            if (x == 0 && !wait(&sm.v_full[s & 1], (s >> 1) & 1)) return false;
+            tc_fence_after();
+            mma_pv<PAIR>(tmem + 256u + uint32_t(x * D), tmem + uint32_t(x * 128), vd0 + uint64_t(s & 1) * kNext, kIdescO,
+                         first ? 0u : 1u, el);
+            if (last) commit<PAIR>(&sm.o_full[x], el);
+            if (x == 1) commit<PAIR>(&sm.v_empty[s & 1], el);
+            return true;
+        };
+        int items = 0;               // whose Q has been waited for
+        bool b_pending = false, b_first = false;
+        for (int s = 0;; ++s) {
+            const int slot = s % kRing;
+            if (!wait(&sm.desc_full[slot], (s / kRing) & 1)) break;
+            const int flags = steps[slot].flags;
+            const bool first = __any_sync(0xffffffffu, flags & kFirst), last = __any_sync(0xffffffffu, flags & kLast);
+            const bool end = __any_sync(0xffffffffu, flags & kEnd);
+            if (lane == 0) mbar_arrive(&sm.desc_empty[slot]);
+            if (end) break;
+            if (rank != 0) continue;     // the first CTA issues for both
+            if (!wait(&sm.k_full[s & 1], (s >> 1) & 1)) break;
+            if (first && !wait(&sm.q_full[0], items & 1)) break;
+            tc_fence_after();
+            const uint64_t kd = kd0 + uint64_t(s & 1) * kNext;
+            mma_s<D, PAIR>(tmem, qd0, kd, kIdescS, el);
+            commit<PAIR>(&sm.s_full[0], el);
+            if (last) commit<PAIR>(&sm.q_empty[0], el);
+            if (b_pending) {
+                b_pending = false;
+                if (!issue_pv(1, s - 1, b_first, false)) break;
             }
-            if (rank == 0) {
-                if constexpr (PAIR)
-                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                                     smem_u32(&sm.drain)) : "memory");
-                else
-                    mma_commit(&sm.drain);
-                mbar_wait(&sm.drain, 0, err, nullptr);
+            if (first && !wait(&sm.q_full[1], items & 1)) break;
+            if (first) ++items;
+            tc_fence_after();
+            mma_s<D, PAIR>(tmem + 128u, qd1, kd, kIdescS, el);
+            commit<PAIR>(&sm.s_full[1], el);
+            commit<PAIR>(&sm.k_empty[s & 1], el);
+            if (last) commit<PAIR>(&sm.q_empty[1], el);
+            if (!issue_pv(0, s, first, last)) break;
+            b_pending = true;
+            b_first = first;
+            if (last) {              // the item's results wait for it, and the next item's Q is still on its way
+                b_pending = false;
+                if (!issue_pv(1, s, first, last)) break;
             }
+        }
+        if (rank == 0) {
+            if constexpr (PAIR)
+                asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                             "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                                 smem_u32(&sm.drain)), "r"(el) : "memory");
+            else
+                commit<false>(&sm.drain, el);
+            mbar_wait(&sm.drain, 0, err, nullptr);
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ Q loader (lane 0)
