@@ -89,8 +89,10 @@ __device__ __forceinline__ uint64_t dup2(float x) {
     asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ void ffma2(float &d0, float &d1, float a0, float a1, uint64_t b2, uint64_t c2) {
-    asm("{\n\t.reg .b64 x, d;\n\tmov.b64 x, {%2, %3};\n\tfma.rn.f32x2 d, x, %4, %5;\n\tmov.b64 {%0, %1}, d;\n\t}"
+// d = (a + b) c
+__device__ __forceinline__ void add_mul2(float &d0, float &d1, float a0, float a1, uint64_t b2, uint64_t c2) {
+    asm("{\n\t.reg .b64 x, d;\n\tmov.b64 x, {%2, %3};\n\tadd.rn.f32x2 d, x, %4;\n\tmul.rn.f32x2 d, d, %5;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
         : "=f"(d0), "=f"(d1)
         : "f"(a0), "f"(a1), "l"(b2), "l"(c2));
 }
@@ -760,26 +762,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             float xa, xb;
-                            ffma2(xa, xb, __uint_as_float(c[2 * i]), __uint_as_float(c[2 * i + 1]), scale2, nref2);
+                            add_mul2(xa, xb, __uint_as_float(c[2 * i]), __uint_as_float(c[2 * i + 1]), nref2, scale2);
                             const float pa = fast_exp2(xa), pb = fast_exp2(xb);
                             w[k >> 1][8 * (k & 1) + i] = pack_bf16x2(pa, pb);
                             fadd2_acc(acc2[i & 3], pa, pb);
                         }
                     }
-                    const float m = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * scale;
-                    const bool raise = m > ref + kRaise;        // false for rows that see nothing
+                    const float m = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+                    const bool raise = (m - ref) * scale > kRaise;   // false for rows that see nothing
                     if (!__any_sync(0xffffffffu, raise)) {
                         tmem_st16(t_s + uint32_t(32 * hb), w[0]);
                         tmem_st16(t_s + uint32_t(32 * hb + 16), w[1]);
                         l += (sum2(acc2[0]) + sum2(acc2[1])) + (sum2(acc2[2]) + sum2(acc2[3]));
                         return;
                     }
-                    // by a whole number, so that what was summed with the old reference is brought to the new one by a
-                    // power of two: exactly, the first half's P (bf16) included
-                    const bool old = raise && ref != -INFINITY;
-                    const float up = old ? ceilf(m - ref) : 0.f;
+                    // by a whole number of binades, so that what was summed with the old reference is brought to the
+                    // new one by a power of two: exactly, the first half's P (bf16) included
+                    const float up = raise && ref != -INFINITY ? ceilf((m - ref) * scale) : 0.f;
                     const float al = up < 126.f ? __int_as_float((127 - int(up)) << 23) : 0.f;
-                    ref = old ? ref + up : raise ? m : ref;
+                    ref = !raise ? ref : up > 0.f && up < 126.f ? ref + up / scale : m;
                     l *= al;
                     const uint32_t al2 = pack_bf16x2(al, al);
                     tmem_st_wait();
@@ -839,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (live) *reinterpret_cast<uint4 *>(o_out + c + i) = w;
                     }
                 }
-                if (live) a.lse[head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+                if (live) a.lse[head] = l == 0.f ? -INFINITY : (ref * scale + log2f(l)) * kLn2;
                 tc_fence_before();
             }
             if (!ok) break;

@@ -677,6 +677,7 @@ msa_status_t msa_decode_step_q8(const void *q, const void *q_idx, const msa_cach
  *   window >= 1, n_sink >= 0
  *   phase  MSA_PHASE_DECODE: each row reads its own tokens.  MSA_PHASE_PREFILL: runs of 128/(Hq/G) consecutive
  *          rows share their reads, on the tensor cores; any rows, but it suits chunks of neighbouring tokens.
+ *          V is below 2^74 in magnitude (else a sum may overflow).
  *   out bf16 [n_rows][Hq][D] out;  lse fp32 [n_rows][Hq] out.  A row with q_req -1 is padding: nothing of it is
  *          written.
  * A bad request or position, or a page outside [0, n_pages) of a block that a row sees, raises

@@ -610,6 +610,53 @@ def test_window_all_key_codes(msa, phase):
 
 
 @pytest.mark.parametrize("phase", [0, 1])
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 1)])
+@pytest.mark.parametrize("shape", ["rising", "falling", "teeth"])
+@pytest.mark.parametrize("size", [-60, 0, 70])
+def test_window_logits_far_apart(msa, phase, D, G, shape, size):
+    """Logits that pass one another by far within a page and from page to page, upwards in every other head and
+    downwards in the rest, over small and large values."""
+    n = 700
+    bt, pool = Q.tables([n], 1)
+    t = torch.arange(n)
+    a = {"rising": t / 4, "falling": (n - t) / 4, "teeth": (t % 96) * 1.0}[shape].double()
+    k = torch.zeros((pool, G, 128, D)).double()
+    k[bt[0].long()[t // 128], :, t % 128] = a[:, None, None].expand(n, G, D)
+    v = Q.normal((pool, G, 128, D), 2).double() * 2.0 ** size
+    kc, vc = Q.to_cache(k), Q.to_cache(v)
+    cache = msa.CacheQ8(*cuda(*kc, *vc))
+    R = 150
+    q = (Q.normal((R, 8 * G, D), 3, 0.05).float() + (1.0 - 2.0 * (torch.arange(8 * G) % 2))[:, None]).to(torch.bfloat16)
+    req, pos = i32([0] * R), torch.arange(n - R, n, dtype=torch.int32)
+    dims = msa.Dims(8 * G, G, D, 64, 1, bt.shape[1], 1.0 / D)
+    out, lse = msa.msa_window_attn_q8(q.cuda(), cache, *cuda(bt, req, pos), 400, 5, dims, phase)
+    o, s, bo, bs = Q.ref_window(q, Q.stored(*kc), Q.stored(*vc), bt, req, pos, 400, 5, 1.0 / D)
+    Q.assert_within(out, o, bo, "out")
+    Q.assert_within(lse, s, bs, "lse")
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 10, 2.0 ** 20, 2.0 ** 40])
+def test_window_huge_logits_of_chunks(msa, scale):
+    """As of decode rows: with logits whose steps in fp32 are whole numbers or more, the output stays a mean of values
+    that the row sees."""
+    n, dims = 300, msa.Dims(16, 2, 128, 64, 1, 3, scale)
+    bt, pool = Q.tables([n], 1)
+    cache, (k, v, _) = make_cache(msa, dims, pool, 2)
+    q = Q.normal((n, 16, 128), 3)
+    req, pos = i32([0] * n), torch.arange(n, dtype=torch.int32)
+    out, lse = msa.msa_window_attn_q8(q.cuda(), cache, *cuda(bt, req, pos), 100, 0, dims, msa.MSA_PHASE_PREFILL)
+    assert bool(torch.isfinite(lse).all())
+    for r in range(0, n, 7):
+        t = torch.arange(max(0, r - 99), r + 1)
+        for g in range(2):
+            seen = v[bt[0].long()[t // 128], g, t % 128]
+            got = out[r, 8 * g:8 * g + 8].double().cpu()
+            top, low = seen.amax(0), seen.amin(0)
+            top, low = top * (1 + top.sign() * 2.0 ** -7), low * (1 - low.sign() * 2.0 ** -7)
+            assert bool((got <= top).all()) and bool((got >= low).all())
+
+
+@pytest.mark.parametrize("phase", [0, 1])
 def test_window_rows_in_any_order(msa, phase):
     """Rows of several requests, shuffled, with padding among them; one row twice."""
     bt, pool = Q.tables([400, 260, 150], 1)
