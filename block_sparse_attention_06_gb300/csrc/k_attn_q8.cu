@@ -22,6 +22,11 @@
 // (The 8-bit MMA of warps takes codes as they are, but is no faster: it unpacks its operands itself, every time, and
 // needs P and q in pieces.)
 //
+// Measured (Hq = 64, G = 8, D = 128).  8 requests x 16 blocks (33 MB): 13.3 us against 5.0 at the copy rate; the chain is a
+// launch, two table loads, four units per warp at some 2,000 cycles and the join.  32 requests, window of 4,096 (257 MB):
+// 50 us against 38; 256 clusters of one CTA on 152 SMs leave a third of the SMs one row where the others have two.  First
+// kernel, with 8-bit MMAs: 17.5 and 94.
+//
 // Layout.  A unit's K and V are 32 rows of D bytes, swizzled by the copy (128- or 64-byte pattern).  Lane (r, c) =
 // (lane / 4, lane % 4) reads a quarter of K's rows 8i + r, i = 0 .. 3, and an eighth of V's rows 8i + 2c and 8i + 2c + 1:
 // with the swizzle both take distinct banks (D = 128).  The C fragment of S^T then has the tokens 8i + r; P packed over
@@ -472,7 +477,10 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int D, int HPG, bool WINDOW>
 cudaError_t launch_t(Args a, long long rows, int units, cudaStream_t st, bool pdl) {
-    // As many CTAs as fit the SMs at two each, as long as every warp of the cluster has two units.
+    // As many CTAs as fit the SMs at two each, as long as every warp of the cluster has two units.  Clusters of 1, 2, 4, 8
+    // and 16 CTAs, in us (*: what this takes): 64 rows of 16 blocks 21.7, 14.5, *13.4, 23.3, 56; 256 rows of a window of
+    // 4,096 *50, 56, 64, 92, 231; 8 rows of a window of 1,024 14.5, 10.2, *8.0, 7.7, 10.7; 24 rows of 11 blocks, D = 64,
+    // 11.9, 8.4, *6.9, 7.5, 16.9.  (Clusters of 16 wait for 16 SMs of one GPC.)
     const long long want = 2LL * sm_count();
     int cs = 1;
     while (cs < kMaxCluster && rows * cs * 2 <= want && cs * 4 * kWarps <= units) cs *= 2;

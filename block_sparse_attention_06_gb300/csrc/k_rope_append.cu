@@ -11,9 +11,15 @@
 // so it is counted in turns in 64-bit fixed point: inv_freq / 2 pi, modulo one turn, as a fraction of 2^64;
 // times the position, modulo 2^64, is the exact fraction of a turn.
 //
-// Memory-bound (16-byte loads and stores, every byte once).  A warp takes 32 chunks of 8 components of one
+// Every byte is moved once, by 16-byte loads and stores.  A warp takes 32 chunks of 8 components of one
 // section (q, k, v, q_idx or k_idx) at a time, in RPC rows at once, so RPC loads of a lane are in flight; a
 // vector's lanes are neighbours, so half-split partners and the largest magnitude come by shuffles.
+//
+// Measured (Hq = 64, G = 8, D = 128, Di = 64).  8,192 rows into bf16 caches: 64 us, 5.8 TB/s, 0.85 of the copy rate;
+// into 8-bit caches: 72 us, 4.8 TB/s, 0.71: some 150 instructions per 512 bytes keep 0.64 of the issue slots
+// busy, and a warp's loads wait for its arithmetic.  8 rows: 2.9 us, the latency of one launch and one
+// load after the table's.  Two or eight rows per CTA, loads ahead of the task at hand, and CTAs that go on over
+// batches of rows were slower or no faster.
 #include "msa_internal.h"
 #include "msa_q8.cuh"
 
@@ -258,9 +264,11 @@ cudaError_t launch_rope_append(const RopeAppend &p, const Shape &s, cudaStream_t
     a.gain = p.gain;
     a.err = p.err;
     // Few rows: one row per CTA and one task per warp, for latency.  Many: four rows per CTA share the
-    // fractions of a turn and keep four loads per lane in flight.
+    // fractions of a turn and keep four loads per lane in flight.  Both, in us, bf16 / 8-bit: 8 rows
+    // 2.6 and 9.1 / 2.9 and 11.1; 304 rows 7.5 and 11.4 / 8.0 and 13.5; 500 rows 11.9 and 12.3 / 12.1 and 13.9; 608 rows
+    // 14.4 and 12.7 / 14.7 and 14.4; 2,048 rows 44 and 21 / 46 and 24.
     const int tasks = s.Hq * s.D / 256 + 2 * ((s.G * s.D + 255) / 256) + (a.index ? 2 * ((s.G * s.Di + 255) / 256) : 0);
-    const bool few = p.n_rows < 4 * sm_count();
+    const bool few = 2LL * p.n_rows < 7LL * sm_count();
     const dim3 grid(unsigned(few ? p.n_rows : (p.n_rows + 3) / 4), unsigned(few ? (tasks + 7) / 8 : 1));
     const bool q8 = p.scale[0] != nullptr;
     void (*k)(Args) = q8 ? (few ? k_rope_append<true, 1> : k_rope_append<true, 4>)

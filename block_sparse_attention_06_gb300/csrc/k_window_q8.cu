@@ -2,27 +2,36 @@
 //
 // Row r (position p of its request) attends the tokens t <= p with t > p - window or t < n_sink.  A tile is
 // 128/HPG consecutive rows times the HPG heads of one KV group = the 128 rows of an MMA's M; an item is two such
-// tiles (A, B) of one group, whose rows need nearly the same pages, and its steps are those pages:
-//   S = Q K^T  (128 x 128 x D),  P = 2^(S scale - ref),  O += P V  (128 x D x 128),  l += row sums of P.
-// ref is a row's reference: its maximum so far, raised only when a logit passes it by 2^8, so O is next to never
-// rescaled; out = O / l, lse = ref + log l.
+// tiles (A, B) per CTA of one group, whose rows need nearly the same pages, and its steps are those pages:
+//   S = Q K^T  (128 x 128 x D),  P = 2^((S - ref) scale),  O += P V  (128 x D x 128),  l += row sums of P.
+// ref is a row's reference, raised only where a logit passes it by 2^24 (P and the sums are bf16 and fp32, whose
+// precision does not depend on size), so O is next to never rescaled; out = O / l, lse = ref scale + log l.
 //
 // K and V come as codes and scales; eight warps turn a page into bf16 tiles in shared memory, exactly (a code
 // becomes code * 2^-120 by shifts and masks, one multiplication by a power of two gives the value), so the MMAs
-// round nothing of the cache.  A row of V that is NaN is written as zeros and the rows that see it are made NaN
-// at the end: what a row does not see cannot reach it, whatever its bits.
+// round nothing of the cache; P is rounded to bf16 (2^-9 of itself), as V is in a bf16 cache.  A row of V that is NaN is
+// written as zeros and the rows that see it are made NaN at the end: what a row does not see cannot reach it, whatever
+// its bits.
 //
-// What bounds it: per step and pair of tiles 2048 cycles of MMAs, about as much of shared memory (the MMAs read 192
-// KB of operands, the converters write 64 KB), and a good half of that of ALU work (exponentials and masks of 2 x 128 x
-// 128 logits, conversion of 32 KB of codes).  So the two tiles take turns: while one's softmax runs, the tensor cores
-// work on the other's S and P V.
+// With heads of 128 two CTAs (a cluster) share an item: each converts half of a page, K by tokens and V by columns,
+// and the MMAs of M = 256 read both halves.  (8,192 rows, window of 4,096, Hq = 64, G = 8: 1.03 ms, against 1.20 with
+// single CTAs, whose converters take twice the issue slots.  Heads of 64 use single CTAs: half of V's columns would be
+// half as wide as the operand's swizzle.)
+//
+// What bounds it: the chain S, softmax, P V of a tile.  TMEM holds two S and two O (512 columns with heads of 128), so
+// two tiles take turns, and a step of both takes about 4,200 cycles, of which the tensor cores work 2,048; issue
+// slots are busy half the time, memory next to never.  Measured: 8,192 rows at 60,000, window of 4,096, 4 sinks: 1.05 ms,
+// 0.55 of the measured bf16 rate counting the visible tokens.  What brought it there from 1.53 ms: arrivals without
+// a release over the cluster (1.61 -> 1.41), a softmax of one pass (1.41 -> 1.17; the maximum first, or a vote for every
+// 32 columns, breaks the code into short pieces), MMAs from a warp that stays together (1.17 -> 1.04).  One thread per
+// row and eight warps need half the instructions of two threads per row and sixteen.
 //
 // One CTA per SM, 20 warps, persistent over items:
 //   warp 0     planner: for each item the pages that any of its rows sees, in a ring of step descriptors;
-//   warp 1     MMA issuer and TMEM owner: S_A(s), P V of B(s-1), S_B(s), P V of A(s), ...;
+//   warp 1     MMA issuer and TMEM owner: S_A(s), P V of B(s-1), S_B(s), P V of A(s), ... (a pair's first CTA for both);
 //   warp 2     Q loader (TMA, one box per tile and 64 columns);   warp 3  idle;
 //   warps 4-7, 8-11   softmax of tiles A and B, one row per thread; each also writes its tile's results;
-//   warps 12-19  converters: K and V of the next two pages wait in registers while this one's are written.
+//   warps 12-19  converters: the next page's codes wait in registers while this one's are written.
 // TMEM: S_A | S_B | O_A | O_B (128 + 128 + D + D columns); P is written over S.
 // Every wait is bounded; a timeout raises MSA_FLAG_TIMEOUT and every role drains.
 #include "msa_internal.h"
@@ -38,7 +47,8 @@ constexpr int kThreads = 640;
 constexpr int kRing = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRaise = 24.f;       // log2 units by which a logit may pass its row's reference
+// log2 units by which a logit may pass its row's reference: with V below 2^74 the sums stay in fp32
+constexpr float kRaise = 24.f;
 
 constexpr int kFirst = 1, kLast = 2, kEnd = 4, kNan = 8, kWhole = 16;   // kWhole: every row sees every token
 
@@ -463,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int r = mine0 + i / HPG;
                     if (r >= a.n_rows || a.q_req[r] == -1) continue;
                     const size_t h = size_t(r) * a.Hq + g * HPG + i % HPG;
-                    for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.out + h * D + d) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int d = 0; d < D; d += 8)
+                        *reinterpret_cast<uint4 *>(a.out + h * D + d) = make_uint4(0u, 0u, 0u, 0u);
                     a.lse[h] = -INFINITY;
                 }
             }
@@ -477,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ MMA issuer
         // The warp stays together, and one lane's MMAs are predicated: descriptors then are uniform registers.
         const uint32_t el = elect_one();
-        const uint64_t qd0 = make_smem_desc(smem_u32(sm.q[0]), 16, 1024, 2), qd1 = make_smem_desc(smem_u32(sm.q[1]), 16, 1024, 2);
+        const uint64_t qd0 = make_smem_desc(smem_u32(sm.q[0]), 16, 1024, 2);
+        const uint64_t qd1 = make_smem_desc(smem_u32(sm.q[1]), 16, 1024, 2);
         const uint64_t kd0 = make_smem_desc(smem_u32(sm.k[0]), 16, 1024, 2);
         const uint64_t vd0 = make_smem_desc(smem_u32(sm.v[0]), 16384, 1024, 2);
         constexpr uint64_t kNext = Smem<D, PAIR>::TILE >> 4;      // from a descriptor to the other stage's

@@ -51,6 +51,7 @@ APPENDS = [
     (4, 1, 64, 64, 64, 32, True, [2097000], 9, 2, True, True),
     (32, 8, 128, 32, 16, 32, False, [1000003], 3, 0, False, True),
     (32, 4, 128, 64, 112, 48, True, [60, 500], 700, 5, True, True),
+    (16, 2, 128, 64, 64, 32, False, [60, 500], 300, 3, True, True),
     (16, 2, 64, 64, 32, 0, False, [100], 40, 2, True, False),
 ]
 
