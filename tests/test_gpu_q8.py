@@ -862,3 +862,121 @@ def test_results_do_not_depend_on_timing(msa):
     for _ in range(20):
         got = msa.msa_sparse_attn_decode_q8(*args)
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+def test_pages_past_32_bits(msa):
+    """Pages whose codes, and whose bf16 rows, lie past 2^32 bytes: every call as on the same pages in front."""
+    dims = msa.Dims(64, 8, 128, 64, 4, 4)
+    bt, pool = Q.tables([500], 1)
+    small, _ = make_cache(msa, dims, pool, 3)
+    far, n_out = 33000, 17000
+    assert (far - pool) * 8 * 128 * 128 > 1 << 32 and (n_out - pool) * 128 * 8 * 128 * 2 > 1 << 32
+    fields = ("k", "k_scale", "v", "v_scale", "kidx", "kidx_scale")
+
+    def moved(x):
+        big = torch.empty((far, *x.shape[1:]), dtype=torch.uint8, device="cuda")
+        big[far - pool:] = u8(x)
+        return big.view(x.dtype)
+    large = msa.CacheQ8(*(moved(getattr(small, f)) for f in fields))
+    tables = bt.cuda(), torch.where(bt >= 0, bt + (far - pool), bt).cuda()
+    rows = [Q.normal((3, 64 if i == 0 else 8, 64 if i > 2 else 128), 40 + i).cuda() for i in range(5)]
+    req, pos, lens = i32([0] * 3).cuda(), i32([497, 498, 499]).cuda(), i32([500]).cuda()
+    rope = msa.Rope.of_base(64, 32)
+    got = []
+    for cache, table in zip((small, large), tables):
+        res = list(msa.msa_rope_append_q8(*rows, cache, table, req, pos, rope, dims))
+        q, qi = res
+        page = table[0, 3].item()
+        res += [u8(getattr(cache, f)[page].contiguous()) for f in fields]
+        res.append(msa.msa_index_score_q8(qi, cache, table, req, pos, dims))
+        res += msa.msa_decode_step_q8(q[2:].contiguous(), qi[2:].contiguous(), cache, table, lens, dims)[:2]
+        for phase in (0, 1):
+            res += msa.msa_window_attn_q8(q, cache, table, req, pos, 300, 5, dims, phase)
+        base = 0 if cache is small else n_out - pool
+        n = pool if cache is small else n_out
+        out = [torch.empty((n, 128, 8, w), dtype=torch.bfloat16, device="cuda") for w in (128, 128, 64)]
+        to = torch.where(bt >= 0, bt + base, bt).cuda()
+        for x in out:
+            x[base:] = 0
+        msa.msa_cache_read_q8(cache, table, to, lens, dims, *out)
+        msa.msa_rope_append(*rows, *out, to, req, pos - 200, rope, dims)
+        res += [x[base:].clone() for x in out]
+        got.append(res)
+    for i, (x, y) in enumerate(zip(*got)):
+        assert torch.equal(x, y), i
+
+
+def test_calls_of_no_rows(msa):
+    dims = msa.Dims(16, 2, 128, 64, 2, 4)
+    cache = msa.CacheQ8.zeros(dims, 3, "cuda")
+    bt = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    none = torch.zeros((0,), dtype=torch.int32, device="cuda")
+    rows = [torch.zeros((0, h, w), dtype=torch.bfloat16, device="cuda")
+            for h, w in ((16, 128), (2, 128), (2, 128), (2, 64), (2, 64))]
+    msa.msa_rope_append_q8(*rows, cache, bt, none, none, msa.Rope(0), dims)
+    assert msa.msa_index_score_q8(rows[3], cache, bt, none, none, dims).numel() == 0
+    for phase in (0, 1):
+        out, lse = msa.msa_window_attn_q8(rows[0], cache, bt, none, none, 5, 1, dims, phase)
+        assert out.numel() == 0 and lse.numel() == 0
+    out, lse = msa.msa_sparse_attn_decode_q8(rows[0], cache, bt.new_zeros((0, 2)), none, dims)
+    assert out.numel() == 0 and lse.numel() == 0
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("phase", [0, 1])
+@pytest.mark.parametrize("D,G", [(128, 2), (64, 1)])
+def test_window_captured_and_two_at_once(msa, phase, D, G):
+    """Two graphs over the same caches, replayed side by side on what their tensors then hold."""
+    dims = msa.Dims(8 * G, G, D, 64, 1, 8)
+    bt, pool = Q.tables([1000], 1)
+    bt = torch.cat([bt, bt.flip(1)])[:, :8].contiguous()
+    cache, _ = make_cache(msa, dims, pool, 3)
+    sets = []
+    for k in range(2):
+        q = torch.zeros((200, 8 * G, D), dtype=torch.bfloat16, device="cuda")
+        table, req = bt.clone().cuda(), torch.zeros(200, dtype=torch.int32, device="cuda")
+        pos = torch.zeros(200, dtype=torch.int32, device="cuda")
+        args = (q, cache, table, req, pos, 333, 7, dims, phase)
+        out, lse = msa.msa_window_attn_q8(*args)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            msa.msa_window_attn_q8(*args, out, lse)
+        sets.append((graph, args, out, lse, torch.cuda.Stream()))
+    for k, (_, args, _, _, _) in enumerate(sets):
+        args[0].copy_(Q.normal((200, 8 * G, D), 50 + k))
+        args[3].copy_(i32([k] * 190 + [-1] * 10))
+        args[4].copy_(torch.arange(700 + 50 * k, 900 + 50 * k, dtype=torch.int32))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, _, _, _, stream in sets:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, args, out, lse, _ in sets:
+        want = msa.msa_window_attn_q8(*args)
+        assert torch.equal(out[:190], want[0][:190]) and torch.equal(lse[:190], want[1][:190])
+
+
+def test_two_captured_steps_at_once(msa):
+    """Two steps of their own buffers and caches, replayed side by side."""
+    dims = msa.Dims(16, 2, 128, 64, 2, 4)
+    bt, pool = Q.tables([300, 400], 1)
+    steps = []
+    for k in range(2):
+        cache, _ = make_cache(msa, dims, pool, 3 + 10 * k)
+        step = msa.DecodeStepQ8(dims, 2, "cuda", msa.Rope.of_base(64, 32))
+        rows = [Q.normal((2, 16 if i == 0 else 2, 64 if i > 2 else 128), 60 + 10 * k + i).cuda() for i in range(5)]
+        args = (*rows, cache, bt.cuda(), i32([299, 399]).cuda(), i32([300, 400]).cuda())
+        step.capture(*args)
+        steps.append((step, args, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for step, _, stream in steps:
+            with torch.cuda.stream(stream):
+                step.replay()
+    torch.cuda.synchronize()
+    for step, args, _ in steps:
+        got = step.out.clone(), step.lse.clone()
+        want = step.step(*args)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
