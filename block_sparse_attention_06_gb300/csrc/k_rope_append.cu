@@ -9,7 +9,8 @@
 //
 // The angle of a far position loses its digits in fp32 (position 2^20 turns the first pair by 2^20 radians),
 // so it is counted in turns in 64-bit fixed point: inv_freq / 2 pi, modulo one turn, as a fraction of 2^64;
-// times the position, modulo 2^64, is the exact fraction of a turn.
+// times the position, modulo 2^64, is the fraction of a turn with the error of inv_freq / 2 pi in 64-bit floating point
+// alone.  It is rounded to fp32 then, between -1 and 1 half turns.
 //
 // Every byte is moved once, by 16-byte loads and stores.  A warp takes 32 chunks of 8 components of one
 // section (q, k, v, q_idx or k_idx) at a time, in RPC rows at once, so RPC loads of a lane are in flight; a
