@@ -5,8 +5,10 @@
 //
 // What bounds it is the read of K and V (one byte per component, and two scale bytes per token), and with
 // few rows the latency of a chain: table, K, softmax, join.  So:
-//   - a unit is 32 tokens of one page, and each warp streams its units through a ring of its own in shared
-//     memory by asynchronous copies, with its own running sums: no barrier between warps until the row's end;
+//   - a unit is 32 tokens of one page, and each warp streams its units through a buffer of its own in shared memory by
+//     asynchronous copies, with its own running sums: no barrier between warps until the row's end.  The next K is
+//     copied as soon as this one is in the MMAs, the next V as soon as this one is, so one buffer for each is
+//     enough and sixteen warps fit an SM (eight with two buffers each took 50 us where these take 47);
 //   - a row's units are dealt to the warps of a cluster of CTAs (more CTAs where there are few rows).  At the end
 //     every warp writes its partial into the shared memory of the CTAs that own a share of the row's output; one
 //     cluster barrier, and each CTA joins its share, always in the same order: no workspace, no atomics.
@@ -22,9 +24,9 @@
 // (The 8-bit MMA of warps takes codes as they are, but is no faster: it unpacks its operands itself, every time, and
 // needs P and q in pieces.)
 //
-// Measured (Hq = 64, G = 8, D = 128).  8 requests x 16 blocks (33 MB): 13.3 us against 5.0 at the copy rate; the chain is a
+// Measured (Hq = 64, G = 8, D = 128).  8 requests x 16 blocks (33 MB): 12.5 us against 5.0 at the copy rate; the chain is a
 // launch, two table loads, four units per warp at some 2,000 cycles and the join.  32 requests, window of 4,096 (257 MB):
-// 50 us against 38; 256 clusters of one CTA on 152 SMs leave a third of the SMs one row where the others have two.  First
+// 47 us against 38; 256 clusters of one CTA on 152 SMs leave a third of the SMs one row where the others have two.  First
 // kernel, with 8-bit MMAs: 17.5 and 94.
 //
 // Layout.  A unit's K and V are 32 rows of D bytes, swizzled by the copy (128- or 64-byte pattern).  Lane (r, c) =
@@ -41,7 +43,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;            // tokens
 constexpr float kShift = 12.f;       // P is at most 2^12 where its reference was set ...
@@ -131,13 +133,13 @@ constexpr int kMaxCluster = 16;
 
 template <int D, int HPG>
 struct Smem {
-    static constexpr int NST = D == 128 ? 2 : 4;      // stages per warp
-    alignas(1024) uint8_t kv[kWarps][NST][2][kUnit * D];
-    alignas(16) uint8_t scale[kWarps][NST][2][kUnit];
+    alignas(1024) uint8_t kv[kWarps][2][kUnit * D];   // a warp's unit: K, V
+    alignas(16) uint8_t scale[kWarps][2][kUnit];
     // this CTA's share of the partials of all warps of the cluster (its HPG * D / cluster components), and their
     // references and sums
     alignas(16) float part[kWarps * HPG * D];
     float rx[kMaxCluster * kWarps][8], rs[kMaxCluster * kWarps][8], l[kMaxCluster * kWarps][8];
+    float factor[8];
 };
 
 // Byte offset of 16-byte column `ch` of row t of a unit.
@@ -147,10 +149,9 @@ __device__ __forceinline__ uint32_t unit_off(int t, int ch) {
 }
 
 template <int D, int HPG, bool WINDOW>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     k_attn_q8(const __grid_constant__ Args a) {
     using S = Smem<D, HPG>;
-    constexpr int NST = S::NST;
     constexpr int KW = D / 16;       // words of K a lane reads per token
     constexpr int VW = D / 32;       // words of V a lane reads per token
     constexpr int MT = D / 16;       // m16 tiles of O
@@ -194,33 +195,38 @@ __global__ void __launch_bounds__(kThreads)
             u_at = t_in | max(v0, 0) << 8 | min(max(v1, 0), kUnit) << 16;
         }
     };
-    int st_page = -1, st_at = 0;     // lane l: what stage l holds (page -1: nothing)
-    auto issue = [&](int i, int stage) {
-        if ((i & 31) == 0) look_up(i);
-        const int page = __shfl_sync(0xffffffffu, u_page, i & 31), at = __shfl_sync(0xffffffffu, u_at, i & 31);
-        if (lane == stage) {
-            st_page = page;
-            st_at = at;
-        }
-        if (page >= 0) {
-            constexpr int CPR = D / 16;                  // 16-byte columns of a row
-            const size_t line = (size_t(page) * a.G + g) * 128 + (at & 127);
-            const uint8_t *const kp = a.k + line * D + lane * 16, *const vp = a.v + line * D + lane * 16;
-            const uint32_t kd = smem_u32(sm.kv[warp][stage][0]), vd = smem_u32(sm.kv[warp][stage][1]);
+    constexpr int CPR = D / 16;                          // 16-byte columns of a row
+    auto line_of = [&](int page, int at) { return (size_t(page) * a.G + g) * 128 + (at & 127); };
+    auto copy = [&](uint32_t dst, const uint8_t *src) {
 #pragma unroll
-            for (int k = 0; k < CPR; ++k) cp_async_16(kd + unit_off<D>((lane + 32 * k) / CPR, lane % CPR), kp + k * 512);
-#pragma unroll
-            for (int k = 0; k < CPR; ++k) cp_async_16(vd + unit_off<D>((lane + 32 * k) / CPR, lane % CPR), vp + k * 512);
-            if (lane < 16)
-                cp_async_4(smem_u32(sm.scale[warp][stage][lane >> 3]) + (lane & 7) * 4,
-                           (lane < 8 ? a.k_scale : a.v_scale) + line + (lane & 7) * 4);
-        }
+        for (int k = 0; k < CPR; ++k)
+            cp_async_16(dst + unit_off<D>((lane + 32 * k) / CPR, lane % CPR), src + lane * 16 + k * 512);
     };
-#pragma unroll
-    for (int i = 0; i < NST; ++i) {
-        if (i < n) issue(i, i);
+    const uint8_t *const ku = sm.kv[warp][0], *const vu = sm.kv[warp][1];
+    // unit i, its page and place; K and both scales are one group of copies, V the next one
+    auto begin = [&](int i, int *page, int *at) {
+        *page = -1;
+        if (i < n) {
+            if ((i & 31) == 0) look_up(i);
+            *page = __shfl_sync(0xffffffffu, u_page, i & 31);
+            *at = __shfl_sync(0xffffffffu, u_at, i & 31);
+            if (*page >= 0) {
+                const size_t line = line_of(*page, *at);
+                copy(smem_u32(ku), a.k + line * D);
+                if (lane < 16)
+                    cp_async_4(smem_u32(sm.scale[warp][lane >> 3]) + (lane & 7) * 4,
+                               (lane < 8 ? a.k_scale : a.v_scale) + line + (lane & 7) * 4);
+            }
+        }
         cp_async_commit();
-    }
+    };
+    auto begin_v = [&](int page, int at) {
+        if (page >= 0) copy(smem_u32(vu), a.v + line_of(page, at) * D);
+        cp_async_commit();
+    };
+    int page, at = 0;                // of the unit at hand
+    begin(0, &page, &at);
+    begin_v(page, at);
 
     // q of head r (a quarter of the components per lane), and the factor of heads 2c, 2c + 1
     uint32_t q[KW][2];
@@ -263,21 +269,19 @@ __global__ void __launch_bounds__(kThreads)
     // heads 2c, 2c + 1: references of P and of the weights, the weights' sum over this lane's tokens
     float rx[2] = {-INFINITY, -INFINITY}, rs[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    int stage = 0;
     for (int i = 0; i < n; ++i) {
-        cp_async_wait<NST - 1>();
-        __syncwarp();                // every lane's part of the stage is there
-        const int page = __shfl_sync(0xffffffffu, st_page, stage), at = __shfl_sync(0xffffffffu, st_at, stage);
-        if (page >= 0) {
-            const uint8_t *const ku = sm.kv[warp][stage][0], *const vu = sm.kv[warp][stage][1];
+        cp_async_wait<1>();
+        __syncwarp();                // every lane's part of K and the scales is there
+        const bool have = page >= 0;
+        const int v0 = at >> 8 & 255, v1 = at >> 16;     // visible tokens
+        float s[4][2], x[4][2];      // logits in log2 units, and x (see above): token 8k + r, head 2c + h
+        float ve;                    // the exponent of V's scale, -inf where the token is not visible, NaN for a NaN row
+        if (have) {
             // scales: of token `lane` here, of tokens 8k + r by shuffles
-            const int v0 = at >> 8 & 255, v1 = at >> 16;
-            const uint32_t vb = sm.scale[warp][stage][1][lane];
+            const uint32_t vb = sm.scale[warp][1][lane];
             const bool seen = lane >= v0 && lane < v1;
-            const float kf = q8_scale(sm.scale[warp][stage][0][lane]);
-            // the exponent of V's scale, -inf where the token is not visible, NaN for a NaN row
-            const float ve = !seen ? -INFINITY : vb == 255u ? __uint_as_float(0x7fffffffu) : float(int(vb) - 127);
-            float s[4][2], x[4][2];  // logits in log2 units, and x (see above): token 8k + r, head 2c + h
+            const float kf = q8_scale(sm.scale[warp][0][lane]);
+            ve = !seen ? -INFINITY : vb == 255u ? __uint_as_float(0x7fffffffu) : float(int(vb) - 127);
             const float base[2] = {rs[0] == -INFINITY ? 0.f : rs[0], rs[1] == -INFINITY ? 0.f : rs[1]};
             float y[2][2][4];        // four chains of MMAs: their latency counts
 #pragma unroll
@@ -320,6 +324,11 @@ __global__ void __launch_bounds__(kThreads)
                         x[2 * mt + k][h] = (v - base[h]) + e;
                     }
                 }
+        }
+        __syncwarp();                // K and the scales have been read
+        int next = -1, next_at = 0;
+        begin(i + 1, &next, &next_at);
+        if (have) {
             bool raise = false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -368,6 +377,8 @@ __global__ void __launch_bounds__(kThreads)
                     pt[k] = transpose8(pack_f16x2(fast_exp2(x[k][0] - bx0), fast_exp2(x[k][1] - bx1)));
                 }
             }
+            cp_async_wait<1>();      // all but the next unit's K
+            __syncwarp();
             uint32_t vw[8][VW];      // tokens 8 (k / 2) + 2c + k % 2
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -414,10 +425,10 @@ __global__ void __launch_bounds__(kThreads)
                                 av[2 * kk + 1][2 * k + 1], pt[2 * kk], pt[2 * kk + 1]);
             }
         }
-        __syncwarp();                // the stage has been read
-        if (i + NST < n) issue(i + NST, stage);
-        cp_async_commit();
-        stage = stage + 1 == NST ? 0 : stage + 1;
+        __syncwarp();                // V has been read
+        begin_v(next, next_at);
+        page = next;
+        at = next_at;
     }
     cp_async_wait<0>();
 
@@ -454,36 +465,56 @@ __global__ void __launch_bounds__(kThreads)
     const size_t head0 = size_t(b) * a.G * HPG + size_t(g) * HPG;
     const int n_part = a.cluster * kWarps;
     auto weight = [](float ref, float top) { return top == -INFINITY ? 0.f : fast_exp2(ref - top); };
+    // a head's largest references, and the partials' weights in place of theirs: a warp per head
+    if (warp < HPG) {
+        float ts = -INFINITY, tx = -INFINITY;            // the largest rs: what every partial is brought to
+        for (int k = lane; k < n_part; k += 32) ts = fmaxf(ts, sm.rs[k][warp]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) ts = fmaxf(ts, __shfl_xor_sync(0xffffffffu, ts, o));
+        auto rx_of = [&](int k) {
+            return sm.rs[k][warp] == -INFINITY ? -INFINITY : sm.rx[k][warp] + (sm.rs[k][warp] - ts);
+        };
+        for (int k = lane; k < n_part; k += 32) tx = fmaxf(tx, rx_of(k));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, o));
+        float sum = 0.f;
+        for (int k = lane; k < n_part; k += 32) {
+            sum += weight(sm.rs[k][warp], ts) * sm.l[k][warp];
+            sm.rx[k][warp] = weight(rx_of(k), tx);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) {
+            sm.factor[warp] = sum == 0.f ? 0.f : weight(tx - kShift, 0.f) / sum;
+            if (rank == warp * D / share) a.lse[head0 + warp] = sum == 0.f ? -INFINITY : (ts + log2f(sum)) * kLn2;
+        }
+    }
+    __syncthreads();
     for (int i = tid * 2; i < share; i += kThreads * 2) {
         const int e = rank * share + i, h = e / D, d = e - h * D;
-        float ts = -INFINITY;            // the largest rs: what every partial is brought to
-        for (int k = 0; k < n_part; ++k) ts = fmaxf(ts, sm.rs[k][h]);
-        auto rx_of = [&](int k) { return sm.rs[k][h] == -INFINITY ? -INFINITY : sm.rx[k][h] + (sm.rs[k][h] - ts); };
-        float tx = -INFINITY;
-        for (int k = 0; k < n_part; ++k) tx = fmaxf(tx, rx_of(k));
-        float sum = 0.f, x = 0.f, y = 0.f;
+        float x = 0.f, y = 0.f;
         for (int k = 0; k < n_part; ++k) {
-            const float wx = weight(rx_of(k), tx);
+            const float wx = sm.rx[k][h];
             const float2 v = *reinterpret_cast<const float2 *>(&sm.part[k * share + i]);
-            sum += weight(sm.rs[k][h], ts) * sm.l[k][h];
             x += wx * v.x;
             y += wx * v.y;
         }
-        const float f = sum == 0.f ? 0.f : weight(tx - kShift, 0.f) / sum;
+        const float f = sm.factor[h];
         *reinterpret_cast<uint32_t *>(a.out + (head0 + h) * D + d) = pack_bf16x2(x * f, y * f);
-        if (d == 0) a.lse[head0 + h] = sum == 0.f ? -INFINITY : (ts + log2f(sum)) * kLn2;
     }
 }
 
 template <int D, int HPG, bool WINDOW>
 cudaError_t launch_t(Args a, long long rows, int units, cudaStream_t st, bool pdl) {
-    // As many CTAs as fit the SMs at two each, as long as every warp of the cluster has two units.  Clusters of 1, 2, 4, 8
-    // and 16 CTAs, in us (*: what this takes): 64 rows of 16 blocks 21.7, 14.5, *13.4, 23.3, 56; 256 rows of a window of
-    // 4,096 *50, 56, 64, 92, 231; 8 rows of a window of 1,024 14.5, 10.2, *8.0, 7.7, 10.7; 24 rows of 11 blocks, D = 64,
-    // 11.9, 8.4, *6.9, 7.5, 16.9.  (Clusters of 16 wait for 16 SMs of one GPC.)
-    const long long want = 2LL * sm_count();
+    // A CTA per SM, as long as every warp of the cluster has a unit; clusters of 8 and 16 for few rows alone, since they
+    // wait for SMs of one GPC, and 16 where every warp has two units.  Clusters of 1, 2, 4, 8 and 16 CTAs, in us (*: what
+    // this takes).  16 blocks, 64 rows: 16.8, *12.5, 14.5, 26.5, 68; 11 blocks, D = 64, 24 rows: 9.6, 7.5, *7.0, 8.4, 19.4;
+    // window of 4,096, 256 rows: *47, 54, 62, 107, 278; 16 rows: 2, 4, 8, 16: 17.5, *12.8, 14.5, 26; 8 rows: 17.0, 12.3,
+    // *10.7, 15.5; 2 rows: 17.0, 12.3, *10.7, 11.8; window of 1,024, 8 rows: 9.4, *8.6, 8.8, 14.6; dense, 60,000 tokens, 8
+    // rows: 158, 84, *47, 46; 2 rows: 158, 83, 47, *30.
+    const long long sms = sm_count();
     int cs = 1;
-    while (cs < kMaxCluster && rows * cs * 2 <= want && cs * 4 * kWarps <= units) cs *= 2;
+    while (cs < kMaxCluster && rows * cs * 2 <= (cs < 4 ? sms : sms / 2) && cs * (cs < 8 ? 2 : 4) * kWarps <= units) cs *= 2;
     a.cluster = cs;
     if (rows * cs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     auto k = k_attn_q8<D, HPG, WINDOW>;

@@ -543,6 +543,8 @@ WINDOWS = [
     (8, 2, 64, [250], 1, 200, 300, 0),
     (16, 2, 128, [96], 70, 32, 31, 5),
     (4, 1, 64, [0, 3], 40, 7, 2, 1),
+    (8, 1, 64, [9000], 2, 1 << 30, 0, 0),
+    (8, 1, 128, [8300, 20], 1, 8200, 50, 0),
 ]
 
 
