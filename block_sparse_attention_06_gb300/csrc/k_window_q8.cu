@@ -71,7 +71,7 @@ struct Smem {
     uint64_t desc_full[kRing], desc_empty[kRing];
     uint64_t q_tma[2], q_full[2], q_empty[2];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2];   // per tile
+    uint64_t s_full[2][2], p_full[2], o_full[2];   // per tile; S by halves of a page
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int EPT = 128 / HPG;       // rows per tile
     constexpr int NSUB = D / 64;         // 64-column sub-tiles
     constexpr int CT = PAIR ? 2 : 1;     // CTAs that work on an item
-    constexpr uint32_t kIdescS = make_idesc_bf16(CT * 128, 128, 0, 0);
+    constexpr uint32_t kIdescS = make_idesc_bf16(CT * 128, 64, 0, 0);
     constexpr uint32_t kIdescO = make_idesc_bf16(CT * 128, D, 0, 1);
     using S = Smem<D, PAIR>;
     extern __shared__ uint8_t smem_raw[];
@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.k_empty[i], 1);
             mbar_init(&sm.v_full[i], 8 * CT);
             mbar_init(&sm.v_empty[i], 1);
-            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_full[i][0], 1);
+            mbar_init(&sm.s_full[i][1], 1);
             mbar_init(&sm.p_full[i], 4 * CT);
             mbar_init(&sm.o_full[i], 1);
         }
@@ -496,19 +497,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait = [&](uint64_t *bar, int parity) {
             return bool(__all_sync(0xffffffffu, mbar_wait(bar, uint32_t(parity), err, &sm.abort)));
         };
+        constexpr uint64_t kHalf = (PAIR ? 4096 : 8192) >> 4;     // from K's first 64 tokens to the others
         // P V of tile x at step s; `first`: overwrite O
-        auto issue_pv = [&](int x, int s, bool first, bool last) -> bool {
-            if (!wait(&sm.p_full[x], s & 1)) return false;
+        auto issue_pv = [&](int x, int s, bool first) -> bool {
             if (x == 0 && !wait(&sm.v_full[s & 1], (s >> 1) & 1)) return false;
             tc_fence_after();
-            mma_pv<PAIR>(tmem + 256u + uint32_t(x * D), tmem + uint32_t(x * 128), vd0 + uint64_t(s & 1) * kNext, kIdescO,
-                         first ? 0u : 1u, el);
-            if (last) commit<PAIR>(&sm.o_full[x], el);
-            if (x == 1) commit<PAIR>(&sm.v_empty[s & 1], el);
+            mma_pv<PAIR>(tmem + 256u + uint32_t(x * D), tmem + uint32_t(x * 128 + (s & 1) * 64),
+                         vd0 + uint64_t(s & 1) * kNext, kIdescO, first ? 0u : 1u, el);
             return true;
         };
         int items = 0;               // whose Q has been waited for
-        bool b_pending = false, b_first = false;
+        bool before = false;         // the step before was its item's first
         for (int s = 0;; ++s) {
             const int slot = s % kRing;
             if (!wait(&sm.desc_full[slot], (s / kRing) & 1)) break;
@@ -519,29 +518,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (end) break;
             if (rank != 0) continue;     // the first CTA issues for both
             if (!wait(&sm.k_full[s & 1], (s >> 1) & 1)) break;
-            if (first && !wait(&sm.q_full[0], items & 1)) break;
-            tc_fence_after();
             const uint64_t kd = kd0 + uint64_t(s & 1) * kNext;
-            mma_s<D, PAIR>(tmem, qd0, kd, kIdescS, el);
-            commit<PAIR>(&sm.s_full[0], el);
-            if (last) commit<PAIR>(&sm.q_empty[0], el);
-            if (b_pending) {
-                b_pending = false;
-                if (!issue_pv(1, s - 1, b_first, false)) break;
+            bool ok = true;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                // P of the step before is there, so all of its S has been read: the half that P is not in is free
+                ok = first ? wait(&sm.q_full[x], items & 1) : wait(&sm.p_full[x], (s - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                mma_s<D, PAIR>(tmem + uint32_t(x * 128 + (s & 1) * 64), x ? qd1 : qd0, kd, kIdescS, el);
+                commit<PAIR>(&sm.s_full[x][0], el);
+                if (!first) {
+                    ok = issue_pv(x, s - 1, before);
+                    if (!ok) break;
+                    if (x == 1) commit<PAIR>(&sm.v_empty[(s - 1) & 1], el);
+                }
+                mma_s<D, PAIR>(tmem + uint32_t(x * 128 + 64 - (s & 1) * 64), x ? qd1 : qd0, kd + kHalf, kIdescS, el);
+                commit<PAIR>(&sm.s_full[x][1], el);
+                if (x == 1) commit<PAIR>(&sm.k_empty[s & 1], el);
+                if (last) commit<PAIR>(&sm.q_empty[x], el);
             }
-            if (first && !wait(&sm.q_full[1], items & 1)) break;
-            if (first) ++items;
-            tc_fence_after();
-            mma_s<D, PAIR>(tmem + 128u, qd1, kd, kIdescS, el);
-            commit<PAIR>(&sm.s_full[1], el);
-            commit<PAIR>(&sm.k_empty[s & 1], el);
-            if (last) commit<PAIR>(&sm.q_empty[1], el);
-            if (!issue_pv(0, s, first, last)) break;
-            b_pending = true;
-            b_first = first;
+            if (!ok) break;
+            items += first;
+            before = first;
             if (last) {              // the item's results wait for it, and the next item's Q is still on its way
-                b_pending = false;
-                if (!issue_pv(1, s, first, last)) break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    ok = wait(&sm.p_full[x], s & 1) && issue_pv(x, s, first);
+                    if (!ok) break;
+                    commit<PAIR>(&sm.o_full[x], el);
+                    if (x == 1) commit<PAIR>(&sm.v_empty[s & 1], el);
+                }
+                if (!ok) break;
             }
         }
         if (rank == 0) {
@@ -602,29 +610,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int KL = D / 16, KT = KL / 2 / CT;         // K: lanes per token, tokens per thread
         constexpr int VL = D / 16 / CT, VT = D / 32 / CT;    // V
         using Lane = struct {
-            int col, tok0;                                   // 16 codes of tokens tok0 ..
+            int col, tok0, row;                              // 16 codes of the tile's tokens tok0 .., the page's row ..
             uint32_t at;                                     // their sub-tile of 64 columns
             int ch;                                          // their first 16-byte chunk in it
             size_t off;                                      // bytes from the page's first row
         };
-        auto lane_of = [&](int lanes, int toks, int row_first, int col_first, uint32_t sub_bytes) {
+        auto lane_of = [&](int lanes, int toks, bool split, int col_first, uint32_t sub_bytes) {
             Lane x;
             x.col = lane % lanes;
             x.tok0 = (w * (32 / lanes) + lane / lanes) * toks;
             x.at = uint32_t(x.col >> 2) * sub_bytes;
             x.ch = (x.col & 3) * 2;
-            x.off = size_t(row_first + x.tok0) * D + col_first + x.col * 16;
+            x.row = split ? (x.tok0 & 31) + rank * 32 + (x.tok0 >> 5) * 64 : x.tok0;   // half of either half page
+            x.off = size_t(x.row) * D + col_first + x.col * 16;
             return x;
         };
-        const Lane kl = lane_of(KL, KT, PAIR ? rank * 64 : 0, 0, PAIR ? 8192u : 16384u);
-        const Lane vl = lane_of(VL, VT, 0, PAIR ? rank * 64 : 0, 16384u);
+        const Lane kl = lane_of(KL, KT, PAIR, 0, PAIR ? 8192u : 16384u);
+        const Lane vl = lane_of(VL, VT, false, PAIR ? rank * 64 : 0, 16384u);
         // codes c[i] of token tok0 + (i ^ swap); returns the scale bytes in that order
-        auto load = [&](const uint8_t *codes, const uint8_t *scales, size_t page_line, const Lane &x, int row_first, auto &c) {
+        auto load = [&](const uint8_t *codes, const uint8_t *scales, size_t page_line, const Lane &x, auto &c) {
             constexpr int T = sizeof(c) / sizeof(uint4);
             const uint8_t *p = codes + page_line * D + x.off;
 #pragma unroll
             for (int i = 0; i < T; ++i) c[i] = __ldg(reinterpret_cast<const uint4 *>(p + (i ^ swap) * D));
-            const uint8_t *sp = scales + page_line + row_first + x.tok0;
+            const uint8_t *sp = scales + page_line + x.row;
             uint32_t sc;
             if constexpr (T == 4) sc = __ldg(reinterpret_cast<const uint32_t *>(sp));
             else sc = __ldg(reinterpret_cast<const uint16_t *>(sp));
@@ -674,8 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         uint4 kc[KT], vc[VT];
         uint32_t ks = 0u, vs = 0u;
-        auto load_k = [&]() { ks = load(a.k, a.k_scale, (size_t(page) * a.G + g) * 128, kl, PAIR ? rank * 64 : 0, kc); };
-        auto load_v = [&]() { vs = load(a.v, a.v_scale, (size_t(page) * a.G + g) * 128, vl, 0, vc); };
+        auto load_k = [&]() { ks = load(a.k, a.k_scale, (size_t(page) * a.G + g) * 128, kl, kc); };
+        auto load_v = [&]() { vs = load(a.v, a.v_scale, (size_t(page) * a.G + g) * 128, vl, vc); };
         bool more = desc();              // there is a step that is not written yet
         if (more) {
             load_k();
@@ -742,14 +751,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) poison |= (nan_v[k] & see[k]) != 0u;
-            ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], s & 1, err, &sm.abort));
-            tc_fence_after();
+            // S of the page's halves comes into the halves of the tile's columns, the first one into that which P of the
+            // step before does not take; P goes over the first one.
+            const uint32_t t_p = t_s + uint32_t((s & 1) * 64);
+            auto wait_s = [&](int hb) {
+                ok &= bool(__all_sync(0xffffffffu, mbar_wait(&sm.s_full[x][hb], s & 1, err, &sm.abort)));
+                tc_fence_after();
+            };
             // One pass over each half of the row: weights by the reference so far, and the maximum beside them.  Where a
             // logit passes the reference too far (S of the half is still there), the reference is raised and the half
             // weighed again.  The code between two votes has no branches: with one per 32 columns a step took 1.4 times
             // as long.
             auto weigh = [&](int hb, uint32_t bits0, uint32_t bits1, auto masked) {
-                const uint32_t t = t_s + uint32_t(64 * hb);
+                const uint32_t t = t_s + uint32_t(((s & 1) ^ hb) * 64);
+                wait_s(hb);
                 for (;;) {
                     const uint64_t nref2 = dup2(ref == -INFINITY ? 0.f : -ref);
                     uint64_t acc2[4] = {0, 0, 0, 0};
@@ -783,8 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float m = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
                     const bool raise = (m - ref) * scale > kRaise;   // false for rows that see nothing
                     if (!__any_sync(0xffffffffu, raise)) {
-                        tmem_st16(t_s + uint32_t(32 * hb), w[0]);
-                        tmem_st16(t_s + uint32_t(32 * hb + 16), w[1]);
+                        tmem_st16(t_p + uint32_t(32 * hb), w[0]);
+                        tmem_st16(t_p + uint32_t(32 * hb + 16), w[1]);
                         l += (sum2(acc2[0]) + sum2(acc2[1])) + (sum2(acc2[2]) + sum2(acc2[3]));
                         return;
                     }
@@ -799,13 +814,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int i = 0; i < 32 * hb; i += 16) {
                         uint32_t o[16];
-                        tmem_ld16(t_s + uint32_t(i), o);
+                        tmem_ld16(t_p + uint32_t(i), o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) o[j] = mul_bf16x2(o[j], al2);
-                        tmem_st16(t_s + uint32_t(i), o);
+                        tmem_st16(t_p + uint32_t(i), o);
                     }
-                    if (!(flags & kFirst)) {   // S of this step came behind the P V before it: O is complete up to there
+                    if (!(flags & kFirst)) {   // S of the second half comes behind the P V before it: O is complete then
+                        wait_s(1);
 #pragma unroll 1
                         for (int i = 0; i < D; i += 16) {
                             uint32_t o[16];
