@@ -19,16 +19,19 @@
 // half as wide as the operand's swizzle.)
 //
 // What bounds it: the chain S, softmax, P V of a tile.  TMEM holds two S and two O (512 columns with heads of 128), so
-// two tiles take turns, and a step of both takes about 4,200 cycles, of which the tensor cores work 2,048; issue
-// slots are busy half the time, memory next to never.  Measured: 8,192 rows at 60,000, window of 4,096, 4 sinks: 1.05 ms,
-// 0.55 of the measured bf16 rate counting the visible tokens.  What brought it there from 1.53 ms: arrivals without
-// a release over the cluster (1.61 -> 1.41), a softmax of one pass (1.41 -> 1.17; the maximum first, or a vote for every
-// 32 columns, breaks the code into short pieces), MMAs from a warp that stays together (1.17 -> 1.04).  One thread per
-// row and eight warps need half the instructions of two threads per row and sixteen.
+// two tiles take turns.  S of a page comes in halves of 64 tokens: P takes half of S's columns, so the first half of the
+// next S goes into the other half as soon as P is there, before P V, and its softmax runs under P V.  A step of
+// both tiles takes about 4,000 cycles, of which the tensor cores work 2,048; issue slots are busy 0.58 of the time, memory
+// next to never.  Measured: 8,192 rows at 60,000, window of 4,096, 4 first tokens: 1.00 ms, 0.58 of the measured bf16 rate
+// counting the visible tokens.  What brought it there from 1.53 ms: arrivals without a release over the cluster (1.61
+// -> 1.41), a softmax of one pass (1.41 -> 1.17; the maximum first, or a vote for every 32 columns, breaks the code into
+// short pieces), MMAs from a warp that stays together (1.17 -> 1.04), S by halves (1.05 -> 1.00).  One thread per row and
+// eight warps need half the instructions of two threads per row and sixteen.
 //
 // One CTA per SM, 20 warps, persistent over items:
 //   warp 0     planner: for each item the pages that any of its rows sees, in a ring of step descriptors;
-//   warp 1     MMA issuer and TMEM owner: S_A(s), P V of B(s-1), S_B(s), P V of A(s), ... (a pair's first CTA for both);
+//   warp 1     MMA issuer and TMEM owner: per tile, once P of step s-1 is there, the first half of S(s), P V of s-1, the
+//              second half of S(s) (a pair's first CTA for both);
 //   warp 2     Q loader (TMA, one box per tile and 64 columns);   warp 3  idle;
 //   warps 4-7, 8-11   softmax of tiles A and B, one row per thread; each also writes its tile's results;
 //   warps 12-19  converters: the next page's codes wait in registers while this one's are written.
