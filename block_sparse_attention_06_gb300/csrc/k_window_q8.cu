@@ -645,28 +645,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto store = [&](uint8_t *tile, const Lane &x, const auto &c, uint32_t sc, bool values) {
             constexpr int T = sizeof(c) / sizeof(uint4);
             const uint32_t base = smem_u32(tile) + x.at;
-            const bool usual = (sc & 0x80808080u) == 0u;     // no scale above 1, no NaN row
-#pragma unroll
-            for (int i = 0; i < T; ++i) {
-                const int t = x.tok0 + (i ^ swap);
-                const uint32_t b = (sc >> (8 * i)) & 255u;
-                uint32_t o[8];
-                if (usual) {             // 2^(120 + e), e = b - 127
-                    convert16(c[i], (b + 120u) * 0x00800080u, o);
-                } else {
-                    // 2^120 and then 2^e where e > 0; a NaN row: of K NaN, so the logits of the rows that see it are; of
-                    // V zeros (see above)
-                    const uint32_t f = b == 255u ? (values ? 0u : 0x7fff7fffu) : (min(b, 127u) + 120u) * 0x00800080u;
-                    const uint32_t up = b == 255u ? 0x3f803f80u : max(b, 127u) * 0x00800080u;
-                    convert16(c[i], f, o);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], up);
-                }
+            auto put = [&](int t, const uint32_t (&o)[8]) {
                 const uint32_t p0 = base + uint32_t(t * 128) + uint32_t((x.ch ^ (t & 7)) << 4);
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0), "r"(o[0]), "r"(o[1]), "r"(o[2]),
                              "r"(o[3]) : "memory");
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0 ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]),
                              "r"(o[7]) : "memory");
+            };
+            if (__all_sync(0xffffffffu, (sc & 0x80808080u) == 0u)) {   // no scale above 1, no NaN row: 2^(120 + e)
+#pragma unroll
+                for (int i = 0; i < T; ++i) {
+                    uint32_t o[8];
+                    convert16(c[i], ((sc >> (8 * i) & 255u) + 120u) * 0x00800080u, o);
+                    put(x.tok0 + (i ^ swap), o);
+                }
+            } else {                     // rolled: short, beside the code that always runs
+#pragma unroll 1
+                for (int i = 0; i < T; ++i) {
+                    // 2^120 and then 2^e where e > 0; a NaN row: of K NaN, so the logits of the rows that see it are; of
+                    // V zeros (see above)
+                    const uint32_t b = (sc >> (8 * i)) & 255u;
+                    const uint32_t f = b == 255u ? (values ? 0u : 0x7fff7fffu) : (min(b, 127u) + 120u) * 0x00800080u;
+                    const uint32_t up = b == 255u ? 0x3f803f80u : max(b, 127u) * 0x00800080u;
+                    uint4 w = c[0];
+#pragma unroll
+                    for (int k = 1; k < T; ++k)
+                        if (i == k) w = c[k];
+                    uint32_t o[8];
+                    convert16(w, f, o);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], up);
+                    put(x.tok0 + (i ^ swap), o);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
