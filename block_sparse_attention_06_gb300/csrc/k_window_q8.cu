@@ -25,9 +25,8 @@
 // next to never.  Measured: 8,192 rows at 60,000, window of 4,096, 4 first tokens: 0.98 ms, 0.59 of the measured bf16 rate
 // counting the visible tokens.  What brought it there from 1.53 ms: arrivals without a release over the cluster (1.61
 // -> 1.41), a softmax of one pass (1.41 -> 1.17; the maximum first, or a vote for every 32 columns, breaks the code into
-// short pieces), MMAs from a warp that stays together (1.17 -> 1.04), S by halves (1.05 -> 1.00), no branch per converted token
-// (1.00 -> 0.98).  One thread per row and
-// eight warps need half the instructions of two threads per row and sixteen.
+// short pieces), MMAs from a warp that stays together (1.17 -> 1.04), S by halves (1.05 -> 1.00), no branch per converted
+// token (1.00 -> 0.98).  One thread per row and eight warps need half the instructions of two threads per row and sixteen.
 //
 // One CTA per SM, 20 warps, persistent over items:
 //   warp 0     planner: for each item the pages that any of its rows sees, in a ring of step descriptors;
