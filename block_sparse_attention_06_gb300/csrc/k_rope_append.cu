@@ -10,17 +10,19 @@
 // The angle of a far position loses its digits in fp32 (position 2^20 turns the first pair by 2^20 radians),
 // so it is counted in turns in 64-bit fixed point: inv_freq / 2 pi, modulo one turn, as a fraction of 2^64;
 // times the position, modulo 2^64, is the fraction of a turn with the error of inv_freq / 2 pi in 64-bit floating point
-// alone.  It is rounded to fp32 then, between -1 and 1 half turns.
+// alone.  Cosine and sine are worked out from it to 2^-29 and rounded once: codes are rounded from what they turn, and an
+// error more would move what lies next to a border.
 //
 // Every byte is moved once, by 16-byte loads and stores.  A warp takes 32 chunks of 8 components of one
 // section (q, k, v, q_idx or k_idx) at a time, in RPC rows at once, so RPC loads of a lane are in flight; a
 // vector's lanes are neighbours, so half-split partners and the largest magnitude come by shuffles.
 //
-// Measured (Hq = 64, G = 8, D = 128, Di = 64).  8,192 rows into bf16 caches: 64 us, 5.8 TB/s, 0.85 of the copy rate;
-// into 8-bit caches: 72 us, 4.8 TB/s, 0.71: some 150 instructions per 512 bytes keep 0.64 of the issue slots
+// Measured (Hq = 64, G = 8, D = 128, Di = 64).  8,192 rows into bf16 caches: 66 us, 5.6 TB/s, 0.82 of the copy rate;
+// into 8-bit caches: 77 us, 4.5 TB/s, 0.67: some 150 instructions per 512 bytes keep 0.62 of the issue slots
 // busy, and a warp's loads wait for its arithmetic.  8 rows: 2.9 us, the latency of one launch and one
-// load after the table's.  Two or eight rows per CTA, loads ahead of the task at hand, and CTAs that go on over
-// batches of rows were slower or no faster.
+// load after the table's.  (With sincospif of the angle in fp32 65 and 75 us; its last bits move codes that lie next to a
+// border.)  Two or eight rows per CTA, loads ahead of the task at hand, and CTAs that go on over batches of rows were
+// slower or no faster.
 #include "msa_internal.h"
 #include "msa_q8.cuh"
 
@@ -49,6 +51,31 @@ __device__ __forceinline__ void turn2(float &y0, float &y1, float p0, float p1, 
         "mov.b64 s, {%6, %7};\n\tmul.rn.f32x2 y, y, c;\n\tfma.rn.f32x2 y, p, s, y;\n\tmov.b64 {%0, %1}, y;\n\t}"
         : "+f"(y0), "+f"(y1)
         : "f"(p0), "f"(p1), "f"(c0), "f"(c1), "f"(s0), "f"(s1));
+}
+
+// gain * (cos, sin) of turn / 2^64 turns, rounded once but for 2^-29: the nearest quarter turn is taken off, and the Taylor
+// series of the angle that is left (at most pi/4) run with the errors of their leading terms carried along.
+__device__ __forceinline__ float2 cos_sin(unsigned long long turn, float gain) {
+    const uint32_t quarters = uint32_t((turn + (1ull << 61)) >> 62);
+    const long long left = (long long)(turn - ((unsigned long long)quarters << 62));   // 2^-63 half turns
+    const float r = __ll2float_rn(left), r_lo = __ll2float_rn(left - (long long)r);
+    constexpr float kPi = 3.14159274f, kPiLo = -8.74227766e-8f, kSixth = -0.166666672f, kSixthLo = 4.96705377e-9f;
+    const float x = r * 0x1p-63f, t = x * kPi, te = fmaf(x, kPi, -t) + fmaf(x, kPiLo, r_lo * 0x1p-63f * kPi);   // angle
+    const float z = t * t, ze = fmaf(t, t, -z) + 2.f * t * te;                                                  // squared
+    // 1 - z/2 + z^2 (1/4! - z/6! + z^2/8! - z^3/10!)
+    const float q = fmaf(z, fmaf(z, fmaf(z, -2.75573192e-7f, 2.48015873e-5f), -1.38888889e-3f), 4.16666667e-2f);
+    const float ch = fmaf(-0.5f, z, 1.f), ct = fmaf(z * z, q, fmaf(-0.5f, z, 1.f - ch) - 0.5f * ze);
+    const float c = ch + ct, c_lo = (ch - c) + ct;
+    // t - t z/3! + t z^2 (1/5! - z/7! + z^2/9! - z^3/11!)
+    const float v = t * z, ve = fmaf(t, z, -v) + fmaf(te, z, t * ze);
+    const float p = v * kSixth, pe = fmaf(v, kSixth, -p) + fmaf(v, kSixthLo, ve * kSixth);
+    const float w = fmaf(z, fmaf(z, fmaf(z, -2.50521084e-8f, 2.75573192e-6f), -1.98412698e-4f), 8.33333333e-3f);
+    const float sh = t + p, st = fmaf(v * z, w, ((t - sh) + p) + (te + pe));
+    const float s = sh + st, s_lo = (sh - s) + st;
+    const bool odd = quarters & 1u;
+    const float g = quarters & 2u ? -gain : gain;
+    const float c1 = odd ? -s : c, c1_lo = odd ? -s_lo : c_lo, s1 = odd ? c : s, s1_lo = odd ? c_lo : s_lo;
+    return make_float2(fmaf(c1, g, c1_lo * g), fmaf(s1, g, s1_lo * g));
 }
 
 template <bool Q8, int RPC>
@@ -117,19 +144,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_rope_append(const __grid_consta
         double f = (i < half ? a.inv_freq[i] : a.inv_freq_idx[i - half]) * 0.15915494309189534561;   // turns
         f -= floor(f);
         const unsigned long long turn = __double2ull_rz(f * 18446744073709551616.0);
+        // Half-split pairs come eight to a chunk: the first four of all chunks, then the second four, so that the lanes of
+        // a vector read neighbouring 16 bytes.
+        const bool idx = i >= half;
+        const int j = idx ? i - half : i, quarter = (idx ? a.rot_idx : a.rot) >> 2;
+        const int at = (idx ? 64 : 0) + (a.interleaved ? j : (j >> 2 & 1) * quarter + (j >> 3) * 4 + (j & 3));
 #pragma unroll
         for (int k = 0; k < RPC; ++k) {
             const int r = row0 + k;
             const unsigned long long pos = r < a.n_rows ? (unsigned long long)(long long)a.q_pos[r] : 0ull;
-            float s, c;
-            sincospif(__ll2float_rn((long long)(turn * pos)) * 0x1p-63f, &s, &c);   // half turns in [-1, 1]
-            // Half-split pairs come eight to a chunk: the first four of all chunks, then the second four, so that the
-            // lanes of a vector read neighbouring 16 bytes.
-            const bool idx = i >= half;
-            const int j = idx ? i - half : i, quarter = (idx ? a.rot_idx : a.rot) >> 2;
-            const int at = (idx ? 64 : 0) + (a.interleaved ? j : (j >> 2 & 1) * quarter + (j >> 3) * 4 + (j & 3));
-            cos_s[k][at] = c * a.gain;
-            sin_s[k][at] = s * a.gain;
+            const float2 y = cos_sin(turn * pos, a.gain);
+            cos_s[k][at] = y.x;
+            sin_s[k][at] = y.y;
         }
     }
     __syncthreads();
