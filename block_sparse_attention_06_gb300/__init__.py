@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from dataclasses import dataclass, field
+from dataclasses import dataclass
 from typing import Optional, Tuple
 
 import torch
@@ -735,7 +735,6 @@ class CacheQ8:
     v_scale: Optional[torch.Tensor]
     kidx: Optional[torch.Tensor] = None
     kidx_scale: Optional[torch.Tensor] = None
-    _checked: dict = field(default_factory=dict, init=False, repr=False, compare=False)
 
     @classmethod
     def zeros(cls, dims: Dims, n_pages: int, device, index: bool = True) -> "CacheQ8":
@@ -748,30 +747,19 @@ class CacheQ8:
         return cls(*one(dims.D), *one(dims.D), *(one(dims.Di) if index else (None, None)))
 
     def _struct(self, dims: Dims, dev: int, kv: bool, index: bool):
-        """(reference to the C struct, n_pages), with what the call needs checked: types, shapes and devices once for
-        each kind of call (the fields are frozen), addresses every time."""
-        key = (dims.page_size, dims.G, dims.D, dims.Di, dev, kv, index)
-        n_pages = self._checked.get(key)
-        if n_pages is None:
-            n_pages = self._checked[key] = self._check(dims, dev, kv, index)
-        p = (self.k.data_ptr(), self.k_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr()) if kv else _NO_KV
-        if index:
-            p += (self.kidx.data_ptr(), self.kidx_scale.data_ptr())
-        return ctypes.byref(msa_cache_q8_t(*p)), n_pages
-
-    def _check(self, dims: Dims, dev: int, kv: bool, index: bool) -> int:
+        """(reference to the C struct, n_pages), with what the call needs checked: in every call, since a tensor of a
+        cache may get another storage, shape or type between two of them."""
         first = self.k if kv else self.kidx
         n_pages = _ndim(first, 4, "cache.k" if kv else "cache.kidx", "[n_pages][G][128][width]")[0]
         line = (n_pages, dims.G, dims.page_size)
+        p = _NO_KV
         if kv:
-            _arg(self.k, _E4M3, (*line, dims.D), dev, "cache.k")
-            _arg(self.k_scale, _E8M0, line, dev, "cache.k_scale")
-            _arg(self.v, _E4M3, (*line, dims.D), dev, "cache.v")
-            _arg(self.v_scale, _E8M0, line, dev, "cache.v_scale")
+            p = (_arg(self.k, _E4M3, (*line, dims.D), dev, "cache.k"), _arg(self.k_scale, _E8M0, line, dev, "cache.k_scale"),
+                 _arg(self.v, _E4M3, (*line, dims.D), dev, "cache.v"), _arg(self.v_scale, _E8M0, line, dev, "cache.v_scale"))
         if index:
-            _arg(self.kidx, _E4M3, (*line, dims.Di), dev, "cache.kidx")
-            _arg(self.kidx_scale, _E8M0, line, dev, "cache.kidx_scale")
-        return n_pages
+            p += (_arg(self.kidx, _E4M3, (*line, dims.Di), dev, "cache.kidx"),
+                  _arg(self.kidx_scale, _E8M0, line, dev, "cache.kidx_scale"))
+        return ctypes.byref(msa_cache_q8_t(*p)), n_pages
 
 
 def rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original_len: int = 0,
