@@ -19,15 +19,16 @@
 //   O^T = V^T P^T (components = M): P carries the token's scale, P_t = 2^(x_t - rx + 12) with x_t = (s_t - rs) + e_t,
 //   and is rounded to f16, 2^-12 of itself or 2^-37 of the largest, whichever is more; the weights 2^(s_t - rs) are
 //   summed in fp32.  rs is raised where a weight would pass 2^60, rx where P would pass 2^15.9, which is rare: a unit
-//   costs no shuffle for them.  (x counts from rs, so logits of any size lose nothing to the exponent.)
+//   costs no shuffle for them.  (x counts from rs, so logits of any size lose nothing to the exponent.)  A row of zeros in
+//   V, whose scale of 1 says nothing of its size, is kept out of rx: beside it values of 2^-40 came back as 0.
 // What a row does not see cannot reach it: its P is 0, and its bytes of V are cleared (a code may be a NaN).
 // (The 8-bit MMA of warps takes codes as they are, but is no faster: it unpacks its operands itself, every time, and
 // needs P and q in pieces.)
 //
 // Measured (Hq = 64, G = 8, D = 128).  8 requests x 16 blocks (33 MB): 12.5 us against 5.0 at the copy rate; the chain is a
 // launch, two table loads, four units per warp at some 2,000 cycles and the join.  32 requests, window of 4,096 (257 MB):
-// 47 us against 38; 256 clusters of one CTA on 152 SMs leave a third of the SMs one row where the others have two.  First
-// kernel, with 8-bit MMAs: 17.5 and 94.
+// 48 us against 38; 256 clusters of one CTA on 152 SMs leave a third of the SMs one row where the others have two.  (12.4
+// and 47.4 without a look at rows of zeros.)  First kernel, with 8-bit MMAs: 17.5 and 94.
 //
 // Layout.  A unit's K and V are 32 rows of D bytes, swizzled by the copy (128- or 64-byte pattern).  Lane (r, c) =
 // (lane / 4, lane % 4) reads a quarter of K's rows 8i + r, i = 0 .. 3, and an eighth of V's rows 8i + 2c and 8i + 2c + 1:
@@ -337,6 +338,19 @@ __global__ void __launch_bounds__(kThreads, 2)
                 raise |= mx > rx[h] + kRaiseP || ms > rs[h] + kRaiseL;
             }
             if (__any_sync(0xffffffffu, raise)) {
+                // A row of zeros in V (its scale is 1) adds nothing and must not set P's reference: values far below 1 beside
+                // it would be lost.  Where a token's scale is 1, V's rows are looked at, token `lane`'s by each lane.
+                if (__any_sync(0xffffffffu, ve == 0.f)) {
+                    cp_async_wait<1>();
+                    __syncwarp();
+                    uint32_t any = 0u;
+#pragma unroll
+                    for (int k = 0; k < CPR; ++k) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(vu + unit_off<D>(lane, k));
+                        any |= y.x | y.y | y.z | y.w;
+                    }
+                    if (ve == 0.f && (any & 0x7f7f7f7fu) == 0u) ve = -INFINITY;
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float ms = fmaxf(fmaxf(s[0][h], s[1][h]), fmaxf(s[2][h], s[3][h]));

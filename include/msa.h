@@ -656,6 +656,8 @@ msa_status_t msa_index_score_q8(const void *q_idx, const msa_cache_q8_t *cache, 
  *   out bf16 [B][Hq][D] out;  lse fp32 [B][Hq] out.  A row that sees nothing gets 0 and -inf.
  * What a row does not see does not reach it, whatever its bits; a NaN that it sees makes it NaN.  q is finite
  * (else its row is NaN); components below 2^-39 of a head's largest count as 0.
+ * Tokens whose weight times V's scale is below 2^-37 of the head's largest count as 0 in out (rows of zeros in V are
+ * left out of that largest one).
  */
 msa_status_t msa_sparse_attn_decode_q8(const void *q, const msa_cache_q8_t *cache, const int32_t *page_table,
                                        const int32_t *row_len, int32_t B, int32_t n_pages, const msa_dims_t *dims,

@@ -12,6 +12,73 @@ from tests.test_gpu_q8 import E4M3, E8M0, cuda, i32, make_cache, msa, u8  # noqa
 pytestmark = pytest.mark.gpu
 
 
+# ------------------------------------------------------------------------------------------------ rows of zeros in V
+
+ZERO_ROWS = list(range(5)) + [37] + list(range(64, 97)) + [255]      # parts of a unit of 32 tokens, a whole one, the last token
+
+
+def _zero_rows(D, G, exp, logit, negative=False):
+    """256 tokens in two pages, V of 2^exp but for rows of zeros whose logits lie `logit` above the others'."""
+    bt, pool = Q.tables([256], 1)
+    k = Q.normal((pool, G, 128, D), 2, 0.3).double()
+    v = Q.normal((pool, G, 128, D), 3).double() * 2.0 ** exp
+    for t in ZERO_ROWS:
+        page = int(bt[0, t // 128])
+        v[page, :, t % 128] = 0.0
+        k[page, :, t % 128, 0] = logit
+    kc, vc = Q.to_cache(k), Q.to_cache(v)
+    assert all(int(u8(vc[1])[int(bt[0, t // 128]), 0, t % 128]) == 127 for t in ZERO_ROWS)
+    if negative:
+        u8(vc[0])[vc[0].float() == 0] = 0x80                                     # -0 is a zero too
+    q = Q.normal((4, 8 * G, D), 4, 0.3)
+    q[..., 0] = 1.0
+    return bt, kc, vc, q
+
+
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 1)])
+@pytest.mark.parametrize("exp,logit,negative", [(-7, 0.0, False), (-24, 0.0, True), (-40, 0.0, False), (-60, 30.0, False),
+                                                (-60, -30.0, True), (-90, 14.0, False), (-30, 400.0, False)])
+@pytest.mark.parametrize("call", ["paged", "decode", "chunk"])
+def test_rows_of_zeros_in_v_take_no_bits_of_the_others(msa, call, D, G, exp, logit, negative):  # noqa: F811
+    bt, kc, vc, q = _zero_rows(D, G, exp, logit, negative)
+    cache = msa.CacheQ8(*cuda(*kc, *vc))
+    k, v = Q.stored(*kc), Q.stored(*vc)
+    # with logits 400 apart what is left of the others is flushed: the bound says so; 1 / 16 keeps the rest in range
+    sc = 1.0 if logit == 400.0 else 1.0 / 16 if abs(logit) < 20 else 0.5
+    dims = msa.Dims(8 * G, G, D, 64, 2, bt.shape[1], sc)
+    pos = i32([255, 254, 130, 60])
+    if call == "paged":
+        table = bt.repeat(4 * G, 1)
+        lens = (pos + 1).repeat_interleave(G).to(torch.int32)
+        out, lse = msa.msa_sparse_attn_decode_q8(q.cuda(), cache, *cuda(table, lens), dims)
+        o, s, bo, bs = Q.ref_paged(q, k, v, table, lens, sc)
+    else:
+        req = i32([0] * 4)
+        out, lse = msa.msa_window_attn_q8(q.cuda(), cache, *cuda(bt, req, pos), 200, 3, dims, int(call == "chunk"))
+        o, s, bo, bs = Q.ref_window(q, k, v, bt, req, pos, 200, 3, sc)
+    Q.assert_within(out, o, bo, "out")
+    Q.assert_within(lse, s, bs, "lse")
+    if logit == 0.0:
+        assert bool((o.abs() > 4 * bo).any())                                    # the bound leaves something to tell
+
+
+@pytest.mark.parametrize("phase", [0, 1])
+def test_rows_of_zeros_alone_and_beside_nan(msa, phase):  # noqa: F811
+    dims = msa.Dims(8, 1, 128, 64, 1, 2)
+    cache, (k, v, _) = make_cache(msa, dims, 2, 3)
+    u8(cache.v).zero_()
+    u8(cache.v_scale).fill_(127)
+    q = Q.normal((2, 8, 128), 1)
+    args = i32([[0, 1]]).cuda(), i32([0, 0]).cuda(), i32([40, 200]).cuda(), 256, 0, dims, phase
+    out, lse = msa.msa_window_attn_q8(q.cuda(), cache, *args)
+    want = Q.ref_window(q, k, v * 0, i32([[0, 1]]), [0, 0], [40, 200], 256, 0, 1 / math.sqrt(128))
+    assert bool((out == 0).all())
+    Q.assert_within(lse, want[1], want[3], "lse")
+    u8(cache.v_scale)[0, 0, 100] = 255                                           # a row of NaN whose codes are zeros
+    out, lse = msa.msa_window_attn_q8(q.cuda(), cache, *args)
+    assert bool((out[0] == 0).all()) and bool(torch.isnan(out[1]).all())
+
+
 # ------------------------------------------------------------------------------------------------ caches
 
 def test_a_cache_whose_tensors_changed_is_refused(msa):  # noqa: F811
