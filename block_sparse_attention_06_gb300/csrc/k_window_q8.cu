@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rp[i] = r < a.n_rows ? a.q_pos[r] : 0;
                 if (rq[i] != -1 && (rq[i] < 0 || rq[i] >= a.n_req || rp[i] < 0 || (rp[i] >> 7) >= a.max_blocks)) {
                     if (g == 0) raise_flag(err, MSA_FLAG_BOUNDS);
-                    rq[i] = -1;
+                    rq[i] = -2;              // sees nothing: no page is whole beside it, and it gets 0 and -inf
                 }
             }
             int rq0[RPL];
@@ -744,6 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 g = steps[slot].g;
                 req = row < a.n_rows ? a.q_req[row] : -1;
                 pos = row < a.n_rows ? a.q_pos[row] : 0;
+                if (pos < 0 || (pos >> 7) >= a.max_blocks) {   // outside the table: sees nothing (nor does a bad request)
+                    req = req == -1 ? -1 : -2;
+                    pos = 0;
+                }
                 ref = -INFINITY;
                 l = 0.f;
                 poison = false;

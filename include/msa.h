@@ -684,7 +684,8 @@ msa_status_t msa_decode_step_q8(const void *q, const void *q_idx, const msa_cach
  *   out bf16 [n_rows][Hq][D] out;  lse fp32 [n_rows][Hq] out.  A row with q_req -1 is padding: nothing of it is
  *          written.
  * A bad request or position, or a page outside [0, n_pages) of a block that a row sees, raises
- * MSA_FLAG_BOUNDS.  What is said of q, V and NaN at msa_sparse_attn_decode_q8 holds here.  max_blocks <= 2^22.
+ * MSA_FLAG_BOUNDS; a row of such a request or position gets 0 and -inf, and the tokens of such a page are left out.
+ * What is said of q, V and NaN at msa_sparse_attn_decode_q8 holds here.  max_blocks <= 2^22.
  */
 msa_status_t msa_window_attn_q8(const void *q, const msa_cache_q8_t *cache, const int32_t *block_table,
                                 const int32_t *q_req, const int32_t *q_pos, int32_t n_rows, int32_t n_req,

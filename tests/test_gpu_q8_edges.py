@@ -79,6 +79,43 @@ def test_rows_of_zeros_alone_and_beside_nan(msa, phase):  # noqa: F811
     assert bool((out[0] == 0).all()) and bool(torch.isnan(out[1]).all())
 
 
+# ------------------------------------------------------------------------------------------------ rows that cannot be answered
+
+@pytest.mark.parametrize("phase", [0, 1])
+@pytest.mark.parametrize("Hq,G,D", [(16, 2, 128), (4, 1, 128), (8, 2, 64), (8, 1, 64)])
+def test_window_bad_rows_among_good_ones(msa, phase, Hq, G, D):  # noqa: F811
+    """Bad requests and positions in the same tiles as good rows, over pages that every good row sees whole: 0 and
+    -inf, as alone; the others as without them."""
+    bt, pool = Q.tables([900], 1)
+    dims = msa.Dims(Hq, G, D, 64, 1, bt.shape[1])
+    cache, (k, v, _) = make_cache(msa, dims, pool, 3)
+    R = 150
+    req, pos = i32([0] * R), torch.arange(700, 700 + R, dtype=torch.int32)
+    low = -2 ** 31
+    for r, a, p in ((3, 1, 710), (9, -2, 710), (17, low, 5), (31, 0, -1), (40, 0, low), (63, 0, bt.shape[1] * 128),
+                    (64, 0, 2 ** 31 - 1), (70, 2 ** 31 - 1, 0), (100, 7, -9), (149, 1, 849)):
+        req[r], pos[r] = a, p
+    bad = (req != 0) | (pos < 0) | (pos >= bt.shape[1] * 128)
+    pad = torch.zeros(R, dtype=torch.bool)
+    pad[[20, 21, 148]] = True
+    req[pad], pos[pad] = -1, low
+    q = Q.normal((R, Hq, D), 5)
+    q[31], q[21] = math.nan, math.inf
+    out = torch.full((R, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((R, Hq), 7.0, device="cuda")
+    err = msa.new_err_word("cuda")
+    for window, sinks in ((650, 0), (100, 300), (1 << 30, 0)):
+        out.fill_(7.0), lse.fill_(7.0), err.zero_()
+        msa.msa_window_attn_q8(q.cuda(), cache, *cuda(bt, req, pos), window, sinks, dims, phase, out, lse, err_word=err)
+        assert int(err) == 1
+        assert bool((out[bad.cuda()] == 0).all()) and bool((lse[bad.cuda()] == -math.inf).all())
+        assert bool((out[pad.cuda()] == 7.0).all()) and bool((lse[pad.cuda()] == 7.0).all())
+        rows = torch.nonzero(~bad & ~pad)[::5, 0]
+        o, s, bo, bs = Q.ref_window(q[rows], k, v, bt, req[rows], pos[rows], window, sinks, 1 / math.sqrt(D))
+        Q.assert_within(out.cpu()[rows], o, bo, "out")
+        Q.assert_within(lse.cpu()[rows], s, bs, "lse")
+
+
 # ------------------------------------------------------------------------------------------------ caches
 
 def test_a_cache_whose_tensors_changed_is_refused(msa):  # noqa: F811
