@@ -78,9 +78,11 @@ struct Smem {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
+    int empty;             // set where some head of a row has no weights
 };
 
 struct Args {
+    const uint16_t *q;
     const uint8_t *k, *k_scale, *v, *v_scale;
     const int32_t *block_table, *q_req, *q_pos;
     int n_rows, n_req, n_pages, max_blocks, Hq, G, window, n_sink, n_items;
@@ -89,6 +91,25 @@ struct Args {
     float *lse;
     int32_t *err;
 };
+
+// A head of a row (both in the whole call's numbering) for which no weight was counted, though the row sees a token, is
+// NaN where its q is not finite: such logits are NaN or infinite, and their sum is NaN unless they all are -inf.
+template <int D>
+__device__ __forceinline__ void poison_empty(const Args &a, int row, int h) {
+    if (row >= a.n_rows) return;
+    const int req = a.q_req[row], pos = a.q_pos[row];
+    const size_t head = size_t(row) * a.Hq + h;
+    if (req < 0 || req >= a.n_req || pos < 0 || (pos >> 7) >= a.max_blocks || a.lse[head] != -INFINITY) return;
+    bool finite = true, saw = false;
+    for (int i = 0; i < D; ++i) finite &= (a.q[head * D + i] & 0x7f80u) != 0x7f80u;
+    for (int j = 0; !finite && !saw && j <= pos >> 7; ++j) {
+        const int page = a.block_table[size_t(req) * a.max_blocks + j];
+        saw = (j * 128 + 127 > pos - a.window || j * 128 < a.n_sink) && page >= 0 && page < a.n_pages;
+    }
+    if (!saw) return;
+    for (int i = 0; i < D; ++i) a.out[head * D + i] = 0x7fffu;
+    a.lse[head] = __uint_as_float(0x7fffffffu);
+}
 
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
@@ -318,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.o_full[i], 1);
         }
         mbar_init(&sm.drain, 1);
-        sm.abort = 0;
+        sm.abort = sm.empty = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -885,6 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (live) *reinterpret_cast<uint4 *>(o_out + c + i) = w;
                     }
                 }
+                if (live && l == 0.f) sm.empty = 1;
                 if (live) a.lse[head] = l == 0.f ? -INFINITY : (ref * scale + log2f(l)) * kLn2;
                 tc_fence_before();
             }
@@ -901,6 +923,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
         else
             tmem_dealloc(tmem, 512);
+    }
+    // Heads without weights got 0 and -inf.  Those whose q is not finite are made NaN here, behind all roles: looked for in
+    // the epilogue, they took 2 % of the kernel's time.
+    if (sm.empty && !sm.abort) {
+        for (int item = blockIdx.x / CT; item < a.n_items; item += gridDim.x / CT) {
+            const int set = item / a.G, g = item - set * a.G;
+            for (int i = tid; i < 2 * EPT * HPG; i += kThreads)
+                poison_empty<D>(a, (set * CT + rank) * 2 * EPT + i / HPG, g * HPG + i % HPG);
+        }
     }
 }
 
@@ -941,6 +972,7 @@ cudaError_t launch_window_prefill_q8(const void *q, const CacheQ8 &c, const int3
                                      const int32_t *q_pos, int n_rows, int n_req, int n_pages, int window, int n_sink,
                                      const Shape &s, void *out, float *lse, int32_t *err, cudaStream_t st) {
     Args a = {};
+    a.q = static_cast<const uint16_t *>(q);
     a.k = static_cast<const uint8_t *>(c.k);
     a.k_scale = static_cast<const uint8_t *>(c.k_scale);
     a.v = static_cast<const uint8_t *>(c.v);

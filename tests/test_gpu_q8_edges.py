@@ -116,6 +116,30 @@ def test_window_bad_rows_among_good_ones(msa, phase, Hq, G, D):  # noqa: F811
         Q.assert_within(lse.cpu()[rows], s, bs, "lse")
 
 
+@pytest.mark.parametrize("phase", [0, 1])
+@pytest.mark.parametrize("D,G", [(128, 2), (64, 1)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_window_of_q_that_is_not_finite(msa, phase, D, G, bad, sign):  # noqa: F811
+    """A component that no key has 0 in, so that all logits of its row may be -inf: NaN in out and lse, and the
+    other rows and heads as without it."""
+    bt, pool = Q.tables([500], 1)
+    dims = msa.Dims(8 * G, G, D, 64, 1, bt.shape[1])
+    k = Q.normal((pool, G, 128, D), 2).double()
+    k[..., 9] = sign
+    cache = msa.CacheQ8(*cuda(*Q.to_cache(k), *Q.pages(pool, G, D, 3)))
+    q = Q.normal((40, 8 * G, D), 5).cuda()
+    args = bt.cuda(), i32([0] * 40).cuda(), torch.arange(400, 440, dtype=torch.int32).cuda(), 300, 5, dims, phase
+    want = msa.msa_window_attn_q8(q, cache, *args)
+    good = torch.ones((40, 8 * G), dtype=torch.bool)
+    for r, h in ((0, 5), (17, 0), (39, 8 * G - 1)):
+        q[r, h, 9] = bad
+        good[r, h] = False
+    out, lse = msa.msa_window_attn_q8(q, cache, *args)
+    assert bool(torch.isnan(out.cpu()[~good]).all()) and bool(torch.isnan(lse.cpu()[~good]).all())
+    assert torch.equal(out.cpu()[good], want[0].cpu()[good]) and torch.equal(lse.cpu()[good], want[1].cpu()[good])
+
+
 # ------------------------------------------------------------------------------------------------ caches
 
 def test_a_cache_whose_tensors_changed_is_refused(msa):  # noqa: F811
