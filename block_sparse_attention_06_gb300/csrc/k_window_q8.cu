@@ -284,6 +284,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// Infinities as the largest number of their sign.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t a) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 x;\n\tmin.bf16x2 x, %1, %2;\n\tmax.bf16x2 %0, x, %3;\n\t}"
+        : "=r"(r) : "r"(a), "r"(0x7f7f7f7fu), "r"(0xff7fff7fu));
+    return r;
+}
+
 // 16 codes as 16 bf16 numbers code * 2^-120 * f (f: a bf16 number in both halves).
 __device__ __forceinline__ void convert16(const uint4 &w, uint32_t f, uint32_t (&o)[8]) {
     const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
@@ -696,6 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     convert16(w, f, o);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], up);
+                    if (values) {    // finite under any scale: P is 0 for a row that does not see it
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = finite_bf16x2(o[k]);
+                    }
                     put(x.tok0 + (i ^ swap), o);
                 }
             }

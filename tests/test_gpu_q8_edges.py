@@ -140,6 +140,28 @@ def test_window_of_q_that_is_not_finite(msa, phase, D, G, bad, sign):  # noqa: F
     assert torch.equal(out.cpu()[good], want[0].cpu()[good]) and torch.equal(lse.cpu()[good], want[1].cpu()[good])
 
 
+@pytest.mark.parametrize("phase", [0, 1])
+@pytest.mark.parametrize("scale", [0, 247, 250, 254])
+@pytest.mark.parametrize("code", [0x7e, 0xfe, 0x7f, 0x01])
+def test_window_unseen_tokens_of_any_scale(msa, phase, scale, code):  # noqa: F811
+    """What lies in pages beside a row's tokens (memory as it came) under scales whose values pass every number."""
+    bt, pool = Q.tables([600], 1)
+    for D, G in ((128, 2), (64, 1)):
+        dims = msa.Dims(8 * G, G, D, 64, 1, bt.shape[1])
+        cache, _ = make_cache(msa, dims, pool, 3)
+        pos = [500 + 3 * i for i in range(20)]
+        q = Q.normal((20, 8 * G, D), 5).cuda()
+        args = (bt.cuda(), i32([0] * 20).cuda(), i32(pos).cuda(), 100, 5, dims, phase)
+        want = msa.msa_window_attn_q8(q, cache, *args)
+        assert bool(torch.isfinite(want[0].float()).all())
+        for t in list(range(5, 401)) + list(range(558, 600)):
+            page = int(bt[0, t // 128])
+            u8(cache.k)[page, :, t % 128] = u8(cache.v)[page, :, t % 128] = code
+            u8(cache.k_scale)[page, :, t % 128] = u8(cache.v_scale)[page, :, t % 128] = scale
+        got = msa.msa_window_attn_q8(q, cache, *args)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ------------------------------------------------------------------------------------------------ caches
 
 def test_a_cache_whose_tensors_changed_is_refused(msa):  # noqa: F811
