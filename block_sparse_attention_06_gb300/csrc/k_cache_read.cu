@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(const __grid_constant__
     const int which = blockIdx.y;
     const int to = a.bt_out[blockIdx.x];
     const int from = a.bt_in[blockIdx.x];
-    const int n_tok = min(128, a.lens[b] - j * 128);
+    const int n_tok = int(min(128LL, a.lens[b] - j * 128LL));   // 64 bits: a length may be any number
     if (to < 0 || n_tok <= 0) return;
     if (from < 0 || from >= a.n_pages || to >= a.n_pages_out) {
         if (threadIdx.x == 0 && which == 0) raise_flag(a.err, MSA_FLAG_BOUNDS);

@@ -628,7 +628,7 @@ msa_status_t msa_rope_append_q8(const msa_rows_t *rows, const msa_rope_t *rope, 
  * msa_cache_read_q8 -- blocks of 8-bit caches as bf16 pages, exactly: what the prefill calls
  * take.  Block j of request b is written to page out_table[b][j] where that is >= 0 and the block
  * holds a token below lens[b]; tokens at or past lens[b] are left as they are.
- *   block_table, out_table  int32 [n_req][max_blocks];  lens int32 [n_req]
+ *   block_table, out_table  int32 [n_req][max_blocks];  lens int32 [n_req] (0 or less: nothing is written)
  *   k_cache, v_cache  bf16 [n_out_pages][128][G][D] out;  kidx_cache bf16 [n_out_pages][128][G][Di] out,
  *                     or NULL (then cache->kidx is not read)
  * A page outside [0, n_pages) of a block to be written, or an out_table entry >= n_out_pages, raises

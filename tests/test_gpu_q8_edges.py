@@ -162,6 +162,21 @@ def test_window_unseen_tokens_of_any_scale(msa, phase, scale, code):  # noqa: F8
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+# ------------------------------------------------------------------------------------------------ ends of the ranges
+
+def test_read_of_lengths_below_zero(msa):  # noqa: F811
+    dims = msa.Dims(8, 2, 64, 32, 2, 3)
+    cache, (k, _, _) = make_cache(msa, dims, 4, 3)
+    out = [torch.full((6, 128, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    tables = i32([[0, 1, 2], [3, 0, 1]]).cuda(), i32([[0, 1, 2], [3, 4, 5]]).cuda()
+    err = msa.new_err_word("cuda")
+    for low in (-2 ** 31, -2 ** 31 + 200, -1, 0):
+        msa.msa_cache_read_q8(cache, *tables, i32([low, 130]).cuda(), dims, *out, err_word=err)
+        msa.msa_check(err)
+        assert bool((out[0][:3] == 7.0).all()) and bool((out[1][:3] == 7.0).all()), low
+    assert torch.equal(out[0][3].cpu().double(), k[3].transpose(0, 1)) and bool((out[0][4, 2:] == 7.0).all())
+
+
 # ------------------------------------------------------------------------------------------------ caches
 
 def test_a_cache_whose_tensors_changed_is_refused(msa):  # noqa: F811
