@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 from dataclasses import dataclass
 from typing import Optional, Tuple
@@ -722,6 +723,7 @@ def msa_commit_tree(k_new, v_new, kidx_new, k_cache, v_cache, kidx_cache, block_
 
 _E4M3, _E8M0, _F64 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.float64
 _NO_KV = (None, None, None, None)
+_I32_MAX = 2 ** 31 - 1
 
 
 @dataclass(frozen=True)
@@ -975,6 +977,7 @@ def msa_window_attn_q8(q, cache: CacheQ8, block_table, q_req, q_pos, window: int
     """Attention over 8-bit caches of each row (the token at q_pos[r] of request q_req[r]; -1: padding, nothing of it
     is written) to the last `window` tokens and the first n_sink -> (out, lse).  phase: MSA_PHASE_DECODE (single rows)
     or MSA_PHASE_PREFILL (chunks)."""
+    window, n_sink = (max(min(operator.index(x), _I32_MAX), -1) for x in (window, n_sink))   # past any context, or refused
     dev = _lead(q, "q")
     n = _ndim(q, 3, "q", "[n_rows][Hq][D]")[0]
     n_req = _ndim(block_table, 2, "block_table", "[n_req][max_blocks]")[0]

@@ -177,6 +177,23 @@ def test_read_of_lengths_below_zero(msa):  # noqa: F811
     assert torch.equal(out[0][3].cpu().double(), k[3].transpose(0, 1)) and bool((out[0][4, 2:] == 7.0).all())
 
 
+@pytest.mark.parametrize("phase", [0, 1])
+def test_windows_past_32_bits(msa, phase):  # noqa: F811
+    """A window or a number of first tokens past the longest context says no more than that one, however large."""
+    bt, pool = Q.tables([300], 1)
+    dims = msa.Dims(8, 1, 64, 64, 1, bt.shape[1])
+    cache, _ = make_cache(msa, dims, pool, 3)
+    q = Q.normal((2, 8, 64), 5).cuda()
+    args = q, cache, bt.cuda(), i32([0, 0]).cuda(), i32([299, 100]).cuda()
+    dense = msa.msa_window_attn_q8(*args, 300, 0, dims, phase)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31, 0), (2 ** 32 + 1, 0), (2 ** 63, 0), (300, 2 ** 32), (300, 2 ** 40 + 3)):
+        got = msa.msa_window_attn_q8(*args, window, sinks, dims, phase)
+        assert torch.equal(got[0], dense[0]) and torch.equal(got[1], dense[1]), (window, sinks)
+    for window, sinks in ((0, 0), (-2 ** 32 + 5, 0), (5, -1), (5, -2 ** 32)):
+        with pytest.raises(msa.MsaError, match="window"):
+            msa.msa_window_attn_q8(*args, window, sinks, dims, phase)
+
+
 # ------------------------------------------------------------------------------------------------ caches
 
 def test_a_cache_whose_tensors_changed_is_refused(msa):  # noqa: F811
