@@ -1002,6 +1002,26 @@ def dims_of(case) -> Dims:
     return Dims(d.Hq, d.G, d.D, d.Di, d.topk, case.max_blocks, d.sm_scale, d.page)
 
 
+class _Graph:
+    """A step recorded into a CUDA graph on the device of its tensors, which need not be the current one: calls of
+    another device are not part of a capture on the current one, and a replay has to follow what that device's current
+    stream holds."""
+
+    def __init__(self, run, index: int):
+        self.index, self.graph = index, torch.cuda.CUDAGraph()
+        with torch.cuda.device(index):
+            torch.cuda.synchronize(index)
+            with torch.cuda.graph(self.graph, stream=torch.cuda.Stream(index)):
+                run()
+
+    def replay(self):
+        if self.index == torch._C._cuda_getDevice():
+            self.graph.replay()
+        else:
+            with torch.cuda.device(self.index):
+                self.graph.replay()
+
+
 class DecodeStep:
     """One MSA decode step with preallocated buffers: index scoring -> top-k ->
     page table -> paged sparse attention.  Buffers are reused across calls so the
@@ -1085,14 +1105,13 @@ class DecodeStep:
         if inputs is not None:
             inputs.upload()
         self._graph_results = self(*args, **res)
-        torch.cuda.synchronize(q.device)
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
+
+        def run():
             if inputs is not None:
                 inputs.upload()
             self(*args, **res)
-        self._graph = graph
-        return graph
+        self._graph = _Graph(run, q.get_device())
+        return self._graph.graph
 
     def replay(self):
         """Replay the step recorded by capture() on the current stream; returns the (out,
@@ -1350,12 +1369,8 @@ class DecodeStepQ8:
         """Record step() on these tensors (one eager step runs first); write new values into them, then replay()."""
         args = (q, k, v, q_idx, k_idx, cache, block_table, q_pos, seq_lens)
         self.step(*args)
-        torch.cuda.synchronize(q.device)
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
-            self.step(*args)
-        self._graph, self._graph_args = graph, args
-        return graph
+        self._graph, self._graph_args = _Graph(lambda: self.step(*args), q.get_device()), args
+        return self._graph.graph
 
     def replay(self):
         """Replay the captured step on the current stream -> its (out, lse)."""

@@ -1,5 +1,6 @@
 """8-bit caches without a GPU: tensors of a cache that change between calls, captures on a device that is not the current
 one, and the frequencies of positions scaled for long contexts."""
+import contextlib
 
 import pytest
 import torch
@@ -39,3 +40,60 @@ def test_a_cache_that_grows_is_taken_as_it_is():
     for name in ("k", "k_scale", "v", "v_scale"):
         getattr(c, name).data = getattr(big, name)
     assert c._struct(dims, dev, True, False)[1] == 5
+
+
+# ------------------------------------------------------------------------------------------------ captures
+
+def test_a_step_is_captured_and_replayed_on_its_own_device(monkeypatch):
+    """On a machine with several GPUs, of which another one is current: recorded stand-ins for torch's calls."""
+    state = {"device": 0, "capture": None}
+    seen = []
+
+    @contextlib.contextmanager
+    def device(d):
+        old, state["device"] = state["device"], torch.device(d).index if not isinstance(d, int) else d
+        yield
+        state["device"] = old
+
+    class Stream:
+        def __init__(self, d=None):
+            self.device = state["device"] if d is None else torch.device(d).index
+
+    @contextlib.contextmanager
+    def graph(g, pool=None, stream=None):
+        old = dict(state)
+        state["capture"] = 0 if stream is None else stream.device               # torch's own capture stream is the first device's
+        state["device"] = state["capture"]
+        yield
+        state.update(old)
+
+    class Graph:
+        def replay(self):
+            seen.append(("replay", state["device"]))
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "graph", graph)
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", Graph)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda d=None: None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["device"], raising=False)
+
+    class Q:
+        device = torch.device("cuda", 1)
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    for cls, n in ((m.DecodeStepQ8, 9), (m.DecodeStep, 7)):
+        step = cls.__new__(cls)
+        step.out, step.lse, step._graph_results = "out", "lse", ("out", "lse")
+        run = lambda *a, **k: seen.append(("step", state["capture"], state["device"]))  # noqa: E731
+        monkeypatch.setattr(cls, "step" if cls is m.DecodeStepQ8 else "__call__",
+                            (lambda f: lambda self, *a, **k: f(*a, **k))(run))
+        seen.clear()
+        step.capture(Q(), *[None] * (n - 1))
+        assert seen[0][:2] == ("step", None) and seen[1] == ("step", 1, 1), cls
+        assert state == {"device": 0, "capture": None}
+        step.replay()
+        assert seen[2] == ("replay", 1) and state["device"] == 0, cls
