@@ -10,8 +10,8 @@
 // The angle of a far position loses its digits in fp32 (position 2^20 turns the first pair by 2^20 radians),
 // so it is counted in turns in 64-bit fixed point: inv_freq / 2 pi, modulo one turn, as a fraction of 2^64;
 // times the position, modulo 2^64, is the fraction of a turn with the error of inv_freq / 2 pi in 64-bit floating point
-// alone.  Cosine and sine are worked out from it to 2^-29 and rounded once: codes are rounded from what they turn, and an
-// error more would move what lies next to a border.
+// and 2^-64 of a turn per position alone.  Cosine and sine are worked out from it to 2^-28 of themselves and rounded
+// once: codes are rounded from what they turn, and an error more would move what lies next to a border.
 //
 // Every byte is moved once, by 16-byte loads and stores.  A warp takes 32 chunks of 8 components of one
 // section (q, k, v, q_idx or k_idx) at a time, in RPC rows at once, so RPC loads of a lane are in flight; a
@@ -53,8 +53,10 @@ __device__ __forceinline__ void turn2(float &y0, float &y1, float p0, float p1, 
         : "f"(p0), "f"(p1), "f"(c0), "f"(c1), "f"(s0), "f"(s1));
 }
 
-// gain * (cos, sin) of turn / 2^64 turns, rounded once but for 2^-29: the nearest quarter turn is taken off, and the Taylor
-// series of the angle that is left (at most pi/4) run with the errors of their leading terms carried along.
+// gain * (cos, sin) of turn / 2^64 turns, rounded once but for 2^-28 of themselves (0.8 and 0.7 x 2^-28 at most of two
+// million angles; 3.2 x 2^-28 without the error of z in z q, and one cosine in thirty near an eighth of a turn then was not
+// the nearest fp32 number, where one in a hundred is not): the nearest quarter turn is taken off, and the Taylor series of
+// the angle that is left (at most pi/4) run with the errors of their leading terms carried along.
 __device__ __forceinline__ float2 cos_sin(unsigned long long turn, float gain) {
     const uint32_t quarters = uint32_t((turn + (1ull << 61)) >> 62);
     const long long left = (long long)(turn - ((unsigned long long)quarters << 62));   // 2^-63 half turns
@@ -62,9 +64,9 @@ __device__ __forceinline__ float2 cos_sin(unsigned long long turn, float gain) {
     constexpr float kPi = 3.14159274f, kPiLo = -8.74227766e-8f, kSixth = -0.166666672f, kSixthLo = 4.96705377e-9f;
     const float x = r * 0x1p-63f, t = x * kPi, te = fmaf(x, kPi, -t) + fmaf(x, kPiLo, r_lo * 0x1p-63f * kPi);   // angle
     const float z = t * t, ze = fmaf(t, t, -z) + 2.f * t * te;                                                  // squared
-    // 1 - z/2 + z^2 (1/4! - z/6! + z^2/8! - z^3/10!)
-    const float q = fmaf(z, fmaf(z, fmaf(z, -2.75573192e-7f, 2.48015873e-5f), -1.38888889e-3f), 4.16666667e-2f);
-    const float ch = fmaf(-0.5f, z, 1.f), ct = fmaf(z * z, q, fmaf(-0.5f, z, 1.f - ch) - 0.5f * ze);
+    // 1 - z/2 + z q, q = z (1/4! - z/6! + z^2/8! - z^3/10!); the error of z turns both by ze (2 q - 1/2)
+    const float q = z * fmaf(z, fmaf(z, fmaf(z, -2.75573192e-7f, 2.48015873e-5f), -1.38888889e-3f), 4.16666667e-2f);
+    const float ch = fmaf(-0.5f, z, 1.f), ct = fmaf(z, q, fmaf(ze, fmaf(2.f, q, -0.5f), fmaf(-0.5f, z, 1.f - ch)));
     const float c = ch + ct, c_lo = (ch - c) + ct;
     // t - t z/3! + t z^2 (1/5! - z/7! + z^2/9! - z^3/11!)
     const float v = t * z, ve = fmaf(t, z, -v) + fmaf(te, z, t * ze);

@@ -593,7 +593,7 @@ typedef struct {
  * (2i, 2i + 1): (a, b) -> gain * (a cos w - b sin w, b cos w + a sin w), w = q_pos * inv_freq[i].  Index
  * vectors likewise with rot_idx and inv_freq_idx.  Positions scaled for long contexts are a matter of
  * inv_freq and gain.  The angle is reduced to a turn at any position with an error of at most
- * q_pos * inv_freq * 2^-54 turns; its cosine and sine are rounded to fp32 once. */
+ * q_pos * (inv_freq * 2^-54 + 2^-64) turns; its cosine and sine are rounded to fp32 once, but for 2^-28 of them. */
 typedef struct {
     int32_t rot, rot_idx;       /* multiples of 16 in [0, D] and [0, Di]                   */
     int32_t interleaved;        /* 0 or 1                                                  */

@@ -194,6 +194,42 @@ def test_windows_past_32_bits(msa, phase):  # noqa: F811
             msa.msa_window_attn_q8(*args, window, sinks, dims, phase)
 
 
+# ------------------------------------------------------------------------------------------------ the angle
+
+@pytest.mark.parametrize("pos", [1, 1000003])
+def test_cosines_and_sines_are_rounded_once(msa, pos):  # noqa: F811
+    """Pairs (1, b) turned by nearly arc cot b: the first component is cos - b sin, in fp32 next to 0, and shows both
+    to their last bit.  Each is a neighbour of the 64-bit value, and the farther one only where the two are as near
+    as 2^-28 of it."""
+    rounds, n = 128, 64
+    dims = msa.Dims(4, 1, 128, 64, 1, pos // 128 + 1)
+    table = torch.zeros((1, dims.max_blocks), dtype=torch.int32, device="cuda")
+    caches = [torch.empty((1, 128, 1, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kv = torch.zeros((1, 1, 128), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(pos)
+    b = 1.0 + torch.randint(0, 24, (rounds, n), generator=g).double() / 128      # bf16 numbers; angles of 0.11 to 0.13 turns
+    f = (torch.atan(1 / b) + (2 * torch.rand((rounds, n), generator=g).double() - 1) * 2.0 ** -18) / pos
+    x = torch.zeros((rounds, 1, 4, 128), dtype=torch.bfloat16)
+    x[:, 0, :, :64], x[:, 0, :, 64:] = 1.0, b[:, None].to(torch.bfloat16)
+    x, fd = x.cuda(), f.cuda()
+    zero, at = i32([0]).cuda(), i32([pos]).cuda()
+    got = torch.stack([msa.msa_rope_append(x[i], kv, kv, None, None, *caches, None, table, zero, at, msa.Rope(128, fd[i]),
+                                           dims)[0][0, 0] for i in range(rounds)]).cpu()
+    w = f * pos
+
+    def near(y):                         # the fp32 numbers that y may have been rounded to
+        y32 = y.float()
+        z32 = torch.nextafter(y32, torch.where(y > y32.double(), 1.0, -1.0).float())
+        half = (z32.double() - y32.double()).abs() / 2
+        return (y32.double(), torch.where((z32.double() - y).abs() <= half + 2.0 ** -28 * y.abs(), z32.double(), y32.double()))
+    c, s = near(torch.cos(w)), near(torch.sin(w))
+    ok = torch.zeros(rounds, n, dtype=torch.bool)
+    for cc in c:
+        for ss in s:
+            ok |= (cc - b * ss).float().to(torch.bfloat16) == got[:, :64]
+    assert bool(ok.all()), f"{int((~ok).sum())} of {ok.numel()} pairs"
+
+
 # ------------------------------------------------------------------------------------------------ caches
 
 def test_a_cache_whose_tensors_changed_is_refused(msa):  # noqa: F811
