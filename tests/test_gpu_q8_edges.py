@@ -230,6 +230,111 @@ def test_cosines_and_sines_are_rounded_once(msa, pos):  # noqa: F811
     assert bool(ok.all()), f"{int((~ok).sum())} of {ok.numel()} pairs"
 
 
+# ------------------------------------------------------------------------------------------------ long streams
+
+@pytest.mark.parametrize("Hq,G,D,n", [(64, 8, 128, 1500), (16, 4, 128, 5200), (32, 4, 64, 2600), (16, 4, 64, 5200)])
+def test_window_more_items_than_ctas(msa, Hq, G, D, n):  # noqa: F811
+    """Several items per CTA: rows of three requests, padding and bad rows, items of padding and of bad rows alone."""
+    lens = [n // 2 + 700, n // 3 + 90, n // 6]
+    bt, pool = Q.tables(lens, 1)
+    dims = msa.Dims(Hq, G, D, 64, 1, bt.shape[1])
+    cache, (k, v, _) = make_cache(msa, dims, pool, 3)
+    rows = [(b, p) for b, m in zip(range(3), (n // 2, n // 3, n // 6)) for p in range(lens[b] - m, lens[b])]
+    rows += [(-1, 0)] * (n - len(rows))
+    req, pos = i32([b for b, _ in rows]), i32([p for _, p in rows])
+    req[256:512] = -1                                                            # whole items of padding
+    req[640:900:2] = -1
+    req[900:1156] = 3                                                            # and of rows without a request
+    q = Q.normal((n, Hq, D), 5)
+    out = torch.full((n, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n, Hq), 7.0, device="cuda")
+    err = msa.new_err_word("cuda")
+    args = q.cuda(), cache, *cuda(bt, req, pos), 150, 9, dims, 1
+    msa.msa_window_attn_q8(*args, out, lse, err_word=err)
+    assert int(err) == 1
+    again = msa.msa_window_attn_q8(*args)
+    live = (req >= 0).cuda()
+    assert torch.equal(out[live], again[0][live]) and torch.equal(lse[live], again[1][live])
+    assert bool((out[~live] == 7.0).all()) and bool((out[(req == 3).cuda()] == 0).all())
+    at = torch.nonzero((req >= 0) & (req < 3))[:, 0]
+    at = at[torch.randperm(at.numel(), generator=torch.Generator().manual_seed(1))[:300]]
+    o, s, bo, bs = Q.ref_window(q[at], k, v, bt, req[at], pos[at], 150, 9, 1 / math.sqrt(D))
+    Q.assert_within(out.cpu()[at], o, bo, "out")
+    Q.assert_within(lse.cpu()[at], s, bs, "lse")
+    # every row against the rows taken one by one: each of the two rounds P and the output, by 2^-8 of the largest value
+    # that a row can see, and 2^-10 of it is more than all else in the bound
+    one = msa.msa_window_attn_q8(*args[:-1], 0)
+    d = (out.float() - one[0].float()).abs()[live]
+    assert float(d.max()) <= float(v.abs().max()) * 2 * (2 * 2.0 ** -8 + 2.0 ** -10)
+
+
+def test_window_second_cta_of_a_pair_with_four_heads(msa):  # noqa: F811
+    bt, pool = Q.tables([600], 1)
+    dims = msa.Dims(8, 2, 128, 64, 1, bt.shape[1])
+    cache, (k, v, _) = make_cache(msa, dims, pool, 3)
+    for n in (65, 128, 200):             # a pair takes 128 rows, 64 a CTA
+        req, pos = i32([0] * n), torch.arange(600 - n, 600, dtype=torch.int32)
+        q = Q.normal((n, 8, 128), 5)
+        out, lse = msa.msa_window_attn_q8(q.cuda(), cache, *cuda(bt, req, pos), 140, 2, dims, 1)
+        o, s, bo, bs = Q.ref_window(q, k, v, bt, req, pos, 140, 2, 1 / math.sqrt(128))
+        Q.assert_within(out, o, bo, "out")
+        Q.assert_within(lse, s, bs, "lse")
+
+
+@pytest.mark.parametrize("Di,G,rows", [(64, 8, 8), (32, 16, 5), (64, 4, 40)])
+def test_score_long_streams(msa, Di, G, rows):  # noqa: F811
+    """Many units per warp: stages filled again and again, runs of more than 32 blocks of one (row, group).  Pages are
+    shared, so the reference needs each once."""
+    pool, MB = 12, 800
+    dims = msa.Dims(4 * G, G, 64, Di, 2, MB)
+    cache, (_, _, x) = make_cache(msa, dims, pool, 3)
+    g = torch.Generator().manual_seed(4)
+    bt = torch.randint(0, pool, (rows, MB), generator=g).to(torch.int32)
+    pos = torch.randint(MB * 128 - 9000, MB * 128, (rows,), generator=g).to(torch.int32)
+    pos[0], pos[1], pos[2] = MB * 128 - 1, 5, 127
+    req = torch.arange(rows, dtype=torch.int32)
+    q = Q.normal((rows, G, Di), 9)
+    err = msa.new_err_word("cuda")
+    got = msa.msa_index_score_q8(q.cuda(), cache, *cuda(bt, req, pos), dims, err_word=err)
+    msa.msa_check(err)
+    assert torch.equal(got, msa.msa_index_score_q8(q.cuda(), cache, *cuda(bt, req, pos), dims))
+    s = torch.einsum("rgd,pgtd->rgpt", Q.f64(q), x)
+    mag = torch.einsum("rgd,pgtd->rgpt", Q.f64(q).abs(), x.abs()).amax(-1) * 1.2 * (Di + 8) * 2.0 ** -23
+    tol = mag + Q.f64(q).abs().amax(-1)[..., None] * x.abs().sum(-1).amax(-1).T[None] * 2.0 ** -39   # as in ref_scores
+    want, bound = torch.full((rows, G, MB), -math.inf).double(), torch.zeros((rows, G, MB)).double()
+    for r in range(rows):
+        last = int(pos[r]) // 128
+        pages = bt[r, :last + 1].long()
+        want[r, :, :last + 1] = s[r].amax(-1)[:, pages]
+        want[r, :, last] = s[r, :, int(pages[-1]), :int(pos[r]) % 128 + 1].amax(-1)
+        bound[r, :, :last + 1] = tol[r][:, pages]
+    Q.assert_within(got, want, bound, "scores")
+
+
+@pytest.mark.parametrize("rows,MB,D", [(80, 160, 64), (80, 150, 128), (1, 1100, 64), (9, 300, 128)])
+def test_window_of_many_units_per_warp(msa, rows, MB, D):  # noqa: F811
+    """More than 32 units per warp: pages are looked up again.  Pages are shared."""
+    pool = 8
+    dims = msa.Dims(8, 1, D, 64, 1, MB)
+    cache, (k, v, _) = make_cache(msa, dims, pool, 3)
+    g = torch.Generator().manual_seed(4)
+    bt = torch.randint(0, pool, (rows, MB), generator=g).to(torch.int32)
+    req = torch.arange(rows, dtype=torch.int32)
+    pos = torch.randint(MB * 128 - 4000, MB * 128, (rows,), generator=g).to(torch.int32)
+    pos[0] = MB * 128 - 1
+    q = Q.normal((rows, 8, D), 9)
+    for window, sinks in ((1 << 30, 0), (MB * 128 - 9000, 700)):
+        out, lse = msa.msa_window_attn_q8(q.cuda(), cache, *cuda(bt, req, pos), window, sinks, dims, 0)
+        for r in range(0, rows, 11):
+            p = int(pos[r])
+            t = torch.arange(p + 1)
+            t = t[(t > p - window) | (t < sinks)]
+            page, slot = bt[r].long()[t // 128], t % 128
+            want = Q.ref_attend(Q.f64(q[r]), k[page, 0, slot], v[page, 0, slot], 1 / math.sqrt(D))
+            Q.assert_within(out[r], want[0], want[2], "out")
+            Q.assert_within(lse[r], want[1], want[3], "lse")
+
+
 # ------------------------------------------------------------------------------------------------ caches
 
 def test_a_cache_whose_tensors_changed_is_refused(msa):  # noqa: F811

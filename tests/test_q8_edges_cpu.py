@@ -1,6 +1,7 @@
 """8-bit caches without a GPU: tensors of a cache that change between calls, captures on a device that is not the current
 one, and the frequencies of positions scaled for long contexts."""
 import contextlib
+import math
 
 import pytest
 import torch
@@ -97,3 +98,26 @@ def test_a_step_is_captured_and_replayed_on_its_own_device(monkeypatch):
         assert state == {"device": 0, "capture": None}
         step.replay()
         assert seen[2] == ("replay", 1) and state["device"] == 0, cls
+
+
+# ------------------------------------------------------------------------------------------------ frequencies
+
+@pytest.mark.parametrize("rot,base,factor,length", [(64, 10000.0, 16.0, 4096), (128, 500000.0, 4.0, 8192), (32, 10000.0, 2.0, 512)])
+def test_yarn_is_its_definition(rot, base, factor, length):
+    """A pair that turns r times over the original length keeps its frequency for r above beta_fast, is divided by the
+    factor below beta_slow, and is blended linearly in the pair's number between the two (their whole pairs outwards)."""
+    got, gain = m.rope_inv_freq(rot, base, "yarn", factor, length)
+    # pair i turns length * base^(-2 i / rot) / (2 pi) times: the first that turns at most r times
+    def at(r):
+        i = 0.0
+        lo, hi = -1000.0, 1000.0
+        for _ in range(200):
+            i = (lo + hi) / 2
+            lo, hi = (i, hi) if length * base ** (-2 * i / rot) / (2 * math.pi) > r else (lo, i)
+        return i
+    lo, hi = max(math.floor(at(32.0)), 0), min(math.ceil(at(1.0)), rot - 1)
+    for i in range(rot // 2):
+        f = base ** (-2 * i / rot)
+        kept = 1.0 if i <= lo else 0.0 if i >= hi else (hi - i) / (hi - lo)
+        assert math.isclose(float(got[i]), f * kept + f / factor * (1 - kept), rel_tol=1e-12), i
+    assert 0 < lo + 1 < hi < rot and math.isclose(gain, 0.1 * math.log(factor) + 1)
