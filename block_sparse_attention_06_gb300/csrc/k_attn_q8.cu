@@ -51,12 +51,6 @@ constexpr float kShift = 12.f;       // P is at most 2^12 where its reference wa
 constexpr float kRaiseP = 3.9f;      // ... and its reference is raised where it would pass 2^15.9 (f16 ends below 2^16)
 constexpr float kRaiseL = 60.f;      // a weight may pass its reference by 2^60
 
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));

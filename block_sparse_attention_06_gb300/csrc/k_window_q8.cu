@@ -111,12 +111,6 @@ __device__ __forceinline__ void poison_empty(const Args &a, int row, int h) {
     a.lse[head] = __uint_as_float(0x7fffffffu);
 }
 
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Two fp32 lanes per instruction; b2 and c2 hold one value in both halves.
 __device__ __forceinline__ uint64_t dup2(float x) {
     uint64_t r;
@@ -143,11 +137,11 @@ __device__ __forceinline__ float sum2(uint64_t acc2) {
 __device__ __forceinline__ uint32_t ones_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // D/16 MMAs of S = Q K^T, both operands K-major with the 128-byte swizzle: a k-step of 16 columns is 32 bytes
-// further in a sub-tile of 64 columns; sub-tiles are 16 KB apart (a pair's halves of K: 8 KB).  One asm block, so that
-// the issuing thread spends as few issue slots as it can.
+// further in a sub-tile of 64 columns; with heads of 128, Q's two sub-tiles are 16 KB apart and those of a CTA's half of K
+// 8 KB.  One asm block, so that the issuing thread spends as few issue slots as it can.
 template <int D, bool PAIR>
 __device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t el) {
-    static_assert(D == 128 || !PAIR, "pairs have D = 128");
+    static_assert(PAIR == (D == 128), "heads of 128 take pairs, heads of 64 single CTAs");
     if constexpr (PAIR) {
         asm volatile(
             "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
@@ -164,24 +158,6 @@ __device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint32
             "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a5, b5, %3, t;\n\t"
             "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a6, b6, %3, t;\n\t"
             "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(el)
-            : "memory");
-    } else if constexpr (D == 128) {
-        asm volatile(
-            "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
-            "setp.ne.b32 e, %4, 0;\n\tsetp.ne.b32 f, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
-            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
-            "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
-            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 1024;\n\t"
-            "add.s64 b5, %2, 1026;\n\tadd.s64 b6, %2, 1028;\n\tadd.s64 b7, %2, 1030;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, t;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(el)
             : "memory");
     } else {
@@ -641,6 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int swap = (lane >> 2) & 1;
         constexpr int KL = D / 16, KT = KL / 2 / CT;         // K: lanes per token, tokens per thread
         constexpr int VL = D / 16 / CT, VT = D / 32 / CT;    // V
+        static_assert(KT == 2 && VT == 2, "the scales of a thread's tokens are one 16-bit load");
         using Lane = struct {
             int col, tok0, row;                              // 16 codes of the tile's tokens tok0 .., the page's row ..
             uint32_t at;                                     // their sub-tile of 64 columns
@@ -666,10 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < T; ++i) c[i] = __ldg(reinterpret_cast<const uint4 *>(p + (i ^ swap) * D));
             const uint8_t *sp = scales + page_line + x.row;
-            uint32_t sc;
-            if constexpr (T == 4) sc = __ldg(reinterpret_cast<const uint32_t *>(sp));
-            else sc = __ldg(reinterpret_cast<const uint16_t *>(sp));
-            return swap ? __byte_perm(sc, 0u, 0x2301) : sc;
+            const uint32_t sc = __ldg(reinterpret_cast<const uint16_t *>(sp));
+            return swap ? __byte_perm(sc, 0u, 0x4401) : sc;
         };
         auto store = [&](uint8_t *tile, const Lane &x, const auto &c, uint32_t sc, bool values) {
             constexpr int T = sizeof(c) / sizeof(uint4);
@@ -681,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p0 ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]),
                              "r"(o[7]) : "memory");
             };
-            if (__all_sync(0xffffffffu, (sc & 0x80808080u) == 0u)) {   // no scale above 1, no NaN row: 2^(120 + e)
+            if (__all_sync(0xffffffffu, (sc & 0x8080u) == 0u)) {   // no scale above 1, no NaN row: 2^(120 + e)
 #pragma unroll
                 for (int i = 0; i < T; ++i) {
                     uint32_t o[8];

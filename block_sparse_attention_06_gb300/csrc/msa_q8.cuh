@@ -90,6 +90,12 @@ __device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint3
         : "memory");
 }
 
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Maximum that keeps a NaN.
 __device__ __forceinline__ float fmax_nan(float a, float b) {
     float r;

@@ -350,3 +350,59 @@ def test_a_cache_whose_tensors_changed_is_refused(msa):  # noqa: F811
         x.data = x[:2].clone()
         with pytest.raises(ValueError, match="shape"):
             call()
+
+
+# ------------------------------------------------------------------------------------------------ shapes
+
+@pytest.mark.parametrize("Hq,G,D", [(12, 3, 64), (40, 5, 128), (24, 3, 128), (80, 20, 64)])
+def test_groups_that_are_no_power_of_two(msa, Hq, G, D):  # noqa: F811
+    """Calls without the index take any number of groups: append, read back, decode and window attention."""
+    n = 200
+    bt, pool = Q.tables([n], 1)
+    dims = msa.Dims(Hq, G, D, 64, 2, bt.shape[1])
+    cache = msa.CacheQ8.zeros(dims, pool, "cuda", index=False)
+    rows = [Q.normal((n, h, D), 7 + i) for i, h in enumerate((Hq, G, G))]
+    req, pos = i32([0] * n), torch.arange(n, dtype=torch.int32)
+    f = 10000.0 ** (-2 * torch.arange(16).double() / 32)
+    err = msa.new_err_word("cuda")
+    q, _ = msa.msa_rope_append_q8(*cuda(*rows), None, None, cache, *cuda(bt, req, pos), msa.Rope(32, f.cuda()), dims,
+                                  err_word=err)
+    y, t = Q.rotated(rows[0], 32, f, pos.long(), False, 1.0)
+    Q.assert_within(q, y, t + (y.abs() + t) * 2.0 ** -8, "q")
+    page, slot = bt.long()[0, pos.long() // 128], pos.long() % 128
+    for x, s, row, rot in ((cache.k, cache.k_scale, rows[1], 32), (cache.v, cache.v_scale, rows[2], 0)):
+        y, t = Q.rotated(row, rot, f, pos.long(), False, 1.0)
+        Q.check_rows8(u8(x).cpu()[page, :, slot].view(E4M3), u8(s).cpu()[page, :, slot].view(E8M0), y, t, "cache")
+    k, v = (Q.stored(x.cpu(), s.cpu()) for x, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    out = [torch.zeros((pool, 128, G, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    msa.msa_cache_read_q8(cache, bt.cuda(), bt.cuda(), i32([n]).cuda(), dims, *out, err_word=err)
+    for x, val in zip(out, (k, v)):
+        assert torch.equal(x.cpu().double().transpose(1, 2), val * (x.cpu() != 0).any(-1)[..., None].transpose(1, 2).double())
+        assert torch.equal(x.cpu()[page, slot].double(), val[page, :, slot])
+    q = q.cpu()
+    at = torch.arange(0, n, 23)
+    o, s, bo, bs = Q.ref_window(q[at], k, v, bt, req[at], pos[at], 90, 5, 1 / math.sqrt(D))
+    for phase in (0, 1):
+        got, lse = msa.msa_window_attn_q8(q.cuda(), cache, *cuda(bt, req, pos), 90, 5, dims, phase, err_word=err)
+        Q.assert_within(got.cpu()[at], o, bo, "out")
+        Q.assert_within(lse.cpu()[at], s, bs, "lse")
+    table, lens = bt.repeat(3 * G, 1), i32([200, 77, 1]).repeat_interleave(G).to(torch.int32)
+    got, lse = msa.msa_sparse_attn_decode_q8(q[:3].cuda(), cache, *cuda(table, lens), dims, err_word=err)
+    o, s, bo, bs = Q.ref_paged(q[:3], k, v, table, lens, 1 / math.sqrt(D))
+    Q.assert_within(got, o, bo, "out")
+    Q.assert_within(lse, s, bs, "lse")
+    msa.msa_check(err)
+
+
+def test_append_of_index_vectors_in_place(msa):  # noqa: F811
+    dims = msa.Dims(8, 2, 64, 32, 2, 3)
+    got = []
+    for inplace in (False, True):
+        cache = msa.CacheQ8.zeros(dims, 3, "cuda")
+        rows = [Q.normal((300, h, w), 20 + i).cuda() for i, (h, w) in enumerate(((8, 64), (2, 64), (2, 64), (2, 32), (2, 32)))]
+        q, qi = msa.msa_rope_append_q8(*rows, cache, i32([[2, 0, 1]]).cuda(), i32([0] * 300).cuda(),
+                                       torch.arange(300, dtype=torch.int32).cuda(), msa.Rope.of_base(48, 32), dims,
+                                       *((rows[0], rows[3]) if inplace else ()))
+        got.append([q, qi] + [u8(getattr(cache, f)) for f in ("k", "v", "kidx", "k_scale", "v_scale", "kidx_scale")])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
