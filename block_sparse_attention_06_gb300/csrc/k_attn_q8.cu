@@ -25,7 +25,7 @@
 // (The 8-bit MMA of warps takes codes as they are, but is no faster: it unpacks its operands itself, every time, and
 // needs P and q in pieces.)
 //
-// Measured (Hq = 64, G = 8, D = 128).  8 requests x 16 blocks (33 MB): 12.5 us against 5.0 at the copy rate; the chain is a
+// Measured (Hq = 64, G = 8, D = 128).  8 requests x 16 blocks (33 MB): 12.5 to 13.0 us against 5.0 at the copy rate; the chain is a
 // launch, two table loads, four units per warp at some 2,000 cycles and the join.  32 requests, window of 4,096 (257 MB):
 // 48 us against 38; 256 clusters of one CTA on 152 SMs leave a third of the SMs one row where the others have two.  (12.4
 // and 47.4 without a look at rows of zeros.)  First kernel, with 8-bit MMAs: 17.5 and 94.
@@ -519,7 +519,9 @@ cudaError_t launch_t(Args a, long long rows, int units, cudaStream_t st, bool pd
     // this takes).  16 blocks, 64 rows: 16.8, *12.5, 14.5, 26.5, 68; 11 blocks, D = 64, 24 rows: 9.6, 7.5, *7.0, 8.4, 19.4;
     // window of 4,096, 256 rows: *47, 54, 62, 107, 278; 16 rows: 2, 4, 8, 16: 17.5, *12.8, 14.5, 26; 8 rows: 17.0, 12.3,
     // *10.7, 15.5; 2 rows: 17.0, 12.3, *10.7, 11.8; window of 1,024, 8 rows: 9.4, *8.6, 8.8, 14.6; dense, 60,000 tokens, 8
-    // rows: 158, 84, *47, 46; 2 rows: 158, 83, 47, *30.
+    // rows: 158, 84, *47, 46; 2 rows: 158, 83, 47, *30.  (Taken before rows of zeros were looked for, which adds 1 %.)
+    // The host does not know the rows' lengths: the rule takes them for full, and short rows in a table for long ones,
+    // or under a window past their length, get clusters whose warps have nothing to do (8 CTAs: 10.7 us, 2: 8.6).
     const long long sms = sm_count();
     int cs = 1;
     while (cs < kMaxCluster && rows * cs * 2 <= (cs < 4 ? sms : sms / 2) && cs * (cs < 8 ? 2 : 4) * kWarps <= units) cs *= 2;

@@ -12,7 +12,7 @@
 // a ring of its own, filled by bulk copies that the warp itself issues as it frees a stage: some 200 KB are in flight
 // per SM, no warp waits for another, and a range keeps q_idx in registers over the blocks of a (row, group).
 //
-// Measured: 8 x 60,000 tokens, G = 8, Di = 64 (250 MB) in 41 us, 0.89 of the copy rate (a CTA per page with loads into
+// Measured: 8 x 60,000 tokens, G = 8, Di = 64 (250 MB) in 42 us, 0.88 of the copy rate (a CTA per page with loads into
 // registers took 67); what is left is the start and the end of the stream.  One request of 1,500 tokens: 4.4 us, one
 // launch and the chain q_pos, table, keys.
 #include "msa_internal.h"

@@ -21,7 +21,7 @@
 // What bounds it: the chain S, softmax, P V of a tile.  TMEM holds two S and two O (512 columns with heads of 128), so
 // two tiles take turns.  S of a page comes in halves of 64 tokens: P takes half of S's columns, so the first half of the
 // next S goes into the other half as soon as P is there, before P V, and its softmax runs under P V.  A step of
-// both tiles takes about 4,000 cycles, of which the tensor cores work 2,048; issue slots are busy 0.58 of the time, memory
+// both tiles takes about 4,000 cycles, of which the tensor cores work 2,048; issue slots are busy 0.60 of the time, memory
 // next to never.  Measured: 8,192 rows at 60,000, window of 4,096, 4 first tokens: 0.98 ms, 0.59 of the measured bf16 rate
 // counting the visible tokens.  What brought it there from 1.53 ms: arrivals without a release over the cluster (1.61
 // -> 1.41), a softmax of one pass (1.41 -> 1.17; the maximum first, or a vote for every 32 columns, breaks the code into

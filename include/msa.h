@@ -571,7 +571,8 @@ msa_status_t msa_commit_tree(const void *k_new, const void *v_new, const void *k
  * 448 (the largest code), at least 2^-100, and 1 for a row of zeros.  Values are rounded
  * once, to the nearest code (ties to even), so a value is off by at most 2^-4 of itself where
  * its code is normal, and by 2^-18 of the row's largest magnitude below; each stored
- * value is also a bf16 number.  A row of k, v or k_idx that holds a NaN or an infinity is stored as
+ * value is also a bf16 number (but for 2^128, which magnitudes above 1.9375 * 2^127 are rounded to: an infinity
+ * where it is read).  A row of k, v or k_idx that holds a NaN or an infinity is stored as
  * a row of NaN and raises MSA_FLAG_NAN.  The 8-bit pages are those of the same page ids and
  * block tables as the bf16 ones.  Codes, scales and bf16 rows are 16-byte aligned.
  */

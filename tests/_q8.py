@@ -2,8 +2,8 @@
 
 Bounds are derived, not fitted.  e4m3 has four significant bits: a code is off by at most 2^-4 of a normal value, and by
 half of the lowest step, 2^-10 in units of the scale, below 2^-6.  A rounding to bf16 is off by at most 2^-8 of the
-value.  The 8-bit MMA's products are exact; an fp32 sum of W terms is off by at most W * 2^-23 of the sum of their
-magnitudes, in any order and with truncating adders."""
+value.  The MMAs' products (of f16 or bf16 factors) are exact; an fp32 sum of W terms is off by at most W * 2^-23 of the
+sum of their magnitudes, in any order and with truncating adders."""
 from __future__ import annotations
 
 import torch
@@ -90,8 +90,8 @@ def rotated(x, rot, inv_freq, pos, interleaved, gain):
         a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
         c, s = gain * torch.cos(w), gain * torch.sin(w)
         y[..., a], y[..., b] = x[..., a] * c - x[..., b] * s, x[..., b] * c + x[..., a] * s
-        # the angle in half turns rounded to fp32 (2^-25 of a half turn), the cosine and the sine good to an ulp or
-        # two (2^-22), the gain, two products and a sum: each below 2^-23 of |a| + |b|
+        # the cosine and the sine, the gain, two products and a sum, each below 2^-23 of |a| + |b|, and 2^-22 besides (the
+        # cosine and the sine are known far better than that: test_gpu_q8_edges.py holds them to their last bit)
         tol[..., a] = tol[..., b] = (x[..., a].abs() + x[..., b].abs()) * abs(gain) * (2.0 ** -22 + 6 * 2.0 ** -23)
     return y, tol
 
@@ -139,7 +139,7 @@ def ref_attend(q, k, v, sm_scale):
         z = torch.zeros_like(q)
         return z, torch.full((q.shape[0],), -torch.inf, dtype=torch.float64), z, torch.zeros(q.shape[0]).double()
     s = q @ k.T * sm_scale
-    # the dot product's sum, its factors' roundings, q's pieces, and the exponent's argument in log2 units
+    # the dot product's sum, its factors' roundings, q in f16, and the exponent's argument in log2 units
     ds = ((q.abs() @ k.abs().T) * sm_scale * (D + 16) * 1.2 * 2.0 ** -23).amax(-1) + s.abs().amax(-1) * 2.0 ** -22
     ds += q.abs().amax(-1) * k.abs().sum(-1).max() * sm_scale * 2.0 ** -39 + 2.0 ** -20
     p = torch.softmax(s, -1)
