@@ -11,7 +11,6 @@ from __future__ import annotations
 
 import ctypes
 import math
-import operator
 import os
 from dataclasses import dataclass
 from typing import Optional, Tuple
@@ -977,7 +976,9 @@ def msa_window_attn_q8(q, cache: CacheQ8, block_table, q_req, q_pos, window: int
     """Attention over 8-bit caches of each row (the token at q_pos[r] of request q_req[r]; -1: padding, nothing of it
     is written) to the last `window` tokens and the first n_sink -> (out, lse).  phase: MSA_PHASE_DECODE (single rows)
     or MSA_PHASE_PREFILL (chunks)."""
-    window, n_sink = (max(min(operator.index(x), _I32_MAX), -1) for x in (window, n_sink))   # past any context, or refused
+    # past 32 bits: past any context, or refused below
+    window = window if 0 <= window <= _I32_MAX else 0 if window < 0 else _I32_MAX
+    n_sink = n_sink if 0 <= n_sink <= _I32_MAX else -1 if n_sink < 0 else _I32_MAX
     dev = _lead(q, "q")
     n = _ndim(q, 3, "q", "[n_rows][Hq][D]")[0]
     n_req = _ndim(block_table, 2, "block_table", "[n_req][max_blocks]")[0]

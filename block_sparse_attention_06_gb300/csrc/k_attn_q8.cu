@@ -25,10 +25,10 @@
 // (The 8-bit MMA of warps takes codes as they are, but is no faster: it unpacks its operands itself, every time, and
 // needs P and q in pieces.)
 //
-// Measured (Hq = 64, G = 8, D = 128).  8 requests x 16 blocks (33 MB): 12.5 to 13.0 us against 5.0 at the copy rate; the chain is a
-// launch, two table loads, four units per warp at some 2,000 cycles and the join.  32 requests, window of 4,096 (257 MB):
-// 48 us against 38; 256 clusters of one CTA on 152 SMs leave a third of the SMs one row where the others have two.  (12.4
-// and 47.4 without a look at rows of zeros.)  First kernel, with 8-bit MMAs: 17.5 and 94.
+// Measured (Hq = 64, G = 8, D = 128).  8 requests x 16 blocks (33 MB): 12.5 to 13.0 us against 5.0 at the copy rate; the
+// chain is a launch, two table loads, four units per warp at some 2,000 cycles and the join.  32 requests, window of 4,096
+// (257 MB): 48 us against 38; 256 clusters of one CTA on 152 SMs leave a third of the SMs one row where the others have
+// two.  (1 % less without a look at rows of zeros.)  First kernel, with 8-bit MMAs: 17.5 and 94.
 //
 // Layout.  A unit's K and V are 32 rows of D bytes, swizzled by the copy (128- or 64-byte pattern).  Lane (r, c) =
 // (lane / 4, lane % 4) reads a quarter of K's rows 8i + r, i = 0 .. 3, and an eighth of V's rows 8i + 2c and 8i + 2c + 1:

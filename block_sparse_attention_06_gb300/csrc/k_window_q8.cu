@@ -102,7 +102,7 @@ __device__ __forceinline__ void poison_empty(const Args &a, int row, int h) {
     if (req < 0 || req >= a.n_req || pos < 0 || (pos >> 7) >= a.max_blocks || a.lse[head] != -INFINITY) return;
     bool finite = true, saw = false;
     for (int i = 0; i < D; ++i) finite &= (a.q[head * D + i] & 0x7f80u) != 0x7f80u;
-    for (int j = 0; !finite && !saw && j <= pos >> 7; ++j) {
+    for (int j = a.n_sink > 0 ? 0 : max(0, pos - (a.window - 1)) >> 7; !finite && !saw && j <= pos >> 7; ++j) {
         const int page = a.block_table[size_t(req) * a.max_blocks + j];
         saw = (j * 128 + 127 > pos - a.window || j * 128 < a.n_sink) && page >= 0 && page < a.n_pages;
     }
